@@ -12,9 +12,21 @@ calls raise instead of computing anything another way.
     Plan(4096, 2048, layout=LAYOUT_REAL_MMAJOR, mmax=1365).r2c(rows)   # band-limited real rows
     Plan(1024, 1, dims=2, ny=512, direction=INVERSE, normalize=True).c2c(img)  # 512 x 1024
     shift(y)                                                # standalone fftshift
+
+The sequence operators (short causal convolution, selective state-space scan, residual norm) are
+in the module `sequence` and under the package's own name:
+
+    out = causal_conv(x, weight, bias, silu=True)           # x [sequences, tokens, channels]
+    y = selective_scan(u, delta, A, B, C, D=D, z=z, softplus=True)
+    r = residual_norm(x, weight, residual=res)
 """
 import ctypes
 import os
+
+from . import sequence
+from .sequence import (causal_conv, causal_conv_backward, causal_conv_step, residual_norm,
+                       residual_norm_backward, selective_scan, selective_scan_backward,
+                       selective_scan_step)
 
 FORWARD = -1
 INVERSE = +1
@@ -45,7 +57,7 @@ ABI_SYMBOLS = (
     "fft_exec_c2c_noalloc", "fft_plan_set_wait_timeout", "fft_shift", "fft_plan_create_2d",
     "fft_plan_query_2d", "fft_plan_set_normalization", "fft_plan_set_real_pairing",
     "fft_plan_set_diagnostic",
-)
+) + sequence.SYMBOLS
 
 _LIB = None
 
@@ -88,6 +100,7 @@ def lib():
         L.fft_version.argtypes = []
         L.fft_exec_c2c_noalloc.argtypes = [i64, i64, ci, ci, vp, vp, vp]
         L.fft_plan_set_wait_timeout.argtypes = [vp, ctypes.c_uint64]
+        sequence.declare(L)
         for name in ABI_SYMBOLS:
             if name != "fft_status_string":
                 getattr(L, name).restype = ci

@@ -1,0 +1,11 @@
+// Selective state-space scan of f32 sequences, backward.
+#include "launch_cache.cuh"
+#include "scan_bwd.cuh"
+
+namespace gbfft {
+
+cudaError_t scan_backward_f32(const ScanBwdArgs& a, cudaStream_t s) {
+    return scan_bwd_run<float>(a, s);
+}
+
+}  // namespace gbfft

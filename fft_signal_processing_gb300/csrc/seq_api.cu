@@ -1,0 +1,297 @@
+// C entry points of the short causal convolution and the selective scan: checks on the host,
+// workspace layout, and the choice of the per-type launcher.  Declared in include/gbfft.h.
+#include "conv.h"
+#include "scan.h"
+#include "scan_bwd.h"
+#include "seq_step.h"
+
+using namespace gbfft;
+
+namespace {
+
+constexpr int64_t kMaxElements = INT64_C(1) << 58;  // strides and offsets stay in 64 bits
+
+int status(cudaError_t e) {
+    return e == cudaSuccess ? FFT_OK
+                            : (e == cudaErrorInvalidValue ? FFT_ERR_UNSUPPORTED_SIZE : FFT_ERR_CUDA);
+}
+
+// A sequence tensor whose rows hold `width` values.
+int check_seq(const fft_seq& s, int64_t width, int64_t nseq, int64_t length, bool packed,
+              size_t size, bool output) {
+    if (!s.data) return length == 0 ? FFT_OK : FFT_ERR_INVALID_ARG;
+    if (s.tok_stride < 0 || s.seq_stride < 0) return FFT_ERR_INVALID_ARG;
+    if (output && length > 1 && s.tok_stride < width) return FFT_ERR_INVALID_ARG;
+    if (output && !packed && nseq > 1 && length > 0 && s.seq_stride < width) return FFT_ERR_INVALID_ARG;
+    if (s.tok_stride > kMaxElements / (length + 1) ||
+        (!packed && s.seq_stride > kMaxElements / (nseq + 1)))
+        return FFT_ERR_UNSUPPORTED_SIZE;
+    return aligned_to(s.data, size) ? FFT_OK : FFT_ERR_MISALIGNED;
+}
+int check_sizes(int64_t nseq, int64_t length, int64_t channels, const int64_t* offsets) {
+    if (nseq < 1 || length < 0 || channels < 1) return FFT_ERR_INVALID_ARG;
+    if (nseq > INT32_MAX || length > INT32_MAX - 65536 || channels > INT32_MAX / 256)
+        return FFT_ERR_UNSUPPORTED_SIZE;
+    return aligned_to(offsets, 8) ? FFT_OK : FFT_ERR_MISALIGNED;
+}
+
+#define TRY(x)                        \
+    do {                              \
+        const int rc_ = (x);          \
+        if (rc_ != FFT_OK) return rc_; \
+    } while (0)
+
+int check_conv(const fft_conv_desc* d, bool pointers) {
+    if (!d || d->dtype < FFT_F32 || d->dtype > FFT_F16 || (d->silu != 0 && d->silu != 1) ||
+        (d->param_dtype != FFT_F32 && d->param_dtype != d->dtype))
+        return FFT_ERR_INVALID_ARG;
+    if (d->width < 1) return FFT_ERR_INVALID_ARG;
+    if (d->width > FFT_CONV_MAX_WIDTH) return FFT_ERR_UNSUPPORTED_SIZE;
+    TRY(check_sizes(d->nseq, d->length, d->channels, d->offsets));
+    if (!pointers) return FFT_OK;
+    if (!d->weight) return FFT_ERR_INVALID_ARG;
+    const size_t e = dtype_size(d->dtype), p = dtype_size(d->param_dtype);
+    if (!aligned_to(d->weight, p) || !aligned_to(d->bias, p) || !aligned_to(d->initial_state, e))
+        return FFT_ERR_MISALIGNED;
+    return check_seq(d->x, d->channels, d->nseq, d->length, d->offsets, e, false);
+}
+
+int64_t conv_tiles(const fft_conv_desc& d) {
+    return (d.offsets ? 1 : d.nseq) * ((d.length + kConvBwdTokens - 1) / kConvBwdTokens);
+}
+
+int check_scan(const fft_scan_desc* d, bool pointers) {
+    if (!d || d->dtype < FFT_F32 || d->dtype > FFT_F16 || (d->softplus != 0 && d->softplus != 1))
+        return FFT_ERR_INVALID_ARG;
+    TRY(check_sizes(d->nseq, d->length, d->channels, d->offsets));
+    if (d->groups < 1 || d->channels % d->groups || d->states < 1) return FFT_ERR_INVALID_ARG;
+    if (d->states > FFT_SCAN_MAX_STATES) return FFT_ERR_UNSUPPORTED_SIZE;
+    if (!pointers) return FFT_OK;
+    if (!d->A) return FFT_ERR_INVALID_ARG;
+    if (!aligned_to(d->A, 4) || !aligned_to(d->D, 4) || !aligned_to(d->delta_bias, 4) ||
+        !aligned_to(d->initial_state, 4))
+        return FFT_ERR_MISALIGNED;
+    const size_t e = dtype_size(d->dtype);
+    const int64_t bc = d->groups * d->states;
+    TRY(check_seq(d->u, d->channels, d->nseq, d->length, d->offsets, e, false));
+    TRY(check_seq(d->delta, d->channels, d->nseq, d->length, d->offsets, e, false));
+    TRY(check_seq(d->B, bc, d->nseq, d->length, d->offsets, e, false));
+    TRY(check_seq(d->C, bc, d->nseq, d->length, d->offsets, e, false));
+    if (d->z.data) TRY(check_seq(d->z, d->channels, d->nseq, d->length, d->offsets, e, false));
+    return FFT_OK;
+}
+
+int64_t up16(int64_t bytes) { return (bytes + 15) / 16 * 16; }
+
+// Forward workspace: carry, dsum, reset.
+int64_t scan_layout(const fft_scan_desc& d, ScanArgs* a) {
+    const ScanChunks p = scan_chunks(d);
+    const int64_t np = scan_shape(d.states).np(), ch = p.rows * p.nchunks;
+    const int64_t carry = p.nchunks > 1 ? up16(ch * d.channels * np * 4) : 0;
+    const int64_t dsum = p.nchunks > 1 ? up16(ch * d.channels * 4) : 0;
+    const int64_t reset = p.nchunks > 1 ? up16(ch * 4) : 0;
+    if (a) {
+        char* w = reinterpret_cast<char*>(a->carry);
+        a->dsum = reinterpret_cast<float*>(w + carry);
+        a->reset = reinterpret_cast<int*>(w + carry + dsum);
+        a->rows = p.rows;
+        a->chunk = p.chunk;
+        a->nchunks = p.nchunks;
+        a->ctiles = p.ctiles;
+    }
+    return carry + dsum + reset;
+}
+
+}  // namespace
+
+namespace gbfft {
+
+int64_t scan_bwd_layout(const fft_scan_desc& d, ScanBwdArgs* a, char* w) {
+    const int64_t n = d.states, np = scan_shape(n).np(), sl = bwd_sl(n), ct = bwd_channels((int)sl);
+    const int64_t dg = d.channels / d.groups, rows = d.offsets ? 1 : d.nseq;
+    const int64_t ctiles = (dg + ct - 1) / ct;
+    // chunks: enough blocks of the main kernel to fill the GPU (two to an SM) several times
+    const int64_t blocks = rows * ctiles * d.groups, want = (int64_t)num_sms() * 8;
+    const int64_t k = (want + blocks - 1) / blocks;
+    int64_t chunk = (d.length + k - 1) / k;
+    chunk = (chunk + 63) / 64 * 64;
+    if (chunk < 64) chunk = 64;
+    const int64_t nchunks = (d.length + chunk - 1) / chunk;
+    const int64_t state_tiles = (d.length + kScanStateTile - 1) / kScanStateTile;
+    int64_t at = 0;
+    auto take = [&](int64_t floats) {
+        float* p = reinterpret_cast<float*>(w ? w + at : nullptr);
+        at += up16(floats * 4);
+        return p;
+    };
+    const int64_t per = d.channels * np, parts = rows * nchunks;
+    ScanBwdArgs b = {};
+    if (a) b = *a;
+    b.ctiles = ctiles;
+    b.f.d = d;
+    b.f.rows = rows;
+    b.f.chunk = chunk;
+    b.f.nchunks = nchunks;
+    b.f.ctiles = (dg + kScanThreads / scan_shape(n).sl - 1) / (kScanThreads / scan_shape(n).sl);
+    if (nchunks > 1) {
+        b.f.carry = take(parts * per);
+        b.f.dsum = take(parts * d.channels);
+        b.f.reset = reinterpret_cast<int*>(take(parts));
+        b.carry = take(parts * per);
+    }
+    b.f.tiles = take(rows * state_tiles * per);
+    b.bc = take(ctiles * rows * d.length * d.groups * 2 * n);
+    b.pA = take(parts * d.channels * n);
+    b.pD = take(parts * d.channels);
+    b.pbias = take(parts * d.channels);
+    if (a) *a = b;
+    return at;
+}
+
+}  // namespace gbfft
+
+extern "C" int fft_conv_forward(const fft_conv_desc* d, const fft_seq* out, void* final_state,
+                                void* stream) {
+    TRY(check_conv(d, true));
+    if (!out) return FFT_ERR_INVALID_ARG;
+    const size_t e = dtype_size(d->dtype);
+    TRY(check_seq(*out, d->channels, d->nseq, d->length, d->offsets, e, true));
+    if (!aligned_to(final_state, e)) return FFT_ERR_MISALIGNED;
+    ConvArgs a = {};
+    a.d = *d;
+    a.out = *out;
+    a.final_state = final_state;
+    cudaStream_t s = (cudaStream_t)stream;
+    return status(d->dtype == FFT_F32 ? conv_forward_f32(a, s)
+                                      : (d->dtype == FFT_BF16 ? conv_forward_bf16(a, s)
+                                                              : conv_forward_f16(a, s)));
+}
+
+extern "C" int fft_conv_workspace(const fft_conv_desc* d, size_t* bytes) {
+    if (!bytes) return FFT_ERR_INVALID_ARG;
+    TRY(check_conv(d, false));
+    *bytes = (size_t)(conv_tiles(*d) * (d->width + 1) * d->channels) * sizeof(float);
+    return FFT_OK;
+}
+
+extern "C" int fft_conv_backward(const fft_conv_desc* d, const fft_seq* dout,
+                                 const void* dfinal_state, const fft_seq* dx, float* dweight,
+                                 float* dbias, void* dinitial_state, void* workspace,
+                                 size_t workspace_bytes, void* stream) {
+    TRY(check_conv(d, true));
+    if (!dout || !dx) return FFT_ERR_INVALID_ARG;
+    const size_t e = dtype_size(d->dtype);
+    TRY(check_seq(*dout, d->channels, d->nseq, d->length, d->offsets, e, false));
+    if (dx->data) TRY(check_seq(*dx, d->channels, d->nseq, d->length, d->offsets, e, true));
+    if (!aligned_to(dfinal_state, e) || !aligned_to(dinitial_state, e) || !aligned_to(dweight, 4) ||
+        !aligned_to(dbias, 4) || !aligned_to(workspace, 16))
+        return FFT_ERR_MISALIGNED;
+    const int64_t tiles = conv_tiles(*d), cols = (d->width + 1) * d->channels;
+    const bool params = dweight || dbias;
+    if (params && tiles > 0 &&
+        (!workspace || workspace_bytes < (size_t)(tiles * cols) * sizeof(float)))
+        return FFT_ERR_INVALID_ARG;
+    ConvArgs a = {};
+    a.d = *d;
+    a.out = *dx;
+    a.dout = *dout;
+    a.final_state = const_cast<void*>(dfinal_state);
+    a.dinitial = dinitial_state;
+    a.parts = params && tiles > 0 ? static_cast<float*>(workspace) : nullptr;
+    cudaStream_t s = (cudaStream_t)stream;
+    cudaError_t r = d->dtype == FFT_F32 ? conv_backward_f32(a, s)
+                                        : (d->dtype == FFT_BF16 ? conv_backward_bf16(a, s)
+                                                                : conv_backward_f16(a, s));
+    // partial rows are [tiles][width + 1][channels], the bias behind the taps
+    if (r == cudaSuccess && dweight)
+        r = run_sum_parts(a.parts, tiles, cols, d->width * d->channels, dweight, d->channels,
+                          d->width, s);
+    if (r == cudaSuccess && dbias)
+        r = run_sum_parts(a.parts ? a.parts + d->width * d->channels : nullptr, tiles, cols,
+                          d->channels, dbias, d->channels, 1, s);
+    return status(r);
+}
+
+static int check_step(const fft_seq* out, const void* state, int64_t pool, const int64_t* slots,
+                      const int64_t* slots_out, int64_t nseq, int64_t length,
+                      const int64_t* offsets, int64_t channels, size_t e, bool needs_state) {
+    if (!out || length != 1 || offsets || pool < 0) return FFT_ERR_INVALID_ARG;
+    if (needs_state && pool > 0 && !state) return FFT_ERR_INVALID_ARG;
+    if (!slots && pool < nseq) return FFT_ERR_INVALID_ARG;
+    if (!aligned_to(slots, 8) || !aligned_to(slots_out, 8)) return FFT_ERR_MISALIGNED;
+    return check_seq(*out, channels, nseq, 1, false, e, true);
+}
+
+extern "C" int fft_conv_step(const fft_conv_desc* d, const fft_seq* out, void* state, int64_t pool,
+                             const int64_t* slots, const int64_t* slots_out, void* stream) {
+    TRY(check_conv(d, true));
+    const size_t e = dtype_size(d->dtype);
+    TRY(check_step(out, state, pool, slots, slots_out, d->nseq, d->length, d->offsets, d->channels,
+                   e, d->width > 1));
+    if (!aligned_to(state, e)) return FFT_ERR_MISALIGNED;
+    const ConvStepArgs a = {*d, *out, state, slots, slots_out, pool};
+    return status(conv_step_any(a, (cudaStream_t)stream));
+}
+
+extern "C" int fft_scan_workspace(const fft_scan_desc* d, int backward, size_t* bytes) {
+    if (!bytes || (backward != 0 && backward != 1)) return FFT_ERR_INVALID_ARG;
+    TRY(check_scan(d, false));
+    *bytes = (size_t)(backward ? scan_bwd_layout(*d, nullptr, nullptr) : scan_layout(*d, nullptr));
+    return FFT_OK;
+}
+
+extern "C" int fft_scan_forward(const fft_scan_desc* d, const fft_seq* out, float* final_state,
+                                void* workspace, size_t workspace_bytes, void* stream) {
+    TRY(check_scan(d, true));
+    if (!out) return FFT_ERR_INVALID_ARG;
+    TRY(check_seq(*out, d->channels, d->nseq, d->length, d->offsets, dtype_size(d->dtype), true));
+    if (!aligned_to(final_state, 4) || !aligned_to(workspace, 16)) return FFT_ERR_MISALIGNED;
+    ScanArgs a = {};
+    a.d = *d;
+    a.out = *out;
+    a.final_state = final_state;
+    a.carry = static_cast<float*>(workspace);
+    const int64_t need = scan_layout(*d, &a);
+    if (need > 0 && (!workspace || workspace_bytes < (size_t)need)) return FFT_ERR_INVALID_ARG;
+    cudaStream_t s = (cudaStream_t)stream;
+    return status(d->dtype == FFT_F32 ? scan_forward_f32(a, s)
+                                      : (d->dtype == FFT_BF16 ? scan_forward_bf16(a, s)
+                                                              : scan_forward_f16(a, s)));
+}
+
+extern "C" int fft_scan_step(const fft_scan_desc* d, const fft_seq* out, float* state, int64_t pool,
+                             const int64_t* slots, const int64_t* slots_out, void* stream) {
+    TRY(check_scan(d, true));
+    TRY(check_step(out, state, pool, slots, slots_out, d->nseq, d->length, d->offsets, d->channels,
+                   dtype_size(d->dtype), true));
+    if (!aligned_to(state, 4)) return FFT_ERR_MISALIGNED;
+    const ScanStepArgs a = {*d, *out, state, slots, slots_out, pool, 0, false};
+    return status(scan_step_any(a, (cudaStream_t)stream));
+}
+
+extern "C" int fft_scan_backward(const fft_scan_desc* d, const fft_scan_grads* g, void* workspace,
+                                 size_t workspace_bytes, void* stream) {
+    TRY(check_scan(d, true));
+    if (!g || (g->dz.data != nullptr) != (d->z.data != nullptr)) return FFT_ERR_INVALID_ARG;
+    const size_t e = dtype_size(d->dtype);
+    const int64_t bc = d->groups * d->states;
+    TRY(check_seq(g->dout, d->channels, d->nseq, d->length, d->offsets, e, false));
+    TRY(check_seq(g->du, d->channels, d->nseq, d->length, d->offsets, e, true));
+    TRY(check_seq(g->ddelta, d->channels, d->nseq, d->length, d->offsets, e, true));
+    TRY(check_seq(g->dB, bc, d->nseq, d->length, d->offsets, e, true));
+    TRY(check_seq(g->dC, bc, d->nseq, d->length, d->offsets, e, true));
+    if (g->dz.data) TRY(check_seq(g->dz, d->channels, d->nseq, d->length, d->offsets, e, true));
+    if (!aligned_to(g->dfinal_state, 4) || !aligned_to(g->dA, 4) || !aligned_to(g->dD, 4) ||
+        !aligned_to(g->ddelta_bias, 4) || !aligned_to(g->dinitial_state, 4) ||
+        !aligned_to(workspace, 16))
+        return FFT_ERR_MISALIGNED;
+    ScanBwdArgs a = {};
+    a.d = *d;
+    a.g = *g;
+    const int64_t need = scan_bwd_layout(*d, &a, static_cast<char*>(workspace));
+    if (need > 0 && (!workspace || workspace_bytes < (size_t)need)) return FFT_ERR_INVALID_ARG;
+    cudaStream_t s = (cudaStream_t)stream;
+    return status(d->dtype == FFT_F32 ? scan_backward_f32(a, s)
+                                      : (d->dtype == FFT_BF16 ? scan_backward_bf16(a, s)
+                                                              : scan_backward_f16(a, s)));
+}

@@ -1,0 +1,156 @@
+// Shared by the sequence operators (short causal convolution, selective scan, residual norm):
+// type conversions, rows addressed by strides, sequences found from packed offsets, and the
+// column sums that close every parameter gradient.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "../../include/gbfft.h"
+
+namespace gbfft {
+
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+
+__device__ __forceinline__ float to_f(float v) { return v; }
+__device__ __forceinline__ float to_f(__nv_bfloat16 v) { return __bfloat162float(v); }
+__device__ __forceinline__ float to_f(__half v) { return __half2float(v); }
+template <class T> __device__ __forceinline__ T from_f(float v);
+template <> __device__ __forceinline__ float from_f<float>(float v) { return v; }
+template <> __device__ __forceinline__ __nv_bfloat16 from_f<__nv_bfloat16>(float v) {
+    return __float2bfloat16_rn(v);
+}
+template <> __device__ __forceinline__ __half from_f<__half>(float v) { return __float2half_rn(v); }
+
+// A run of V contiguous values of T, moved in accesses of up to 16 bytes.
+template <class T, int V>
+struct alignas(sizeof(T) * V > 16 ? 16 : sizeof(T) * V) Pack {
+    T v[V];
+};
+template <int V, class T>
+__device__ __forceinline__ Pack<T, V> ld_pack(const T* p) {
+    return *reinterpret_cast<const Pack<T, V>*>(p);
+}
+template <int V, class T>
+__device__ __forceinline__ void st_pack(T* p, const Pack<T, V>& x) {
+    *reinterpret_cast<Pack<T, V>*>(p) = x;
+}
+
+// A parameter of type float or T (f32 != 0: float).
+template <class T>
+__device__ __forceinline__ float ld_param(const void* p, int64_t i, int f32) {
+    return f32 ? static_cast<const float*>(p)[i] : to_f(static_cast<const T*>(p)[i]);
+}
+
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ float rcp(float x) {
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+// 1 / (1 + exp(-x)): exp(-x) overflows to infinity for x < -88 and the quotient is 0.
+__device__ __forceinline__ float sigmoid(float x) { return rcp(1.0f + ex2(-kLog2e * x)); }
+
+// log(1 + exp(x)) = max(x, 0) + log1p(t), t = exp(-|x|) in (0, 1], log1p(t) = 2 atanh(t / (2 + t))
+// by the odd series in s = t / (2 + t) <= 1/3, whose terms left out are below 2e-8 of the sum.
+// The exponent's rounding error is put back, since t is the result itself where x << 0.
+__device__ __forceinline__ float softplus(float x) {
+    const float y = -fabsf(x);
+    const float hi = y * kLog2e;
+    const float lo = fmaf(y, kLog2e, -hi) + y * 1.9259630e-8f;  // log2(e) beyond 24 bits
+    float t = ex2(hi);
+    t = fmaf(t, lo * kLn2, t);
+    if (!(y > -88.f)) t = y != y ? y : 0.f;  // exp underflows; -inf would leave lo a NaN
+    const float s = t * rcp(2.f + t), q = s * s;
+    float p = fmaf(q, 1.f / 13.f, 1.f / 11.f);
+    p = fmaf(q, p, 1.f / 9.f);
+    p = fmaf(q, p, 1.f / 7.f);
+    p = fmaf(q, p, 1.f / 5.f);
+    p = fmaf(q, p, 1.f / 3.f);
+    p = fmaf(q, p, 1.f);
+    return fmaxf(x, 0.f) + 2.f * s * p;
+}
+
+// Two float32 values in one 64-bit register pair: sm_103a multiplies and adds both at once.
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+    float2 d;
+    asm("mul.rn.f32x2 %0, %1, %2;"
+        : "=l"(reinterpret_cast<unsigned long long&>(d))
+        : "l"(reinterpret_cast<unsigned long long&>(a)),
+          "l"(reinterpret_cast<unsigned long long&>(b)));
+    return d;
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+    float2 d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;"
+        : "=l"(reinterpret_cast<unsigned long long&>(d))
+        : "l"(reinterpret_cast<unsigned long long&>(a)),
+          "l"(reinterpret_cast<unsigned long long&>(b)),
+          "l"(reinterpret_cast<unsigned long long&>(c)));
+    return d;
+}
+
+// Number of ascending offsets[0 .. n-1] that are <= t, found by a whole warp: 32 probes a step
+// instead of one, since each step costs a trip to L2.
+__device__ __forceinline__ int64_t warp_count_le(const int64_t* offsets, int64_t n, int64_t t) {
+    const int lane = (int)(threadIdx.y * blockDim.x + threadIdx.x) & 31;
+    int64_t lo = 0, hi = n;  // the count lies in [lo, hi]
+    while (hi > lo) {
+        const int64_t step = (hi - lo + 31) / 32;
+        const int64_t i = lo + (int64_t)(lane + 1) * step - 1;
+        const unsigned le = __ballot_sync(0xffffffffu, i < hi && __ldg(offsets + i) <= t);
+        const int k = __popc(le);  // the first k probes are <= t
+        const int64_t nlo = lo + (int64_t)k * step;
+        const int64_t nhi = lo + (int64_t)(k + 1) * step - 1;
+        hi = nhi < hi ? nhi : hi;
+        lo = nlo < hi ? nlo : hi;
+    }
+    return lo;
+}
+
+// The sequence that token t of a row belongs to: [begin, end) are its tokens.
+struct SeqAt {
+    int64_t q, begin, end;
+};
+// Dense rows: sequence q is the row itself.  Packed: found by the whole warp.
+__device__ __forceinline__ SeqAt seq_at(const int64_t* offsets, int64_t nseq, int64_t length,
+                                        int64_t row, int64_t t) {
+    if (!offsets) return {row, 0, length};
+    int64_t q = warp_count_le(offsets, nseq + 1, t) - 1;
+    q = q < 0 ? 0 : (q >= nseq ? nseq - 1 : q);
+    const int64_t begin = offsets[q];
+    return {q, begin < 0 ? 0 : begin, offsets[q + 1]};
+}
+// The sequence that begins where s ends (token t = s.end), empty ones skipped.
+__device__ __forceinline__ void seq_next(const int64_t* offsets, int64_t nseq, int64_t t, SeqAt* s) {
+    while (s->q + 1 < nseq && s->end <= t) {
+        s->q += 1;
+        s->begin = s->end < 0 ? 0 : s->end;
+        s->end = offsets[s->q + 1];
+    }
+}
+
+// Sums over parts, the last step of a parameter gradient, in an order that does not depend on the
+// launch: column k * chan + c of parts[p * stride + column] (cols of them) goes to
+// out[c * (cols / chan) + k].  No parts: zeros.
+cudaError_t run_sum_parts(const float* parts, int64_t nparts, int64_t stride, int64_t cols,
+                          float* out, int64_t chan, int64_t wide, cudaStream_t s);
+
+inline bool aligned_to(const void* p, uintptr_t a) { return ((uintptr_t)p & (a - 1)) == 0; }
+inline size_t dtype_size(int t) { return t == FFT_F32 ? 4 : (t == FFT_E4M3 ? 1 : 2); }
+inline int num_sms() {
+    int dev = 0, n = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess ||
+        cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n < 1)
+        return 152;
+    return n;
+}
+
+}  // namespace gbfft

@@ -331,6 +331,174 @@ int fft_exec_c2c_noalloc(int64_t n, int64_t batch, int direction, int shift, con
 int fft_shift(const void* in, void* out, int64_t nx, int64_t ny, int64_t batch, int dims,
               int inverse, void* stream);
 
+/* ---- sequence operators ---------------------------------------------------------------------
+ *
+ * Filters along the tokens of a sequence whose coefficients change from token to token, which no
+ * transfer function (and so no transform plan) describes, and the norm that stands between two
+ * such layers.  They need no plan: the caller passes descriptors, device pointers and, where a
+ * *_workspace function says so, a workspace that is in use until the call's kernels have run.
+ * The calls validate on the host, enqueue kernels on `stream` and return; they allocate nothing,
+ * never synchronise and can be captured into a graph.  Repeated calls give the same bits.
+ *
+ * Data types: u, x, z, outputs and their gradients are all of the descriptor's dtype (FFT_F32,
+ * FFT_BF16 or FFT_F16).  All arithmetic, states of the scan, gradients of parameters and
+ * reductions are float32; each output is rounded once.
+ *
+ * Sequences: token t of sequence q of an fft_seq is the contiguous row of channels (for B and C
+ * the row of groups * states values) at data + (q*seq_stride + t*tok_stride) elements.
+ *   offsets == NULL  nseq sequences of `length` tokens each (length 0 allowed).
+ *   offsets != NULL  device int64 [nseq + 1], ascending, offsets[0] = 0, offsets[nseq] = length:
+ *                    sequence q is the rows offsets[q] .. offsets[q+1]-1 of one packed row of
+ *                    `length` tokens (seq_stride is not used).  Empty sequences are allowed.
+ *                    Offsets that break the rule give undefined outputs, but no access outside
+ *                    the tensors.
+ * Row strides of outputs must not make rows overlap.  data needs only the alignment of its type;
+ * 16-byte aligned rows are faster.  A NULL data pointer means the tensor is absent where that is
+ * allowed. */
+enum { FFT_F32 = 0, FFT_BF16 = 1, FFT_F16 = 2, FFT_E4M3 = 3 };
+
+typedef struct fft_seq {
+    void* data;
+    int64_t seq_stride; /* elements from one sequence to the next */
+    int64_t tok_stride; /* elements from one token to the next */
+} fft_seq;
+
+#define FFT_CONV_MAX_WIDTH 8
+#define FFT_SCAN_MAX_STATES 128
+#define FFT_NORM_MAX_COLUMNS 16384
+
+/*
+ * Short causal convolution of every channel c along its tokens, with bias and (silu = 1) SiLU:
+ *   p[t,c] = bias[c] + sum_{k<width} weight[c,k] * x[t-(width-1)+k, c]
+ *   out[t,c] = p  or  p / (1 + exp(-p))
+ * Before a sequence's start x continues with the rows of its initial state (row width-2 is the
+ * token just before the start), or with zeros.  The final state is the last width-1 inputs (of
+ * the initial state where the sequence is shorter).  weight [channels][width] and bias
+ * [channels] (or NULL) are of type param_dtype (FFT_F32 or dtype); states are
+ * [nseq][width-1][channels] of dtype.  1 <= width <= FFT_CONV_MAX_WIDTH.
+ */
+typedef struct fft_conv_desc {
+    int32_t dtype, param_dtype, width, silu;
+    int64_t nseq, length, channels;
+    const int64_t* offsets;
+    const void* weight;
+    const void* bias;
+    const void* initial_state; /* or NULL: zeros */
+    fft_seq x;
+} fft_conv_desc;
+
+/* fft_conv_forward - out and, unless NULL, final_state.  out may not overlap x.
+ * Returns FFT_OK, FFT_ERR_INVALID_ARG, FFT_ERR_UNSUPPORTED_SIZE, FFT_ERR_MISALIGNED or
+ * FFT_ERR_CUDA. */
+int fft_conv_forward(const fft_conv_desc* d, const fft_seq* out, void* final_state, void* stream);
+
+/* fft_conv_backward - gradients of sum(out * dout) + sum(final_state * dfinal_state):
+ * dx (data NULL: not computed), dweight [channels][width] and dbias [channels] in float32 (either
+ * may be NULL), dinitial_state like initial_state (NULL: not computed).  dfinal_state NULL:
+ * zeros.  workspace: 16-byte aligned, at least fft_conv_workspace bytes (0 if both parameter
+ * gradients are NULL). */
+int fft_conv_workspace(const fft_conv_desc* d, size_t* bytes);
+int fft_conv_backward(const fft_conv_desc* d, const fft_seq* dout, const void* dfinal_state,
+                      const fft_seq* dx, float* dweight, float* dbias, void* dinitial_state,
+                      void* workspace, size_t workspace_bytes, void* stream);
+
+/* fft_conv_step - one token for each of nseq sequences (length 1, offsets NULL, x and out rows
+ * at seq_stride, initial_state not used): reads the state at slots[q] of a pool of `pool` states
+ * [pool][width-1][channels] and writes the shifted state to slots_out[q].  slots NULL: sequence q
+ * has slot q; slots_out NULL: slots (in place).  A slot outside [0, pool) marks a padding row:
+ * its output is 0 and no state is written.  A slot that one sequence writes may not be read or
+ * written by another. */
+int fft_conv_step(const fft_conv_desc* d, const fft_seq* out, void* state, int64_t pool,
+                  const int64_t* slots, const int64_t* slots_out, void* stream);
+
+/*
+ * Selective state-space scan.  Channel c of group g = c / (channels / groups), state s:
+ *   e[t,c] = delta[t,c] + delta_bias[c];  d = softplus ? log(1 + exp(e)) : e
+ *   h[t,c,s] = exp(d * A[c,s]) * h[t-1,c,s] + d * u[t,c] * B[t,g,s]
+ *   y[t,c] = sum_s C[t,g,s] * h[t,c,s] + D[c] * u[t,c];  out = y  or  y * z / (1 + exp(-z))
+ * with h before a sequence's start its initial state, or 0.  A [channels][states], D [channels]
+ * and delta_bias [channels] (each of the two may be NULL) and the states
+ * [nseq][channels][states] are float32.  groups divides channels;
+ * 1 <= states <= FFT_SCAN_MAX_STATES.  z.data may be NULL (no gate).
+ */
+typedef struct fft_scan_desc {
+    int32_t dtype, softplus;
+    int64_t nseq, length, channels, groups, states;
+    const int64_t* offsets;
+    const float* A;
+    const float* D;
+    const float* delta_bias;
+    const float* initial_state; /* or NULL: zeros */
+    fft_seq u, delta, B, C, z;
+} fft_scan_desc;
+
+/* fft_scan_workspace - bytes of workspace for the forward (backward = 0) or backward call;
+ * it may be 0.  Needs the descriptor's sizes and dtype only (pointers are not read). */
+int fft_scan_workspace(const fft_scan_desc* d, int backward, size_t* bytes);
+
+/* fft_scan_forward - out and, unless NULL, final_state [nseq][channels][states].  out may be
+ * u or z themselves (same data and strides); any other overlap is an error of the caller.
+ * Returns FFT_OK, FFT_ERR_INVALID_ARG, FFT_ERR_UNSUPPORTED_SIZE, FFT_ERR_MISALIGNED or
+ * FFT_ERR_CUDA. */
+int fft_scan_forward(const fft_scan_desc* d, const fft_seq* out, float* final_state,
+                     void* workspace, size_t workspace_bytes, void* stream);
+
+/* Gradients of sum(out * dout) + sum(final_state * dfinal_state).  Sequences are of dtype, the
+ * rest float32.  du, ddelta, dB and dC are required (dz where z is given); the others are
+ * computed where not NULL. */
+typedef struct fft_scan_grads {
+    fft_seq dout;
+    const float* dfinal_state; /* or NULL: zeros */
+    fft_seq du, ddelta, dB, dC, dz;
+    float* dA;
+    float* dD;
+    float* ddelta_bias;
+    float* dinitial_state;
+} fft_scan_grads;
+
+int fft_scan_backward(const fft_scan_desc* d, const fft_scan_grads* g, void* workspace,
+                      size_t workspace_bytes, void* stream);
+
+/* fft_scan_step - one token for each of nseq sequences (length 1, offsets NULL, initial_state not
+ * used; rows at seq_stride): state pool [pool][channels][states] float32, slots as for
+ * fft_conv_step. */
+int fft_scan_step(const fft_scan_desc* d, const fft_seq* out, float* state, int64_t pool,
+                  const int64_t* slots, const int64_t* slots_out, void* stream);
+
+/*
+ * Root-mean-square norm with the residual's addition, rows of `columns` values:
+ *   r = x + residual (or x);  y = r / sqrt(mean(r^2) + eps) * weight
+ * computed in float32 on the unrounded sum.  residual (or data NULL) and the sum are of type
+ * res_dtype, weight [columns] of type param_dtype (FFT_F32 or dtype).
+ */
+typedef struct fft_norm_desc {
+    int32_t dtype, res_dtype, param_dtype, out_dtype;
+    int64_t rows, columns;
+    int64_t group; /* FFT_E4M3: columns per scale (32, 64 or 128), 0 = the whole row */
+    float eps;
+    const void* weight;
+} fft_norm_desc;
+
+/* fft_norm_forward - row i of a tensor is at data + i*stride elements.  out is of out_dtype:
+ * dtype, or FFT_E4M3 with scale (float32 [rows][ceil(columns/group)], contiguous):
+ *   m = max |y| over the group;  scale = m / 448;  out = e4m3(y * (448 / m)), 0 where m = 0.
+ * A NaN in a group makes its scale NaN.  sum: receives r rounded to res_dtype, NULL: not
+ * written; it may be the residual itself (in place). */
+int fft_norm_forward(const fft_norm_desc* d, const void* x, int64_t x_stride, const void* residual,
+                     int64_t residual_stride, void* out, int64_t out_stride, float* scale,
+                     void* sum, int64_t sum_stride, void* stream);
+
+/* fft_norm_backward - gradients at r (the stored sum, res_dtype), from dout (dtype) at y and
+ * dresidual (res_dtype or NULL) at r itself:
+ *   w = rstd * (weight dout) - r rstd^3 mean(weight dout r) + dresidual
+ * into dsum (res_dtype) and dx (dtype; either may be NULL), dweight = sum_rows dout r rstd in
+ * float32 (or NULL).  dsum may be dresidual itself.  workspace as above. */
+int fft_norm_workspace(const fft_norm_desc* d, size_t* bytes);
+int fft_norm_backward(const fft_norm_desc* d, const void* dout, int64_t dout_stride, const void* r,
+                      int64_t r_stride, const void* dresidual, int64_t dresidual_stride,
+                      void* dsum, int64_t dsum_stride, void* dx, int64_t dx_stride,
+                      float* dweight, void* workspace, size_t workspace_bytes, void* stream);
+
 /* fft_status_string - static description of a status code (never NULL). */
 const char* fft_status_string(int status);
 
