@@ -2,18 +2,20 @@
 //
 //   h[t] = exp(d[t] A) h[t-1] + d[t] u[t] B[t];  y[t] = sum_s C[t,s] h[t,s] + D u[t]
 //
-// A thread holds SPT states of one channel in registers and walks the tokens; SL lanes share a
-// channel.  Tiles of 8 tokens: B and C (shared by all channels of a group) are staged in shared
-// memory as float32, double buffered; u, delta and z are loaded a tile ahead into the registers
-// of the lane that owns the token, which also computes d and the gate, so nothing is done twice.
-// Per state: one ex2, and a multiply (d A), a multiply (d u B) and two fused multiply-adds, two
-// states to an instruction.
+// A thread holds the states of its channels in registers and walks the tokens.  Per state and
+// token that costs one ex2, and a multiply (d A), a multiply (d u B) and two fused multiply-adds,
+// two states to an instruction; the multiply-add pipe and the exponential unit are about equally
+// busy, and both far busier than HBM.  Up to 16 states: k_scan, two channels per thread, so that
+// one load of B and C from shared memory serves both (with one channel per thread those loads
+// filled the shared-memory pipe).  More states, or more channels: k_scan_lanes, several lanes per
+// channel.
 //
 // With too few channels for the GPU, time is cut into chunks.  A chunk's effect on the state is
 // h -> exp(A sum d) h + h_local, so pass 1 computes h_local and sum d of every chunk (from zero),
 // pass 2 runs along the chunks, and pass 3 is the full scan of each chunk from its true start.
 #pragma once
 
+#include "launch_cache.cuh"
 #include "scan.h"
 
 namespace gbfft {
@@ -61,49 +63,400 @@ __device__ __forceinline__ void store_states(float* p, int s0, int n, const floa
     }
 }
 
-// A state beyond n has A = B = C = 0; EXACT (n == SPT * SL) drops the selects that keep such
-// states at 0 where u is infinite.
-template <class T, int SPT, int SL, int PASS, bool EXACT>
-__global__ void __launch_bounds__(kScanThreads) k_scan(const ScanArgs a) {
-    constexpr int NP = SPT * SL, CT = kScanThreads / SL, TK = kScanTile, OWN = TK / SL;
-    constexpr int CL = 32 / SL;  // channels of a warp
+// The blocks behind the outputs: a sequence without tokens ends in its initial state.
+__device__ __forceinline__ void scan_empty(const ScanArgs& a, int64_t q) {
+    const int64_t per = a.d.channels * a.d.states;
+    if (a.d.offsets ? a.d.offsets[q] < a.d.offsets[q + 1] : a.d.length != 0) return;
+    for (int64_t i = threadIdx.x; i < per; i += blockDim.x)
+        a.final_state[q * per + i] = a.d.initial_state ? a.d.initial_state[q * per + i] : 0.f;
+}
+
+constexpr int kPairThreads = 64, kPairChannels = 2 * kPairThreads, kPairTile = 8;
+constexpr int kPairBatch = 8;  // tokens whose softplus and gates run side by side
+template <int N>
+struct Count {
+    static constexpr int value = N;
+};
+
+template <class T, int SPT, int PASS>
+struct ScanPairSmem {
+    static constexpr bool OUTPUT = PASS == SCAN_OUTPUT;
+    static constexpr int kStages = 3, kRaw = kPairTile * kPairChannels, kTensors = OUTPUT ? 3 : 2;
+    static constexpr int kBC = kPairTile * SPT * (OUTPUT ? 2 : 1);  // floats of a buffer
+    static constexpr int kBytesRaw = kStages * kTensors * kRaw * (int)sizeof(T);
+    static constexpr int kBytes = kBytesRaw + 2 * kBC * 4;
+};
+
+// Up to 16 states: a thread holds all SPT states of two neighbouring channels.  Tiles of 8
+// tokens: u, delta and z come by asynchronous copies two tiles ahead, B and C a tile ahead
+// through registers, double buffered in shared memory as float32: one barrier per tile.
+// A state beyond n has A = B = C = 0; EXACT (n == SPT) drops the selects that keep such states at
+// 0 where u is infinite.
+template <class T, int SPT, int PASS, bool EXACT>
+__global__ void __launch_bounds__(kPairThreads) k_scan(const ScanArgs a) {
+    using M = ScanPairSmem<T, SPT, PASS>;
+    constexpr int NT = kPairThreads, CT = kPairChannels, TK = kPairTile, ST = M::kStages;
     constexpr bool SUMMARY = PASS == SCAN_SUMMARY, OUTPUT = PASS == SCAN_OUTPUT;
-    constexpr int BCN = (TK * NP + kScanThreads - 1) / kScanThreads;  // B values per thread, tile
-    __shared__ alignas(16) float sB[2][TK][NP];
-    __shared__ alignas(16) float sC[2][OUTPUT ? TK : 1][NP];
-    const int n = (int)a.d.states, tid = (int)threadIdx.x, lane = tid & 31;
-    const bool packed = a.d.offsets != nullptr;
+    constexpr int BCN = (TK * SPT + NT - 1) / NT;  // B values per thread and tile
+    extern __shared__ float4 smem4[];
+    T* raw = reinterpret_cast<T*>(smem4);  // [stage][tensor][token][channel]
+    float* sbc = reinterpret_cast<float*>(reinterpret_cast<char*>(smem4) + M::kBytesRaw);
+
+    const int n = (int)a.d.states, tid = (int)threadIdx.x;
+    const bool packed = a.d.offsets != nullptr, gate = OUTPUT && a.d.z.data != nullptr;
     const int64_t nch = SUMMARY ? a.nchunks - 1 : a.nchunks;
     const int64_t mains = a.rows * nch * a.ctiles * a.d.groups;
-    if (OUTPUT && (int64_t)blockIdx.x >= mains) {
-        // the blocks behind: a sequence without tokens ends in its initial state
-        const int64_t q = blockIdx.x - mains, per = a.d.channels * n;
-        const bool empty = packed ? a.d.offsets[q] >= a.d.offsets[q + 1] : a.d.length == 0;
-        if (empty)
-            for (int64_t i = tid; i < per; i += kScanThreads)
-                a.final_state[q * per + i] = a.d.initial_state ? a.d.initial_state[q * per + i] : 0.f;
-        return;
-    }
+    if (OUTPUT && (int64_t)blockIdx.x >= mains) return scan_empty(a, blockIdx.x - mains);
     const ScanBlock blk = scan_block(a, blockIdx.x, nch, CT);
     SeqAt sq = seq_at(a.d.offsets, a.d.nseq, a.d.length, blk.row, blk.t0);
-    const int sl = lane / CL;
-    const int64_t c = blk.c0 + (tid >> 5) * CL + lane % CL;
-    const bool live = c < blk.cend;
-    const int s0 = sl * SPT;
-    const T* u = row_of<T>(a.d.u, packed, blk.row) + c;
-    const T* dl = row_of<T>(a.d.delta, packed, blk.row) + c;
-    const T* z = row_of<T>(a.d.z, packed, blk.row) + c;
-    const T* Bp = row_of<T>(a.d.B, packed, blk.row) + blk.g * n;
-    const T* Cp = row_of<T>(a.d.C, packed, blk.row) + blk.g * n;
-    T* out = const_cast<T*>(row_of<T>(a.out, packed, blk.row)) + c;
-    const bool gate = a.d.z.data != nullptr;
+    const int width = (int)(blk.cend - blk.c0 < CT ? blk.cend - blk.c0 : CT);  // channels here
+    const int lc = 2 * tid, len = (int)(blk.t1 - blk.t0);
+    const int64_t c = blk.c0 + lc;
+    const bool live[2] = {lc < width, lc + 1 < width};
+    // token t0 of the chunk; from here on tokens count from t0
+    const T* src[3] = {row_of<T>(a.d.u, packed, blk.row) + blk.t0 * a.d.u.tok_stride + blk.c0,
+                       row_of<T>(a.d.delta, packed, blk.row) + blk.t0 * a.d.delta.tok_stride + blk.c0,
+                       gate ? row_of<T>(a.d.z, packed, blk.row) + blk.t0 * a.d.z.tok_stride + blk.c0
+                            : nullptr};
+    const int64_t str[3] = {a.d.u.tok_stride, a.d.delta.tok_stride, a.d.z.tok_stride};
+    const T* Bp = row_of<T>(a.d.B, packed, blk.row) + blk.t0 * a.d.B.tok_stride + blk.g * n;
+    const T* Cp = row_of<T>(a.d.C, packed, blk.row) + blk.t0 * a.d.C.tok_stride + blk.g * n;
+
+    auto copy = [&](int t, int stage) {  // the tile at t; zeros beyond the chunk
+#pragma unroll
+        for (int k = 0; k < M::kTensors; ++k) {
+            if (k == 2 && !gate) break;
+            T* dst = raw + (stage * M::kTensors + k) * M::kRaw;
+            if (a.vec) {
+                constexpr int V = 16 / sizeof(T), R = CT / V, STEP = NT / R;
+                const int j0 = tid / R, x = (tid - j0 * R) * V;
+                const T* p = src[k] + (t + j0) * str[k] + x;
+#pragma unroll
+                for (int j = 0; j < TK; j += STEP, p += STEP * str[k]) {
+                    const bool in = t + j0 + j < len && x < width;
+                    copy16(dst + (j0 + j) * CT + x, in ? p : src[k], in);
+                }
+            } else {
+#pragma unroll 1
+                for (int j = 0; j < TK; j += 4) {
+                    T v[4][2];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            const int x = tid + e * NT;
+                            v[i][e] = t + j + i < len && x < width ? src[k][(t + j + i) * str[k] + x]
+                                                                   : from_f<T>(0.f);
+                        }
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) dst[(j + i) * CT + tid + e * NT] = v[i][e];
+                }
+            }
+        }
+        copy_commit();
+    };
+    T pB[BCN], pC[OUTPUT ? BCN : 1];
+    auto fetch = [&](int t) {  // B and C of the tile at t
+#pragma unroll
+        for (int i = 0; i < BCN; ++i) {
+            const int e = tid + i * NT, j = e / SPT, s = e - j * SPT;
+            const bool in = (TK * SPT % NT == 0 || e < TK * SPT) && s < n && t + j < len;
+            pB[i] = in ? Bp[(t + j) * a.d.B.tok_stride + s] : from_f<T>(0.f);
+            if (OUTPUT) pC[i] = in ? Cp[(t + j) * a.d.C.tok_stride + s] : from_f<T>(0.f);
+        }
+    };
+    auto stage_bc = [&](int buf) {
+        float* sB = sbc + buf * M::kBC;
+#pragma unroll
+        for (int i = 0; i < BCN; ++i) {
+            const int e = tid + i * NT;
+            if (TK * SPT % NT == 0 || e < TK * SPT) {
+                sB[e] = to_f(pB[i]);
+                if (OUTPUT) sB[TK * SPT + e] = to_f(pC[i]);
+            }
+        }
+    };
+#pragma unroll
+    for (int i = 0; i < ST - 1; ++i) copy(i * TK, i);
+    fetch(0);
+
+    float2 A2[2][SPT / 2], h[2][SPT / 2];
+    float2 bias = splat(0.f), D = splat(0.f), dsum = splat(0.f);
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+        load_states<SPT>(live[k] ? a.d.A + (c + k) * n : nullptr, 0, n, A2[k]);
+#pragma unroll
+        for (int i = 0; i < SPT / 2; ++i) A2[k][i] = mul2(A2[k][i], splat(kLog2e));
+        if (live[k] && a.d.delta_bias) (k ? bias.y : bias.x) = a.d.delta_bias[c + k];
+        if (OUTPUT && live[k] && a.d.D) (k ? D.y : D.x) = a.d.D[c + k];
+    }
+    auto initial = [&]() {
+#pragma unroll
+        for (int k = 0; k < 2; ++k)
+            load_states<SPT>(live[k] && a.d.initial_state
+                                 ? a.d.initial_state + (sq.q * a.d.channels + c + k) * n : nullptr,
+                             0, n, h[k]);
+    };
+    const int64_t carry_at = ((blk.row * a.nchunks + blk.chunk) * a.d.channels + c) * SPT;
+    bool has_reset = sq.begin == blk.t0;
+    if (sq.begin == blk.t0) {
+        initial();
+    } else {
+#pragma unroll
+        for (int k = 0; k < 2; ++k)
+            load_states<SPT>(!SUMMARY && live[k] ? a.carry + carry_at + k * SPT : nullptr, 0, SPT, h[k]);
+    }
+    stage_bc(0);
+    fetch(TK);
+    T* out = OUTPUT ? const_cast<T*>(row_of<T>(a.out, packed, blk.row)) + blk.t0 * a.out.tok_stride + c
+                    : nullptr;
+    const int64_t ostr = a.out.tok_stride;
+
+    int stage = 0, buf = 0;
+    for (int t = 0; t < len; t += TK) {
+        copy_wait<ST - 2>();
+        __syncthreads();  // this tile has landed; the last one's buffers are free
+        copy(t + (ST - 1) * TK, stage >= 1 ? stage - 1 : ST - 1);
+        stage_bc(buf ^ 1);
+        fetch(t + 2 * TK);
+        if (PASS == SCAN_TILES && t % kScanTile == 0) {
+            const int64_t tiles = (a.d.length + kScanTile - 1) / kScanTile;
+            float* p = a.tiles + ((blk.row * tiles + (blk.t0 + t) / kScanTile) * a.d.channels + c) * SPT;
+#pragma unroll
+            for (int k = 0; k < 2; ++k)
+                if (live[k]) store_states<SPT>(p + k * SPT, 0, SPT, h[k]);
+        }
+        const T* ru = raw + stage * M::kTensors * M::kRaw + lc;
+        const T* rd = ru + M::kRaw;
+        const T* rz = rd + M::kRaw;
+        const float* sB = sbc + buf * M::kBC;
+        const float* sC = sB + TK * SPT;
+        // N tokens at j: first d and d u of all, then the recurrence, then the gates, so that the
+        // long chains of softplus and the gate run side by side
+        auto tokens = [&](auto count, int j0) {
+            constexpr int N = decltype(count)::value;
+            float2 d[N], du[N], y[N];
+#pragma unroll
+            for (int j = 0; j < N; ++j) {
+                const Pack<T, 2> pd = ld_pack<2>(rd + (j0 + j) * CT), pu = ld_pack<2>(ru + (j0 + j) * CT);
+                d[j] = add2(make_float2(to_f(pd.v[0]), to_f(pd.v[1])), bias);
+                du[j] = make_float2(to_f(pu.v[0]), to_f(pu.v[1]));
+                y[j] = mul2(D, du[j]);
+            }
+            if (a.d.softplus) {
+#pragma unroll
+                for (int j = 0; j < N; ++j) d[j] = softplus2(d[j]);
+            }
+#pragma unroll
+            for (int j = 0; j < N; ++j) {
+                du[j] = mul2(d[j], du[j]);
+                if (SUMMARY) dsum = add2(dsum, d[j]);
+            }
+#pragma unroll
+            for (int j = 0; j < N; ++j) {
+                const float2 dd[2] = {splat(d[j].x), splat(d[j].y)};
+                const float2 dv[2] = {splat(du[j].x), splat(du[j].y)};
+                float2 acc[2][2] = {};
+#pragma unroll
+                for (int i = 0; i < SPT / 4; ++i) {
+                    const float4 b4 = *reinterpret_cast<const float4*>(sB + (j0 + j) * SPT + 4 * i);
+                    float4 c4;
+                    if (OUTPUT) c4 = *reinterpret_cast<const float4*>(sC + (j0 + j) * SPT + 4 * i);
+#pragma unroll
+                    for (int p = 0; p < 2; ++p) {
+                        const float2 b = p ? make_float2(b4.z, b4.w) : make_float2(b4.x, b4.y);
+#pragma unroll
+                        for (int k = 0; k < 2; ++k) {
+                            float2& hh = h[k][2 * i + p];
+                            const float2 e = mul2(dd[k], A2[k][2 * i + p]);
+                            hh = fma2(make_float2(ex2(e.x), ex2(e.y)), hh, mul2(dv[k], b));
+                            if (!EXACT) {
+                                if (4 * i + 2 * p >= n) hh.x = 0.f;
+                                if (4 * i + 2 * p + 1 >= n) hh.y = 0.f;
+                            }
+                            if (OUTPUT)
+                                acc[k][p] = fma2(p ? make_float2(c4.z, c4.w) : make_float2(c4.x, c4.y),
+                                                 hh, acc[k][p]);
+                        }
+                    }
+                }
+                if (OUTPUT) {
+                    const float2 s0 = add2(acc[0][0], acc[0][1]), s1 = add2(acc[1][0], acc[1][1]);
+                    y[j] = add2(y[j], make_float2(s0.x + s0.y, s1.x + s1.y));
+                }
+            }
+            if (OUTPUT) {
+                if (gate) {
+#pragma unroll
+                    for (int j = 0; j < N; ++j) {
+                        const Pack<T, 2> pz = ld_pack<2>(rz + (j0 + j) * CT);
+                        const float2 z = make_float2(to_f(pz.v[0]), to_f(pz.v[1]));
+                        y[j] = mul2(y[j], mul2(z, make_float2(sigmoid(z.x), sigmoid(z.y))));
+                    }
+                }
+                T* o = out + (t + j0) * ostr;
+#pragma unroll
+                for (int j = 0; j < N; ++j, o += ostr) {
+                    Pack<T, 2> po;
+                    po.v[0] = from_f<T>(y[j].x);
+                    po.v[1] = from_f<T>(y[j].y);
+                    if (a.pair) {
+                        if (live[0]) st_pack<2>(o, po);
+                    } else {
+                        if (live[0]) o[0] = po.v[0];
+                        if (live[1]) o[1] = po.v[1];
+                    }
+                }
+            }
+        };
+        const int64_t at = blk.t0 + t;
+        if (at + TK < sq.end) {  // no sequence ends here
+#pragma unroll 1
+            for (int j = 0; j < TK; j += kPairBatch) tokens(Count<kPairBatch>{}, j);
+        } else {
+            const int tl = len - t < TK ? len - t : TK;
+            int j = 0;
+            while (j < tl) {
+                if (at + j >= sq.end) {  // packed: the next sequence begins
+                    const int64_t q = sq.q;
+                    seq_next(a.d.offsets, a.d.nseq, at + j, &sq);
+                    if (sq.q != q) {
+                        initial();
+                        has_reset = true;
+                    }
+                }
+                const int je = sq.end > at + j && sq.end < at + tl ? (int)(sq.end - at) : tl;
+#pragma unroll 1
+                for (; j < je; ++j) tokens(Count<1>{}, j);
+                if (OUTPUT && a.final_state && at + j == sq.end) {
+#pragma unroll
+                    for (int k = 0; k < 2; ++k)
+                        if (live[k])
+                            store_states<SPT>(a.final_state + (sq.q * a.d.channels + c + k) * n, 0, n,
+                                              h[k]);
+                }
+            }
+        }
+        stage = stage + 1 < ST ? stage + 1 : 0;
+        buf ^= 1;
+    }
+    copy_wait<0>();
+    if (SUMMARY) {
+#pragma unroll
+        for (int k = 0; k < 2; ++k)
+            if (live[k]) {
+                store_states<SPT>(a.carry + carry_at + k * SPT, 0, SPT, h[k]);
+                a.dsum[(blk.row * a.nchunks + blk.chunk) * a.d.channels + c + k] = k ? dsum.y : dsum.x;
+            }
+        if (tid == 0 && blk.c0 == 0) a.reset[blk.row * a.nchunks + blk.chunk] = has_reset;
+    }
+}
+
+constexpr int kLanesThreads = 64, kLanesTile = 16, kLanesBatch = 8;
+
+template <class T, int SPT, int SL, int PASS>
+struct ScanLanesSmem {
+    static constexpr bool OUTPUT = PASS == SCAN_OUTPUT;
+    static constexpr int CT = kLanesThreads / SL, NP = SPT * SL;
+    static constexpr int kStages = 3, kRaw = kLanesTile * CT, kTensors = OUTPUT ? 3 : 2;
+    static constexpr int kBC = kLanesTile * NP * (OUTPUT ? 2 : 1);  // floats of a buffer
+    static constexpr int kBytesRaw = kStages * kTensors * kRaw * (int)sizeof(T);
+    static constexpr int kBytes = kBytesRaw + 2 * kBC * 4;
+};
+
+// SL lanes share a channel, SPT states each: more than 16 states, or enough channels to fill the
+// GPU without cutting time when each has more threads.  Tiles of 16 tokens in two batches of 8.
+// In a batch each lane prepares and finishes its own 8 / SL tokens (softplus, gate, store); d and
+// d u are broadcast from the token's lane, and the partial sums over states handed back to it.
+template <class T, int SPT, int SL, int PASS, bool EXACT>
+__global__ void __launch_bounds__(kLanesThreads) k_scan_lanes(const ScanArgs a) {
+    using M = ScanLanesSmem<T, SPT, SL, PASS>;
+    constexpr int NT = kLanesThreads, CT = M::CT, CL = 32 / SL, NP = M::NP, TK = kLanesTile;
+    constexpr int ST = M::kStages, N = kLanesBatch, OWN = N / SL;
+    constexpr bool SUMMARY = PASS == SCAN_SUMMARY, OUTPUT = PASS == SCAN_OUTPUT;
+    constexpr int BCN = TK * NP / NT;  // B values per thread and tile
+    extern __shared__ float4 smem4[];
+    T* raw = reinterpret_cast<T*>(smem4);  // [stage][tensor][token][channel]
+    float* sbc = reinterpret_cast<float*>(reinterpret_cast<char*>(smem4) + M::kBytesRaw);
+
+    const int n = (int)a.d.states, tid = (int)threadIdx.x, lane = tid & 31;
+    const bool packed = a.d.offsets != nullptr, gate = OUTPUT && a.d.z.data != nullptr;
+    const int64_t nch = SUMMARY ? a.nchunks - 1 : a.nchunks;
+    const int64_t mains = a.rows * nch * a.ctiles * a.d.groups;
+    if (OUTPUT && (int64_t)blockIdx.x >= mains) return scan_empty(a, blockIdx.x - mains);
+    const ScanBlock blk = scan_block(a, blockIdx.x, nch, CT);
+    SeqAt sq = seq_at(a.d.offsets, a.d.nseq, a.d.length, blk.row, blk.t0);
+    const int width = (int)(blk.cend - blk.c0 < CT ? blk.cend - blk.c0 : CT);  // channels here
+    const int sl = lane / CL, ch = lane % CL, lc = (tid >> 5) * CL + ch, s0 = sl * SPT;
+    const int len = (int)(blk.t1 - blk.t0);
+    const int64_t c = blk.c0 + lc;
+    const bool live = lc < width;
+    // token t0 of the chunk; from here on tokens count from t0
+    const T* src[3] = {row_of<T>(a.d.u, packed, blk.row) + blk.t0 * a.d.u.tok_stride + blk.c0,
+                       row_of<T>(a.d.delta, packed, blk.row) + blk.t0 * a.d.delta.tok_stride + blk.c0,
+                       gate ? row_of<T>(a.d.z, packed, blk.row) + blk.t0 * a.d.z.tok_stride + blk.c0
+                            : nullptr};
+    const int64_t str[3] = {a.d.u.tok_stride, a.d.delta.tok_stride, a.d.z.tok_stride};
+    const T* Bp = row_of<T>(a.d.B, packed, blk.row) + blk.t0 * a.d.B.tok_stride + blk.g * n;
+    const T* Cp = row_of<T>(a.d.C, packed, blk.row) + blk.t0 * a.d.C.tok_stride + blk.g * n;
+
+    auto copy = [&](int t, int stage) {  // the tile at t; zeros beyond the chunk
+#pragma unroll
+        for (int k = 0; k < M::kTensors; ++k) {
+            if (k == 2 && !gate) break;
+            T* dst = raw + (stage * M::kTensors + k) * M::kRaw;
+            if (a.vec) {
+                constexpr int V = 16 / sizeof(T), R = CT / V;
+#pragma unroll
+                for (int i = 0; i < (TK * R + NT - 1) / NT; ++i) {
+                    const int e = tid + i * NT, j = e / R, x = (e - j * R) * V;
+                    const bool in = t + j < len && x < width;
+                    if (TK * R % NT == 0 || e < TK * R)
+                        copy16(dst + j * CT + x, in ? src[k] + (t + j) * str[k] + x : src[k], in);
+                }
+            } else {
+                T v[TK / SL];
+#pragma unroll
+                for (int i = 0; i < TK / SL; ++i) {
+                    const int e = tid + i * NT, j = e / CT, x = e - j * CT;
+                    v[i] = t + j < len && x < width ? src[k][(t + j) * str[k] + x] : from_f<T>(0.f);
+                }
+#pragma unroll
+                for (int i = 0; i < TK / SL; ++i) dst[tid + i * NT] = v[i];
+            }
+        }
+        copy_commit();
+    };
+    T pB[BCN], pC[OUTPUT ? BCN : 1];
+    auto fetch = [&](int t) {  // B and C of the tile at t
+#pragma unroll
+        for (int i = 0; i < BCN; ++i) {
+            const int e = tid + i * NT, j = e / NP, s = e - j * NP;
+            const bool in = s < n && t + j < len;
+            pB[i] = in ? Bp[(t + j) * a.d.B.tok_stride + s] : from_f<T>(0.f);
+            if (OUTPUT) pC[i] = in ? Cp[(t + j) * a.d.C.tok_stride + s] : from_f<T>(0.f);
+        }
+    };
+    auto stage_bc = [&](int buf) {
+        float* sB = sbc + buf * M::kBC;
+#pragma unroll
+        for (int i = 0; i < BCN; ++i) {
+            sB[tid + i * NT] = to_f(pB[i]);
+            if (OUTPUT) sB[TK * NP + tid + i * NT] = to_f(pC[i]);
+        }
+    };
+#pragma unroll
+    for (int i = 0; i < ST - 1; ++i) copy(i * TK, i);
+    fetch(0);
 
     float2 A2[SPT / 2], h[SPT / 2];
     load_states<SPT>(live ? a.d.A + c * n : nullptr, s0, n, A2);
 #pragma unroll
-    for (int i = 0; i < SPT / 2; ++i) A2[i] = mul2(A2[i], make_float2(kLog2e, kLog2e));
+    for (int i = 0; i < SPT / 2; ++i) A2[i] = mul2(A2[i], splat(kLog2e));
     const float bias = live && a.d.delta_bias ? a.d.delta_bias[c] : 0.f;
-    const float D = live && a.d.D ? a.d.D[c] : 0.f;
+    const float D = OUTPUT && live && a.d.D ? a.d.D[c] : 0.f;
     auto initial = [&]() {
         load_states<SPT>(live && a.d.initial_state
                              ? a.d.initial_state + (sq.q * a.d.channels + c) * n : nullptr, s0, n, h);
@@ -112,121 +465,148 @@ __global__ void __launch_bounds__(kScanThreads) k_scan(const ScanArgs a) {
     bool has_reset = sq.begin == blk.t0;
     if (sq.begin == blk.t0)
         initial();
-    else if (SUMMARY)
-        load_states<SPT>(nullptr, s0, n, h);
     else
-        load_states<SPT>(live ? a.carry + carry_at : nullptr, s0, NP, h);
+        load_states<SPT>(!SUMMARY && live ? a.carry + carry_at : nullptr, s0, NP, h);
     float dsum = 0.f;
+    stage_bc(0);
+    fetch(TK);
+    T* out = OUTPUT ? const_cast<T*>(row_of<T>(a.out, packed, blk.row)) + blk.t0 * a.out.tok_stride + c
+                    : nullptr;
+    const int64_t ostr = a.out.tok_stride;
 
-    T pu[OWN], pd[OWN], pz[OWN], pB[BCN], pC[BCN];
-    auto fetch = [&](int64_t t) {  // tile at t into registers; zeros outside
-#pragma unroll
-        for (int j = 0; j < OWN; ++j) {
-            const int64_t tt = t + sl * OWN + j;
-            const bool in = live && tt < blk.t1;
-            pu[j] = in ? u[tt * a.d.u.tok_stride] : from_f<T>(0.f);
-            pd[j] = in ? dl[tt * a.d.delta.tok_stride] : from_f<T>(0.f);
-            if (OUTPUT) pz[j] = in && gate ? z[tt * a.d.z.tok_stride] : from_f<T>(0.f);
-        }
-#pragma unroll
-        for (int i = 0; i < BCN; ++i) {
-            const int k = tid + i * kScanThreads;
-            const int64_t tt = t + k / NP;
-            const bool in = k < TK * NP && k % NP < n && tt < blk.t1;
-            pB[i] = in ? Bp[tt * a.d.B.tok_stride + k % NP] : from_f<T>(0.f);
-            if (OUTPUT) pC[i] = in ? Cp[tt * a.d.C.tok_stride + k % NP] : from_f<T>(0.f);
-        }
-    };
-    auto stage = [&](int buf) {
-#pragma unroll
-        for (int i = 0; i < BCN; ++i) {
-            const int k = tid + i * kScanThreads;
-            if (k < TK * NP) {
-                (&sB[buf][0][0])[k] = to_f(pB[i]);
-                if (OUTPUT) (&sC[buf][0][0])[k] = to_f(pC[i]);
-            }
-        }
-    };
-    fetch(blk.t0);
-    stage(0);
-    __syncthreads();
-    int buf = 0;
-    for (int64_t t = blk.t0; t < blk.t1; t += TK) {
-        float od[OWN], ou[OWN], oz[OWN];  // the tokens that this lane owns
-#pragma unroll
-        for (int j = 0; j < OWN; ++j) {
-            const float e = to_f(pd[j]) + bias;
-            od[j] = a.d.softplus ? softplus(e) : e;
-            ou[j] = to_f(pu[j]);
-            if (OUTPUT) oz[j] = to_f(pz[j]);
-        }
-        if (PASS == SCAN_TILES && t % kScanStateTile == 0 && live) {
-            const int64_t tiles = (a.d.length + kScanStateTile - 1) / kScanStateTile;
-            store_states<SPT>(a.tiles + ((blk.row * tiles + t / kScanStateTile) * a.d.channels + c) * NP,
+    int stage = 0, buf = 0;
+    for (int t = 0; t < len; t += TK) {
+        copy_wait<ST - 2>();
+        __syncthreads();  // this tile has landed; the last one's buffers are free
+        copy(t + (ST - 1) * TK, stage >= 1 ? stage - 1 : ST - 1);
+        stage_bc(buf ^ 1);
+        fetch(t + 2 * TK);
+        static_assert(kLanesTile == kScanTile, "states are written once a tile");
+        if (PASS == SCAN_TILES && live) {
+            const int64_t tiles = (a.d.length + kScanTile - 1) / kScanTile;
+            store_states<SPT>(a.tiles + ((blk.row * tiles + (blk.t0 + t) / kScanTile) * a.d.channels + c) * NP,
                               s0, NP, h);
         }
-        if (t + TK < blk.t1) fetch(t + TK);
-        float y[TK];
+        const T* ru = raw + stage * M::kTensors * M::kRaw + lc;
+        const T* rd = ru + M::kRaw;
+        const T* rz = rd + M::kRaw;
+        const float* sB = sbc + buf * M::kBC + s0;
+        const float* sC = sB + TK * NP;
+        // the recurrence over one token; the sum over this lane's states
+        auto step = [&](int j, float d, float du) {
+            const float2 dd = splat(d), dv = splat(du);
+            float2 acc[2] = {};
 #pragma unroll
-        for (int j = 0; j < TK; ++j) {
-            if (t + j >= blk.t1) {
-                y[j] = 0.f;
-                continue;
-            }
-            if (t + j >= sq.end) {  // packed: the next sequence begins
-                seq_next(a.d.offsets, a.d.nseq, t + j, &sq);
-                initial();
-                has_reset = true;
-            }
-            float d = od[j % OWN], uu = ou[j % OWN];
-            if (SL > 1) {
-                d = __shfl_sync(0xffffffffu, d, (j / OWN) * CL + lane % CL);
-                uu = __shfl_sync(0xffffffffu, uu, (j / OWN) * CL + lane % CL);
-            }
-            if (SUMMARY) dsum += d;
-            const float2 dd = make_float2(d, d), du = make_float2(d * uu, d * uu);
-            float2 acc = make_float2(0.f, 0.f);
+            for (int i = 0; i < SPT / 4; ++i) {
+                const float4 b4 = *reinterpret_cast<const float4*>(sB + j * NP + 4 * i);
+                float4 c4;
+                if (OUTPUT) c4 = *reinterpret_cast<const float4*>(sC + j * NP + 4 * i);
 #pragma unroll
-            for (int i = 0; i < SPT / 2; ++i) {
-                const float2 arg = mul2(dd, A2[i]);
-                const float2 b = mul2(du, *reinterpret_cast<const float2*>(&sB[buf][j][s0 + 2 * i]));
-                h[i] = fma2(make_float2(ex2(arg.x), ex2(arg.y)), h[i], b);
-                if (!EXACT) {
-                    if (s0 + 2 * i >= n) h[i].x = 0.f;
-                    if (s0 + 2 * i + 1 >= n) h[i].y = 0.f;
-                }
-                if (OUTPUT)
-                    acc = fma2(*reinterpret_cast<const float2*>(&sC[buf][j][s0 + 2 * i]), h[i], acc);
-            }
-            y[j] = acc.x + acc.y;
-            if (OUTPUT && a.final_state && t + j + 1 == sq.end && live)
-                store_states<SPT>(a.final_state + (sq.q * a.d.channels + c) * n, s0, n, h);
-        }
-        if (OUTPUT) {
-            // sums over the SL lanes: each step halves the tokens that a lane still carries
-#pragma unroll
-            for (int w = SL / 2, cnt = TK / 2; w; w /= 2, cnt /= 2) {
-                const bool up = sl & w;
-#pragma unroll
-                for (int j = 0; j < cnt; ++j) {
-                    const float send = up ? y[j] : y[j + cnt], keep = up ? y[j + cnt] : y[j];
-                    y[j] = keep + __shfl_xor_sync(0xffffffffu, send, w * CL);
+                for (int p = 0; p < 2; ++p) {
+                    float2& hh = h[2 * i + p];
+                    const float2 e = mul2(dd, A2[2 * i + p]);
+                    hh = fma2(make_float2(ex2(e.x), ex2(e.y)), hh,
+                              mul2(dv, p ? make_float2(b4.z, b4.w) : make_float2(b4.x, b4.y)));
+                    if (!EXACT) {
+                        if (s0 + 4 * i + 2 * p >= n) hh.x = 0.f;
+                        if (s0 + 4 * i + 2 * p + 1 >= n) hh.y = 0.f;
+                    }
+                    if (OUTPUT)
+                        acc[p] = fma2(p ? make_float2(c4.z, c4.w) : make_float2(c4.x, c4.y), hh, acc[p]);
                 }
             }
+            const float2 y = add2(acc[0], acc[1]);
+            return y.x + y.y;
+        };
+        const int64_t at = blk.t0 + t;
+        if (at + TK < sq.end) {  // no sequence ends here
+#pragma unroll 1
+            for (int j0 = 0; j0 < TK; j0 += N) {
+                float2 d[(OWN + 1) / 2], du[(OWN + 1) / 2], uu[(OWN + 1) / 2];  // pairs of own tokens
+                const int own = j0 + sl * OWN;
 #pragma unroll
-            for (int j = 0; j < OWN; ++j) {
-                const int64_t tt = t + sl * OWN + j;
-                float v = fmaf(D, ou[j], y[j]);
-                if (gate) v *= oz[j] * sigmoid(oz[j]);
-                if (live && tt < blk.t1) out[tt * a.out.tok_stride] = from_f<T>(v);
+                for (int j = 0; j < OWN; ++j) {
+                    (j & 1 ? d[j / 2].y : d[j / 2].x) = to_f(rd[(own + j) * CT]) + bias;
+                    (j & 1 ? uu[j / 2].y : uu[j / 2].x) = to_f(ru[(own + j) * CT]);
+                }
+                if (OWN == 1) d[0].y = uu[0].y = 0.f;
+#pragma unroll
+                for (int j = 0; j < (OWN + 1) / 2; ++j) {
+                    if (a.d.softplus) d[j] = softplus2(d[j]);
+                    du[j] = mul2(d[j], uu[j]);
+                }
+                float y[N];
+#pragma unroll
+                for (int j = 0; j < N; ++j) {
+                    const int k = j % OWN, from = j / OWN * CL + ch;
+                    const float dj = __shfl_sync(0xffffffffu, k & 1 ? d[k / 2].y : d[k / 2].x, from);
+                    const float duj = __shfl_sync(0xffffffffu, k & 1 ? du[k / 2].y : du[k / 2].x, from);
+                    if (SUMMARY) dsum += dj;
+                    y[j] = step(j0 + j, dj, duj);
+                }
+                if (OUTPUT) {
+#pragma unroll
+                    for (int w = SL / 2, cnt = N / 2; w; w /= 2, cnt /= 2) {
+                        const bool up = sl & w;
+#pragma unroll
+                        for (int j = 0; j < N / 2; ++j) {
+                            if (j < cnt) {
+                                const float send = up ? y[j] : y[j + cnt], keep = up ? y[j + cnt] : y[j];
+                                y[j] = keep + __shfl_xor_sync(0xffffffffu, send, w * CL);
+                            }
+                        }
+                    }
+                    T* o = out + (t + own) * ostr;
+#pragma unroll
+                    for (int j = 0; j < OWN; ++j, o += ostr) {
+                        float v = fmaf(D, j & 1 ? uu[j / 2].y : uu[j / 2].x, y[j]);
+                        if (gate) {
+                            const float z = to_f(rz[(own + j) * CT]);
+                            v *= z * sigmoid(z);
+                        }
+                        if (live) *o = from_f<T>(v);
+                    }
+                }
+            }
+        } else {  // token by token, every lane preparing it
+            const int tl = len - t < TK ? len - t : TK;
+            int j = 0;
+            while (j < tl) {
+                if (at + j >= sq.end) {  // packed: the next sequence begins
+                    const int64_t q = sq.q;
+                    seq_next(a.d.offsets, a.d.nseq, at + j, &sq);
+                    if (sq.q != q) {
+                        initial();
+                        has_reset = true;
+                    }
+                }
+                const int je = sq.end > at + j && sq.end < at + tl ? (int)(sq.end - at) : tl;
+#pragma unroll 1
+                for (; j < je; ++j) {
+                    float d = to_f(rd[j * CT]) + bias;
+                    const float uj = to_f(ru[j * CT]);
+                    if (a.d.softplus) d = softplus(d);
+                    if (SUMMARY) dsum += d;
+                    float y = step(j, d, d * uj);
+                    if (OUTPUT) {
+#pragma unroll
+                        for (int w = 1; w < SL; w *= 2) y += __shfl_xor_sync(0xffffffffu, y, w * CL);
+                        y = fmaf(D, uj, y);
+                        if (gate) {
+                            const float z = to_f(rz[j * CT]);
+                            y *= z * sigmoid(z);
+                        }
+                        if (live && sl == 0) out[(t + j) * ostr] = from_f<T>(y);
+                    }
+                }
+                if (OUTPUT && a.final_state && at + j == sq.end && live)
+                    store_states<SPT>(a.final_state + (sq.q * a.d.channels + c) * n, s0, n, h);
             }
         }
-        if (t + TK < blk.t1) {
-            buf ^= 1;
-            stage(buf);
-            __syncthreads();
-        }
+        stage = stage + 1 < ST ? stage + 1 : 0;
+        buf ^= 1;
     }
+    copy_wait<0>();
     if (SUMMARY) {
         if (live) {
             store_states<SPT>(a.carry + carry_at, s0, NP, h);
@@ -236,11 +616,14 @@ __global__ void __launch_bounds__(kScanThreads) k_scan(const ScanArgs a) {
     }
 }
 
+// Few threads and a chain of chunks: small blocks on many SMs, and many chunks loaded at once.
+constexpr int kCarryThreads = 64, kCarryAhead = 32;
+
 // Pass 2: along the chunks of every (row, channel, state); the state after a chunk that a
 // sequence starts in does not depend on what came before.
 template <int NP>
-__global__ void __launch_bounds__(256) k_scan_carry(const ScanArgs a) {
-    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x, per = a.d.channels * NP;
+__global__ void __launch_bounds__(kCarryThreads) k_scan_carry(const ScanArgs a) {
+    const int64_t i = (int64_t)blockIdx.x * kCarryThreads + threadIdx.x, per = a.d.channels * NP;
     if (i >= a.rows * per) return;
     const int64_t row = i / per, cs = i - row * per, c = cs / NP;
     const int s = (int)(cs - c * NP), n = (int)a.d.states;
@@ -249,14 +632,16 @@ __global__ void __launch_bounds__(256) k_scan_carry(const ScanArgs a) {
     const float* dsum = a.dsum + row * a.nchunks * a.d.channels + c;
     const int* reset = a.reset + row * a.nchunks;
     float h = 0.f;
-    constexpr int U = 8;
+    constexpr int U = kCarryAhead;
     for (int64_t k = 0; k < a.nchunks; k += U) {
         float local[U], decay[U];
 #pragma unroll
         for (int j = 0; j < U; ++j) {
             if (k + j < a.nchunks - 1) {
+                const int cut = reset[k + j];
+                const float sum = dsum[(k + j) * a.d.channels];
                 local[j] = carry[(k + j) * per];
-                decay[j] = reset[k + j] ? -1.f : ex2(A2 * dsum[(k + j) * a.d.channels]);
+                decay[j] = cut ? -1.f : ex2(A2 * sum);
             }
         }
 #pragma unroll
@@ -268,6 +653,29 @@ __global__ void __launch_bounds__(256) k_scan_carry(const ScanArgs a) {
     }
 }
 
+// SL 0: k_scan, otherwise k_scan_lanes.
+template <class T, int SPT, int SL, int PASS, bool EXACT>
+cudaError_t scan_kernel(const ScanArgs& a, int64_t blocks, cudaStream_t s) {
+    static LaunchCache cache;
+    LaunchGeom geo;
+    if constexpr (SL == 0) {
+        constexpr int bytes = ScanPairSmem<T, SPT, PASS>::kBytes;
+        const cudaError_t e = cache.get([](int dev, LaunchGeom* g) {
+            return setup_persistent(k_scan<T, SPT, PASS, EXACT>, kPairThreads, bytes, dev, g);
+        }, &geo);
+        if (e != cudaSuccess) return e;
+        k_scan<T, SPT, PASS, EXACT><<<(unsigned)blocks, kPairThreads, bytes, s>>>(a);
+    } else {
+        constexpr int bytes = ScanLanesSmem<T, SPT, SL, PASS>::kBytes;
+        const cudaError_t e = cache.get([](int dev, LaunchGeom* g) {
+            return setup_persistent(k_scan_lanes<T, SPT, SL, PASS, EXACT>, kLanesThreads, bytes, dev, g);
+        }, &geo);
+        if (e != cudaSuccess) return e;
+        k_scan_lanes<T, SPT, SL, PASS, EXACT><<<(unsigned)blocks, kLanesThreads, bytes, s>>>(a);
+    }
+    return cudaGetLastError();
+}
+
 // Passes 1 and 2 where time is cut, then the pass that was asked for.
 template <class T, int SPT, int SL, int PASS, bool EXACT>
 cudaError_t scan_launch(const ScanArgs& a, cudaStream_t s) {
@@ -277,30 +685,43 @@ cudaError_t scan_launch(const ScanArgs& a, cudaStream_t s) {
     if (blocks < 1) return cudaSuccess;
     if (blocks > INT32_MAX) return cudaErrorInvalidValue;
     if (a.nchunks > 1) {
-        k_scan<T, SPT, SL, SCAN_SUMMARY, EXACT>
-            <<<(unsigned)(a.rows * (a.nchunks - 1) * tiles), kScanThreads, 0, s>>>(a);
-        k_scan_carry<SPT * SL>
-            <<<(unsigned)((a.rows * a.d.channels * SPT * SL + 255) / 256), 256, 0, s>>>(a);
+        const cudaError_t e = scan_kernel<T, SPT, SL, SCAN_SUMMARY, EXACT>(
+            a, a.rows * (a.nchunks - 1) * tiles, s);
+        if (e != cudaSuccess) return e;
+        constexpr int NP = SPT * (SL ? SL : 1);
+        k_scan_carry<NP><<<(unsigned)((a.rows * a.d.channels * NP + kCarryThreads - 1) / kCarryThreads),
+                           kCarryThreads, 0, s>>>(a);
     }
-    k_scan<T, SPT, SL, PASS, EXACT><<<(unsigned)blocks, kScanThreads, 0, s>>>(a);
-    return cudaGetLastError();
+    return scan_kernel<T, SPT, SL, PASS, EXACT>(a, blocks, s);
 }
 
 template <class T, int SPT, int SL, int PASS>
 cudaError_t scan_exact(const ScanArgs& a, cudaStream_t s) {
-    return a.d.states == SPT * SL ? scan_launch<T, SPT, SL, PASS, true>(a, s)
-                                  : scan_launch<T, SPT, SL, PASS, false>(a, s);
+    return a.d.states == SPT * (SL ? SL : 1) ? scan_launch<T, SPT, SL, PASS, true>(a, s)
+                                             : scan_launch<T, SPT, SL, PASS, false>(a, s);
 }
 template <class T, int PASS>
-cudaError_t scan_run(const ScanArgs& a, cudaStream_t s) {
-    const ScanShape sh = scan_shape(a.d.states);
-    if (sh.sl == 1)
-        return sh.spt == 4 ? scan_exact<T, 4, 1, PASS>(a, s)
-                           : (sh.spt == 8 ? scan_exact<T, 8, 1, PASS>(a, s)
-                                          : scan_exact<T, 16, 1, PASS>(a, s));
-    return sh.sl == 2 ? scan_exact<T, 16, 2, PASS>(a, s)
-                      : (sh.sl == 4 ? scan_exact<T, 16, 4, PASS>(a, s)
-                                    : scan_exact<T, 16, 8, PASS>(a, s));
+cudaError_t scan_run(ScanArgs a, cudaStream_t s) {
+    const bool packed = a.d.offsets != nullptr;
+    const int64_t dg = a.d.channels / a.d.groups;
+    auto rows_on = [&](const fft_seq& q, int64_t bytes) {
+        return !q.data || (aligned_to(q.data, bytes) && q.tok_stride * sizeof(T) % bytes == 0 &&
+                           (packed || q.seq_stride * sizeof(T) % bytes == 0));
+    };
+    a.vec = dg * sizeof(T) % 16 == 0 && rows_on(a.d.u, 16) && rows_on(a.d.delta, 16) &&
+            rows_on(a.d.z, 16);
+    a.pair = dg % 2 == 0 && rows_on(a.out, 2 * sizeof(T));
+    switch (scan_np(a.d.states) * 100 + a.sl) {
+        case 400: return scan_exact<T, 4, 0, PASS>(a, s);
+        case 800: return scan_exact<T, 8, 0, PASS>(a, s);
+        case 802: return scan_exact<T, 4, 2, PASS>(a, s);
+        case 1600: return scan_exact<T, 16, 0, PASS>(a, s);
+        case 1602: return scan_exact<T, 8, 2, PASS>(a, s);
+        case 3202: return scan_exact<T, 16, 2, PASS>(a, s);
+        case 6404: return scan_exact<T, 16, 4, PASS>(a, s);
+        case 12808: return scan_exact<T, 16, 8, PASS>(a, s);
+        default: return cudaErrorInvalidValue;
+    }
 }
 
 }  // namespace gbfft

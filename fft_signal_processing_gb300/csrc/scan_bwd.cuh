@@ -24,21 +24,19 @@
 
 namespace gbfft {
 
-__device__ __forceinline__ float2 add2(float2 a, float2 b) {
-    return make_float2(a.x + b.x, a.y + b.y);
-}
-
 // The gradient that a chunk sends back, with nothing entering from behind.
 template <class T, int SPT, int SL>
 __global__ void __launch_bounds__(kScanThreads) k_scan_back(const ScanBwdArgs a) {
-    constexpr int NP = SPT * SL, CT = kScanThreads / SL, TK = kScanTile, OWN = TK / SL;
+    constexpr int NP = SPT * SL, CT = kScanThreads / SL, TK = 8, OWN = TK / SL;
     constexpr int CL = 32 / SL;
     constexpr int CN = (TK * NP + kScanThreads - 1) / kScanThreads;
     __shared__ alignas(16) float sC[TK][NP];
     const int n = (int)a.d.states, tid = (int)threadIdx.x, lane = tid & 31;
     const bool packed = a.d.offsets != nullptr, gate = a.d.z.data != nullptr;
     // chunk 0 sends nothing on: blocks are the chunks 1 ...
-    ScanBlock blk = scan_block(a.f, blockIdx.x, a.f.nchunks - 1, CT);
+    ScanArgs f = a.f;
+    f.ctiles = a.back_ctiles;
+    ScanBlock blk = scan_block(f, blockIdx.x, a.f.nchunks - 1, CT);
     blk.chunk += 1;
     blk.t0 += a.f.chunk;
     blk.t1 = blk.t0 + a.f.chunk < a.d.length ? blk.t0 + a.f.chunk : a.d.length;
@@ -120,8 +118,8 @@ __global__ void __launch_bounds__(kScanThreads) k_scan_back(const ScanBwdArgs a)
 
 // From the last chunk to the first: the gradient that enters every chunk from behind.
 template <int NP>
-__global__ void __launch_bounds__(256) k_scan_back_carry(const ScanBwdArgs a) {
-    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x, per = a.d.channels * NP;
+__global__ void __launch_bounds__(kCarryThreads) k_scan_back_carry(const ScanBwdArgs a) {
+    const int64_t i = (int64_t)blockIdx.x * kCarryThreads + threadIdx.x, per = a.d.channels * NP;
     if (i >= a.f.rows * per) return;
     const int64_t row = i / per, cs = i - row * per, c = cs / NP, nch = a.f.nchunks;
     const int s = (int)(cs - c * NP), n = (int)a.d.states;
@@ -130,16 +128,17 @@ __global__ void __launch_bounds__(256) k_scan_back_carry(const ScanBwdArgs a) {
     const float* dsum = a.f.dsum + row * nch * a.d.channels + c;
     const int* reset = a.f.reset + row * nch;
     float m = 0.f;
-    constexpr int U = 8;
+    constexpr int U = kCarryAhead;
     for (int64_t k = nch - 1; k >= 0; k -= U) {
         float local[U], decay[U];
 #pragma unroll
         for (int j = 0; j < U; ++j) {
             if (k - j > 0) {
-                local[j] = carry[(k - j) * per];
                 // nothing enters the last chunk, and its sum of d is not known
-                decay[j] = k - j == nch - 1 || reset[k - j]
-                               ? -1.f : ex2(A2 * dsum[(k - j) * a.d.channels]);
+                const int cut = k - j == nch - 1 || reset[k - j];
+                const float sum = dsum[(k - j) * a.d.channels];
+                local[j] = carry[(k - j) * per];
+                decay[j] = cut ? -1.f : ex2(A2 * sum);
             }
         }
 #pragma unroll
@@ -178,7 +177,7 @@ template <int SL>
 struct BwdShape {
     static constexpr int NW = SL < 4 ? SL : 4, NT = NW * 32, CL = 32 / SL, CW = CL * 4;
     static constexpr int CT = NW * CW, NP = SL * 4;
-    static constexpr int TK = kScanStateTile, TS = 4, PIECES = TK / TS;
+    static constexpr int TK = kScanTile, TS = 4, PIECES = TK / TS;
     // shared memory, in floats
     static constexpr int kIn = TK * CT;               // d, u, dy
     static constexpr int kBC = TK * NP * 2;           // B, C, each value twice
@@ -589,11 +588,12 @@ cudaError_t scan_bwd_main(const ScanBwdArgs& a, cudaStream_t s) {
 }
 template <class T, int SPT, int SL>
 cudaError_t scan_bwd_back(const ScanBwdArgs& a, cudaStream_t s) {
-    const int64_t tiles = a.f.ctiles * a.d.groups;
+    const int64_t tiles = a.back_ctiles * a.d.groups;
     k_scan_back<T, SPT, SL>
         <<<(unsigned)(a.f.rows * (a.f.nchunks - 1) * tiles), kScanThreads, 0, s>>>(a);
     k_scan_back_carry<SPT * SL>
-        <<<(unsigned)((a.f.rows * a.d.channels * SPT * SL + 255) / 256), 256, 0, s>>>(a);
+        <<<(unsigned)((a.f.rows * a.d.channels * SPT * SL + kCarryThreads - 1) / kCarryThreads),
+           kCarryThreads, 0, s>>>(a);
     return cudaGetLastError();
 }
 
@@ -602,16 +602,17 @@ cudaError_t scan_bwd_run(const ScanBwdArgs& a, cudaStream_t s) {
     cudaError_t e = cudaSuccess;
     const int64_t n = a.d.states, parts = a.f.rows * a.f.nchunks;
     if (a.d.length > 0) {
-        if (parts * a.f.ctiles * a.d.groups > INT32_MAX) return cudaErrorInvalidValue;
+        if (parts * a.back_ctiles * a.d.groups > INT32_MAX) return cudaErrorInvalidValue;
         e = scan_run<T, SCAN_TILES>(a.f, s);
         if (e == cudaSuccess && a.f.nchunks > 1) {
-            const ScanShape sh = scan_shape(n);
-            if (sh.sl == 1)
-                e = sh.spt == 4 ? scan_bwd_back<T, 4, 1>(a, s)
-                                : (sh.spt == 8 ? scan_bwd_back<T, 8, 1>(a, s) : scan_bwd_back<T, 16, 1>(a, s));
-            else
-                e = sh.sl == 2 ? scan_bwd_back<T, 16, 2>(a, s)
-                               : (sh.sl == 4 ? scan_bwd_back<T, 16, 4>(a, s) : scan_bwd_back<T, 16, 8>(a, s));
+            switch (scan_np(n)) {
+                case 4: e = scan_bwd_back<T, 4, 1>(a, s); break;
+                case 8: e = scan_bwd_back<T, 8, 1>(a, s); break;
+                case 16: e = scan_bwd_back<T, 16, 1>(a, s); break;
+                case 32: e = scan_bwd_back<T, 16, 2>(a, s); break;
+                case 64: e = scan_bwd_back<T, 16, 4>(a, s); break;
+                default: e = scan_bwd_back<T, 16, 8>(a, s); break;
+            }
         }
         if (e != cudaSuccess) return e;
         switch (bwd_sl(n)) {

@@ -16,6 +16,7 @@ struct ScanBwdArgs {
     float* pD;         // partial dD [rows * chunks][channels]
     float* pbias;      // partial ddelta_bias [rows * chunks][channels]
     int64_t ctiles;    // channel tiles per group of the main kernel
+    int64_t back_ctiles;  // and of the pass that finds what the chunks send back
 };
 
 // Lanes that share a channel and warps per block of the main kernel: a thread holds 4 channels x

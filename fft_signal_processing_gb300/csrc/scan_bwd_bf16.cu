@@ -1,5 +1,4 @@
 // Selective state-space scan of bf16 sequences, backward.
-#include "launch_cache.cuh"
 #include "scan_bwd.cuh"
 
 namespace gbfft {

@@ -83,31 +83,63 @@ int check_scan(const fft_scan_desc* d, bool pointers) {
 
 int64_t up16(int64_t bytes) { return (bytes + 15) / 16 * 16; }
 
-// Forward workspace: carry, dsum, reset.
-int64_t scan_layout(const fft_scan_desc& d, ScanArgs* a) {
-    const ScanChunks p = scan_chunks(d);
-    const int64_t np = scan_shape(d.states).np(), ch = p.rows * p.nchunks;
-    const int64_t carry = p.nchunks > 1 ? up16(ch * d.channels * np * 4) : 0;
-    const int64_t dsum = p.nchunks > 1 ? up16(ch * d.channels * 4) : 0;
-    const int64_t reset = p.nchunks > 1 ? up16(ch * 4) : 0;
-    if (a) {
-        char* w = reinterpret_cast<char*>(a->carry);
-        a->dsum = reinterpret_cast<float*>(w + carry);
-        a->reset = reinterpret_cast<int*>(w + carry + dsum);
-        a->rows = p.rows;
-        a->chunk = p.chunk;
-        a->nchunks = p.nchunks;
-        a->ctiles = p.ctiles;
+// Forward plan and workspace: carry, dsum, reset.
+int64_t scan_layout(const fft_scan_desc& d, ScanArgs* a, char* w) {
+    ScanArgs b = {};
+    if (a) b = *a;
+    b.d = d;
+    scan_plan(&b);
+    int64_t at = 0;
+    auto take = [&](int64_t bytes) {
+        char* p = w ? w + at : nullptr;
+        at += up16(bytes);
+        return p;
+    };
+    if (b.nchunks > 1) {
+        const int64_t ch = b.rows * b.nchunks;
+        b.carry = reinterpret_cast<float*>(take(ch * d.channels * scan_np(d.states) * 4));
+        b.dsum = reinterpret_cast<float*>(take(ch * d.channels * 4));
+        b.reset = reinterpret_cast<int*>(take(ch * 4));
     }
-    return carry + dsum + reset;
+    if (a) *a = b;
+    return at;
 }
 
 }  // namespace
 
 namespace gbfft {
 
+void scan_plan(ScanArgs* a) {
+    const fft_scan_desc& d = a->d;
+    const int np = scan_np(d.states);
+    const int64_t dg = d.channels / d.groups;
+    a->rows = d.offsets ? 1 : d.nseq;
+    auto blocks = [&](int sl) {
+        const int ct = scan_channels(sl);
+        return a->rows * d.groups * ((dg + ct - 1) / ct);
+    };
+    a->sl = scan_lanes(np);
+    // Uncut with two lanes per channel where that alone gives every SM four blocks or more (8
+    // sequences x 4096 channels: 0.44 ms, cut in two with k_scan 0.51 ms); else about six blocks of
+    // k_scan for every SM (one sequence of 16384 x 2048: 0.28 ms at 4 to 6, 0.33 ms at 5 or 8).
+    const int64_t sms = num_sms();
+    int64_t k = 1;
+    if ((np == 8 || np == 16) && blocks(2) >= sms * 4)
+        a->sl = 2;
+    else
+        k = (sms * 6 + blocks(a->sl) / 2) / blocks(a->sl);
+    a->ctiles = blocks(a->sl) / (a->rows * d.groups);
+    a->chunk = d.length;
+    if (k > 1) {
+        a->chunk = (d.length + k - 1) / k;
+        a->chunk = (a->chunk + 15) / 16 * 16;
+    }
+    if (a->chunk < 64) a->chunk = 64;
+    a->nchunks = (d.length + a->chunk - 1) / a->chunk;
+}
+
 int64_t scan_bwd_layout(const fft_scan_desc& d, ScanBwdArgs* a, char* w) {
-    const int64_t n = d.states, np = scan_shape(n).np(), sl = bwd_sl(n), ct = bwd_channels((int)sl);
+    const int64_t n = d.states, np = scan_np(n), sl = bwd_sl(n), ct = bwd_channels((int)sl);
     const int64_t dg = d.channels / d.groups, rows = d.offsets ? 1 : d.nseq;
     const int64_t ctiles = (dg + ct - 1) / ct;
     // chunks: enough blocks of the main kernel to fill the GPU (two to an SM) several times
@@ -117,7 +149,7 @@ int64_t scan_bwd_layout(const fft_scan_desc& d, ScanBwdArgs* a, char* w) {
     chunk = (chunk + 63) / 64 * 64;
     if (chunk < 64) chunk = 64;
     const int64_t nchunks = (d.length + chunk - 1) / chunk;
-    const int64_t state_tiles = (d.length + kScanStateTile - 1) / kScanStateTile;
+    const int64_t state_tiles = (d.length + kScanTile - 1) / kScanTile;
     int64_t at = 0;
     auto take = [&](int64_t floats) {
         float* p = reinterpret_cast<float*>(w ? w + at : nullptr);
@@ -132,7 +164,11 @@ int64_t scan_bwd_layout(const fft_scan_desc& d, ScanBwdArgs* a, char* w) {
     b.f.rows = rows;
     b.f.chunk = chunk;
     b.f.nchunks = nchunks;
-    b.f.ctiles = (dg + kScanThreads / scan_shape(n).sl - 1) / (kScanThreads / scan_shape(n).sl);
+    b.f.sl = scan_lanes((int)np);
+    const int64_t fct = scan_channels(b.f.sl);
+    b.f.ctiles = (dg + fct - 1) / fct;
+    const int64_t bct = np <= 16 ? kScanThreads : kScanThreads * 16 / np;
+    b.back_ctiles = (dg + bct - 1) / bct;
     if (nchunks > 1) {
         b.f.carry = take(parts * per);
         b.f.dsum = take(parts * d.channels);
@@ -236,7 +272,8 @@ extern "C" int fft_conv_step(const fft_conv_desc* d, const fft_seq* out, void* s
 extern "C" int fft_scan_workspace(const fft_scan_desc* d, int backward, size_t* bytes) {
     if (!bytes || (backward != 0 && backward != 1)) return FFT_ERR_INVALID_ARG;
     TRY(check_scan(d, false));
-    *bytes = (size_t)(backward ? scan_bwd_layout(*d, nullptr, nullptr) : scan_layout(*d, nullptr));
+    *bytes = (size_t)(backward ? scan_bwd_layout(*d, nullptr, nullptr)
+                               : scan_layout(*d, nullptr, nullptr));
     return FFT_OK;
 }
 
@@ -250,8 +287,7 @@ extern "C" int fft_scan_forward(const fft_scan_desc* d, const fft_seq* out, floa
     a.d = *d;
     a.out = *out;
     a.final_state = final_state;
-    a.carry = static_cast<float*>(workspace);
-    const int64_t need = scan_layout(*d, &a);
+    const int64_t need = scan_layout(*d, &a, static_cast<char*>(workspace));
     if (need > 0 && (!workspace || workspace_bytes < (size_t)need)) return FFT_ERR_INVALID_ARG;
     cudaStream_t s = (cudaStream_t)stream;
     return status(d->dtype == FFT_F32 ? scan_forward_f32(a, s)

@@ -58,26 +58,6 @@ __device__ __forceinline__ float rcp(float x) {
 // 1 / (1 + exp(-x)): exp(-x) overflows to infinity for x < -88 and the quotient is 0.
 __device__ __forceinline__ float sigmoid(float x) { return rcp(1.0f + ex2(-kLog2e * x)); }
 
-// log(1 + exp(x)) = max(x, 0) + log1p(t), t = exp(-|x|) in (0, 1], log1p(t) = 2 atanh(t / (2 + t))
-// by the odd series in s = t / (2 + t) <= 1/3, whose terms left out are below 2e-8 of the sum.
-// The exponent's rounding error is put back, since t is the result itself where x << 0.
-__device__ __forceinline__ float softplus(float x) {
-    const float y = -fabsf(x);
-    const float hi = y * kLog2e;
-    const float lo = fmaf(y, kLog2e, -hi) + y * 1.9259630e-8f;  // log2(e) beyond 24 bits
-    float t = ex2(hi);
-    t = fmaf(t, lo * kLn2, t);
-    if (!(y > -88.f)) t = y != y ? y : 0.f;  // exp underflows; -inf would leave lo a NaN
-    const float s = t * rcp(2.f + t), q = s * s;
-    float p = fmaf(q, 1.f / 13.f, 1.f / 11.f);
-    p = fmaf(q, p, 1.f / 9.f);
-    p = fmaf(q, p, 1.f / 7.f);
-    p = fmaf(q, p, 1.f / 5.f);
-    p = fmaf(q, p, 1.f / 3.f);
-    p = fmaf(q, p, 1.f);
-    return fmaxf(x, 0.f) + 2.f * s * p;
-}
-
 // Two float32 values in one 64-bit register pair: sm_103a multiplies and adds both at once.
 __device__ __forceinline__ float2 mul2(float2 a, float2 b) {
     float2 d;
@@ -95,6 +75,55 @@ __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
           "l"(reinterpret_cast<unsigned long long&>(b)),
           "l"(reinterpret_cast<unsigned long long&>(c)));
     return d;
+}
+
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+    float2 d;
+    asm("add.rn.f32x2 %0, %1, %2;"
+        : "=l"(reinterpret_cast<unsigned long long&>(d))
+        : "l"(reinterpret_cast<unsigned long long&>(a)),
+          "l"(reinterpret_cast<unsigned long long&>(b)));
+    return d;
+}
+__device__ __forceinline__ float2 splat(float v) { return make_float2(v, v); }
+__device__ __forceinline__ float max_nan(float a, float b) {  // a NaN stays
+    float d;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
+    return d;
+}
+
+// log(1 + exp(x)) = max(x, 0) + log1p(t), t = exp(-|x|) in (0, 1], and log1p(t) = 2 atanh(w) with
+// w = t / (2 + t) <= 1/3: w times a polynomial in w^2, interpolated at Chebyshev nodes of
+// [0, 1/9] (relative error 8e-9).  The exponent's rounding error is put back, since t is the
+// result itself where x << 0; below -87, where t leaves the normal range, the result stays there.
+__device__ __forceinline__ float2 softplus2(float2 x) {
+    const float2 y = make_float2(max_nan(-fabsf(x.x), -87.f), max_nan(-fabsf(x.y), -87.f));
+    const float2 hi = mul2(y, splat(kLog2e));
+    float2 lo = fma2(y, splat(kLog2e), make_float2(-hi.x, -hi.y));
+    lo = fma2(y, splat(1.9259630e-8f), lo);  // log2(e) beyond 24 bits
+    float2 t = make_float2(ex2(hi.x), ex2(hi.y));
+    t = fma2(mul2(lo, splat(kLn2)), t, t);
+    const float2 den = add2(t, splat(2.f));
+    const float2 w = mul2(t, make_float2(rcp(den.x), rcp(den.y))), q = mul2(w, w);
+    float2 p = fma2(q, splat(0.28157779574394226f), splat(0.27965158224105835f));
+    p = fma2(q, p, splat(0.4002459645271301f));
+    p = fma2(q, p, splat(0.6666632294654846f));
+    p = fma2(q, p, splat(2.f));
+    return fma2(w, p, make_float2(max_nan(x.x, 0.f), max_nan(x.y, 0.f)));
+}
+__device__ __forceinline__ float softplus(float x) { return softplus2(splat(x)).x; }
+
+// Asynchronous copy of 16 bytes into shared memory; zeros where `in` is false (nothing is read).
+__device__ __forceinline__ void copy16(void* dst, const void* src, bool in) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(
+                     (unsigned)__cvta_generic_to_shared(dst)),
+                 "l"(src), "r"(in ? 16 : 0)
+                 : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copy_wait() {  // all but the last N groups have landed
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
 // Number of ascending offsets[0 .. n-1] that are <= t, found by a whole warp: 32 probes a step

@@ -19,40 +19,19 @@ Outputs and workspaces are allocated by torch on the stream that the call runs o
 """
 import contextlib
 import ctypes
+import struct
 from typing import NamedTuple, Optional
-
-_i32, _i64, _vp = ctypes.c_int32, ctypes.c_int64, ctypes.c_void_p
 
 F32, BF16, F16, E4M3 = 0, 1, 2, 3
 
-
-class Seq(ctypes.Structure):  # fft_seq
-    _fields_ = [("data", _vp), ("seq_stride", _i64), ("tok_stride", _i64)]
-
-
-class ConvDesc(ctypes.Structure):  # fft_conv_desc
-    _fields_ = [("dtype", _i32), ("param_dtype", _i32), ("width", _i32), ("silu", _i32),
-                ("nseq", _i64), ("length", _i64), ("channels", _i64), ("offsets", _vp),
-                ("weight", _vp), ("bias", _vp), ("initial_state", _vp), ("x", Seq)]
-
-
-class ScanDesc(ctypes.Structure):  # fft_scan_desc
-    _fields_ = [("dtype", _i32), ("softplus", _i32), ("nseq", _i64), ("length", _i64),
-                ("channels", _i64), ("groups", _i64), ("states", _i64), ("offsets", _vp),
-                ("A", _vp), ("D", _vp), ("delta_bias", _vp), ("initial_state", _vp), ("u", Seq),
-                ("delta", Seq), ("B", Seq), ("C", Seq), ("z", Seq)]
-
-
-class ScanGradsArg(ctypes.Structure):  # fft_scan_grads
-    _fields_ = [("dout", Seq), ("dfinal_state", _vp), ("du", Seq), ("ddelta", Seq), ("dB", Seq),
-                ("dC", Seq), ("dz", Seq), ("dA", _vp), ("dD", _vp), ("ddelta_bias", _vp),
-                ("dinitial_state", _vp)]
-
-
-class NormDesc(ctypes.Structure):  # fft_norm_desc
-    _fields_ = [("dtype", _i32), ("res_dtype", _i32), ("param_dtype", _i32), ("out_dtype", _i32),
-                ("rows", _i64), ("columns", _i64), ("group", _i64), ("eps", ctypes.c_float),
-                ("weight", _vp)]
+# The descriptors of include/gbfft.h, packed in one go: building a ctypes structure field by field
+# takes longer than a single-token call's kernel.
+_SEQ = struct.Struct("@P2q")  # fft_seq
+_CONV = struct.Struct("@4i3q4PP2q")  # fft_conv_desc
+_SCAN = struct.Struct("@2i5q5P" + "P2q" * 5)  # fft_scan_desc
+_GRADS = struct.Struct("@P2qP" + "P2q" * 5 + "4P")  # fft_scan_grads
+_NORM = struct.Struct("@4i3qfP")  # fft_norm_desc
+_NONE = (0, 0, 0)  # an absent fft_seq
 
 
 class ConvGrads(NamedTuple):
@@ -88,20 +67,19 @@ class NormGrads(NamedTuple):
 
 def declare(L):
     """Argument types of the sequence operators (called when the library is loaded)."""
-    pc, ps, pn, pq = (ctypes.POINTER(t) for t in (ConvDesc, ScanDesc, NormDesc, Seq))
-    sz = ctypes.c_size_t
-    L.fft_conv_forward.argtypes = [pc, pq, _vp, _vp]
-    L.fft_conv_workspace.argtypes = [pc, ctypes.POINTER(sz)]
-    L.fft_conv_backward.argtypes = [pc, pq, _vp, pq, _vp, _vp, _vp, _vp, sz, _vp]
-    L.fft_conv_step.argtypes = [pc, pq, _vp, _i64, _vp, _vp, _vp]
-    L.fft_scan_workspace.argtypes = [ps, ctypes.c_int, ctypes.POINTER(sz)]
-    L.fft_scan_forward.argtypes = [ps, pq, _vp, _vp, sz, _vp]
-    L.fft_scan_backward.argtypes = [ps, ctypes.POINTER(ScanGradsArg), _vp, sz, _vp]
-    L.fft_scan_step.argtypes = [ps, pq, _vp, _i64, _vp, _vp, _vp]
-    L.fft_norm_forward.argtypes = [pn, _vp, _i64, _vp, _i64, _vp, _i64, _vp, _vp, _i64, _vp]
-    L.fft_norm_workspace.argtypes = [pn, ctypes.POINTER(sz)]
-    L.fft_norm_backward.argtypes = [pn, _vp, _i64, _vp, _i64, _vp, _i64, _vp, _i64, _vp, _i64,
-                                    _vp, _vp, sz, _vp]
+    desc, vp, i64, sz = ctypes.c_char_p, ctypes.c_void_p, ctypes.c_int64, ctypes.c_size_t
+    L.fft_conv_forward.argtypes = [desc, desc, vp, vp]
+    L.fft_conv_workspace.argtypes = [desc, ctypes.POINTER(sz)]
+    L.fft_conv_backward.argtypes = [desc, desc, vp, desc, vp, vp, vp, vp, sz, vp]
+    L.fft_conv_step.argtypes = [desc, desc, vp, i64, vp, vp, vp]
+    L.fft_scan_workspace.argtypes = [desc, ctypes.c_int, ctypes.POINTER(sz)]
+    L.fft_scan_forward.argtypes = [desc, desc, vp, vp, sz, vp]
+    L.fft_scan_backward.argtypes = [desc, desc, vp, sz, vp]
+    L.fft_scan_step.argtypes = [desc, desc, vp, i64, vp, vp, vp]
+    L.fft_norm_forward.argtypes = [desc, vp, i64, vp, i64, vp, i64, vp, vp, i64, vp]
+    L.fft_norm_workspace.argtypes = [desc, ctypes.POINTER(sz)]
+    L.fft_norm_backward.argtypes = [desc, vp, i64, vp, i64, vp, i64, vp, i64, vp, i64, vp, vp, sz,
+                                    vp]
 
 
 SYMBOLS = ("fft_conv_forward", "fft_conv_workspace", "fft_conv_backward", "fft_conv_step",
@@ -111,21 +89,21 @@ SYMBOLS = ("fft_conv_forward", "fft_conv_workspace", "fft_conv_backward", "fft_c
 
 # ---- checks ---------------------------------------------------------------------------------
 
-_CODES = {}
+_L = torch = _CODES = _raw_stream = None
 
 
-def _codes():
-    if not _CODES:
-        import torch
+def _setup():
+    """Bind the library and torch on the first call."""
+    global _L, torch, _CODES, _raw_stream
+    import torch as _torch
 
-        _CODES.update({torch.float32: F32, torch.bfloat16: BF16, torch.float16: F16})
-    return _CODES
-
-
-def _lib():
     from . import lib
 
-    return lib()
+    _CODES = {_torch.float32: F32, _torch.bfloat16: BF16, _torch.float16: F16}
+    _raw_stream = getattr(_torch._C, "_cuda_getCurrentRawStream", None) or (
+        lambda device: _torch.cuda.current_stream(device).cuda_stream)
+    torch = _torch
+    _L = lib()
 
 
 def _check(rc, what):
@@ -135,104 +113,105 @@ def _check(rc, what):
         raise GbfftError(rc, what)
 
 
-def _dtype(t, what):
-    code = _codes().get(getattr(t, "dtype", None))
-    if code is None:
+def _first(t, what):
+    """(type code, device index) of the tensor that the others are compared with."""
+    if _L is None:
+        _setup()
+    code = _CODES.get(getattr(t, "dtype", None))
+    if code is None or not t.is_cuda:
         raise TypeError(f"{what}: expected a float32, bfloat16 or float16 CUDA tensor")
-    return code
+    dev = t.get_device()
+    if dev != torch.cuda.current_device():  # the library launches there
+        raise ValueError(f"{what}: expected a tensor on the current CUDA device")
+    return code, dev
 
 
-def _need(t, like, shape, dtype, what):
-    """t on like's device, of this dtype (None: like's) and shape, its last axis contiguous."""
-    if not hasattr(t, "data_ptr") or not t.is_cuda or t.device != like.device:
-        raise TypeError(f"{what}: expected a CUDA tensor on {like.device}")
-    if t.dtype != (like.dtype if dtype is None else dtype):
-        raise TypeError(f"{what}: expected {like.dtype if dtype is None else dtype}, got {t.dtype}")
+def _tell(t, dev, dtype, shape, what):
+    """Say what is wrong with a tensor that failed a check."""
+    if not hasattr(t, "data_ptr") or not t.is_cuda or t.get_device() != dev:
+        raise TypeError(f"{what}: expected a CUDA tensor on device {dev}")
+    if t.dtype != dtype:
+        raise TypeError(f"{what}: expected {dtype}, got {t.dtype}")
     if tuple(t.shape) != tuple(shape):
         raise ValueError(f"{what}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
-    if t.stride(-1) != 1 and t.shape[-1] > 1:
-        raise ValueError(f"{what}: the last axis must be contiguous")
+    raise ValueError(f"{what}: the last axis must be contiguous, and parameters and states whole")
+
+
+def _need(t, dev, dtype, shape, what):
+    """t on the device, of this dtype and shape, its last axis contiguous."""
+    if (getattr(t, "dtype", None) is not dtype or t.shape != shape or t.get_device() != dev
+            or (t.stride(-1) != 1 and t.shape[-1] > 1)):
+        _tell(t, dev, dtype, shape, what)
     return t
 
 
-def _flat(t, like, shape, dtype, what):
-    """The address of a contiguous tensor, or None for None."""
+def _flat(t, dev, dtype, shape, what):
+    """The address of a contiguous tensor, or 0 for None."""
     if t is None:
-        return None
-    _need(t, like, shape, dtype, what)
-    if not t.is_contiguous():
-        raise ValueError(f"{what}: tensor must be contiguous")
+        return 0
+    if (getattr(t, "dtype", None) is not dtype or t.shape != shape or t.get_device() != dev
+            or not t.is_contiguous()):
+        _tell(t, dev, dtype, shape, what)
     return t.data_ptr()
 
 
-def _on(t):
-    """The tensor's device has to be the current one: the library launches there."""
-    import torch
-
-    if not t.is_cuda:
-        raise TypeError("expected CUDA tensors")
-    if t.device.index != torch.cuda.current_device():
-        raise ValueError("expected tensors on the current CUDA device")
-
-
-def _offsets(offsets, like):
+def _offsets(offsets, dev):
     if offsets is None:
-        return None
-    import torch
-
+        return 0
     if offsets.dim() != 1 or offsets.numel() < 2:
         raise ValueError("offsets: expected one more value than sequences")
-    return _flat(offsets, like, offsets.shape, torch.int64, "offsets")
+    return _flat(offsets, dev, torch.int64, offsets.shape, "offsets")
 
 
 def _seq(t, packed):
-    return Seq(t.data_ptr(), 0, t.stride(0)) if packed else Seq(t.data_ptr(), t.stride(0), t.stride(1))
+    """The fields of an fft_seq."""
+    if t is None:
+        return _NONE
+    return (t.data_ptr(), 0, t.stride(0)) if packed else (t.data_ptr(), t.stride(0), t.stride(1))
 
 
 def _row(t):
-    return Seq(t.data_ptr(), t.stride(0), 0)
+    return (t.data_ptr(), t.stride(0), 0) if t is not None else _NONE
 
 
-def _groups(t, like, lead, what):
+def _ptr(t):
+    return t.data_ptr() if t is not None else None
+
+
+def _groups(t, dev, dtype, lead, what):
     """B or C: [..., groups, n] or [..., n], groups back to back."""
     if t.dim() == len(lead) + 1:
         t = t.unsqueeze(-2)
-    _need(t, like, (*lead, *t.shape[-2:]), None, what)
-    if t.shape[-2] > 1 and t.stride(-2) != t.shape[-1]:
+    shape = t.shape
+    if (t.dtype is not dtype or shape[:-2] != lead or t.get_device() != dev
+            or (t.stride(-1) != 1 and shape[-1] > 1)):
+        _tell(t, dev, dtype, (*lead, *shape[-2:]), what)
+    if shape[-2] > 1 and t.stride(-2) != shape[-1]:
         raise ValueError(f"{what}: the groups must lie back to back")
     return t
 
 
-def _empty(like, shape=None, dtype=None):
-    import torch
-
-    return torch.empty(like.shape if shape is None else shape,
-                       dtype=like.dtype if dtype is None else dtype, device=like.device)
-
-
-def _out(out, like, shape=None):
+def _out(out, like, dev):
     if out is None:
-        return _empty(like, shape)
-    return _need(out, like, like.shape if shape is None else shape, None, "out")
+        return like.new_empty(like.shape)
+    return _need(out, dev, like.dtype, like.shape, "out")
 
 
 _SAME = contextlib.nullcontext()
 
 
-def _stream(stream):
+def _stream(stream, dev):
     """(context in which torch allocates for the stream, the stream's handle)."""
-    import torch
-
     if stream is None:
-        return _SAME, torch.cuda.current_stream().cuda_stream
+        return _SAME, _raw_stream(dev)
     return torch.cuda.stream(stream), stream.cuda_stream
 
 
 def _workspace(fn, args, like, what):
-    import torch
-
+    """(tensor, address, bytes): the tensor is freed to torch's allocator when the caller is done
+    with it, which hands it out again on this stream only."""
     size = ctypes.c_size_t()
-    _check(fn(*args, ctypes.byref(size)), what)
+    _check(fn(*args, size), what)
     if size.value == 0:
         return None, None, 0
     w = torch.empty(size.value, dtype=torch.uint8, device=like.device)
@@ -244,34 +223,38 @@ def _lead(x, offsets, what):
     if x.dim() != (2 if packed else 3):
         raise ValueError(f"{what}: expected [tokens, channels] with offsets, "
                          "[sequences, tokens, channels] without")
-    nseq = offsets.numel() - 1 if packed else x.shape[0]
-    return packed, nseq, (x.shape[0] if packed else x.shape[1])
+    shape = x.shape
+    return packed, offsets.numel() - 1 if packed else shape[0], shape[0] if packed else shape[1]
 
 
 # ---- short causal convolution ---------------------------------------------------------------
 
 
 def _conv_desc(x, weight, bias, silu, initial_state, offsets, step=False):
-    code = _dtype(x, "x")
-    _on(x)
-    d = x.shape[-1]
-    off = _offsets(offsets, x)
+    """(packed fft_conv_desc, device, sequences, channels, width)."""
+    code, dev = _first(x, "x")
+    dtype, shape = x.dtype, x.shape
+    d = shape[-1]
     if step:
-        packed, nseq, length = False, x.shape[0], 1
+        if x.dim() != 2:
+            raise ValueError("x: expected [sequences, channels]")
+        packed, nseq, length = False, shape[0], 1
     else:
         packed, nseq, length = _lead(x, offsets, "x")
-    _need(x, x, x.shape, None, "x")
+    if x.stride(-1) != 1 and d > 1:
+        _tell(x, dev, dtype, shape, "x")
     if weight.dim() != 2:
         raise ValueError("weight: expected [channels, width]")
-    w = weight.shape[1]
-    pcode = _dtype(weight, "weight")
-    if pcode not in (F32, code):
+    w, ptype = weight.shape[1], weight.dtype
+    if ptype is not dtype and ptype is not torch.float32:
         raise TypeError("weight: expected float32 or the type of x")
-    return ConvDesc(code, pcode, w, int(bool(silu)), nseq, length, d, off,
-                    _flat(weight, x, (d, w), weight.dtype, "weight"),
-                    _flat(bias, x, (d,), weight.dtype, "bias"),
-                    _flat(initial_state, x, (nseq, w - 1, d), None, "initial_state"),
-                    _row(x) if step else _seq(x, packed))
+    desc = _CONV.pack(code, F32 if ptype is torch.float32 else code, w, 1 if silu else 0, nseq,
+                      length, d, _offsets(offsets, dev),
+                      _flat(weight, dev, ptype, (d, w), "weight"),
+                      _flat(bias, dev, ptype, (d,), "bias"),
+                      _flat(initial_state, dev, dtype, (nseq, w - 1, d), "initial_state"),
+                      *(_row(x) if step else _seq(x, packed)))
+    return desc, dev, nseq, d, w
 
 
 def causal_conv(x, weight, bias=None, silu=False, initial_state=None, offsets=None,
@@ -279,62 +262,49 @@ def causal_conv(x, weight, bias=None, silu=False, initial_state=None, offsets=No
     """Short causal convolution of every channel (fft_conv_forward): weight [channels, width],
     bias [channels], both float32 or of x's type; initial_state [sequences, width-1, channels].
     Returns out, or (out, final_state)."""
-    desc = _conv_desc(x, weight, bias, silu, initial_state, offsets)
-    on, s = _stream(stream)
+    desc, dev, nseq, d, w = _conv_desc(x, weight, bias, silu, initial_state, offsets)
+    on, s = _stream(stream, dev)
     with on:
-        out = _out(out, x)
-        state = _empty(x, (desc.nseq, desc.width - 1, desc.channels)) if return_state else None
-        _check(_lib().fft_conv_forward(desc, _seq(out, offsets is not None),
-                                       state.data_ptr() if return_state else None, s),
-               "fft_conv_forward")
+        out = _out(out, x, dev)
+        state = x.new_empty((nseq, w - 1, d)) if return_state else None
+        _check(_L.fft_conv_forward(desc, _SEQ.pack(*_seq(out, offsets is not None)), _ptr(state),
+                                   s), "fft_conv_forward")
     return (out, state) if return_state else out
 
 
 def causal_conv_backward(dout, x, weight, bias=None, silu=False, initial_state=None, offsets=None,
                          dfinal_state=None, stream=None):
     """Gradients of causal_conv from dout (and dfinal_state): ConvGrads."""
-    import torch
-
-    desc = _conv_desc(x, weight, bias, silu, initial_state, offsets)
-    _need(dout, x, x.shape, None, "dout")
-    packed, shape = offsets is not None, (desc.nseq, desc.width - 1, desc.channels)
-    dfin = _flat(dfinal_state, x, shape, None, "dfinal_state")
-    on, s = _stream(stream)
+    desc, dev, nseq, d, w = _conv_desc(x, weight, bias, silu, initial_state, offsets)
+    _need(dout, dev, x.dtype, x.shape, "dout")
+    packed, shape = offsets is not None, (nseq, w - 1, d)
+    dfin = _flat(dfinal_state, dev, x.dtype, shape, "dfinal_state")
+    on, s = _stream(stream, dev)
     with on:
-        dx = _empty(x)
-        dw = _empty(x, weight.shape, torch.float32)
-        db = _empty(x, (desc.channels,), torch.float32) if bias is not None else None
-        di = _empty(x, shape) if initial_state is not None else None
-        w, wp, size = _workspace(_lib().fft_conv_workspace, (desc,), x, "fft_conv_workspace")
-        _check(_lib().fft_conv_backward(desc, _seq(dout, packed), dfin, _seq(dx, packed),
-                                        dw.data_ptr(), db.data_ptr() if db is not None else None,
-                                        di.data_ptr() if di is not None else None, wp, size, s),
-               "fft_conv_backward")
+        dx = x.new_empty(x.shape)
+        dw = x.new_empty(weight.shape, dtype=torch.float32)
+        db = x.new_empty((d,), dtype=torch.float32) if bias is not None else None
+        di = x.new_empty(shape) if initial_state is not None else None
+        ws, wp, size = _workspace(_L.fft_conv_workspace, (desc,), x, "fft_conv_workspace")
+        _check(_L.fft_conv_backward(desc, _SEQ.pack(*_seq(dout, packed)), dfin,
+                                    _SEQ.pack(*_seq(dx, packed)), dw.data_ptr(), _ptr(db),
+                                    _ptr(di), wp, size, s), "fft_conv_backward")
     return ConvGrads(dx, dw, db, di)
-
-
-def _slot(t, like, nseq, what):
-    if t is None:
-        return None
-    import torch
-
-    return _flat(t, like, (nseq,), torch.int64, what)
 
 
 def causal_conv_step(state, x, weight, bias=None, silu=False, slots=None, slots_out=None, out=None,
                      stream=None):
     """One token for each sequence (fft_conv_step): x [sequences, channels], state the pool
     [pool, width-1, channels], updated in place; slots, slots_out int64 [sequences]."""
-    if x.dim() != 2:
-        raise ValueError("x: expected [sequences, channels]")
-    desc = _conv_desc(x, weight, bias, silu, None, None, step=True)
-    pool = _flat(state, x, (state.shape[0], desc.width - 1, desc.channels), None, "state")
-    on, s = _stream(stream)
+    desc, dev, nseq, d, w = _conv_desc(x, weight, bias, silu, None, None, step=True)
+    size = state.shape[0]
+    pool = _flat(state, dev, x.dtype, (size, w - 1, d), "state")
+    on, s = _stream(stream, dev)
     with on:
-        out = _out(out, x)
-        _check(_lib().fft_conv_step(desc, _row(out), pool, state.shape[0],
-                                    _slot(slots, x, desc.nseq, "slots"),
-                                    _slot(slots_out, x, desc.nseq, "slots_out"), s),
+        out = _out(out, x, dev)
+        _check(_L.fft_conv_step(desc, _SEQ.pack(*_row(out)), pool, size,
+                                _flat(slots, dev, torch.int64, (nseq,), "slots"),
+                                _flat(slots_out, dev, torch.int64, (nseq,), "slots_out"), s),
                "fft_conv_step")
     return out
 
@@ -343,31 +313,35 @@ def causal_conv_step(state, x, weight, bias=None, silu=False, slots=None, slots_
 
 
 def _scan_desc(u, delta, A, B, C, D, z, delta_bias, softplus, initial_state, offsets, step=False):
-    import torch
-
-    f32 = torch.float32
-    code = _dtype(u, "u")
-    _on(u)
-    d = u.shape[-1]
-    off = _offsets(offsets, u)
+    """(packed fft_scan_desc, device, sequences, channels, states)."""
+    code, dev = _first(u, "u")
+    f32, dtype, shape = torch.float32, u.dtype, u.shape
+    d, lead = shape[-1], shape[:-1]
     if step:
-        packed, nseq, length = False, u.shape[0], 1
+        if u.dim() != 2:
+            raise ValueError("u: expected [sequences, channels]")
+        packed, nseq, length = False, shape[0], 1
     else:
         packed, nseq, length = _lead(u, offsets, "u")
-    _need(u, u, u.shape, None, "u")
-    _need(delta, u, u.shape, None, "delta")
-    lead = u.shape[:-1]
-    B, C = _groups(B, u, lead, "B"), _groups(C, u, lead, "C")
+    if u.stride(-1) != 1 and d > 1:
+        _tell(u, dev, dtype, shape, "u")
+    _need(delta, dev, dtype, shape, "delta")
+    B, C = _groups(B, dev, dtype, lead, "B"), _groups(C, dev, dtype, lead, "C")
     groups, n = B.shape[-2:]
-    if C.shape[-2:] != B.shape[-2:]:
+    if C.shape != B.shape:
         raise ValueError("C: expected the shape of B")
-    view = _row if step else (lambda t: _seq(t, packed))
-    return ScanDesc(code, int(bool(softplus)), nseq, length, d, groups, n, off,
-                    _flat(A, u, (d, n), f32, "A"), _flat(D, u, (d,), f32, "D"),
-                    _flat(delta_bias, u, (d,), f32, "delta_bias"),
-                    _flat(initial_state, u, (nseq, d, n), f32, "initial_state"),
-                    view(u), view(delta), view(B), view(C),
-                    view(_need(z, u, u.shape, None, "z")) if z is not None else Seq())
+    if z is not None:
+        _need(z, dev, dtype, shape, "z")
+    heads = (code, 1 if softplus else 0, nseq, length, d, groups, n, _offsets(offsets, dev),
+             _flat(A, dev, f32, (d, n), "A"), _flat(D, dev, f32, (d,), "D"),
+             _flat(delta_bias, dev, f32, (d,), "delta_bias"),
+             _flat(initial_state, dev, f32, (nseq, d, n), "initial_state"))
+    if step:
+        desc = _SCAN.pack(*heads, *_row(u), *_row(delta), *_row(B), *_row(C), *_row(z))
+    else:
+        desc = _SCAN.pack(*heads, *_seq(u, packed), *_seq(delta, packed), *_seq(B, packed),
+                          *_seq(C, packed), *_seq(z, packed))
+    return desc, dev, nseq, d, n
 
 
 def selective_scan(u, delta, A, B, C, D=None, z=None, delta_bias=None, softplus=False,
@@ -375,18 +349,15 @@ def selective_scan(u, delta, A, B, C, D=None, z=None, delta_bias=None, softplus=
     """Selective state-space scan (fft_scan_forward): u, delta, z [..., channels], A [channels, n],
     B, C [..., groups, n] or [..., n], D, delta_bias [channels]; states [sequences, channels, n].
     A, D, delta_bias and states are float32.  Returns out, or (out, final_state)."""
-    import torch
-
-    desc = _scan_desc(u, delta, A, B, C, D, z, delta_bias, softplus, initial_state, offsets)
-    on, s = _stream(stream)
+    desc, dev, nseq, d, n = _scan_desc(u, delta, A, B, C, D, z, delta_bias, softplus,
+                                       initial_state, offsets)
+    on, s = _stream(stream, dev)
     with on:
-        out = _out(out, u)
-        state = (_empty(u, (desc.nseq, desc.channels, desc.states), torch.float32)
-                 if return_state else None)
-        w, wp, size = _workspace(_lib().fft_scan_workspace, (desc, 0), u, "fft_scan_workspace")
-        _check(_lib().fft_scan_forward(desc, _seq(out, offsets is not None),
-                                       state.data_ptr() if return_state else None, wp, size, s),
-               "fft_scan_forward")
+        out = _out(out, u, dev)
+        state = u.new_empty((nseq, d, n), dtype=torch.float32) if return_state else None
+        ws, wp, size = _workspace(_L.fft_scan_workspace, (desc, 0), u, "fft_scan_workspace")
+        _check(_L.fft_scan_forward(desc, _SEQ.pack(*_seq(out, offsets is not None)), _ptr(state),
+                                   wp, size, s), "fft_scan_forward")
     return (out, state) if return_state else out
 
 
@@ -394,28 +365,26 @@ def selective_scan_backward(dout, u, delta, A, B, C, D=None, z=None, delta_bias=
                             softplus=False, initial_state=None, offsets=None, dfinal_state=None,
                             stream=None):
     """Gradients of selective_scan from dout (and dfinal_state): ScanGrads."""
-    import torch
-
+    desc, dev, nseq, d, n = _scan_desc(u, delta, A, B, C, D, z, delta_bias, softplus,
+                                       initial_state, offsets)
     f32 = torch.float32
-    desc = _scan_desc(u, delta, A, B, C, D, z, delta_bias, softplus, initial_state, offsets)
-    _need(dout, u, u.shape, None, "dout")
-    packed, shape = offsets is not None, (desc.nseq, desc.channels, desc.states)
-    dfin = _flat(dfinal_state, u, shape, f32, "dfinal_state")
-    on, s = _stream(stream)
+    _need(dout, dev, u.dtype, u.shape, "dout")
+    packed, shape = offsets is not None, (nseq, d, n)
+    dfin = _flat(dfinal_state, dev, f32, shape, "dfinal_state")
+    on, s = _stream(stream, dev)
     with on:
-        du, dd = _empty(u), _empty(u)
-        dz = _empty(u) if z is not None else None
-        dB, dC = _empty(u, B.shape), _empty(u, C.shape)
-        dA = _empty(u, A.shape, f32)
-        dD = _empty(u, D.shape, f32) if D is not None else None
-        db = _empty(u, delta_bias.shape, f32) if delta_bias is not None else None
-        di = _empty(u, shape, f32) if initial_state is not None else None
-        at = [t.data_ptr() if t is not None else None for t in (dA, dD, db, di)]
-        grads = ScanGradsArg(_seq(dout, packed), dfin, _seq(du, packed), _seq(dd, packed),
-                             _seq(dB, packed), _seq(dC, packed),
-                             _seq(dz, packed) if dz is not None else Seq(), *at)
-        w, wp, size = _workspace(_lib().fft_scan_workspace, (desc, 1), u, "fft_scan_workspace")
-        _check(_lib().fft_scan_backward(desc, grads, wp, size, s), "fft_scan_backward")
+        du, dd = u.new_empty(u.shape), u.new_empty(u.shape)
+        dz = u.new_empty(u.shape) if z is not None else None
+        dB, dC = u.new_empty(B.shape), u.new_empty(C.shape)
+        dA = u.new_empty((d, n), dtype=f32)
+        dD = u.new_empty((d,), dtype=f32) if D is not None else None
+        db = u.new_empty((d,), dtype=f32) if delta_bias is not None else None
+        di = u.new_empty(shape, dtype=f32) if initial_state is not None else None
+        grads = _GRADS.pack(*_seq(dout, packed), dfin, *_seq(du, packed), *_seq(dd, packed),
+                            *_seq(dB, packed), *_seq(dC, packed), *_seq(dz, packed),
+                            *[_ptr(t) or 0 for t in (dA, dD, db, di)])
+        ws, wp, size = _workspace(_L.fft_scan_workspace, (desc, 1), u, "fft_scan_workspace")
+        _check(_L.fft_scan_backward(desc, grads, wp, size, s), "fft_scan_backward")
     return ScanGrads(du, dd, dA, dB, dC, dD, dz, db, di)
 
 
@@ -424,18 +393,16 @@ def selective_scan_step(state, u, delta, A, B, C, D=None, z=None, delta_bias=Non
     """One token for each sequence (fft_scan_step): u, delta, z [sequences, channels], B, C
     [sequences, groups, n] or [sequences, n], state the pool [pool, channels, n] float32, updated
     in place; slots, slots_out int64 [sequences]."""
-    import torch
-
-    if u.dim() != 2:
-        raise ValueError("u: expected [sequences, channels]")
-    desc = _scan_desc(u, delta, A, B, C, D, z, delta_bias, softplus, None, None, step=True)
-    pool = _flat(state, u, (state.shape[0], desc.channels, desc.states), torch.float32, "state")
-    on, s = _stream(stream)
+    desc, dev, nseq, d, n = _scan_desc(u, delta, A, B, C, D, z, delta_bias, softplus, None, None,
+                                       step=True)
+    size = state.shape[0]
+    pool = _flat(state, dev, torch.float32, (size, d, n), "state")
+    on, s = _stream(stream, dev)
     with on:
-        out = _out(out, u)
-        _check(_lib().fft_scan_step(desc, _row(out), pool, state.shape[0],
-                                    _slot(slots, u, desc.nseq, "slots"),
-                                    _slot(slots_out, u, desc.nseq, "slots_out"), s),
+        out = _out(out, u, dev)
+        _check(_L.fft_scan_step(desc, _SEQ.pack(*_row(out)), pool, size,
+                                _flat(slots, dev, torch.int64, (nseq,), "slots"),
+                                _flat(slots_out, dev, torch.int64, (nseq,), "slots_out"), s),
                "fft_scan_step")
     return out
 
@@ -445,10 +412,13 @@ def selective_scan_step(state, u, delta, A, B, C, D=None, z=None, delta_bias=Non
 
 def _rows(t):
     """[..., columns] as rows of one stride: (rows, stride)."""
-    if t.dim() < 2:
+    dim = t.dim()
+    if dim == 2:
+        return t.shape[0], t.stride(0)
+    if dim < 2:
         return (1, t.shape[-1])
     rows, stride = t.shape[-2], t.stride(-2)
-    for k in range(t.dim() - 3, -1, -1):
+    for k in range(dim - 3, -1, -1):
         if t.shape[k] != 1 and rows != 1 and t.stride(k) != rows * stride:
             raise ValueError("expected rows at one stride")
         if rows == 1:
@@ -457,17 +427,20 @@ def _rows(t):
     return rows, stride
 
 
-def _norm_desc(x, res_dtype, weight, eps, out_code, group):
-    code = _dtype(x, "x")
-    _on(x)
-    _need(x, x, x.shape, None, "x")
+def _norm_desc(x, res_dtype, weight, eps, e4m3, group):
+    """(packed fft_norm_desc, device, columns, row stride of x)."""
+    code, dev = _first(x, "x")
     d = x.shape[-1]
+    if x.stride(-1) != 1 and d > 1:
+        _tell(x, dev, x.dtype, x.shape, "x")
     rows, stride = _rows(x)
-    pcode = _dtype(weight, "weight")
-    if pcode not in (F32, code):
+    ptype = weight.dtype
+    if ptype is not x.dtype and ptype is not torch.float32:
         raise TypeError("weight: expected float32 or the type of x")
-    return NormDesc(code, _codes().get(res_dtype, -1), pcode, code if out_code is None else out_code,
-                    rows, d, group, eps, _flat(weight, x, (d,), weight.dtype, "weight")), stride
+    desc = _NORM.pack(code, _CODES.get(res_dtype, -1), F32 if ptype is torch.float32 else code,
+                      E4M3 if e4m3 else code, rows, d, group, eps,
+                      _flat(weight, dev, ptype, (d,), "weight"))
+    return desc, dev, d, stride
 
 
 def residual_norm(x, weight, residual=None, eps=1e-6, out_dtype=None, group=0, out=None,
@@ -476,55 +449,54 @@ def residual_norm(x, weight, residual=None, eps=1e-6, out_dtype=None, group=0, o
     residual is of x's type or float32, and so is the sum that is returned (written over it with
     inplace_residual).  out_dtype torch.float8_e4m3fn: out in 8 bits with scale
     [..., ceil(columns / group)], group 32, 64 or 128 columns, or 0 for one scale per row."""
-    import torch
-
-    e4m3 = out_dtype is not None and out_dtype != x.dtype
-    if e4m3 and out_dtype != torch.float8_e4m3fn:
+    if _L is None:
+        _setup()
+    dtype, shape = x.dtype, x.shape
+    e4m3 = out_dtype is not None and out_dtype is not dtype
+    if e4m3 and out_dtype is not torch.float8_e4m3fn:
         raise TypeError("out_dtype: expected the type of x or torch.float8_e4m3fn")
-    res_dtype = x.dtype if residual is None else residual.dtype
-    desc, xs = _norm_desc(x, res_dtype, weight, eps, E4M3 if e4m3 else None, int(group))
-    rp, rs, total, ts = None, 0, None, 0
+    res_dtype = dtype if residual is None else residual.dtype
+    group = int(group)
+    desc, dev, d, xs = _norm_desc(x, res_dtype, weight, eps, e4m3, group)
+    rp = rs = ts = 0
     if residual is not None:
-        _need(residual, x, x.shape, res_dtype, "residual")
+        _need(residual, dev, res_dtype, shape, "residual")
         rp, rs = residual.data_ptr(), _rows(residual)[1]
-    on, s = _stream(stream)
+    on, s = _stream(stream, dev)
     with on:
+        otype = out_dtype if e4m3 else dtype
         if out is None:
-            out = _empty(x, None, out_dtype)
+            out = x.new_empty(shape, dtype=otype)
         else:
-            _need(out, x, x.shape, out_dtype, "out")
-        scale = None
+            _need(out, dev, otype, shape, "out")
+        scale = total = None
         if e4m3:
-            groups = -(-desc.columns // group) if group > 0 else 1
-            scale = _empty(x, (*x.shape[:-1], groups), torch.float32)
+            groups = -(-d // group) if group > 0 else 1
+            scale = x.new_empty((*shape[:-1], groups), dtype=torch.float32)
         if residual is not None:
-            total = residual if inplace_residual else _empty(x, None, res_dtype)
+            total = residual if inplace_residual else x.new_empty(shape, dtype=res_dtype)
             ts = _rows(total)[1]
-        _check(_lib().fft_norm_forward(desc, x.data_ptr(), xs, rp, rs, out.data_ptr(),
-                                       _rows(out)[1], scale.data_ptr() if e4m3 else None,
-                                       total.data_ptr() if total is not None else None, ts, s),
-               "fft_norm_forward")
+        _check(_L.fft_norm_forward(desc, x.data_ptr(), xs, rp, rs, out.data_ptr(), _rows(out)[1],
+                                   _ptr(scale), _ptr(total), ts, s), "fft_norm_forward")
     return NormOut(out, scale, total)
 
 
 def residual_norm_backward(dout, r, weight, dresidual=None, eps=1e-6, stream=None):
     """Gradients of residual_norm at its sum r (NormOut.residual, or x without a residual) from
     dout and from dresidual, the gradient that reaches the sum by itself: NormGrads."""
-    import torch
-
-    desc, gs = _norm_desc(dout, r.dtype, weight, eps, None, 0)
-    _need(r, dout, dout.shape, r.dtype, "r")
+    desc, dev, d, gs = _norm_desc(dout, r.dtype, weight, eps, False, 0)
+    shape = dout.shape
+    _need(r, dev, r.dtype, shape, "r")
     if dresidual is not None:
-        _need(dresidual, dout, dout.shape, r.dtype, "dresidual")
-    on, s = _stream(stream)
+        _need(dresidual, dev, r.dtype, shape, "dresidual")
+    on, s = _stream(stream, dev)
     with on:
-        dr = _empty(dout, None, r.dtype)
-        dx = dr if r.dtype == dout.dtype else _empty(dout)
-        dw = _empty(dout, weight.shape, torch.float32)
-        w, wp, size = _workspace(_lib().fft_norm_workspace, (desc,), dout, "fft_norm_workspace")
-        _check(_lib().fft_norm_backward(
-            desc, dout.data_ptr(), gs, r.data_ptr(), _rows(r)[1],
-            dresidual.data_ptr() if dresidual is not None else None,
+        dr = dout.new_empty(shape, dtype=r.dtype)
+        dx = dr if r.dtype is dout.dtype else dout.new_empty(shape)
+        dw = dout.new_empty((d,), dtype=torch.float32)
+        ws, wp, size = _workspace(_L.fft_norm_workspace, (desc,), dout, "fft_norm_workspace")
+        _check(_L.fft_norm_backward(
+            desc, dout.data_ptr(), gs, r.data_ptr(), _rows(r)[1], _ptr(dresidual),
             _rows(dresidual)[1] if dresidual is not None else 0, dr.data_ptr(), _rows(dr)[1],
             None if dx is dr else dx.data_ptr(), _rows(dx)[1], dw.data_ptr(), wp, size, s),
             "fft_norm_backward")
