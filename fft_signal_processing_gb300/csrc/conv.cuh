@@ -4,196 +4,227 @@
 //   dp = dout * act'(p);  dx[t] = sum_k weight[k] dp[t+(W-1)-k]
 //   dweight[k] = sum_t dp[t] x[t-(W-1)+k];  dbias = sum_t dp[t]
 //
-// A thread holds VEC neighbouring channels (16 bytes) and walks a run of tokens with the last
-// W-1 inputs in registers, so every input is read once and a run pays W-1 rows of halo.  Bound by
-// HBM: 2 (backward 3) values moved per 2W (6W) operations.
+// A thread holds VEC neighbouring channels and walks a run of 32 tokens with the last W-1 inputs
+// (and, backward, the last W-1 dp) in registers, so a run reads its rows once and W-1 (backward
+// 2(W-1)) rows of halo.  Channels go in pairs, two float32 operations to an instruction.  Four
+// tokens at a time where they lie inside one sequence: their rows are loaded together and the
+// window slides by renaming; token by token at sequence ends and in the halo.  Bound by HBM: 2
+// (backward 3) values moved per 2W (6W) operations; VEC is 4 of 16 bits and 2 of 32 bits, since
+// 16 bytes a thread took so many registers that too few loads were in flight.
 #pragma once
 
 #include "conv.h"
 
 namespace gbfft {
 
-constexpr int kConvRun = 16;     // tokens per thread, forward
-constexpr int kConvBatch = 4;    // rows loaded ahead of their use
-constexpr int kConvThreads = 128;
+constexpr int kConvBatch = 4;
+constexpr int kConvThreads = kConvLanes * kConvRuns;
 
-template <class T, int VEC>
-struct Row {  // VEC channels of one token
-    Pack<T, VEC> p;
+template <int VEC>
+struct Pairs {  // VEC channels; one channel leaves the second half idle
+    static constexpr int P = (VEC + 1) / 2;
+    float2 v[P];
 };
-
-// Channels of a block and token runs of a block: blockDim.x lanes of VEC channels,
-// blockDim.y runs.
-struct ConvShape {
-    unsigned x, y;
-};
-inline ConvShape conv_shape(int64_t channels, int vec, int threads) {
-    unsigned x = 1;
-    while (x < (unsigned)threads && (int64_t)x * vec < channels) x *= 2;
-    return {x, (unsigned)threads / x};
-}
-
 template <class T, int VEC>
-__device__ __forceinline__ void load_f(const T* p, float (&v)[VEC]) {
-    const Pack<T, VEC> x = ld_pack<VEC>(p);
+__device__ __forceinline__ Pairs<VEC> widen(const Pack<T, VEC>& x) {
+    Pairs<VEC> r;
 #pragma unroll
-    for (int k = 0; k < VEC; ++k) v[k] = to_f(x.v[k]);
+    for (int p = 0; p < Pairs<VEC>::P; ++p)
+        r.v[p] = make_float2(to_f(x.v[2 * p]), VEC > 1 ? to_f(x.v[VEC > 1 ? 2 * p + 1 : 0]) : 0.f);
+    return r;
+}
+template <class T, int VEC>
+__device__ __forceinline__ Pack<T, VEC> narrow(const Pairs<VEC>& x) {
+    Pack<T, VEC> r;
+    if constexpr (VEC == 1) {
+        r.v[0] = from_f<T>(x.v[0].x);
+    } else {
+#pragma unroll
+        for (int p = 0; p < VEC / 2; ++p) {
+            const Pack<T, 2> y = from_f2<T>(x.v[p]);
+            r.v[2 * p] = y.v[0];
+            r.v[2 * p + 1] = y.v[1];
+        }
+    }
+    return r;
+}
+template <int VEC>
+__device__ __forceinline__ Pairs<VEC> zeros() {
+    Pairs<VEC> r;
+#pragma unroll
+    for (int p = 0; p < Pairs<VEC>::P; ++p) r.v[p] = make_float2(0.f, 0.f);
+    return r;
 }
 
 // x at position t of sequence s (t < s.begin: its initial state, or zero; older: zero).
 template <class T, int VEC, int W>
-__device__ __forceinline__ void load_before(const ConvArgs& a, const T* x, const SeqAt& s,
-                                            int64_t t, int64_t c, float (&v)[VEC]) {
-    if (t >= s.begin) {
-        load_f<T, VEC>(x + t * a.d.x.tok_stride + c, v);
-    } else {
-        const int64_t row = (W - 1) + (t - s.begin);
-        if (a.d.initial_state && row >= 0) {
-            load_f<T, VEC>(static_cast<const T*>(a.d.initial_state) +
-                               (s.q * (W - 1) + row) * a.d.channels + c, v);
-        } else {
-#pragma unroll
-            for (int k = 0; k < VEC; ++k) v[k] = 0.f;
-        }
-    }
+__device__ __forceinline__ Pairs<VEC> load_before(const ConvArgs& a, const T* x, const SeqAt& s,
+                                                  int64_t t, int64_t c) {
+    if (t >= s.begin) return widen<T, VEC>(ld_pack<VEC>(x + t * a.d.x.tok_stride + c));
+    const int64_t row = (W - 1) + (t - s.begin);
+    if (a.d.initial_state && row >= 0)
+        return widen<T, VEC>(ld_pack<VEC>(static_cast<const T*>(a.d.initial_state) +
+                                          (s.q * (W - 1) + row) * a.d.channels + c));
+    return zeros<VEC>();
 }
 
 template <class T, int VEC, int W>
-__device__ __forceinline__ void load_weights(const ConvArgs& a, int64_t c, float (&w)[W][VEC],
-                                             float (&bias)[VEC]) {
+__device__ __forceinline__ void load_weights(const ConvArgs& a, int64_t c, Pairs<VEC> (&w)[W],
+                                             Pairs<VEC>& bias) {
     const int f32 = a.d.param_dtype == FFT_F32;
+    bias = zeros<VEC>();
+#pragma unroll
+    for (int i = 0; i < W; ++i) w[i] = zeros<VEC>();
 #pragma unroll
     for (int k = 0; k < VEC; ++k) {
 #pragma unroll
-        for (int i = 0; i < W; ++i) w[i][k] = ld_param<T>(a.d.weight, (c + k) * W + i, f32);
-        bias[k] = a.d.bias ? ld_param<T>(a.d.bias, c + k, f32) : 0.f;
+        for (int i = 0; i < W; ++i)
+            (k & 1 ? w[i].v[k / 2].y : w[i].v[k / 2].x) = ld_param<T>(a.d.weight, (c + k) * W + i, f32);
+        if (a.d.bias) (k & 1 ? bias.v[k / 2].y : bias.v[k / 2].x) = ld_param<T>(a.d.bias, c + k, f32);
     }
 }
 
-// The last W-1 inputs of every sequence: one block per sequence and channel tile.
+__device__ __forceinline__ SeqAt conv_seq(const ConvArgs& a, int64_t q) {
+    return a.d.offsets ? SeqAt{q, a.d.offsets[q], a.d.offsets[q + 1]} : SeqAt{q, 0, a.d.length};
+}
+
+// The last W-1 inputs of every sequence: the blocks behind the outputs.
 template <class T, int VEC, int W>
 __device__ void conv_final(const ConvArgs& a, int64_t q, int64_t c) {
-    const SeqAt s = a.d.offsets ? SeqAt{q, a.d.offsets[q], a.d.offsets[q + 1]}
-                                : SeqAt{q, 0, a.d.length};
+    const SeqAt s = conv_seq(a, q);
     if (s.begin < 0 || s.end < s.begin || s.end > a.d.length || c >= a.d.channels) return;
     const T* x = static_cast<const T*>(a.d.x.data) + (a.d.offsets ? 0 : q * a.d.x.seq_stride);
-    for (int r = 0; r < W - 1; ++r) {
-        float v[VEC];
-        load_before<T, VEC, W>(a, x, s, s.end - (W - 1) + r, c, v);
-        Pack<T, VEC> p;
-#pragma unroll
-        for (int k = 0; k < VEC; ++k) p.v[k] = from_f<T>(v[k]);
-        st_pack<VEC>(static_cast<T*>(a.final_state) + (q * (W - 1) + r) * a.d.channels + c, p);
-    }
+    for (int r = 0; r < W - 1; ++r)
+        st_pack<VEC>(static_cast<T*>(a.final_state) + (q * (W - 1) + r) * a.d.channels + c,
+                     narrow<T, VEC>(load_before<T, VEC, W>(a, x, s, s.end - (W - 1) + r, c)));
 }
 
 template <class T, int VEC, int W>
 __global__ void __launch_bounds__(kConvThreads) k_conv_fwd(const ConvArgs a) {
+    constexpr int P = Pairs<VEC>::P, N = kConvBatch;
     const int64_t ct = blockIdx.x % a.ctiles, tile = blockIdx.x / a.ctiles;
-    const int64_t c = (ct * blockDim.x + threadIdx.x) * VEC;
+    const int64_t c = (ct * kConvLanes + threadIdx.x) * VEC;
     const int64_t rows = a.d.offsets ? 1 : a.d.nseq;
-    if (tile >= rows * a.ttiles) {  // the blocks behind the outputs: final states
-        const int64_t q = tile - rows * a.ttiles;
-        if (threadIdx.y == 0) conv_final<T, VEC, W>(a, q, c);
+    if (tile >= rows * a.ttiles) {
+        if (threadIdx.y == 0) conv_final<T, VEC, W>(a, tile - rows * a.ttiles, c);
         return;
     }
     const int64_t row = tile / a.ttiles;
-    const int64_t t0 = ((tile - row * a.ttiles) * blockDim.y) * kConvRun;
-    const int64_t b = t0 + (int64_t)threadIdx.y * kConvRun;
+    const int64_t b = (tile - row * a.ttiles) * kConvTile + (int64_t)threadIdx.y * kConvRun;
     const int64_t e = b + kConvRun < a.d.length ? b + kConvRun : a.d.length;
-    // packed rows: the whole warp looks for the block's first token, then each run walks on
-    SeqAt s = seq_at(a.d.offsets, a.d.nseq, a.d.length, row, t0);
-    if (c >= a.d.channels || b >= e) return;
-    seq_next(a.d.offsets, a.d.nseq, b, &s);
+    if (b >= e) return;  // a warp is one run
+    SeqAt s = seq_at(a.d.offsets, a.d.nseq, a.d.length, row, b);
+    if (c >= a.d.channels) return;
+    const int64_t xs = a.d.x.tok_stride, os = a.out.tok_stride;
     const T* x = static_cast<const T*>(a.d.x.data) + (a.d.offsets ? 0 : row * a.d.x.seq_stride);
     T* out = static_cast<T*>(a.out.data) + (a.d.offsets ? 0 : row * a.out.seq_stride);
-    float w[W][VEC], bias[VEC], win[W][VEC];
+    Pairs<VEC> w[W], bias, win[W - 1 + N];  // win[W-1] is the token at hand
     load_weights<T, VEC, W>(a, c, w, bias);
+    auto refill = [&](int64_t t) {
 #pragma unroll
-    for (int i = 0; i < W - 1; ++i)
-        load_before<T, VEC, W>(a, x, s, b - (W - 1) + i, c, win[i]);
-    for (int64_t t = b; t < e; t += kConvBatch) {
-        Pack<T, VEC> next[kConvBatch];
+        for (int i = 0; i < W - 1; ++i) win[i] = load_before<T, VEC, W>(a, x, s, t - (W - 1) + i, c);
+    };
+    auto emit = [&](int j, T* o) {  // the output of token j of the window
+        Pairs<VEC> y;
 #pragma unroll
-        for (int j = 0; j < kConvBatch; ++j)
-            if (t + j < e) next[j] = ld_pack<VEC>(x + (t + j) * a.d.x.tok_stride + c);
+        for (int p = 0; p < P; ++p) {
+            float2 v = bias.v[p];
 #pragma unroll
-        for (int j = 0; j < kConvBatch; ++j) {
-            if (t + j >= e) break;
-            if (t + j >= s.end) {  // packed: the next sequence begins here
-                seq_next(a.d.offsets, a.d.nseq, t + j, &s);
+            for (int i = 0; i < W; ++i) v = fma2(w[i].v[p], win[j + i].v[p], v);
+            if (a.d.silu) v = mul2(v, make_float2(sigmoid(v.x), sigmoid(v.y)));
+            y.v[p] = v;
+        }
+        st_pack<VEC>(o, narrow<T, VEC>(y));
+    };
+    auto slide = [&](int by) {
 #pragma unroll
-                for (int i = 0; i < W - 1; ++i)
-                    load_before<T, VEC, W>(a, x, s, t + j - (W - 1) + i, c, win[i]);
+        for (int i = 0; i < W - 1; ++i) win[i] = win[by + i];
+    };
+    refill(b);
+    const T* xp = x + b * xs + c;
+    T* op = out + b * os + c;
+    int64_t t = b;
+    while (t < e) {
+        if (t + N <= e && t + N <= s.end) {
+            Pack<T, VEC> next[N];
+#pragma unroll
+            for (int j = 0; j < N; ++j) next[j] = ld_pack<VEC>(xp + j * xs);
+#pragma unroll
+            for (int j = 0; j < N; ++j) win[W - 1 + j] = widen<T, VEC>(next[j]);
+#pragma unroll
+            for (int j = 0; j < N; ++j) emit(j, op + j * os);
+            slide(N);
+            t += N;
+            xp += N * xs;
+            op += N * os;
+        } else {
+            if (t >= s.end) {  // packed: the next sequence begins here
+                const int64_t q = s.q;
+                seq_next(a.d.offsets, a.d.nseq, t, &s);
+                if (s.q != q) refill(t);
             }
-            Pack<T, VEC> y;
-#pragma unroll
-            for (int k = 0; k < VEC; ++k) {
-                win[W - 1][k] = to_f(next[j].v[k]);
-                float p = bias[k];
-#pragma unroll
-                for (int i = 0; i < W; ++i) p += w[i][k] * win[i][k];
-                if (a.d.silu) p *= sigmoid(p);
-                y.v[k] = from_f<T>(p);
-#pragma unroll
-                for (int i = 0; i < W - 1; ++i) win[i][k] = win[i + 1][k];
-            }
-            st_pack<VEC>(out + (t + j) * a.out.tok_stride + c, y);
+            win[W - 1] = widen<T, VEC>(ld_pack<VEC>(xp));
+            emit(0, op);
+            slide(1);
+            t += 1;
+            xp += xs;
+            op += os;
         }
     }
 }
 
-__device__ __forceinline__ float act_grad(float p, float dout, int silu) {
+// dout * act'(p), act = silu: g (1 + p (1 - g)) with g = sigmoid(p)
+__device__ __forceinline__ float2 act_grad(float2 p, float2 dout, int silu) {
     if (!silu) return dout;
-    const float g = sigmoid(p);
-    return dout * (g * (1.f + p * (1.f - g)));
+    const float2 g = make_float2(sigmoid(p.x), sigmoid(p.y));
+    const float2 r = fma2(p, make_float2(1.f - g.x, 1.f - g.y), splat(1.f));
+    return mul2(dout, mul2(g, r));
 }
 
 // Gradient of every sequence's initial state: row r of the state reaches the outputs of tokens
 // r - k, k <= r, and (in a sequence shorter than the state) the final state's row r - length.
 template <class T, int VEC, int W>
 __device__ void conv_dinitial(const ConvArgs& a, int64_t q, int64_t c) {
-    const SeqAt s = a.d.offsets ? SeqAt{q, a.d.offsets[q], a.d.offsets[q + 1]}
-                                : SeqAt{q, 0, a.d.length};
+    constexpr int P = Pairs<VEC>::P;
+    const SeqAt s = conv_seq(a, q);
     if (s.begin < 0 || s.end < s.begin || s.end > a.d.length || c >= a.d.channels) return;
     const int64_t base = a.d.offsets ? 0 : q;
     const T* x = static_cast<const T*>(a.d.x.data) + base * a.d.x.seq_stride;
     const T* dout = static_cast<const T*>(a.dout.data) + base * a.dout.seq_stride;
     const int64_t len = s.end - s.begin;
-    float w[W][VEC], bias[VEC], acc[W][VEC] = {};
+    Pairs<VEC> w[W], bias, acc[W];
     load_weights<T, VEC, W>(a, c, w, bias);
-    for (int64_t t = 0; t < W - 1 && t < len; ++t) {
-        float p[VEC], g[VEC];
 #pragma unroll
-        for (int k = 0; k < VEC; ++k) p[k] = bias[k];
+    for (int r = 0; r < W; ++r) acc[r] = zeros<VEC>();
+    for (int64_t t = 0; t < W - 1 && t < len; ++t) {
+        Pairs<VEC> p = bias;
 #pragma unroll
         for (int i = 0; i < W; ++i) {
-            float v[VEC];
-            load_before<T, VEC, W>(a, x, s, s.begin + t - (W - 1) + i, c, v);
+            const Pairs<VEC> v = load_before<T, VEC, W>(a, x, s, s.begin + t - (W - 1) + i, c);
 #pragma unroll
-            for (int k = 0; k < VEC; ++k) p[k] += w[i][k] * v[k];
+            for (int k = 0; k < P; ++k) p.v[k] = fma2(w[i].v[k], v.v[k], p.v[k]);
         }
-        load_f<T, VEC>(dout + (s.begin + t) * a.dout.tok_stride + c, g);
+        const Pairs<VEC> g = widen<T, VEC>(ld_pack<VEC>(dout + (s.begin + t) * a.dout.tok_stride + c));
 #pragma unroll
-        for (int k = 0; k < VEC; ++k) {
-            const float dp = act_grad(p[k], g[k], a.d.silu);
+        for (int k = 0; k < P; ++k) {
+            const float2 dp = act_grad(p.v[k], g.v[k], a.d.silu);
 #pragma unroll
             for (int r = 0; r < W - 1; ++r)  // tap i = r - t of the state's row r
 #pragma unroll
                 for (int i = 0; i < W; ++i)
-                    if (r - t == i) acc[r][k] += w[i][k] * dp;
+                    if (r - t == i) acc[r].v[k] = fma2(w[i].v[k], dp, acc[r].v[k]);
         }
     }
 #pragma unroll
     for (int r = 0; r < W - 1; ++r) {
-        Pack<T, VEC> p;
-        float f[VEC] = {};
-        if (a.final_state && r >= len)
-            load_f<T, VEC>(static_cast<const T*>(a.final_state) +
-                               (q * (W - 1) + (r - len)) * a.d.channels + c, f);
+        if (a.final_state && r >= len) {
+            const Pairs<VEC> f = widen<T, VEC>(ld_pack<VEC>(
+                static_cast<const T*>(a.final_state) + (q * (W - 1) + (r - len)) * a.d.channels + c));
 #pragma unroll
-        for (int k = 0; k < VEC; ++k) p.v[k] = from_f<T>(acc[r][k] + f[k]);
-        st_pack<VEC>(static_cast<T*>(a.dinitial) + (q * (W - 1) + r) * a.d.channels + c, p);
+            for (int k = 0; k < P; ++k) acc[r].v[k] = add2(acc[r].v[k], f.v[k]);
+        }
+        st_pack<VEC>(static_cast<T*>(a.dinitial) + (q * (W - 1) + r) * a.d.channels + c,
+                     narrow<T, VEC>(acc[r]));
     }
 }
 
@@ -202,107 +233,150 @@ __device__ void conv_dinitial(const ConvArgs& a, int64_t q, int64_t c) {
 // summed in shared memory, one partial row per token tile.
 template <class T, int VEC, int W>
 __global__ void __launch_bounds__(kConvThreads) k_conv_bwd(const ConvArgs a) {
-    extern __shared__ float red[];  // [blockDim.y][blockDim.x * VEC], used once per tap
+    constexpr int P = Pairs<VEC>::P, N = kConvBatch, LANES = kConvLanes * VEC;
+    __shared__ float red[kConvRuns][LANES];
     const int64_t ct = blockIdx.x % a.ctiles, tile = blockIdx.x / a.ctiles;
-    const int64_t c = (ct * blockDim.x + threadIdx.x) * VEC;
+    const int64_t c = (ct * kConvLanes + threadIdx.x) * VEC;
     const int64_t rows = a.d.offsets ? 1 : a.d.nseq;
     if (tile >= rows * a.ttiles) {
         if (threadIdx.y == 0) conv_dinitial<T, VEC, W>(a, tile - rows * a.ttiles, c);
         return;
     }
-    const int64_t row = tile / a.ttiles, run = kConvBwdTokens / blockDim.y;
-    const int64_t t0 = (tile - row * a.ttiles) * kConvBwdTokens;
-    const int64_t b = t0 + (int64_t)threadIdx.y * run;
-    const int64_t e = b + run < a.d.length ? b + run : a.d.length;
-    SeqAt s = seq_at(a.d.offsets, a.d.nseq, a.d.length, row, t0);
-    float dw[W][VEC] = {}, db[VEC] = {};
+    const int64_t row = tile / a.ttiles;
+    const int64_t b = (tile - row * a.ttiles) * kConvTile + (int64_t)threadIdx.y * kConvRun;
+    const int64_t e = b + kConvRun < a.d.length ? b + kConvRun : a.d.length;
+    Pairs<VEC> dw[W], db = zeros<VEC>();
+#pragma unroll
+    for (int i = 0; i < W; ++i) dw[i] = zeros<VEC>();
+    SeqAt s = {0, 0, 0};
+    if (b < e) s = seq_at(a.d.offsets, a.d.nseq, a.d.length, row, b);  // a warp is one run
     if (c < a.d.channels && b < e) {
-        seq_next(a.d.offsets, a.d.nseq, b, &s);
         const int64_t base = a.d.offsets ? 0 : row;
+        const int64_t xs = a.d.x.tok_stride, gs = a.dout.tok_stride, os = a.out.tok_stride;
         const T* x = static_cast<const T*>(a.d.x.data) + base * a.d.x.seq_stride;
-        const T* dout = static_cast<const T*>(a.dout.data) + base * a.dout.seq_stride;
-        T* dx = static_cast<T*>(a.out.data) + base * a.out.seq_stride;
+        const T* dout = static_cast<const T*>(a.dout.data) + base * a.dout.seq_stride + c;
+        T* dx = a.out.data ? static_cast<T*>(a.out.data) + base * a.out.seq_stride + c : nullptr;
         const T* dfin = static_cast<const T*>(a.final_state);
-        float w[W][VEC], bias[VEC], win[W][VEC], dps[W][VEC] = {};
+        Pairs<VEC> w[W], bias, win[W - 1 + N], dps[W - 1 + N];
         load_weights<T, VEC, W>(a, c, w, bias);
+        auto refill = [&](int64_t t) {
 #pragma unroll
-        for (int i = 0; i < W - 1; ++i)
-            load_before<T, VEC, W>(a, x, s, b - (W - 1) + i, c, win[i]);
-        // dps[j] is dp of token t - (W-1) + j; past a sequence's end it is 0, and dfinal joins
+            for (int i = 0; i < W - 1; ++i)
+                win[i] = load_before<T, VEC, W>(a, x, s, t - (W - 1) + i, c);
+        };
+        // dp of token j of the window from its dout
+        auto grad = [&](int j, const Pairs<VEC>& g) {
+#pragma unroll
+            for (int p = 0; p < P; ++p) {
+                float2 v = bias.v[p];
+#pragma unroll
+                for (int i = 0; i < W; ++i) v = fma2(w[i].v[p], win[j + i].v[p], v);
+                dps[W - 1 + j].v[p] = act_grad(v, g.v[p], a.d.silu);
+            }
+        };
+        auto params = [&](int j) {
+#pragma unroll
+            for (int p = 0; p < P; ++p) {
+                db.v[p] = add2(db.v[p], dps[W - 1 + j].v[p]);
+#pragma unroll
+                for (int i = 0; i < W; ++i)
+                    dw[i].v[p] = fma2(dps[W - 1 + j].v[p], win[j + i].v[p], dw[i].v[p]);
+            }
+        };
+        auto slide = [&](int by) {
+#pragma unroll
+            for (int i = 0; i < W - 1; ++i) {
+                win[i] = win[by + i];
+                dps[i] = dps[by + i];
+            }
+        };
+#pragma unroll
+        for (int i = 0; i < W - 1; ++i) dps[i] = zeros<VEC>();
+        refill(b);
         SeqAt cur = s;  // the sequence of token t - (W-1), whose dx leaves at step t
-        int64_t dp_end = s.end < a.d.length ? s.end : a.d.length;
-        for (int64_t t = b; t < e + (W - 1); ++t) {
-            float xv[VEC] = {}, g[VEC] = {};
-            const bool in = t < a.d.length;
-            if (in) {
-                load_f<T, VEC>(x + t * a.d.x.tok_stride + c, xv);
-                load_f<T, VEC>(dout + t * a.dout.tok_stride + c, g);
-                if (t >= s.end) {
+        int64_t t = b;
+        while (t < e + (W - 1)) {
+            if (t - (W - 1) >= b && t - (W - 1) >= s.begin && t + N <= e && t + N <= s.end) {
+                // inside one sequence, and so are the tokens whose dx leaves
+                Pack<T, VEC> nx[N], ng[N];
+#pragma unroll
+                for (int j = 0; j < N; ++j) {
+                    nx[j] = ld_pack<VEC>(x + (t + j) * xs + c);
+                    ng[j] = ld_pack<VEC>(dout + (t + j) * gs);
+                }
+#pragma unroll
+                for (int j = 0; j < N; ++j) win[W - 1 + j] = widen<T, VEC>(nx[j]);
+#pragma unroll
+                for (int j = 0; j < N; ++j) {
+                    grad(j, widen<T, VEC>(ng[j]));
+                    params(j);
+                }
+                if (dx) {
+                    T* o = dx + (t - (W - 1)) * os;
+#pragma unroll
+                    for (int j = 0; j < N; ++j) {
+                        Pairs<VEC> y = zeros<VEC>();
+#pragma unroll
+                        for (int p = 0; p < P; ++p)
+#pragma unroll
+                            for (int i = 0; i < W; ++i)
+                                y.v[p] = fma2(w[W - 1 - i].v[p], dps[j + i].v[p], y.v[p]);
+                        st_pack<VEC>(o + j * os, narrow<T, VEC>(y));
+                    }
+                }
+                slide(N);
+                cur = s;
+                t += N;
+                continue;
+            }
+            win[W - 1] = dps[W - 1] = zeros<VEC>();
+            if (t < a.d.length) {
+                if (t >= s.end) {  // packed: the next sequence begins here
+                    const int64_t q = s.q;
                     seq_next(a.d.offsets, a.d.nseq, t, &s);
-#pragma unroll
-                    for (int i = 0; i < W - 1; ++i)
-                        load_before<T, VEC, W>(a, x, s, t - (W - 1) + i, c, win[i]);
+                    if (s.q != q) refill(t);
                 }
+                win[W - 1] = widen<T, VEC>(ld_pack<VEC>(x + t * xs + c));
+                grad(0, widen<T, VEC>(ld_pack<VEC>(dout + t * gs)));
+                if (t < e) params(0);
             }
-#pragma unroll
-            for (int k = 0; k < VEC; ++k) {
-                win[W - 1][k] = xv[k];
-                float p = bias[k];
-#pragma unroll
-                for (int i = 0; i < W; ++i) p += w[i][k] * win[i][k];
-                const float dp = in ? act_grad(p, g[k], a.d.silu) : 0.f;
-                dps[W - 1][k] = dp;
-                if (t < e) {
-                    db[k] += dp;
-#pragma unroll
-                    for (int i = 0; i < W; ++i) dw[i][k] += dp * win[i][k];
-                }
-#pragma unroll
-                for (int i = 0; i < W - 1; ++i) win[i][k] = win[i + 1][k];
-            }
-            const int64_t td = t - (W - 1);  // dx[td] = sum_j weight[W-1-j] dp[td + j]
-            if (td >= b && a.out.data) {
-                if (td >= cur.end) {
-                    seq_next(a.d.offsets, a.d.nseq, td, &cur);
-                    dp_end = cur.end < a.d.length ? cur.end : a.d.length;
-                }
-                float f[VEC] = {};
-                const int64_t fr = td + (W - 1) - dp_end;  // row of the final state that td is
+            const int64_t td = t - (W - 1);  // dx[td] = sum_i weight[W-1-i] dp[td + i]
+            if (td >= b && dx) {
+                if (td >= cur.end) seq_next(a.d.offsets, a.d.nseq, td, &cur);
+                const int64_t end = cur.end < a.d.length ? cur.end : a.d.length;
+                Pairs<VEC> y = zeros<VEC>();
+                const int64_t fr = td + (W - 1) - end;  // row of the final state that td is
                 if (dfin && fr >= 0 && fr < W - 1)
-                    load_f<T, VEC>(dfin + (cur.q * (W - 1) + fr) * a.d.channels + c, f);
-                Pack<T, VEC> y;
+                    y = widen<T, VEC>(ld_pack<VEC>(dfin + (cur.q * (W - 1) + fr) * a.d.channels + c));
 #pragma unroll
-                for (int k = 0; k < VEC; ++k) {
-                    float d = f[k];
+                for (int p = 0; p < P; ++p)
 #pragma unroll
-                    for (int j = 0; j < W; ++j)
-                        if (td + j < dp_end) d += w[W - 1 - j][k] * dps[j][k];
-                    y.v[k] = from_f<T>(d);
-                }
-                st_pack<VEC>(dx + td * a.out.tok_stride + c, y);
+                    for (int i = 0; i < W; ++i)
+                        if (td + i < end) y.v[p] = fma2(w[W - 1 - i].v[p], dps[i].v[p], y.v[p]);
+                st_pack<VEC>(dx + td * os, narrow<T, VEC>(y));
             }
-#pragma unroll
-            for (int k = 0; k < VEC; ++k)
-#pragma unroll
-                for (int i = 0; i < W - 1; ++i) dps[i][k] = dps[i + 1][k];
+            slide(1);
+            t += 1;
         }
     }
     if (!a.parts) return;
-    const int lanes = (int)blockDim.x * VEC;
+    const int tid = (int)(threadIdx.y * kConvLanes + threadIdx.x);
 #pragma unroll
     for (int i = 0; i <= W; ++i) {
         __syncthreads();
 #pragma unroll
-        for (int k = 0; k < VEC; ++k)
-            red[threadIdx.y * lanes + threadIdx.x * VEC + k] = i < W ? dw[i < W ? i : 0][k] : db[k];
+        for (int k = 0; k < VEC; ++k) {
+            const float2 v = i < W ? dw[i < W ? i : 0].v[k / 2] : db.v[k / 2];
+            red[threadIdx.y][threadIdx.x * VEC + k] = k & 1 ? v.y : v.x;
+        }
         __syncthreads();
-        const int tid = (int)(threadIdx.y * blockDim.x + threadIdx.x);
-        for (int l = tid; l < lanes; l += kConvThreads) {
-            const int64_t ch = ct * lanes + l;
-            if (ch < a.d.channels) {
+        for (int l = tid; l < LANES; l += kConvThreads) {
+            const int64_t chan = ct * LANES + l;
+            if (chan < a.d.channels) {
                 float v = 0.f;
-                for (int y = 0; y < (int)blockDim.y; ++y) v += red[y * lanes + l];
-                a.parts[(tile * (W + 1) + i) * a.d.channels + ch] = v;
+#pragma unroll
+                for (int y = 0; y < kConvRuns; ++y) v += red[y][l];
+                a.parts[(tile * (W + 1) + i) * a.d.channels + chan] = v;
             }
         }
     }
@@ -310,20 +384,18 @@ __global__ void __launch_bounds__(kConvThreads) k_conv_bwd(const ConvArgs a) {
 
 template <class T, int VEC, int W>
 cudaError_t conv_launch(ConvArgs a, bool backward, cudaStream_t s) {
-    const ConvShape sh = conv_shape(a.d.channels, VEC, kConvThreads);
     const int64_t rows = a.d.offsets ? 1 : a.d.nseq;
-    a.ctiles = (a.d.channels + (int64_t)sh.x * VEC - 1) / ((int64_t)sh.x * VEC);
-    const int64_t per = backward ? kConvBwdTokens : (int64_t)sh.y * kConvRun;
-    a.ttiles = (a.d.length + per - 1) / per;
+    a.ctiles = (a.d.channels + kConvLanes * VEC - 1) / (kConvLanes * VEC);
+    a.ttiles = (a.d.length + kConvTile - 1) / kConvTile;
     const bool states = W > 1 && (backward ? a.dinitial : a.final_state) != nullptr;
     const int64_t blocks = a.ctiles * (rows * a.ttiles + (states ? a.d.nseq : 0));
     if (blocks < 1) return cudaSuccess;
     if (blocks > INT32_MAX) return cudaErrorInvalidValue;
+    const dim3 threads(kConvLanes, kConvRuns);
     if (backward)
-        k_conv_bwd<T, VEC, W><<<(unsigned)blocks, dim3(sh.x, sh.y),
-                                sizeof(float) * kConvThreads * VEC, s>>>(a);
+        k_conv_bwd<T, VEC, W><<<(unsigned)blocks, threads, 0, s>>>(a);
     else
-        k_conv_fwd<T, VEC, W><<<(unsigned)blocks, dim3(sh.x, sh.y), 0, s>>>(a);
+        k_conv_fwd<T, VEC, W><<<(unsigned)blocks, threads, 0, s>>>(a);
     return cudaGetLastError();
 }
 

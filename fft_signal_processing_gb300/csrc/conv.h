@@ -15,8 +15,10 @@ struct ConvArgs {
     int64_t ctiles, ttiles;  // channel tiles; token tiles per row
 };
 
-// Tokens of one block of the backward pass.
-constexpr int kConvBwdTokens = 512;
+// A block has 32 lanes along the channels and 8 runs of tokens; the runs of a block are its token
+// tile (one partial row of the parameter gradients).
+constexpr int kConvLanes = 32, kConvRuns = 8, kConvRun = 32;
+constexpr int kConvTile = kConvRuns * kConvRun;
 
 cudaError_t conv_forward_f32(ConvArgs a, cudaStream_t s);
 cudaError_t conv_forward_bf16(ConvArgs a, cudaStream_t s);

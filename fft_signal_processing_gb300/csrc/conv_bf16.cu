@@ -3,7 +3,7 @@
 
 namespace gbfft {
 
-cudaError_t conv_forward_bf16(ConvArgs a, cudaStream_t s) { return conv_run<__nv_bfloat16, 8>(a, false, s); }
+cudaError_t conv_forward_bf16(ConvArgs a, cudaStream_t s) { return conv_run<__nv_bfloat16, 4>(a, false, s); }
 cudaError_t conv_backward_bf16(ConvArgs a, cudaStream_t s) { return conv_run<__nv_bfloat16, 4>(a, true, s); }
 
 }  // namespace gbfft

@@ -3,7 +3,7 @@
 
 namespace gbfft {
 
-cudaError_t conv_forward_f16(ConvArgs a, cudaStream_t s) { return conv_run<__half, 8>(a, false, s); }
+cudaError_t conv_forward_f16(ConvArgs a, cudaStream_t s) { return conv_run<__half, 4>(a, false, s); }
 cudaError_t conv_backward_f16(ConvArgs a, cudaStream_t s) { return conv_run<__half, 4>(a, true, s); }
 
 }  // namespace gbfft

@@ -3,7 +3,7 @@
 
 namespace gbfft {
 
-cudaError_t conv_forward_f32(ConvArgs a, cudaStream_t s) { return conv_run<float, 4>(a, false, s); }
-cudaError_t conv_backward_f32(ConvArgs a, cudaStream_t s) { return conv_run<float, 4>(a, true, s); }
+cudaError_t conv_forward_f32(ConvArgs a, cudaStream_t s) { return conv_run<float, 2>(a, false, s); }
+cudaError_t conv_backward_f32(ConvArgs a, cudaStream_t s) { return conv_run<float, 2>(a, true, s); }
 
 }  // namespace gbfft

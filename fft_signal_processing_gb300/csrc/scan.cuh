@@ -299,9 +299,7 @@ __global__ void __launch_bounds__(kPairThreads) k_scan(const ScanArgs a) {
                 T* o = out + (t + j0) * ostr;
 #pragma unroll
                 for (int j = 0; j < N; ++j, o += ostr) {
-                    Pack<T, 2> po;
-                    po.v[0] = from_f<T>(y[j].x);
-                    po.v[1] = from_f<T>(y[j].y);
+                    const Pack<T, 2> po = from_f2<T>(y[j]);
                     if (a.pair) {
                         if (live[0]) st_pack<2>(o, po);
                     } else {
@@ -617,7 +615,7 @@ __global__ void __launch_bounds__(kLanesThreads) k_scan_lanes(const ScanArgs a) 
 }
 
 // Few threads and a chain of chunks: small blocks on many SMs, and many chunks loaded at once.
-constexpr int kCarryThreads = 64, kCarryAhead = 32;
+constexpr int kCarryThreads = 64, kCarryAhead = 16;
 
 // Pass 2: along the chunks of every (row, channel, state); the state after a chunk that a
 // sequence starts in does not depend on what came before.
@@ -634,21 +632,20 @@ __global__ void __launch_bounds__(kCarryThreads) k_scan_carry(const ScanArgs a) 
     float h = 0.f;
     constexpr int U = kCarryAhead;
     for (int64_t k = 0; k < a.nchunks; k += U) {
-        float local[U], decay[U];
+        float local[U], sum[U];
+        int cut[U];
 #pragma unroll
-        for (int j = 0; j < U; ++j) {
-            if (k + j < a.nchunks - 1) {
-                const int cut = reset[k + j];
-                const float sum = dsum[(k + j) * a.d.channels];
-                local[j] = carry[(k + j) * per];
-                decay[j] = cut ? -1.f : ex2(A2 * sum);
-            }
+        for (int j = 0; j < U; ++j) {  // no branches: the loads have to be in flight together
+            const int64_t i = k + j < a.nchunks ? k + j : a.nchunks - 1;
+            local[j] = carry[i * per];
+            sum[j] = dsum[i * a.d.channels];
+            cut[j] = reset[i];
         }
 #pragma unroll
         for (int j = 0; j < U; ++j) {
             if (k + j >= a.nchunks) break;
             carry[(k + j) * per] = h;
-            if (k + j < a.nchunks - 1) h = decay[j] < 0.f ? local[j] : fmaf(decay[j], h, local[j]);
+            h = cut[j] ? local[j] : fmaf(ex2(A2 * sum[j]), h, local[j]);
         }
     }
 }

@@ -130,22 +130,21 @@ __global__ void __launch_bounds__(kCarryThreads) k_scan_back_carry(const ScanBwd
     float m = 0.f;
     constexpr int U = kCarryAhead;
     for (int64_t k = nch - 1; k >= 0; k -= U) {
-        float local[U], decay[U];
+        float local[U], sum[U];
+        int cut[U];
 #pragma unroll
         for (int j = 0; j < U; ++j) {
-            if (k - j > 0) {
-                // nothing enters the last chunk, and its sum of d is not known
-                const int cut = k - j == nch - 1 || reset[k - j];
-                const float sum = dsum[(k - j) * a.d.channels];
-                local[j] = carry[(k - j) * per];
-                decay[j] = cut ? -1.f : ex2(A2 * sum);
-            }
+            const int64_t i = k - j > 0 ? k - j : 0;
+            local[j] = carry[i * per];
+            sum[j] = dsum[i * a.d.channels];
+            // nothing enters the last chunk, and its sum of d is not known
+            cut[j] = reset[i] || i == nch - 1;
         }
 #pragma unroll
         for (int j = 0; j < U; ++j) {
             if (k - j < 0) break;
             carry[(k - j) * per] = m;
-            if (k - j > 0) m = decay[j] < 0.f ? local[j] : fmaf(decay[j], m, local[j]);
+            m = cut[j] ? local[j] : fmaf(ex2(A2 * sum[j]), m, local[j]);
         }
     }
 }

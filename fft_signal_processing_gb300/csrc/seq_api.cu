@@ -57,7 +57,7 @@ int check_conv(const fft_conv_desc* d, bool pointers) {
 }
 
 int64_t conv_tiles(const fft_conv_desc& d) {
-    return (d.offsets ? 1 : d.nseq) * ((d.length + kConvBwdTokens - 1) / kConvBwdTokens);
+    return (d.offsets ? 1 : d.nseq) * ((d.length + kConvTile - 1) / kConvTile);
 }
 
 int check_scan(const fft_scan_desc* d, bool pointers) {

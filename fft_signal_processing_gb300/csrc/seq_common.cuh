@@ -39,6 +39,20 @@ __device__ __forceinline__ void st_pack(T* p, const Pack<T, V>& x) {
     *reinterpret_cast<Pack<T, V>*>(p) = x;
 }
 
+// Two values rounded at once.
+template <class T> __device__ __forceinline__ Pack<T, 2> from_f2(float2 v);
+template <> __device__ __forceinline__ Pack<float, 2> from_f2<float>(float2 v) {
+    return {v.x, v.y};
+}
+template <> __device__ __forceinline__ Pack<__nv_bfloat16, 2> from_f2<__nv_bfloat16>(float2 v) {
+    const __nv_bfloat162 r = __floats2bfloat162_rn(v.x, v.y);
+    return {r.x, r.y};
+}
+template <> __device__ __forceinline__ Pack<__half, 2> from_f2<__half>(float2 v) {
+    const __half2 r = __floats2half2_rn(v.x, v.y);
+    return {r.x, r.y};
+}
+
 // A parameter of type float or T (f32 != 0: float).
 template <class T>
 __device__ __forceinline__ float ld_param(const void* p, int64_t i, int f32) {
