@@ -4,22 +4,54 @@
 //   dp = dout * act'(p);  dx[t] = sum_k weight[k] dp[t+(W-1)-k]
 //   dweight[k] = sum_t dp[t] x[t-(W-1)+k];  dbias = sum_t dp[t]
 //
-// A thread holds VEC neighbouring channels and walks a run of 32 tokens with the last W-1 inputs
-// (and, backward, the last W-1 dp) in registers, so a run reads its rows once and W-1 (backward
-// 2(W-1)) rows of halo.  Channels go in pairs, two float32 operations to an instruction.  Four
-// tokens at a time where they lie inside one sequence: their rows are loaded together and the
-// window slides by renaming; token by token at sequence ends and in the halo.  Bound by HBM: 2
-// (backward 3) values moved per 2W (6W) operations; VEC is 4 of 16 bits and 2 of 32 bits, since
-// 16 bytes a thread took so many registers that too few loads were in flight.
+// A thread holds VEC neighbouring channels (8 bytes) and walks a run of 64 tokens with the last W-1
+// inputs (and, backward, the last W-1 dp) in registers, so a run reads its rows once and W-1
+// (backward 2(W-1)) rows of halo.  Channels go in pairs, two float32 operations to an
+// instruction.  Tokens go by fours: their rows come by asynchronous copies into the thread's own
+// places in shared memory, three fours ahead, which keeps more loads in flight than the registers
+// would; inside a sequence the window slides by renaming, at sequence ends and in the halo tokens
+// go one by one.  Bound by HBM: 2 (backward 3) values moved per 2W (6W) operations.
 #pragma once
 
 #include "conv.h"
+#include "launch_cache.cuh"
 
 namespace gbfft {
 
 constexpr int kConvBatch = 4;
+constexpr int kConvAhead = 3;  // fours of rows on their way
 constexpr int kConvThreads = kConvLanes * kConvRuns;
 
+// The rows of a run, in fours, R tensors side by side.  VEC 1: no ring, rows are loaded when they
+// are needed.
+template <class T, int VEC, int R>
+struct ConvRing {
+    static constexpr bool kOn = VEC * sizeof(T) == 8;
+    static constexpr int kFours = kConvAhead + 1;
+    static constexpr int kBytes = kOn ? kFours * kConvBatch * R * kConvThreads * 8 : 0;
+    // [four][row][tensor][thread]; `four` counts from the run's start
+    char* mine;  // the thread's place
+    __device__ __forceinline__ explicit ConvRing(void* memory)
+        : mine(static_cast<char*>(memory) + (threadIdx.y * kConvLanes + threadIdx.x) * 8) {}
+    __device__ __forceinline__ char* at(int four, int row, int r) const {
+        return mine + (four % kFours) * (kConvBatch * R * kConvThreads * 8) +
+               (row * R + r) * (kConvThreads * 8);
+    }
+    __device__ __forceinline__ Pack<T, VEC> get(int four, int row, int r) const {
+        return *reinterpret_cast<const Pack<T, VEC>*>(at(four, row, r));
+    }
+    // row 4 * four + j of a tensor at p + j * stride, rows from `left` on do not exist
+    __device__ __forceinline__ void copy(int four, int r, const T* p, int64_t stride, int left) const {
+        if (left >= kConvBatch) {
+#pragma unroll
+            for (int j = 0; j < kConvBatch; ++j, p += stride) copy8(at(four, j, r), p, true);
+        } else {
+#pragma unroll
+            for (int j = 0; j < kConvBatch; ++j)
+                if (j < left) copy8(at(four, j, r), p + j * stride, true);
+        }
+    }
+};
 template <int VEC>
 struct Pairs {  // VEC channels; one channel leaves the second half idle
     static constexpr int P = (VEC + 1) / 2;
@@ -56,11 +88,12 @@ __device__ __forceinline__ Pairs<VEC> zeros() {
     return r;
 }
 
-// x at position t of sequence s (t < s.begin: its initial state, or zero; older: zero).
+// x at position t of sequence s (t < s.begin: its initial state, or zero; older: zero); x points
+// at channel c.
 template <class T, int VEC, int W>
 __device__ __forceinline__ Pairs<VEC> load_before(const ConvArgs& a, const T* x, const SeqAt& s,
                                                   int64_t t, int64_t c) {
-    if (t >= s.begin) return widen<T, VEC>(ld_pack<VEC>(x + t * a.d.x.tok_stride + c));
+    if (t >= s.begin) return widen<T, VEC>(ld_pack<VEC>(x + t * a.d.x.tok_stride));
     const int64_t row = (W - 1) + (t - s.begin);
     if (a.d.initial_state && row >= 0)
         return widen<T, VEC>(ld_pack<VEC>(static_cast<const T*>(a.d.initial_state) +
@@ -93,7 +126,7 @@ template <class T, int VEC, int W>
 __device__ void conv_final(const ConvArgs& a, int64_t q, int64_t c) {
     const SeqAt s = conv_seq(a, q);
     if (s.begin < 0 || s.end < s.begin || s.end > a.d.length || c >= a.d.channels) return;
-    const T* x = static_cast<const T*>(a.d.x.data) + (a.d.offsets ? 0 : q * a.d.x.seq_stride);
+    const T* x = static_cast<const T*>(a.d.x.data) + (a.d.offsets ? 0 : q * a.d.x.seq_stride) + c;
     for (int r = 0; r < W - 1; ++r)
         st_pack<VEC>(static_cast<T*>(a.final_state) + (q * (W - 1) + r) * a.d.channels + c,
                      narrow<T, VEC>(load_before<T, VEC, W>(a, x, s, s.end - (W - 1) + r, c)));
@@ -102,6 +135,9 @@ __device__ void conv_final(const ConvArgs& a, int64_t q, int64_t c) {
 template <class T, int VEC, int W>
 __global__ void __launch_bounds__(kConvThreads) k_conv_fwd(const ConvArgs a) {
     constexpr int P = Pairs<VEC>::P, N = kConvBatch;
+    using Ring = ConvRing<T, VEC, 1>;
+    extern __shared__ uint2 ring_memory[];
+    const Ring ring(ring_memory);
     const int64_t ct = blockIdx.x % a.ctiles, tile = blockIdx.x / a.ctiles;
     const int64_t c = (ct * kConvLanes + threadIdx.x) * VEC;
     const int64_t rows = a.d.offsets ? 1 : a.d.nseq;
@@ -116,13 +152,13 @@ __global__ void __launch_bounds__(kConvThreads) k_conv_fwd(const ConvArgs a) {
     SeqAt s = seq_at(a.d.offsets, a.d.nseq, a.d.length, row, b);
     if (c >= a.d.channels) return;
     const int64_t xs = a.d.x.tok_stride, os = a.out.tok_stride;
-    const T* x = static_cast<const T*>(a.d.x.data) + (a.d.offsets ? 0 : row * a.d.x.seq_stride);
+    const T* x0 = static_cast<const T*>(a.d.x.data) + (a.d.offsets ? 0 : row * a.d.x.seq_stride) + c;
     T* out = static_cast<T*>(a.out.data) + (a.d.offsets ? 0 : row * a.out.seq_stride);
     Pairs<VEC> w[W], bias, win[W - 1 + N];  // win[W-1] is the token at hand
     load_weights<T, VEC, W>(a, c, w, bias);
     auto refill = [&](int64_t t) {
 #pragma unroll
-        for (int i = 0; i < W - 1; ++i) win[i] = load_before<T, VEC, W>(a, x, s, t - (W - 1) + i, c);
+        for (int i = 0; i < W - 1; ++i) win[i] = load_before<T, VEC, W>(a, x0, s, t - (W - 1) + i, c);
     };
     auto emit = [&](int j, T* o) {  // the output of token j of the window
         Pairs<VEC> y;
@@ -131,7 +167,7 @@ __global__ void __launch_bounds__(kConvThreads) k_conv_fwd(const ConvArgs a) {
             float2 v = bias.v[p];
 #pragma unroll
             for (int i = 0; i < W; ++i) v = fma2(w[i].v[p], win[j + i].v[p], v);
-            if (a.d.silu) v = mul2(v, make_float2(sigmoid(v.x), sigmoid(v.y)));
+            if (a.d.silu) v = mul2(v, sigmoid2(v));
             y.v[p] = v;
         }
         st_pack<VEC>(o, narrow<T, VEC>(y));
@@ -140,44 +176,59 @@ __global__ void __launch_bounds__(kConvThreads) k_conv_fwd(const ConvArgs a) {
 #pragma unroll
         for (int i = 0; i < W - 1; ++i) win[i] = win[by + i];
     };
+    const int len = (int)(e - b);
+    const T* x = x0 + b * xs;  // rows count from the run's start
+    const T* next = x;
+    auto ahead = [&](int four) {
+        ring.copy(four, 0, next, xs, len - four * N);
+        next += N * xs;
+        copy_commit();
+    };
+    if constexpr (Ring::kOn) {
+#pragma unroll
+        for (int k = 0; k < kConvAhead; ++k) ahead(k);
+    }
     refill(b);
-    const T* xp = x + b * xs + c;
     T* op = out + b * os + c;
-    int64_t t = b;
-    while (t < e) {
-        if (t + N <= e && t + N <= s.end) {
-            Pack<T, VEC> next[N];
+    for (int i = 0, four = 0; i < len; i += N, ++four, op += N * os) {
+        if constexpr (Ring::kOn) {
+            ahead(four + kConvAhead);
+            copy_wait<kConvAhead>();
+        }
+        auto row_at = [&](int j) {
+            if constexpr (Ring::kOn) return ring.get(four, j, 0);
+            return ld_pack<VEC>(x + (i + j) * xs);
+        };
+        if (i + N <= len && b + i + N <= s.end) {
+            Pack<T, VEC> rows_[N];
 #pragma unroll
-            for (int j = 0; j < N; ++j) next[j] = ld_pack<VEC>(xp + j * xs);
+            for (int j = 0; j < N; ++j) rows_[j] = row_at(j);
 #pragma unroll
-            for (int j = 0; j < N; ++j) win[W - 1 + j] = widen<T, VEC>(next[j]);
+            for (int j = 0; j < N; ++j) win[W - 1 + j] = widen<T, VEC>(rows_[j]);
 #pragma unroll
             for (int j = 0; j < N; ++j) emit(j, op + j * os);
             slide(N);
-            t += N;
-            xp += N * xs;
-            op += N * os;
         } else {
-            if (t >= s.end) {  // packed: the next sequence begins here
-                const int64_t q = s.q;
-                seq_next(a.d.offsets, a.d.nseq, t, &s);
-                if (s.q != q) refill(t);
+            for (int j = 0; j < N && i + j < len; ++j) {
+                if (b + i + j >= s.end) {  // packed: the next sequence begins here
+                    const int64_t q = s.q;
+                    seq_next(a.d.offsets, a.d.nseq, b + i + j, &s);
+                    if (s.q != q) refill(b + i + j);
+                }
+                win[W - 1] = widen<T, VEC>(row_at(j));
+                emit(0, op + j * os);
+                slide(1);
             }
-            win[W - 1] = widen<T, VEC>(ld_pack<VEC>(xp));
-            emit(0, op);
-            slide(1);
-            t += 1;
-            xp += xs;
-            op += os;
         }
     }
+    if constexpr (Ring::kOn) copy_wait<0>();
 }
 
 // dout * act'(p), act = silu: g (1 + p (1 - g)) with g = sigmoid(p)
 __device__ __forceinline__ float2 act_grad(float2 p, float2 dout, int silu) {
     if (!silu) return dout;
-    const float2 g = make_float2(sigmoid(p.x), sigmoid(p.y));
-    const float2 r = fma2(p, make_float2(1.f - g.x, 1.f - g.y), splat(1.f));
+    const float2 g = sigmoid2(p);
+    const float2 r = fma2(p, fma2(g, splat(-1.f), splat(1.f)), splat(1.f));
     return mul2(dout, mul2(g, r));
 }
 
@@ -189,7 +240,7 @@ __device__ void conv_dinitial(const ConvArgs& a, int64_t q, int64_t c) {
     const SeqAt s = conv_seq(a, q);
     if (s.begin < 0 || s.end < s.begin || s.end > a.d.length || c >= a.d.channels) return;
     const int64_t base = a.d.offsets ? 0 : q;
-    const T* x = static_cast<const T*>(a.d.x.data) + base * a.d.x.seq_stride;
+    const T* x = static_cast<const T*>(a.d.x.data) + base * a.d.x.seq_stride + c;
     const T* dout = static_cast<const T*>(a.dout.data) + base * a.dout.seq_stride;
     const int64_t len = s.end - s.begin;
     Pairs<VEC> w[W], bias, acc[W];
@@ -234,6 +285,9 @@ __device__ void conv_dinitial(const ConvArgs& a, int64_t q, int64_t c) {
 template <class T, int VEC, int W>
 __global__ void __launch_bounds__(kConvThreads) k_conv_bwd(const ConvArgs a) {
     constexpr int P = Pairs<VEC>::P, N = kConvBatch, LANES = kConvLanes * VEC;
+    using Ring = ConvRing<T, VEC, 2>;
+    extern __shared__ uint2 ring_memory[];
+    const Ring ring(ring_memory);
     __shared__ float red[kConvRuns][LANES];
     const int64_t ct = blockIdx.x % a.ctiles, tile = blockIdx.x / a.ctiles;
     const int64_t c = (ct * kConvLanes + threadIdx.x) * VEC;
@@ -253,8 +307,24 @@ __global__ void __launch_bounds__(kConvThreads) k_conv_bwd(const ConvArgs a) {
     if (c < a.d.channels && b < e) {
         const int64_t base = a.d.offsets ? 0 : row;
         const int64_t xs = a.d.x.tok_stride, gs = a.dout.tok_stride, os = a.out.tok_stride;
-        const T* x = static_cast<const T*>(a.d.x.data) + base * a.d.x.seq_stride;
-        const T* dout = static_cast<const T*>(a.dout.data) + base * a.dout.seq_stride + c;
+        const T* x0 = static_cast<const T*>(a.d.x.data) + base * a.d.x.seq_stride + c;
+        const T* x = x0 + b * xs;  // rows count from the run's start
+        const T* dout = static_cast<const T*>(a.dout.data) + base * a.dout.seq_stride + b * gs + c;
+        const int len = (int)(e - b), all = len + W - 1;  // own tokens, and with the halo
+        const int there = a.d.length - b < all ? (int)(a.d.length - b) : all;  // that exist
+        const T* nextx = x;
+        const T* nextg = dout;
+        auto ahead = [&](int four) {
+            ring.copy(four, 0, nextx, xs, there - four * N);
+            ring.copy(four, 1, nextg, gs, there - four * N);
+            nextx += N * xs;
+            nextg += N * gs;
+            copy_commit();
+        };
+        if constexpr (Ring::kOn) {
+#pragma unroll
+            for (int k = 0; k < kConvAhead; ++k) ahead(k);
+        }
         T* dx = a.out.data ? static_cast<T*>(a.out.data) + base * a.out.seq_stride + c : nullptr;
         const T* dfin = static_cast<const T*>(a.final_state);
         Pairs<VEC> w[W], bias, win[W - 1 + N], dps[W - 1 + N];
@@ -262,7 +332,7 @@ __global__ void __launch_bounds__(kConvThreads) k_conv_bwd(const ConvArgs a) {
         auto refill = [&](int64_t t) {
 #pragma unroll
             for (int i = 0; i < W - 1; ++i)
-                win[i] = load_before<T, VEC, W>(a, x, s, t - (W - 1) + i, c);
+                win[i] = load_before<T, VEC, W>(a, x0, s, t - (W - 1) + i, c);
         };
         // dp of token j of the window from its dout
         auto grad = [&](int j, const Pairs<VEC>& g) {
@@ -294,15 +364,27 @@ __global__ void __launch_bounds__(kConvThreads) k_conv_bwd(const ConvArgs a) {
         for (int i = 0; i < W - 1; ++i) dps[i] = zeros<VEC>();
         refill(b);
         SeqAt cur = s;  // the sequence of token t - (W-1), whose dx leaves at step t
-        int64_t t = b;
-        while (t < e + (W - 1)) {
-            if (t - (W - 1) >= b && t - (W - 1) >= s.begin && t + N <= e && t + N <= s.end) {
+        for (int i = 0, four = 0; i < all; i += N, ++four) {
+            if constexpr (Ring::kOn) {
+                ahead(four + kConvAhead);
+                copy_wait<kConvAhead>();
+            }
+            auto x_at = [&](int j) {
+                if constexpr (Ring::kOn) return ring.get(four, j, 0);
+                return ld_pack<VEC>(x + (i + j) * xs);
+            };
+            auto g_at = [&](int j) {
+                if constexpr (Ring::kOn) return ring.get(four, j, 1);
+                return ld_pack<VEC>(dout + (i + j) * gs);
+            };
+            const int64_t t0 = b + i;
+            if (i >= W - 1 && t0 - (W - 1) >= s.begin && i + N <= len && t0 + N <= s.end) {
                 // inside one sequence, and so are the tokens whose dx leaves
                 Pack<T, VEC> nx[N], ng[N];
 #pragma unroll
                 for (int j = 0; j < N; ++j) {
-                    nx[j] = ld_pack<VEC>(x + (t + j) * xs + c);
-                    ng[j] = ld_pack<VEC>(dout + (t + j) * gs);
+                    nx[j] = x_at(j);
+                    ng[j] = g_at(j);
                 }
 #pragma unroll
                 for (int j = 0; j < N; ++j) win[W - 1 + j] = widen<T, VEC>(nx[j]);
@@ -312,52 +394,55 @@ __global__ void __launch_bounds__(kConvThreads) k_conv_bwd(const ConvArgs a) {
                     params(j);
                 }
                 if (dx) {
-                    T* o = dx + (t - (W - 1)) * os;
+                    T* o = dx + (t0 - (W - 1)) * os;
 #pragma unroll
                     for (int j = 0; j < N; ++j) {
                         Pairs<VEC> y = zeros<VEC>();
 #pragma unroll
                         for (int p = 0; p < P; ++p)
 #pragma unroll
-                            for (int i = 0; i < W; ++i)
-                                y.v[p] = fma2(w[W - 1 - i].v[p], dps[j + i].v[p], y.v[p]);
+                            for (int k = 0; k < W; ++k)
+                                y.v[p] = fma2(w[W - 1 - k].v[p], dps[j + k].v[p], y.v[p]);
                         st_pack<VEC>(o + j * os, narrow<T, VEC>(y));
                     }
                 }
                 slide(N);
                 cur = s;
-                t += N;
                 continue;
             }
-            win[W - 1] = dps[W - 1] = zeros<VEC>();
-            if (t < a.d.length) {
-                if (t >= s.end) {  // packed: the next sequence begins here
-                    const int64_t q = s.q;
-                    seq_next(a.d.offsets, a.d.nseq, t, &s);
-                    if (s.q != q) refill(t);
+            for (int j = 0; j < N && i + j < all; ++j) {
+                const int64_t t = t0 + j;
+                win[W - 1] = dps[W - 1] = zeros<VEC>();
+                if (i + j < there) {
+                    if (t >= s.end) {  // packed: the next sequence begins here
+                        const int64_t q = s.q;
+                        seq_next(a.d.offsets, a.d.nseq, t, &s);
+                        if (s.q != q) refill(t);
+                    }
+                    win[W - 1] = widen<T, VEC>(x_at(j));
+                    grad(0, widen<T, VEC>(g_at(j)));
+                    if (t < e) params(0);
                 }
-                win[W - 1] = widen<T, VEC>(ld_pack<VEC>(x + t * xs + c));
-                grad(0, widen<T, VEC>(ld_pack<VEC>(dout + t * gs)));
-                if (t < e) params(0);
-            }
-            const int64_t td = t - (W - 1);  // dx[td] = sum_i weight[W-1-i] dp[td + i]
-            if (td >= b && dx) {
-                if (td >= cur.end) seq_next(a.d.offsets, a.d.nseq, td, &cur);
-                const int64_t end = cur.end < a.d.length ? cur.end : a.d.length;
-                Pairs<VEC> y = zeros<VEC>();
-                const int64_t fr = td + (W - 1) - end;  // row of the final state that td is
-                if (dfin && fr >= 0 && fr < W - 1)
-                    y = widen<T, VEC>(ld_pack<VEC>(dfin + (cur.q * (W - 1) + fr) * a.d.channels + c));
+                const int64_t td = t - (W - 1);  // dx[td] = sum_k weight[W-1-k] dp[td + k]
+                if (td >= b && dx) {
+                    if (td >= cur.end) seq_next(a.d.offsets, a.d.nseq, td, &cur);
+                    const int64_t end = cur.end < a.d.length ? cur.end : a.d.length;
+                    Pairs<VEC> y = zeros<VEC>();
+                    const int64_t fr = td + (W - 1) - end;  // row of the final state that td is
+                    if (dfin && fr >= 0 && fr < W - 1)
+                        y = widen<T, VEC>(
+                            ld_pack<VEC>(dfin + (cur.q * (W - 1) + fr) * a.d.channels + c));
 #pragma unroll
-                for (int p = 0; p < P; ++p)
+                    for (int p = 0; p < P; ++p)
 #pragma unroll
-                    for (int i = 0; i < W; ++i)
-                        if (td + i < end) y.v[p] = fma2(w[W - 1 - i].v[p], dps[i].v[p], y.v[p]);
-                st_pack<VEC>(dx + td * os, narrow<T, VEC>(y));
+                        for (int k = 0; k < W; ++k)
+                            if (td + k < end) y.v[p] = fma2(w[W - 1 - k].v[p], dps[k].v[p], y.v[p]);
+                    st_pack<VEC>(dx + td * os, narrow<T, VEC>(y));
+                }
+                slide(1);
             }
-            slide(1);
-            t += 1;
         }
+        if constexpr (Ring::kOn) copy_wait<0>();
     }
     if (!a.parts) return;
     const int tid = (int)(threadIdx.y * kConvLanes + threadIdx.x);
@@ -392,10 +477,19 @@ cudaError_t conv_launch(ConvArgs a, bool backward, cudaStream_t s) {
     if (blocks < 1) return cudaSuccess;
     if (blocks > INT32_MAX) return cudaErrorInvalidValue;
     const dim3 threads(kConvLanes, kConvRuns);
-    if (backward)
-        k_conv_bwd<T, VEC, W><<<(unsigned)blocks, threads, 0, s>>>(a);
-    else
-        k_conv_fwd<T, VEC, W><<<(unsigned)blocks, threads, 0, s>>>(a);
+    if (backward) {
+        constexpr int bytes = ConvRing<T, VEC, 2>::kBytes;
+        static LaunchCache cache;
+        LaunchGeom geo;
+        const cudaError_t e = cache.get([](int dev, LaunchGeom* g) {
+            return setup_persistent(k_conv_bwd<T, VEC, W>, kConvThreads, bytes, dev, g);
+        }, &geo);
+        if (e != cudaSuccess) return e;
+        k_conv_bwd<T, VEC, W><<<(unsigned)blocks, threads, bytes, s>>>(a);
+    } else {
+        constexpr int bytes = ConvRing<T, VEC, 1>::kBytes;
+        k_conv_fwd<T, VEC, W><<<(unsigned)blocks, threads, bytes, s>>>(a);
+    }
     return cudaGetLastError();
 }
 

@@ -17,7 +17,7 @@ struct ConvArgs {
 
 // A block has 32 lanes along the channels and 8 runs of tokens; the runs of a block are its token
 // tile (one partial row of the parameter gradients).
-constexpr int kConvLanes = 32, kConvRuns = 8, kConvRun = 32;
+constexpr int kConvLanes = 32, kConvRuns = 8, kConvRun = 64;
 constexpr int kConvTile = kConvRuns * kConvRun;
 
 cudaError_t conv_forward_f32(ConvArgs a, cudaStream_t s);

@@ -293,7 +293,7 @@ __global__ void __launch_bounds__(kPairThreads) k_scan(const ScanArgs a) {
                     for (int j = 0; j < N; ++j) {
                         const Pack<T, 2> pz = ld_pack<2>(rz + (j0 + j) * CT);
                         const float2 z = make_float2(to_f(pz.v[0]), to_f(pz.v[1]));
-                        y[j] = mul2(y[j], mul2(z, make_float2(sigmoid(z.x), sigmoid(z.y))));
+                        y[j] = mul2(y[j], mul2(z, sigmoid2(z)));
                     }
                 }
                 T* o = out + (t + j0) * ostr;

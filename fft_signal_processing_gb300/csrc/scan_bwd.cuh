@@ -149,29 +149,6 @@ __global__ void __launch_bounds__(kCarryThreads) k_scan_back_carry(const ScanBwd
     }
 }
 
-// Sum of V values over lanes that differ in the bits of `mask` steps (from W down to 1, times
-// STEP): while a lane carries more than one value it keeps half of them.
-template <int V, int W, int STEP>
-__device__ __forceinline__ void hand_out(float (&v)[V], int id) {
-    int cnt = V;
-#pragma unroll
-    for (int w = W; w; w /= 2) {
-        if (cnt > 1) {
-            cnt /= 2;
-            const bool up = id & w;
-#pragma unroll
-            for (int j = 0; j < V / 2; ++j) {
-                if (j < cnt) {
-                    const float send = up ? v[j] : v[j + cnt], keep = up ? v[j + cnt] : v[j];
-                    v[j] = keep + __shfl_xor_sync(0xffffffffu, send, w * STEP);
-                }
-            }
-        } else {
-            v[0] += __shfl_xor_sync(0xffffffffu, v[0], w * STEP);
-        }
-    }
-}
-
 template <int SL>
 struct BwdShape {
     static constexpr int NW = SL < 4 ? SL : 4, NT = NW * 32, CL = 32 / SL, CW = CL * 4;

@@ -106,6 +106,12 @@ __device__ __forceinline__ float max_nan(float a, float b) {  // a NaN stays
     return d;
 }
 
+__device__ __forceinline__ float2 sigmoid2(float2 x) {
+    const float2 e = mul2(x, splat(-kLog2e));
+    const float2 d = add2(make_float2(ex2(e.x), ex2(e.y)), splat(1.f));
+    return make_float2(rcp(d.x), rcp(d.y));
+}
+
 // log(1 + exp(x)) = max(x, 0) + log1p(t), t = exp(-|x|) in (0, 1], and log1p(t) = 2 atanh(w) with
 // w = t / (2 + t) <= 1/3: w times a polynomial in w^2, interpolated at Chebyshev nodes of
 // [0, 1/9] (relative error 8e-9).  The exponent's rounding error is put back, since t is the
@@ -127,11 +133,41 @@ __device__ __forceinline__ float2 softplus2(float2 x) {
 }
 __device__ __forceinline__ float softplus(float x) { return softplus2(splat(x)).x; }
 
-// Asynchronous copy of 16 bytes into shared memory; zeros where `in` is false (nothing is read).
+// Sum of V values over lanes that differ in the bits of `mask` steps (from W down to 1, times
+// STEP): while a lane carries more than one value it keeps half of them.
+template <int V, int W, int STEP>
+__device__ __forceinline__ void hand_out(float (&v)[V], int id) {
+    int cnt = V;
+#pragma unroll
+    for (int w = W; w; w /= 2) {
+        if (cnt > 1) {
+            cnt /= 2;
+            const bool up = id & w;
+#pragma unroll
+            for (int j = 0; j < V / 2; ++j) {
+                if (j < cnt) {
+                    const float send = up ? v[j] : v[j + cnt], keep = up ? v[j + cnt] : v[j];
+                    v[j] = keep + __shfl_xor_sync(0xffffffffu, send, w * STEP);
+                }
+            }
+        } else {
+            v[0] += __shfl_xor_sync(0xffffffffu, v[0], w * STEP);
+        }
+    }
+}
+
+// Asynchronous copies of 16 and 8 bytes into shared memory; zeros where `in` is false (nothing is
+// read).
 __device__ __forceinline__ void copy16(void* dst, const void* src, bool in) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(
                      (unsigned)__cvta_generic_to_shared(dst)),
                  "l"(src), "r"(in ? 16 : 0)
+                 : "memory");
+}
+__device__ __forceinline__ void copy8(void* dst, const void* src, bool in) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(
+                     (unsigned)__cvta_generic_to_shared(dst)),
+                 "l"(src), "r"(in ? 8 : 0)
                  : "memory");
 }
 __device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }

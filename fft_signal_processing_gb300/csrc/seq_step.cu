@@ -61,74 +61,120 @@ __global__ void __launch_bounds__(kThreads) k_conv_step(const ConvStepArgs a) {
     if (w > 1) st_pack<VEC>(dst + (w - 2) * a.d.channels, x);
 }
 
-// L lanes share a channel, four states each: a warp moves 32 * 16 contiguous bytes of states.
+// L lanes share a channel, four states each, and a thread has four channels, 32 / L apart, so that
+// a warp's accesses to the states are 512 contiguous bytes each.  What is needed once per channel
+// (softplus, the gate, the output) is done by the lane that owns it: the step is then bound by
+// the states' bytes and not by instructions.
 template <class T, int L>
 __global__ void __launch_bounds__(kThreads) k_scan_step(const ScanStepArgs a) {
-    constexpr int CT = kThreads / L;
+    constexpr int G = 32 / L, OWN = L >= 4 ? 1 : 4 / L;  // groups of lanes; channels a lane owns
     const int64_t q = blockIdx.x / a.ctiles;
-    const int64_t c = (blockIdx.x - q * a.ctiles) * CT + threadIdx.x / L;
-    const int n = (int)a.d.states, s0 = (int)(threadIdx.x % L) * 4;
-    const bool in = c < a.d.channels;
+    const int lane = (int)threadIdx.x & 31, sl = lane % L, s0 = sl * 4;
+    // channel k of the thread: cw + k * G
+    const int64_t cw = ((blockIdx.x - q * a.ctiles) * (kThreads / 32) + threadIdx.x / 32) * (4 * G) + lane / L;
+    const int n = (int)a.d.states, own0 = (sl & 3) * OWN % 4;  // the first channel that it owns
+    const bool owner = sl < 4;
     int64_t from, to;
     const bool live = step_slots(a.slots, a.slots_out, a.pool, q, &from, &to);
-    float y = 0.f, uu = 0.f, gate = 1.f;
-    if (in && live) {
-        const int64_t g = c / (a.d.channels / a.d.groups);
-        const T* B = static_cast<const T*>(a.d.B.data) + q * a.d.B.seq_stride + g * n;
-        const T* C = static_cast<const T*>(a.d.C.data) + q * a.d.C.seq_stride + g * n;
-        const float* src = a.state + (from * a.d.channels + c) * n;
-        float* dst = a.state + (to * a.d.channels + c) * n;
-        float h[4], A[4], b[4], cc[4];
+    const float* src = a.state + (live ? from * a.d.channels * n : 0);
+    float* dst = a.state + (live ? to * a.d.channels * n : 0);
+    float2 h[4][2], A[4][2];
+    auto states = [&](const float* p, bool in, float2 (&v)[2]) {
         if (a.vec) {
-            if (s0 < n) {
-                const float4 hv = *reinterpret_cast<const float4*>(src + s0);
-                const float4 av = *reinterpret_cast<const float4*>(a.d.A + c * n + s0);
-                h[0] = hv.x; h[1] = hv.y; h[2] = hv.z; h[3] = hv.w;
-                A[0] = av.x; A[1] = av.y; A[2] = av.z; A[3] = av.w;
-            }
+            float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (in && s0 < n) x = *reinterpret_cast<const float4*>(p + s0);
+            v[0] = make_float2(x.x, x.y);
+            v[1] = make_float2(x.z, x.w);
         } else {
 #pragma unroll
             for (int i = 0; i < 4; ++i)
-                if (s0 + i < n) {
-                    h[i] = src[s0 + i];
-                    A[i] = a.d.A[c * n + s0 + i];
-                }
+                (i & 1 ? v[i / 2].y : v[i / 2].x) = in && s0 + i < n ? p[s0 + i] : 0.f;
         }
+    };
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-            if (s0 + i < n) {
-                b[i] = to_f(B[s0 + i]);
-                cc[i] = to_f(C[s0 + i]);
-            }
-        uu = to_f(static_cast<const T*>(a.d.u.data)[q * a.d.u.seq_stride + c]);
-        float d = to_f(static_cast<const T*>(a.d.delta.data)[q * a.d.delta.seq_stride + c]);
-        if (a.d.z.data) {
-            const float z = to_f(static_cast<const T*>(a.d.z.data)[q * a.d.z.seq_stride + c]);
-            gate = z * sigmoid(z);
+    for (int k = 0; k < 4; ++k) {
+        const int64_t c = cw + k * G;
+        states(src + c * n, live && c < a.d.channels, h[k]);
+        states(a.d.A + c * n, live && c < a.d.channels, A[k]);
+    }
+    // B and C of the thread's states; with one group they serve all four channels
+    const T* B = static_cast<const T*>(a.d.B.data) + q * a.d.B.seq_stride;
+    const T* C = static_cast<const T*>(a.d.C.data) + q * a.d.C.seq_stride;
+    float2 b[2], cc[2];
+    auto inputs = [&](int64_t g) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const bool in = s0 + i < n;
+            (i & 1 ? b[i / 2].y : b[i / 2].x) = in ? to_f(B[g * n + s0 + i]) : 0.f;
+            (i & 1 ? cc[i / 2].y : cc[i / 2].x) = in ? to_f(C[g * n + s0 + i]) : 0.f;
         }
-        if (a.d.delta_bias) d += a.d.delta_bias[c];
-        if (a.d.softplus) d = softplus(d);
-        const float du = d * uu;
+    };
+    inputs(0);
+    float d[OWN], du[OWN], uu[OWN], z[OWN], D[OWN];
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-            if (s0 + i < n) {
-                h[i] = fmaf(ex2(d * (A[i] * kLog2e)), h[i], du * b[i]);
-                y = fmaf(cc[i], h[i], y);
-            }
-        if (a.vec) {
-            if (s0 < n) *reinterpret_cast<float4*>(dst + s0) = make_float4(h[0], h[1], h[2], h[3]);
-        } else {
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-                if (s0 + i < n) dst[s0 + i] = h[i];
-        }
+    for (int j = 0; j < OWN; ++j) {
+        const int64_t c = cw + (own0 + j) * G;
+        const bool in = live && c < a.d.channels;
+        uu[j] = in ? to_f(static_cast<const T*>(a.d.u.data)[q * a.d.u.seq_stride + c]) : 0.f;
+        d[j] = in ? to_f(static_cast<const T*>(a.d.delta.data)[q * a.d.delta.seq_stride + c]) : 0.f;
+        z[j] = in && a.d.z.data ? to_f(static_cast<const T*>(a.d.z.data)[q * a.d.z.seq_stride + c]) : 0.f;
+        D[j] = in && a.d.D ? a.d.D[c] : 0.f;
+        if (in && a.d.delta_bias) d[j] += a.d.delta_bias[c];
     }
 #pragma unroll
-    for (int o = L / 2; o; o >>= 1) y += __shfl_xor_sync(0xffffffffu, y, o);
-    if (in && threadIdx.x % L == 0) {
-        if (live && a.d.D) y = fmaf(a.d.D[c], uu, y);
-        if (live && a.d.z.data) y *= gate;
-        static_cast<T*>(a.out.data)[q * a.out.seq_stride + c] = from_f<T>(y);
+    for (int j = 0; j < OWN; ++j) {
+        if (a.d.softplus) d[j] = softplus(d[j]);
+        du[j] = d[j] * uu[j];
+    }
+    float y[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        const int64_t c = cw + k * G;
+        const int from_lane = lane - sl + k / OWN;
+        const float dk = L > 1 ? __shfl_sync(0xffffffffu, d[k % OWN], from_lane) : d[k % OWN];
+        const float uk = L > 1 ? __shfl_sync(0xffffffffu, du[k % OWN], from_lane) : du[k % OWN];
+        if (a.d.groups > 1 && c < a.d.channels) inputs(c / (a.d.channels / a.d.groups));
+        float2 acc = splat(0.f);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const float2 e = mul2(splat(dk), mul2(A[k][i], splat(kLog2e)));
+            h[k][i] = fma2(make_float2(ex2(e.x), ex2(e.y)), h[k][i], mul2(splat(uk), b[i]));
+            if (!a.vec) {  // a state beyond n stays out of y where d u is infinite
+                if (s0 + 2 * i >= n) h[k][i].x = 0.f;
+                if (s0 + 2 * i + 1 >= n) h[k][i].y = 0.f;
+            } else if (s0 >= n) {
+                h[k][i] = splat(0.f);
+            }
+            acc = fma2(cc[i], h[k][i], acc);
+        }
+        y[k] = acc.x + acc.y;
+        if (live && c < a.d.channels) {
+            float* p = dst + c * n;
+            if (a.vec) {
+                if (s0 < n)
+                    *reinterpret_cast<float4*>(p + s0) =
+                        make_float4(h[k][0].x, h[k][0].y, h[k][1].x, h[k][1].y);
+            } else {
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    if (s0 + i < n) p[s0 + i] = i & 1 ? h[k][i / 2].y : h[k][i / 2].x;
+            }
+        }
+    }
+    if constexpr (L >= 4) {
+        hand_out<4, 2, 1>(y, sl);
+#pragma unroll
+        for (int w = 4; w < L; w *= 2) y[0] += __shfl_xor_sync(0xffffffffu, y[0], w);
+    } else if constexpr (L == 2) {
+        hand_out<4, 1, 1>(y, sl);
+    }
+#pragma unroll
+    for (int j = 0; j < OWN; ++j) {
+        const int64_t c = cw + (own0 + j) * G;
+        float v = live ? fmaf(D[j], uu[j], y[j]) : 0.f;
+        if (live && a.d.z.data) v *= z[j] * sigmoid(z[j]);
+        if (owner && c < a.d.channels)
+            static_cast<T*>(a.out.data)[q * a.out.seq_stride + c] = from_f<T>(v);
     }
 }
 
@@ -151,7 +197,8 @@ cudaError_t conv_step(const ConvStepArgs& a, cudaStream_t s) {
 
 template <class T, int L>
 cudaError_t scan_step_lanes(ScanStepArgs a, cudaStream_t s) {
-    a.ctiles = (a.d.channels + kThreads / L - 1) / (kThreads / L);
+    constexpr int CT = kThreads / L * 4;
+    a.ctiles = (a.d.channels + CT - 1) / CT;
     if (a.ctiles * a.d.nseq > INT32_MAX) return cudaErrorInvalidValue;
     k_scan_step<T, L><<<(unsigned)(a.ctiles * a.d.nseq), kThreads, 0, s>>>(a);
     return cudaGetLastError();
