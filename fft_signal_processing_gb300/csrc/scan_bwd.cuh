@@ -10,8 +10,9 @@
 // before every 16th token.  Time is cut into chunks as in the forward scan; the gradient that a
 // chunk sends back, m = a[t0] q[t0], is m_local + exp(A sum d) m_in, so one pass computes m_local,
 // one runs along the chunks, and the main kernel walks each chunk from behind, 16 tokens at a
-// time: forward over the tile (start states of its 4-token pieces to shared memory), then
-// piece by piece backwards with the piece's states in registers.
+// time: what a token needs once per channel is prepared for the tile (the next tile's copies are
+// then on their way), then forward over the tile (start states of its 4-token pieces to shared
+// memory), then piece by piece backwards with the piece's states in registers.
 //
 // Main kernel: a thread holds 4 channels x 4 states, so the sums over states (for du, dd and y)
 // and over channels (for dB and dC) are mostly within the thread; what crosses lanes is summed
@@ -149,35 +150,42 @@ __global__ void __launch_bounds__(kCarryThreads) k_scan_back_carry(const ScanBwd
     }
 }
 
-template <int SL>
+template <class T, int SL>
 struct BwdShape {
     static constexpr int NW = SL < 4 ? SL : 4, NT = NW * 32, CL = 32 / SL, CW = CL * 4;
     static constexpr int CT = NW * CW, NP = SL * 4;
     static constexpr int TK = kScanTile, TS = 4, PIECES = TK / TS;
+    // dB and dC of a token: after one step over channel lanes a lane carries KV of the 8 values
+    static constexpr int KV = CL > 1 ? 4 : 8, RS = SL < 32 ? 32 + SL : 32;
     // shared memory, in floats
-    static constexpr int kIn = TK * CT;               // d, u, dy
-    static constexpr int kBC = TK * NP * 2;           // B, C, each value twice
-    static constexpr int kStart = PIECES * 4 * NT * 4;  // start states of the pieces
-    static constexpr int kRed = NW * TS * 8 * SL;     // dB, dC of the warps, double buffered
-    static constexpr int kFloats = 3 * kIn + 2 * kBC + kStart + 2 * kRed;
-    static constexpr int kBytes = kFloats * 4 + TK * 16;
+    static constexpr int kRaw = TK * CT;                         // values of one tensor's tile
+    static constexpr int kIn = TK * CT;                          // d, u, dy, and two factors
+    static constexpr int kBC = TK * NP * 2;                      // B, C, each value twice
+    static constexpr int kStart = (PIECES - 1) * 4 * NT * 4;     // start states of later pieces
+    static constexpr int kRed = TS * NW * KV * RS;               // dB, dC of a piece
+    static constexpr int kFloats = 5 * kIn + 2 * kBC + kStart + kRed;
+    static constexpr int kBytes = kFloats * 4 + 4 * kRaw * (int)sizeof(T) + TK * 8 + 16;
 };
 
 template <class T, int SL>
-__global__ void __launch_bounds__(BwdShape<SL>::NT) k_scan_bwd(const ScanBwdArgs a) {
-    using S = BwdShape<SL>;
+__global__ void __launch_bounds__(BwdShape<T, SL>::NT) k_scan_bwd(const ScanBwdArgs a) {
+    using S = BwdShape<T, SL>;
     constexpr int NT = S::NT, CL = S::CL, CT = S::CT, NP = S::NP, TK = S::TK, TS = S::TS;
+    constexpr int KV = S::KV, RS = S::RS;
     constexpr int OWN = SL == 1 ? 4 : (SL == 2 ? 2 : 1);  // channels that a lane owns
     extern __shared__ float4 smem4[];
-    float* sd = reinterpret_cast<float*>(smem4);
-    float* su = sd + S::kIn;
-    float* sy = su + S::kIn;
-    float* sB = sy + S::kIn;
+    float* sd = reinterpret_cast<float*>(smem4);  // d
+    float* su = sd + S::kIn;                      // u
+    float* sy = su + S::kIn;                      // dy = dout silu(z)
+    float* sf = sy + S::kIn;                      // dout silu'(z): dz = sf y
+    float* sg = sf + S::kIn;                      // derivative of d by delta
+    float* sB = sg + S::kIn;
     float* sC = sB + S::kBC;
-    float4* sh = reinterpret_cast<float4*>(sC + S::kBC);  // [piece][channel][thread]
-    float* sred = reinterpret_cast<float*>(sh) + S::kStart;
-    int64_t* sq_id = reinterpret_cast<int64_t*>(sred + 2 * S::kRed);  // [TK]
-    int* sq_flag = reinterpret_cast<int*>(sq_id + TK);                // [TK] 1: start, 2: end
+    float4* sh = reinterpret_cast<float4*>(sC + S::kBC);  // [piece - 1][channel][thread]
+    float* red = reinterpret_cast<float*>(sh) + S::kStart;
+    T* raw = reinterpret_cast<T*>(red + S::kRed);  // [tensor][token][channel]
+    int64_t* sq_id = reinterpret_cast<int64_t*>(raw + 4 * S::kRaw);  // [TK]
+    unsigned* sq_mask = reinterpret_cast<unsigned*>(sq_id + TK);     // tokens that start, that end
 
     const int n = (int)a.d.states, tid = (int)threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const bool packed = a.d.offsets != nullptr, gate = a.d.z.data != nullptr;
@@ -186,6 +194,7 @@ __global__ void __launch_bounds__(BwdShape<SL>::NT) k_scan_bwd(const ScanBwdArgs
     const int64_t chunk = rest % a.f.nchunks, row = rest / a.f.nchunks;
     const int64_t g = tile / a.ctiles, ct = tile - g * a.ctiles;
     const int64_t c0 = g * dg + ct * CT, cend = (g + 1) * dg;
+    const int width = (int)(cend - c0 < CT ? cend - c0 : CT);
     const int64_t t0 = chunk * a.f.chunk;
     const int64_t t1 = t0 + a.f.chunk < a.d.length ? t0 + a.f.chunk : a.d.length;
     const int sl = lane % SL, cl = lane / SL, s0 = sl * 4;
@@ -194,15 +203,42 @@ __global__ void __launch_bounds__(BwdShape<SL>::NT) k_scan_bwd(const ScanBwdArgs
     const int lo = lc + (SL == 1 ? 0 : (SL == 2 ? sl * 2 : (sl & 3)));
     const bool owner = SL <= 4 || sl < 4;
 
-    const T* u = row_of<T>(a.d.u, packed, row);
-    const T* dl = row_of<T>(a.d.delta, packed, row);
-    const T* z = row_of<T>(a.d.z, packed, row);
-    const T* dout = row_of<T>(a.g.dout, packed, row);
+    const T* src[4] = {row_of<T>(a.d.u, packed, row) + c0, row_of<T>(a.d.delta, packed, row) + c0,
+                       row_of<T>(a.g.dout, packed, row) + c0,
+                       gate ? row_of<T>(a.d.z, packed, row) + c0 : nullptr};
+    const int64_t str[4] = {a.d.u.tok_stride, a.d.delta.tok_stride, a.g.dout.tok_stride,
+                            a.d.z.tok_stride};
     const T* Bp = row_of<T>(a.d.B, packed, row) + g * n;
     const T* Cp = row_of<T>(a.d.C, packed, row) + g * n;
-    T* du = const_cast<T*>(row_of<T>(a.g.du, packed, row));
-    T* ddl = const_cast<T*>(row_of<T>(a.g.ddelta, packed, row));
-    T* dz = const_cast<T*>(row_of<T>(a.g.dz, packed, row));
+    T* du = const_cast<T*>(row_of<T>(a.g.du, packed, row)) + c0 + lo;
+    T* ddl = const_cast<T*>(row_of<T>(a.g.ddelta, packed, row)) + c0 + lo;
+    T* dz = const_cast<T*>(row_of<T>(a.g.dz, packed, row)) + c0 + lo;
+
+    auto copy = [&](int64_t tl) {  // the tile at tl; zeros outside the chunk
+        if (tl < t0) return;
+        const int len = t1 - tl < TK ? (int)(t1 - tl) : TK;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            if (k == 3 && !gate) break;
+            T* dst = raw + k * S::kRaw;
+            const T* p = src[k] + tl * str[k];
+            if (a.f.vec) {
+                constexpr int V = 16 / sizeof(T), R = CT / V;
+                for (int e = tid; e < TK * R; e += NT) {
+                    const int j = e / R, x = (e - j * R) * V;
+                    const bool in = j < len && x < width;
+                    copy16(dst + j * CT + x, in ? p + j * str[k] + x : src[k], in);
+                }
+            } else {
+#pragma unroll 4
+                for (int e = tid; e < TK * CT; e += NT) {
+                    const int j = e / CT, x = e - j * CT;
+                    dst[e] = j < len && x < width ? p[j * str[k] + x] : from_f<T>(0.f);
+                }
+            }
+        }
+        copy_commit();
+    };
 
     // pairs over channels: [state][channel pair]
     float2 A2[4][2], m[4][2], dA[4][2];
@@ -229,89 +265,128 @@ __global__ void __launch_bounds__(BwdShape<SL>::NT) k_scan_bwd(const ScanBwdArgs
             (i & 1 ? v[3][i / 2].y : v[3][i / 2].x) = x.w;
         }
     };
-    auto put = [&](int piece, const float2(&v)[4][2]) {
+    auto put = [&](int piece, const float2(&v)[4][2]) {  // a thread's own places
+        float4* p = sh + (piece - 1) * 4 * NT + tid;
 #pragma unroll
-        for (int p = 0; p < 2; ++p) {
-            sh[(piece * 4 + 2 * p) * NT + tid] = make_float4(v[0][p].x, v[1][p].x, v[2][p].x, v[3][p].x);
-            sh[(piece * 4 + 2 * p + 1) * NT + tid] =
-                make_float4(v[0][p].y, v[1][p].y, v[2][p].y, v[3][p].y);
+        for (int i = 0; i < 2; ++i) {
+            p[2 * i * NT] = make_float4(v[0][i].x, v[1][i].x, v[2][i].x, v[3][i].x);
+            p[(2 * i + 1) * NT] = make_float4(v[0][i].y, v[1][i].y, v[2][i].y, v[3][i].y);
         }
     };
     auto get = [&](int piece, float2(&v)[4][2]) {
+        const float4* p = sh + (piece - 1) * 4 * NT + tid;
 #pragma unroll
-        for (int p = 0; p < 2; ++p) {
-            const float4 x = sh[(piece * 4 + 2 * p) * NT + tid], y = sh[(piece * 4 + 2 * p + 1) * NT + tid];
-            v[0][p] = make_float2(x.x, y.x);
-            v[1][p] = make_float2(x.y, y.y);
-            v[2][p] = make_float2(x.z, y.z);
-            v[3][p] = make_float2(x.w, y.w);
+        for (int i = 0; i < 2; ++i) {
+            const float4 x = p[2 * i * NT], y = p[(2 * i + 1) * NT];
+            v[0][i] = make_float2(x.x, y.x);
+            v[1][i] = make_float2(x.y, y.y);
+            v[2][i] = make_float2(x.z, y.z);
+            v[3][i] = make_float2(x.w, y.w);
         }
     };
     auto initial = [&](int j, float2(&v)[4][2]) {
         load4(a.d.initial_state ? a.d.initial_state + sq_id[j] * a.d.channels * n : nullptr, n, v);
     };
+    const int64_t last_tile = (t1 - 1) / TK * TK, ntiles = (a.d.length + TK - 1) / TK;
+    copy(last_tile);
     load4(a.d.A, n, A2);
 #pragma unroll
     for (int s = 0; s < 4; ++s)
 #pragma unroll
         for (int p = 0; p < 2; ++p) {
-            A2[s][p] = mul2(A2[s][p], make_float2(kLog2e, kLog2e));
-            dA[s][p] = make_float2(0.f, 0.f);
-            m[s][p] = make_float2(0.f, 0.f);
+            A2[s][p] = mul2(A2[s][p], splat(kLog2e));
+            dA[s][p] = m[s][p] = splat(0.f);
         }
     if (a.f.nchunks > 1)
         load_padded(a.carry + (row * a.f.nchunks + chunk) * a.d.channels * NP, m);
-    float oD[OWN], obias[OWN], aD[OWN] = {}, abias[OWN] = {};
+    float oD[OWN], aD[OWN] = {}, abias[OWN] = {};
 #pragma unroll
-    for (int k = 0; k < OWN; ++k) {
-        const int64_t c = c0 + lo + k;
-        oD[k] = c < cend && a.d.D ? a.d.D[c] : 0.f;
-        obias[k] = c < cend && a.d.delta_bias ? a.d.delta_bias[c] : 0.f;
-    }
-    const int64_t ntiles = (a.d.length + TK - 1) / TK;
-    int rbuf = 0;
+    for (int k = 0; k < OWN; ++k) oD[k] = lo + k < width && a.d.D ? a.d.D[c0 + lo + k] : 0.f;
+    // the pairs of channels that this thread prepares: one where the block has as many threads
+    constexpr int HALF = CT / 2;
+    auto bias_of = [&](int pc) {
+        float2 v = splat(0.f);
+        if (a.d.delta_bias) {
+            if (pc < width) v.x = a.d.delta_bias[c0 + pc];
+            if (pc + 1 < width) v.y = a.d.delta_bias[c0 + pc + 1];
+        }
+        return v;
+    };
+    const float2 own_bias = bias_of(2 * (tid % HALF));
+    SeqAt cur = seq_at(a.d.offsets, a.d.nseq, a.d.length, row, t1 - 1);
+    auto down_to = [&](int64_t t, SeqAt& s) {  // packed: the sequence that holds an earlier token
+        while (s.q > 0 && t < s.begin) {
+            s.q -= 1;
+            s.end = s.begin;
+            s.begin = a.d.offsets[s.q];
+        }
+    };
 
-    for (int64_t tl = (t1 - 1) / TK * TK; tl >= t0; tl -= TK) {
+    for (int64_t tl = last_tile; tl >= t0; tl -= TK) {
         const int len = t1 - tl < TK ? (int)(t1 - tl) : TK;
-        __syncthreads();  // the last tile's shared memory is free
+        copy_wait<0>();
+        __syncthreads();  // the tile has landed; the last one's shared memory is free
+        if (packed) down_to(tl + len - 1, cur);
         if (warp == 0) {
-            SeqAt s = seq_at(a.d.offsets, a.d.nseq, a.d.length, row, tl);
+            SeqAt s = cur;
+            bool start = false, end = false;
             if (lane < len) {
-                seq_next(a.d.offsets, a.d.nseq, tl + lane, &s);
+                if (packed) down_to(tl + lane, s);
                 sq_id[lane] = s.q;
-                sq_flag[lane] = (tl + lane == s.begin ? 1 : 0) | (tl + lane + 1 == s.end ? 2 : 0);
+                start = tl + lane == s.begin;
+                end = tl + lane + 1 == s.end;
+            }
+            const unsigned starts = __ballot_sync(0xffffffffu, start);
+            const unsigned ends = __ballot_sync(0xffffffffu, end);
+            if (lane == 0) {
+                sq_mask[0] = starts;
+                sq_mask[1] = ends;
             }
         }
-        for (int i = tid; i < TK * CT; i += NT) {
-            const int j = i / CT, k = i - j * CT;
-            const int64_t c = c0 + k, t = tl + j;
-            float d = 0.f, uu = 0.f, dy = 0.f;
-            if (j < len && c < cend) {
-                d = to_f(dl[t * a.d.delta.tok_stride + c]);
-                if (a.d.delta_bias) d += a.d.delta_bias[c];
-                if (a.d.softplus) d = softplus(d);
-                uu = to_f(u[t * a.d.u.tok_stride + c]);
-                dy = to_f(dout[t * a.g.dout.tok_stride + c]);
-                if (gate) {
-                    const float zz = to_f(z[t * a.d.z.tok_stride + c]);
-                    dy *= zz * sigmoid(zz);
-                }
+#pragma unroll 2
+        for (int i = tid; i < TK * HALF; i += NT) {
+            const int j = i / HALF, pc = 2 * (i - j * HALF), e = j * CT + pc;
+            const float2 bias = NT >= HALF ? own_bias : bias_of(pc);
+            const Pack<T, 2> pu = ld_pack<2>(raw + e), pd = ld_pack<2>(raw + S::kRaw + e);
+            const Pack<T, 2> po = ld_pack<2>(raw + 2 * S::kRaw + e);
+            float2 d = add2(make_float2(to_f(pd.v[0]), to_f(pd.v[1])), bias), slope = splat(1.f);
+            if (a.d.softplus) {
+                slope = sigmoid2(d);
+                d = softplus2(d);
             }
-            sd[i] = d;
-            su[i] = uu;
-            sy[i] = dy;
+            float2 dy = make_float2(to_f(po.v[0]), to_f(po.v[1])), f = dy;
+            if (gate) {
+                const Pack<T, 2> pz = ld_pack<2>(raw + 3 * S::kRaw + e);
+                const float2 z = make_float2(to_f(pz.v[0]), to_f(pz.v[1])), s = sigmoid2(z);
+                f = mul2(dy, mul2(s, fma2(z, fma2(s, splat(-1.f), splat(1.f)), splat(1.f))));
+                dy = mul2(dy, mul2(z, s));
+            }
+            *reinterpret_cast<float2*>(sd + e) = d;
+            *reinterpret_cast<float2*>(su + e) = make_float2(to_f(pu.v[0]), to_f(pu.v[1]));
+            *reinterpret_cast<float2*>(sy + e) = dy;
+            *reinterpret_cast<float2*>(sf + e) = f;
+            *reinterpret_cast<float2*>(sg + e) = slope;
         }
         for (int i = tid; i < TK * NP; i += NT) {
             const int j = i / NP, s = i - j * NP;
             const bool in = j < len && s < n;
             const float b = in ? to_f(Bp[(tl + j) * a.d.B.tok_stride + s]) : 0.f;
             const float c = in ? to_f(Cp[(tl + j) * a.d.C.tok_stride + s]) : 0.f;
-            sB[2 * i] = sB[2 * i + 1] = b;
-            sC[2 * i] = sC[2 * i + 1] = c;
+            *reinterpret_cast<float2*>(sB + 2 * i) = splat(b);
+            *reinterpret_cast<float2*>(sC + 2 * i) = splat(c);
         }
-        __syncthreads();
-
+        const float* start_states = a.f.tiles + (row * ntiles + tl / TK) * a.d.channels * NP;
         float2 h[4][2];
+        load_padded(start_states, h);
+        __syncthreads();
+        copy(tl - TK);
+        const unsigned starts = sq_mask[0], ends = sq_mask[1];
+        T* pdu = du + tl * a.g.du.tok_stride;
+        T* pdd = ddl + tl * a.g.ddelta.tok_stride;
+        T* pdz = dz + tl * a.g.dz.tok_stride;
+        const int sdu = (int)a.g.du.tok_stride, sdd = (int)a.g.ddelta.tok_stride;
+        const int sdz = (int)a.g.dz.tok_stride;
+
         auto step = [&](int j) {  // h of token j from h of the token before
             const float4 d4 = *reinterpret_cast<const float4*>(sd + j * CT + lc);
             const float4 u4 = *reinterpret_cast<const float4*>(su + j * CT + lc);
@@ -319,74 +394,60 @@ __global__ void __launch_bounds__(BwdShape<SL>::NT) k_scan_bwd(const ScanBwdArgs
             const float2 du2[2] = {mul2(dd[0], make_float2(u4.x, u4.y)),
                                    mul2(dd[1], make_float2(u4.z, u4.w))};
 #pragma unroll
-            for (int s = 0; s < 4; ++s) {
-                const float2 b = *reinterpret_cast<const float2*>(sB + (j * NP + s0 + s) * 2);
+            for (int s = 0; s < 4; s += 2) {
+                const float4 b4 = *reinterpret_cast<const float4*>(sB + (j * NP + s0 + s) * 2);
 #pragma unroll
-                for (int p = 0; p < 2; ++p) {
-                    const float2 e = mul2(dd[p], A2[s][p]);
-                    h[s][p] = fma2(make_float2(ex2(e.x), ex2(e.y)), h[s][p], mul2(du2[p], b));
-                    if (s0 + s >= n) h[s][p] = make_float2(0.f, 0.f);
+                for (int k = 0; k < 2; ++k) {
+                    const float2 b = k ? make_float2(b4.z, b4.w) : make_float2(b4.x, b4.y);
+#pragma unroll
+                    for (int p = 0; p < 2; ++p) {
+                        const float2 e = mul2(dd[p], A2[s + k][p]);
+                        h[s + k][p] = fma2(make_float2(ex2(e.x), ex2(e.y)), h[s + k][p], mul2(du2[p], b));
+                        if (s0 + s + k >= n) h[s + k][p] = splat(0.f);
+                    }
                 }
             }
         };
-        load_padded(a.f.tiles + (row * ntiles + tl / TK) * a.d.channels * NP, h);
         const int last = (len - 1) / TS;
-        for (int piece = 0; piece <= last; ++piece) {
-            put(piece, h);
-            if (piece < last) {
-#pragma unroll
-                for (int j = 0; j < TS; ++j) {
-                    if (sq_flag[piece * TS + j] & 1) initial(piece * TS + j, h);
-                    step(piece * TS + j);
-                }
-            }
-        }
-        for (int piece = last; piece >= 0; --piece) {
-            float2 hist[TS][4][2], hs[4][2];
-            get(piece, h);
-#pragma unroll
-            for (int s = 0; s < 4; ++s)
-#pragma unroll
-                for (int p = 0; p < 2; ++p) hs[s][p] = h[s][p];
+        for (int piece = 0; piece < last; ++piece) {
 #pragma unroll
             for (int j = 0; j < TS; ++j) {
-                if (piece * TS + j < len) {
-                    if (sq_flag[piece * TS + j] & 1) initial(piece * TS + j, h);
-                    step(piece * TS + j);
-                }
+                if (starts >> (piece * TS + j) & 1) initial(piece * TS + j, h);
+                step(piece * TS + j);
+            }
+            put(piece + 1, h);
+        }
+        for (int piece = last; piece >= 0; --piece) {
+            float2 hist[TS + 1][4][2];  // the states before the piece and after its tokens
+            if (piece < last) {
+                if (piece > 0)
+                    get(piece, h);
+                else
+                    load_padded(start_states, h);
+            }
+#pragma unroll
+            for (int j = 0; j <= TS; ++j) {
 #pragma unroll
                 for (int s = 0; s < 4; ++s)
 #pragma unroll
                     for (int p = 0; p < 2; ++p) hist[j][s][p] = h[s][p];
+                if (j < TS && piece * TS + j < len) {
+                    if (starts >> (piece * TS + j) & 1) initial(piece * TS + j, h);
+                    step(piece * TS + j);
+                }
             }
-            float* red = sred + rbuf * S::kRed;
 #pragma unroll
             for (int jj = TS - 1; jj >= 0; --jj) {
                 const int j = piece * TS + jj;
                 if (j >= len) continue;
-                const int64_t t = tl + j;
-                const int flag = sq_flag[j];
-                // what the owner of a channel still needs of its inputs
-                float ro[OWN], rz[OWN], re[OWN];
-#pragma unroll
-                for (int k = 0; k < OWN; ++k) {
-                    const int64_t c = c0 + lo + k;
-                    const bool in = owner && c < cend;
-                    ro[k] = in && gate ? to_f(dout[t * a.g.dout.tok_stride + c]) : 0.f;
-                    rz[k] = in && gate ? to_f(z[t * a.d.z.tok_stride + c]) : 0.f;
-                    re[k] = in && a.d.softplus ? to_f(dl[t * a.d.delta.tok_stride + c]) + obias[k] : 0.f;
-                }
-                if (flag & 2)
+                if (ends >> j & 1)
                     load4(a.g.dfinal_state ? a.g.dfinal_state + sq_id[j] * a.d.channels * n : nullptr,
                           n, m);
-                float2 hp[4][2];  // the state before the token
-                if (flag & 1) {
-                    initial(j, hp);
-                } else {
-#pragma unroll
-                    for (int s = 0; s < 4; ++s)
-#pragma unroll
-                        for (int p = 0; p < 2; ++p) hp[s][p] = jj > 0 ? hist[jj > 0 ? jj - 1 : 0][s][p] : hs[s][p];
+                // before a sequence's first token stands its initial state; what stands there is
+                // also the state after the token before, kept in a place that is free by now
+                if (starts >> j & 1) {
+                    put(piece ? piece : 1, hist[jj]);
+                    initial(j, hist[jj]);
                 }
                 const float4 d4 = *reinterpret_cast<const float4*>(sd + j * CT + lc);
                 const float4 u4 = *reinterpret_cast<const float4*>(su + j * CT + lc);
@@ -401,38 +462,39 @@ __global__ void __launch_bounds__(BwdShape<SL>::NT) k_scan_bwd(const ScanBwdArgs
                 for (int s = 0; s < 4; ++s) {
                     const float2 b = *reinterpret_cast<const float2*>(sB + (j * NP + s0 + s) * 2);
                     const float2 c = *reinterpret_cast<const float2*>(sC + (j * NP + s0 + s) * 2);
-                    float2 db = make_float2(0.f, 0.f), dc = make_float2(0.f, 0.f);
+                    float2 db, dc;
 #pragma unroll
                     for (int p = 0; p < 2; ++p) {
                         const float2 e = mul2(dd[p], A2[s][p]);
                         const float2 q = fma2(dy[p], c, m[s][p]);
                         const float2 aq = mul2(make_float2(ex2(e.x), ex2(e.y)), q);
-                        const float2 w = mul2(aq, hp[s][p]);
-                        yv[p] = fma2(c, hist[jj][s][p], yv[p]);
+                        const float2 w = mul2(aq, hist[jj][s][p]);
+                        yv[p] = fma2(c, hist[jj + 1][s][p], yv[p]);
                         qb[p] = fma2(q, b, qb[p]);
                         qa[p] = fma2(w, A2[s][p], qa[p]);
                         dA[s][p] = fma2(w, dd[p], dA[s][p]);
-                        db = fma2(q, du2[p], db);
-                        dc = fma2(dy[p], hist[jj][s][p], dc);
+                        db = p ? fma2(q, du2[p], db) : mul2(q, du2[p]);
+                        dc = p ? fma2(dy[p], hist[jj + 1][s][p], dc) : mul2(dy[p], hist[jj + 1][s][p]);
                         m[s][p] = aq;
                     }
                     bc[s] = db.x + db.y;
                     bc[4 + s] = dc.x + dc.y;
                 }
-                if (flag & 1) {  // the sequence's first token
+                if (starts >> j & 1) {  // the sequence's first token
                     if (a.g.dinitial_state) {
 #pragma unroll
                         for (int i = 0; i < 4; ++i)
 #pragma unroll
                             for (int s = 0; s < 4; ++s)
-                                if (c0 + lc + i < cend && s0 + s < n)
+                                if (lc + i < width && s0 + s < n)
                                     a.g.dinitial_state[(sq_id[j] * a.d.channels + c0 + lc + i) * n + s0 + s] =
                                         i & 1 ? m[s][i / 2].y : m[s][i / 2].x;
                     }
 #pragma unroll
                     for (int s = 0; s < 4; ++s)
 #pragma unroll
-                        for (int p = 0; p < 2; ++p) m[s][p] = make_float2(0.f, 0.f);
+                        for (int p = 0; p < 2; ++p) m[s][p] = splat(0.f);
+                    get(piece ? piece : 1, hist[jj]);
                 }
                 // sums over states, handed out to the lanes of a channel group
                 float vy[4] = {yv[0].x, yv[0].y, yv[1].x, yv[1].y};
@@ -455,67 +517,66 @@ __global__ void __launch_bounds__(BwdShape<SL>::NT) k_scan_bwd(const ScanBwdArgs
                 }
 #pragma unroll
                 for (int k = 0; k < OWN; ++k) {
-                    const int64_t c = c0 + lo + k;
-                    if (!owner || c >= cend) continue;
-                    const float d = sd[j * CT + lo + k], uu = su[j * CT + lo + k], dyk = sy[j * CT + lo + k];
-                    du[t * a.g.du.tok_stride + c] = from_f<T>(fmaf(d, vb[k], dyk * oD[k]));
-                    float e = fmaf(uu, vb[k], va[k] * kLn2);  // A = A2 ln 2
-                    if (a.d.softplus) e *= sigmoid(re[k]);
-                    ddl[t * a.g.ddelta.tok_stride + c] = from_f<T>(e);
-                    abias[k] += e;
+                    const int e = j * CT + lo + k;
+                    const float d = sd[e], uu = su[e], dyk = sy[e];
+                    const float dv = fmaf(d, vb[k], dyk * oD[k]);
+                    const float de = fmaf(uu, vb[k], va[k] * kLn2) * sg[e];  // A = A2 ln 2
+                    abias[k] += de;
                     aD[k] = fmaf(dyk, uu, aD[k]);
-                    if (gate) {
-                        const float y = fmaf(oD[k], uu, vy[k]), sg = sigmoid(rz[k]);
-                        dz[t * a.g.dz.tok_stride + c] =
-                            from_f<T>(ro[k] * y * (sg * (1.f + rz[k] * (1.f - sg))));
+                    if (owner && lo + k < width) {
+                        pdu[(int64_t)j * sdu + k] = from_f<T>(dv);
+                        pdd[(int64_t)j * sdd + k] = from_f<T>(de);
+                        if (gate) pdz[(int64_t)j * sdz + k] = from_f<T>(sf[e] * fmaf(oD[k], uu, vy[k]));
                     }
                 }
-                // sums over channels, handed out to the channel lanes
-                constexpr int LEFT = CL >= 8 ? 1 : 8 / CL;
-                hand_out<8, CL / 2, SL>(bc, cl);
-                int vi = 0;
-                if (CL >= 2) vi += (cl & (CL / 2)) ? 4 : 0;
-                if (CL >= 4) vi += (cl & (CL / 4)) ? 2 : 0;
-                if (CL >= 8) vi += (cl & (CL / 8)) ? 1 : 0;
-                if (CL <= 8 || cl % (CL / 8) == 0) {
+                // sums over channels: one step between lanes, the rest through shared memory
+                if constexpr (CL > 1) {
+                    const bool up = cl & (CL / 2);
 #pragma unroll
-                    for (int k = 0; k < LEFT; ++k)
-                        red[((warp * TS + jj) * 8 + vi + k) * SL + sl] = bc[k];
+                    for (int k = 0; k < 4; ++k) {
+                        const float send = up ? bc[k] : bc[k + 4], keep = up ? bc[k + 4] : bc[k];
+                        bc[k] = keep + __shfl_xor_sync(0xffffffffu, send, CL / 2 * SL);
+                    }
                 }
+#pragma unroll
+                for (int k = 0; k < KV; ++k) red[((jj * S::NW + warp) * KV + k) * RS + lane] = bc[k];
             }
             __syncthreads();
-            // the piece's dB and dC, summed over the warps; the other buffer is filled meanwhile
+            // the piece's dB and dC: value v (dB of 4 states, dC of 4 states) of state lane i
             const int plen = len - piece * TS < TS ? len - piece * TS : TS;
-            for (int i = tid; i < plen * 8 * SL; i += NT) {
-                const int jj = i / (8 * SL), v = (i / SL) % 8, state = (i % SL) * 4 + (v & 3);
+            for (int o = tid; o < plen * 8 * SL; o += NT) {
+                const int jj = o / (8 * SL), v = o / SL % 8, i = o % SL, state = i * 4 + (v & 3);
+                constexpr int LANES = CL > 1 ? CL / 2 : 1;
+                const float* p = red + (jj * S::NW * KV + (CL > 1 ? v & 3 : v)) * RS + i +
+                                 (CL > 1 ? (v >> 2) * (CL / 2) * SL : 0);
                 float x = 0.f;
 #pragma unroll
-                for (int w = 0; w < S::NW; ++w) x += red[w * TS * 8 * SL + i];
+                for (int w = 0; w < S::NW; ++w)
+#pragma unroll
+                    for (int k = 0; k < LANES; ++k) x += p[w * KV * RS + k * SL];
                 if (state < n) {
                     const int64_t t = tl + piece * TS + jj;
                     a.bc[((((ct * a.f.rows + row) * a.d.length + t) * a.d.groups + g) * 2 + (v >> 2)) * n +
                          state] = x;
                 }
             }
-            rbuf ^= 1;
+            if (piece) __syncthreads();  // the next piece writes the same places
         }
     }
+    copy_wait<0>();
     const int64_t part = row * a.f.nchunks + chunk;
-    if (a.pA) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
+    for (int i = 0; i < 4; ++i)
 #pragma unroll
-            for (int s = 0; s < 4; ++s)
-                if (c0 + lc + i < cend && s0 + s < n)
-                    a.pA[(part * a.d.channels + c0 + lc + i) * n + s0 + s] =
-                        i & 1 ? dA[s][i / 2].y : dA[s][i / 2].x;
-    }
+        for (int s = 0; s < 4; ++s)
+            if (lc + i < width && s0 + s < n)
+                a.pA[(part * a.d.channels + c0 + lc + i) * n + s0 + s] =
+                    i & 1 ? dA[s][i / 2].y : dA[s][i / 2].x;
 #pragma unroll
     for (int k = 0; k < OWN; ++k) {
-        const int64_t c = c0 + lo + k;
-        if (!owner || c >= cend) continue;
-        if (a.pD) a.pD[part * a.d.channels + c] = aD[k];
-        if (a.pbias) a.pbias[part * a.d.channels + c] = abias[k];
+        if (!owner || lo + k >= width) continue;
+        a.pD[part * a.d.channels + c0 + lo + k] = aD[k];
+        a.pbias[part * a.d.channels + c0 + lo + k] = abias[k];
     }
 }
 
@@ -550,7 +611,7 @@ __global__ void __launch_bounds__(256) k_scan_back_empty(const ScanBwdArgs a) {
 
 template <class T, int SL>
 cudaError_t scan_bwd_main(const ScanBwdArgs& a, cudaStream_t s) {
-    using S = BwdShape<SL>;
+    using S = BwdShape<T, SL>;
     static LaunchCache cache;
     LaunchGeom geo;
     cudaError_t e = cache.get([](int dev, LaunchGeom* g) {
@@ -574,8 +635,14 @@ cudaError_t scan_bwd_back(const ScanBwdArgs& a, cudaStream_t s) {
 }
 
 template <class T>
-cudaError_t scan_bwd_run(const ScanBwdArgs& a, cudaStream_t s) {
+cudaError_t scan_bwd_run(ScanBwdArgs a, cudaStream_t s) {
     cudaError_t e = cudaSuccess;
+    auto rows16 = [&](const fft_seq& q) {
+        return !q.data || (aligned_to(q.data, 16) && q.tok_stride * sizeof(T) % 16 == 0 &&
+                           (a.d.offsets || q.seq_stride * sizeof(T) % 16 == 0));
+    };
+    a.f.vec = a.d.channels / a.d.groups * sizeof(T) % 16 == 0 && rows16(a.d.u) &&
+              rows16(a.d.delta) && rows16(a.d.z) && rows16(a.g.dout);
     const int64_t n = a.d.states, parts = a.f.rows * a.f.nchunks;
     if (a.d.length > 0) {
         if (parts * a.back_ctiles * a.d.groups > INT32_MAX) return cudaErrorInvalidValue;

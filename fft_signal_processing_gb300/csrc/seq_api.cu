@@ -9,7 +9,8 @@ using namespace gbfft;
 
 namespace {
 
-constexpr int64_t kMaxElements = INT64_C(1) << 58;  // strides and offsets stay in 64 bits
+constexpr int64_t kMaxElements = INT64_C(1) << 58;  // offsets stay in 64 bits
+constexpr int64_t kMaxTokStride = INT64_C(1) << 26;  // 16 tokens stay in 32 bits
 
 int status(cudaError_t e) {
     return e == cudaSuccess ? FFT_OK
@@ -23,7 +24,7 @@ int check_seq(const fft_seq& s, int64_t width, int64_t nseq, int64_t length, boo
     if (s.tok_stride < 0 || s.seq_stride < 0) return FFT_ERR_INVALID_ARG;
     if (output && length > 1 && s.tok_stride < width) return FFT_ERR_INVALID_ARG;
     if (output && !packed && nseq > 1 && length > 0 && s.seq_stride < width) return FFT_ERR_INVALID_ARG;
-    if (s.tok_stride > kMaxElements / (length + 1) ||
+    if (s.tok_stride > kMaxTokStride ||
         (!packed && s.seq_stride > kMaxElements / (nseq + 1)))
         return FFT_ERR_UNSUPPORTED_SIZE;
     return aligned_to(s.data, size) ? FFT_OK : FFT_ERR_MISALIGNED;
