@@ -63,6 +63,24 @@ __device__ __forceinline__ void store_states(float* p, int s0, int n, const floa
     }
 }
 
+// The same for rows padded to a multiple of four states, 16-byte aligned.
+template <int SPT>
+__device__ __forceinline__ void load_row(const float* p, float2 (&h)[SPT / 2]) {
+#pragma unroll
+    for (int i = 0; i < SPT / 4; ++i) {
+        const float4 v = *reinterpret_cast<const float4*>(p + 4 * i);
+        h[2 * i] = make_float2(v.x, v.y);
+        h[2 * i + 1] = make_float2(v.z, v.w);
+    }
+}
+template <int SPT>
+__device__ __forceinline__ void store_row(float* p, const float2 (&h)[SPT / 2]) {
+#pragma unroll
+    for (int i = 0; i < SPT / 4; ++i)
+        *reinterpret_cast<float4*>(p + 4 * i) =
+            make_float4(h[2 * i].x, h[2 * i].y, h[2 * i + 1].x, h[2 * i + 1].y);
+}
+
 // The blocks behind the outputs: a sequence without tokens ends in its initial state.
 __device__ __forceinline__ void scan_empty(const ScanArgs& a, int64_t q) {
     const int64_t per = a.d.channels * a.d.states;
@@ -205,8 +223,12 @@ __global__ void __launch_bounds__(kPairThreads) k_scan(const ScanArgs a) {
         initial();
     } else {
 #pragma unroll
-        for (int k = 0; k < 2; ++k)
-            load_states<SPT>(!SUMMARY && live[k] ? a.carry + carry_at + k * SPT : nullptr, 0, SPT, h[k]);
+        for (int k = 0; k < 2; ++k) {
+            if (!SUMMARY && live[k])
+                load_row<SPT>(a.carry + carry_at + k * SPT, h[k]);
+            else
+                load_states<SPT>(nullptr, 0, SPT, h[k]);
+        }
     }
     stage_bc(0);
     fetch(TK);
@@ -226,7 +248,7 @@ __global__ void __launch_bounds__(kPairThreads) k_scan(const ScanArgs a) {
             float* p = a.tiles + ((blk.row * tiles + (blk.t0 + t) / kScanTile) * a.d.channels + c) * SPT;
 #pragma unroll
             for (int k = 0; k < 2; ++k)
-                if (live[k]) store_states<SPT>(p + k * SPT, 0, SPT, h[k]);
+                if (live[k]) store_row<SPT>(p + k * SPT, h[k]);
         }
         const T* ru = raw + stage * M::kTensors * M::kRaw + lc;
         const T* rd = ru + M::kRaw;
@@ -345,7 +367,7 @@ __global__ void __launch_bounds__(kPairThreads) k_scan(const ScanArgs a) {
 #pragma unroll
         for (int k = 0; k < 2; ++k)
             if (live[k]) {
-                store_states<SPT>(a.carry + carry_at + k * SPT, 0, SPT, h[k]);
+                store_row<SPT>(a.carry + carry_at + k * SPT, h[k]);
                 a.dsum[(blk.row * a.nchunks + blk.chunk) * a.d.channels + c + k] = k ? dsum.y : dsum.x;
             }
         if (tid == 0 && blk.c0 == 0) a.reset[blk.row * a.nchunks + blk.chunk] = has_reset;
@@ -463,8 +485,10 @@ __global__ void __launch_bounds__(kLanesThreads) k_scan_lanes(const ScanArgs a) 
     bool has_reset = sq.begin == blk.t0;
     if (sq.begin == blk.t0)
         initial();
+    else if (!SUMMARY && live)
+        load_row<SPT>(a.carry + carry_at + s0, h);
     else
-        load_states<SPT>(!SUMMARY && live ? a.carry + carry_at : nullptr, s0, NP, h);
+        load_states<SPT>(nullptr, 0, SPT, h);
     float dsum = 0.f;
     stage_bc(0);
     fetch(TK);
@@ -482,8 +506,8 @@ __global__ void __launch_bounds__(kLanesThreads) k_scan_lanes(const ScanArgs a) 
         static_assert(kLanesTile == kScanTile, "states are written once a tile");
         if (PASS == SCAN_TILES && live) {
             const int64_t tiles = (a.d.length + kScanTile - 1) / kScanTile;
-            store_states<SPT>(a.tiles + ((blk.row * tiles + (blk.t0 + t) / kScanTile) * a.d.channels + c) * NP,
-                              s0, NP, h);
+            store_row<SPT>(
+                a.tiles + ((blk.row * tiles + (blk.t0 + t) / kScanTile) * a.d.channels + c) * NP + s0, h);
         }
         const T* ru = raw + stage * M::kTensors * M::kRaw + lc;
         const T* rd = ru + M::kRaw;
@@ -607,7 +631,7 @@ __global__ void __launch_bounds__(kLanesThreads) k_scan_lanes(const ScanArgs a) 
     copy_wait<0>();
     if (SUMMARY) {
         if (live) {
-            store_states<SPT>(a.carry + carry_at, s0, NP, h);
+            store_row<SPT>(a.carry + carry_at + s0, h);
             if (sl == 0) a.dsum[(blk.row * a.nchunks + blk.chunk) * a.d.channels + c] = dsum;
         }
         if (tid == 0 && blk.c0 == 0) a.reset[blk.row * a.nchunks + blk.chunk] = has_reset;

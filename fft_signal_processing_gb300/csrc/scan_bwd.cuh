@@ -25,7 +25,170 @@
 
 namespace gbfft {
 
-// The gradient that a chunk sends back, with nothing entering from behind.
+// The gradient that a chunk sends back, with nothing entering from behind: the tokens in reverse,
+//   m <- a[t] (dy[t] C[t] + m).
+// Up to 16 states: two channels per thread, built like the forward kernel k_scan.
+template <class T, int SPT>
+__global__ void __launch_bounds__(kPairThreads) k_scan_back_pair(const ScanBwdArgs a) {
+    constexpr int NT = kPairThreads, CT = kPairChannels, TK = kPairTile, ST = 3, RAW = TK * CT;
+    constexpr int CN = (TK * SPT + NT - 1) / NT;
+    extern __shared__ float4 smem4[];
+    T* raw = reinterpret_cast<T*>(smem4);  // [stage][delta, dout, z][token][channel]
+    float* sc = reinterpret_cast<float*>(raw + ST * 3 * RAW);  // [buffer][token][state]
+    const int n = (int)a.d.states, tid = (int)threadIdx.x;
+    const bool packed = a.d.offsets != nullptr, gate = a.d.z.data != nullptr;
+    // chunk 0 sends nothing on: blocks are the chunks 1 ...
+    ScanBlock blk = scan_block(a.f, blockIdx.x, a.f.nchunks - 1, CT);
+    blk.chunk += 1;
+    blk.t0 += a.f.chunk;
+    blk.t1 = blk.t0 + a.f.chunk < a.d.length ? blk.t0 + a.f.chunk : a.d.length;
+    const int width = (int)(blk.cend - blk.c0 < CT ? blk.cend - blk.c0 : CT);
+    const int lc = 2 * tid, len = (int)(blk.t1 - blk.t0);
+    const int64_t c = blk.c0 + lc;
+    const bool live[2] = {lc < width, lc + 1 < width};
+    // tokens count from t0; tiles lie at multiples of TK, the last one may be short
+    const T* src[3] = {row_of<T>(a.d.delta, packed, blk.row) + blk.t0 * a.d.delta.tok_stride + blk.c0,
+                       row_of<T>(a.g.dout, packed, blk.row) + blk.t0 * a.g.dout.tok_stride + blk.c0,
+                       gate ? row_of<T>(a.d.z, packed, blk.row) + blk.t0 * a.d.z.tok_stride + blk.c0
+                            : nullptr};
+    const int64_t str[3] = {a.d.delta.tok_stride, a.g.dout.tok_stride, a.d.z.tok_stride};
+    const T* Cp = row_of<T>(a.d.C, packed, blk.row) + blk.t0 * a.d.C.tok_stride + blk.g * n;
+    auto copy = [&](int t, int stage) {
+        if (t >= 0) {
+#pragma unroll
+            for (int k = 0; k < 3; ++k) {
+                if (k == 2 && !gate) break;
+                T* dst = raw + (stage * 3 + k) * RAW;
+                if (a.f.vec) {
+                    constexpr int V = 16 / sizeof(T), R = CT / V, STEP = NT / R;
+                    const int j0 = tid / R, x = (tid - j0 * R) * V;
+                    const T* p = src[k] + (t + j0) * str[k] + x;
+#pragma unroll
+                    for (int j = 0; j < TK; j += STEP, p += STEP * str[k]) {
+                        const bool in = t + j0 + j < len && x < width;
+                        copy16(dst + (j0 + j) * CT + x, in ? p : src[k], in);
+                    }
+                } else {
+#pragma unroll 4
+                    for (int e = tid; e < RAW; e += NT) {
+                        const int j = e / CT, x = e - j * CT;
+                        dst[e] = t + j < len && x < width ? src[k][(t + j) * str[k] + x] : from_f<T>(0.f);
+                    }
+                }
+            }
+        }
+        copy_commit();
+    };
+    T pC[CN];
+    auto fetch = [&](int t) {
+#pragma unroll
+        for (int i = 0; i < CN; ++i) {
+            const int e = tid + i * NT, j = e / SPT, s = e - j * SPT;
+            const bool in = (TK * SPT % NT == 0 || e < TK * SPT) && s < n && t >= 0 && t + j < len;
+            pC[i] = in ? Cp[(t + j) * a.d.C.tok_stride + s] : from_f<T>(0.f);
+        }
+    };
+    auto stage_c = [&](int buf) {
+#pragma unroll
+        for (int i = 0; i < CN; ++i) {
+            const int e = tid + i * NT;
+            if (TK * SPT % NT == 0 || e < TK * SPT) sc[buf * TK * SPT + e] = to_f(pC[i]);
+        }
+    };
+    const int first = (len - 1) / TK * TK;
+#pragma unroll
+    for (int i = 0; i < ST - 1; ++i) copy(first - i * TK, i);
+    fetch(first);
+    float2 A2[2][SPT / 2], m[2][SPT / 2], bias = splat(0.f);
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+        load_states<SPT>(live[k] ? a.d.A + (c + k) * n : nullptr, 0, n, A2[k]);
+        load_states<SPT>(nullptr, 0, n, m[k]);
+#pragma unroll
+        for (int i = 0; i < SPT / 2; ++i) A2[k][i] = mul2(A2[k][i], splat(kLog2e));
+        if (live[k] && a.d.delta_bias) (k ? bias.y : bias.x) = a.d.delta_bias[c + k];
+    }
+    stage_c(0);
+    fetch(first - TK);
+    SeqAt sq = seq_at(a.d.offsets, a.d.nseq, a.d.length, blk.row, blk.t1 - 1);
+    int stage = 0, buf = 0;
+    for (int t = first; t >= 0; t -= TK) {
+        copy_wait<ST - 2>();
+        __syncthreads();  // this tile has landed; the last one's buffers are free
+        copy(t - (ST - 1) * TK, stage >= 1 ? stage - 1 : ST - 1);
+        stage_c(buf ^ 1);
+        fetch(t - 2 * TK);
+        const T* rd = raw + stage * 3 * RAW + lc;
+        const T* ro = rd + RAW;
+        const T* rz = ro + RAW;
+        const float* sC = sc + buf * TK * SPT;
+        const int tl = len - t < TK ? len - t : TK;
+        // d and dy of all tokens, then the recurrence
+        float2 d[TK], dy[TK];
+#pragma unroll
+        for (int j = 0; j < TK; ++j) {
+            const Pack<T, 2> pd = ld_pack<2>(rd + j * CT), po = ld_pack<2>(ro + j * CT);
+            d[j] = add2(make_float2(to_f(pd.v[0]), to_f(pd.v[1])), bias);
+            dy[j] = make_float2(to_f(po.v[0]), to_f(po.v[1]));
+            if (a.d.softplus) d[j] = softplus2(d[j]);
+            if (gate) {
+                const Pack<T, 2> pz = ld_pack<2>(rz + j * CT);
+                const float2 z = make_float2(to_f(pz.v[0]), to_f(pz.v[1]));
+                dy[j] = mul2(dy[j], mul2(z, sigmoid2(z)));
+            }
+        }
+        const int64_t at = blk.t0 + t;
+        const bool inside = at > sq.begin && at + tl < sq.end && tl == TK;
+#pragma unroll
+        for (int j = TK - 1; j >= 0; --j) {
+            bool start = false;
+            if (!inside) {
+                if (j >= tl) continue;
+                while (packed && sq.q > 0 && at + j < sq.begin) {
+                    sq.q -= 1;
+                    sq.end = sq.begin;
+                    sq.begin = a.d.offsets[sq.q];
+                }
+                start = at + j == sq.begin;
+                if (at + j + 1 == sq.end) {
+#pragma unroll
+                    for (int k = 0; k < 2; ++k)
+                        load_states<SPT>(live[k] && a.g.dfinal_state
+                                             ? a.g.dfinal_state + (sq.q * a.d.channels + c + k) * n
+                                             : nullptr, 0, n, m[k]);
+                }
+            }
+            const float2 dd[2] = {splat(d[j].x), splat(d[j].y)};
+            const float2 yy[2] = {splat(dy[j].x), splat(dy[j].y)};
+#pragma unroll
+            for (int i = 0; i < SPT / 4; ++i) {
+                const float4 c4 = *reinterpret_cast<const float4*>(sC + j * SPT + 4 * i);
+#pragma unroll
+                for (int p = 0; p < 2; ++p)
+#pragma unroll
+                    for (int k = 0; k < 2; ++k) {
+                        float2& mm = m[k][2 * i + p];
+                        const float2 e = mul2(dd[k], A2[k][2 * i + p]);
+                        const float2 q = fma2(yy[k], p ? make_float2(c4.z, c4.w) : make_float2(c4.x, c4.y), mm);
+                        mm = mul2(make_float2(ex2(e.x), ex2(e.y)), q);
+                    }
+            }
+            if (start) {
+#pragma unroll
+                for (int k = 0; k < 2; ++k) load_states<SPT>(nullptr, 0, n, m[k]);
+            }
+        }
+        stage = stage + 1 < ST ? stage + 1 : 0;
+        buf ^= 1;
+    }
+    copy_wait<0>();
+#pragma unroll
+    for (int k = 0; k < 2; ++k)
+        if (live[k])
+            store_row<SPT>(a.carry + ((blk.row * a.f.nchunks + blk.chunk) * a.d.channels + c + k) * SPT, m[k]);
+}
+
+// More states: several lanes per channel, 16 states each.
 template <class T, int SPT, int SL>
 __global__ void __launch_bounds__(kScanThreads) k_scan_back(const ScanBwdArgs a) {
     constexpr int NP = SPT * SL, CT = kScanThreads / SL, TK = 8, OWN = TK / SL;
@@ -167,7 +330,8 @@ struct BwdShape {
     static constexpr int kBytes = kFloats * 4 + 4 * kRaw * (int)sizeof(T) + TK * 8 + 16;
 };
 
-template <class T, int SL>
+// EXACT (n == 4 * SL) drops the selects that keep states beyond n at 0 where u is infinite.
+template <class T, int SL, bool EXACT>
 __global__ void __launch_bounds__(BwdShape<T, SL>::NT) k_scan_bwd(const ScanBwdArgs a) {
     using S = BwdShape<T, SL>;
     constexpr int NT = S::NT, CL = S::CL, CT = S::CT, NP = S::NP, TK = S::TK, TS = S::TS;
@@ -403,165 +567,173 @@ __global__ void __launch_bounds__(BwdShape<T, SL>::NT) k_scan_bwd(const ScanBwdA
                     for (int p = 0; p < 2; ++p) {
                         const float2 e = mul2(dd[p], A2[s + k][p]);
                         h[s + k][p] = fma2(make_float2(ex2(e.x), ex2(e.y)), h[s + k][p], mul2(du2[p], b));
-                        if (s0 + s + k >= n) h[s + k][p] = splat(0.f);
+                        if (!EXACT && s0 + s + k >= n) h[s + k][p] = splat(0.f);
                     }
                 }
             }
         };
-        const int last = (len - 1) / TS;
-        for (int piece = 0; piece < last; ++piece) {
+        // a tile inside one sequence, and whole, takes code without questions
+        auto walk = [&](auto plain) {
+            constexpr bool PLAIN = decltype(plain)::value != 0;
+            const int last = PLAIN ? S::PIECES - 1 : (len - 1) / TS;
+            for (int piece = 0; piece < last; ++piece) {
 #pragma unroll
-            for (int j = 0; j < TS; ++j) {
-                if (starts >> (piece * TS + j) & 1) initial(piece * TS + j, h);
-                step(piece * TS + j);
-            }
-            put(piece + 1, h);
-        }
-        for (int piece = last; piece >= 0; --piece) {
-            float2 hist[TS + 1][4][2];  // the states before the piece and after its tokens
-            if (piece < last) {
-                if (piece > 0)
-                    get(piece, h);
-                else
-                    load_padded(start_states, h);
-            }
-#pragma unroll
-            for (int j = 0; j <= TS; ++j) {
-#pragma unroll
-                for (int s = 0; s < 4; ++s)
-#pragma unroll
-                    for (int p = 0; p < 2; ++p) hist[j][s][p] = h[s][p];
-                if (j < TS && piece * TS + j < len) {
-                    if (starts >> (piece * TS + j) & 1) initial(piece * TS + j, h);
+                for (int j = 0; j < TS; ++j) {
+                    if (!PLAIN && starts >> (piece * TS + j) & 1) initial(piece * TS + j, h);
                     step(piece * TS + j);
                 }
+                put(piece + 1, h);
             }
-#pragma unroll
-            for (int jj = TS - 1; jj >= 0; --jj) {
-                const int j = piece * TS + jj;
-                if (j >= len) continue;
-                if (ends >> j & 1)
-                    load4(a.g.dfinal_state ? a.g.dfinal_state + sq_id[j] * a.d.channels * n : nullptr,
-                          n, m);
-                // before a sequence's first token stands its initial state; what stands there is
-                // also the state after the token before, kept in a place that is free by now
-                if (starts >> j & 1) {
-                    put(piece ? piece : 1, hist[jj]);
-                    initial(j, hist[jj]);
+            for (int piece = last; piece >= 0; --piece) {
+                float2 hist[TS + 1][4][2];  // the states before the piece and after its tokens
+                if (piece < last) {
+                    if (piece > 0)
+                        get(piece, h);
+                    else
+                        load_padded(start_states, h);
                 }
-                const float4 d4 = *reinterpret_cast<const float4*>(sd + j * CT + lc);
-                const float4 u4 = *reinterpret_cast<const float4*>(su + j * CT + lc);
-                const float4 y4 = *reinterpret_cast<const float4*>(sy + j * CT + lc);
-                const float2 dd[2] = {make_float2(d4.x, d4.y), make_float2(d4.z, d4.w)};
-                const float2 dy[2] = {make_float2(y4.x, y4.y), make_float2(y4.z, y4.w)};
-                const float2 du2[2] = {mul2(dd[0], make_float2(u4.x, u4.y)),
-                                       mul2(dd[1], make_float2(u4.z, u4.w))};
-                float2 yv[2] = {}, qb[2] = {}, qa[2] = {};
-                float bc[8];
 #pragma unroll
-                for (int s = 0; s < 4; ++s) {
-                    const float2 b = *reinterpret_cast<const float2*>(sB + (j * NP + s0 + s) * 2);
-                    const float2 c = *reinterpret_cast<const float2*>(sC + (j * NP + s0 + s) * 2);
-                    float2 db, dc;
-#pragma unroll
-                    for (int p = 0; p < 2; ++p) {
-                        const float2 e = mul2(dd[p], A2[s][p]);
-                        const float2 q = fma2(dy[p], c, m[s][p]);
-                        const float2 aq = mul2(make_float2(ex2(e.x), ex2(e.y)), q);
-                        const float2 w = mul2(aq, hist[jj][s][p]);
-                        yv[p] = fma2(c, hist[jj + 1][s][p], yv[p]);
-                        qb[p] = fma2(q, b, qb[p]);
-                        qa[p] = fma2(w, A2[s][p], qa[p]);
-                        dA[s][p] = fma2(w, dd[p], dA[s][p]);
-                        db = p ? fma2(q, du2[p], db) : mul2(q, du2[p]);
-                        dc = p ? fma2(dy[p], hist[jj + 1][s][p], dc) : mul2(dy[p], hist[jj + 1][s][p]);
-                        m[s][p] = aq;
-                    }
-                    bc[s] = db.x + db.y;
-                    bc[4 + s] = dc.x + dc.y;
-                }
-                if (starts >> j & 1) {  // the sequence's first token
-                    if (a.g.dinitial_state) {
-#pragma unroll
-                        for (int i = 0; i < 4; ++i)
-#pragma unroll
-                            for (int s = 0; s < 4; ++s)
-                                if (lc + i < width && s0 + s < n)
-                                    a.g.dinitial_state[(sq_id[j] * a.d.channels + c0 + lc + i) * n + s0 + s] =
-                                        i & 1 ? m[s][i / 2].y : m[s][i / 2].x;
-                    }
+                for (int j = 0; j <= TS; ++j) {
 #pragma unroll
                     for (int s = 0; s < 4; ++s)
 #pragma unroll
-                        for (int p = 0; p < 2; ++p) m[s][p] = splat(0.f);
-                    get(piece ? piece : 1, hist[jj]);
-                }
-                // sums over states, handed out to the lanes of a channel group
-                float vy[4] = {yv[0].x, yv[0].y, yv[1].x, yv[1].y};
-                float vb[4] = {qb[0].x, qb[0].y, qb[1].x, qb[1].y};
-                float va[4] = {qa[0].x, qa[0].y, qa[1].x, qa[1].y};
-                if constexpr (SL >= 4) {
-                    hand_out<4, 2, 1>(vy, sl);
-                    hand_out<4, 2, 1>(vb, sl);
-                    hand_out<4, 2, 1>(va, sl);
-#pragma unroll
-                    for (int w = 4; w < SL; w *= 2) {
-                        vy[0] += __shfl_xor_sync(0xffffffffu, vy[0], w);
-                        vb[0] += __shfl_xor_sync(0xffffffffu, vb[0], w);
-                        va[0] += __shfl_xor_sync(0xffffffffu, va[0], w);
-                    }
-                } else if constexpr (SL == 2) {
-                    hand_out<4, 1, 1>(vy, sl);
-                    hand_out<4, 1, 1>(vb, sl);
-                    hand_out<4, 1, 1>(va, sl);
-                }
-#pragma unroll
-                for (int k = 0; k < OWN; ++k) {
-                    const int e = j * CT + lo + k;
-                    const float d = sd[e], uu = su[e], dyk = sy[e];
-                    const float dv = fmaf(d, vb[k], dyk * oD[k]);
-                    const float de = fmaf(uu, vb[k], va[k] * kLn2) * sg[e];  // A = A2 ln 2
-                    abias[k] += de;
-                    aD[k] = fmaf(dyk, uu, aD[k]);
-                    if (owner && lo + k < width) {
-                        pdu[(int64_t)j * sdu + k] = from_f<T>(dv);
-                        pdd[(int64_t)j * sdd + k] = from_f<T>(de);
-                        if (gate) pdz[(int64_t)j * sdz + k] = from_f<T>(sf[e] * fmaf(oD[k], uu, vy[k]));
-                    }
-                }
-                // sums over channels: one step between lanes, the rest through shared memory
-                if constexpr (CL > 1) {
-                    const bool up = cl & (CL / 2);
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        const float send = up ? bc[k] : bc[k + 4], keep = up ? bc[k + 4] : bc[k];
-                        bc[k] = keep + __shfl_xor_sync(0xffffffffu, send, CL / 2 * SL);
+                        for (int p = 0; p < 2; ++p) hist[j][s][p] = h[s][p];
+                    if (j < TS && (PLAIN || piece * TS + j < len)) {
+                        if (!PLAIN && starts >> (piece * TS + j) & 1) initial(piece * TS + j, h);
+                        step(piece * TS + j);
                     }
                 }
 #pragma unroll
-                for (int k = 0; k < KV; ++k) red[((jj * S::NW + warp) * KV + k) * RS + lane] = bc[k];
+                for (int jj = TS - 1; jj >= 0; --jj) {
+                    const int j = piece * TS + jj;
+                    if (!PLAIN && j >= len) continue;
+                    if (!PLAIN && ends >> j & 1)
+                        load4(a.g.dfinal_state ? a.g.dfinal_state + sq_id[j] * a.d.channels * n : nullptr,
+                              n, m);
+                    // before a sequence's first token stands its initial state; what stands there is
+                    // also the state after the token before, kept in a place that is free by now
+                    if (!PLAIN && starts >> j & 1) {
+                        put(piece ? piece : 1, hist[jj]);
+                        initial(j, hist[jj]);
+                    }
+                    const float4 d4 = *reinterpret_cast<const float4*>(sd + j * CT + lc);
+                    const float4 u4 = *reinterpret_cast<const float4*>(su + j * CT + lc);
+                    const float4 y4 = *reinterpret_cast<const float4*>(sy + j * CT + lc);
+                    const float2 dd[2] = {make_float2(d4.x, d4.y), make_float2(d4.z, d4.w)};
+                    const float2 dy[2] = {make_float2(y4.x, y4.y), make_float2(y4.z, y4.w)};
+                    const float2 du2[2] = {mul2(dd[0], make_float2(u4.x, u4.y)),
+                                           mul2(dd[1], make_float2(u4.z, u4.w))};
+                    float2 yv[2] = {}, qb[2] = {}, qa[2] = {};
+                    float bc[8];
+#pragma unroll
+                    for (int s = 0; s < 4; ++s) {
+                        const float2 b = *reinterpret_cast<const float2*>(sB + (j * NP + s0 + s) * 2);
+                        const float2 c = *reinterpret_cast<const float2*>(sC + (j * NP + s0 + s) * 2);
+                        float2 db, dc;
+#pragma unroll
+                        for (int p = 0; p < 2; ++p) {
+                            const float2 e = mul2(dd[p], A2[s][p]);
+                            const float2 q = fma2(dy[p], c, m[s][p]);
+                            const float2 aq = mul2(make_float2(ex2(e.x), ex2(e.y)), q);
+                            const float2 w = mul2(aq, hist[jj][s][p]);
+                            yv[p] = fma2(c, hist[jj + 1][s][p], yv[p]);
+                            qb[p] = fma2(q, b, qb[p]);
+                            qa[p] = fma2(w, A2[s][p], qa[p]);
+                            dA[s][p] = fma2(w, dd[p], dA[s][p]);
+                            db = p ? fma2(q, du2[p], db) : mul2(q, du2[p]);
+                            dc = p ? fma2(dy[p], hist[jj + 1][s][p], dc) : mul2(dy[p], hist[jj + 1][s][p]);
+                            m[s][p] = aq;
+                        }
+                        bc[s] = db.x + db.y;
+                        bc[4 + s] = dc.x + dc.y;
+                    }
+                    if (!PLAIN && starts >> j & 1) {  // the sequence's first token
+                        if (a.g.dinitial_state) {
+#pragma unroll
+                            for (int i = 0; i < 4; ++i)
+#pragma unroll
+                                for (int s = 0; s < 4; ++s)
+                                    if (lc + i < width && s0 + s < n)
+                                        a.g.dinitial_state[(sq_id[j] * a.d.channels + c0 + lc + i) * n + s0 + s] =
+                                            i & 1 ? m[s][i / 2].y : m[s][i / 2].x;
+                        }
+#pragma unroll
+                        for (int s = 0; s < 4; ++s)
+#pragma unroll
+                            for (int p = 0; p < 2; ++p) m[s][p] = splat(0.f);
+                        get(piece ? piece : 1, hist[jj]);
+                    }
+                    // sums over states, handed out to the lanes of a channel group
+                    float vy[4] = {yv[0].x, yv[0].y, yv[1].x, yv[1].y};
+                    float vb[4] = {qb[0].x, qb[0].y, qb[1].x, qb[1].y};
+                    float va[4] = {qa[0].x, qa[0].y, qa[1].x, qa[1].y};
+                    if constexpr (SL >= 4) {
+                        hand_out<4, 2, 1>(vy, sl);
+                        hand_out<4, 2, 1>(vb, sl);
+                        hand_out<4, 2, 1>(va, sl);
+#pragma unroll
+                        for (int w = 4; w < SL; w *= 2) {
+                            vy[0] += __shfl_xor_sync(0xffffffffu, vy[0], w);
+                            vb[0] += __shfl_xor_sync(0xffffffffu, vb[0], w);
+                            va[0] += __shfl_xor_sync(0xffffffffu, va[0], w);
+                        }
+                    } else if constexpr (SL == 2) {
+                        hand_out<4, 1, 1>(vy, sl);
+                        hand_out<4, 1, 1>(vb, sl);
+                        hand_out<4, 1, 1>(va, sl);
+                    }
+#pragma unroll
+                    for (int k = 0; k < OWN; ++k) {
+                        const int e = j * CT + lo + k;
+                        const float d = sd[e], uu = su[e], dyk = sy[e];
+                        const float dv = fmaf(d, vb[k], dyk * oD[k]);
+                        const float de = fmaf(uu, vb[k], va[k] * kLn2) * sg[e];  // A = A2 ln 2
+                        abias[k] += de;
+                        aD[k] = fmaf(dyk, uu, aD[k]);
+                        if (owner && lo + k < width) {
+                            pdu[(int64_t)j * sdu + k] = from_f<T>(dv);
+                            pdd[(int64_t)j * sdd + k] = from_f<T>(de);
+                            if (gate) pdz[(int64_t)j * sdz + k] = from_f<T>(sf[e] * fmaf(oD[k], uu, vy[k]));
+                        }
+                    }
+                    // sums over channels: one step between lanes, the rest through shared memory
+                    if constexpr (CL > 1) {
+                        const bool up = cl & (CL / 2);
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            const float send = up ? bc[k] : bc[k + 4], keep = up ? bc[k + 4] : bc[k];
+                            bc[k] = keep + __shfl_xor_sync(0xffffffffu, send, CL / 2 * SL);
+                        }
+                    }
+#pragma unroll
+                    for (int k = 0; k < KV; ++k) red[((jj * S::NW + warp) * KV + k) * RS + lane] = bc[k];
+                }
+                __syncthreads();
+                // the piece's dB and dC: value v (dB of 4 states, dC of 4 states) of state lane i
+                const int plen = PLAIN || len - piece * TS > TS ? TS : len - piece * TS;
+                for (int o = tid; o < plen * 8 * SL; o += NT) {
+                    const int jj = o / (8 * SL), v = o / SL % 8, i = o % SL, state = i * 4 + (v & 3);
+                    constexpr int LANES = CL > 1 ? CL / 2 : 1;
+                    const float* p = red + (jj * S::NW * KV + (CL > 1 ? v & 3 : v)) * RS + i +
+                                     (CL > 1 ? (v >> 2) * (CL / 2) * SL : 0);
+                    float x = 0.f;
+#pragma unroll
+                    for (int w = 0; w < S::NW; ++w)
+#pragma unroll
+                        for (int k = 0; k < LANES; ++k) x += p[w * KV * RS + k * SL];
+                    if (state < n) {
+                        const int64_t t = tl + piece * TS + jj;
+                        a.bc[((((ct * a.f.rows + row) * a.d.length + t) * a.d.groups + g) * 2 + (v >> 2)) * n +
+                             state] = x;
+                    }
+                }
+                if (piece) __syncthreads();  // the next piece writes the same places
             }
-            __syncthreads();
-            // the piece's dB and dC: value v (dB of 4 states, dC of 4 states) of state lane i
-            const int plen = len - piece * TS < TS ? len - piece * TS : TS;
-            for (int o = tid; o < plen * 8 * SL; o += NT) {
-                const int jj = o / (8 * SL), v = o / SL % 8, i = o % SL, state = i * 4 + (v & 3);
-                constexpr int LANES = CL > 1 ? CL / 2 : 1;
-                const float* p = red + (jj * S::NW * KV + (CL > 1 ? v & 3 : v)) * RS + i +
-                                 (CL > 1 ? (v >> 2) * (CL / 2) * SL : 0);
-                float x = 0.f;
-#pragma unroll
-                for (int w = 0; w < S::NW; ++w)
-#pragma unroll
-                    for (int k = 0; k < LANES; ++k) x += p[w * KV * RS + k * SL];
-                if (state < n) {
-                    const int64_t t = tl + piece * TS + jj;
-                    a.bc[((((ct * a.f.rows + row) * a.d.length + t) * a.d.groups + g) * 2 + (v >> 2)) * n +
-                         state] = x;
-                }
-            }
-            if (piece) __syncthreads();  // the next piece writes the same places
-        }
+        };
+        if (len == TK && !(starts | ends))
+            walk(Count<1>{});
+        else
+            walk(Count<0>{});
     }
     copy_wait<0>();
     const int64_t part = row * a.f.nchunks + chunk;
@@ -609,29 +781,50 @@ __global__ void __launch_bounds__(256) k_scan_back_empty(const ScanBwdArgs a) {
         a.g.dinitial_state[q * per + i] = a.g.dfinal_state ? a.g.dfinal_state[q * per + i] : 0.f;
 }
 
-template <class T, int SL>
-cudaError_t scan_bwd_main(const ScanBwdArgs& a, cudaStream_t s) {
+template <class T, int SL, bool EXACT>
+cudaError_t scan_bwd_launch(const ScanBwdArgs& a, cudaStream_t s) {
     using S = BwdShape<T, SL>;
     static LaunchCache cache;
     LaunchGeom geo;
     cudaError_t e = cache.get([](int dev, LaunchGeom* g) {
-        return setup_persistent(k_scan_bwd<T, SL>, S::NT, S::kBytes, dev, g);
+        return setup_persistent(k_scan_bwd<T, SL, EXACT>, S::NT, S::kBytes, dev, g);
     }, &geo);
     if (e != cudaSuccess) return e;
     const int64_t blocks = a.f.rows * a.f.nchunks * a.ctiles * a.d.groups;
     if (blocks > INT32_MAX) return cudaErrorInvalidValue;
-    k_scan_bwd<T, SL><<<(unsigned)blocks, S::NT, S::kBytes, s>>>(a);
+    k_scan_bwd<T, SL, EXACT><<<(unsigned)blocks, S::NT, S::kBytes, s>>>(a);
     return cudaGetLastError();
+}
+template <class T, int SL>
+cudaError_t scan_bwd_main(const ScanBwdArgs& a, cudaStream_t s) {
+    return a.d.states == 4 * SL ? scan_bwd_launch<T, SL, true>(a, s)
+                                : scan_bwd_launch<T, SL, false>(a, s);
+}
+template <int NP>
+cudaError_t scan_bwd_carry(const ScanBwdArgs& a, cudaStream_t s) {
+    k_scan_back_carry<NP>
+        <<<(unsigned)((a.f.rows * a.d.channels * NP + kCarryThreads - 1) / kCarryThreads),
+           kCarryThreads, 0, s>>>(a);
+    return cudaGetLastError();
+}
+template <class T, int SPT>
+cudaError_t scan_bwd_back_pair(const ScanBwdArgs& a, cudaStream_t s) {
+    constexpr int bytes = 3 * 3 * kPairTile * kPairChannels * (int)sizeof(T) + 2 * kPairTile * SPT * 4;
+    static LaunchCache cache;
+    LaunchGeom geo;
+    const cudaError_t e = cache.get([](int dev, LaunchGeom* g) {
+        return setup_persistent(k_scan_back_pair<T, SPT>, kPairThreads, bytes, dev, g);
+    }, &geo);
+    if (e != cudaSuccess) return e;
+    k_scan_back_pair<T, SPT><<<(unsigned)(a.f.rows * (a.f.nchunks - 1) * a.f.ctiles * a.d.groups),
+                               kPairThreads, bytes, s>>>(a);
+    return scan_bwd_carry<SPT>(a, s);
 }
 template <class T, int SPT, int SL>
 cudaError_t scan_bwd_back(const ScanBwdArgs& a, cudaStream_t s) {
-    const int64_t tiles = a.back_ctiles * a.d.groups;
-    k_scan_back<T, SPT, SL>
-        <<<(unsigned)(a.f.rows * (a.f.nchunks - 1) * tiles), kScanThreads, 0, s>>>(a);
-    k_scan_back_carry<SPT * SL>
-        <<<(unsigned)((a.f.rows * a.d.channels * SPT * SL + kCarryThreads - 1) / kCarryThreads),
-           kCarryThreads, 0, s>>>(a);
-    return cudaGetLastError();
+    k_scan_back<T, SPT, SL><<<(unsigned)(a.f.rows * (a.f.nchunks - 1) * a.back_ctiles * a.d.groups),
+                              kScanThreads, 0, s>>>(a);
+    return scan_bwd_carry<SPT * SL>(a, s);
 }
 
 template <class T>
@@ -649,9 +842,9 @@ cudaError_t scan_bwd_run(ScanBwdArgs a, cudaStream_t s) {
         e = scan_run<T, SCAN_TILES>(a.f, s);
         if (e == cudaSuccess && a.f.nchunks > 1) {
             switch (scan_np(n)) {
-                case 4: e = scan_bwd_back<T, 4, 1>(a, s); break;
-                case 8: e = scan_bwd_back<T, 8, 1>(a, s); break;
-                case 16: e = scan_bwd_back<T, 16, 1>(a, s); break;
+                case 4: e = scan_bwd_back_pair<T, 4>(a, s); break;
+                case 8: e = scan_bwd_back_pair<T, 8>(a, s); break;
+                case 16: e = scan_bwd_back_pair<T, 16>(a, s); break;
                 case 32: e = scan_bwd_back<T, 16, 2>(a, s); break;
                 case 64: e = scan_bwd_back<T, 16, 4>(a, s); break;
                 default: e = scan_bwd_back<T, 16, 8>(a, s); break;
