@@ -81,6 +81,108 @@ __device__ __forceinline__ void store_row(float* p, const float2 (&h)[SPT / 2]) 
             make_float4(h[2 * i].x, h[2 * i].y, h[2 * i + 1].x, h[2 * i + 1].y);
 }
 
+// Tokens t .. t + TK - 1 of a tensor (p: token 0, the block's first channel) into dst[token][CT],
+// zeros beyond `len` tokens and `width` channels.  align: bytes that every row starts on, 16 (the
+// only case of FAST kernels) or 4; smaller: single values, and then not asynchronously.
+template <class T, int TK, int CT, int NT, bool FAST>
+__device__ __forceinline__ void copy_tile(T* dst, const T* p, int64_t stride, int t, int len,
+                                          int width, int align) {
+    const int tid = (int)threadIdx.x;
+    if (FAST || align >= 16) {
+        constexpr int V = 16 / sizeof(T), R = CT / V;  // accesses of a row
+        if constexpr (NT % R == 0 && TK % (NT / R) == 0) {
+            constexpr int STEP = NT / R;
+            const int j0 = tid / R, x = (tid - j0 * R) * V;
+            const T* q = p + (t + j0) * stride + x;
+#pragma unroll
+            for (int j = 0; j < TK; j += STEP, q += STEP * stride) {
+                const bool in = t + j0 + j < len && x < width;
+                copy16(dst + (j0 + j) * CT + x, in ? q : p, in);
+            }
+        } else {
+#pragma unroll
+            for (int e = tid; e < TK * R; e += NT) {
+                const int j = e / R, x = (e - j * R) * V;
+                const bool in = t + j < len && x < width;
+                copy16(dst + j * CT + x, in ? p + (t + j) * stride + x : p, in);
+            }
+        }
+    } else if (align >= 4) {
+        constexpr int V = 4 / sizeof(T), R = CT / V;
+#pragma unroll 4
+        for (int e = tid; e < TK * R; e += NT) {
+            const int j = e / R, x = (e - j * R) * V;
+            const bool in = t + j < len && x < width;
+            copy4(dst + j * CT + x, in ? p + (t + j) * stride + x : p, in);
+        }
+    } else {
+#pragma unroll 8
+        for (int e = tid; e < TK * CT; e += NT) {
+            const int j = e / CT, x = e - j * CT;
+            dst[e] = t + j < len && x < width ? p[(t + j) * stride + x] : from_f<T>(0.f);
+        }
+    }
+}
+
+// B (and C) of a tile, from global memory through registers to float32 [token][NP] in shared
+// memory.  FAST: the n == NP values of a token are whole 16-byte accesses.
+template <class T, int TK, int NP, int NT, bool BOTH, bool FAST>
+struct RowsAhead {
+    static constexpr int V = 16 / sizeof(T);
+    static constexpr int WIDE = FAST ? (TK * NP / V + NT - 1) / NT : 0;  // accesses per thread
+    static constexpr int ONE = (TK * NP + NT - 1) / NT;
+    uint4 wide[BOTH ? 2 : 1][FAST ? WIDE : 1];
+    T one[BOTH ? 2 : 1][FAST ? 1 : ONE];
+    __device__ __forceinline__ void fetch(const T* b, int64_t bs, const T* c, int64_t cs, int t,
+                                          int len, int n) {
+        const int tid = (int)threadIdx.x;
+        if constexpr (FAST) {
+#pragma unroll
+            for (int i = 0; i < WIDE; ++i) {
+                const int e = tid + i * NT, j = e / (NP / V), s = (e - j * (NP / V)) * V;
+                const bool in = j < TK && t >= 0 && t + j < len;
+                wide[0][i] = in ? *reinterpret_cast<const uint4*>(b + (t + j) * bs + s) : uint4{};
+                if (BOTH)
+                    wide[BOTH][i] = in ? *reinterpret_cast<const uint4*>(c + (t + j) * cs + s) : uint4{};
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < ONE; ++i) {
+                const int e = tid + i * NT, j = e / NP, s = e - j * NP;
+                const bool in = j < TK && s < n && t >= 0 && t + j < len;
+                one[0][i] = in ? b[(t + j) * bs + s] : from_f<T>(0.f);
+                if (BOTH) one[BOTH][i] = in ? c[(t + j) * cs + s] : from_f<T>(0.f);
+            }
+        }
+    }
+    __device__ __forceinline__ void stage(float* sb) {
+        const int tid = (int)threadIdx.x;
+#pragma unroll
+        for (int k = 0; k < (BOTH ? 2 : 1); ++k) {
+            float* dst = sb + k * TK * NP;
+            if constexpr (FAST) {
+#pragma unroll
+                for (int i = 0; i < WIDE; ++i) {
+                    const int e = tid + i * NT;
+                    if (e * V < TK * NP) {
+                        const Pack<T, V> p = *reinterpret_cast<const Pack<T, V>*>(&wide[k][i]);
+#pragma unroll
+                        for (int v = 0; v < V; v += 4)
+                            *reinterpret_cast<float4*>(dst + e * V + v) = make_float4(
+                                to_f(p.v[v]), to_f(p.v[v + 1]), to_f(p.v[v + 2]), to_f(p.v[v + 3]));
+                    }
+                }
+            } else {
+#pragma unroll
+                for (int i = 0; i < ONE; ++i) {
+                    const int e = tid + i * NT;
+                    if (TK * NP % NT == 0 || e < TK * NP) dst[e] = to_f(one[k][i]);
+                }
+            }
+        }
+    }
+};
+
 // The blocks behind the outputs: a sequence without tokens ends in its initial state.
 __device__ __forceinline__ void scan_empty(const ScanArgs& a, int64_t q) {
     const int64_t per = a.d.channels * a.d.states;
@@ -108,14 +210,14 @@ struct ScanPairSmem {
 // Up to 16 states: a thread holds all SPT states of two neighbouring channels.  Tiles of 8
 // tokens: u, delta and z come by asynchronous copies two tiles ahead, B and C a tile ahead
 // through registers, double buffered in shared memory as float32: one barrier per tile.
-// A state beyond n has A = B = C = 0; EXACT (n == SPT) drops the selects that keep such states at
-// 0 where u is infinite.
-template <class T, int SPT, int PASS, bool EXACT>
+// A pair of states beyond n is left out, and the odd one of a last pair kept at 0 (its B is 0, but
+// u may be infinite).  FAST: n == SPT and all rows are whole 16-byte accesses, the usual case,
+// whose code is free of these questions.
+template <class T, int SPT, int PASS, bool FAST>
 __global__ void __launch_bounds__(kPairThreads) k_scan(const ScanArgs a) {
     using M = ScanPairSmem<T, SPT, PASS>;
     constexpr int NT = kPairThreads, CT = kPairChannels, TK = kPairTile, ST = M::kStages;
     constexpr bool SUMMARY = PASS == SCAN_SUMMARY, OUTPUT = PASS == SCAN_OUTPUT;
-    constexpr int BCN = (TK * SPT + NT - 1) / NT;  // B values per thread and tile
     extern __shared__ float4 smem4[];
     T* raw = reinterpret_cast<T*>(smem4);  // [stage][tensor][token][channel]
     float* sbc = reinterpret_cast<float*>(reinterpret_cast<char*>(smem4) + M::kBytesRaw);
@@ -140,62 +242,20 @@ __global__ void __launch_bounds__(kPairThreads) k_scan(const ScanArgs a) {
     const T* Bp = row_of<T>(a.d.B, packed, blk.row) + blk.t0 * a.d.B.tok_stride + blk.g * n;
     const T* Cp = row_of<T>(a.d.C, packed, blk.row) + blk.t0 * a.d.C.tok_stride + blk.g * n;
 
-    auto copy = [&](int t, int stage) {  // the tile at t; zeros beyond the chunk
+    auto copy = [&](int t, int stage) {  // the tile at t
 #pragma unroll
         for (int k = 0; k < M::kTensors; ++k) {
             if (k == 2 && !gate) break;
-            T* dst = raw + (stage * M::kTensors + k) * M::kRaw;
-            if (a.vec) {
-                constexpr int V = 16 / sizeof(T), R = CT / V, STEP = NT / R;
-                const int j0 = tid / R, x = (tid - j0 * R) * V;
-                const T* p = src[k] + (t + j0) * str[k] + x;
-#pragma unroll
-                for (int j = 0; j < TK; j += STEP, p += STEP * str[k]) {
-                    const bool in = t + j0 + j < len && x < width;
-                    copy16(dst + (j0 + j) * CT + x, in ? p : src[k], in);
-                }
-            } else {
-#pragma unroll 1
-                for (int j = 0; j < TK; j += 4) {
-                    T v[4][2];
-#pragma unroll
-                    for (int i = 0; i < 4; ++i)
-#pragma unroll
-                        for (int e = 0; e < 2; ++e) {
-                            const int x = tid + e * NT;
-                            v[i][e] = t + j + i < len && x < width ? src[k][(t + j + i) * str[k] + x]
-                                                                   : from_f<T>(0.f);
-                        }
-#pragma unroll
-                    for (int i = 0; i < 4; ++i)
-#pragma unroll
-                        for (int e = 0; e < 2; ++e) dst[(j + i) * CT + tid + e * NT] = v[i][e];
-                }
-            }
+            copy_tile<T, TK, CT, NT, FAST>(raw + (stage * M::kTensors + k) * M::kRaw, src[k], str[k], t, len,
+                                     width, a.vec);
         }
         copy_commit();
     };
-    T pB[BCN], pC[OUTPUT ? BCN : 1];
-    auto fetch = [&](int t) {  // B and C of the tile at t
-#pragma unroll
-        for (int i = 0; i < BCN; ++i) {
-            const int e = tid + i * NT, j = e / SPT, s = e - j * SPT;
-            const bool in = (TK * SPT % NT == 0 || e < TK * SPT) && s < n && t + j < len;
-            pB[i] = in ? Bp[(t + j) * a.d.B.tok_stride + s] : from_f<T>(0.f);
-            if (OUTPUT) pC[i] = in ? Cp[(t + j) * a.d.C.tok_stride + s] : from_f<T>(0.f);
-        }
+    RowsAhead<T, TK, SPT, NT, OUTPUT, FAST> bc;
+    auto fetch = [&](int t) {
+        bc.fetch(Bp, a.d.B.tok_stride, Cp, a.d.C.tok_stride, t, len, n);
     };
-    auto stage_bc = [&](int buf) {
-        float* sB = sbc + buf * M::kBC;
-#pragma unroll
-        for (int i = 0; i < BCN; ++i) {
-            const int e = tid + i * NT;
-            if (TK * SPT % NT == 0 || e < TK * SPT) {
-                sB[e] = to_f(pB[i]);
-                if (OUTPUT) sB[TK * SPT + e] = to_f(pC[i]);
-            }
-        }
-    };
+    auto stage_bc = [&](int buf) { bc.stage(sbc + buf * M::kBC); };
 #pragma unroll
     for (int i = 0; i < ST - 1; ++i) copy(i * TK, i);
     fetch(0);
@@ -291,13 +351,11 @@ __global__ void __launch_bounds__(kPairThreads) k_scan(const ScanArgs a) {
                         const float2 b = p ? make_float2(b4.z, b4.w) : make_float2(b4.x, b4.y);
 #pragma unroll
                         for (int k = 0; k < 2; ++k) {
+                            if (!FAST && 4 * i + 2 * p >= n) continue;
                             float2& hh = h[k][2 * i + p];
                             const float2 e = mul2(dd[k], A2[k][2 * i + p]);
                             hh = fma2(make_float2(ex2(e.x), ex2(e.y)), hh, mul2(dv[k], b));
-                            if (!EXACT) {
-                                if (4 * i + 2 * p >= n) hh.x = 0.f;
-                                if (4 * i + 2 * p + 1 >= n) hh.y = 0.f;
-                            }
+                            if (!FAST && 4 * i + 2 * p + 1 >= n) hh.y = 0.f;
                             if (OUTPUT)
                                 acc[k][p] = fma2(p ? make_float2(c4.z, c4.w) : make_float2(c4.x, c4.y),
                                                  hh, acc[k][p]);
@@ -390,13 +448,12 @@ struct ScanLanesSmem {
 // GPU without cutting time when each has more threads.  Tiles of 16 tokens in two batches of 8.
 // In a batch each lane prepares and finishes its own 8 / SL tokens (softplus, gate, store); d and
 // d u are broadcast from the token's lane, and the partial sums over states handed back to it.
-template <class T, int SPT, int SL, int PASS, bool EXACT>
+template <class T, int SPT, int SL, int PASS, bool FAST>
 __global__ void __launch_bounds__(kLanesThreads) k_scan_lanes(const ScanArgs a) {
     using M = ScanLanesSmem<T, SPT, SL, PASS>;
     constexpr int NT = kLanesThreads, CT = M::CT, CL = 32 / SL, NP = M::NP, TK = kLanesTile;
     constexpr int ST = M::kStages, N = kLanesBatch, OWN = N / SL;
     constexpr bool SUMMARY = PASS == SCAN_SUMMARY, OUTPUT = PASS == SCAN_OUTPUT;
-    constexpr int BCN = TK * NP / NT;  // B values per thread and tile
     extern __shared__ float4 smem4[];
     T* raw = reinterpret_cast<T*>(smem4);  // [stage][tensor][token][channel]
     float* sbc = reinterpret_cast<float*>(reinterpret_cast<char*>(smem4) + M::kBytesRaw);
@@ -422,51 +479,20 @@ __global__ void __launch_bounds__(kLanesThreads) k_scan_lanes(const ScanArgs a) 
     const T* Bp = row_of<T>(a.d.B, packed, blk.row) + blk.t0 * a.d.B.tok_stride + blk.g * n;
     const T* Cp = row_of<T>(a.d.C, packed, blk.row) + blk.t0 * a.d.C.tok_stride + blk.g * n;
 
-    auto copy = [&](int t, int stage) {  // the tile at t; zeros beyond the chunk
+    auto copy = [&](int t, int stage) {  // the tile at t
 #pragma unroll
         for (int k = 0; k < M::kTensors; ++k) {
             if (k == 2 && !gate) break;
-            T* dst = raw + (stage * M::kTensors + k) * M::kRaw;
-            if (a.vec) {
-                constexpr int V = 16 / sizeof(T), R = CT / V;
-#pragma unroll
-                for (int i = 0; i < (TK * R + NT - 1) / NT; ++i) {
-                    const int e = tid + i * NT, j = e / R, x = (e - j * R) * V;
-                    const bool in = t + j < len && x < width;
-                    if (TK * R % NT == 0 || e < TK * R)
-                        copy16(dst + j * CT + x, in ? src[k] + (t + j) * str[k] + x : src[k], in);
-                }
-            } else {
-                T v[TK / SL];
-#pragma unroll
-                for (int i = 0; i < TK / SL; ++i) {
-                    const int e = tid + i * NT, j = e / CT, x = e - j * CT;
-                    v[i] = t + j < len && x < width ? src[k][(t + j) * str[k] + x] : from_f<T>(0.f);
-                }
-#pragma unroll
-                for (int i = 0; i < TK / SL; ++i) dst[tid + i * NT] = v[i];
-            }
+            copy_tile<T, TK, CT, NT, FAST>(raw + (stage * M::kTensors + k) * M::kRaw, src[k], str[k], t, len,
+                                     width, a.vec);
         }
         copy_commit();
     };
-    T pB[BCN], pC[OUTPUT ? BCN : 1];
-    auto fetch = [&](int t) {  // B and C of the tile at t
-#pragma unroll
-        for (int i = 0; i < BCN; ++i) {
-            const int e = tid + i * NT, j = e / NP, s = e - j * NP;
-            const bool in = s < n && t + j < len;
-            pB[i] = in ? Bp[(t + j) * a.d.B.tok_stride + s] : from_f<T>(0.f);
-            if (OUTPUT) pC[i] = in ? Cp[(t + j) * a.d.C.tok_stride + s] : from_f<T>(0.f);
-        }
+    RowsAhead<T, TK, NP, NT, OUTPUT, FAST> bc;
+    auto fetch = [&](int t) {
+        bc.fetch(Bp, a.d.B.tok_stride, Cp, a.d.C.tok_stride, t, len, n);
     };
-    auto stage_bc = [&](int buf) {
-        float* sB = sbc + buf * M::kBC;
-#pragma unroll
-        for (int i = 0; i < BCN; ++i) {
-            sB[tid + i * NT] = to_f(pB[i]);
-            if (OUTPUT) sB[TK * NP + tid + i * NT] = to_f(pC[i]);
-        }
-    };
+    auto stage_bc = [&](int buf) { bc.stage(sbc + buf * M::kBC); };
 #pragma unroll
     for (int i = 0; i < ST - 1; ++i) copy(i * TK, i);
     fetch(0);
@@ -529,7 +555,7 @@ __global__ void __launch_bounds__(kLanesThreads) k_scan_lanes(const ScanArgs a) 
                     const float2 e = mul2(dd, A2[2 * i + p]);
                     hh = fma2(make_float2(ex2(e.x), ex2(e.y)), hh,
                               mul2(dv, p ? make_float2(b4.z, b4.w) : make_float2(b4.x, b4.y)));
-                    if (!EXACT) {
+                    if (!FAST) {
                         if (s0 + 4 * i + 2 * p >= n) hh.x = 0.f;
                         if (s0 + 4 * i + 2 * p + 1 >= n) hh.y = 0.f;
                     }
@@ -675,30 +701,30 @@ __global__ void __launch_bounds__(kCarryThreads) k_scan_carry(const ScanArgs a) 
 }
 
 // SL 0: k_scan, otherwise k_scan_lanes.
-template <class T, int SPT, int SL, int PASS, bool EXACT>
+template <class T, int SPT, int SL, int PASS, bool FAST>
 cudaError_t scan_kernel(const ScanArgs& a, int64_t blocks, cudaStream_t s) {
     static LaunchCache cache;
     LaunchGeom geo;
     if constexpr (SL == 0) {
         constexpr int bytes = ScanPairSmem<T, SPT, PASS>::kBytes;
         const cudaError_t e = cache.get([](int dev, LaunchGeom* g) {
-            return setup_persistent(k_scan<T, SPT, PASS, EXACT>, kPairThreads, bytes, dev, g);
+            return setup_persistent(k_scan<T, SPT, PASS, FAST>, kPairThreads, bytes, dev, g);
         }, &geo);
         if (e != cudaSuccess) return e;
-        k_scan<T, SPT, PASS, EXACT><<<(unsigned)blocks, kPairThreads, bytes, s>>>(a);
+        k_scan<T, SPT, PASS, FAST><<<(unsigned)blocks, kPairThreads, bytes, s>>>(a);
     } else {
         constexpr int bytes = ScanLanesSmem<T, SPT, SL, PASS>::kBytes;
         const cudaError_t e = cache.get([](int dev, LaunchGeom* g) {
-            return setup_persistent(k_scan_lanes<T, SPT, SL, PASS, EXACT>, kLanesThreads, bytes, dev, g);
+            return setup_persistent(k_scan_lanes<T, SPT, SL, PASS, FAST>, kLanesThreads, bytes, dev, g);
         }, &geo);
         if (e != cudaSuccess) return e;
-        k_scan_lanes<T, SPT, SL, PASS, EXACT><<<(unsigned)blocks, kLanesThreads, bytes, s>>>(a);
+        k_scan_lanes<T, SPT, SL, PASS, FAST><<<(unsigned)blocks, kLanesThreads, bytes, s>>>(a);
     }
     return cudaGetLastError();
 }
 
 // Passes 1 and 2 where time is cut, then the pass that was asked for.
-template <class T, int SPT, int SL, int PASS, bool EXACT>
+template <class T, int SPT, int SL, int PASS, bool FAST>
 cudaError_t scan_launch(const ScanArgs& a, cudaStream_t s) {
     const int64_t tiles = a.ctiles * a.d.groups;
     const bool empties = PASS == SCAN_OUTPUT && a.final_state && (a.d.offsets || a.d.length == 0);
@@ -706,20 +732,21 @@ cudaError_t scan_launch(const ScanArgs& a, cudaStream_t s) {
     if (blocks < 1) return cudaSuccess;
     if (blocks > INT32_MAX) return cudaErrorInvalidValue;
     if (a.nchunks > 1) {
-        const cudaError_t e = scan_kernel<T, SPT, SL, SCAN_SUMMARY, EXACT>(
+        const cudaError_t e = scan_kernel<T, SPT, SL, SCAN_SUMMARY, FAST>(
             a, a.rows * (a.nchunks - 1) * tiles, s);
         if (e != cudaSuccess) return e;
         constexpr int NP = SPT * (SL ? SL : 1);
         k_scan_carry<NP><<<(unsigned)((a.rows * a.d.channels * NP + kCarryThreads - 1) / kCarryThreads),
                            kCarryThreads, 0, s>>>(a);
     }
-    return scan_kernel<T, SPT, SL, PASS, EXACT>(a, blocks, s);
+    return scan_kernel<T, SPT, SL, PASS, FAST>(a, blocks, s);
 }
 
 template <class T, int SPT, int SL, int PASS>
-cudaError_t scan_exact(const ScanArgs& a, cudaStream_t s) {
-    return a.d.states == SPT * (SL ? SL : 1) ? scan_launch<T, SPT, SL, PASS, true>(a, s)
-                                             : scan_launch<T, SPT, SL, PASS, false>(a, s);
+cudaError_t scan_fast(const ScanArgs& a, cudaStream_t s) {
+    return a.d.states == SPT * (SL ? SL : 1) && a.vec >= 16 && a.wide
+               ? scan_launch<T, SPT, SL, PASS, true>(a, s)
+               : scan_launch<T, SPT, SL, PASS, false>(a, s);
 }
 template <class T, int PASS>
 cudaError_t scan_run(ScanArgs a, cudaStream_t s) {
@@ -729,18 +756,22 @@ cudaError_t scan_run(ScanArgs a, cudaStream_t s) {
         return !q.data || (aligned_to(q.data, bytes) && q.tok_stride * sizeof(T) % bytes == 0 &&
                            (packed || q.seq_stride * sizeof(T) % bytes == 0));
     };
-    a.vec = dg * sizeof(T) % 16 == 0 && rows_on(a.d.u, 16) && rows_on(a.d.delta, 16) &&
-            rows_on(a.d.z, 16);
+    auto all_on = [&](int64_t bytes) {
+        return dg * sizeof(T) % bytes == 0 && rows_on(a.d.u, bytes) && rows_on(a.d.delta, bytes) &&
+               rows_on(a.d.z, bytes);
+    };
+    a.vec = all_on(16) ? 16 : (all_on(4) ? 4 : 0);
+    a.wide = rows_on(a.d.B, 16) && rows_on(a.d.C, 16) && a.d.states * sizeof(T) % 16 == 0;
     a.pair = dg % 2 == 0 && rows_on(a.out, 2 * sizeof(T));
     switch (scan_np(a.d.states) * 100 + a.sl) {
-        case 400: return scan_exact<T, 4, 0, PASS>(a, s);
-        case 800: return scan_exact<T, 8, 0, PASS>(a, s);
-        case 802: return scan_exact<T, 4, 2, PASS>(a, s);
-        case 1600: return scan_exact<T, 16, 0, PASS>(a, s);
-        case 1602: return scan_exact<T, 8, 2, PASS>(a, s);
-        case 3202: return scan_exact<T, 16, 2, PASS>(a, s);
-        case 6404: return scan_exact<T, 16, 4, PASS>(a, s);
-        case 12808: return scan_exact<T, 16, 8, PASS>(a, s);
+        case 400: return scan_fast<T, 4, 0, PASS>(a, s);
+        case 800: return scan_fast<T, 8, 0, PASS>(a, s);
+        case 802: return scan_fast<T, 4, 2, PASS>(a, s);
+        case 1600: return scan_fast<T, 16, 0, PASS>(a, s);
+        case 1602: return scan_fast<T, 8, 2, PASS>(a, s);
+        case 3202: return scan_fast<T, 16, 2, PASS>(a, s);
+        case 6404: return scan_fast<T, 16, 4, PASS>(a, s);
+        case 12808: return scan_fast<T, 16, 8, PASS>(a, s);
         default: return cudaErrorInvalidValue;
     }
 }

@@ -31,7 +31,8 @@ struct ScanArgs {
     float* tiles;  // the state before every tile [rows][tiles][channels][np]
     int64_t rows, chunk, nchunks, ctiles;  // tokens per chunk; channel tiles per group
     int sl;    // 0: k_scan, else the lanes per channel of k_scan_lanes
-    int vec;   // rows of u, delta and z start on 16-byte boundaries
+    int vec;   // bytes that rows of u, delta and z start on: 16, 4 or 0
+    int wide;  // the states of B and C are whole 16-byte accesses
     int pair;  // two channels of out are one access
 };
 

@@ -28,10 +28,9 @@ namespace gbfft {
 // The gradient that a chunk sends back, with nothing entering from behind: the tokens in reverse,
 //   m <- a[t] (dy[t] C[t] + m).
 // Up to 16 states: two channels per thread, built like the forward kernel k_scan.
-template <class T, int SPT>
+template <class T, int SPT, bool FAST>
 __global__ void __launch_bounds__(kPairThreads) k_scan_back_pair(const ScanBwdArgs a) {
     constexpr int NT = kPairThreads, CT = kPairChannels, TK = kPairTile, ST = 3, RAW = TK * CT;
-    constexpr int CN = (TK * SPT + NT - 1) / NT;
     extern __shared__ float4 smem4[];
     T* raw = reinterpret_cast<T*>(smem4);  // [stage][delta, dout, z][token][channel]
     float* sc = reinterpret_cast<float*>(raw + ST * 3 * RAW);  // [buffer][token][state]
@@ -58,43 +57,15 @@ __global__ void __launch_bounds__(kPairThreads) k_scan_back_pair(const ScanBwdAr
 #pragma unroll
             for (int k = 0; k < 3; ++k) {
                 if (k == 2 && !gate) break;
-                T* dst = raw + (stage * 3 + k) * RAW;
-                if (a.f.vec) {
-                    constexpr int V = 16 / sizeof(T), R = CT / V, STEP = NT / R;
-                    const int j0 = tid / R, x = (tid - j0 * R) * V;
-                    const T* p = src[k] + (t + j0) * str[k] + x;
-#pragma unroll
-                    for (int j = 0; j < TK; j += STEP, p += STEP * str[k]) {
-                        const bool in = t + j0 + j < len && x < width;
-                        copy16(dst + (j0 + j) * CT + x, in ? p : src[k], in);
-                    }
-                } else {
-#pragma unroll 4
-                    for (int e = tid; e < RAW; e += NT) {
-                        const int j = e / CT, x = e - j * CT;
-                        dst[e] = t + j < len && x < width ? src[k][(t + j) * str[k] + x] : from_f<T>(0.f);
-                    }
-                }
+                copy_tile<T, TK, CT, NT, FAST>(raw + (stage * 3 + k) * RAW, src[k], str[k], t, len, width,
+                                         a.f.vec);
             }
         }
         copy_commit();
     };
-    T pC[CN];
-    auto fetch = [&](int t) {
-#pragma unroll
-        for (int i = 0; i < CN; ++i) {
-            const int e = tid + i * NT, j = e / SPT, s = e - j * SPT;
-            const bool in = (TK * SPT % NT == 0 || e < TK * SPT) && s < n && t >= 0 && t + j < len;
-            pC[i] = in ? Cp[(t + j) * a.d.C.tok_stride + s] : from_f<T>(0.f);
-        }
-    };
-    auto stage_c = [&](int buf) {
-#pragma unroll
-        for (int i = 0; i < CN; ++i) {
-            const int e = tid + i * NT;
-            if (TK * SPT % NT == 0 || e < TK * SPT) sc[buf * TK * SPT + e] = to_f(pC[i]);
-        }
-    };
+    RowsAhead<T, TK, SPT, NT, false, FAST> rows;
+    auto fetch = [&](int t) { rows.fetch(Cp, a.d.C.tok_stride, Cp, 0, t, len, n); };
+    auto stage_c = [&](int buf) { rows.stage(sc + buf * TK * SPT); };
     const int first = (len - 1) / TK * TK;
 #pragma unroll
     for (int i = 0; i < ST - 1; ++i) copy(first - i * TK, i);
@@ -330,8 +301,9 @@ struct BwdShape {
     static constexpr int kBytes = kFloats * 4 + 4 * kRaw * (int)sizeof(T) + TK * 8 + 16;
 };
 
-// EXACT (n == 4 * SL) drops the selects that keep states beyond n at 0 where u is infinite.
-template <class T, int SL, bool EXACT>
+// FAST: n == 4 * SL, so that no state beyond n has to be kept at 0 where u is infinite, and rows on
+// 16-byte boundaries.
+template <class T, int SL, bool FAST>
 __global__ void __launch_bounds__(BwdShape<T, SL>::NT) k_scan_bwd(const ScanBwdArgs a) {
     using S = BwdShape<T, SL>;
     constexpr int NT = S::NT, CL = S::CL, CT = S::CT, NP = S::NP, TK = S::TK, TS = S::TS;
@@ -384,22 +356,8 @@ __global__ void __launch_bounds__(BwdShape<T, SL>::NT) k_scan_bwd(const ScanBwdA
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
             if (k == 3 && !gate) break;
-            T* dst = raw + k * S::kRaw;
-            const T* p = src[k] + tl * str[k];
-            if (a.f.vec) {
-                constexpr int V = 16 / sizeof(T), R = CT / V;
-                for (int e = tid; e < TK * R; e += NT) {
-                    const int j = e / R, x = (e - j * R) * V;
-                    const bool in = j < len && x < width;
-                    copy16(dst + j * CT + x, in ? p + j * str[k] + x : src[k], in);
-                }
-            } else {
-#pragma unroll 4
-                for (int e = tid; e < TK * CT; e += NT) {
-                    const int j = e / CT, x = e - j * CT;
-                    dst[e] = j < len && x < width ? p[j * str[k] + x] : from_f<T>(0.f);
-                }
-            }
+            copy_tile<T, TK, CT, NT, FAST>(raw + k * S::kRaw, src[k] + tl * str[k], str[k], 0, len, width,
+                                     a.f.vec);
         }
         copy_commit();
     };
@@ -567,7 +525,7 @@ __global__ void __launch_bounds__(BwdShape<T, SL>::NT) k_scan_bwd(const ScanBwdA
                     for (int p = 0; p < 2; ++p) {
                         const float2 e = mul2(dd[p], A2[s + k][p]);
                         h[s + k][p] = fma2(make_float2(ex2(e.x), ex2(e.y)), h[s + k][p], mul2(du2[p], b));
-                        if (!EXACT && s0 + s + k >= n) h[s + k][p] = splat(0.f);
+                        if (!FAST && s0 + s + k >= n) h[s + k][p] = splat(0.f);
                     }
                 }
             }
@@ -781,23 +739,23 @@ __global__ void __launch_bounds__(256) k_scan_back_empty(const ScanBwdArgs a) {
         a.g.dinitial_state[q * per + i] = a.g.dfinal_state ? a.g.dfinal_state[q * per + i] : 0.f;
 }
 
-template <class T, int SL, bool EXACT>
+template <class T, int SL, bool FAST>
 cudaError_t scan_bwd_launch(const ScanBwdArgs& a, cudaStream_t s) {
     using S = BwdShape<T, SL>;
     static LaunchCache cache;
     LaunchGeom geo;
     cudaError_t e = cache.get([](int dev, LaunchGeom* g) {
-        return setup_persistent(k_scan_bwd<T, SL, EXACT>, S::NT, S::kBytes, dev, g);
+        return setup_persistent(k_scan_bwd<T, SL, FAST>, S::NT, S::kBytes, dev, g);
     }, &geo);
     if (e != cudaSuccess) return e;
     const int64_t blocks = a.f.rows * a.f.nchunks * a.ctiles * a.d.groups;
     if (blocks > INT32_MAX) return cudaErrorInvalidValue;
-    k_scan_bwd<T, SL, EXACT><<<(unsigned)blocks, S::NT, S::kBytes, s>>>(a);
+    k_scan_bwd<T, SL, FAST><<<(unsigned)blocks, S::NT, S::kBytes, s>>>(a);
     return cudaGetLastError();
 }
 template <class T, int SL>
 cudaError_t scan_bwd_main(const ScanBwdArgs& a, cudaStream_t s) {
-    return a.d.states == 4 * SL ? scan_bwd_launch<T, SL, true>(a, s)
+    return a.d.states == 4 * SL && a.f.vec >= 16 ? scan_bwd_launch<T, SL, true>(a, s)
                                 : scan_bwd_launch<T, SL, false>(a, s);
 }
 template <int NP>
@@ -807,18 +765,23 @@ cudaError_t scan_bwd_carry(const ScanBwdArgs& a, cudaStream_t s) {
            kCarryThreads, 0, s>>>(a);
     return cudaGetLastError();
 }
-template <class T, int SPT>
-cudaError_t scan_bwd_back_pair(const ScanBwdArgs& a, cudaStream_t s) {
+template <class T, int SPT, bool FAST>
+cudaError_t scan_bwd_pair_launch(const ScanBwdArgs& a, cudaStream_t s) {
     constexpr int bytes = 3 * 3 * kPairTile * kPairChannels * (int)sizeof(T) + 2 * kPairTile * SPT * 4;
     static LaunchCache cache;
     LaunchGeom geo;
     const cudaError_t e = cache.get([](int dev, LaunchGeom* g) {
-        return setup_persistent(k_scan_back_pair<T, SPT>, kPairThreads, bytes, dev, g);
+        return setup_persistent(k_scan_back_pair<T, SPT, FAST>, kPairThreads, bytes, dev, g);
     }, &geo);
     if (e != cudaSuccess) return e;
-    k_scan_back_pair<T, SPT><<<(unsigned)(a.f.rows * (a.f.nchunks - 1) * a.f.ctiles * a.d.groups),
-                               kPairThreads, bytes, s>>>(a);
+    const int64_t blocks = a.f.rows * (a.f.nchunks - 1) * a.f.ctiles * a.d.groups;
+    k_scan_back_pair<T, SPT, FAST><<<(unsigned)blocks, kPairThreads, bytes, s>>>(a);
     return scan_bwd_carry<SPT>(a, s);
+}
+template <class T, int SPT>
+cudaError_t scan_bwd_back_pair(const ScanBwdArgs& a, cudaStream_t s) {
+    return a.d.states == SPT && a.f.vec >= 16 && a.f.wide ? scan_bwd_pair_launch<T, SPT, true>(a, s)
+                                                          : scan_bwd_pair_launch<T, SPT, false>(a, s);
 }
 template <class T, int SPT, int SL>
 cudaError_t scan_bwd_back(const ScanBwdArgs& a, cudaStream_t s) {
@@ -830,12 +793,16 @@ cudaError_t scan_bwd_back(const ScanBwdArgs& a, cudaStream_t s) {
 template <class T>
 cudaError_t scan_bwd_run(ScanBwdArgs a, cudaStream_t s) {
     cudaError_t e = cudaSuccess;
-    auto rows16 = [&](const fft_seq& q) {
-        return !q.data || (aligned_to(q.data, 16) && q.tok_stride * sizeof(T) % 16 == 0 &&
-                           (a.d.offsets || q.seq_stride * sizeof(T) % 16 == 0));
+    auto rows_on = [&](const fft_seq& q, int64_t bytes) {
+        return !q.data || (aligned_to(q.data, bytes) && q.tok_stride * sizeof(T) % bytes == 0 &&
+                           (a.d.offsets || q.seq_stride * sizeof(T) % bytes == 0));
     };
-    a.f.vec = a.d.channels / a.d.groups * sizeof(T) % 16 == 0 && rows16(a.d.u) &&
-              rows16(a.d.delta) && rows16(a.d.z) && rows16(a.g.dout);
+    auto all_on = [&](int64_t bytes) {
+        return a.d.channels / a.d.groups * sizeof(T) % bytes == 0 && rows_on(a.d.u, bytes) &&
+               rows_on(a.d.delta, bytes) && rows_on(a.d.z, bytes) && rows_on(a.g.dout, bytes);
+    };
+    a.f.vec = all_on(16) ? 16 : (all_on(4) ? 4 : 0);
+    a.f.wide = rows_on(a.d.B, 16) && rows_on(a.d.C, 16) && a.d.states * sizeof(T) % 16 == 0;
     const int64_t n = a.d.states, parts = a.f.rows * a.f.nchunks;
     if (a.d.length > 0) {
         if (parts * a.back_ctiles * a.d.groups > INT32_MAX) return cudaErrorInvalidValue;

@@ -143,12 +143,23 @@ int64_t scan_bwd_layout(const fft_scan_desc& d, ScanBwdArgs* a, char* w) {
     const int64_t n = d.states, np = scan_np(n), sl = bwd_sl(n), ct = bwd_channels((int)sl);
     const int64_t dg = d.channels / d.groups, rows = d.offsets ? 1 : d.nseq;
     const int64_t ctiles = (dg + ct - 1) / ct;
-    // chunks: enough blocks of the main kernel to fill the GPU (two to an SM) several times
-    const int64_t blocks = rows * ctiles * d.groups, want = (int64_t)num_sms() * 8;
-    const int64_t k = (want + blocks - 1) / blocks;
-    int64_t chunk = (d.length + k - 1) / k;
-    chunk = (chunk + 63) / 64 * 64;
-    if (chunk < 64) chunk = 64;
+    // Chunks: the main kernel holds two blocks on an SM, so the time goes with the rounds of blocks
+    // times the tokens of a chunk (and about 16 tokens' time to start a block); the fewest chunks
+    // of the best.  Four rows of 2048 tokens and 2048 channels: nine chunks of 240 tokens.
+    const int64_t blocks = rows * ctiles * d.groups, resident = (int64_t)num_sms() * 2;
+    int64_t chunk = 64, best = INT64_MAX;
+    for (int64_t k = 1; k <= 256; ++k) {
+        int64_t size = (d.length + k - 1) / k;
+        size = (size + 15) / 16 * 16;
+        if (size < 64) size = 64;
+        const int64_t n = (d.length + size - 1) / size;
+        const int64_t cost = (blocks * n + resident - 1) / resident * (size + 16);
+        if (cost < best) {
+            best = cost;
+            chunk = size;
+        }
+        if (size == 64) break;
+    }
     const int64_t nchunks = (d.length + chunk - 1) / chunk;
     const int64_t state_tiles = (d.length + kScanTile - 1) / kScanTile;
     int64_t at = 0;

@@ -156,7 +156,7 @@ __device__ __forceinline__ void hand_out(float (&v)[V], int id) {
     }
 }
 
-// Asynchronous copies of 16 and 8 bytes into shared memory; zeros where `in` is false (nothing is
+// Asynchronous copies of 16, 8 and 4 bytes into shared memory; zeros where `in` is false (nothing is
 // read).
 __device__ __forceinline__ void copy16(void* dst, const void* src, bool in) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(
@@ -168,6 +168,12 @@ __device__ __forceinline__ void copy8(void* dst, const void* src, bool in) {
     asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(
                      (unsigned)__cvta_generic_to_shared(dst)),
                  "l"(src), "r"(in ? 8 : 0)
+                 : "memory");
+}
+__device__ __forceinline__ void copy4(void* dst, const void* src, bool in) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(
+                     (unsigned)__cvta_generic_to_shared(dst)),
+                 "l"(src), "r"(in ? 4 : 0)
                  : "memory");
 }
 __device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
