@@ -214,7 +214,7 @@ struct ScanPairSmem {
 // u may be infinite).  FAST: n == SPT and all rows are whole 16-byte accesses, the usual case,
 // whose code is free of these questions.
 template <class T, int SPT, int PASS, bool FAST>
-__global__ void __launch_bounds__(kPairThreads) k_scan(const ScanArgs a) {
+__global__ void __launch_bounds__(kPairThreads, 6) k_scan(const ScanArgs a) {
     using M = ScanPairSmem<T, SPT, PASS>;
     constexpr int NT = kPairThreads, CT = kPairChannels, TK = kPairTile, ST = M::kStages;
     constexpr bool SUMMARY = PASS == SCAN_SUMMARY, OUTPUT = PASS == SCAN_OUTPUT;

@@ -89,12 +89,12 @@ SYMBOLS = ("fft_conv_forward", "fft_conv_workspace", "fft_conv_backward", "fft_c
 
 # ---- checks ---------------------------------------------------------------------------------
 
-_L = torch = _CODES = _raw_stream = None
+_L = torch = _CODES = _raw_stream = _device = None
 
 
 def _setup():
     """Bind the library and torch on the first call."""
-    global _L, torch, _CODES, _raw_stream
+    global _L, torch, _CODES, _raw_stream, _device
     import torch as _torch
 
     from . import lib
@@ -102,6 +102,7 @@ def _setup():
     _CODES = {_torch.float32: F32, _torch.bfloat16: BF16, _torch.float16: F16}
     _raw_stream = getattr(_torch._C, "_cuda_getCurrentRawStream", None) or (
         lambda device: _torch.cuda.current_stream(device).cuda_stream)
+    _device = getattr(_torch._C, "_cuda_getDevice", None) or _torch.cuda.current_device
     torch = _torch
     _L = lib()
 
@@ -121,7 +122,7 @@ def _first(t, what):
     if code is None or not t.is_cuda:
         raise TypeError(f"{what}: expected a float32, bfloat16 or float16 CUDA tensor")
     dev = t.get_device()
-    if dev != torch.cuda.current_device():  # the library launches there
+    if dev != _device():  # the library launches there
         raise ValueError(f"{what}: expected a tensor on the current CUDA device")
     return code, dev
 
@@ -182,13 +183,18 @@ def _groups(t, dev, dtype, lead, what):
     """B or C: [..., groups, n] or [..., n], groups back to back."""
     if t.dim() == len(lead) + 1:
         t = t.unsqueeze(-2)
-    shape = t.shape
+    shape = tuple(t.shape)
     if (t.dtype is not dtype or shape[:-2] != lead or t.get_device() != dev
             or (t.stride(-1) != 1 and shape[-1] > 1)):
         _tell(t, dev, dtype, (*lead, *shape[-2:]), what)
     if shape[-2] > 1 and t.stride(-2) != shape[-1]:
         raise ValueError(f"{what}: the groups must lie back to back")
     return t
+
+
+def _slots(slots, slots_out, dev, nseq):
+    return (_flat(slots, dev, torch.int64, (nseq,), "slots"),
+            _flat(slots_out, dev, torch.int64, (nseq,), "slots_out"))
 
 
 def _out(out, like, dev):
@@ -299,13 +305,16 @@ def causal_conv_step(state, x, weight, bias=None, silu=False, slots=None, slots_
     desc, dev, nseq, d, w = _conv_desc(x, weight, bias, silu, None, None, step=True)
     size = state.shape[0]
     pool = _flat(state, dev, x.dtype, (size, w - 1, d), "state")
-    on, s = _stream(stream, dev)
-    with on:
-        out = _out(out, x, dev)
-        _check(_L.fft_conv_step(desc, _SEQ.pack(*_row(out)), pool, size,
-                                _flat(slots, dev, torch.int64, (nseq,), "slots"),
-                                _flat(slots_out, dev, torch.int64, (nseq,), "slots_out"), s),
-               "fft_conv_step")
+    src, dst = _slots(slots, slots_out, dev, nseq)
+    if out is None and stream is None:  # the usual call
+        out, s = x.new_empty((nseq, d)), _raw_stream(dev)
+        rc = _L.fft_conv_step(desc, _SEQ.pack(out.data_ptr(), d, 0), pool, size, src, dst, s)
+    else:
+        on, s = _stream(stream, dev)
+        with on:
+            out = _out(out, x, dev)
+            rc = _L.fft_conv_step(desc, _SEQ.pack(*_row(out)), pool, size, src, dst, s)
+    _check(rc, "fft_conv_step")
     return out
 
 
@@ -315,7 +324,7 @@ def causal_conv_step(state, x, weight, bias=None, silu=False, slots=None, slots_
 def _scan_desc(u, delta, A, B, C, D, z, delta_bias, softplus, initial_state, offsets, step=False):
     """(packed fft_scan_desc, device, sequences, channels, states)."""
     code, dev = _first(u, "u")
-    f32, dtype, shape = torch.float32, u.dtype, u.shape
+    f32, dtype, shape = torch.float32, u.dtype, tuple(u.shape)
     d, lead = shape[-1], shape[:-1]
     if step:
         if u.dim() != 2:
@@ -397,13 +406,16 @@ def selective_scan_step(state, u, delta, A, B, C, D=None, z=None, delta_bias=Non
                                        step=True)
     size = state.shape[0]
     pool = _flat(state, dev, torch.float32, (size, d, n), "state")
-    on, s = _stream(stream, dev)
-    with on:
-        out = _out(out, u, dev)
-        _check(_L.fft_scan_step(desc, _SEQ.pack(*_row(out)), pool, size,
-                                _flat(slots, dev, torch.int64, (nseq,), "slots"),
-                                _flat(slots_out, dev, torch.int64, (nseq,), "slots_out"), s),
-               "fft_scan_step")
+    src, dst = _slots(slots, slots_out, dev, nseq)
+    if out is None and stream is None:  # the usual call
+        out, s = u.new_empty((nseq, d)), _raw_stream(dev)
+        rc = _L.fft_scan_step(desc, _SEQ.pack(out.data_ptr(), d, 0), pool, size, src, dst, s)
+    else:
+        on, s = _stream(stream, dev)
+        with on:
+            out = _out(out, u, dev)
+            rc = _L.fft_scan_step(desc, _SEQ.pack(*_row(out)), pool, size, src, dst, s)
+    _check(rc, "fft_scan_step")
     return out
 
 
