@@ -118,10 +118,9 @@ def _first(t, what):
     """(type code, device index) of the tensor that the others are compared with."""
     if _L is None:
         _setup()
-    code = _CODES.get(getattr(t, "dtype", None))
-    if code is None or not t.is_cuda:
+    code, dev = _CODES.get(t.dtype), t.get_device()
+    if code is None or dev < 0:
         raise TypeError(f"{what}: expected a float32, bfloat16 or float16 CUDA tensor")
-    dev = t.get_device()
     if dev != _device():  # the library launches there
         raise ValueError(f"{what}: expected a tensor on the current CUDA device")
     return code, dev
@@ -140,7 +139,7 @@ def _tell(t, dev, dtype, shape, what):
 
 def _need(t, dev, dtype, shape, what):
     """t on the device, of this dtype and shape, its last axis contiguous."""
-    if (getattr(t, "dtype", None) is not dtype or t.shape != shape or t.get_device() != dev
+    if (t.dtype is not dtype or t.shape != shape or t.get_device() != dev
             or (t.stride(-1) != 1 and t.shape[-1] > 1)):
         _tell(t, dev, dtype, shape, what)
     return t
@@ -150,10 +149,22 @@ def _flat(t, dev, dtype, shape, what):
     """The address of a contiguous tensor, or 0 for None."""
     if t is None:
         return 0
-    if (getattr(t, "dtype", None) is not dtype or t.shape != shape or t.get_device() != dev
+    if (t.dtype is not dtype or t.shape != shape or t.get_device() != dev
             or not t.is_contiguous()):
         _tell(t, dev, dtype, shape, what)
     return t.data_ptr()
+
+
+def _token(t, dev, dtype, shape, what):
+    """The fields of an fft_seq of one token per sequence, [sequences, ...]: one question each, as
+    a single-token call takes less time on the GPU than a dozen tensors asked twice."""
+    st = t.stride()
+    if (t.dtype is not dtype or t.shape != shape or t.get_device() != dev
+            or (st[-1] != 1 and shape[-1] > 1)):
+        _tell(t, dev, dtype, shape, what)
+    if len(st) == 3 and shape[1] > 1 and st[1] != shape[2]:
+        raise ValueError(f"{what}: the groups must lie back to back")
+    return t.data_ptr(), st[0], 0
 
 
 def _offsets(offsets, dev):
@@ -172,7 +183,7 @@ def _seq(t, packed):
 
 
 def _row(t):
-    return (t.data_ptr(), t.stride(0), 0) if t is not None else _NONE
+    return t.data_ptr(), t.stride(0), 0
 
 
 def _ptr(t):
@@ -190,11 +201,6 @@ def _groups(t, dev, dtype, lead, what):
     if shape[-2] > 1 and t.stride(-2) != shape[-1]:
         raise ValueError(f"{what}: the groups must lie back to back")
     return t
-
-
-def _slots(slots, slots_out, dev, nseq):
-    return (_flat(slots, dev, torch.int64, (nseq,), "slots"),
-            _flat(slots_out, dev, torch.int64, (nseq,), "slots_out"))
 
 
 def _out(out, like, dev):
@@ -236,17 +242,12 @@ def _lead(x, offsets, what):
 # ---- short causal convolution ---------------------------------------------------------------
 
 
-def _conv_desc(x, weight, bias, silu, initial_state, offsets, step=False):
+def _conv_desc(x, weight, bias, silu, initial_state, offsets):
     """(packed fft_conv_desc, device, sequences, channels, width)."""
     code, dev = _first(x, "x")
     dtype, shape = x.dtype, x.shape
     d = shape[-1]
-    if step:
-        if x.dim() != 2:
-            raise ValueError("x: expected [sequences, channels]")
-        packed, nseq, length = False, shape[0], 1
-    else:
-        packed, nseq, length = _lead(x, offsets, "x")
+    packed, nseq, length = _lead(x, offsets, "x")
     if x.stride(-1) != 1 and d > 1:
         _tell(x, dev, dtype, shape, "x")
     if weight.dim() != 2:
@@ -259,7 +260,7 @@ def _conv_desc(x, weight, bias, silu, initial_state, offsets, step=False):
                       _flat(weight, dev, ptype, (d, w), "weight"),
                       _flat(bias, dev, ptype, (d,), "bias"),
                       _flat(initial_state, dev, dtype, (nseq, w - 1, d), "initial_state"),
-                      *(_row(x) if step else _seq(x, packed)))
+                      *_seq(x, packed))
     return desc, dev, nseq, d, w
 
 
@@ -302,36 +303,43 @@ def causal_conv_step(state, x, weight, bias=None, silu=False, slots=None, slots_
                      stream=None):
     """One token for each sequence (fft_conv_step): x [sequences, channels], state the pool
     [pool, width-1, channels], updated in place; slots, slots_out int64 [sequences]."""
-    desc, dev, nseq, d, w = _conv_desc(x, weight, bias, silu, None, None, step=True)
+    code, dev = _first(x, "x")
+    dtype, shape = x.dtype, x.shape
+    if len(shape) != 2 or weight.dim() != 2:
+        raise ValueError("x: expected [sequences, channels], weight: [channels, width]")
+    nseq, d = shape
+    w, ptype = weight.shape[1], weight.dtype
+    if ptype is not dtype and ptype is not torch.float32:
+        raise TypeError("weight: expected float32 or the type of x")
+    desc = _CONV.pack(code, F32 if ptype is torch.float32 else code, w, 1 if silu else 0, nseq, 1, d,
+                      0, _flat(weight, dev, ptype, (d, w), "weight"),
+                      _flat(bias, dev, ptype, (d,), "bias"), 0, *_token(x, dev, dtype, shape, "x"))
     size = state.shape[0]
-    pool = _flat(state, dev, x.dtype, (size, w - 1, d), "state")
-    src, dst = _slots(slots, slots_out, dev, nseq)
+    pool = _flat(state, dev, dtype, (size, w - 1, d), "state")
+    src = _flat(slots, dev, torch.int64, (nseq,), "slots")
+    dst = _flat(slots_out, dev, torch.int64, (nseq,), "slots_out")
     if out is None and stream is None:  # the usual call
-        out, s = x.new_empty((nseq, d)), _raw_stream(dev)
-        rc = _L.fft_conv_step(desc, _SEQ.pack(out.data_ptr(), d, 0), pool, size, src, dst, s)
-    else:
-        on, s = _stream(stream, dev)
-        with on:
-            out = _out(out, x, dev)
-            rc = _L.fft_conv_step(desc, _SEQ.pack(*_row(out)), pool, size, src, dst, s)
-    _check(rc, "fft_conv_step")
+        out = x.new_empty(shape)
+        _check(_L.fft_conv_step(desc, _SEQ.pack(out.data_ptr(), d, 0), pool, size, src, dst,
+                                _raw_stream(dev)), "fft_conv_step")
+        return out
+    on, s = _stream(stream, dev)
+    with on:
+        out = _out(out, x, dev)
+        _check(_L.fft_conv_step(desc, _SEQ.pack(*_row(out)), pool, size, src, dst, s),
+               "fft_conv_step")
     return out
 
 
 # ---- selective scan -------------------------------------------------------------------------
 
 
-def _scan_desc(u, delta, A, B, C, D, z, delta_bias, softplus, initial_state, offsets, step=False):
+def _scan_desc(u, delta, A, B, C, D, z, delta_bias, softplus, initial_state, offsets):
     """(packed fft_scan_desc, device, sequences, channels, states)."""
     code, dev = _first(u, "u")
     f32, dtype, shape = torch.float32, u.dtype, tuple(u.shape)
     d, lead = shape[-1], shape[:-1]
-    if step:
-        if u.dim() != 2:
-            raise ValueError("u: expected [sequences, channels]")
-        packed, nseq, length = False, shape[0], 1
-    else:
-        packed, nseq, length = _lead(u, offsets, "u")
+    packed, nseq, length = _lead(u, offsets, "u")
     if u.stride(-1) != 1 and d > 1:
         _tell(u, dev, dtype, shape, "u")
     _need(delta, dev, dtype, shape, "delta")
@@ -345,11 +353,8 @@ def _scan_desc(u, delta, A, B, C, D, z, delta_bias, softplus, initial_state, off
              _flat(A, dev, f32, (d, n), "A"), _flat(D, dev, f32, (d,), "D"),
              _flat(delta_bias, dev, f32, (d,), "delta_bias"),
              _flat(initial_state, dev, f32, (nseq, d, n), "initial_state"))
-    if step:
-        desc = _SCAN.pack(*heads, *_row(u), *_row(delta), *_row(B), *_row(C), *_row(z))
-    else:
-        desc = _SCAN.pack(*heads, *_seq(u, packed), *_seq(delta, packed), *_seq(B, packed),
-                          *_seq(C, packed), *_seq(z, packed))
+    desc = _SCAN.pack(*heads, *_seq(u, packed), *_seq(delta, packed), *_seq(B, packed),
+                      *_seq(C, packed), *_seq(z, packed))
     return desc, dev, nseq, d, n
 
 
@@ -402,20 +407,32 @@ def selective_scan_step(state, u, delta, A, B, C, D=None, z=None, delta_bias=Non
     """One token for each sequence (fft_scan_step): u, delta, z [sequences, channels], B, C
     [sequences, groups, n] or [sequences, n], state the pool [pool, channels, n] float32, updated
     in place; slots, slots_out int64 [sequences]."""
-    desc, dev, nseq, d, n = _scan_desc(u, delta, A, B, C, D, z, delta_bias, softplus, None, None,
-                                       step=True)
+    code, dev = _first(u, "u")
+    f32, dtype, shape, bshape = torch.float32, u.dtype, u.shape, B.shape
+    if len(shape) != 2 or len(bshape) not in (2, 3) or bshape[0] != shape[0]:
+        raise ValueError("u: expected [sequences, channels], B: [sequences, groups, n]")
+    nseq, d = shape
+    groups, n = (1, bshape[1]) if len(bshape) == 2 else bshape[1:]
+    desc = _SCAN.pack(code, 1 if softplus else 0, nseq, 1, d, groups, n, 0,
+                      _flat(A, dev, f32, (d, n), "A"), _flat(D, dev, f32, (d,), "D"),
+                      _flat(delta_bias, dev, f32, (d,), "delta_bias"), 0,
+                      *_token(u, dev, dtype, shape, "u"), *_token(delta, dev, dtype, shape, "delta"),
+                      *_token(B, dev, dtype, bshape, "B"), *_token(C, dev, dtype, bshape, "C"),
+                      *(_token(z, dev, dtype, shape, "z") if z is not None else _NONE))
     size = state.shape[0]
-    pool = _flat(state, dev, torch.float32, (size, d, n), "state")
-    src, dst = _slots(slots, slots_out, dev, nseq)
+    pool = _flat(state, dev, f32, (size, d, n), "state")
+    src = _flat(slots, dev, torch.int64, (nseq,), "slots")
+    dst = _flat(slots_out, dev, torch.int64, (nseq,), "slots_out")
     if out is None and stream is None:  # the usual call
-        out, s = u.new_empty((nseq, d)), _raw_stream(dev)
-        rc = _L.fft_scan_step(desc, _SEQ.pack(out.data_ptr(), d, 0), pool, size, src, dst, s)
-    else:
-        on, s = _stream(stream, dev)
-        with on:
-            out = _out(out, u, dev)
-            rc = _L.fft_scan_step(desc, _SEQ.pack(*_row(out)), pool, size, src, dst, s)
-    _check(rc, "fft_scan_step")
+        out = u.new_empty(shape)
+        _check(_L.fft_scan_step(desc, _SEQ.pack(out.data_ptr(), d, 0), pool, size, src, dst,
+                                _raw_stream(dev)), "fft_scan_step")
+        return out
+    on, s = _stream(stream, dev)
+    with on:
+        out = _out(out, u, dev)
+        _check(_L.fft_scan_step(desc, _SEQ.pack(*_row(out)), pool, size, src, dst, s),
+               "fft_scan_step")
     return out
 
 
@@ -423,30 +440,29 @@ def selective_scan_step(state, u, delta, A, B, C, D=None, z=None, delta_bias=Non
 
 
 def _rows(t):
-    """[..., columns] as rows of one stride: (rows, stride)."""
-    dim = t.dim()
-    if dim == 2:
-        return t.shape[0], t.stride(0)
-    if dim < 2:
-        return (1, t.shape[-1])
-    rows, stride = t.shape[-2], t.stride(-2)
-    for k in range(dim - 3, -1, -1):
-        if t.shape[k] != 1 and rows != 1 and t.stride(k) != rows * stride:
+    """[..., columns] as rows of one stride: (rows, stride); the last axis is contiguous."""
+    shape, st = t.shape, t.stride()
+    if st[-1] != 1 and shape[-1] > 1:
+        raise ValueError("expected rows whose last axis is contiguous")
+    if len(shape) == 2:
+        return shape[0], st[0]
+    if len(shape) < 2:
+        return 1, shape[-1]
+    rows, stride = shape[-2], st[-2]
+    for k in range(len(shape) - 3, -1, -1):
+        if shape[k] != 1 and rows != 1 and st[k] != rows * stride:
             raise ValueError("expected rows at one stride")
         if rows == 1:
-            stride = t.stride(k)
-        rows *= t.shape[k]
+            stride = st[k]
+        rows *= shape[k]
     return rows, stride
 
 
 def _norm_desc(x, res_dtype, weight, eps, e4m3, group):
     """(packed fft_norm_desc, device, columns, row stride of x)."""
     code, dev = _first(x, "x")
-    d = x.shape[-1]
-    if x.stride(-1) != 1 and d > 1:
-        _tell(x, dev, x.dtype, x.shape, "x")
     rows, stride = _rows(x)
-    ptype = weight.dtype
+    d, ptype = x.shape[-1], weight.dtype
     if ptype is not x.dtype and ptype is not torch.float32:
         raise TypeError("weight: expected float32 or the type of x")
     desc = _NORM.pack(code, _CODES.get(res_dtype, -1), F32 if ptype is torch.float32 else code,
@@ -464,32 +480,37 @@ def residual_norm(x, weight, residual=None, eps=1e-6, out_dtype=None, group=0, o
     if _L is None:
         _setup()
     dtype, shape = x.dtype, x.shape
-    e4m3 = out_dtype is not None and out_dtype is not dtype
-    if e4m3 and out_dtype is not torch.float8_e4m3fn:
+    otype = dtype if out_dtype is None else out_dtype
+    e4m3 = otype is not dtype
+    if e4m3 and otype is not torch.float8_e4m3fn:
         raise TypeError("out_dtype: expected the type of x or torch.float8_e4m3fn")
     res_dtype = dtype if residual is None else residual.dtype
-    group = int(group)
     desc, dev, d, xs = _norm_desc(x, res_dtype, weight, eps, e4m3, group)
-    rp = rs = ts = 0
+    rp = rs = 0
     if residual is not None:
-        _need(residual, dev, res_dtype, shape, "residual")
+        if residual.shape != shape or residual.get_device() != dev:
+            _tell(residual, dev, res_dtype, shape, "residual")
         rp, rs = residual.data_ptr(), _rows(residual)[1]
     on, s = _stream(stream, dev)
     with on:
-        otype = out_dtype if e4m3 else dtype
         if out is None:
-            out = x.new_empty(shape, dtype=otype)
+            out, os = x.new_empty(shape, dtype=otype), d
         else:
-            _need(out, dev, otype, shape, "out")
-        scale = total = None
+            os = _rows(_need(out, dev, otype, shape, "out"))[1]
+        scale = total = sp = tp = None
+        ts = d
         if e4m3:
             groups = -(-d // group) if group > 0 else 1
             scale = x.new_empty((*shape[:-1], groups), dtype=torch.float32)
+            sp = scale.data_ptr()
         if residual is not None:
-            total = residual if inplace_residual else x.new_empty(shape, dtype=res_dtype)
-            ts = _rows(total)[1]
-        _check(_L.fft_norm_forward(desc, x.data_ptr(), xs, rp, rs, out.data_ptr(), _rows(out)[1],
-                                   _ptr(scale), _ptr(total), ts, s), "fft_norm_forward")
+            if inplace_residual:
+                total, tp, ts = residual, rp, rs
+            else:
+                total = x.new_empty(shape, dtype=res_dtype)
+                tp = total.data_ptr()
+        rc = _L.fft_norm_forward(desc, x.data_ptr(), xs, rp, rs, out.data_ptr(), os, sp, tp, ts, s)
+    _check(rc, "fft_norm_forward")
     return NormOut(out, scale, total)
 
 
