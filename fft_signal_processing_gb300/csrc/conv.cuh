@@ -4,7 +4,7 @@
 //   dp = dout * act'(p);  dx[t] = sum_k weight[k] dp[t+(W-1)-k]
 //   dweight[k] = sum_t dp[t] x[t-(W-1)+k];  dbias = sum_t dp[t]
 //
-// A thread holds VEC neighbouring channels (8 bytes) and walks a run of 64 tokens with the last W-1
+// A thread holds VEC neighbouring channels (8 bytes) and walks a run of up to 64 tokens with the last W-1
 // inputs (and, backward, the last W-1 dp) in registers, so a run reads its rows once and W-1
 // (backward 2(W-1)) rows of halo.  Channels go in pairs, two float32 operations to an
 // instruction.  Tokens go by fours: their rows come by asynchronous copies into the thread's own
@@ -146,8 +146,8 @@ __global__ void __launch_bounds__(kConvThreads) k_conv_fwd(const ConvArgs a) {
         return;
     }
     const int64_t row = tile / a.ttiles;
-    const int64_t b = (tile - row * a.ttiles) * kConvTile + (int64_t)threadIdx.y * kConvRun;
-    const int64_t e = b + kConvRun < a.d.length ? b + kConvRun : a.d.length;
+    const int64_t b = ((tile - row * a.ttiles) * kConvRuns + threadIdx.y) * a.run;
+    const int64_t e = b + a.run < a.d.length ? b + a.run : a.d.length;
     if (b >= e) return;  // a warp is one run
     SeqAt s = seq_at(a.d.offsets, a.d.nseq, a.d.length, row, b);
     if (c >= a.d.channels) return;
@@ -297,8 +297,8 @@ __global__ void __launch_bounds__(kConvThreads) k_conv_bwd(const ConvArgs a) {
         return;
     }
     const int64_t row = tile / a.ttiles;
-    const int64_t b = (tile - row * a.ttiles) * kConvTile + (int64_t)threadIdx.y * kConvRun;
-    const int64_t e = b + kConvRun < a.d.length ? b + kConvRun : a.d.length;
+    const int64_t b = ((tile - row * a.ttiles) * kConvRuns + threadIdx.y) * a.run;
+    const int64_t e = b + a.run < a.d.length ? b + a.run : a.d.length;
     Pairs<VEC> dw[W], db = zeros<VEC>();
 #pragma unroll
     for (int i = 0; i < W; ++i) dw[i] = zeros<VEC>();
@@ -471,7 +471,8 @@ template <class T, int VEC, int W>
 cudaError_t conv_launch(ConvArgs a, bool backward, cudaStream_t s) {
     const int64_t rows = a.d.offsets ? 1 : a.d.nseq;
     a.ctiles = (a.d.channels + kConvLanes * VEC - 1) / (kConvLanes * VEC);
-    a.ttiles = (a.d.length + kConvTile - 1) / kConvTile;
+    a.run = conv_run_tokens(a.d, backward);
+    a.ttiles = (a.d.length + kConvRuns * a.run - 1) / (kConvRuns * a.run);
     const bool states = W > 1 && (backward ? a.dinitial : a.final_state) != nullptr;
     const int64_t blocks = a.ctiles * (rows * a.ttiles + (states ? a.d.nseq : 0));
     if (blocks < 1) return cudaSuccess;

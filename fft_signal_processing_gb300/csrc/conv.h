@@ -13,12 +13,35 @@ struct ConvArgs {
     void* dinitial;     // backward, or null
     float* parts;       // backward: partial sums [token tiles][(width + 1) * channels], or null
     int64_t ctiles, ttiles;  // channel tiles; token tiles per row
+    int run;                 // tokens of a run
 };
 
 // A block has 32 lanes along the channels and 8 runs of tokens; the runs of a block are its token
 // tile (one partial row of the parameter gradients).
-constexpr int kConvLanes = 32, kConvRuns = 8, kConvRun = 64;
-constexpr int kConvTile = kConvRuns * kConvRun;
+constexpr int kConvLanes = 32, kConvRuns = 8;
+constexpr int kConvMaxRun = 64;
+
+// Tokens of a run: of 64 and less, the number whose rounds of resident blocks (three to an SM
+// forward, two backward) take the fewest tokens' time, with the halo and about 8 tokens to start.
+// 16001 tokens of 2000 channels, backward: 56.
+inline int conv_run_tokens(const fft_conv_desc& d, bool backward) {
+    const int64_t lanes = d.dtype == FFT_F32 ? 2 : 4;  // channels of a lane
+    const int64_t ctiles = (d.channels + kConvLanes * lanes - 1) / (kConvLanes * lanes);
+    const int64_t rows = d.offsets ? 1 : d.nseq, resident = (int64_t)num_sms() * (backward ? 2 : 3);
+    int64_t best = INT64_MAX;
+    int run = kConvMaxRun;
+    // forward, many rounds of full runs: shorter ones only read more halo
+    if (!backward && ctiles * rows * (d.length / (kConvRuns * run)) >= 2 * resident) return run;
+    for (int r = kConvMaxRun; r >= 16; r -= 4) {
+        const int64_t blocks = ctiles * rows * ((d.length + kConvRuns * r - 1) / (kConvRuns * r));
+        const int64_t cost = (blocks + resident - 1) / resident * (r + 2 * (d.width - 1) + 8);
+        if (cost < best) {
+            best = cost;
+            run = r;
+        }
+    }
+    return run;
+}
 
 cudaError_t conv_forward_f32(ConvArgs a, cudaStream_t s);
 cudaError_t conv_forward_bf16(ConvArgs a, cudaStream_t s);

@@ -58,7 +58,8 @@ int check_conv(const fft_conv_desc* d, bool pointers) {
 }
 
 int64_t conv_tiles(const fft_conv_desc& d) {
-    return (d.offsets ? 1 : d.nseq) * ((d.length + kConvTile - 1) / kConvTile);
+    const int64_t tile = kConvRuns * conv_run_tokens(d, true);
+    return (d.offsets ? 1 : d.nseq) * ((d.length + tile - 1) / tile);
 }
 
 int check_scan(const fft_scan_desc* d, bool pointers) {
