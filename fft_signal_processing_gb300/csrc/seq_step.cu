@@ -1,6 +1,9 @@
 // Single tokens of the sequence operators (fft_conv_step, fft_scan_step): every sequence reads
 // its state from a slot of a pool, takes one token and writes the new state to a slot.  Both are
-// bound by the state's bytes for many sequences and by latency for one.
+// bound by the state's bytes for many sequences and by latency for one.  Measured: scan of 256
+// sequences of 4096 channels and 16 states 39 us, 3.7 TB/s (54% of the copy rate: two dependent
+// trips, slot then state); one sequence of 2048 channels 4.8 us on the GPU, 17 us with the host
+// side of the call; convolution of one sequence of 4096 channels 5.4 and 18 us.
 #include "seq_step.h"
 
 namespace gbfft {

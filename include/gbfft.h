@@ -22,6 +22,10 @@
  * detected on the host before anything is enqueued.  There is no CPU fallback: if the device
  * or the kernels are unavailable the call fails with FFT_ERR_CUDA.
  *
+ * Beside the transforms, which are plans, stand the sequence operators (fft_conv_*, fft_scan_*,
+ * fft_norm_*, further down): filters along the tokens of a sequence whose coefficients change from
+ * token to token, so that no spectrum describes them.  They need no plan.
+ *
  * Thread-safety: distinct plans may be used concurrently.  One plan must not be executed on
  * two streams at the same time (its workspace is shared by its executions).
  */
@@ -338,7 +342,8 @@ int fft_shift(const void* in, void* out, int64_t nx, int64_t ny, int64_t batch, 
  * such layers.  They need no plan: the caller passes descriptors, device pointers and, where a
  * *_workspace function says so, a workspace that is in use until the call's kernels have run.
  * The calls validate on the host, enqueue kernels on `stream` and return; they allocate nothing,
- * never synchronise and can be captured into a graph.  Repeated calls give the same bits.
+ * never synchronise and can be captured into a graph.  Repeated calls give the same bits.  Calls
+ * may overlap on different streams and threads if their workspaces and outputs are apart.
  *
  * Data types: u, x, z, outputs and their gradients are all of the descriptor's dtype (FFT_F32,
  * FFT_BF16 or FFT_F16).  All arithmetic, states of the scan, gradients of parameters and
@@ -352,7 +357,8 @@ int fft_shift(const void* in, void* out, int64_t nx, int64_t ny, int64_t batch, 
  *                    `length` tokens (seq_stride is not used).  Empty sequences are allowed.
  *                    Offsets that break the rule give undefined outputs, but no access outside
  *                    the tensors.
- * Row strides of outputs must not make rows overlap.  data needs only the alignment of its type;
+ * Row strides of outputs must not make rows overlap; a tok_stride is at most 2^26 and a
+ * length below 2^31 - 65536 (else FFT_ERR_UNSUPPORTED_SIZE).  data needs only the alignment of its type;
  * 16-byte aligned rows are faster.  A NULL data pointer means the tensor is absent where that is
  * allowed. */
 enum { FFT_F32 = 0, FFT_BF16 = 1, FFT_F16 = 2, FFT_E4M3 = 3 };
