@@ -316,7 +316,8 @@ __global__ void __launch_bounds__(kConvThreads) k_conv_bwd(const ConvArgs a) {
         const T* x = x0 + b * xs;  // rows count from the run's start
         const T* dout = static_cast<const T*>(a.dout.data) + base * a.dout.seq_stride + b * gs + c;
         const int len = (int)(e - b), all = len + W - 1;  // own tokens, and with the halo
-        const int there = a.d.length - b < all ? (int)(a.d.length - b) : all;  // that exist
+        const int fours = (all + N - 1) / N * N;
+        const int there = a.d.length - b < fours ? (int)(a.d.length - b) : fours;  // that exist
         const T* nextx = x;
         const T* nextg = dout;
         auto ahead = [&](int four) {
@@ -349,7 +350,8 @@ __global__ void __launch_bounds__(kConvThreads) k_conv_bwd(const ConvArgs a) {
                 dps[W - 1 + j].v[p] = act_grad(v, g.v[p], a.d.silu);
             }
         };
-        auto params = [&](int j) {
+        auto params = [&](int j, bool own) {
+            if (!own) return;
 #pragma unroll
             for (int p = 0; p < P; ++p) {
                 db.v[p] = add2(db.v[p], dps[W - 1 + j].v[p]);
@@ -383,8 +385,8 @@ __global__ void __launch_bounds__(kConvThreads) k_conv_bwd(const ConvArgs a) {
                 return ld_pack<VEC>(dout + (i + j) * gs);
             };
             const int64_t t0 = b + i;
-            if (i >= W - 1 && t0 - (W - 1) >= s.begin && i + N <= len && t0 + N <= s.end) {
-                // inside one sequence, and so are the tokens whose dx leaves
+            if ((i == 0 || t0 - (W - 1) >= s.begin) && i + N <= there && t0 + N <= s.end) {
+                // inside one sequence, and so are the tokens whose dx leaves (those of the run)
                 Pack<T, VEC> nx[N], ng[N];
 #pragma unroll
                 for (int j = 0; j < N; ++j) {
@@ -396,7 +398,7 @@ __global__ void __launch_bounds__(kConvThreads) k_conv_bwd(const ConvArgs a) {
 #pragma unroll
                 for (int j = 0; j < N; ++j) {
                     grad(j, widen<T, VEC>(ng[j]));
-                    params(j);
+                    params(j, i + j < len);
                 }
                 if (dx) {
                     T* o = dx + (t0 - (W - 1)) * os;
@@ -408,7 +410,7 @@ __global__ void __launch_bounds__(kConvThreads) k_conv_bwd(const ConvArgs a) {
 #pragma unroll
                             for (int k = 0; k < W; ++k)
                                 y.v[p] = fma2(w[W - 1 - k].v[p], dps[j + k].v[p], y.v[p]);
-                        st_pack<VEC>(o + j * os, narrow<T, VEC>(y));
+                        if (i + j >= W - 1 && i + j < all) st_pack<VEC>(o + j * os, narrow<T, VEC>(y));
                     }
                 }
                 slide(N);
@@ -426,7 +428,7 @@ __global__ void __launch_bounds__(kConvThreads) k_conv_bwd(const ConvArgs a) {
                     }
                     win[W - 1] = widen<T, VEC>(x_at(j));
                     grad(0, widen<T, VEC>(g_at(j)));
-                    if (t < e) params(0);
+                    params(0, t < e);
                 }
                 const int64_t td = t - (W - 1);  // dx[td] = sum_k weight[W-1-k] dp[td + k]
                 if (td >= b && dx) {

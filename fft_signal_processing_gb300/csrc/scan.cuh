@@ -214,14 +214,16 @@ struct ScanPairSmem {
 // Up to 16 states: a thread holds all SPT states of two neighbouring channels.  Tiles of 8
 // tokens: u, delta and z come by asynchronous copies two tiles ahead, B and C a tile ahead
 // through registers, double buffered in shared memory as float32: one barrier per tile.
-// A pair of states beyond n is left out, and the odd one of a last pair kept at 0 (its B is 0, but
-// u may be infinite).  FAST: n == SPT and all rows are whole 16-byte accesses, the usual case,
+// SPT is n rounded up to fours; a state beyond n is kept at 0 (its B is 0, but u may be infinite).
+// FAST: n == SPT and all rows are whole 16-byte accesses, the usual case,
 // whose code is free of these questions.
 template <class T, int SPT, int PASS, bool FAST>
 __global__ void __launch_bounds__(kPairThreads, 6) k_scan(const ScanArgs a) {
     using M = ScanPairSmem<T, SPT, PASS>;
     constexpr int NT = kPairThreads, CT = kPairChannels, TK = kPairTile, ST = M::kStages;
     constexpr bool SUMMARY = PASS == SCAN_SUMMARY, OUTPUT = PASS == SCAN_OUTPUT;
+    // fours below this one lie within n; the backward pass's 16 may stand for as few as nine
+    constexpr int WHOLE = SPT == 16 && !OUTPUT ? 2 : SPT / 4 - 1;
     extern __shared__ float4 smem4[];
     T* raw = reinterpret_cast<T*>(smem4);  // [stage][tensor][token][channel]
     float* sbc = reinterpret_cast<float*>(reinterpret_cast<char*>(smem4) + M::kBytesRaw);
@@ -355,11 +357,13 @@ __global__ void __launch_bounds__(kPairThreads, 6) k_scan(const ScanArgs a) {
                         const float2 b = p ? make_float2(b4.z, b4.w) : make_float2(b4.x, b4.y);
 #pragma unroll
                         for (int k = 0; k < 2; ++k) {
-                            if (!FAST && 4 * i + 2 * p >= n) continue;
                             float2& hh = h[k][2 * i + p];
                             const float2 e = mul2(dd[k], A2[k][2 * i + p]);
                             hh = fma2(make_float2(ex2(e.x), ex2(e.y)), hh, mul2(dv[k], b));
-                            if (!FAST && 4 * i + 2 * p + 1 >= n) hh.y = 0.f;
+                            if (!FAST && i >= WHOLE) {
+                                if (4 * i + 2 * p >= n) hh.x = 0.f;
+                                if (4 * i + 2 * p + 1 >= n) hh.y = 0.f;
+                            }
                             if (OUTPUT)
                                 acc[k][p] = fma2(p ? make_float2(c4.z, c4.w) : make_float2(c4.x, c4.y),
                                                  hh, acc[k][p]);
@@ -767,6 +771,9 @@ cudaError_t scan_run(ScanArgs a, cudaStream_t s) {
     a.vec = all_on(16) ? 16 : (all_on(4) ? 4 : 0);
     a.wide = rows_on(a.d.B, 16) && rows_on(a.d.C, 16) && a.d.states * sizeof(T) % 16 == 0;
     a.pair = dg % 2 == 0 && rows_on(a.out, 2 * sizeof(T));
+    // nine to twelve states: the backward pass keeps rows of 16
+    if (PASS == SCAN_OUTPUT && a.sl == 0 && scan_out_np(a.d.states) == 12)
+        return scan_fast<T, 12, 0, SCAN_OUTPUT>(a, s);
     switch (scan_np(a.d.states) * 100 + a.sl) {
         case 400: return scan_fast<T, 4, 0, PASS>(a, s);
         case 800: return scan_fast<T, 8, 0, PASS>(a, s);

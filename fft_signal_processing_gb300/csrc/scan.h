@@ -12,6 +12,8 @@ inline int scan_np(int64_t n) {
     while (np < n) np *= 2;
     return np;
 }
+// The same in the forward call, whose kernel also comes for twelve states.
+inline int scan_out_np(int64_t n) { return n > 8 && n <= 12 ? 12 : scan_np(n); }
 constexpr int kScanThreads = 128;
 constexpr int kScanTile = 16;  // the backward pass restarts at these tiles
 // Channels of a block of 64 threads: two per thread (sl 0), or sl lanes per channel.

@@ -99,7 +99,7 @@ int64_t scan_layout(const fft_scan_desc& d, ScanArgs* a, char* w) {
     };
     if (b.nchunks > 1) {
         const int64_t ch = b.rows * b.nchunks;
-        b.carry = reinterpret_cast<float*>(take(ch * d.channels * scan_np(d.states) * 4));
+        b.carry = reinterpret_cast<float*>(take(ch * d.channels * scan_out_np(d.states) * 4));
         b.dsum = reinterpret_cast<float*>(take(ch * d.channels * 4));
         b.reset = reinterpret_cast<int*>(take(ch * 4));
     }
@@ -126,7 +126,7 @@ void scan_plan(ScanArgs* a) {
     // k_scan for every SM (one sequence of 16384 x 2048: 0.28 ms at 4 to 6, 0.33 ms at 5 or 8).
     const int64_t sms = num_sms();
     int64_t k = 1;
-    if ((np == 8 || np == 16) && blocks(2) >= sms * 4)
+    if ((np == 8 || np == 16) && scan_out_np(d.states) != 12 && blocks(2) >= sms * 4)
         a->sl = 2;
     else
         k = (sms * 6 + blocks(a->sl) / 2) / blocks(a->sl);

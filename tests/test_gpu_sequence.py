@@ -231,7 +231,9 @@ SCANS = [  # d, n, groups, dtype, gate, initial, strided
     (6, 1, 2, "f32", False, True, True), (130, 4, 1, "f16", True, True, True),
     (21, 5, 3, "f32", True, True, False), (10, 8, 2, "bf16", False, False, True),
     (9, 24, 1, "f32", True, True, True), (5, 64, 1, "f32", False, True, False),
-    (4, 100, 2, "f32", True, True, True), (3, 128, 1, "bf16", True, False, False)]
+    (4, 100, 2, "f32", True, True, True), (3, 128, 1, "bf16", True, False, False),
+    (15, 10, 1, "f32", True, True, True), (16, 12, 2, "bf16", False, True, False),
+    (24, 13, 1, "f16", True, False, True), (128, 32, 1, "bf16", True, True, False)]
 
 
 @pytest.mark.parametrize("layout", LAYOUTS, ids=str)
@@ -294,10 +296,11 @@ def test_scan_no_tokens():
     assert torch.equal(g.dinitial_state, init) and (g.dweight == 0).all()
 
 
-def test_scan_infinite_and_missing_values():
+@pytest.mark.parametrize("n", [6, 10, 12, 16, 20])
+def test_scan_infinite_and_missing_values(n):
     """A NaN or infinity reaches its own channel from its token on, and a new sequence is clean;
     a state beyond n stays out of it."""
-    c = scan_data([30, 20], 8, 6, 1, torch.float32, gate=False, seed=7)
+    c = scan_data([30, 20], 8, n, 1, torch.float32, gate=False, seed=7)
     c["u"] = c["u"].clone()
     c["u"][10, 3] = float("nan")
     c["u"][12, 5] = float("inf")
@@ -407,6 +410,30 @@ def test_scan_in_a_graph():
     g.replay()
     torch.cuda.synchronize()
     assert torch.equal(got, want)
+
+
+def test_offsets_beyond_32_bits():
+    """Rows 2^22 elements apart: the later of 600 tokens lie more than 2^31 elements in."""
+    length, d, far = 600, 8, 1 << 22
+    wide = torch.empty(length * far, dtype=torch.bfloat16, device="cuda")
+    view = wide.as_strided((1, length, d), (length * far, far, 1))
+    c = scan_data((1, length), d, 16, 1, torch.bfloat16, strided=False, seed=16)
+    view.copy_(c["u"])
+    want, state = fx().selective_scan(**c, return_state=True)
+    out = wide.as_strided((1, length, d), (length * far, far, 1), far // 2)
+    got, end = fx().selective_scan(**{**c, "u": view}, out=out, return_state=True)
+    assert torch.equal(got, want) and torch.equal(end, state)
+    dout = torch.randn_like(want)
+    for a, b in zip(fx().selective_scan_backward(dout, **{**c, "u": view}),
+                    fx().selective_scan_backward(dout, **c)):
+        assert torch.equal(a, b)
+    w = torch.randn(d, 4, device="cuda")
+    assert torch.equal(fx().causal_conv(view, w, silu=True), fx().causal_conv(c["u"], w, silu=True))
+    for a, b in zip(fx().causal_conv_backward(dout, view, w), fx().causal_conv_backward(dout, c["u"], w)):
+        assert a is None or torch.equal(a, b)
+    got = fx().residual_norm(view[0], torch.ones(d, device="cuda"), residual=c["z"][0])
+    want = fx().residual_norm(c["u"][0], torch.ones(d, device="cuda"), residual=c["z"][0])
+    assert torch.equal(got.out, want.out) and torch.equal(got.residual, want.residual)
 
 
 # ---- residual norm --------------------------------------------------------------------------
