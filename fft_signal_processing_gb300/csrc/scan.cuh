@@ -579,11 +579,11 @@ __global__ void __launch_bounds__(kLanesThreads) k_scan_lanes(const ScanArgs a) 
 #pragma unroll 1
             for (int j0 = 0; j0 < TK; j0 += N) {
                 float2 d[(OWN + 1) / 2], du[(OWN + 1) / 2], uu[(OWN + 1) / 2];  // pairs of own tokens
-                const int own = j0 + sl * OWN;
+                const int own = j0 + sl;  // tokens own, own + SL, ...: apart in shared memory's banks
 #pragma unroll
                 for (int j = 0; j < OWN; ++j) {
-                    (j & 1 ? d[j / 2].y : d[j / 2].x) = to_f(rd[(own + j) * CT]) + bias;
-                    (j & 1 ? uu[j / 2].y : uu[j / 2].x) = to_f(ru[(own + j) * CT]);
+                    (j & 1 ? d[j / 2].y : d[j / 2].x) = to_f(rd[(own + j * SL) * CT]) + bias;
+                    (j & 1 ? uu[j / 2].y : uu[j / 2].x) = to_f(ru[(own + j * SL) * CT]);
                 }
                 if (OWN == 1) d[0].y = uu[0].y = 0.f;
 #pragma unroll
@@ -594,7 +594,7 @@ __global__ void __launch_bounds__(kLanesThreads) k_scan_lanes(const ScanArgs a) 
                 float y[N];
 #pragma unroll
                 for (int j = 0; j < N; ++j) {
-                    const int k = j % OWN, from = j / OWN * CL + ch;
+                    const int k = j / SL, from = j % SL * CL + ch;
                     const float dj = __shfl_sync(0xffffffffu, k & 1 ? d[k / 2].y : d[k / 2].x, from);
                     const float duj = __shfl_sync(0xffffffffu, k & 1 ? du[k / 2].y : du[k / 2].x, from);
                     if (SUMMARY) dsum += dj;
@@ -602,22 +602,23 @@ __global__ void __launch_bounds__(kLanesThreads) k_scan_lanes(const ScanArgs a) 
                 }
                 if (OUTPUT) {
 #pragma unroll
-                    for (int w = SL / 2, cnt = N / 2; w; w /= 2, cnt /= 2) {
+                    for (int w = 1, cnt = N / 2; w < SL; w *= 2, cnt /= 2) {
                         const bool up = sl & w;
 #pragma unroll
                         for (int j = 0; j < N / 2; ++j) {
                             if (j < cnt) {
-                                const float send = up ? y[j] : y[j + cnt], keep = up ? y[j + cnt] : y[j];
+                                const float send = up ? y[2 * j] : y[2 * j + 1];
+                                const float keep = up ? y[2 * j + 1] : y[2 * j];
                                 y[j] = keep + __shfl_xor_sync(0xffffffffu, send, w * CL);
                             }
                         }
                     }
                     T* o = out + (t + own) * ostr;
 #pragma unroll
-                    for (int j = 0; j < OWN; ++j, o += ostr) {
+                    for (int j = 0; j < OWN; ++j, o += SL * ostr) {
                         float v = fmaf(D, j & 1 ? uu[j / 2].y : uu[j / 2].x, y[j]);
                         if (gate) {
-                            const float z = to_f(rz[(own + j) * CT]);
+                            const float z = to_f(rz[(own + j * SL) * CT]);
                             v *= z * sigmoid(z);
                         }
                         if (live) *o = from_f<T>(v);
