@@ -13,7 +13,7 @@
 // go one by one.  2 (backward 3) values are moved per 2W (6W) operations: forward is bound by HBM
 // (4 x 4096 tokens of 4096 bfloat16 channels, W = 4: 51 us, 5.2 TB/s), backward by instruction
 // issue at the 16 warps of an SM that 125 registers allow (16001 packed tokens of 2000 channels:
-// 80 us, 2.4 TB/s, 2.0 instructions a cycle).  16 bytes a thread took so many registers that it
+// 78 us, 2.5 TB/s, 2.0 instructions a cycle).  16 bytes a thread took so many registers that it
 // was slower (78 and 107 us at the time, against 72 and 89), 4 bytes too many instructions (83,
 // 107).
 #pragma once
