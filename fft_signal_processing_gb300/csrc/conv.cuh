@@ -217,7 +217,7 @@ __global__ void __launch_bounds__(kConvThreads) k_conv_fwd(const ConvArgs a) {
             for (int j = 0; j < N && i + j < len; ++j) {
                 if (b + i + j >= s.end) {  // packed: the next sequence begins here
                     const int64_t q = s.q;
-                    seq_next(a.d.offsets, a.d.nseq, b + i + j, &s);
+                    seq_next(a.d.offsets, a.d.nseq, a.d.length, b + i + j, &s);
                     if (s.q != q) refill(b + i + j);
                 }
                 win[W - 1] = widen<T, VEC>(row_at(j));
@@ -423,7 +423,7 @@ __global__ void __launch_bounds__(kConvThreads) k_conv_bwd(const ConvArgs a) {
                 if (i + j < there) {
                     if (t >= s.end) {  // packed: the next sequence begins here
                         const int64_t q = s.q;
-                        seq_next(a.d.offsets, a.d.nseq, t, &s);
+                        seq_next(a.d.offsets, a.d.nseq, a.d.length, t, &s);
                         if (s.q != q) refill(t);
                     }
                     win[W - 1] = widen<T, VEC>(x_at(j));
@@ -432,7 +432,7 @@ __global__ void __launch_bounds__(kConvThreads) k_conv_bwd(const ConvArgs a) {
                 }
                 const int64_t td = t - (W - 1);  // dx[td] = sum_k weight[W-1-k] dp[td + k]
                 if (td >= b && dx) {
-                    if (td >= cur.end) seq_next(a.d.offsets, a.d.nseq, td, &cur);
+                    if (td >= cur.end) seq_next(a.d.offsets, a.d.nseq, a.d.length, td, &cur);
                     const int64_t end = cur.end < a.d.length ? cur.end : a.d.length;
                     Pairs<VEC> y = zeros<VEC>();
                     const int64_t fr = td + (W - 1) - end;  // row of the final state that td is

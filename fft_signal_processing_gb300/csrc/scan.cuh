@@ -407,7 +407,7 @@ __global__ void __launch_bounds__(kPairThreads, 6) k_scan(const ScanArgs a) {
             while (j < tl) {
                 if (at + j >= sq.end) {  // packed: the next sequence begins
                     const int64_t q = sq.q;
-                    seq_next(a.d.offsets, a.d.nseq, at + j, &sq);
+                    seq_next(a.d.offsets, a.d.nseq, a.d.length, at + j, &sq);
                     if (sq.q != q) {
                         initial();
                         has_reset = true;
@@ -631,7 +631,7 @@ __global__ void __launch_bounds__(kLanesThreads) k_scan_lanes(const ScanArgs a) 
             while (j < tl) {
                 if (at + j >= sq.end) {  // packed: the next sequence begins
                     const int64_t q = sq.q;
-                    seq_next(a.d.offsets, a.d.nseq, at + j, &sq);
+                    seq_next(a.d.offsets, a.d.nseq, a.d.length, at + j, &sq);
                     if (sq.q != q) {
                         initial();
                         has_reset = true;
