@@ -284,8 +284,8 @@ __global__ void __launch_bounds__(kPairThreads, 6) k_scan(const ScanArgs a) {
                              0, n, h[k]);
     };
     const int64_t carry_at = ((blk.row * a.nchunks + blk.chunk) * a.d.channels + c) * SPT;
-    bool has_reset = sq.begin == blk.t0;
-    if (sq.begin == blk.t0) {
+    bool has_reset = starts_at(sq, blk.t0);
+    if (has_reset) {
         initial();
     } else {
 #pragma unroll
@@ -516,8 +516,8 @@ __global__ void __launch_bounds__(kLanesThreads) k_scan_lanes(const ScanArgs a) 
                              ? a.d.initial_state + (sq.q * a.d.channels + c) * n : nullptr, s0, n, h);
     };
     const int64_t carry_at = ((blk.row * a.nchunks + blk.chunk) * a.d.channels + c) * NP;
-    bool has_reset = sq.begin == blk.t0;
-    if (sq.begin == blk.t0)
+    bool has_reset = starts_at(sq, blk.t0);
+    if (has_reset)
         initial();
     else if (!SUMMARY && live)
         load_row<SPT>(a.carry + carry_at + s0, h);

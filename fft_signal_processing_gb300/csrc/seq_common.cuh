@@ -229,6 +229,13 @@ __host__ __device__ __forceinline__ void seq_next(const int64_t* offsets, int64_
     }
 }
 
+// Whether the state of a scan starts anew at token t of its row: at a sequence's first token and,
+// where offsets leave the first tokens to no sequence, at the row's.  (A chunk's own start state
+// exists only where time is cut.)
+__host__ __device__ __forceinline__ bool starts_at(const SeqAt& s, int64_t t) {
+    return t == 0 || s.begin == t;
+}
+
 // Sums over parts, the last step of a parameter gradient, in an order that does not depend on the
 // launch: column k * chan + c of parts[p * stride + column] (cols of them) goes to
 // out[c * (cols / chan) + k].  No parts: zeros.

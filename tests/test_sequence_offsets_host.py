@@ -22,11 +22,16 @@ int main(int argc, char** argv) {
     std::vector<int64_t> o;
     for (int i = 5; i < argc; ++i) o.push_back(atoll(argv[i]));
     const int64_t* offsets = o.data();
+    int goes_on = 0;
     for (int64_t t0 = 0; t0 < length; t0 += chunk) {
         const int64_t t1 = t0 + chunk < length ? t0 + chunk : length, len = t1 - t0;
         int64_t below = 0;  // as warp_count_le counts on ascending values
         while (below <= nseq && offsets[below] <= t0) ++below;
         SeqAt sq = seq_span(offsets, nseq, length, below - 1);
+        if (!starts_at(sq, t0)) {  // the chunk goes on from the state that the one before left
+            if (t0 == 0) return 3;
+            ++goes_on;
+        }
         for (int64_t t = 0; t < len; t += tile) {
             const int64_t at = t0 + t;
             if (sq.q < 0 || sq.q >= nseq) return 2;
@@ -44,6 +49,7 @@ int main(int argc, char** argv) {
             }
         }
     }
+    fprintf(stderr, "%d", goes_on);
     return 0;
 }
 """
@@ -63,7 +69,7 @@ def walk(tmp_path_factory):
         r = subprocess.run([str(exe), *map(str, (length, chunk, tile, len(offsets) - 1, *offsets))],
                            capture_output=True, text=True)
         assert r.returncode == 0
-        return [int(v) for v in r.stdout.split()]
+        return [int(v) for v in r.stdout.split()], int(r.stderr)
 
     return run
 
@@ -79,4 +85,17 @@ OFFSETS = [
 @pytest.mark.parametrize("chunk", [64, 1000])
 @pytest.mark.parametrize("tile", [8, 16])
 def test_every_token_of_the_row_and_none_beyond(walk, length, offsets, chunk, tile):
-    assert walk(length, chunk, tile, offsets) == list(range(length))
+    tokens, _ = walk(length, chunk, tile, offsets)
+    assert tokens == list(range(length))
+
+
+@pytest.mark.parametrize("length,offsets", OFFSETS, ids=str)
+def test_a_row_that_is_not_cut_reads_no_chunk_state(walk, length, offsets):
+    """There is none then: also not where no sequence holds the first token."""
+    assert walk(length, 1000, 8, offsets)[1] == 0
+
+
+def test_chunks_go_on_inside_sequences(walk):
+    assert walk(200, 64, 8, [0, 200])[1] == 3
+    assert walk(200, 64, 8, [0, 64, 128, 192, 200])[1] == 0
+    assert walk(200, 64, 8, [0, 65, 128, 200])[1] == 2
