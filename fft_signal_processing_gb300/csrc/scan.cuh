@@ -673,6 +673,15 @@ __global__ void __launch_bounds__(kLanesThreads) k_scan_lanes(const ScanArgs a) 
     }
 }
 
+// A state h carried over a chunk that takes it to exp2(x) h + local.  Steps below zero make states
+// grow, and exp2(x) may then be infinite where the product is not: with h = 0, nothing has grown, and
+// small states are multiplied in two steps.
+__device__ __forceinline__ float carried(float x, float h, float local) {
+    if (x <= 126.f) return fmaf(ex2(x), h, local);
+    const float e = ex2(0.5f * x);
+    return h == 0.f ? local : fmaf(e, e * h, local);
+}
+
 // Few threads and a chain of chunks: small blocks on many SMs, and many chunks loaded at once.
 constexpr int kCarryThreads = 64, kCarryAhead = 16;
 
@@ -704,7 +713,7 @@ __global__ void __launch_bounds__(kCarryThreads) k_scan_carry(const ScanArgs a) 
         for (int j = 0; j < U; ++j) {
             if (k + j >= a.nchunks) break;
             carry[(k + j) * per] = h;
-            h = cut[j] ? local[j] : fmaf(ex2(A2 * sum[j]), h, local[j]);
+            h = cut[j] ? local[j] : carried(A2 * sum[j], h, local[j]);
         }
     }
 }

@@ -285,7 +285,7 @@ __global__ void __launch_bounds__(kCarryThreads) k_scan_back_carry(const ScanBwd
         for (int j = 0; j < U; ++j) {
             if (k - j < 0) break;
             carry[(k - j) * per] = m;
-            m = cut[j] ? local[j] : fmaf(ex2(A2 * sum[j]), m, local[j]);
+            m = cut[j] ? local[j] : carried(A2 * sum[j], m, local[j]);
         }
     }
 }
