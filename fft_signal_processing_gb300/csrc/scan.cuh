@@ -358,8 +358,7 @@ __global__ void __launch_bounds__(kPairThreads, 6) k_scan(const ScanArgs a) {
 #pragma unroll
                         for (int k = 0; k < 2; ++k) {
                             float2& hh = h[k][2 * i + p];
-                            const float2 e = mul2(dd[k], A2[k][2 * i + p]);
-                            hh = fma2(make_float2(ex2(e.x), ex2(e.y)), hh, mul2(dv[k], b));
+                            hh = fma2(decay2(dd[k], A2[k][2 * i + p]), hh, mul2(dv[k], b));
                             if (!FAST && i >= WHOLE) {
                                 if (4 * i + 2 * p >= n) hh.x = 0.f;
                                 if (4 * i + 2 * p + 1 >= n) hh.y = 0.f;
@@ -560,8 +559,7 @@ __global__ void __launch_bounds__(kLanesThreads) k_scan_lanes(const ScanArgs a) 
 #pragma unroll
                 for (int p = 0; p < 2; ++p) {
                     float2& hh = h[2 * i + p];
-                    const float2 e = mul2(dd, A2[2 * i + p]);
-                    hh = fma2(make_float2(ex2(e.x), ex2(e.y)), hh,
+                    hh = fma2(decay2(dd, A2[2 * i + p]), hh,
                               mul2(dv, p ? make_float2(b4.z, b4.w) : make_float2(b4.x, b4.y)));
                     if (!FAST) {
                         if (s0 + 4 * i + 2 * p >= n) hh.x = 0.f;

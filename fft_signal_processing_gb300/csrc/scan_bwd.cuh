@@ -145,9 +145,8 @@ __global__ void __launch_bounds__(kPairThreads) k_scan_back_pair(const ScanBwdAr
 #pragma unroll
                     for (int k = 0; k < 2; ++k) {
                         float2& mm = m[k][2 * i + p];
-                        const float2 e = mul2(dd[k], A2[k][2 * i + p]);
                         const float2 q = fma2(yy[k], p ? make_float2(c4.z, c4.w) : make_float2(c4.x, c4.y), mm);
-                        mm = mul2(make_float2(ex2(e.x), ex2(e.y)), q);
+                        mm = mul2(decay2(dd[k], A2[k][2 * i + p]), q);
                     }
             }
             if (start) {
@@ -245,9 +244,8 @@ __global__ void __launch_bounds__(kScanThreads) k_scan_back(const ScanBwdArgs a)
             const bool start = t + j == sq.begin;
 #pragma unroll
             for (int i = 0; i < SPT / 2; ++i) {
-                const float2 arg = mul2(dd, A2[i]);
                 const float2 q = fma2(yy, *reinterpret_cast<const float2*>(&sC[j][s0 + 2 * i]), m[i]);
-                m[i] = mul2(make_float2(ex2(arg.x), ex2(arg.y)), q);
+                m[i] = mul2(decay2(dd, A2[i]), q);
                 if (start) m[i] = make_float2(0.f, 0.f);
             }
         }
@@ -529,8 +527,7 @@ __global__ void __launch_bounds__(BwdShape<T, SL>::NT) k_scan_bwd(const ScanBwdA
                     const float2 b = k ? make_float2(b4.z, b4.w) : make_float2(b4.x, b4.y);
 #pragma unroll
                     for (int p = 0; p < 2; ++p) {
-                        const float2 e = mul2(dd[p], A2[s + k][p]);
-                        h[s + k][p] = fma2(make_float2(ex2(e.x), ex2(e.y)), h[s + k][p], mul2(du2[p], b));
+                        h[s + k][p] = fma2(decay2(dd[p], A2[s + k][p]), h[s + k][p], mul2(du2[p], b));
                         if (!FAST && s0 + s + k >= n) h[s + k][p] = splat(0.f);
                     }
                 }
@@ -596,9 +593,8 @@ __global__ void __launch_bounds__(BwdShape<T, SL>::NT) k_scan_bwd(const ScanBwdA
                         float2 db, dc;
 #pragma unroll
                         for (int p = 0; p < 2; ++p) {
-                            const float2 e = mul2(dd[p], A2[s][p]);
                             const float2 q = fma2(dy[p], c, m[s][p]);
-                            const float2 aq = mul2(make_float2(ex2(e.x), ex2(e.y)), q);
+                            const float2 aq = mul2(decay2(dd[p], A2[s][p]), q);
                             const float2 w = mul2(aq, hist[jj][s][p]);
                             yv[p] = fma2(c, hist[jj + 1][s][p], yv[p]);
                             qb[p] = fma2(q, b, qb[p]);

@@ -100,6 +100,17 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b) {
     return d;
 }
 __device__ __forceinline__ float2 splat(float v) { return make_float2(v, v); }
+// exp(d A) of two states, A2 = A log2(e).  ex2.approx lies low: for d A between -1e-6 and -4 its
+// results are on average 0.1 to 0.5 units of 2^-24 below the exponential, and a state that is kept
+// for a thousand tokens collects that a thousand times.  The shift of the argument costs no
+// instruction and takes the average to within 0.28 units (0.2 above -0.5).  Gradients of A, 4 x 2048
+// tokens of 2048 bfloat16 channels: off by 1.7e-6 without it, 0.8e-6 with it; at 2.5e-8 sequences of
+// 6000 tokens, whose slow states are kept longest, come out worse again (0.74e-6 against 0.96e-6).
+constexpr float kEx2Shift = 2e-8f;
+__device__ __forceinline__ float2 decay2(float2 d, float2 A2) {
+    const float2 e = fma2(d, A2, splat(kEx2Shift));
+    return make_float2(ex2(e.x), ex2(e.y));
+}
 __device__ __forceinline__ float max_nan(float a, float b) {  // a NaN stays
     float d;
     asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));

@@ -140,8 +140,7 @@ __global__ void __launch_bounds__(kThreads) k_scan_step(const ScanStepArgs a) {
         float2 acc = splat(0.f);
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-            const float2 e = mul2(splat(dk), mul2(A[k][i], splat(kLog2e)));
-            h[k][i] = fma2(make_float2(ex2(e.x), ex2(e.y)), h[k][i], mul2(splat(uk), b[i]));
+            h[k][i] = fma2(decay2(splat(dk), mul2(A[k][i], splat(kLog2e))), h[k][i], mul2(splat(uk), b[i]));
             if (!a.vec) {  // a state beyond n stays out of y where d u is infinite
                 if (s0 + 2 * i >= n) h[k][i].x = 0.f;
                 if (s0 + 2 * i + 1 >= n) h[k][i].y = 0.f;
