@@ -448,6 +448,27 @@ __global__ void __launch_bounds__(BwdShape<T, SL>::NT) k_scan_bwd(const ScanBwdA
         }
     };
 
+    // the sums over tokens go to partial row k and start anew
+    auto leave = [&](int64_t k) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int s = 0; s < 4; ++s) {
+                float& v = i & 1 ? dA[s][i / 2].y : dA[s][i / 2].x;
+                if (lc + i < width && s0 + s < n)
+                    a.pA[(k * a.d.channels + c0 + lc + i) * n + s0 + s] = v;
+                v = 0.f;
+            }
+#pragma unroll
+        for (int i = 0; i < OWN; ++i) {
+            if (owner && lo + i < width) {
+                a.pD[k * a.d.channels + c0 + lo + i] = aD[i];
+                a.pbias[k * a.d.channels + c0 + lo + i] = abias[i];
+            }
+            aD[i] = abias[i] = 0.f;
+        }
+    };
+
     for (int64_t tl = last_tile; tl >= t0; tl -= TK) {
         const int len = t1 - tl < TK ? (int)(t1 - tl) : TK;
         copy_wait<0>();
@@ -694,22 +715,9 @@ __global__ void __launch_bounds__(BwdShape<T, SL>::NT) k_scan_bwd(const ScanBwdA
             walk(Count<1>{});
         else
             walk(Count<0>{});
+        if ((tl - t0) % kScanPart == 0) leave(row * a.parts + chunk * a.cuts + (tl - t0) / kScanPart);
     }
     copy_wait<0>();
-    const int64_t part = row * a.f.nchunks + chunk;
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int s = 0; s < 4; ++s)
-            if (lc + i < width && s0 + s < n)
-                a.pA[(part * a.d.channels + c0 + lc + i) * n + s0 + s] =
-                    i & 1 ? dA[s][i / 2].y : dA[s][i / 2].x;
-#pragma unroll
-    for (int k = 0; k < OWN; ++k) {
-        if (!owner || lo + k >= width) continue;
-        a.pD[part * a.d.channels + c0 + lo + k] = aD[k];
-        a.pbias[part * a.d.channels + c0 + lo + k] = abias[k];
-    }
 }
 
 // dB and dC: the channel tiles' partial sums, added in order.
@@ -805,9 +813,9 @@ cudaError_t scan_bwd_run(ScanBwdArgs a, cudaStream_t s) {
     };
     a.f.vec = all_on(16) ? 16 : (all_on(4) ? 4 : 0);
     a.f.wide = rows_on(a.d.B, 16) && rows_on(a.d.C, 16) && a.d.states * sizeof(T) % 16 == 0;
-    const int64_t n = a.d.states, parts = a.f.rows * a.f.nchunks;
+    const int64_t n = a.d.states, parts = a.f.rows * a.parts;
     if (a.d.length > 0) {
-        if (parts * a.back_ctiles * a.d.groups > INT32_MAX) return cudaErrorInvalidValue;
+        if (a.f.rows * a.f.nchunks * a.back_ctiles * a.d.groups > INT32_MAX) return cudaErrorInvalidValue;
         e = scan_run<T, SCAN_TILES>(a.f, s);
         if (e == cudaSuccess && a.f.nchunks > 1) {
             switch (scan_np(n)) {

@@ -6,15 +6,20 @@
 
 namespace gbfft {
 
+// Tokens whose dA, dD and ddelta_bias one float32 accumulator adds up.  A sum of T terms one after
+// another is off by some sqrt(T) / 4 units of 2^-24, and chunks may be as long as the row.
+constexpr int kScanPart = 256;
+
 struct ScanBwdArgs {
     fft_scan_desc d;
     fft_scan_grads g;
     ScanArgs f;        // the forward passes (carry, dsum, reset, tiles)
     float* carry;      // gradient that enters every chunk from behind [rows][chunks][channels][np]
     float* bc;         // partial dB, dC [channel tiles][rows][length][groups][2][states]
-    float* pA;         // partial dA [rows * chunks][channels * states]
-    float* pD;         // partial dD [rows * chunks][channels]
-    float* pbias;      // partial ddelta_bias [rows * chunks][channels]
+    float* pA;         // partial dA [rows * parts][channels * states]
+    float* pD;         // partial dD [rows * parts][channels]
+    float* pbias;      // partial ddelta_bias [rows * parts][channels]
+    int64_t cuts, parts;  // partial rows of a chunk, kScanPart tokens each, and of a row
     int64_t ctiles;    // channel tiles per group of the main kernel
     int64_t back_ctiles;  // and of the pass that finds what the chunks send back
 };

@@ -170,6 +170,8 @@ int64_t scan_bwd_layout(const fft_scan_desc& d, ScanBwdArgs* a, char* w) {
         return p;
     };
     const int64_t per = d.channels * np, parts = rows * nchunks;
+    const int64_t cuts = (chunk + kScanPart - 1) / kScanPart;
+    const int64_t last = d.length - (nchunks - 1) * chunk;  // tokens of a row's last chunk
     ScanBwdArgs b = {};
     if (a) b = *a;
     b.ctiles = ctiles;
@@ -190,9 +192,11 @@ int64_t scan_bwd_layout(const fft_scan_desc& d, ScanBwdArgs* a, char* w) {
     }
     b.f.tiles = take(rows * state_tiles * per);
     b.bc = take(ctiles * rows * d.length * d.groups * 2 * n);
-    b.pA = take(parts * d.channels * n);
-    b.pD = take(parts * d.channels);
-    b.pbias = take(parts * d.channels);
+    b.cuts = cuts;
+    b.parts = nchunks ? (nchunks - 1) * cuts + (last + kScanPart - 1) / kScanPart : 0;
+    b.pA = take(rows * b.parts * d.channels * n);
+    b.pD = take(rows * b.parts * d.channels);
+    b.pbias = take(rows * b.parts * d.channels);
     if (a) *a = b;
     return at;
 }

@@ -60,3 +60,35 @@ def test_steps_of_zero_keep_the_state(n, nseq, d):
     pool = state.clone()
     fx.selective_scan_step(pool, randn(rng, nseq, d), zero[:, 0], A, B[:, 0], B[:, 0])
     assert torch.equal(pool, state)
+
+
+def test_sums_over_long_chunks():
+    """Sequences enough to fill the GPU, so that time is hardly cut: 4096 tokens enter dA, dD and the
+    bias's gradient.  A walk of 256 additions is 8 units of 2^-24, the terms' own roundings 4."""
+    import fft_signal_processing_gb300 as fx
+
+    g = torch.Generator("cuda").manual_seed(1)
+    nseq, length, d, n, some = 304, 4096, 128, 4, 8
+
+    def rand(*shape):
+        return torch.randn(*shape, device="cuda", generator=g)
+
+    u, delta, dout = (rand(nseq, length, d) for _ in range(3))
+    B, C = rand(nseq, length, 1, n), rand(nseq, length, 1, n)
+    A = -torch.rand(d, n, device="cuda", generator=g) * 2 - 0.5
+    D, bias = rand(d), rand(d) * 0.1 - 1.0
+    got = fx.selective_scan_backward(dout, u, delta, A, B, C, D=D, delta_bias=bias, softplus=True)
+    v = [A[:some].double().requires_grad_(True), D[:some].double().requires_grad_(True),
+         bias[:some].double().requires_grad_(True)]
+    us, gs = u[..., :some].double(), dout[..., :some].double()
+    steps = torch.nn.functional.softplus(delta[..., :some].double() + v[2])
+    h, loss = u.new_zeros(nseq, some, n, dtype=torch.float64), 0.0
+    for t in range(length):
+        dt = steps[:, t, :, None]
+        h = torch.exp(dt * v[0]) * h + dt * us[:, t, :, None] * B[:, t].double()
+        loss = loss + (gs[:, t] * ((h * C[:, t].double()).sum(-1) + v[1] * us[:, t])).sum()
+    ref = torch.autograd.grad(loss, v)
+    for k, r in zip(("dA", "dD", "ddelta_bias"), ref):
+        mine = getattr(got, k)[:some].double()
+        err = float((mine - r).norm() / r.norm())
+        assert err <= 12 * 2.0 ** -24, (k, err)
