@@ -601,10 +601,11 @@ extern "C" int fft_norm_forward(const fft_norm_desc* d, const void* x, int64_t x
     if (rc != FFT_OK) return rc;
     const bool q = d->out_dtype == FFT_E4M3;
     if (!q && d->out_dtype != d->dtype) return FFT_ERR_INVALID_ARG;
-    if (q ? (!scale || (d->group != 0 && d->group != 32 && d->group != 64 && d->group != 128))
+    const bool rows = d->rows > 0;  // tensors without rows may have no address
+    if (q ? ((rows && !scale) || (d->group != 0 && d->group != 32 && d->group != 64 && d->group != 128))
           : d->group != 0)
         return FFT_ERR_INVALID_ARG;
-    if (!x || !out || !stride_ok(x, x_stride, d) || !stride_ok(residual, residual_stride, d) ||
+    if ((rows && (!x || !out)) || !stride_ok(x, x_stride, d) || !stride_ok(residual, residual_stride, d) ||
         !stride_ok(out, out_stride, d) || !stride_ok(sum, sum_stride, d))
         return FFT_ERR_INVALID_ARG;
     const size_t e = dtype_size(d->dtype), r = dtype_size(d->res_dtype);
@@ -612,7 +613,7 @@ extern "C" int fft_norm_forward(const fft_norm_desc* d, const void* x, int64_t x
         !aligned_to(out, dtype_size(d->out_dtype)) || !aligned_to(scale, 4) ||
         !aligned_to(d->weight, dtype_size(d->param_dtype)))
         return FFT_ERR_MISALIGNED;
-    if (d->rows == 0) return FFT_OK;
+    if (!rows) return FFT_OK;
     const NormArgs a = {x, residual, out, scale, sum, d->weight, x_stride, residual_stride,
                         out_stride, sum_stride, d->rows, (int)d->columns, d->param_dtype == FFT_F32,
                         aligned_to(d->weight, 16), (int)d->group, (float)d->columns, d->eps};
@@ -644,12 +645,13 @@ extern "C" int fft_norm_backward(const fft_norm_desc* d, const void* dout, int64
                                  size_t workspace_bytes, void* stream) {
     int rc = norm_sizes(d);
     if (rc != FFT_OK) return rc;
-    if (!dout || !r || (!dsum && !dx && !dweight) || !stride_ok(dout, dout_stride, d) ||
+    const bool none = d->rows == 0;  // tensors without rows may have no address
+    if ((!none && (!dout || !r || (!dsum && !dx && !dweight))) || !stride_ok(dout, dout_stride, d) ||
         !stride_ok(r, r_stride, d) || !stride_ok(dresidual, dresidual_stride, d) ||
         !stride_ok(dsum, dsum_stride, d) || !stride_ok(dx, dx_stride, d))
         return FFT_ERR_INVALID_ARG;
     const int64_t blocks = bwd_blocks(d->rows, d->columns);
-    if (dweight && d->rows > 0 &&
+    if (dweight && !none &&
         (!workspace || workspace_bytes < (size_t)(blocks * d->columns) * sizeof(float)))
         return FFT_ERR_INVALID_ARG;
     const size_t e = dtype_size(d->dtype), rs = dtype_size(d->res_dtype);
@@ -658,7 +660,7 @@ extern "C" int fft_norm_backward(const fft_norm_desc* d, const void* dout, int64
         !aligned_to(workspace, 16) || !aligned_to(d->weight, dtype_size(d->param_dtype)))
         return FFT_ERR_MISALIGNED;
     cudaStream_t s = (cudaStream_t)stream;
-    if (d->rows == 0) {
+    if (none) {
         if (dweight && cudaMemsetAsync(dweight, 0, (size_t)d->columns * 4, s) != cudaSuccess)
             return FFT_ERR_CUDA;
         return FFT_OK;

@@ -448,6 +448,8 @@ def _rows(t):
         return shape[0], st[0]
     if len(shape) < 2:
         return 1, shape[-1]
+    if 0 in shape[:-1]:
+        return 0, shape[-1]
     rows, stride = shape[-2], st[-2]
     for k in range(len(shape) - 3, -1, -1):
         if shape[k] != 1 and rows != 1 and st[k] != rows * stride:

@@ -163,3 +163,15 @@ def test_norm_calls_refuse(lib):
 def test_lib_names_are_exported():
     for name in sq.SYMBOLS:
         assert name in fx.ABI_SYMBOLS
+
+
+def test_norm_of_no_rows_needs_no_address(lib):
+    """Tensors without elements have the address 0."""
+    d = norm(rows=0)
+    assert lib.fft_norm_forward(d, None, 64, None, 0, None, 64, None, None, 0, None) == fx.FFT_OK
+    q = norm(rows=0, out=sq.E4M3, group=32)
+    assert lib.fft_norm_forward(q, None, 64, None, 0, None, 64, None, None, 64, None) == fx.FFT_OK
+    assert lib.fft_norm_backward(d, None, 64, None, 64, None, 0, None, 64, None, 64, None, None, 0,
+                                 None) == fx.FFT_OK
+    assert lib.fft_norm_forward(norm(rows=0, columns=0), None, 1, None, 0, None, 1, None, None, 0,
+                                None) == INVALID
