@@ -11,7 +11,8 @@ current CUDA stream: every step runs in the library's kernels.
     q = residual_norm(x, weight, out_dtype=torch.float8_e4m3fn, group=128)     # q.out, q.scale
 
 Sequences are [sequences, tokens, channels] or, with `offsets` (int64, on the device, sequences + 1
-ascending values from 0 to the number of tokens), packed [tokens, channels].  The last axis is
+ascending values from 0 to the number of tokens), packed [tokens, channels]; sequences may be without
+tokens and batches without sequences.  The last axis is
 contiguous, the others may have any stride: halves of a projection need no copy.  The *_backward
 calls return the gradients; nothing is recorded for autograd.  The *_step calls take one token per
 sequence and move its state from slots[i] to slots_out[i] of a pool (in place by default).
@@ -170,7 +171,7 @@ def _token(t, dev, dtype, shape, what):
 def _offsets(offsets, dev):
     if offsets is None:
         return 0
-    if offsets.dim() != 1 or offsets.numel() < 2:
+    if offsets.dim() != 1 or offsets.numel() < 1:
         raise ValueError("offsets: expected one more value than sequences")
     return _flat(offsets, dev, torch.int64, offsets.shape, "offsets")
 
@@ -239,6 +240,18 @@ def _lead(x, offsets, what):
     return packed, offsets.numel() - 1 if packed else shape[0], shape[0] if packed else shape[1]
 
 
+def _batch(offsets, dev, nseq, length, packed):
+    """What the library is told of (sequences, tokens, offsets).  No sequences are one without
+    tokens, which writes nothing (states of no sequences have no address) but zeros to gradients of
+    parameters."""
+    at = _offsets(offsets, dev)
+    if nseq:
+        return nseq, length, at
+    if packed and length:
+        raise ValueError("offsets: tokens that belong to no sequence")
+    return 1, 0, 0
+
+
 # ---- short causal convolution ---------------------------------------------------------------
 
 
@@ -255,8 +268,9 @@ def _conv_desc(x, weight, bias, silu, initial_state, offsets):
     w, ptype = weight.shape[1], weight.dtype
     if ptype is not dtype and ptype is not torch.float32:
         raise TypeError("weight: expected float32 or the type of x")
-    desc = _CONV.pack(code, F32 if ptype is torch.float32 else code, w, 1 if silu else 0, nseq,
-                      length, d, _offsets(offsets, dev),
+    count, length, at = _batch(offsets, dev, nseq, length, packed)
+    desc = _CONV.pack(code, F32 if ptype is torch.float32 else code, w, 1 if silu else 0, count,
+                      length, d, at,
                       _flat(weight, dev, ptype, (d, w), "weight"),
                       _flat(bias, dev, ptype, (d,), "bias"),
                       _flat(initial_state, dev, dtype, (nseq, w - 1, d), "initial_state"),
@@ -318,6 +332,8 @@ def causal_conv_step(state, x, weight, bias=None, silu=False, slots=None, slots_
     pool = _flat(state, dev, dtype, (size, w - 1, d), "state")
     src = _flat(slots, dev, torch.int64, (nseq,), "slots")
     dst = _flat(slots_out, dev, torch.int64, (nseq,), "slots_out")
+    if nseq == 0:
+        return _out(out, x, dev)
     if out is None and stream is None:  # the usual call
         out = x.new_empty(shape)
         _check(_L.fft_conv_step(desc, _SEQ.pack(out.data_ptr(), d, 0), pool, size, src, dst,
@@ -349,7 +365,8 @@ def _scan_desc(u, delta, A, B, C, D, z, delta_bias, softplus, initial_state, off
         raise ValueError("C: expected the shape of B")
     if z is not None:
         _need(z, dev, dtype, shape, "z")
-    heads = (code, 1 if softplus else 0, nseq, length, d, groups, n, _offsets(offsets, dev),
+    count, length, at = _batch(offsets, dev, nseq, length, packed)
+    heads = (code, 1 if softplus else 0, count, length, d, groups, n, at,
              _flat(A, dev, f32, (d, n), "A"), _flat(D, dev, f32, (d,), "D"),
              _flat(delta_bias, dev, f32, (d,), "delta_bias"),
              _flat(initial_state, dev, f32, (nseq, d, n), "initial_state"))
@@ -423,6 +440,8 @@ def selective_scan_step(state, u, delta, A, B, C, D=None, z=None, delta_bias=Non
     pool = _flat(state, dev, f32, (size, d, n), "state")
     src = _flat(slots, dev, torch.int64, (nseq,), "slots")
     dst = _flat(slots_out, dev, torch.int64, (nseq,), "slots_out")
+    if nseq == 0:
+        return _out(out, u, dev)
     if out is None and stream is None:  # the usual call
         out = u.new_empty(shape)
         _check(_L.fft_scan_step(desc, _SEQ.pack(out.data_ptr(), d, 0), pool, size, src, dst,
