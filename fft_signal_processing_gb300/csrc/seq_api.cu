@@ -36,6 +36,39 @@ int check_sizes(int64_t nseq, int64_t length, int64_t channels, const int64_t* o
     return aligned_to(offsets, 8) ? FFT_OK : FFT_ERR_MISALIGNED;
 }
 
+// Bytes that a sequence tensor's rows of `width` values may touch, from its first value on.
+int64_t seq_span_bytes(const fft_seq& s, int64_t width, int64_t nseq, int64_t length, bool packed,
+                       size_t size) {
+    if (!s.data || length < 1) return 0;
+    return ((packed ? 0 : (nseq - 1) * s.seq_stride) + (length - 1) * s.tok_stride + width) * (int64_t)size;
+}
+bool bytes_meet(const void* a, int64_t na, const void* b, int64_t nb) {
+    const uintptr_t x = (uintptr_t)a, y = (uintptr_t)b;
+    return a && b && na > 0 && nb > 0 && x < y + nb && y < x + na;
+}
+// Whether two sequence tensors share values.  Spans may meet without that, as those of two halves of
+// one projection do: every row of both starts a multiple of the strides' common divisor after the
+// first one of its tensor, so the columns modulo it tell them apart.
+bool seqs_meet(const fft_seq& a, const fft_seq& b, int64_t width, int64_t bwidth, int64_t nseq,
+               int64_t length, bool packed, size_t size) {
+    if (!bytes_meet(a.data, seq_span_bytes(a, width, nseq, length, packed, size), b.data,
+                    seq_span_bytes(b, bwidth, nseq, length, packed, size)))
+        return false;
+    int64_t period = 0;
+    auto add = [&](int64_t stride) {
+        while (stride) {
+            const int64_t r = period % stride;
+            period = stride;
+            stride = r;
+        }
+    };
+    if (length > 1) add(a.tok_stride), add(b.tok_stride);
+    if (!packed && nseq > 1) add(a.seq_stride), add(b.seq_stride);
+    if (!period) return true;
+    const int64_t apart = ((intptr_t)b.data - (intptr_t)a.data) / (int64_t)size % period;
+    const int64_t column = apart < 0 ? apart + period : apart;  // of b's rows, a's being 0
+    return column < width || column + bwidth > period;
+}
 #define TRY(x)                        \
     do {                              \
         const int rc_ = (x);          \
@@ -210,6 +243,10 @@ extern "C" int fft_conv_forward(const fft_conv_desc* d, const fft_seq* out, void
     const size_t e = dtype_size(d->dtype);
     TRY(check_seq(*out, d->channels, d->nseq, d->length, d->offsets, e, true));
     if (!aligned_to(final_state, e)) return FFT_ERR_MISALIGNED;
+    const int64_t states = d->nseq * (d->width - 1) * d->channels * (int64_t)e;
+    if (seqs_meet(*out, d->x, d->channels, d->channels, d->nseq, d->length, d->offsets, e) ||
+        bytes_meet(final_state, states, d->initial_state, states))
+        return FFT_ERR_INVALID_ARG;
     ConvArgs a = {};
     a.d = *d;
     a.out = *out;
@@ -243,6 +280,13 @@ extern "C" int fft_conv_backward(const fft_conv_desc* d, const fft_seq* dout,
     const bool params = dweight || dbias;
     if (params && tiles > 0 &&
         (!workspace || workspace_bytes < (size_t)(tiles * cols) * sizeof(float)))
+        return FFT_ERR_INVALID_ARG;
+    const int64_t states = d->nseq * (d->width - 1) * d->channels * (int64_t)e;
+    auto meets = [&](const fft_seq& in) {
+        return seqs_meet(*dx, in, d->channels, d->channels, d->nseq, d->length, d->offsets, e);
+    };
+    if (meets(d->x) || meets(*dout) || bytes_meet(dinitial_state, states, d->initial_state, states) ||
+        bytes_meet(dinitial_state, states, dfinal_state, states))
         return FFT_ERR_INVALID_ARG;
     ConvArgs a = {};
     a.d = *d;

@@ -282,7 +282,7 @@ def causal_conv(x, weight, bias=None, silu=False, initial_state=None, offsets=No
                 return_state=False, out=None, stream=None):
     """Short causal convolution of every channel (fft_conv_forward): weight [channels, width],
     bias [channels], both float32 or of x's type; initial_state [sequences, width-1, channels].
-    Returns out, or (out, final_state)."""
+    out may not overlap x.  Returns out, or (out, final_state)."""
     desc, dev, nseq, d, w = _conv_desc(x, weight, bias, silu, initial_state, offsets)
     on, s = _stream(stream, dev)
     with on:

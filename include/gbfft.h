@@ -393,7 +393,9 @@ typedef struct fft_conv_desc {
     fft_seq x;
 } fft_conv_desc;
 
-/* fft_conv_forward - out and, unless NULL, final_state.  out may not overlap x.
+/* fft_conv_forward - out and, unless NULL, final_state.  Tokens are read by their neighbours too:
+ * out may not overlap x, nor final_state initial_state (FFT_ERR_INVALID_ARG); out and x may be
+ * different columns of the same rows.
  * Returns FFT_OK, FFT_ERR_INVALID_ARG, FFT_ERR_UNSUPPORTED_SIZE, FFT_ERR_MISALIGNED or
  * FFT_ERR_CUDA. */
 int fft_conv_forward(const fft_conv_desc* d, const fft_seq* out, void* final_state, void* stream);
@@ -402,7 +404,8 @@ int fft_conv_forward(const fft_conv_desc* d, const fft_seq* out, void* final_sta
  * dx (data NULL: not computed), dweight [channels][width] and dbias [channels] in float32 (either
  * may be NULL), dinitial_state like initial_state (NULL: not computed).  dfinal_state NULL:
  * zeros.  workspace: 16-byte aligned, at least fft_conv_workspace bytes (0 if both parameter
- * gradients are NULL). */
+ * gradients are NULL).  dx may not overlap x or dout, nor dinitial_state the states that are read
+ * (FFT_ERR_INVALID_ARG). */
 int fft_conv_workspace(const fft_conv_desc* d, size_t* bytes);
 int fft_conv_backward(const fft_conv_desc* d, const fft_seq* dout, const void* dfinal_state,
                       const fft_seq* dx, float* dweight, float* dbias, void* dinitial_state,

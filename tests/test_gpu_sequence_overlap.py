@@ -1,0 +1,92 @@
+"""Outputs over inputs.  A token of the convolution is read by the width - 1 behind it, which other
+threads compute: an output over the input is refused, columns of the same rows are not."""
+import pytest
+
+torch = pytest.importorskip("torch")
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def built():
+    import __graft_entry__
+
+    __graft_entry__.build()
+
+
+@pytest.mark.parametrize("packed", [False, True])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_convolution_over_its_input(packed, dtype):
+    import fft_signal_processing_gb300 as fx
+
+    torch.manual_seed(1)
+    d = 24
+    lead = (40,) if packed else (3, 40)
+    offsets = torch.tensor([0, 7, 40], device="cuda") if packed else None
+    w = torch.randn(d, 4, device="cuda")
+    wide = torch.randn(*lead, 3 * d, device="cuda").to(dtype)
+    x = wide[..., d:2 * d]
+    want = fx.causal_conv(x, w, offsets=offsets)
+    keep = wide.clone()
+    for out in (x, wide[..., d - 1:2 * d - 1], wide[..., d + 8:2 * d + 8], wide[..., 1:1 + d]):
+        with pytest.raises(fx.GbfftError):
+            fx.causal_conv(x, w, offsets=offsets, out=out)
+    assert torch.equal(wide, keep)
+    for out in (wide[..., :d], wide[..., 2 * d:]):  # other columns of the same rows
+        assert fx.causal_conv(x, w, offsets=offsets, out=out) is out
+        assert torch.equal(out, want) and torch.equal(x, keep[..., d:2 * d])
+
+
+def test_rows_in_turn():
+    """Tokens by sequences, and every second row: spans that meet without a common value."""
+    import fft_signal_processing_gb300 as fx
+
+    torch.manual_seed(2)
+    d = 16
+    w = torch.randn(d, 4, device="cuda")
+    buf = torch.randn(30, 4, 2 * d, device="cuda")
+    x, out = (buf[..., k * d:(k + 1) * d].transpose(0, 1) for k in (0, 1))  # [4, 30, d]
+    want = fx.causal_conv(x.contiguous(), w)
+    assert torch.equal(fx.causal_conv(x, w, out=out), want)
+    rows = torch.randn(1, 60, d, device="cuda")
+    want = fx.causal_conv(rows[:, ::2].contiguous(), w)
+    assert torch.equal(fx.causal_conv(rows[:, ::2], w, out=rows[:, 1::2]), want)
+    with pytest.raises(fx.GbfftError):
+        fx.causal_conv(rows[:, 10:20], w, out=rows[:, 15:25])
+    one = torch.randn(1, 1, d, device="cuda")
+    with pytest.raises(fx.GbfftError):
+        fx.causal_conv(one, w, out=one)
+    assert fx.causal_conv(rows[:, 10:20], w, out=rows[:, 20:30]).shape == (1, 10, d)
+
+
+def test_gradients_and_states_over_inputs():
+    """The C calls, where outputs are the caller's."""
+    import ctypes
+
+    import fft_signal_processing_gb300 as fx
+    from fft_signal_processing_gb300 import sequence as sq
+
+    L, d = fx.lib(), 16
+    x, dout, w = (torch.randn(2, 9, d, device="cuda") for _ in range(3))
+    init, fin = torch.randn(2, 3, d, device="cuda"), torch.empty(2, 3, d, device="cuda")
+    weight = torch.randn(d, 4, device="cuda")
+
+    def seq(t):
+        return t.data_ptr(), t.stride(0), t.stride(1)
+
+    desc = sq._CONV.pack(sq.F32, sq.F32, 4, 0, 2, 9, d, 0, weight.data_ptr(), 0, init.data_ptr(), *seq(x))
+    stream = torch.cuda.current_stream().cuda_stream
+
+    def forward(out, final):
+        return L.fft_conv_forward(desc, sq._SEQ.pack(*seq(out)), final.data_ptr(), stream)
+
+    def backward(dx, dinit):
+        return L.fft_conv_backward(desc, sq._SEQ.pack(*seq(dout)), fin.data_ptr(), sq._SEQ.pack(*seq(dx)),
+                                   None, None, dinit.data_ptr(), None, 0, ctypes.c_void_p(stream))
+
+    assert forward(w, init) == fx.FFT_ERR_INVALID_ARG and forward(w, fin) == fx.FFT_OK
+    other = torch.empty_like(init)
+    for dx, dinit in ((x, other), (dout, other), (w, init), (w, fin)):
+        assert backward(dx, dinit) == fx.FFT_ERR_INVALID_ARG
+    assert backward(w, other) == fx.FFT_OK
+    torch.cuda.synchronize()

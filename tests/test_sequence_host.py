@@ -175,3 +175,11 @@ def test_norm_of_no_rows_needs_no_address(lib):
                                  None) == fx.FFT_OK
     assert lib.fft_norm_forward(norm(rows=0, columns=0), None, 1, None, 0, None, 1, None, None, 0,
                                 None) == INVALID
+
+
+def test_convolution_over_its_input_is_refused(lib):
+    assert lib.fft_conv_forward(conv(), OUT, None, None) == INVALID
+    assert lib.fft_conv_forward(conv(x=(A, 256, 32)), sq._SEQ.pack(A + 30, 256, 32), None, None) == INVALID
+    apart = sq._SEQ.pack(A + 4096, 128, 16)
+    assert lib.fft_conv_forward(conv(initial=A + 8192), apart, A + 8192 + 64, None) == INVALID
+    assert lib.fft_conv_backward(conv(), apart, None, apart, None, None, None, None, 0, None) == INVALID
