@@ -69,6 +69,11 @@ bool seqs_meet(const fft_seq& a, const fft_seq& b, int64_t width, int64_t bwidth
     const int64_t column = apart < 0 ? apart + period : apart;  // of b's rows, a's being 0
     return column < width || column + bwidth > period;
 }
+bool seqs_same(const fft_seq& a, const fft_seq& b, int64_t nseq, int64_t length, bool packed) {
+    return a.data == b.data && (length < 2 || a.tok_stride == b.tok_stride) &&
+           (packed || nseq < 2 || a.seq_stride == b.seq_stride);
+}
+
 #define TRY(x)                        \
     do {                              \
         const int rc_ = (x);          \
@@ -350,6 +355,16 @@ extern "C" int fft_scan_forward(const fft_scan_desc* d, const fft_seq* out, floa
     a.final_state = final_state;
     const int64_t need = scan_layout(*d, &a, static_cast<char*>(workspace));
     if (need > 0 && (!workspace || workspace_bytes < (size_t)need)) return FFT_ERR_INVALID_ARG;
+    const int64_t states = d->nseq * d->channels * d->states * 4;
+    auto meets = [&](const fft_seq& in, int64_t width) {
+        return seqs_meet(*out, in, d->channels, width, d->nseq, d->length, d->offsets, dtype_size(d->dtype));
+    };
+    for (const fft_seq* in : {&d->u, &d->z})  // read where they are written, by the same thread
+        if (!seqs_same(*out, *in, d->nseq, d->length, d->offsets) && meets(*in, d->channels))
+            return FFT_ERR_INVALID_ARG;
+    if (meets(d->delta, d->channels) || meets(d->B, d->groups * d->states) ||
+        meets(d->C, d->groups * d->states) || bytes_meet(final_state, states, d->initial_state, states))
+        return FFT_ERR_INVALID_ARG;
     cudaStream_t s = (cudaStream_t)stream;
     return status(d->dtype == FFT_F32 ? scan_forward_f32(a, s)
                                       : (d->dtype == FFT_BF16 ? scan_forward_bf16(a, s)

@@ -379,7 +379,8 @@ def selective_scan(u, delta, A, B, C, D=None, z=None, delta_bias=None, softplus=
                    initial_state=None, offsets=None, return_state=False, out=None, stream=None):
     """Selective state-space scan (fft_scan_forward): u, delta, z [..., channels], A [channels, n],
     B, C [..., groups, n] or [..., n], D, delta_bias [channels]; states [sequences, channels, n].
-    A, D, delta_bias and states are float32.  Returns out, or (out, final_state)."""
+    A, D, delta_bias and states are float32.  out may be u or z and overlaps no other input.
+    Returns out, or (out, final_state)."""
     desc, dev, nseq, d, n = _scan_desc(u, delta, A, B, C, D, z, delta_bias, softplus,
                                        initial_state, offsets)
     on, s = _stream(stream, dev)

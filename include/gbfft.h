@@ -446,7 +446,8 @@ typedef struct fft_scan_desc {
 int fft_scan_workspace(const fft_scan_desc* d, int backward, size_t* bytes);
 
 /* fft_scan_forward - out and, unless NULL, final_state [nseq][channels][states].  out may be
- * u or z themselves (same data and strides); any other overlap is an error of the caller.
+ * u or z themselves (same data and strides); any other overlap of out with a sequence that is read,
+ * or of final_state with initial_state, is refused (FFT_ERR_INVALID_ARG).
  * Returns FFT_OK, FFT_ERR_INVALID_ARG, FFT_ERR_UNSUPPORTED_SIZE, FFT_ERR_MISALIGNED or
  * FFT_ERR_CUDA. */
 int fft_scan_forward(const fft_scan_desc* d, const fft_seq* out, float* final_state,

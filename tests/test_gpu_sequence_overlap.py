@@ -90,3 +90,24 @@ def test_gradients_and_states_over_inputs():
         assert backward(dx, dinit) == fx.FFT_ERR_INVALID_ARG
     assert backward(w, other) == fx.FFT_OK
     torch.cuda.synchronize()
+
+
+def test_scan_over_its_inputs():
+    import fft_signal_processing_gb300 as fx
+
+    torch.manual_seed(3)
+    d, n = 24, 16
+    wide = torch.randn(2, 70, 3 * d, device="cuda")
+    u, z, rest = (wide[..., k * d:(k + 1) * d] for k in range(3))
+    delta, B, C = (torch.randn(2, 70, k, device="cuda") for k in (d, n, n))
+    A = -torch.rand(d, n, device="cuda") - 0.5
+    c = dict(u=u, delta=delta, A=A, B=B, C=C, z=z, softplus=True)
+    want = fx.selective_scan(**c)
+    for out in (delta, wide[..., 1:d + 1], wide[..., d + 3:2 * d + 3], wide[..., d - 1:2 * d - 1]):
+        with pytest.raises(fx.GbfftError):
+            fx.selective_scan(**c, out=out)
+    assert torch.equal(fx.selective_scan(**c, out=rest), want) and torch.equal(rest, want)
+    keep = wide.clone()
+    assert torch.equal(fx.selective_scan(**c, out=z), want)
+    wide.copy_(keep)
+    assert torch.equal(fx.selective_scan(**c, out=u), want)

@@ -183,3 +183,20 @@ def test_convolution_over_its_input_is_refused(lib):
     apart = sq._SEQ.pack(A + 4096, 128, 16)
     assert lib.fft_conv_forward(conv(initial=A + 8192), apart, A + 8192 + 64, None) == INVALID
     assert lib.fft_conv_backward(conv(), apart, None, apart, None, None, None, None, 0, None) == INVALID
+
+
+def test_scan_over_its_inputs_is_refused(lib):
+    def at(offset):
+        return A + (offset << 12), 128, 16
+
+    apart = dict(u=at(1), delta=at(2), B=at(3), C=at(4))
+    for name in apart:  # from the 8th column on
+        data, *strides = apart[name]
+        assert lib.fft_scan_forward(scan(**apart), sq._SEQ.pack(data + 16, *strides), None, None, 0,
+                                    None) == INVALID, name
+    for name in ("delta", "B", "C"):
+        assert lib.fft_scan_forward(scan(**apart), sq._SEQ.pack(*apart[name]), None, None, 0,
+                                    None) == INVALID, name
+    state = A + (9 << 12)
+    assert lib.fft_scan_forward(scan(**apart, initial=state), sq._SEQ.pack(*at(5)), state, None, 0,
+                                None) == INVALID
