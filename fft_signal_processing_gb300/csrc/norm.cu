@@ -11,7 +11,6 @@
 // ring of later rows in shared memory instead of registers (130 -> 81 us), sums over the warps of
 // a row by one shuffle tree instead of a loop.
 #include <cuda_fp8.h>
-#include <float.h>
 
 #include "launch_cache.cuh"
 #include "seq_common.cuh"
@@ -96,11 +95,12 @@ __device__ __forceinline__ float max_abs_nan(float m, float v) {  // a NaN stays
 }
 
 // 448 / m, for t = r * weight and m = max |t|: with q = t * (448 / m) rstd cancels, and m * rstd is
-// max |y|.  Held finite for tiny m; 0 where y is 0 all over the group; a NaN stays.
+// max |y|.  0 where y is 0 all over the group; a NaN stays.  Below kTiny the quotient is beyond
+// float32: m counts raised by kRaise there, and so have the values to be.
+constexpr float kTiny = 0x1p-119f, kRaise = 0x1p64f;
 __device__ __forceinline__ float e4m3_inv(float m, float my) {
     if (my == 0.f) return 0.f;
-    const float inv = 448.f / m;
-    return inv > FLT_MAX ? FLT_MAX : inv;
+    return 448.f / (m < kTiny ? m * kRaise : m);
 }
 
 // Rows ahead of the present one wait in shared memory: a thread copies the 16-byte pieces of its
@@ -265,6 +265,10 @@ __global__ void __launch_bounds__(MAXT, kNormResident / MAXT) k_norm_fwd(const N
             uint8_t* out = static_cast<uint8_t*>(a.out) + row * a.out_stride;
             float inv = OUT == 1 ? e4m3_inv(m, m * rstd) : 0.f;
             if (OUT == 1 && live && j == 0) a.scale[row] = m * rstd / 448.f;
+            if (OUT == 1 && m < kTiny) {
+#pragma unroll
+                for (int e = 0; e < E / 2; ++e) v.v[e] = mul2(v.v[e], splat(kRaise));
+            }
 #pragma unroll
             for (int i = 0; i < NV; ++i) {
                 const int c = (i * tpr + j) * VEC;
@@ -280,6 +284,10 @@ __global__ void __launch_bounds__(MAXT, kNormResident / MAXT) k_norm_fwd(const N
                             m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
                     }
                     inv = e4m3_inv(m, m * rstd);
+                    if (m < kTiny) {
+#pragma unroll
+                        for (int k = 0; k < VEC; ++k) v[i * VEC + k] *= kRaise;
+                    }
                     if (in && c % a.group == 0) a.scale[row * groups + c / a.group] = m * rstd / 448.f;
                 }
                 if constexpr (VEC == 1) {
