@@ -306,6 +306,7 @@ __global__ void __launch_bounds__(MAXT, kNormResident / MAXT) k_norm_fwd(const N
             if constexpr (OUT == 2 && VEC == 1) __syncthreads();
         }
     }
+    if constexpr (AHEAD) copy_wait<0>();  // rows beyond the last: zeros on their way to shared memory
 }
 
 struct NormBwdArgs {
@@ -441,6 +442,7 @@ __global__ void __launch_bounds__(MAXT) k_norm_bwd(const NormBwdArgs a) {
             }
         }
     }
+    if constexpr (AHEAD) copy_wait<0>();  // rows beyond the last: zeros on their way to shared memory
     if (a.parts) {
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
