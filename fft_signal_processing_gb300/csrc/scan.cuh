@@ -133,6 +133,7 @@ __device__ __forceinline__ void copy_tile(T* dst, const T* p, int64_t stride, in
 template <class T, int TK, int NP, int NT, bool BOTH, bool FAST>
 struct RowsAhead {
     static constexpr int V = 16 / sizeof(T);
+    static_assert(!FAST || NP % V == 0, "a token's states are whole accesses");
     static constexpr int WIDE = FAST ? (TK * NP / V + NT - 1) / NT : 0;  // accesses per thread
     static constexpr int ONE = (TK * NP + NT - 1) / NT;
     uint4 wide[BOTH ? 2 : 1][FAST ? WIDE : 1];
@@ -758,11 +759,18 @@ cudaError_t scan_launch(const ScanArgs& a, cudaStream_t s) {
     return scan_kernel<T, SPT, SL, PASS, FAST>(a, blocks, s);
 }
 
+// Whether NP states of type T can be whole 16-byte accesses.
+template <class T>
+constexpr bool whole_states(int np) {
+    return np * sizeof(T) % 16 == 0;
+}
 template <class T, int SPT, int SL, int PASS>
 cudaError_t scan_fast(const ScanArgs& a, cudaStream_t s) {
-    return a.d.states == SPT * (SL ? SL : 1) && a.vec >= 16 && a.wide
-               ? scan_launch<T, SPT, SL, PASS, true>(a, s)
-               : scan_launch<T, SPT, SL, PASS, false>(a, s);
+    constexpr int NP = SPT * (SL ? SL : 1);
+    if constexpr (whole_states<T>(NP)) {
+        if (a.d.states == NP && a.vec >= 16 && a.wide) return scan_launch<T, SPT, SL, PASS, true>(a, s);
+    }
+    return scan_launch<T, SPT, SL, PASS, false>(a, s);
 }
 template <class T, int PASS>
 cudaError_t scan_run(ScanArgs a, cudaStream_t s) {

@@ -790,8 +790,10 @@ cudaError_t scan_bwd_pair_launch(const ScanBwdArgs& a, cudaStream_t s) {
 }
 template <class T, int SPT>
 cudaError_t scan_bwd_back_pair(const ScanBwdArgs& a, cudaStream_t s) {
-    return a.d.states == SPT && a.f.vec >= 16 && a.f.wide ? scan_bwd_pair_launch<T, SPT, true>(a, s)
-                                                          : scan_bwd_pair_launch<T, SPT, false>(a, s);
+    if constexpr (whole_states<T>(SPT)) {
+        if (a.d.states == SPT && a.f.vec >= 16 && a.f.wide) return scan_bwd_pair_launch<T, SPT, true>(a, s);
+    }
+    return scan_bwd_pair_launch<T, SPT, false>(a, s);
 }
 template <class T, int SPT, int SL>
 cudaError_t scan_bwd_back(const ScanBwdArgs& a, cudaStream_t s) {
