@@ -286,9 +286,10 @@ __device__ void conv_dinitial(const ConvArgs& a, int64_t q, int64_t c) {
 
 // Backward.  A run walks its tokens [b, e) and W-1 more: dp of the tokens up to e-1+(W-1) gives
 // dx of [b, e); only dp of its own tokens enters dweight and dbias.  The runs of a block are
-// summed in shared memory, one partial row per token tile.
+// summed in shared memory, one partial row per token tile.  Four channels and up to four taps fit the
+// 128 registers that two blocks of an SM leave; said to the compiler, which takes 134 otherwise.
 template <class T, int VEC, int W>
-__global__ void __launch_bounds__(kConvThreads) k_conv_bwd(const ConvArgs a) {
+__global__ void __launch_bounds__(kConvThreads, VEC == 4 && W <= 4 ? 2 : 0) k_conv_bwd(const ConvArgs a) {
     constexpr int P = Pairs<VEC>::P, N = kConvBatch, LANES = kConvLanes * VEC;
     using Ring = ConvRing<T, VEC, 2>;
     extern __shared__ uint2 ring_memory[];
