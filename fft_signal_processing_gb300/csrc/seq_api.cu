@@ -331,6 +331,9 @@ extern "C" int fft_conv_step(const fft_conv_desc* d, const fft_seq* out, void* s
     TRY(check_step(out, state, pool, slots, slots_out, d->nseq, d->length, d->offsets, d->channels,
                    e, d->width > 1));
     if (!aligned_to(state, e)) return FFT_ERR_MISALIGNED;
+    if (!seqs_same(*out, d->x, d->nseq, 1, false) &&
+        seqs_meet(*out, d->x, d->channels, d->channels, d->nseq, 1, false, e))
+        return FFT_ERR_INVALID_ARG;
     const ConvStepArgs a = {*d, *out, state, slots, slots_out, pool};
     return status(conv_step_any(a, (cudaStream_t)stream));
 }
@@ -377,6 +380,13 @@ extern "C" int fft_scan_step(const fft_scan_desc* d, const fft_seq* out, float* 
     TRY(check_step(out, state, pool, slots, slots_out, d->nseq, d->length, d->offsets, d->channels,
                    dtype_size(d->dtype), true));
     if (!aligned_to(state, 4)) return FFT_ERR_MISALIGNED;
+    const int64_t bc = d->groups * d->states;
+    auto meets = [&](const fft_seq& in, int64_t width) {
+        return seqs_meet(*out, in, d->channels, width, d->nseq, 1, false, dtype_size(d->dtype));
+    };
+    for (const fft_seq* in : {&d->u, &d->delta, &d->z})
+        if (!seqs_same(*out, *in, d->nseq, 1, false) && meets(*in, d->channels)) return FFT_ERR_INVALID_ARG;
+    if (meets(d->B, bc) || meets(d->C, bc)) return FFT_ERR_INVALID_ARG;
     const ScanStepArgs a = {*d, *out, state, slots, slots_out, pool, 0, false};
     return status(scan_step_any(a, (cudaStream_t)stream));
 }

@@ -416,7 +416,8 @@ int fft_conv_backward(const fft_conv_desc* d, const fft_seq* dout, const void* d
  * [pool][width-1][channels] and writes the shifted state to slots_out[q].  slots NULL: sequence q
  * has slot q; slots_out NULL: slots (in place).  A slot outside [0, pool) marks a padding row:
  * its output is 0 and no state is written.  A slot that one sequence writes may not be read or
- * written by another. */
+ * written by another.  out may be x itself; another overlap of the two is refused
+ * (FFT_ERR_INVALID_ARG). */
 int fft_conv_step(const fft_conv_desc* d, const fft_seq* out, void* state, int64_t pool,
                   const int64_t* slots, const int64_t* slots_out, void* stream);
 
@@ -471,7 +472,7 @@ int fft_scan_backward(const fft_scan_desc* d, const fft_scan_grads* g, void* wor
 
 /* fft_scan_step - one token for each of nseq sequences (length 1, offsets NULL, initial_state not
  * used; rows at seq_stride): state pool [pool][channels][states] float32, slots as for
- * fft_conv_step. */
+ * fft_conv_step.  out may be u, delta or z itself; another overlap with what is read is refused. */
 int fft_scan_step(const fft_scan_desc* d, const fft_seq* out, float* state, int64_t pool,
                   const int64_t* slots, const int64_t* slots_out, void* stream);
 

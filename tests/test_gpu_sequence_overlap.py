@@ -111,3 +111,34 @@ def test_scan_over_its_inputs():
     assert torch.equal(fx.selective_scan(**c, out=z), want)
     wide.copy_(keep)
     assert torch.equal(fx.selective_scan(**c, out=u), want)
+
+
+def test_steps_over_their_inputs():
+    import fft_signal_processing_gb300 as fx
+
+    torch.manual_seed(4)
+    d, n = 40, 16
+    wide = torch.randn(5, 2 * d, device="cuda")
+    x, w = wide[:, :d], torch.randn(d, 4, device="cuda")
+    pool = torch.randn(5, 3, d, device="cuda")
+    want = fx.causal_conv_step(pool.clone(), x, w)
+    for out in (wide[:, 8:d + 8], wide[:, 1:d + 1]):
+        with pytest.raises(fx.GbfftError):
+            fx.causal_conv_step(pool.clone(), x, w, out=out)
+    assert torch.equal(fx.causal_conv_step(pool.clone(), x, w, out=wide[:, d:]), want)
+    assert torch.equal(fx.causal_conv_step(pool.clone(), x, w, out=x), want)
+    delta, h = torch.randn(5, d, device="cuda"), torch.randn(5, d, n, device="cuda")
+    A, bc = -torch.rand(d, n, device="cuda") - 0.5, torch.randn(5, d + 2 * n, device="cuda")
+    B, C = bc[:, :n], bc[:, n:2 * n]
+
+    def step(**k):
+        return fx.selective_scan_step(h.clone(), wide[:, :d], delta, A, B, C, z=wide[:, d:], softplus=True, **k)
+
+    want = step()
+    for out in (wide[:, d - 8:2 * d - 8], bc[:, :d], bc[:, 8:d + 8]):
+        with pytest.raises(fx.GbfftError):
+            step(out=out)
+    for out in (wide[:, :d], delta, wide[:, d:]):
+        keep = out.clone()
+        assert torch.equal(step(out=out), want)
+        out.copy_(keep)

@@ -200,3 +200,12 @@ def test_scan_over_its_inputs_is_refused(lib):
     state = A + (9 << 12)
     assert lib.fft_scan_forward(scan(**apart, initial=state), sq._SEQ.pack(*at(5)), state, None, 0,
                                 None) == INVALID
+
+
+def test_steps_over_their_inputs_are_refused(lib):
+    one = conv(length=1, x=(A, 128, 16))
+    assert lib.fft_conv_step(one, sq._SEQ.pack(A + 16, 128, 16), A + 4096, 4, None, None, None) == INVALID
+    one = scan(length=1, u=(A, 128, 16), delta=(A + 4096, 128, 16), B=(A + 8192, 128, 16),
+               C=(A + 12288, 128, 16))
+    for at in (A + 16, A + 4096 + 16, A + 8192, A + 12288):
+        assert lib.fft_scan_step(one, sq._SEQ.pack(at, 128, 16), A + 16384, 4, None, None, None) == INVALID
