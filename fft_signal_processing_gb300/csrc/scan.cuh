@@ -96,6 +96,7 @@ __device__ __forceinline__ void copy_tile(T* dst, const T* p, int64_t stride, in
         constexpr int V = 16 / sizeof(T), R = CT / V;  // accesses of a row
         if constexpr (NT % R == 0 && TK % (NT / R) == 0) {
             constexpr int STEP = NT / R;
+            static_assert(STEP > 0, "the loop ends");
             const int j0 = tid / R, x = (tid - j0 * R) * V;
             const T* q = p + (t + j0) * stride + x;
 #pragma unroll
@@ -672,13 +673,12 @@ __global__ void __launch_bounds__(kLanesThreads) k_scan_lanes(const ScanArgs a) 
     }
 }
 
-// A state h carried over a chunk that takes it to exp2(x) h + local.  Steps below zero make states
-// grow, and exp2(x) may then be infinite where the product is not: with h = 0, nothing has grown, and
-// small states are multiplied in two steps.
-__device__ __forceinline__ float carried(float x, float h, float local) {
-    if (x <= 126.f) return fmaf(ex2(x), h, local);
-    const float e = ex2(0.5f * x);
-    return h == 0.f ? local : fmaf(e, e * h, local);
+// A state h carried over a chunk that takes it to e^2 h + local.  Steps below zero make states grow,
+// and e^2 may then be infinite where the product is not: it is multiplied in two halves, and a state
+// of 0 has not grown.  cut: the chunk does not go on from h.
+__device__ __forceinline__ float carried(float e, float h, float local, bool cut) {
+    const float grown = fmaf(e, e * h, local);
+    return cut | (h == 0.f) ? local : grown;
 }
 
 // Few threads and a chain of chunks: small blocks on many SMs, and many chunks loaded at once.
@@ -709,10 +709,12 @@ __global__ void __launch_bounds__(kCarryThreads) k_scan_carry(const ScanArgs a) 
             cut[j] = reset[i];
         }
 #pragma unroll
+        for (int j = 0; j < U; ++j) sum[j] = ex2(0.5f * A2 * sum[j]);
+#pragma unroll
         for (int j = 0; j < U; ++j) {
             if (k + j >= a.nchunks) break;
             carry[(k + j) * per] = h;
-            h = cut[j] ? local[j] : carried(A2 * sum[j], h, local[j]);
+            h = carried(sum[j], h, local[j], cut[j]);
         }
     }
 }

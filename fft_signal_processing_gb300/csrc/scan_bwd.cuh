@@ -280,10 +280,12 @@ __global__ void __launch_bounds__(kCarryThreads) k_scan_back_carry(const ScanBwd
             cut[j] = reset[i] || i == nch - 1;
         }
 #pragma unroll
+        for (int j = 0; j < U; ++j) sum[j] = ex2(0.5f * A2 * sum[j]);
+#pragma unroll
         for (int j = 0; j < U; ++j) {
             if (k - j < 0) break;
             carry[(k - j) * per] = m;
-            m = cut[j] ? local[j] : carried(A2 * sum[j], m, local[j]);
+            m = carried(sum[j], m, local[j], cut[j]);
         }
     }
 }
