@@ -217,7 +217,7 @@ __global__ void __launch_bounds__(kConvThreads) k_conv_fwd(const ConvArgs a) {
             for (int j = 0; j < N && i + j < len; ++j) {
                 if (b + i + j >= s.end) {  // packed: the next sequence begins here
                     const int64_t q = s.q;
-                    seq_next(a.d.offsets, a.d.nseq, a.d.length, b + i + j, &s);
+                    seq_next(a.d.offsets, a.d.nseq, b + i + j, &s);
                     if (s.q != q) refill(b + i + j);
                 }
                 win[W - 1] = widen<T, VEC>(row_at(j));
@@ -286,10 +286,9 @@ __device__ void conv_dinitial(const ConvArgs& a, int64_t q, int64_t c) {
 
 // Backward.  A run walks its tokens [b, e) and W-1 more: dp of the tokens up to e-1+(W-1) gives
 // dx of [b, e); only dp of its own tokens enters dweight and dbias.  The runs of a block are
-// summed in shared memory, one partial row per token tile.  Four channels and up to four taps fit the
-// 128 registers that two blocks of an SM leave; said to the compiler, which takes 134 otherwise.
+// summed in shared memory, one partial row per token tile.
 template <class T, int VEC, int W>
-__global__ void __launch_bounds__(kConvThreads, VEC == 4 && W <= 4 ? 2 : 0) k_conv_bwd(const ConvArgs a) {
+__global__ void __launch_bounds__(kConvThreads) k_conv_bwd(const ConvArgs a) {
     constexpr int P = Pairs<VEC>::P, N = kConvBatch, LANES = kConvLanes * VEC;
     using Ring = ConvRing<T, VEC, 2>;
     extern __shared__ uint2 ring_memory[];
@@ -424,7 +423,7 @@ __global__ void __launch_bounds__(kConvThreads, VEC == 4 && W <= 4 ? 2 : 0) k_co
                 if (i + j < there) {
                     if (t >= s.end) {  // packed: the next sequence begins here
                         const int64_t q = s.q;
-                        seq_next(a.d.offsets, a.d.nseq, a.d.length, t, &s);
+                        seq_next(a.d.offsets, a.d.nseq, t, &s);
                         if (s.q != q) refill(t);
                     }
                     win[W - 1] = widen<T, VEC>(x_at(j));
@@ -433,7 +432,7 @@ __global__ void __launch_bounds__(kConvThreads, VEC == 4 && W <= 4 ? 2 : 0) k_co
                 }
                 const int64_t td = t - (W - 1);  // dx[td] = sum_k weight[W-1-k] dp[td + k]
                 if (td >= b && dx) {
-                    if (td >= cur.end) seq_next(a.d.offsets, a.d.nseq, a.d.length, td, &cur);
+                    if (td >= cur.end) seq_next(a.d.offsets, a.d.nseq, td, &cur);
                     const int64_t end = cur.end < a.d.length ? cur.end : a.d.length;
                     Pairs<VEC> y = zeros<VEC>();
                     const int64_t fr = td + (W - 1) - end;  // row of the final state that td is

@@ -304,7 +304,7 @@ __global__ void __launch_bounds__(kPairThreads, 6) k_scan(const ScanArgs a) {
                     : nullptr;
     const int64_t ostr = a.out.tok_stride;
 
-    int stage = 0, buf = 0;
+    int stage = 0, buf = 0, stop = seq_stop(sq, blk.t0, len);
     for (int t = 0; t < len; t += TK) {
         copy_wait<ST - 2>();
         __syncthreads();  // this tile has landed; the last one's buffers are free
@@ -399,7 +399,7 @@ __global__ void __launch_bounds__(kPairThreads, 6) k_scan(const ScanArgs a) {
             }
         };
         const int64_t at = blk.t0 + t;
-        if (at + TK < sq.end) {  // no sequence ends here
+        if (t + TK < stop) {  // no sequence ends here
 #pragma unroll 1
             for (int j = 0; j < TK; j += kPairBatch) tokens(Count<kPairBatch>{}, j);
         } else {
@@ -408,7 +408,8 @@ __global__ void __launch_bounds__(kPairThreads, 6) k_scan(const ScanArgs a) {
             while (j < tl) {
                 if (at + j >= sq.end) {  // packed: the next sequence begins
                     const int64_t q = sq.q;
-                    seq_next(a.d.offsets, a.d.nseq, a.d.length, at + j, &sq);
+                    seq_next(a.d.offsets, a.d.nseq, at + j, &sq);
+                    stop = seq_stop(sq, blk.t0, len);
                     if (sq.q != q) {
                         initial();
                         has_reset = true;
@@ -531,7 +532,7 @@ __global__ void __launch_bounds__(kLanesThreads) k_scan_lanes(const ScanArgs a) 
                     : nullptr;
     const int64_t ostr = a.out.tok_stride;
 
-    int stage = 0, buf = 0;
+    int stage = 0, buf = 0, stop = seq_stop(sq, blk.t0, len);
     for (int t = 0; t < len; t += TK) {
         copy_wait<ST - 2>();
         __syncthreads();  // this tile has landed; the last one's buffers are free
@@ -575,7 +576,7 @@ __global__ void __launch_bounds__(kLanesThreads) k_scan_lanes(const ScanArgs a) 
             return y.x + y.y;
         };
         const int64_t at = blk.t0 + t;
-        if (at + TK < sq.end) {  // no sequence ends here
+        if (t + TK < stop) {  // no sequence ends here
 #pragma unroll 1
             for (int j0 = 0; j0 < TK; j0 += N) {
                 float2 d[(OWN + 1) / 2], du[(OWN + 1) / 2], uu[(OWN + 1) / 2];  // pairs of own tokens
@@ -631,7 +632,8 @@ __global__ void __launch_bounds__(kLanesThreads) k_scan_lanes(const ScanArgs a) 
             while (j < tl) {
                 if (at + j >= sq.end) {  // packed: the next sequence begins
                     const int64_t q = sq.q;
-                    seq_next(a.d.offsets, a.d.nseq, a.d.length, at + j, &sq);
+                    seq_next(a.d.offsets, a.d.nseq, at + j, &sq);
+                    stop = seq_stop(sq, blk.t0, len);
                     if (sq.q != q) {
                         initial();
                         has_reset = true;

@@ -212,32 +212,36 @@ __device__ __forceinline__ int64_t warp_count_le(const int64_t* offsets, int64_t
 }
 
 // The sequence that token t of a row belongs to: [begin, end) are its tokens.  Offsets lie on the
-// device and no host check sees them, so an end is held to the row: the kernels take a tile whole
-// where its sequence goes on behind it.
+// device and no host check sees them: q is a sequence that there is, begin and end may be anything.
 struct SeqAt {
     int64_t q, begin, end;
 };
-__host__ __device__ __forceinline__ SeqAt seq_span(const int64_t* offsets, int64_t nseq,
-                                                   int64_t length, int64_t q) {
+__host__ __device__ __forceinline__ SeqAt seq_span(const int64_t* offsets, int64_t nseq, int64_t q) {
     q = q < 0 ? 0 : (q >= nseq ? nseq - 1 : q);
-    const int64_t begin = offsets[q], end = offsets[q + 1];
-    return {q, begin < 0 ? 0 : begin, end < length ? end : length};
+    const int64_t begin = offsets[q];
+    return {q, begin < 0 ? 0 : begin, offsets[q + 1]};
 }
 // Dense rows: sequence q is the row itself.  Packed: found by the whole warp.
 __device__ __forceinline__ SeqAt seq_at(const int64_t* offsets, int64_t nseq, int64_t length,
                                         int64_t row, int64_t t) {
     if (!offsets) return {row, 0, length};
-    return seq_span(offsets, nseq, length, warp_count_le(offsets, nseq + 1, t) - 1);
+    return seq_span(offsets, nseq, warp_count_le(offsets, nseq + 1, t) - 1);
 }
 // The sequence that begins where s ends (token t = s.end), empty ones skipped.
-__host__ __device__ __forceinline__ void seq_next(const int64_t* offsets, int64_t nseq,
-                                                  int64_t length, int64_t t, SeqAt* s) {
+__host__ __device__ __forceinline__ void seq_next(const int64_t* offsets, int64_t nseq, int64_t t,
+                                                  SeqAt* s) {
     while (s->q + 1 < nseq && s->end <= t) {
         s->q += 1;
         s->begin = s->end < 0 ? 0 : s->end;
-        const int64_t end = offsets[s->q + 1];
-        s->end = end < length ? end : length;
+        s->end = offsets[s->q + 1];
     }
+}
+// The end of s counted from token t0 of a run of len tokens: len + 1 where s goes on behind the run.
+// A tile [t, t + n) with t + n < seq_stop lies within the run, whatever the offsets say, and s does
+// not end in it.
+__host__ __device__ __forceinline__ int seq_stop(const SeqAt& s, int64_t t0, int len) {
+    const int64_t end = s.end - t0;
+    return end > len ? len + 1 : (end < 0 ? 0 : (int)end);
 }
 
 // Whether the state of a scan starts anew at token t of its row: at a sequence's first token and,

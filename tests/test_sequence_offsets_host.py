@@ -27,22 +27,26 @@ int main(int argc, char** argv) {
         const int64_t t1 = t0 + chunk < length ? t0 + chunk : length, len = t1 - t0;
         int64_t below = 0;  // as warp_count_le counts on ascending values
         while (below <= nseq && offsets[below] <= t0) ++below;
-        SeqAt sq = seq_span(offsets, nseq, length, below - 1);
+        SeqAt sq = seq_span(offsets, nseq, below - 1);
         if (!starts_at(sq, t0)) {  // the chunk goes on from the state that the one before left
             if (t0 == 0) return 3;
             ++goes_on;
         }
+        int stop = seq_stop(sq, t0, (int)len);
         for (int64_t t = 0; t < len; t += tile) {
             const int64_t at = t0 + t;
             if (sq.q < 0 || sq.q >= nseq) return 2;
-            if (at + tile < sq.end) {
+            if (t + tile < stop) {
                 for (int64_t j = 0; j < tile; ++j) printf("%lld ", (long long)(at + j));
                 continue;
             }
             const int64_t tl = len - t < tile ? len - t : tile;
             int64_t j = 0;
             while (j < tl) {
-                if (at + j >= sq.end) seq_next(offsets, nseq, length, at + j, &sq);
+                if (at + j >= sq.end) {
+                    seq_next(offsets, nseq, at + j, &sq);
+                    stop = seq_stop(sq, t0, (int)len);
+                }
                 if (sq.q < 0 || sq.q >= nseq) return 2;
                 const int64_t je = sq.end > at + j && sq.end < at + tl ? sq.end - at : tl;
                 for (; j < je; ++j) printf("%lld ", (long long)(at + j));
