@@ -11,9 +11,9 @@
 // places in shared memory, three fours ahead, which keeps more loads in flight than the registers
 // would; inside a sequence the window slides by renaming, at sequence ends and in the halo tokens
 // go one by one.  2 (backward 3) values are moved per 2W (6W) operations: forward is bound by HBM
-// (4 x 4096 tokens of 4096 bfloat16 channels, W = 4: 51 us, 5.2 TB/s), backward by instruction
-// issue at the 16 warps of an SM that 125 registers allow (16001 packed tokens of 2000 channels:
-// 78 us, 2.5 TB/s, 2.0 instructions a cycle).  16 bytes a thread took so many registers that it
+// (4 x 4096 tokens of 4096 bfloat16 channels, W = 4: 51 us, 5.2 TB/s), backward by the
+// 16 warps of an SM that 126 registers leave (16001 packed tokens of 2000 channels:
+// 78 us, 2.5 TB/s, 2.0 of 4 instructions a cycle).  16 bytes a thread took so many registers that it
 // was slower (78 and 107 us at the time, against 72 and 89), 4 bytes too many instructions (83,
 // 107).
 #pragma once

@@ -23,7 +23,9 @@ constexpr int kConvMaxRun = 64;
 
 // Tokens of a run: of 64 and less, the number whose rounds of resident blocks (three to an SM
 // forward, two backward) take the fewest tokens' time, with the halo and about 8 tokens to start.
-// 16001 tokens of 2000 channels, backward: 56.
+// 16001 tokens of 2000 channels, backward: 56.  Three and two are what width 4 in 16 bits has; by
+// their registers other widths hold two to five and one to three, float32 three to six and two to
+// four, and the rule is used for them as it is.
 inline int conv_run_tokens(const fft_conv_desc& d, bool backward) {
     const int64_t lanes = d.dtype == FFT_F32 ? 2 : 4;  // channels of a lane
     const int64_t ctiles = (d.channels + kConvLanes * lanes - 1) / (kConvLanes * lanes);

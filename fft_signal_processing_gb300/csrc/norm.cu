@@ -4,12 +4,14 @@
 //   dr = rstd (w dy) - r rstd^3 mean(w dy r) + dresidual,  dweight = sum_rows dy r rstd.
 // A dozen operations per element: bound by HBM.  Each row is read once into registers (up to 16
 // values per thread), reduced across its threads, and written once.  Measured with inputs that
-// change from call to call: 16384 rows of 4096 bfloat16 with a bfloat16 residual to e4m3 83 us,
+// change from call to call: 16384 rows of 4096 bfloat16 with a bfloat16 residual to e4m3 82 us,
 // 5.7 TB/s (84% of the copy rate; 69 us from a clean L2); gradients of 8192 x 2560 bfloat16 with a
 // float32 residual 79 us, 4.2 TB/s, where five tensors per row leave room for two rows on their
 // way.  What carried it: weights in registers (reading them for every row filled the L1 port), a
 // ring of later rows in shared memory instead of registers (130 -> 81 us), sums over the warps of
-// a row by one shuffle tree instead of a loop.
+// a row by one shuffle tree instead of a loop.  Rows off 16-byte boundaries, which are loaded value by
+// value when they are needed, are far from that: 16384 x 4095 347 us, to e4m3 356, with a scale per
+// 128 columns 772 (an atomic maximum for every value).
 #include <cuda_fp8.h>
 
 #include "launch_cache.cuh"

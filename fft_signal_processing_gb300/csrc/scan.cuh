@@ -9,8 +9,8 @@
 // one load of B and C from shared memory serves both (with one channel per thread those loads
 // filled the shared-memory pipe).  More states, or more channels: k_scan_lanes, several lanes per
 // channel.  Measured, bfloat16, 16 states, gated: one sequence of 16384 x 2048 247 us (the
-// exponential unit 50 to 62% and the multiply-add pipe 56% busy at 12 warps of an SM), 8 x 2048 x
-// 4096 in one pass 410 us (34% and 44%).  What carried it: softplus and gates of 8 tokens side by
+// exponential unit 50 to 62% and the multiply-add pipe 57% busy at 12 warps of an SM), 8 x 2048 x
+// 4096 in one pass 404 us (35% and 45%).  What carried it: softplus and gates of 8 tokens side by
 // side (their chains are long: 175 -> 153 us for the last pass of the long sequence), and kernels
 // without questions for whole 16-byte rows (153 -> 136 us).
 //

@@ -19,10 +19,10 @@
 // with the values handed out to the lanes (each step halves what a lane carries).  Channel tiles
 // leave partial dB and dC, and chunks partial dA, dD, ddelta_bias, added up in a fixed order.
 //
-// Measured, 4 sequences of 2048 tokens, 2048 bfloat16 channels, 16 states, gated: 660 us, of which
-// the main kernel 384 (1.9 instructions a cycle at the 8 warps of an SM that 250 registers and 92
+// Measured, 4 sequences of 2048 tokens, 2048 bfloat16 channels, 16 states, gated: 666 us, of which
+// the main kernel 390 (1.9 instructions a cycle at the 8 warps of an SM that 250 registers and 92
 // KB of shared memory allow; about 415 instructions per token and 32 channels), the pass from
-// behind 89, the forward passes 58 and 69, the rest sums and carries.  Keeping questions about
+// behind 90, the forward passes 59 and 70, the rest sums and carries.  Keeping questions about
 // sequence ends out of whole tiles took the main kernel from 614 to 385 us.
 #pragma once
 

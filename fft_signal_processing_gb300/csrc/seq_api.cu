@@ -159,9 +159,15 @@ void scan_plan(ScanArgs* a) {
         return a->rows * d.groups * ((dg + ct - 1) / ct);
     };
     a->sl = scan_lanes(np);
-    // Uncut with two lanes per channel where that alone gives every SM four blocks or more (8
-    // sequences x 4096 channels: 0.44 ms, cut in two with k_scan 0.51 ms); else about six blocks of
-    // k_scan for every SM (one sequence of 16384 x 2048: 0.28 ms at 4 to 6, 0.33 ms at 5 or 8).
+    // Uncut with two lanes per channel where that alone gives every SM four blocks or more, else k_scan
+    // with time cut into as many chunks as give every SM about six blocks.  Measured, bfloat16, 16
+    // states, gated, 2048 tokens, by the SM's blocks of two lanes (us: two lanes uncut / k_scan at its
+    // best cut): 3.4 (4 x 4096 channels) 262 / 265, 4.2 (5 x 4096) 325 / 355, 5.1 327 / 373, 6.7 406 /
+    // 475; k_scan uncut takes 375 to 379 at all of these, so it is the faster one at 6.7, and with 8
+    // states (265 / 235 at 4.2, 313 / 265 at 6.7) the rule is not the best.  Blocks of k_scan to an SM,
+    // 2 / 3 / 4 / 5 / 6 / 7 / 8: one sequence of 16384 x 2048 287 326 250 295 250 293 262; 4 of 4096 x
+    // 2048 377 327 297 295 262 293 262; 3 of 5000 x 2000 286 289 287 272 241 276 247; one of 4096 x
+    // 2048 94 106 87 103 98 106 106.
     const int64_t sms = num_sms();
     int64_t k = 1;
     if ((np == 8 || np == 16) && scan_out_np(d.states) != 12 && blocks(2) >= sms * 4)

@@ -14,7 +14,8 @@ Sequences are [sequences, tokens, channels] or, with `offsets` (int64, on the de
 ascending values from 0 to the number of tokens), packed [tokens, channels]; sequences may be without
 tokens and batches without sequences.  The last axis is
 contiguous, the others may have any stride: halves of a projection need no copy.  The *_backward
-calls return the gradients; nothing is recorded for autograd.  The *_step calls take one token per
+calls return the gradients; nothing is recorded for autograd, and outputs of inputs that require
+gradients do not require any.  The *_step calls take one token per
 sequence and move its state from slots[i] to slots_out[i] of a pool (in place by default).
 Outputs and workspaces are allocated by torch on the stream that the call runs on.
 """
@@ -282,7 +283,8 @@ def causal_conv(x, weight, bias=None, silu=False, initial_state=None, offsets=No
                 return_state=False, out=None, stream=None):
     """Short causal convolution of every channel (fft_conv_forward): weight [channels, width],
     bias [channels], both float32 or of x's type; initial_state [sequences, width-1, channels].
-    out may not overlap x.  Returns out, or (out, final_state)."""
+    out may not overlap x.  Returns out, or (out, final_state).  Not recorded for autograd: gradients
+    come from causal_conv_backward."""
     desc, dev, nseq, d, w = _conv_desc(x, weight, bias, silu, initial_state, offsets)
     on, s = _stream(stream, dev)
     with on:
@@ -316,7 +318,9 @@ def causal_conv_backward(dout, x, weight, bias=None, silu=False, initial_state=N
 def causal_conv_step(state, x, weight, bias=None, silu=False, slots=None, slots_out=None, out=None,
                      stream=None):
     """One token for each sequence (fft_conv_step): x [sequences, channels], state the pool
-    [pool, width-1, channels], updated in place; slots, slots_out int64 [sequences]."""
+    [pool, width-1, channels], updated in place; slots, slots_out int64 [sequences].  A slot outside
+    the pool marks a padding row (output 0, no state written); a slot that one sequence writes may
+    not be read or written by another.  out may be x itself."""
     code, dev = _first(x, "x")
     dtype, shape = x.dtype, x.shape
     if len(shape) != 2 or weight.dim() != 2:
@@ -380,7 +384,8 @@ def selective_scan(u, delta, A, B, C, D=None, z=None, delta_bias=None, softplus=
     """Selective state-space scan (fft_scan_forward): u, delta, z [..., channels], A [channels, n],
     B, C [..., groups, n] or [..., n], D, delta_bias [channels]; states [sequences, channels, n].
     A, D, delta_bias and states are float32.  out may be u or z and overlaps no other input.
-    Returns out, or (out, final_state)."""
+    Returns out, or (out, final_state).  Not recorded for autograd: gradients come from
+    selective_scan_backward."""
     desc, dev, nseq, d, n = _scan_desc(u, delta, A, B, C, D, z, delta_bias, softplus,
                                        initial_state, offsets)
     on, s = _stream(stream, dev)
@@ -424,7 +429,8 @@ def selective_scan_step(state, u, delta, A, B, C, D=None, z=None, delta_bias=Non
                         slots=None, slots_out=None, out=None, stream=None):
     """One token for each sequence (fft_scan_step): u, delta, z [sequences, channels], B, C
     [sequences, groups, n] or [sequences, n], state the pool [pool, channels, n] float32, updated
-    in place; slots, slots_out int64 [sequences]."""
+    in place; slots, slots_out int64 [sequences] as in causal_conv_step.  out may be u, delta or z
+    itself."""
     code, dev = _first(u, "u")
     f32, dtype, shape, bshape = torch.float32, u.dtype, u.shape, B.shape
     if len(shape) != 2 or len(bshape) not in (2, 3) or bshape[0] != shape[0]:
@@ -498,7 +504,8 @@ def residual_norm(x, weight, residual=None, eps=1e-6, out_dtype=None, group=0, o
     """Root-mean-square norm of x + residual (fft_norm_forward), rows along the last axis: NormOut.
     residual is of x's type or float32, and so is the sum that is returned (written over it with
     inplace_residual).  out_dtype torch.float8_e4m3fn: out in 8 bits with scale
-    [..., ceil(columns / group)], group 32, 64 or 128 columns, or 0 for one scale per row."""
+    [..., ceil(columns / group)], group 32, 64 or 128 columns, or 0 for one scale per row.  Not
+    recorded for autograd: gradients come from residual_norm_backward."""
     if _L is None:
         _setup()
     dtype, shape = x.dtype, x.shape
