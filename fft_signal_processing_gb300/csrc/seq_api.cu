@@ -3,6 +3,7 @@
 #include "conv.h"
 #include "scan.h"
 #include "scan_bwd.h"
+#include "seq_overlap.h"
 #include "seq_step.h"
 
 using namespace gbfft;
@@ -34,44 +35,6 @@ int check_sizes(int64_t nseq, int64_t length, int64_t channels, const int64_t* o
     if (nseq > INT32_MAX || length > INT32_MAX - 65536 || channels > INT32_MAX / 256)
         return FFT_ERR_UNSUPPORTED_SIZE;
     return aligned_to(offsets, 8) ? FFT_OK : FFT_ERR_MISALIGNED;
-}
-
-// Bytes that a sequence tensor's rows of `width` values may touch, from its first value on.
-int64_t seq_span_bytes(const fft_seq& s, int64_t width, int64_t nseq, int64_t length, bool packed,
-                       size_t size) {
-    if (!s.data || length < 1) return 0;
-    return ((packed ? 0 : (nseq - 1) * s.seq_stride) + (length - 1) * s.tok_stride + width) * (int64_t)size;
-}
-bool bytes_meet(const void* a, int64_t na, const void* b, int64_t nb) {
-    const uintptr_t x = (uintptr_t)a, y = (uintptr_t)b;
-    return a && b && na > 0 && nb > 0 && x < y + nb && y < x + na;
-}
-// Whether two sequence tensors share values.  Spans may meet without that, as those of two halves of
-// one projection do: every row of both starts a multiple of the strides' common divisor after the
-// first one of its tensor, so the columns modulo it tell them apart.
-bool seqs_meet(const fft_seq& a, const fft_seq& b, int64_t width, int64_t bwidth, int64_t nseq,
-               int64_t length, bool packed, size_t size) {
-    if (!bytes_meet(a.data, seq_span_bytes(a, width, nseq, length, packed, size), b.data,
-                    seq_span_bytes(b, bwidth, nseq, length, packed, size)))
-        return false;
-    int64_t period = 0;
-    auto add = [&](int64_t stride) {
-        while (stride) {
-            const int64_t r = period % stride;
-            period = stride;
-            stride = r;
-        }
-    };
-    if (length > 1) add(a.tok_stride), add(b.tok_stride);
-    if (!packed && nseq > 1) add(a.seq_stride), add(b.seq_stride);
-    if (!period) return true;
-    const int64_t apart = ((intptr_t)b.data - (intptr_t)a.data) / (int64_t)size % period;
-    const int64_t column = apart < 0 ? apart + period : apart;  // of b's rows, a's being 0
-    return column < width || column + bwidth > period;
-}
-bool seqs_same(const fft_seq& a, const fft_seq& b, int64_t nseq, int64_t length, bool packed) {
-    return a.data == b.data && (length < 2 || a.tok_stride == b.tok_stride) &&
-           (packed || nseq < 2 || a.seq_stride == b.seq_stride);
 }
 
 #define TRY(x)                        \

@@ -142,3 +142,55 @@ def test_steps_over_their_inputs():
         keep = out.clone()
         assert torch.equal(step(out=out), want)
         out.copy_(keep)
+
+
+@pytest.mark.parametrize("nseq", [1, 3])
+def test_ranges_of_tokens_of_one_buffer(nseq):
+    """The spans of two ranges of tokens meet where there are several sequences; values do not."""
+    import fft_signal_processing_gb300 as fx
+
+    torch.manual_seed(5)
+    d, n = 16, 8
+    w = torch.randn(d, 4, device="cuda")
+    buf = torch.randn(nseq, 40, d, device="cuda")
+    x = buf[:, :20]
+    keep, want = x.clone(), fx.causal_conv(x, w)
+    assert torch.equal(fx.causal_conv(x, w, out=buf[:, 20:]), want)
+    assert torch.equal(buf[:, 20:], want) and torch.equal(x, keep)
+    back = fx.causal_conv(buf[:, 20:], w)
+    assert torch.equal(fx.causal_conv(buf[:, 20:], w, out=x), back)
+    for out in (buf[:, 19:39], buf[:, 1:21]):
+        with pytest.raises(fx.GbfftError):
+            fx.causal_conv(x, w, out=out)
+    A, B = -torch.rand(d, n, device="cuda") - 0.5, torch.randn(nseq, 20, n, device="cuda")
+    want = fx.selective_scan(buf[:, :20], keep, A, B, B)
+    assert torch.equal(fx.selective_scan(buf[:, :20], keep, A, B, B, out=buf[:, 20:]), want)
+    with pytest.raises(fx.GbfftError):
+        fx.selective_scan(buf[:, :20], keep, A, B, B, out=buf[:, 5:25])
+
+
+def test_refusals_are_the_shared_values():
+    """Against sets of addresses, for tensors of the same strides in one buffer."""
+    import fft_signal_processing_gb300 as fx
+
+    rng = torch.Generator().manual_seed(6)
+    buf = torch.zeros(1200, device="cuda")
+    w = torch.ones(3, 2, device="cuda")
+    seen = [0, 0]
+    for _ in range(300):
+        pick = lambda lo, hi: int(torch.randint(lo, hi, (1,), generator=rng))
+        nseq, length, tok = pick(1, 4), pick(1, 5), pick(3, 12)
+        seq = pick(3, 40) if pick(0, 2) else tok * length + pick(0, 9)
+        at = [[o + q * seq + t * tok + c for q in range(nseq) for t in range(length) for c in range(3)]
+              for o in (pick(0, 60), pick(0, 60))]
+        if len(set(at[0])) < len(at[0]) or len(set(at[1])) < len(at[1]):
+            continue  # rows of one tensor overlap
+        x, out = (buf.as_strided((nseq, length, 3), (seq, tok, 1), a[0]) for a in at)
+        meet = bool(set(at[0]) & set(at[1]))
+        seen[meet] += 1
+        if meet:
+            with pytest.raises(fx.GbfftError):
+                fx.causal_conv(x, w, out=out)
+        else:
+            fx.causal_conv(x, w, out=out)
+    assert min(seen) > 20
