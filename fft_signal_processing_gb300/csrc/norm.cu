@@ -16,6 +16,7 @@
 
 #include "launch_cache.cuh"
 #include "seq_common.cuh"
+#include "seq_overlap.h"
 
 namespace gbfft {
 namespace {
@@ -592,6 +593,18 @@ bool stride_ok(const void* p, int64_t stride, const fft_norm_desc* d) {
     return !p || stride >= d->columns || (d->rows <= 1 && stride >= 0);
 }
 
+// Whether rows that are written lie over rows that are read without being the same ones: a thread
+// reads what it writes, and later rows are copied ahead.
+bool rows_clash(const void* out, int64_t out_stride, size_t out_size, const void* in, int64_t in_stride,
+                size_t in_size, const fft_norm_desc* d) {
+    if (!out || !in || (out == in && out_size == in_size && (out_stride == in_stride || d->rows == 1)))
+        return false;
+    const fft_seq a = {const_cast<void*>(out), 0, out_stride * (int64_t)out_size};
+    const fft_seq b = {const_cast<void*>(in), 0, in_stride * (int64_t)in_size};
+    return seqs_meet(a, b, d->columns * (int64_t)out_size, d->columns * (int64_t)in_size, 1, d->rows,
+                     false, 1);
+}
+
 }  // namespace
 
 cudaError_t run_sum_parts(const float* parts, int64_t nparts, int64_t stride, int64_t cols,
@@ -626,6 +639,12 @@ extern "C" int fft_norm_forward(const fft_norm_desc* d, const void* x, int64_t x
         !aligned_to(d->weight, dtype_size(d->param_dtype)))
         return FFT_ERR_MISALIGNED;
     if (!rows) return FFT_OK;
+    const size_t o = dtype_size(d->out_dtype);
+    if (rows_clash(out, out_stride, o, x, x_stride, e, d) ||
+        rows_clash(out, out_stride, o, residual, residual_stride, r, d) ||
+        rows_clash(sum, sum_stride, r, x, x_stride, e, d) ||
+        rows_clash(sum, sum_stride, r, residual, residual_stride, r, d))
+        return FFT_ERR_INVALID_ARG;
     const NormArgs a = {x, residual, out, scale, sum, d->weight, x_stride, residual_stride,
                         out_stride, sum_stride, d->rows, (int)d->columns, d->param_dtype == FFT_F32,
                         aligned_to(d->weight, 16), (int)d->group, (float)d->columns, d->eps};

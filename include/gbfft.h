@@ -494,8 +494,8 @@ typedef struct fft_norm_desc {
  * dtype, or FFT_E4M3 with scale (float32 [rows][ceil(columns/group)], contiguous):
  *   m = max |y| over the group;  scale = m / 448;  out = e4m3(y * (448 / m)), 0 where m = 0.
  * A NaN in a group makes its scale NaN.  sum: receives r rounded to res_dtype, NULL: not
- * written; it may be the residual itself (in place), and out may be x itself; other overlaps are
- * errors of the caller.  No rows: nothing is done, and pointers may be NULL. */
+ * written.  Either of out and sum may be x or the residual themselves (same type and stride); another
+ * overlap with what is read is refused (FFT_ERR_INVALID_ARG).  No rows: nothing is done, and pointers may be NULL. */
 int fft_norm_forward(const fft_norm_desc* d, const void* x, int64_t x_stride, const void* residual,
                      int64_t residual_stride, void* out, int64_t out_stride, float* scale,
                      void* sum, int64_t sum_stride, void* stream);

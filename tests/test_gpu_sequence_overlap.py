@@ -194,3 +194,35 @@ def test_refusals_are_the_shared_values():
         else:
             fx.causal_conv(x, w, out=out)
     assert min(seen) > 20
+
+
+def test_norm_over_its_inputs():
+    import fft_signal_processing_gb300 as fx
+
+    torch.manual_seed(7)
+    w = torch.randn(128, device="cuda")
+    wide = torch.randn(700, 400, device="cuda").bfloat16()
+    x, res = wide[:, :128], wide[:, 128:256]
+    want = fx.residual_norm(x, w, residual=res)
+    q = fx.residual_norm(x, w, residual=res, out_dtype=torch.float8_e4m3fn)
+    for out in (wide[:, 8:136], wide[:, 120:248], wide[:, 200:328]):
+        with pytest.raises(fx.GbfftError):
+            fx.residual_norm(x, w, residual=res, out=out)
+    with pytest.raises(fx.GbfftError):  # 8 bits over the second half of x
+        fx.residual_norm(x, w, residual=res, out_dtype=torch.float8_e4m3fn,
+                         out=wide.view(torch.float8_e4m3fn)[:, 128:256])
+    spare = wide.view(torch.float8_e4m3fn)[:, 512:640]
+    got = fx.residual_norm(x, w, residual=res, out_dtype=torch.float8_e4m3fn, out=spare)
+    assert torch.equal(got.out.view(torch.uint8), q.out.view(torch.uint8))
+    keep = wide.clone()
+    for out in (wide[:, 256:384], x, res):
+        got = fx.residual_norm(x, w, residual=res, out=out)
+        assert torch.equal(got.out, want.out) and torch.equal(got.residual, want.residual)
+        wide.copy_(keep)
+    got = fx.residual_norm(x, w, residual=res, inplace_residual=True, out=x)
+    assert torch.equal(got.out, want.out) and torch.equal(res, want.residual)
+    rows = torch.randn(300, 128, device="cuda")
+    with pytest.raises(fx.GbfftError):
+        fx.residual_norm(rows[:200], w, out=rows[1:201])
+    want = fx.residual_norm(rows[::2], w).out
+    assert torch.equal(fx.residual_norm(rows[::2], w, out=rows[1::2]).out, want)

@@ -209,3 +209,13 @@ def test_steps_over_their_inputs_are_refused(lib):
                C=(A + 12288, 128, 16))
     for at in (A + 16, A + 4096 + 16, A + 8192, A + 12288):
         assert lib.fft_scan_step(one, sq._SEQ.pack(at, 128, 16), A + 16384, 4, None, None, None) == INVALID
+
+
+def test_norm_over_its_inputs_is_refused(lib):
+    d = norm()
+    for at in (A + 2, A + 16, A - 126):
+        assert lib.fft_norm_forward(d, A, 64, None, 0, at, 64, None, None, 0, None) == INVALID
+        assert lib.fft_norm_forward(norm(res=sq.BF16), A + 8192, 64, A, 64, A + 16384, 64, None, at, 64,
+                                    None) == INVALID
+    q = norm(out=sq.E4M3)
+    assert lib.fft_norm_forward(q, A, 64, None, 0, A, 64, A + 8192, None, 0, None) == INVALID
