@@ -24,7 +24,9 @@ import ctypes
 import os
 
 from . import sequence
-from .sequence import (causal_conv, causal_conv_backward, causal_conv_step, residual_norm,
+from .sequence import (causal_conv, causal_conv_backward, causal_conv_step, group_norm,
+                       group_norm_backward, linear_attention,
+                       linear_attention_backward, linear_attention_step, residual_norm,
                        residual_norm_backward, selective_scan, selective_scan_backward,
                        selective_scan_step)
 

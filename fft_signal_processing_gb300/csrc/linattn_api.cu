@@ -1,0 +1,662 @@
+// C entry points of linear attention: checks on the host, cuts of time, workspace layout, and the
+// kernels around k_linattn (gradients of the decay and of shared heads, states of sequences without
+// tokens, single tokens).  Declared in include/gbfft.h.
+#include "linattn.h"
+#include "seq_overlap.h"
+
+namespace gbfft {
+namespace {
+
+// ---- single tokens --------------------------------------------------------------------------
+
+constexpr int kStepThreads = 128, kStepCols = 32;
+
+struct AttnStepArgs {
+    fft_linattn_desc d;
+    fft_heads out;
+    float* state;
+    const int64_t* slots;
+    const int64_t* slots_out;
+    int64_t pool;
+    int ctiles;
+};
+
+// A block takes 32 columns of one head's state: VEC columns per thread, so 32 / VEC lanes hold a row
+// and the rows are dealt to groups of lanes, four loads of each under way at once.
+template <class T, int VEC>
+__global__ void __launch_bounds__(kStepThreads) k_linattn_step(const AttnStepArgs a) {
+    constexpr int LANES = kStepCols / VEC, GROUPS = kStepThreads / LANES, DEEP = VEC == 4 ? 8 : 4;
+    __shared__ float red[GROUPS][kStepCols + 1];
+    const int lane = (int)threadIdx.x % LANES, group = (int)threadIdx.x / LANES;
+    int64_t b = blockIdx.x;
+    const int ct = (int)(b % a.ctiles);
+    b /= a.ctiles;
+    const int64_t h = b % a.d.heads, q = b / a.d.heads, g = h / (a.d.heads / a.d.groups);
+    const int dk = (int)a.d.dk, dv = (int)a.d.dv, c = ct * kStepCols + lane * VEC;
+    const bool in = c < dv;
+    const int64_t from = a.slots ? a.slots[q] : q, to = a.slots_out ? a.slots_out[q] : from;
+    const bool live = from >= 0 && from < a.pool && to >= 0 && to < a.pool;
+    const T* qp = static_cast<const T*>(a.d.q.data) + q * a.d.q.seq_stride + g * a.d.q.head_stride;
+    const T* kp = static_cast<const T*>(a.d.k.data) + q * a.d.k.seq_stride + g * a.d.k.head_stride;
+    const T* vp = static_cast<const T*>(a.d.v.data) + q * a.d.v.seq_stride + h * a.d.v.head_stride + c;
+    const float gl = to_f(static_cast<const T*>(a.d.decay.data)[q * a.d.decay.seq_stride + h]);
+    float y[VEC] = {};
+    if (live) {
+        const float e = ex2((gl > 0.f ? 0.f : (gl < -200.f ? -200.f : gl)) * kLog2e);
+        const int64_t per = (int64_t)dk * dv;
+        const float* src = a.state + (from * a.d.heads + h) * per + c;
+        float* dst = a.state + (to * a.d.heads + h) * per + c;
+        float v[VEC];
+#pragma unroll
+        for (int k = 0; k < VEC; ++k) v[k] = in ? to_f(vp[k]) : 0.f;
+        for (int r0 = group; r0 < dk; r0 += GROUPS * DEEP) {
+            Pack<float, VEC> s[DEEP];
+            float qv[DEEP], kv[DEEP];
+#pragma unroll
+            for (int i = 0; i < DEEP; ++i) {
+                const int r = r0 + i * GROUPS;
+                if (r < dk && in) s[i] = ld_pack<VEC>(src + (int64_t)r * dv);
+                qv[i] = r < dk ? to_f(qp[r]) : 0.f;
+                kv[i] = r < dk ? to_f(kp[r]) : 0.f;
+            }
+#pragma unroll
+            for (int i = 0; i < DEEP; ++i) {
+                const int r = r0 + i * GROUPS;
+                if (r < dk && in) {
+#pragma unroll
+                    for (int k = 0; k < VEC; ++k) {
+                        s[i].v[k] = fmaf(e, s[i].v[k], kv[i] * v[k]);
+                        y[k] = fmaf(qv[i], s[i].v[k], y[k]);
+                    }
+                    st_pack<VEC>(dst + (int64_t)r * dv, s[i]);
+                }
+            }
+        }
+    }
+#pragma unroll
+    for (int k = 0; k < VEC; ++k) red[group][lane * VEC + k] = y[k];
+    __syncthreads();
+    const int t = (int)threadIdx.x;
+    if (t < kStepCols && ct * kStepCols + t < dv) {
+        float sum = 0.f;
+#pragma unroll
+        for (int i = 0; i < GROUPS; ++i) sum += red[i][t];
+        static_cast<T*>(a.out.data)[q * a.out.seq_stride + h * a.out.head_stride + ct * kStepCols + t] =
+            from_f<T>(live ? sum * a.d.scale : 0.f);
+    }
+}
+
+template <class T>
+cudaError_t attn_step(AttnStepArgs a, cudaStream_t s) {
+    a.ctiles = (int)((a.d.dv + kStepCols - 1) / kStepCols);
+    const int64_t blocks = a.d.nseq * a.d.heads * a.ctiles;
+    if (blocks > INT32_MAX) return cudaErrorInvalidValue;
+    if (a.d.dv % 4 == 0 && aligned_to(a.state, 16))
+        k_linattn_step<T, 4><<<(unsigned)blocks, kStepThreads, 0, s>>>(a);
+    else
+        k_linattn_step<T, 1><<<(unsigned)blocks, kStepThreads, 0, s>>>(a);
+    return cudaGetLastError();
+}
+
+// ---- around the kernel of whole sequences ---------------------------------------------------
+
+// States of sequences without tokens: what they begin with.
+__global__ void k_linattn_empty(const int64_t* offsets, const float* from, float* to, int64_t per) {
+    const int64_t q = blockIdx.x;
+    if (offsets[q + 1] > offsets[q]) return;
+    for (int64_t i = threadIdx.x; i < per; i += blockDim.x) to[q * per + i] = from ? from[q * per + i] : 0.f;
+}
+
+// Sums over the heads that share queries or keys.
+template <class T>
+__global__ void k_linattn_shared(const float* parts, fft_heads out, int64_t length, int64_t groups, int64_t share,
+                                 int64_t dim, int64_t total) {
+    const int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
+    if (i >= total) return;
+    const int64_t d = i % dim, g = i / dim % groups, t = i / (dim * groups);
+    const float* p = parts + (t * groups * share + g * share) * dim + d;
+    float v = 0.f;
+    for (int64_t h = 0; h < share; ++h) v += p[h * dim];
+    static_cast<T*>(out.data)[t / length * out.seq_stride + t % length * out.tok_stride + g * out.head_stride + d] =
+        from_f<T>(v);
+}
+
+struct DecayGradArgs {
+    fft_seq decay, ddecay;
+    const int64_t* offsets;
+    int64_t nseq, length, rows, heads, segment, nsegments, ztiles;
+    int initial;  // sequences have initial states
+    // [ztile][head][row * length + t]: of the rows of dq and dk, between chunks and altogether
+    const float* q_inter;
+    const float* q_all;
+    const float* k_inter;
+    const float* k_all;
+    const float* final_dots;  // [ztile][sequence][head], or null
+    double* carry;            // [row][segment][head]
+    int* stops;
+};
+
+__device__ __forceinline__ float tiles_sum(const float* p, int64_t tiles, int64_t step) {
+    float v = 0.f;
+    for (int64_t z = 0; z < tiles; ++z) v += p[z * step];
+    return v;
+}
+
+// Pairs (j, i) of tokens j < t <= i weigh w[j,i] = scale decay(j, i) (q[i] k[j]) (dout[i] v[j]), and
+// the gradient of decay t is the sum of them all (initial and final states count as tokens before and
+// behind the sequence).  With X the sum over the pairs that cross a chunk's first token,
+//   dg[t] = X - sum_{i < t} qi[i] + sum_{j < t} ki[j] + sum_{i >= t} (qa[i] - ka[i])
+// over the chunk's tokens, where qi and ki are those rows' pairs with tokens of other chunks and qa,
+// ka those within the chunk; X in turn is that of the next chunk and what the rows between change.
+// Only between chunks do such sums run on, over terms that were formed from states in two or three
+// pieces, so that what cancels within a chunk is not carried along.
+// One block per segment and head; a warp takes every eighth chunk, two tokens per lane.
+constexpr int kDgWarps = 8, kDgBatch = 64;
+
+// What the tokens of a segment's first sequence change (X at the segment's start less that at its
+// end), and whether that sequence ends there.
+__global__ void __launch_bounds__(kDgWarps * 32) k_decay_sums(const DecayGradArgs a) {
+    __shared__ double red[kDgWarps];
+    const int64_t head = blockIdx.x % a.heads, seg = blockIdx.x / a.heads % a.nsegments,
+                  row = blockIdx.x / (a.heads * a.nsegments);
+    const int64_t t0 = seg * a.segment, t1 = t0 + a.segment < a.length ? t0 + a.segment : a.length;
+    const SeqAt s = seq_at(a.offsets, a.nseq, a.length, row, t0);
+    const int64_t end = s.end > t1 || s.end <= t0 ? t1 : s.end;
+    const int64_t step = a.heads * a.rows * a.length, at = (head * a.rows + row) * a.length;
+    double v = 0.0;
+    for (int64_t t = t0 + threadIdx.x; t < end; t += kDgWarps * 32)
+        v += (double)tiles_sum(a.q_inter + at + t, a.ztiles, step) - (double)tiles_sum(a.k_inter + at + t, a.ztiles, step);
+#pragma unroll
+    for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    if ((threadIdx.x & 31) == 0) red[threadIdx.x / 32] = v;
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        for (int w = 1; w < kDgWarps; ++w) v += red[w];
+        a.carry[blockIdx.x] = v;
+        a.stops[blockIdx.x] = s.end <= t1;
+    }
+}
+
+template <class T>
+__global__ void __launch_bounds__(kDgWarps * 32) k_decay_grads(const DecayGradArgs a) {
+    __shared__ double change[kDgBatch], cross[kDgBatch];
+    const int64_t head = blockIdx.x % a.heads, seg = blockIdx.x / a.heads % a.nsegments,
+                  row = blockIdx.x / (a.heads * a.nsegments);
+    const int64_t t0 = seg * a.segment, t1 = t0 + a.segment < a.length ? t0 + a.segment : a.length;
+    const int64_t step = a.heads * a.rows * a.length, at = (head * a.rows + row) * a.length;
+    const int lane = (int)threadIdx.x & 31, warp = (int)threadIdx.x >> 5;
+    auto sum2 = [&](const float* p, int64_t t, int64_t end) {
+        return make_float2(t < end ? tiles_sum(p + at + t, a.ztiles, step) : 0.f,
+                           t + 1 < end ? tiles_sum(p + at + t + 1, a.ztiles, step) : 0.f);
+    };
+    for (int64_t stop = t1; stop > t0;) {
+        const SeqAt s = seq_at(a.offsets, a.nseq, a.length, row, stop - 1);
+        const int64_t begin = s.begin > stop - 1 ? stop - 1 : (s.begin < t0 ? t0 : s.begin), end = stop;
+        double X = 0.0;  // at `end`
+        if (s.end <= end || end == a.length) {
+            if (a.final_dots)
+                for (int64_t z = 0; z < a.ztiles; ++z) X += a.final_dots[(z * a.nseq + s.q) * a.heads + head];
+        } else {
+            int64_t k = seg + 1;
+            for (; k < a.nsegments; ++k) {
+                const int64_t i = (row * a.nsegments + k) * a.heads + head;
+                X += a.carry[i];
+                if (a.stops[i]) break;
+            }
+            if (a.final_dots)
+                for (int64_t z = 0; z < a.ztiles; ++z) X += a.final_dots[(z * a.nseq + s.q) * a.heads + head];
+        }
+        const int64_t chunks = (end - begin + kAttnChunk - 1) / kAttnChunk;
+        for (int64_t c1 = chunks; c1 > 0; c1 -= kDgBatch) {
+            const int64_t c0 = c1 > kDgBatch ? c1 - kDgBatch : 0;
+            for (int64_t c = c0 + warp; c < c1; c += kDgWarps) {
+                const int64_t t = begin + c * kAttnChunk + 2 * lane;
+                const float2 qi = sum2(a.q_inter, t, end), ki = sum2(a.k_inter, t, end);
+                double v = ((double)qi.x - ki.x) + ((double)qi.y - ki.y);
+                // tokens of the next chunk are not this one's: a chunk is 64 = 2 x 32 tokens
+#pragma unroll
+                for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+                if (lane == 0) change[c - c0] = v;
+            }
+            __syncthreads();
+            if (threadIdx.x == 0)
+                for (int64_t c = c1 - 1; c >= c0; --c) cross[c - c0] = X += change[c - c0];
+            __syncthreads();
+            X = cross[0];
+            // nothing crosses a sequence's first token but its initial state
+            const bool zero = c0 == 0 && !a.initial && (begin == 0 || s.begin == begin);
+            for (int64_t c = c0 + warp; c < c1; c += kDgWarps) {
+                const int64_t t = begin + c * kAttnChunk + 2 * lane;
+                const float2 qi = sum2(a.q_inter, t, end), ki = sum2(a.k_inter, t, end);
+                const float2 qa = sum2(a.q_all, t, end), ka = sum2(a.k_all, t, end);
+                // between chunks: what tokens before t have, from the left
+                const float n0 = ki.x - qi.x, n1 = ki.y - qi.y;
+                float left = n0 + n1;
+#pragma unroll
+                for (int o = 1; o < 32; o *= 2) {
+                    const float v = __shfl_up_sync(0xffffffffu, left, o);
+                    if (lane >= o) left += v;
+                }
+                left = __shfl_up_sync(0xffffffffu, left, 1);
+                if (lane == 0) left = 0.f;
+                // within the chunk, from the right
+                const float w0 = (qa.x - qi.x) - (ka.x - ki.x), w1 = (qa.y - qi.y) - (ka.y - ki.y);
+                float right = w0 + w1;
+#pragma unroll
+                for (int o = 1; o < 32; o *= 2) {
+                    const float v = __shfl_down_sync(0xffffffffu, right, o);
+                    if (lane + o < 32) right += v;
+                }
+                const float base = zero && c == 0 ? 0.f : (float)cross[c - c0];
+                const float dg[2] = {base + left + right, base + (left + n0) + (right - w0)};
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    if (t + k >= end) continue;
+                    const float g = to_f(static_cast<const T*>(a.decay.data)[row * a.decay.seq_stride +
+                                                                           (t + k) * a.decay.tok_stride + head]);
+                    // above 0 the decay is 0 whatever its value, below -104 its exponential is
+                    const float v = g > 0.f || g < -104.f ? 0.f : dg[k];
+                    static_cast<T*>(a.ddecay.data)[row * a.ddecay.seq_stride + (t + k) * a.ddecay.tok_stride + head] =
+                        from_f<T>(v);
+                }
+            }
+            __syncthreads();
+        }
+        stop = begin;
+    }
+}
+
+// ---- checks and plans -----------------------------------------------------------------------
+
+constexpr int64_t kMaxElements = INT64_C(1) << 58, kMaxTokStride = INT64_C(1) << 26;
+
+int status(cudaError_t e) {
+    return e == cudaSuccess ? FFT_OK : (e == cudaErrorInvalidValue ? FFT_ERR_UNSUPPORTED_SIZE : FFT_ERR_CUDA);
+}
+
+#define TRY(x)                         \
+    do {                               \
+        const int rc_ = (x);           \
+        if (rc_ != FFT_OK) return rc_; \
+    } while (0)
+
+// Rows of an output must lie apart: from the axis of the smallest stride on, each stride is beyond
+// what the axes before it take.
+bool rows_apart(const fft_heads& t, int64_t dim, int64_t heads, int64_t nseq, int64_t length) {
+    int64_t stride[3] = {t.head_stride, t.tok_stride, t.seq_stride}, count[3] = {heads, length, nseq};
+    for (int i = 0; i < 2; ++i)
+        for (int j = 0; j < 2 - i; ++j)
+            if (stride[j] > stride[j + 1]) {
+                int64_t v = stride[j];
+                stride[j] = stride[j + 1], stride[j + 1] = v;
+                v = count[j], count[j] = count[j + 1], count[j + 1] = v;
+            }
+    int64_t span = dim;
+    for (int i = 0; i < 3; ++i) {
+        if (count[i] < 2) continue;
+        if (stride[i] < span) return false;
+        span += (count[i] - 1) * stride[i];
+    }
+    return true;
+}
+
+int check_heads(const fft_heads& t, int64_t dim, int64_t heads, const fft_linattn_desc& d, bool output) {
+    if (!t.data) return d.length == 0 ? FFT_OK : FFT_ERR_INVALID_ARG;
+    if (t.tok_stride < 0 || t.seq_stride < 0 || t.head_stride < 0) return FFT_ERR_INVALID_ARG;
+    if (t.tok_stride > kMaxTokStride || t.head_stride > kMaxElements / (heads + 1) ||
+        (!d.offsets && t.seq_stride > kMaxElements / (d.nseq + 1)))
+        return FFT_ERR_UNSUPPORTED_SIZE;
+    if (output && d.length > 0 && !rows_apart(t, dim, heads, d.offsets ? 1 : d.nseq, d.length))
+        return FFT_ERR_INVALID_ARG;
+    return aligned_to(t.data, dtype_size(d.dtype)) ? FFT_OK : FFT_ERR_MISALIGNED;
+}
+int check_decay(const fft_seq& t, const fft_linattn_desc& d, bool output) {
+    const fft_heads h = {t.data, t.seq_stride, t.tok_stride, 1};
+    return check_heads(h, 1, d.heads, d, output);
+}
+
+int check_linattn(const fft_linattn_desc* d, bool pointers) {
+    if (!d || d->dtype < FFT_F32 || d->dtype > FFT_F16) return FFT_ERR_INVALID_ARG;
+    if (d->nseq < 1 || d->length < 0 || d->heads < 1 || d->groups < 1 || d->heads % d->groups || d->dk < 1 ||
+        d->dv < 1)
+        return FFT_ERR_INVALID_ARG;
+    if (d->nseq > INT32_MAX || d->length > INT32_MAX - 65536 || d->heads > FFT_LINATTN_MAX_HEADS ||
+        d->dk > FFT_LINATTN_MAX_DIM || d->dv > FFT_LINATTN_MAX_DIM)
+        return FFT_ERR_UNSUPPORTED_SIZE;
+    if (!aligned_to(d->offsets, 8)) return FFT_ERR_MISALIGNED;
+    if (!pointers) return FFT_OK;
+    if (!aligned_to(d->initial_state, 4)) return FFT_ERR_MISALIGNED;
+    TRY(check_heads(d->q, d->dk, d->groups, *d, false));
+    TRY(check_heads(d->k, d->dk, d->groups, *d, false));
+    TRY(check_heads(d->v, d->dv, d->heads, *d, false));
+    return check_decay(d->decay, *d, false);
+}
+
+// Whether an output shares values with what is read: as rows of columns where heads lie back to
+// back, by their ranges of addresses otherwise.
+struct Place {
+    fft_heads t;
+    int64_t dim, heads;
+};
+bool places_meet(const Place& a, const Place& b, const fft_linattn_desc& d) {
+    const size_t e = dtype_size(d.dtype);
+    auto together = [](const Place& p) { return p.heads == 1 || p.t.head_stride == p.dim; };
+    const int64_t nseq = d.offsets ? 1 : d.nseq;
+    auto bytes = [&](const Place& p) -> int64_t {
+        if (!p.t.data || d.length < 1) return 0;
+        return ((nseq - 1) * p.t.seq_stride + (d.length - 1) * p.t.tok_stride + (p.heads - 1) * p.t.head_stride +
+                p.dim) * (int64_t)e;
+    };
+    if (!bytes_meet(a.t.data, bytes(a), b.t.data, bytes(b))) return false;
+    if (!together(a) || !together(b)) return true;
+    const fft_seq x = {a.t.data, a.t.seq_stride, a.t.tok_stride}, y = {b.t.data, b.t.seq_stride, b.t.tok_stride};
+    return seqs_meet(x, y, a.dim * a.heads, b.dim * b.heads, d.nseq, d.length, d.offsets, e);
+}
+Place decay_place(const fft_seq& t, int64_t heads) { return {{t.data, t.seq_stride, t.tok_stride, 1}, 1, heads}; }
+bool meets_inputs(const Place& out, const fft_linattn_desc& d) {
+    return places_meet(out, {d.q, d.dk, d.groups}, d) || places_meet(out, {d.k, d.dk, d.groups}, d) ||
+           places_meet(out, {d.v, d.dv, d.heads}, d) || places_meet(out, decay_place(d.decay, d.heads), d);
+}
+
+AttnRows rows_of(const fft_heads& t, int64_t dim, int64_t heads, const fft_linattn_desc& d, int share) {
+    const int64_t e = (int64_t)dtype_size(d.dtype);
+    const int64_t seq = d.offsets || d.nseq == 1 ? 0 : t.seq_stride, tok = d.length > 1 ? t.tok_stride : 0,
+                  head = heads > 1 ? t.head_stride : 0;
+    AttnRows r = {t.data, seq, tok, head, share, 0};
+    for (int v : {16, 4})
+        if (!r.vec && aligned_to(t.data, v) && dim * e % v == 0 && seq * e % v == 0 && tok * e % v == 0 && head * e % v == 0)
+            r.vec = v;
+    return r;
+}
+
+int64_t up16(int64_t bytes) { return (bytes + 15) / 16 * 16; }
+
+// One pass of the kernel: shapes, and time cut into as many segments as give the least time, counted
+// in rounds of resident blocks times the chunks of a segment.  A cut call reads keys and values
+// twice.
+void attn_plan(const fft_linattn_desc& d, int64_t dx, int64_t dz, AttnArgs* a) {
+    a->offsets = d.offsets;
+    a->nseq = d.nseq;
+    a->length = d.length;
+    a->rows = d.offsets ? 1 : d.nseq;
+    a->heads = d.heads;
+    a->dx = dx;
+    a->dz = dz;
+    const int64_t zt = attn_ztile(d.dtype, dx, dz);
+    a->ztiles = (dz + zt - 1) / zt;
+}
+int64_t attn_segment(const fft_linattn_desc& d, int64_t ztiles, int64_t resident) {
+    const int64_t rows = d.offsets ? 1 : d.nseq, blocks = rows * d.heads * ztiles;
+    int64_t segment = d.length, best = INT64_MAX;
+    for (int64_t k = 1; k <= 256; ++k) {
+        int64_t size = (d.length + k - 1) / k;
+        size = (size + kAttnChunk - 1) / kAttnChunk * kAttnChunk;
+        const int64_t n = (d.length + size - 1) / size;
+        const int64_t cost = (blocks * n + resident - 1) / resident * (size / kAttnChunk * (n > 1 ? 3 : 2) + 4) + (n > 1 ? 8 : 0);
+        if (cost < best) best = cost, segment = size;
+        if (size <= 2 * kAttnChunk) break;
+    }
+    return segment < 1 ? kAttnChunk : segment;
+}
+void attn_cut(AttnArgs* a, int64_t segment) {
+    a->segment = segment;
+    a->nsegments = (a->length + segment - 1) / segment;
+}
+
+struct Taker {
+    char* w;
+    int64_t at = 0;
+    template <class P>
+    P* take(int64_t count) {
+        P* p = reinterpret_cast<P*>(w ? w + at : nullptr);
+        at += up16(count * (int64_t)sizeof(P));
+        return p;
+    }
+};
+void take_carry(AttnArgs* a, int dtype, Taker* t) {
+    if (a->nsegments < 2) return;
+    const int64_t n = a->rows * a->nsegments * a->heads;
+    a->carry = t->take<float>(n * a->ztiles * attn_carry(dtype, a->dx, a->dz));
+    a->carry_decay = t->take<float>(n);
+    a->carry_reset = t->take<int>(n);
+}
+
+int64_t forward_layout(const fft_linattn_desc& d, AttnArgs* a, char* w) {
+    attn_plan(d, d.dk, d.dv, a);
+    attn_cut(a, attn_segment(d, a->ztiles, (int64_t)num_sms() * (attn_warps(d.dtype, d.dk, d.dv) == 4 ? 2 : 1)));
+    Taker t = {w};
+    take_carry(a, d.dtype, &t);
+    return t.at;
+}
+
+// The three passes of the gradients share their cuts, so that chunks are the same ones.
+struct BackwardPlan {
+    AttnArgs q, k, v;  // passes for dq, dk, dv
+    DecayGradArgs g;
+    float *dq_parts, *dk_parts;
+};
+int64_t backward_layout(const fft_linattn_desc& d, const fft_linattn_grads* gr, BackwardPlan* p, char* w) {
+    attn_plan(d, d.dv, d.dk, &p->q);
+    attn_plan(d, d.dv, d.dk, &p->k);
+    attn_plan(d, d.dk, d.dv, &p->v);
+    const int64_t zk = p->q.ztiles, zv = p->v.ztiles;
+    const int64_t segment = attn_segment(d, zk > zv ? zk : zv, (int64_t)num_sms());
+    Taker t = {w};
+    for (AttnArgs* a : {&p->q, &p->k, &p->v}) {
+        attn_cut(a, segment);
+        take_carry(a, d.dtype, &t);
+    }
+    const int64_t tokens = p->q.rows * d.length, dots = zk * d.heads * tokens;
+    p->q.dots_inter = t.take<float>(dots);
+    p->q.dots_all = t.take<float>(dots);
+    p->k.dots_inter = t.take<float>(dots);
+    p->k.dots_all = t.take<float>(dots);
+    const int64_t n = p->q.rows * p->q.nsegments * d.heads;
+    float* final_dots = t.take<float>(zk * d.nseq * d.heads);
+    DecayGradArgs& g = p->g;
+    g.carry = t.take<double>(n);
+    g.stops = t.take<int>(n);
+    const bool shared = d.heads > d.groups;
+    p->dq_parts = shared ? t.take<float>(tokens * d.heads * d.dk) : nullptr;
+    p->dk_parts = shared ? t.take<float>(tokens * d.heads * d.dk) : nullptr;
+    if (!w || !gr) return t.at;
+    p->q.final_dots = final_dots;
+    g.decay = d.decay;
+    g.ddecay = gr->ddecay;
+    g.offsets = d.offsets;
+    g.nseq = d.nseq;
+    g.length = d.length;
+    g.rows = p->q.rows;
+    g.heads = d.heads;
+    g.segment = segment;
+    g.nsegments = p->q.nsegments;
+    g.ztiles = zk;
+    g.initial = d.initial_state != nullptr;
+    g.q_inter = p->q.dots_inter;
+    g.q_all = p->q.dots_all;
+    g.k_inter = p->k.dots_inter;
+    g.k_all = p->k.dots_all;
+    g.final_dots = gr->dfinal_state ? final_dots : nullptr;
+    return t.at;
+}
+
+void set_out(AttnArgs* a, const fft_heads& out, const fft_linattn_desc& d, float* parts) {
+    if (parts) {
+        a->out = parts;
+        a->out_f32 = 1;
+        a->out_head = a->dz;
+        a->out_tok = d.heads * a->dz;
+        a->out_seq = d.length * a->out_tok;
+        return;
+    }
+    a->out = out.data;
+    a->out_seq = d.offsets ? 0 : out.seq_stride;
+    a->out_tok = out.tok_stride;
+    a->out_head = out.head_stride;
+    a->out_pair = a->dz % 2 == 0 && aligned_to(out.data, 2 * dtype_size(d.dtype)) && a->out_seq % 2 == 0 &&
+                  a->out_tok % 2 == 0 && a->out_head % 2 == 0;
+}
+
+template <class F32, class B16, class F16>
+cudaError_t by_type(int dtype, F32 f32, B16 b16, F16 f16, const AttnArgs& a, cudaStream_t s) {
+    return dtype == FFT_F32 ? f32(a, s) : (dtype == FFT_BF16 ? b16(a, s) : f16(a, s));
+}
+cudaError_t run_forward(const AttnArgs& a, int dtype, cudaStream_t s) {
+    return by_type(dtype, attn_f32_fwd, attn_bf16_fwd, attn_f16_fwd, a, s);
+}
+cudaError_t run_backward(const AttnArgs& a, int dtype, cudaStream_t s) {
+    return by_type(dtype, attn_f32_bwd, attn_bf16_bwd, attn_f16_bwd, a, s);
+}
+
+cudaError_t fill_empty(const fft_linattn_desc& d, const float* from, float* to, cudaStream_t s) {
+    const int64_t per = d.heads * d.dk * d.dv;
+    if (!to) return cudaSuccess;
+    if (d.offsets && d.length > 0) {
+        k_linattn_empty<<<(unsigned)d.nseq, 256, 0, s>>>(d.offsets, from, to, per);
+        return cudaGetLastError();
+    }
+    if (d.length > 0) return cudaSuccess;
+    const size_t bytes = (size_t)(d.nseq * per) * sizeof(float);
+    return from ? cudaMemcpyAsync(to, from, bytes, cudaMemcpyDeviceToDevice, s) : cudaMemsetAsync(to, 0, bytes, s);
+}
+
+template <class T>
+cudaError_t run_shared(const float* parts, const fft_heads& out, const fft_linattn_desc& d, cudaStream_t s) {
+    const int64_t total = (d.offsets ? 1 : d.nseq) * d.length * d.groups * d.dk;
+    const int64_t blocks = (total + 255) / 256;
+    if (blocks > INT32_MAX) return cudaErrorInvalidValue;
+    k_linattn_shared<T><<<(unsigned)blocks, 256, 0, s>>>(parts, out, d.length, d.groups, d.heads / d.groups, d.dk,
+                                                         total);
+    return cudaGetLastError();
+}
+
+template <class T>
+cudaError_t finish_backward(const BackwardPlan& p, const fft_linattn_desc& d, const fft_linattn_grads& g,
+                            cudaStream_t s) {
+    const unsigned blocks = (unsigned)(p.g.rows * p.g.nsegments * p.g.heads);
+    if (p.g.nsegments > 1) k_decay_sums<<<blocks, kDgWarps * 32, 0, s>>>(p.g);
+    k_decay_grads<T><<<blocks, kDgWarps * 32, 0, s>>>(p.g);
+    cudaError_t e = cudaGetLastError();
+    if (e == cudaSuccess && p.dq_parts) e = run_shared<T>(p.dq_parts, g.dq, d, s);
+    if (e == cudaSuccess && p.dk_parts) e = run_shared<T>(p.dk_parts, g.dk, d, s);
+    return e;
+}
+
+}  // namespace
+}  // namespace gbfft
+
+using namespace gbfft;
+
+extern "C" int fft_linattn_workspace(const fft_linattn_desc* d, int backward, size_t* bytes) {
+    if (!bytes || (backward != 0 && backward != 1)) return FFT_ERR_INVALID_ARG;
+    TRY(check_linattn(d, false));
+    AttnArgs a = {};
+    BackwardPlan p = {};
+    *bytes = d->length < 1 ? 0 : (size_t)(backward ? backward_layout(*d, nullptr, &p, nullptr)
+                                                  : forward_layout(*d, &a, nullptr));
+    return FFT_OK;
+}
+
+extern "C" int fft_linattn_forward(const fft_linattn_desc* d, const fft_heads* out, float* final_state,
+                                   void* workspace, size_t workspace_bytes, void* stream) {
+    TRY(check_linattn(d, true));
+    if (!out) return FFT_ERR_INVALID_ARG;
+    TRY(check_heads(*out, d->dv, d->heads, *d, true));
+    if (!aligned_to(final_state, 4) || !aligned_to(workspace, 16)) return FFT_ERR_MISALIGNED;
+    const int64_t states = d->nseq * d->heads * d->dk * d->dv * 4;
+    if (meets_inputs({*out, d->dv, d->heads}, *d) || bytes_meet(final_state, states, d->initial_state, states))
+        return FFT_ERR_INVALID_ARG;
+    cudaStream_t s = (cudaStream_t)stream;
+    if (d->length > 0) {
+        AttnArgs a = {};
+        const int64_t need = forward_layout(*d, &a, static_cast<char*>(workspace));
+        if (need > 0 && (!workspace || workspace_bytes < (size_t)need)) return FFT_ERR_INVALID_ARG;
+        const int share = (int)(d->heads / d->groups);
+        a.x = rows_of(d->q, d->dk, d->groups, *d, share);
+        a.y = rows_of(d->k, d->dk, d->groups, *d, share);
+        a.z = rows_of(d->v, d->dv, d->heads, *d, 1);
+        a.decay = d->decay;
+        a.scale_pair = a.scale_inter = d->scale;
+        a.scale_update = 1.f;
+        a.initial = d->initial_state;
+        a.final_state = final_state;
+        a.state_x = d->dv;
+        a.state_z = 1;
+        set_out(&a, *out, *d, nullptr);
+        TRY(status(run_forward(a, d->dtype, s)));
+    }
+    return status(fill_empty(*d, d->initial_state, final_state, s));
+}
+
+extern "C" int fft_linattn_backward(const fft_linattn_desc* d, const fft_linattn_grads* g, void* workspace,
+                                    size_t workspace_bytes, void* stream) {
+    TRY(check_linattn(d, true));
+    if (!g) return FFT_ERR_INVALID_ARG;
+    TRY(check_heads(g->dout, d->dv, d->heads, *d, false));
+    TRY(check_heads(g->dq, d->dk, d->groups, *d, true));
+    TRY(check_heads(g->dk, d->dk, d->groups, *d, true));
+    TRY(check_heads(g->dv, d->dv, d->heads, *d, true));
+    TRY(check_decay(g->ddecay, *d, true));
+    if (!aligned_to(g->dfinal_state, 4) || !aligned_to(g->dinitial_state, 4) || !aligned_to(workspace, 16))
+        return FFT_ERR_MISALIGNED;
+    const int64_t states = d->nseq * d->heads * d->dk * d->dv * 4;
+    const Place dout = {g->dout, d->dv, d->heads};
+    for (const Place& o : {Place{g->dq, d->dk, d->groups}, Place{g->dk, d->dk, d->groups},
+                           Place{g->dv, d->dv, d->heads}, decay_place(g->ddecay, d->heads)})
+        if (meets_inputs(o, *d) || places_meet(o, dout, *d)) return FFT_ERR_INVALID_ARG;
+    if (bytes_meet(g->dinitial_state, states, d->initial_state, states) ||
+        bytes_meet(g->dinitial_state, states, g->dfinal_state, states))
+        return FFT_ERR_INVALID_ARG;
+    cudaStream_t s = (cudaStream_t)stream;
+    if (d->length > 0) {
+        BackwardPlan p = {};
+        const int64_t need = backward_layout(*d, g, &p, static_cast<char*>(workspace));
+        if (!workspace || workspace_bytes < (size_t)need) return FFT_ERR_INVALID_ARG;
+        const int share = (int)(d->heads / d->groups);
+        const AttnRows q = rows_of(d->q, d->dk, d->groups, *d, share), k = rows_of(d->k, d->dk, d->groups, *d, share),
+                       v = rows_of(d->v, d->dv, d->heads, *d, 1), o = rows_of(g->dout, d->dv, d->heads, *d, 1);
+        AttnArgs& a = p.q;  // dq[i] = sum over j <= i of (dout[i] v[j]) k[j]
+        a.x = o, a.y = v, a.z = k, a.partner = q;
+        a.initial = d->initial_state;
+        a.scale_pair = a.scale_inter = d->scale;
+        a.scale_update = 1.f;
+        a.state_x = 1, a.state_z = d->dv;
+        a.final_dot = g->dfinal_state;
+        set_out(&a, g->dq, *d, p.dq_parts);
+        AttnArgs& b = p.k;  // dk[j] = sum over i >= j of (v[j] dout[i]) q[i]
+        b.x = v, b.y = o, b.z = q, b.partner = k;
+        b.state_x = 1, b.state_z = d->dv;
+        set_out(&b, g->dk, *d, p.dk_parts);
+        AttnArgs& c = p.v;  // dv[j] = sum over i >= j of (k[j] q[i]) dout[i]
+        c.x = k, c.y = q, c.z = o;
+        c.state_x = d->dv, c.state_z = 1;
+        c.final_state = g->dinitial_state;
+        set_out(&c, g->dv, *d, nullptr);
+        for (AttnArgs* r : {&b, &c}) {
+            r->reverse = 1;
+            r->initial = g->dfinal_state;
+            r->scale_pair = r->scale_update = d->scale;
+            r->scale_inter = 1.f;
+        }
+        a.decay = b.decay = c.decay = d->decay;
+        for (const AttnArgs* r : {&a, &b, &c}) TRY(status(run_backward(*r, d->dtype, s)));
+        TRY(status(d->dtype == FFT_F32 ? finish_backward<float>(p, *d, *g, s)
+                                       : (d->dtype == FFT_BF16 ? finish_backward<__nv_bfloat16>(p, *d, *g, s)
+                                                               : finish_backward<__half>(p, *d, *g, s))));
+    }
+    return status(fill_empty(*d, g->dfinal_state, g->dinitial_state, s));
+}
+
+extern "C" int fft_linattn_step(const fft_linattn_desc* d, const fft_heads* out, float* state, int64_t pool,
+                                const int64_t* slots, const int64_t* slots_out, void* stream) {
+    TRY(check_linattn(d, true));
+    if (!out || d->length != 1 || d->offsets || pool < 0) return FFT_ERR_INVALID_ARG;
+    if ((pool > 0 && !state) || (!slots && pool < d->nseq)) return FFT_ERR_INVALID_ARG;
+    if (!aligned_to(slots, 8) || !aligned_to(slots_out, 8) || !aligned_to(state, 4)) return FFT_ERR_MISALIGNED;
+    TRY(check_heads(*out, d->dv, d->heads, *d, true));
+    if (meets_inputs({*out, d->dv, d->heads}, *d)) return FFT_ERR_INVALID_ARG;
+    const AttnStepArgs a = {*d, *out, state, slots, slots_out, pool, 0};
+    cudaStream_t s = (cudaStream_t)stream;
+    return status(d->dtype == FFT_F32 ? attn_step<float>(a, s)
+                                      : (d->dtype == FFT_BF16 ? attn_step<__nv_bfloat16>(a, s) : attn_step<__half>(a, s)));
+}

@@ -1,4 +1,5 @@
-"""Sequence operators: short causal convolution, selective state-space scan, residual norm.
+"""Sequence operators: short causal convolution, selective state-space scan, linear attention with
+decays, residual norm, group norm.
 
 Filters along the tokens of a sequence whose coefficients change from token to token (so that no
 transform plan describes them), and the norm between two such layers; see include/gbfft.h for the
@@ -7,6 +8,8 @@ current CUDA stream: every step runs in the library's kernels.
 
     out, state = causal_conv(x, weight, bias, silu=True, return_state=True)    # x [b, l, d]
     y, h = selective_scan(u, delta, A, B, C, D=D, z=z, softplus=True, return_state=True)
+    o, S = linear_attention(q, k, v, decay, return_state=True)      # q, k [b, l, groups, dk]
+    r = group_norm(x, groups, weight, bias, z=z)                    # r.out, r.mean, r.rstd
     r = residual_norm(x, weight, residual=res)                      # r.out, r.residual
     q = residual_norm(x, weight, out_dtype=torch.float8_e4m3fn, group=128)     # q.out, q.scale
 
@@ -33,6 +36,11 @@ _CONV = struct.Struct("@4i3q4PP2q")  # fft_conv_desc
 _SCAN = struct.Struct("@2i5q5P" + "P2q" * 5)  # fft_scan_desc
 _GRADS = struct.Struct("@P2qP" + "P2q" * 5 + "4P")  # fft_scan_grads
 _NORM = struct.Struct("@4i3qfP")  # fft_norm_desc
+_HEADS = struct.Struct("@P3q")  # fft_heads
+_ATTN = struct.Struct("@if6q2P" + "P3q" * 3 + "P2q")  # fft_linattn_desc
+_ATTN_GRADS = struct.Struct("@P3qP" + "P3q" * 3 + "P2qP")  # fft_linattn_grads
+_GNORM = struct.Struct("@3if4q3P" + "P2q" * 2)  # fft_gnorm_desc
+_GNORM_GRADS = struct.Struct("@2P" + "P2q" * 3 + "2P")  # fft_gnorm_grads
 _NONE = (0, 0, 0)  # an absent fft_seq
 
 
@@ -67,6 +75,27 @@ class NormGrads(NamedTuple):
     dweight: object
 
 
+class AttentionGrads(NamedTuple):
+    dq: object
+    dk: object
+    dv: object
+    ddecay: object
+    dinitial_state: Optional[object]
+
+
+class GroupNormOut(NamedTuple):
+    out: object
+    mean: object  # float32 [sequences, groups]
+    rstd: object
+
+
+class GroupNormGrads(NamedTuple):
+    dx: object
+    dz: Optional[object]
+    dweight: Optional[object]  # float32 [channels]
+    dbias: Optional[object]
+
+
 def declare(L):
     """Argument types of the sequence operators (called when the library is loaded)."""
     desc, vp, i64, sz = ctypes.c_char_p, ctypes.c_void_p, ctypes.c_int64, ctypes.c_size_t
@@ -78,15 +107,24 @@ def declare(L):
     L.fft_scan_forward.argtypes = [desc, desc, vp, vp, sz, vp]
     L.fft_scan_backward.argtypes = [desc, desc, vp, sz, vp]
     L.fft_scan_step.argtypes = [desc, desc, vp, i64, vp, vp, vp]
+    L.fft_linattn_workspace.argtypes = [desc, ctypes.c_int, ctypes.POINTER(sz)]
+    L.fft_linattn_forward.argtypes = [desc, desc, vp, vp, sz, vp]
+    L.fft_linattn_backward.argtypes = [desc, desc, vp, sz, vp]
+    L.fft_linattn_step.argtypes = [desc, desc, vp, i64, vp, vp, vp]
     L.fft_norm_forward.argtypes = [desc, vp, i64, vp, i64, vp, i64, vp, vp, i64, vp]
     L.fft_norm_workspace.argtypes = [desc, ctypes.POINTER(sz)]
     L.fft_norm_backward.argtypes = [desc, vp, i64, vp, i64, vp, i64, vp, i64, vp, i64, vp, vp, sz,
                                     vp]
+    L.fft_gnorm_workspace.argtypes = [desc, ctypes.c_int, ctypes.POINTER(sz)]
+    L.fft_gnorm_forward.argtypes = [desc, desc, vp, vp, vp, sz, vp]
+    L.fft_gnorm_backward.argtypes = [desc, desc, vp, sz, vp]
 
 
 SYMBOLS = ("fft_conv_forward", "fft_conv_workspace", "fft_conv_backward", "fft_conv_step",
            "fft_scan_workspace", "fft_scan_forward", "fft_scan_backward", "fft_scan_step",
-           "fft_norm_forward", "fft_norm_workspace", "fft_norm_backward")
+           "fft_linattn_workspace", "fft_linattn_forward", "fft_linattn_backward",
+           "fft_linattn_step", "fft_norm_forward", "fft_norm_workspace", "fft_norm_backward",
+           "fft_gnorm_workspace", "fft_gnorm_forward", "fft_gnorm_backward")
 
 
 # ---- checks ---------------------------------------------------------------------------------
@@ -462,6 +500,111 @@ def selective_scan_step(state, u, delta, A, B, C, D=None, z=None, delta_bias=Non
     return out
 
 
+# ---- linear attention -----------------------------------------------------------------------
+
+
+def _heads(t, packed):
+    """The fields of an fft_heads."""
+    st = t.stride()
+    return (t.data_ptr(), 0, st[0], st[1]) if packed else (t.data_ptr(), st[0], st[1], st[2])
+
+
+def _attn_desc(q, k, v, decay, scale, initial_state, offsets):
+    """(packed fft_linattn_desc, device, sequences, heads, dk, dv)."""
+    code, dev = _first(q, "q")
+    dtype, packed = q.dtype, offsets is not None
+    if q.dim() != (3 if packed else 4) or v.dim() != q.dim():
+        raise ValueError("q: expected [tokens, groups, dk] with offsets, [sequences, tokens, groups, dk] "
+                         "without, and v [..., heads, dv]")
+    lead, (groups, dk), (heads, dv) = q.shape[:-2], q.shape[-2:], v.shape[-2:]
+    _need(q, dev, dtype, q.shape, "q")
+    _need(k, dev, dtype, q.shape, "k")
+    _need(v, dev, dtype, (*lead, heads, dv), "v")
+    if decay.dtype is not dtype or decay.shape != (*lead, heads) or decay.get_device() != dev or (
+            decay.stride(-1) != 1 and heads > 1 and decay.numel()):
+        _tell(decay, dev, dtype, (*lead, heads), "decay")
+    nseq, length = (offsets.numel() - 1, lead[0]) if packed else lead
+    count, length, at = _batch(offsets, dev, nseq, length, packed)
+    st = decay.stride()
+    desc = _ATTN.pack(code, dk ** -0.5 if scale is None else scale, count, length, heads, groups, dk, dv,
+                      at, _flat(initial_state, dev, torch.float32, (nseq, heads, dk, dv), "initial_state"),
+                      *_heads(q, packed), *_heads(k, packed), *_heads(v, packed),
+                      *((decay.data_ptr(), 0, st[0]) if packed else (decay.data_ptr(), st[0], st[1])))
+    return desc, dev, nseq, heads, dk, dv
+
+
+def linear_attention(q, k, v, decay, scale=None, initial_state=None, offsets=None, return_state=False,
+                     out=None, stream=None):
+    """Linear attention with a decay for each head (fft_linattn_forward): q, k [..., groups, dk],
+    v [..., heads, dv], decay [..., heads] (logs, at most 0; of q's dtype; strides of 0 for decays that do
+    not change), scale dk ** -0.5 unless given; states [sequences, heads, dk, dv] float32.  Any strides but
+    of the last axis, so heads may lie beside tokens or around them.  out overlaps no input.  Returns out,
+    or (out, final_state).  Not recorded for autograd: gradients come from linear_attention_backward."""
+    desc, dev, nseq, heads, dk, dv = _attn_desc(q, k, v, decay, scale, initial_state, offsets)
+    on, s = _stream(stream, dev)
+    with on:
+        out = v.new_empty(v.shape) if out is None else _need(out, dev, v.dtype, v.shape, "out")
+        state = v.new_empty((nseq, heads, dk, dv), dtype=torch.float32) if return_state else None
+        ws, wp, size = _workspace(_L.fft_linattn_workspace, (desc, 0), v, "fft_linattn_workspace")
+        _check(_L.fft_linattn_forward(desc, _HEADS.pack(*_heads(out, offsets is not None)), _ptr(state),
+                                      wp, size, s), "fft_linattn_forward")
+    return (out, state) if return_state else out
+
+
+def linear_attention_backward(dout, q, k, v, decay, scale=None, initial_state=None, offsets=None,
+                              dfinal_state=None, stream=None):
+    """Gradients of linear_attention from dout (and dfinal_state): AttentionGrads.  Those of queries and
+    keys are sums over the heads that share them; ddecay has decay's shape, also where decay is a view
+    whose strides are 0."""
+    desc, dev, nseq, heads, dk, dv = _attn_desc(q, k, v, decay, scale, initial_state, offsets)
+    _need(dout, dev, v.dtype, v.shape, "dout")
+    packed, shape = offsets is not None, (nseq, heads, dk, dv)
+    dfin = _flat(dfinal_state, dev, torch.float32, shape, "dfinal_state")
+    on, s = _stream(stream, dev)
+    with on:
+        dq, dkey, dval = q.new_empty(q.shape), q.new_empty(q.shape), v.new_empty(v.shape)
+        dg = v.new_empty(decay.shape)
+        di = v.new_empty(shape, dtype=torch.float32) if initial_state is not None else None
+        grads = _ATTN_GRADS.pack(*_heads(dout, packed), dfin, *_heads(dq, packed), *_heads(dkey, packed),
+                                 *_heads(dval, packed), *_seq(dg, packed), _ptr(di) or 0)
+        ws, wp, size = _workspace(_L.fft_linattn_workspace, (desc, 1), v, "fft_linattn_workspace")
+        _check(_L.fft_linattn_backward(desc, grads, wp, size, s), "fft_linattn_backward")
+    return AttentionGrads(dq, dkey, dval, dg, di)
+
+
+def linear_attention_step(state, q, k, v, decay, scale=None, slots=None, slots_out=None, out=None,
+                          stream=None):
+    """One token for each sequence (fft_linattn_step): q, k [sequences, groups, dk], v [sequences, heads,
+    dv], decay [sequences, heads], state the pool [pool, heads, dk, dv] float32, updated in place; slots,
+    slots_out int64 [sequences] as in causal_conv_step.  out overlaps no input."""
+    code, dev = _first(q, "q")
+    dtype, qs, vs = q.dtype, q.shape, v.shape
+    if len(qs) != 3 or len(vs) != 3:
+        raise ValueError("q: expected [sequences, groups, dk], v: [sequences, heads, dv]")
+    nseq, groups, dk = qs
+    heads, dv = vs[1:]
+    _need(q, dev, dtype, qs, "q")
+    _need(k, dev, dtype, qs, "k")
+    _need(v, dev, dtype, (nseq, heads, dv), "v")
+    qt, kt, vt = q.stride(), k.stride(), v.stride()
+    desc = _ATTN.pack(code, dk ** -0.5 if scale is None else scale, nseq, 1, heads, groups, dk, dv, 0, 0,
+                      q.data_ptr(), qt[0], 0, qt[1], k.data_ptr(), kt[0], 0, kt[1],
+                      v.data_ptr(), vt[0], 0, vt[1], *_token(decay, dev, dtype, (nseq, heads), "decay"))
+    size = state.shape[0]
+    pool = _flat(state, dev, torch.float32, (size, heads, dk, dv), "state")
+    src = _flat(slots, dev, torch.int64, (nseq,), "slots")
+    dst = _flat(slots_out, dev, torch.int64, (nseq,), "slots_out")
+    on, s = _stream(stream, dev)
+    with on:
+        out = v.new_empty(vs) if out is None else _need(out, dev, dtype, vs, "out")
+        if nseq == 0:
+            return out
+        ot = out.stride()
+        _check(_L.fft_linattn_step(desc, _HEADS.pack(out.data_ptr(), ot[0], 0, ot[1]), pool, size, src, dst, s),
+               "fft_linattn_step")
+    return out
+
+
 # ---- residual norm --------------------------------------------------------------------------
 
 
@@ -563,3 +706,86 @@ def residual_norm_backward(dout, r, weight, dresidual=None, eps=1e-6, stream=Non
             None if dx is dr else dx.data_ptr(), _rows(dx)[1], dw.data_ptr(), wp, size, s),
             "fft_norm_backward")
     return NormGrads(dx, dr, dw)
+
+
+# ---- group norm -----------------------------------------------------------------------------
+
+
+def _gnorm_rows(t):
+    """The fields of an fft_seq of [rows, channels] (sequences of one token), [sequences, tokens,
+    channels] or, packed, [tokens, channels]."""
+    st = t.stride()
+    return (t.data_ptr(), st[0], st[1] if len(st) == 3 else 0)
+
+
+def _gnorm_desc(x, groups, weight, bias, z, silu, eps, offsets):
+    """(packed fft_gnorm_desc, device, sequences)."""
+    code, dev = _first(x, "x")
+    dtype, shape, packed = x.dtype, x.shape, offsets is not None
+    if len(shape) != 2 and (packed or len(shape) != 3):
+        raise ValueError("x: expected [tokens, channels] with offsets, [sequences, tokens, channels] or [rows, "
+                         "channels] without")
+    _need(x, dev, dtype, shape, "x")
+    d = shape[-1]
+    nseq = offsets.numel() - 1 if packed else shape[0]
+    length = shape[0] if packed else (shape[1] if len(shape) == 3 else 1)
+    ptype = torch.float32
+    for t, what in ((weight, "weight"), (bias, "bias")):
+        if t is not None:
+            if t.dtype is not dtype and t.dtype is not torch.float32:
+                raise TypeError(f"{what}: expected float32 or the type of x")
+            ptype = t.dtype
+    if z is not None:
+        _need(z, dev, dtype, shape, "z")
+    count, length, at = _batch(offsets, dev, nseq, length, packed)
+    rows = _seq if packed else (lambda t, _: _gnorm_rows(t))
+    desc = _GNORM.pack(code, F32 if ptype is torch.float32 else code, 1 if silu else 0, eps, count, length, d,
+                       groups, at, _flat(weight, dev, ptype, (d,), "weight"),
+                       _flat(bias, dev, ptype, (d,), "bias"), *rows(x, packed),
+                       *(rows(z, packed) if z is not None else _NONE))
+    return desc, dev, nseq, rows
+
+
+def group_norm(x, groups, weight=None, bias=None, z=None, silu=False, eps=1e-5, offsets=None, out=None,
+               stream=None):
+    """Group norm, channels last (fft_gnorm_forward): x [sequences, tokens, channels], packed [tokens,
+    channels] with offsets, or [rows, channels], each row by itself; weight, bias [channels], both
+    float32 or of x's type; silu applies SiLU, z [like x] gates what comes out.  out may be x or z itself.
+    Returns GroupNormOut: out, and mean and rstd [sequences, groups] for group_norm_backward.  Not
+    recorded for autograd."""
+    desc, dev, nseq, rows = _gnorm_desc(x, groups, weight, bias, z, silu, eps, offsets)
+    on, s = _stream(stream, dev)
+    with on:
+        out = _out(out, x, dev)
+        stats = x.new_empty((2, nseq, groups), dtype=torch.float32)
+        mean, rstd = stats[0], stats[1]
+        if nseq == 0:
+            return GroupNormOut(out, mean, rstd)
+        ws, wp, size = _workspace(_L.fft_gnorm_workspace, (desc, 0), x, "fft_gnorm_workspace")
+        _check(_L.fft_gnorm_forward(desc, _SEQ.pack(*rows(out, offsets is not None)), mean.data_ptr(),
+                                    rstd.data_ptr(), wp, size, s), "fft_gnorm_forward")
+    return GroupNormOut(out, mean, rstd)
+
+
+def group_norm_backward(dout, x, mean, rstd, weight=None, bias=None, z=None, silu=False, offsets=None,
+                        stream=None):
+    """Gradients of group_norm from dout and the forward call's mean and rstd: GroupNormGrads."""
+    groups = mean.shape[-1]
+    desc, dev, nseq, rows = _gnorm_desc(x, groups, weight, bias, z, silu, 0.0, offsets)
+    _need(dout, dev, x.dtype, x.shape, "dout")
+    packed, f32 = offsets is not None, torch.float32
+    mp, rp = _flat(mean, dev, f32, (nseq, groups), "mean"), _flat(rstd, dev, f32, (nseq, groups), "rstd")
+    on, s = _stream(stream, dev)
+    with on:
+        dx = x.new_empty(x.shape)
+        dz = x.new_empty(x.shape) if z is not None else None
+        make = x.new_empty if nseq else x.new_zeros
+        dw = make(weight.shape, dtype=f32) if weight is not None else None
+        db = make(bias.shape, dtype=f32) if bias is not None else None
+        if nseq == 0:
+            return GroupNormGrads(dx, dz, dw, db)
+        grads = _GNORM_GRADS.pack(mp, rp, *rows(dout, packed), *rows(dx, packed),
+                                  *(rows(dz, packed) if z is not None else _NONE), _ptr(dw) or 0, _ptr(db) or 0)
+        ws, wp, size = _workspace(_L.fft_gnorm_workspace, (desc, 1), x, "fft_gnorm_workspace")
+        _check(_L.fft_gnorm_backward(desc, grads, wp, size, s), "fft_gnorm_backward")
+    return GroupNormGrads(dx, dz, dw, db)

@@ -511,6 +511,119 @@ int fft_norm_backward(const fft_norm_desc* d, const void* dout, int64_t dout_str
                       void* dsum, int64_t dsum_stride, void* dx, int64_t dx_stride,
                       float* dweight, void* workspace, size_t workspace_bytes, void* stream);
 
+/*
+ * Linear attention with a decay for each head.  Head h reads the queries and keys of group
+ * h / (heads / groups); its state S is a matrix of dk by dv:
+ *   S[t] = exp(decay[t,h]) * S[t-1] + k[t] v[t]^T;   out[t] = scale * S[t]^T q[t]
+ * with S before a sequence's start its initial state, or 0.  decay is a log: 0 keeps the state,
+ * -infinity clears it, and a value above 0 counts as 0 (its gradient is 0).  Token t of sequence s
+ * and head h of an fft_heads is the contiguous row of dk or dv values at data + (s*seq_stride +
+ * t*tok_stride + h*head_stride) elements, so heads may lie beside tokens or around them; decay is
+ * an fft_seq with rows of `heads` values, whose strides may be 0 (decays that do not change).
+ * Sequences, decay and their gradients are of dtype; states [nseq][heads][dk][dv] are float32.
+ * 1 <= dk, dv <= FFT_LINATTN_MAX_DIM; groups divides heads, at most FFT_LINATTN_MAX_HEADS.
+ * A value that is not finite reaches the outputs of its own token and later ones only.
+ */
+#define FFT_LINATTN_MAX_DIM 256
+#define FFT_LINATTN_MAX_HEADS 65535
+
+typedef struct fft_heads {
+    void* data;
+    int64_t seq_stride;  /* elements from one sequence to the next */
+    int64_t tok_stride;  /* elements from one token to the next */
+    int64_t head_stride; /* elements from one head to the next */
+} fft_heads;
+
+typedef struct fft_linattn_desc {
+    int32_t dtype;
+    float scale;
+    int64_t nseq, length, heads, groups, dk, dv;
+    const int64_t* offsets;
+    const float* initial_state; /* or NULL: zeros */
+    fft_heads q, k, v;
+    fft_seq decay;
+} fft_linattn_desc;
+
+/* fft_linattn_workspace - bytes of workspace for the forward (backward = 0) or backward call; it
+ * may be 0.  Needs the descriptor's sizes and dtype only, and whether offsets is NULL. */
+int fft_linattn_workspace(const fft_linattn_desc* d, int backward, size_t* bytes);
+
+/* fft_linattn_forward - out and, unless NULL, final_state.  Other blocks read what a block has
+ * read: out may not overlap q, k, v or decay, nor final_state initial_state
+ * (FFT_ERR_INVALID_ARG).  Columns of the same rows are told apart where heads lie back to back;
+ * otherwise tensors whose ranges of addresses meet count as overlapping.
+ * Returns FFT_OK, FFT_ERR_INVALID_ARG, FFT_ERR_UNSUPPORTED_SIZE, FFT_ERR_MISALIGNED or
+ * FFT_ERR_CUDA. */
+int fft_linattn_forward(const fft_linattn_desc* d, const fft_heads* out, float* final_state,
+                        void* workspace, size_t workspace_bytes, void* stream);
+
+/* Gradients of sum(out * dout) + sum(final_state * dfinal_state).  dq, dk, dv and ddecay are
+ * required and of dtype; those of queries and keys are sums over the heads that read them. */
+typedef struct fft_linattn_grads {
+    fft_heads dout;
+    const float* dfinal_state; /* or NULL: zeros */
+    fft_heads dq, dk, dv;
+    fft_seq ddecay;
+    float* dinitial_state; /* or NULL */
+} fft_linattn_grads;
+
+/* The gradients may not overlap what is read (FFT_ERR_INVALID_ARG). */
+int fft_linattn_backward(const fft_linattn_desc* d, const fft_linattn_grads* g, void* workspace,
+                         size_t workspace_bytes, void* stream);
+
+/* fft_linattn_step - one token for each of nseq sequences (length 1, offsets NULL, initial_state
+ * not used; rows at seq_stride): state pool [pool][heads][dk][dv] float32, slots as for
+ * fft_conv_step.  out may not overlap what is read. */
+int fft_linattn_step(const fft_linattn_desc* d, const fft_heads* out, float* state, int64_t pool,
+                     const int64_t* slots, const int64_t* slots_out, void* stream);
+
+/*
+ * Group norm, channels last, with an activation.  Group g holds channels / groups channels; over all
+ * tokens of a sequence and the channels of a group
+ *   n = (x - mean) * rstd,  rstd = 1 / sqrt(mean((x - mean)^2) + eps);  y = n * weight + bias
+ *   p = silu ? y / (1 + exp(-y)) : y;   out = z ? p * z / (1 + exp(-z)) : p
+ * Sequences of one token are normalised token by token (the heads of an attention).  weight and
+ * bias [channels] (each may be NULL: 1 and 0) are of param_dtype (FFT_F32 or dtype), mean and rstd
+ * [nseq][groups] float32; a sequence without tokens has mean 0 and rstd 1 / sqrt(eps).  groups
+ * divides channels, at most FFT_GNORM_MAX_CHANNELS; z.data may be NULL (no gate).
+ */
+#define FFT_GNORM_MAX_CHANNELS 65536
+
+typedef struct fft_gnorm_desc {
+    int32_t dtype, param_dtype, silu;
+    float eps;
+    int64_t nseq, length, channels, groups;
+    const int64_t* offsets;
+    const void* weight;
+    const void* bias;
+    fft_seq x, z;
+} fft_gnorm_desc;
+
+/* fft_gnorm_workspace - bytes of workspace for the forward (backward = 0) or backward call; it may
+ * be 0.  Needs the descriptor's sizes and dtype only, and whether offsets is NULL. */
+int fft_gnorm_workspace(const fft_gnorm_desc* d, int backward, size_t* bytes);
+
+/* fft_gnorm_forward - out, mean and rstd.  out may be x or z themselves (same data and strides);
+ * another overlap with them is refused (FFT_ERR_INVALID_ARG).
+ * Returns FFT_OK, FFT_ERR_INVALID_ARG, FFT_ERR_UNSUPPORTED_SIZE, FFT_ERR_MISALIGNED or
+ * FFT_ERR_CUDA. */
+int fft_gnorm_forward(const fft_gnorm_desc* d, const fft_seq* out, float* mean, float* rstd,
+                      void* workspace, size_t workspace_bytes, void* stream);
+
+/* Gradients of sum(out * dout) from mean and rstd of the forward call: dx, dz (where z is given) of
+ * dtype; dweight and dbias [channels] float32 or NULL.  dx and dz may not overlap what is read
+ * (FFT_ERR_INVALID_ARG). */
+typedef struct fft_gnorm_grads {
+    const float* mean;
+    const float* rstd;
+    fft_seq dout, dx, dz;
+    float* dweight;
+    float* dbias;
+} fft_gnorm_grads;
+
+int fft_gnorm_backward(const fft_gnorm_desc* d, const fft_gnorm_grads* g, void* workspace,
+                       size_t workspace_bytes, void* stream);
+
 /* fft_status_string - static description of a status code (never NULL). */
 const char* fft_status_string(int status);
 
