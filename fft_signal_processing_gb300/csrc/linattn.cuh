@@ -141,6 +141,24 @@ __device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint3
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
+// d += a b with a in NA pieces and b in NB, products of pieces i and j up to i + j = ORDER, the small
+// ones first.  Where all 24 bits are wanted the products are summed by themselves and then added: the
+// units cut their sums off where float32 additions round, and a chain of a hundred would lose 4 bits.
+template <int NA, int NB, int ORDER>
+__device__ __forceinline__ void mma_pieces(float (&d)[4], const uint32_t (&a)[NA][4], const uint32_t (&b)[NB][4], int h) {
+    float t[4] = {};
+    float(&sum)[4] = NB == 3 ? t : d;
+#pragma unroll
+    for (int u = NA - 1; u >= 0; --u)
+#pragma unroll
+        for (int v = NB - 1; v >= 0; --v)
+            if (u + v <= ORDER) mma(sum, a[u], b[v][h], b[v][h + 2]);
+    if (NB == 3) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) d[k] += t[k];
+    }
+}
+
 // ---- sizes ----------------------------------------------------------------------------------
 
 template <class T, int DX, int WARPS, bool BWD>
@@ -196,11 +214,45 @@ __device__ __forceinline__ const T* rows_at(const AttnRows& r, int64_t row, int6
     return static_cast<const T*>(r.data) + row * r.seq + (head / r.share) * r.head;
 }
 
+// A number in two floats, 48 bits.
+struct Two {
+    float hi, lo;
+};
+__device__ __forceinline__ Two add(Two a, Two b) {
+    const float s = a.hi + b.hi, t = s - a.hi;
+    const float e = (a.hi - (s - t)) + (b.hi - t) + (a.lo + b.lo);
+    const float hi = s + e;
+    return {hi, e - (hi - s)};
+}
 // A log decay in units of log2: at most 0 (a NaN stays), and at least -288, where every float32
 // number has become 0.
-__device__ __forceinline__ double log2_decay(float g) {
-    const float c = g > 0.f ? 0.f : (g < -200.f ? -200.f : g);
-    return (double)c * 1.4426950408889634;
+__device__ __forceinline__ Two log2_decay(float g) {
+    const float c = g > 0.f ? 0.f : (g < -200.f ? -200.f : g), hi = c * kLog2e;
+    return {hi, fmaf(c, 1.9259630e-8f, fmaf(c, kLog2e, -hi))};  // log2(e) beyond 24 bits
+}
+// The chunk's sums and factors from the log decays of tokens 2 lane and 2 lane + 1: one warp.
+__device__ __forceinline__ void make_decays(Decays& dc, float g0, float g1, bool reverse, float inter, float update) {
+    const int lane = (int)threadIdx.x & 31;
+    const Two d0 = log2_decay(g0), own = add(d0, log2_decay(g1));
+    Two sum = own;
+#pragma unroll
+    for (int o = 1; o < 32; o *= 2) {
+        const Two v = {__shfl_up_sync(0xffffffffu, sum.hi, o), __shfl_up_sync(0xffffffffu, sum.lo, o)};
+        if (lane >= o) sum = add(v, sum);
+    }
+    const Two all = {__shfl_sync(0xffffffffu, sum.hi, 31), __shfl_sync(0xffffffffu, sum.lo, 31)};
+    Two before = {__shfl_up_sync(0xffffffffu, sum.hi, 1), __shfl_up_sync(0xffffffffu, sum.lo, 1)};
+    if (lane == 0) before = {0.f, 0.f};
+    const Two G[2] = {add(before, d0), sum};
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+        const float gone = ex2(G[k].hi), left = ex2((all.hi - G[k].hi) + (all.lo - G[k].lo));
+        dc.hi[2 * lane + k] = G[k].hi;
+        dc.lo[2 * lane + k] = G[k].lo;
+        dc.inter[2 * lane + k] = (reverse ? left : gone) * inter;
+        dc.update[2 * lane + k] = (reverse ? gone : left) * update;
+    }
+    if (lane == 0) dc.total = ex2(all.hi), dc.total_log2 = all.hi;
 }
 
 // The part of a segment that belongs to one sequence.
@@ -317,47 +369,32 @@ __global__ void __launch_bounds__(WARPS * 32, AttnShape<T, DX, WARPS, BWD>::kBlo
         const int chunks = (int)((part.end - part.begin + C - 1) / C);
         auto chunk_at = [&](int i) { return part.begin + (int64_t)(reverse ? chunks - 1 - i : i) * C; };
         auto count_at = [&](int64_t t) { return (int)(part.end - t < C ? part.end - t : C); };
-        float g0 = 0.f, g1 = 0.f;  // warp 0: the log decays of tokens 2 lane and 2 lane + 1
+        float g0 = 0.f, g1 = 0.f;  // one warp: the log decays of tokens 2 lane and 2 lane + 1
         auto fetch_decays = [&](int64_t t, int count) {
             const T* p = pg + t * a.decay.tok_stride;
             g0 = 2 * lane < count ? to_f(p[2 * lane * a.decay.tok_stride]) : 0.f;
             g1 = 2 * lane + 1 < count ? to_f(p[(2 * lane + 1) * a.decay.tok_stride]) : 0.f;
         };
         fetch(0, chunk_at(0), count_at(chunk_at(0)));
-        if (warp == 0) fetch_decays(chunk_at(0), count_at(chunk_at(0)));
+        if (warp == 0) {
+            fetch_decays(chunk_at(0), count_at(chunk_at(0)));
+            make_decays(decays[0], g0, g1, reverse, a.scale_inter, a.scale_update);
+        }
 
         for (int i = 0; i < chunks; ++i) {
             const int64_t t = chunk_at(i);
             const int count = count_at(t);
-            Decays& dc = decays[i & 1];
-            if (warp == 0) {
-                const double d0 = log2_decay(g0), d1 = d0 + log2_decay(g1);
-                double sum = d1;
-#pragma unroll
-                for (int o = 1; o < 32; o *= 2) {
-                    const double v = __shfl_up_sync(0xffffffffu, sum, o);
-                    if (lane >= o) sum += v;
-                }
-                const double all = __shfl_sync(0xffffffffu, sum, 31);
-                const double G[2] = {sum - d1 + d0, sum};
-#pragma unroll
-                for (int k = 0; k < 2; ++k) {
-                    const float hi = (float)G[k], left = ex2((float)(all - G[k]));
-                    dc.hi[2 * lane + k] = hi;
-                    dc.lo[2 * lane + k] = (float)(G[k] - (double)hi);
-                    dc.inter[2 * lane + k] = (reverse ? left : ex2(hi)) * a.scale_inter;
-                    dc.update[2 * lane + k] = (reverse ? ex2(hi) : left) * a.scale_update;
-                }
-                if (lane == 0) dc.total = ex2((float)all), dc.total_log2 = (float)all;
-                gone += all;
-            }
+            const Decays& dc = decays[i & 1];
             copy_wait<0>();
             __syncthreads();
+            // the next chunk's decays are one warp's, another one's each time
+            const bool ahead = i + 1 < chunks && warp == (i + 1) % WARPS;
             if (i + 1 < chunks) {
                 const int64_t tn = chunk_at(i + 1);
                 if (Shape::kStages == 2) fetch((i + 1) & 1, tn, count_at(tn));
-                if (warp == 0) fetch_decays(tn, count_at(tn));
+                if (ahead) fetch_decays(tn, count_at(tn));
             }
+            if (summary) gone += dc.total_log2;
             const T* sx = stage(i & 1);
             const T* sy = sx + C * XS;
             const T* sz = sy + C * XS;
@@ -383,11 +420,7 @@ __global__ void __launch_bounds__(WARPS * 32, AttnShape<T, DX, WARPS, BWD>::kBlo
                         load_rows<T>(sy, XS, cb * 16, k * 16, fb);
                         block_pieces<T>(fb, pb);
 #pragma unroll
-                        for (int u = NP - 1; u >= 0; --u)
-#pragma unroll
-                            for (int v = NP - 1 - u; v >= 0; --v)
-#pragma unroll
-                                for (int h = 0; h < 2; ++h) mma(acc[2 * n + h], pa[u], pb[v][h], pb[v][h + 2]);
+                        for (int h = 0; h < 2; ++h) mma_pieces<NP, NP, NP - 1>(acc[2 * n + h], pa, pb, h);
                     }
                 }
 #pragma unroll
@@ -444,11 +477,7 @@ __global__ void __launch_bounds__(WARPS * 32, AttnShape<T, DX, WARPS, BWD>::kBlo
                             load_rows<T>(sx, XS, m * 16, k * 16, fa);
                             block_pieces<T>(fa, pa);
 #pragma unroll
-                            for (int u = NP - 1; u >= 0; --u)
-#pragma unroll
-                                for (int v = ORDER - u; v >= 0; --v)
-#pragma unroll
-                                    for (int h = 0; h < 2; ++h) mma(o[m][h], pa[u], ps[v][h], ps[v][h + 2]);
+                            for (int h = 0; h < 2; ++h) mma_pieces<NP, PO, ORDER>(o[m][h], pa, ps, h);
                         }
                     }
 #pragma unroll
@@ -520,11 +549,7 @@ __global__ void __launch_bounds__(WARPS * 32, AttnShape<T, DX, WARPS, BWD>::kBlo
                                 ldmatrix<bf16, false>(weighted + (u * C + m * 16 + (lane & 15)) * PS + k * 16 + (lane >> 4) * 8,
                                                       pw[u]);
 #pragma unroll
-                            for (int u = PO - 1; u >= 0; --u)
-#pragma unroll
-                                for (int v = (ORDER - u < NP - 1 ? ORDER - u : NP - 1); v >= 0; --v)
-#pragma unroll
-                                    for (int h = 0; h < 2; ++h) mma(o[m][h], pw[u], pv[v][h], pv[v][h + 2]);
+                            for (int h = 0; h < 2; ++h) mma_pieces<PO, NP, ORDER>(o[m][h], pw, pv, h);
                         }
                     }
                 } else {
@@ -606,28 +631,32 @@ __global__ void __launch_bounds__(WARPS * 32, AttnShape<T, DX, WARPS, BWD>::kBlo
 #pragma unroll
                     for (int u = 0; u < 3; ++u) pz[k][u][h] = q[u];
                 }
+            // two blocks of 16 rows at once where there are no more pieces than one: four chains
+            constexpr int WIDE = NP == 1 ? 2 : 1;
 #pragma unroll
-            for (int j = 0; j < NX / 2; ++j) {
-                float add[2][4] = {};
+            for (int j = 0; j < NX / 2; j += WIDE) {
+                float add[WIDE][2][4] = {};
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    Pair<T> fy[4];
-                    uint32_t py2[NP][4];
-                    load_cols<T>(sy, XS, k * 16, j * 16, fy);
-                    block_pieces<T>(fy, py2);
+                for (int k = 0; k < 4; ++k)
 #pragma unroll
-                    for (int u = 2; u >= 0; --u)
+                    for (int w = 0; w < WIDE; ++w) {
+                        Pair<T> fy[4];
+                        uint32_t py2[NP][4];
+                        load_cols<T>(sy, XS, k * 16, (j + w) * 16, fy);
+                        block_pieces<T>(fy, py2);
 #pragma unroll
-                        for (int v = (2 - u < NP - 1 ? 2 - u : NP - 1); v >= 0; --v)
+                        for (int h = 0; h < 2; ++h) mma_pieces<3, NP, 2>(add[w][h], pz[k], py2, h);
+                    }
 #pragma unroll
-                            for (int h = 0; h < 2; ++h) mma(add[h], pz[k][u], py2[v][h], py2[v][h + 2]);
-                }
+                for (int w = 0; w < WIDE; ++w)
 #pragma unroll
-                for (int h = 0; h < 2; ++h)
+                    for (int h = 0; h < 2; ++h)
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) S[2 * j + h][k] = fmaf(total, S[2 * j + h][k], add[h][k]);
+                        for (int k = 0; k < 4; ++k)
+                            S[2 * (j + w) + h][k] = fmaf(total, S[2 * (j + w) + h][k], add[w][h][k]);
             }
             some = true;
+            if (ahead) make_decays(decays[(i + 1) & 1], g0, g1, reverse, a.scale_inter, a.scale_update);
 
             if (BWD && pp && !summary) {
                 __syncthreads();

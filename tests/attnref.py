@@ -48,7 +48,7 @@ def group_norm(x, groups, weight, bias, z, silu, eps, offsets):
     outs, means, rstds = [], [], []
     for sp in spans(x, offsets):
         xs = cut(x, sp)
-        p = xs.reshape(xs.shape[0], groups, -1)
+        p = xs.reshape(xs.shape[0], groups, xs.shape[1] // groups)
         if xs.shape[0]:
             mean = p.mean((0, 2))
             rstd = (((p - mean[:, None]) ** 2).mean((0, 2)) + eps) ** -0.5
