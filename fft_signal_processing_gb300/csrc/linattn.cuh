@@ -715,29 +715,6 @@ __global__ void __launch_bounds__(WARPS * 32, AttnShape<T, DX, WARPS, BWD>::kBlo
     }
 }
 
-// Turns what every segment adds into the state that it begins with: one thread for four values.
-__global__ void k_linattn_carry(const AttnArgs a, int64_t quads) {
-    const int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
-    if (i >= quads) return;
-    const int64_t head = blockIdx.y, row = blockIdx.z;
-    float4* p = reinterpret_cast<float4*>(a.carry) + ((row * a.nsegments * a.heads) + head) * quads + i;
-    const int64_t step = a.heads * quads;
-    const float* gone = a.carry_decay + row * a.nsegments * a.heads + head;
-    const int* reset = a.carry_reset + row * a.nsegments * a.heads + head;
-    float4 c = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int64_t k = 0; k < a.nsegments; ++k) {
-        const int64_t s = a.reverse ? a.nsegments - 1 - k : k;
-        const float4 own = p[s * step];
-        p[s * step] = c;
-        const bool r = reset[s * a.heads];
-        const float f = ex2(gone[s * a.heads]);
-        c.x = r ? own.x : fmaf(f, c.x, own.x);
-        c.y = r ? own.y : fmaf(f, c.y, own.y);
-        c.z = r ? own.z : fmaf(f, c.z, own.z);
-        c.w = r ? own.w : fmaf(f, c.w, own.w);
-    }
-}
-
 template <class T, int DX, int WARPS, bool BWD>
 cudaError_t launch_attn(const AttnArgs& args, cudaStream_t s) {
     using Shape = AttnShape<T, DX, WARPS, BWD>;
@@ -751,23 +728,14 @@ cudaError_t launch_attn(const AttnArgs& args, cudaStream_t s) {
     if (e != cudaSuccess) return e;
     AttnArgs a = args;
     const int64_t blocks = a.rows * a.nsegments * a.heads * a.ztiles;
-    if (blocks > INT32_MAX || a.heads > 65535 || a.rows > INT32_MAX) return cudaErrorInvalidValue;
+    if (blocks > INT32_MAX) return cudaErrorInvalidValue;
     if (a.nsegments > 1) {
         a.summary = 1;
         k_linattn<T, DX, WARPS, BWD><<<(unsigned)blocks, Shape::kThreads, Shape::kBytes, s>>>(a);
         e = cudaGetLastError();
         if (e != cudaSuccess) return e;
-        const int64_t quads = a.ztiles * (DX * Shape::kZ / 4);
-        for (int64_t r = 0; r < a.rows; r += 65535) {
-            AttnArgs c = a;
-            const int64_t n = a.rows - r < 65535 ? a.rows - r : 65535;
-            c.carry += r * a.nsegments * a.heads * quads * 4;
-            c.carry_decay += r * a.nsegments * a.heads;
-            c.carry_reset += r * a.nsegments * a.heads;
-            k_linattn_carry<<<dim3((unsigned)((quads + 127) / 128), (unsigned)a.heads, (unsigned)n), 128, 0, s>>>(c, quads);
-            e = cudaGetLastError();
-            if (e != cudaSuccess) return e;
-        }
+        e = attn_carry_pass(a, a.ztiles * (DX * Shape::kZ / 4), s);
+        if (e != cudaSuccess) return e;
         a.summary = 0;
     }
     k_linattn<T, DX, WARPS, BWD><<<(unsigned)blocks, Shape::kThreads, Shape::kBytes, s>>>(a);

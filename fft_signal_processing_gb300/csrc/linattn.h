@@ -58,9 +58,10 @@ inline int attn_warps(int dtype, int64_t dx, int64_t dz) {
     return dz <= 64 || (dtype == FFT_F32 && dx > 128) ? 4 : 8;
 }
 inline int64_t attn_ztile(int dtype, int64_t dx, int64_t dz) { return 16 * attn_warps(dtype, dx, dz); }
-// Values of a carried state: what the threads of a block hold, zeros beyond dx and dz among them.
+// Values of a carried state: what the threads of a block hold, zeros beyond dx and dz among them
+// (the tcgen05 kernel's always have 128 columns of z).
 inline int64_t attn_carry(int dtype, int64_t dx, int64_t dz) {
-    return attn_pad(dx) * attn_ztile(dtype, dx, dz);
+    return attn_pad(dx) * (dtype == FFT_BF16 && dx <= 128 ? 128 : attn_ztile(dtype, dx, dz));
 }
 
 cudaError_t attn_f32_fwd(const AttnArgs& a, cudaStream_t s);
@@ -69,5 +70,12 @@ cudaError_t attn_bf16_fwd(const AttnArgs& a, cudaStream_t s);
 cudaError_t attn_bf16_bwd(const AttnArgs& a, cudaStream_t s);
 cudaError_t attn_f16_fwd(const AttnArgs& a, cudaStream_t s);
 cudaError_t attn_f16_bwd(const AttnArgs& a, cudaStream_t s);
+
+// The same on tcgen05: rows on 16-byte boundaries, dx at most 128; err: the device's error word.
+cudaError_t attn_tc_fwd(const AttnArgs& a, int* err, cudaStream_t s);
+cudaError_t attn_tc_bwd(const AttnArgs& a, int* err, cudaStream_t s);
+
+// Turns what every segment adds into the state that it begins with; quads: float4 of a head's.
+cudaError_t attn_carry_pass(const AttnArgs& a, int64_t quads, cudaStream_t s);
 
 }  // namespace gbfft

@@ -3,6 +3,7 @@
 // tokens, single tokens).  Declared in include/gbfft.h.
 #include "linattn.h"
 #include "seq_overlap.h"
+#include "tma.cuh"
 
 namespace gbfft {
 namespace {
@@ -100,6 +101,29 @@ cudaError_t attn_step(AttnStepArgs a, cudaStream_t s) {
 
 // ---- around the kernel of whole sequences ---------------------------------------------------
 
+// Turns what every segment adds into the state that it begins with: one thread for four values.
+__global__ void k_linattn_carry(const AttnArgs a, int64_t quads) {
+    const int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
+    if (i >= quads) return;
+    const int64_t head = blockIdx.y, row = blockIdx.z;
+    float4* p = reinterpret_cast<float4*>(a.carry) + ((row * a.nsegments * a.heads) + head) * quads + i;
+    const int64_t step = a.heads * quads;
+    const float* gone = a.carry_decay + row * a.nsegments * a.heads + head;
+    const int* reset = a.carry_reset + row * a.nsegments * a.heads + head;
+    float4 c = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int64_t k = 0; k < a.nsegments; ++k) {
+        const int64_t s = a.reverse ? a.nsegments - 1 - k : k;
+        const float4 own = p[s * step];
+        p[s * step] = c;
+        const bool r = reset[s * a.heads];
+        const float f = ex2(gone[s * a.heads]);
+        c.x = r ? own.x : fmaf(f, c.x, own.x);
+        c.y = r ? own.y : fmaf(f, c.y, own.y);
+        c.z = r ? own.z : fmaf(f, c.z, own.z);
+        c.w = r ? own.w : fmaf(f, c.w, own.w);
+    }
+}
+
 // States of sequences without tokens: what they begin with.
 __global__ void k_linattn_empty(const int64_t* offsets, const float* from, float* to, int64_t per) {
     const int64_t q = blockIdx.x;
@@ -150,8 +174,9 @@ __device__ __forceinline__ float tiles_sum(const float* p, int64_t tiles, int64_
 // ka those within the chunk; X in turn is that of the next chunk and what the rows between change.
 // Only between chunks do such sums run on, over terms that were formed from states in two or three
 // pieces, so that what cancels within a chunk is not carried along.
-// One block per segment and head; a warp takes every eighth chunk, two tokens per lane.
+// One block per segment and head; a warp takes every eighth chunk.
 constexpr int kDgWarps = 8, kDgBatch = 64;
+constexpr int kTcChunk = 128;  // tokens of a chunk of the tcgen05 kernel
 
 // What the tokens of a segment's first sequence change (X at the segment's start less that at its
 // end), and whether that sequence ends there.
@@ -177,43 +202,44 @@ __global__ void __launch_bounds__(kDgWarps * 32) k_decay_sums(const DecayGradArg
     }
 }
 
-template <class T>
+// PER: tokens of a chunk per lane.
+template <class T, int PER>
 __global__ void __launch_bounds__(kDgWarps * 32) k_decay_grads(const DecayGradArgs a) {
+    constexpr int C = 32 * PER;
     __shared__ double change[kDgBatch], cross[kDgBatch];
     const int64_t head = blockIdx.x % a.heads, seg = blockIdx.x / a.heads % a.nsegments,
                   row = blockIdx.x / (a.heads * a.nsegments);
     const int64_t t0 = seg * a.segment, t1 = t0 + a.segment < a.length ? t0 + a.segment : a.length;
     const int64_t step = a.heads * a.rows * a.length, at = (head * a.rows + row) * a.length;
     const int lane = (int)threadIdx.x & 31, warp = (int)threadIdx.x >> 5;
-    auto sum2 = [&](const float* p, int64_t t, int64_t end) {
-        return make_float2(t < end ? tiles_sum(p + at + t, a.ztiles, step) : 0.f,
-                           t + 1 < end ? tiles_sum(p + at + t + 1, a.ztiles, step) : 0.f);
+    auto sums = [&](const float* p, int64_t t, int64_t end, float (&v)[PER]) {
+#pragma unroll
+        for (int k = 0; k < PER; ++k) v[k] = t + k < end ? tiles_sum(p + at + t + k, a.ztiles, step) : 0.f;
     };
     for (int64_t stop = t1; stop > t0;) {
         const SeqAt s = seq_at(a.offsets, a.nseq, a.length, row, stop - 1);
         const int64_t begin = s.begin > stop - 1 ? stop - 1 : (s.begin < t0 ? t0 : s.begin), end = stop;
         double X = 0.0;  // at `end`
-        if (s.end <= end || end == a.length) {
-            if (a.final_dots)
-                for (int64_t z = 0; z < a.ztiles; ++z) X += a.final_dots[(z * a.nseq + s.q) * a.heads + head];
-        } else {
-            int64_t k = seg + 1;
-            for (; k < a.nsegments; ++k) {
+        if (!(s.end <= end || end == a.length)) {
+            for (int64_t k = seg + 1; k < a.nsegments; ++k) {
                 const int64_t i = (row * a.nsegments + k) * a.heads + head;
                 X += a.carry[i];
                 if (a.stops[i]) break;
             }
-            if (a.final_dots)
-                for (int64_t z = 0; z < a.ztiles; ++z) X += a.final_dots[(z * a.nseq + s.q) * a.heads + head];
         }
-        const int64_t chunks = (end - begin + kAttnChunk - 1) / kAttnChunk;
+        if (a.final_dots)
+            for (int64_t z = 0; z < a.ztiles; ++z) X += a.final_dots[(z * a.nseq + s.q) * a.heads + head];
+        const int64_t chunks = (end - begin + C - 1) / C;
         for (int64_t c1 = chunks; c1 > 0; c1 -= kDgBatch) {
             const int64_t c0 = c1 > kDgBatch ? c1 - kDgBatch : 0;
             for (int64_t c = c0 + warp; c < c1; c += kDgWarps) {
-                const int64_t t = begin + c * kAttnChunk + 2 * lane;
-                const float2 qi = sum2(a.q_inter, t, end), ki = sum2(a.k_inter, t, end);
-                double v = ((double)qi.x - ki.x) + ((double)qi.y - ki.y);
-                // tokens of the next chunk are not this one's: a chunk is 64 = 2 x 32 tokens
+                const int64_t t = begin + c * C + PER * lane;
+                float qi[PER], ki[PER];
+                sums(a.q_inter, t, end, qi);
+                sums(a.k_inter, t, end, ki);
+                double v = 0.0;
+#pragma unroll
+                for (int k = 0; k < PER; ++k) v += (double)qi[k] - ki[k];
 #pragma unroll
                 for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
                 if (lane == 0) change[c - c0] = v;
@@ -226,38 +252,45 @@ __global__ void __launch_bounds__(kDgWarps * 32) k_decay_grads(const DecayGradAr
             // nothing crosses a sequence's first token but its initial state
             const bool zero = c0 == 0 && !a.initial && (begin == 0 || s.begin == begin);
             for (int64_t c = c0 + warp; c < c1; c += kDgWarps) {
-                const int64_t t = begin + c * kAttnChunk + 2 * lane;
-                const float2 qi = sum2(a.q_inter, t, end), ki = sum2(a.k_inter, t, end);
-                const float2 qa = sum2(a.q_all, t, end), ka = sum2(a.k_all, t, end);
-                // between chunks: what tokens before t have, from the left
-                const float n0 = ki.x - qi.x, n1 = ki.y - qi.y;
-                float left = n0 + n1;
+                const int64_t t = begin + c * C + PER * lane;
+                float qi[PER], ki[PER], w[PER], ka[PER];
+                sums(a.q_inter, t, end, qi);
+                sums(a.k_inter, t, end, ki);
+                sums(a.q_all, t, end, w);
+                sums(a.k_all, t, end, ka);
+                // between chunks: what tokens before t have, from the left; within the chunk, from the right
+                float left = 0.f, right = 0.f;
+#pragma unroll
+                for (int k = 0; k < PER; ++k) {
+                    w[k] = (w[k] - qi[k]) - (ka[k] - ki[k]);
+                    ki[k] -= qi[k];
+                    left += ki[k];
+                    right += w[k];
+                }
 #pragma unroll
                 for (int o = 1; o < 32; o *= 2) {
-                    const float v = __shfl_up_sync(0xffffffffu, left, o);
-                    if (lane >= o) left += v;
+                    const float l = __shfl_up_sync(0xffffffffu, left, o), r = __shfl_down_sync(0xffffffffu, right, o);
+                    if (lane >= o) left += l;
+                    if (lane + o < 32) right += r;
                 }
                 left = __shfl_up_sync(0xffffffffu, left, 1);
+                right = __shfl_down_sync(0xffffffffu, right, 1);
                 if (lane == 0) left = 0.f;
-                // within the chunk, from the right
-                const float w0 = (qa.x - qi.x) - (ka.x - ki.x), w1 = (qa.y - qi.y) - (ka.y - ki.y);
-                float right = w0 + w1;
+                if (lane == 31) right = 0.f;
+                float tail[PER];
 #pragma unroll
-                for (int o = 1; o < 32; o *= 2) {
-                    const float v = __shfl_down_sync(0xffffffffu, right, o);
-                    if (lane + o < 32) right += v;
-                }
+                for (int k = PER - 1; k >= 0; --k) tail[k] = right += w[k];
                 const float base = zero && c == 0 ? 0.f : (float)cross[c - c0];
-                const float dg[2] = {base + left + right, base + (left + n0) + (right - w0)};
 #pragma unroll
-                for (int k = 0; k < 2; ++k) {
+                for (int k = 0; k < PER; ++k) {
+                    const float dg = base + left + tail[k];
+                    left += ki[k];
                     if (t + k >= end) continue;
                     const float g = to_f(static_cast<const T*>(a.decay.data)[row * a.decay.seq_stride +
                                                                            (t + k) * a.decay.tok_stride + head]);
                     // above 0 the decay is 0 whatever its value, below -104 its exponential is
-                    const float v = g > 0.f || g < -104.f ? 0.f : dg[k];
                     static_cast<T*>(a.ddecay.data)[row * a.ddecay.seq_stride + (t + k) * a.ddecay.tok_stride + head] =
-                        from_f<T>(v);
+                        from_f<T>(g > 0.f || g < -104.f ? 0.f : dg);
                 }
             }
             __syncthreads();
@@ -265,6 +298,25 @@ __global__ void __launch_bounds__(kDgWarps * 32) k_decay_grads(const DecayGradAr
         stop = begin;
     }
 }
+
+}  // namespace
+
+cudaError_t attn_carry_pass(const AttnArgs& a, int64_t quads, cudaStream_t s) {
+    if (a.heads > 65535) return cudaErrorInvalidValue;
+    for (int64_t r = 0; r < a.rows; r += 65535) {
+        AttnArgs c = a;
+        const int64_t n = a.rows - r < 65535 ? a.rows - r : 65535;
+        c.carry += r * a.nsegments * a.heads * quads * 4;
+        c.carry_decay += r * a.nsegments * a.heads;
+        c.carry_reset += r * a.nsegments * a.heads;
+        k_linattn_carry<<<dim3((unsigned)((quads + 127) / 128), (unsigned)a.heads, (unsigned)n), 128, 0, s>>>(c, quads);
+        const cudaError_t e = cudaGetLastError();
+        if (e != cudaSuccess) return e;
+    }
+    return cudaSuccess;
+}
+
+namespace {
 
 // ---- checks and plans -----------------------------------------------------------------------
 
@@ -385,18 +437,22 @@ void attn_plan(const fft_linattn_desc& d, int64_t dx, int64_t dz, AttnArgs* a) {
     const int64_t zt = attn_ztile(d.dtype, dx, dz);
     a->ztiles = (dz + zt - 1) / zt;
 }
-int64_t attn_segment(const fft_linattn_desc& d, int64_t ztiles, int64_t resident) {
+// Whether sizes and type are the tcgen05 kernel's; rows have to lie on 16-byte boundaries too.
+bool tc_sizes(const fft_linattn_desc& d, bool backward) {
+    return d.dtype == FFT_BF16 && d.dk <= 128 && (!backward || d.dv <= 128);
+}
+int64_t attn_segment(const fft_linattn_desc& d, int64_t ztiles, int64_t resident, int64_t chunk) {
     const int64_t rows = d.offsets ? 1 : d.nseq, blocks = rows * d.heads * ztiles;
-    int64_t segment = d.length, best = INT64_MAX;
+    int64_t segment = (d.length + chunk - 1) / chunk * chunk, best = INT64_MAX;
     for (int64_t k = 1; k <= 256; ++k) {
         int64_t size = (d.length + k - 1) / k;
-        size = (size + kAttnChunk - 1) / kAttnChunk * kAttnChunk;
+        size = (size + chunk - 1) / chunk * chunk;
         const int64_t n = (d.length + size - 1) / size;
-        const int64_t cost = (blocks * n + resident - 1) / resident * (size / kAttnChunk * (n > 1 ? 3 : 2) + 4) + (n > 1 ? 8 : 0);
+        const int64_t cost = (blocks * n + resident - 1) / resident * (size / chunk * (n > 1 ? 3 : 2) + 4) + (n > 1 ? 8 : 0);
         if (cost < best) best = cost, segment = size;
-        if (size <= 2 * kAttnChunk) break;
+        if (size <= chunk) break;
     }
-    return segment < 1 ? kAttnChunk : segment;
+    return segment < 1 ? chunk : segment;
 }
 void attn_cut(AttnArgs* a, int64_t segment) {
     a->segment = segment;
@@ -423,7 +479,9 @@ void take_carry(AttnArgs* a, int dtype, Taker* t) {
 
 int64_t forward_layout(const fft_linattn_desc& d, AttnArgs* a, char* w) {
     attn_plan(d, d.dk, d.dv, a);
-    attn_cut(a, attn_segment(d, a->ztiles, (int64_t)num_sms() * (attn_warps(d.dtype, d.dk, d.dv) == 4 ? 2 : 1)));
+    const bool tc = tc_sizes(d, false);
+    const int64_t resident = (int64_t)num_sms() * (!tc && attn_warps(d.dtype, d.dk, d.dv) == 4 ? 2 : 1);
+    attn_cut(a, attn_segment(d, a->ztiles, resident, tc ? kTcChunk : kAttnChunk));
     Taker t = {w};
     take_carry(a, d.dtype, &t);
     return t.at;
@@ -440,7 +498,7 @@ int64_t backward_layout(const fft_linattn_desc& d, const fft_linattn_grads* gr, 
     attn_plan(d, d.dv, d.dk, &p->k);
     attn_plan(d, d.dk, d.dv, &p->v);
     const int64_t zk = p->q.ztiles, zv = p->v.ztiles;
-    const int64_t segment = attn_segment(d, zk > zv ? zk : zv, (int64_t)num_sms());
+    const int64_t segment = attn_segment(d, zk > zv ? zk : zv, (int64_t)num_sms(), tc_sizes(d, true) ? kTcChunk : kAttnChunk);
     Taker t = {w};
     for (AttnArgs* a : {&p->q, &p->k, &p->v}) {
         attn_cut(a, segment);
@@ -501,6 +559,23 @@ template <class F32, class B16, class F16>
 cudaError_t by_type(int dtype, F32 f32, B16 b16, F16 f16, const AttnArgs& a, cudaStream_t s) {
     return dtype == FFT_F32 ? f32(a, s) : (dtype == FFT_BF16 ? b16(a, s) : f16(a, s));
 }
+// The device's error word: set by a wait that has run out.
+__device__ int g_attn_error;
+cudaError_t error_word(int** word) {
+    return cudaGetSymbolAddress(reinterpret_cast<void**>(word), g_attn_error);
+}
+// Whether a pass runs on tcgen05: its rows and outputs lie on 16-byte boundaries.
+bool tc_rows(const AttnArgs& a) {
+    auto even = [](int64_t stride) { return stride % 8 == 0; };
+    return a.x.vec == 16 && a.y.vec == 16 && a.z.vec == 16 && (!a.partner.data || a.partner.vec == 16) &&
+           aligned_to(a.out, 16) && even(a.out_seq) && even(a.out_tok) && even(a.out_head);
+}
+cudaError_t run_tc(const AttnArgs& a, bool backward, cudaStream_t s) {
+    int* err = nullptr;
+    const cudaError_t e = error_word(&err);
+    if (e != cudaSuccess) return e;
+    return backward ? attn_tc_bwd(a, err, s) : attn_tc_fwd(a, err, s);
+}
 cudaError_t run_forward(const AttnArgs& a, int dtype, cudaStream_t s) {
     return by_type(dtype, attn_f32_fwd, attn_bf16_fwd, attn_f16_fwd, a, s);
 }
@@ -532,10 +607,13 @@ cudaError_t run_shared(const float* parts, const fft_heads& out, const fft_linat
 
 template <class T>
 cudaError_t finish_backward(const BackwardPlan& p, const fft_linattn_desc& d, const fft_linattn_grads& g,
-                            cudaStream_t s) {
+                            bool tc, cudaStream_t s) {
     const unsigned blocks = (unsigned)(p.g.rows * p.g.nsegments * p.g.heads);
     if (p.g.nsegments > 1) k_decay_sums<<<blocks, kDgWarps * 32, 0, s>>>(p.g);
-    k_decay_grads<T><<<blocks, kDgWarps * 32, 0, s>>>(p.g);
+    if (tc)
+        k_decay_grads<T, kTcChunk / 32><<<blocks, kDgWarps * 32, 0, s>>>(p.g);
+    else
+        k_decay_grads<T, kAttnChunk / 32><<<blocks, kDgWarps * 32, 0, s>>>(p.g);
     cudaError_t e = cudaGetLastError();
     if (e == cudaSuccess && p.dq_parts) e = run_shared<T>(p.dq_parts, g.dq, d, s);
     if (e == cudaSuccess && p.dk_parts) e = run_shared<T>(p.dk_parts, g.dk, d, s);
@@ -583,7 +661,7 @@ extern "C" int fft_linattn_forward(const fft_linattn_desc* d, const fft_heads* o
         a.state_x = d->dv;
         a.state_z = 1;
         set_out(&a, *out, *d, nullptr);
-        TRY(status(run_forward(a, d->dtype, s)));
+        TRY(status(tc_sizes(*d, false) && tc_rows(a) ? run_tc(a, false, s) : run_forward(a, d->dtype, s)));
     }
     return status(fill_empty(*d, d->initial_state, final_state, s));
 }
@@ -639,12 +717,24 @@ extern "C" int fft_linattn_backward(const fft_linattn_desc* d, const fft_linattn
             r->scale_inter = 1.f;
         }
         a.decay = b.decay = c.decay = d->decay;
-        for (const AttnArgs* r : {&a, &b, &c}) TRY(status(run_backward(*r, d->dtype, s)));
-        TRY(status(d->dtype == FFT_F32 ? finish_backward<float>(p, *d, *g, s)
-                                       : (d->dtype == FFT_BF16 ? finish_backward<__nv_bfloat16>(p, *d, *g, s)
-                                                               : finish_backward<__half>(p, *d, *g, s))));
+        // all three on the same kernel: the decay's gradient takes their sums by chunks
+        const bool tc = tc_sizes(*d, true) && tc_rows(a) && tc_rows(b) && tc_rows(c);
+        for (const AttnArgs* r : {&a, &b, &c}) TRY(status(tc ? run_tc(*r, true, s) : run_backward(*r, d->dtype, s)));
+        TRY(status(d->dtype == FFT_F32 ? finish_backward<float>(p, *d, *g, tc, s)
+                                       : (d->dtype == FFT_BF16 ? finish_backward<__nv_bfloat16>(p, *d, *g, tc, s)
+                                                               : finish_backward<__half>(p, *d, *g, tc, s))));
     }
     return status(fill_empty(*d, g->dfinal_state, g->dinitial_state, s));
+}
+
+extern "C" int fft_linattn_check(void* stream) {
+    if (cudaStreamSynchronize((cudaStream_t)stream) != cudaSuccess) return FFT_ERR_CUDA;
+    int *word = nullptr, h = 0;
+    if (error_word(&word) != cudaSuccess || cudaMemcpy(&h, word, sizeof(int), cudaMemcpyDeviceToHost) != cudaSuccess)
+        return FFT_ERR_CUDA;
+    if (h == 0) return FFT_OK;
+    if (cudaMemset(word, 0, sizeof(int)) != cudaSuccess) return FFT_ERR_CUDA;
+    return kerr_status(h);
 }
 
 extern "C" int fft_linattn_step(const fft_linattn_desc* d, const fft_heads* out, float* state, int64_t pool,

@@ -1,0 +1,813 @@
+// Linear attention in bfloat16 on the fifth-generation tensor cores (tcgen05): chunks of 128 tokens,
+// the same products as linattn.cuh, for heads of up to 128 values whose rows lie on 16-byte
+// boundaries.
+//
+// Operands lie in shared memory in the 128-byte swizzle, panels of 64 columns, rows of tokens; the
+// same tile is an operand summed over its columns (scores) and one summed over its rows (outputs,
+// state).  Accumulators lie in tensor memory:
+//   columns   0..127  scores, then the weighted ones as an operand (in place, one or two pieces)
+//           128..255  outputs
+//           256..383  what the chunk adds to S^T: row = column of z, column = column of x
+//           384..511  the first two pieces of the weighted z^T, an operand; the third is in shared
+//                     memory
+// The state itself is float32 in the registers of the warps that own the rows of S^T: what a chunk
+// adds is summed by itself and then added, since the units cut their sums off where float32
+// additions round.  One block per SM, ten warps:
+//   A (four warps, a token each thread): rows of x, weights of the scores, outputs
+//   B (four warps, a column of z each thread): rows of y and z, weighted z^T, the state
+//   one warp issues the products, one sums the decays.
+// They meet at mbarriers, each of which completes once per chunk (twice-buffered ones every other
+// chunk); every wait is bounded in time.
+#pragma once
+
+#include "linattn.h"
+#include "tma.cuh"
+
+namespace gbfft {
+namespace {
+
+using bf16 = __nv_bfloat16;
+constexpr int kTcChunk = 128;
+constexpr int kTcThreads = 320;
+constexpr uint64_t kTcWaitNs = 2000000000ull;
+
+// ---- tcgen05 --------------------------------------------------------------------------------
+
+// Shared-memory operand in the 128-byte swizzle: 8 rows of 128 bytes are 1024 bytes (the stride
+// offset); `lead` bytes from a panel of 64 columns to the next (for operands summed over rows).
+__device__ __forceinline__ uint64_t tc_desc(uint32_t addr, uint32_t lead) {
+    return (uint64_t)((addr & 0x3ffffu) >> 4) | (uint64_t)((lead & 0x3ffffu) >> 4) << 16 | (uint64_t)(1024 >> 4) << 32 |
+           (uint64_t)1 << 46 | (uint64_t)2 << 61;
+}
+// float32 sums of bfloat16 products, 128 rows by n columns; b_rows: the second operand is summed over its rows.
+constexpr uint32_t tc_idesc(int n, bool b_rows) {
+    return 1u << 4 | 1u << 7 | 1u << 10 | (b_rows ? 1u << 16 : 0u) | (uint32_t)(n >> 3) << 17 | (128u >> 4) << 24;
+}
+__device__ __forceinline__ void tc_mma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool add) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d), "l"(a), "l"(b), "r"(idesc),
+        "r"((uint32_t)add)
+        : "memory");
+}
+__device__ __forceinline__ void tc_mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool add) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d), "r"(a), "l"(b), "r"(idesc),
+        "r"((uint32_t)add)
+        : "memory");
+}
+__device__ __forceinline__ void tc_commit(uint64_t* bar) {
+    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_addr(bar))
+                 : "memory");
+}
+__device__ __forceinline__ void tc_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tc_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+// Loads have landed; `r` is among what they have written (so that no use of it moves ahead).
+__device__ __forceinline__ void tc_wait_ld(uint32_t (&r)[32]) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+                   "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]),
+                   "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]), "+r"(r[23]),
+                   "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]), "+r"(r[30]), "+r"(r[31])
+                 :
+                 : "memory");
+}
+__device__ __forceinline__ void tc_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+// 32 columns of this warp's 32 rows, one row per thread.
+__device__ __forceinline__ void tc_ld32(uint32_t addr, uint32_t (&r)[32]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
+        "%15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
+          "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+          "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+        : "r"(addr));
+}
+__device__ __forceinline__ void tc_st32(uint32_t addr, const uint32_t (&r)[32]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
+        "%15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};" ::"r"(addr),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+        "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]),
+        "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
+        "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+        : "memory");
+}
+__device__ __forceinline__ void tc_st16(uint32_t addr, const uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
+        "%15, %16};" ::"r"(addr),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+        "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+        : "memory");
+}
+__device__ __forceinline__ void tc_st8(uint32_t addr, const uint32_t (&r)[8]) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(addr), "r"(r[0]),
+                 "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+                 : "memory");
+}
+__device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
+    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_addr(bar)) : "memory");
+}
+// Sixteen bytes at byte `at` of a swizzled tile: chunk c of row r of a panel.
+__device__ __forceinline__ int tc_chunk(int r, int c) { return r * 128 + ((c ^ (r & 7)) << 4); }
+
+__device__ __forceinline__ uint32_t tc_pack(float x, float y) {
+    uint32_t r;
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(y), "f"(x));
+    return r;
+}
+// What a piece leaves over; nothing where the piece is not finite.
+__device__ __forceinline__ float tc_rest(float v, uint32_t bits) {
+    const float h = __uint_as_float(bits);
+    return fabsf(h) < INFINITY ? v - h : 0.f;
+}
+template <int N>
+__device__ __forceinline__ void tc_split(float x, float y, uint32_t (&p)[N]) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        p[i] = tc_pack(x, y);
+        if (i + 1 < N) {
+            x = tc_rest(x, p[i] << 16);
+            y = tc_rest(y, p[i] & 0xffff0000u);
+        }
+    }
+}
+
+// ---- sizes ----------------------------------------------------------------------------------
+
+template <int DX, int DZ, bool BWD>
+struct TcShape {
+    static constexpr int kPO = BWD ? 2 : 1;  // pieces of weighted scores and of the state as an operand
+    static constexpr int kTileX = kTcChunk * DX * 2, kTileZ = kTcChunk * DZ * 2, kTileS = kPO * DZ * DX * 2,
+                         kTileW = kTcChunk * kTcChunk * 2;
+    static constexpr int kOne = 2 * kTileX + kTileZ + kTileS + kTileW;  // every tile once
+    // y and z twice where that fits, y alone else
+    static constexpr int kStageZ = kOne + kTileX + kTileZ <= 224 * 1024 ? 2 : 1;
+    static constexpr int kStageY = 2;
+    static constexpr int kTiles = kTileX + kStageY * kTileX + kStageZ * kTileZ + kTileS + kTileW;
+};
+
+enum { TC_X, TC_YZ0, TC_YZ1, TC_SCORES, TC_INTER, TC_OUT, TC_UPDATE, TC_WEIGHTED, TC_STATE, TC_WZ, TC_TAKEN, TC_DECAYS,
+       TC_FREE, TC_BARS };
+
+// Behind the tiles.
+struct TcSmall {
+    float2 G[kTcChunk];  // the sums of the decays (log2) in two floats
+    float update[kTcChunk];
+    float total, total_log2, all_hi, all_lo;
+    uint64_t bars[TC_BARS];
+    // of every column of z the place of a value that is not finite, plus 1: the first one, 255 for none;
+    // reversed the last one, 0 for none
+    unsigned char bad_at[2][kTcChunk];
+    int bad_any[2];
+    float warp_sums[4];
+    uint32_t tmem;
+};
+template <class Shape> constexpr int kTcBytes = Shape::kTiles + (int)sizeof(TcSmall);
+static_assert(224 * 1024 + sizeof(TcSmall) <= 227 * 1024, "shared memory");
+
+// A number in two floats, 48 bits.
+struct TcTwo {
+    float hi, lo;
+};
+__device__ __forceinline__ TcTwo tc_add(TcTwo a, TcTwo b) {
+    const float s = a.hi + b.hi, t = s - a.hi;
+    const float e = (a.hi - (s - t)) + (b.hi - t) + (a.lo + b.lo);
+    const float hi = s + e;
+    return {hi, e - (hi - s)};
+}
+// A log decay in units of log2: at most 0 (a NaN stays), at least -288.
+__device__ __forceinline__ TcTwo tc_log2_decay(float g) {
+    const float c = g > 0.f ? 0.f : (g < -200.f ? -200.f : g), hi = c * kLog2e;
+    return {hi, fmaf(c, 1.9259630e-8f, fmaf(c, kLog2e, -hi))};  // log2(e) beyond 24 bits
+}
+
+// The part of a segment that belongs to one sequence (offsets of any kind: it holds token `at` and
+// stays in the segment).
+struct TcPart {
+    int64_t begin, end, seq;
+    bool first, last;
+};
+__device__ __forceinline__ TcPart tc_part(const AttnArgs& a, int64_t row, int64_t t0, int64_t t1, int64_t at) {
+    const SeqAt s = seq_at(a.offsets, a.nseq, a.length, row, at);
+    TcPart p;
+    p.seq = s.q;
+    p.begin = s.begin > at ? at : (s.begin < t0 ? t0 : s.begin);
+    p.end = s.end <= at ? at + 1 : (s.end > t1 ? t1 : s.end);
+    p.first = p.begin == 0 || (s.begin >= t0 && s.begin <= at);
+    p.last = p.end == a.length || (s.end <= t1 && s.end > at);
+    return p;
+}
+
+// Copies rows of up to D values into a swizzled tile, zeros beyond count and dim: 128 threads.
+template <int D>
+__device__ __forceinline__ void tc_load(char* tile, const bf16* g, int64_t tok, int count, int dim, int tid) {
+    constexpr int N = D / 8;
+#pragma unroll 4
+    for (int i = tid; i < kTcChunk * N; i += 128) {
+        const int r = i / N, c = i % N;
+        const bool in = r < count && c * 8 < dim;
+        copy16(tile + (c >> 3) * (kTcChunk * 128) + tc_chunk(r, c & 7), in ? g + r * tok + c * 8 : g, in);
+    }
+}
+
+template <int DX, int DZ, bool BWD>
+__global__ void __launch_bounds__(kTcThreads, 1) k_linattn_tc(const AttnArgs a, int* err) {
+    using Shape = TcShape<DX, DZ, BWD>;
+    constexpr int C = kTcChunk, PO = Shape::kPO, PANEL = C * 128;
+    extern __shared__ __align__(1024) char base[];
+    char* tile_x = base;
+    char* tile_y = tile_x + Shape::kTileX;
+    char* tile_z = tile_y + Shape::kStageY * Shape::kTileX;
+    char* tile_s = tile_z + Shape::kStageZ * Shape::kTileZ;
+    char* tile_w = tile_s + Shape::kTileS;
+    TcSmall& sm = *reinterpret_cast<TcSmall*>(base + Shape::kTiles);
+    uint64_t* bars = sm.bars;
+    if (!tma_stage_aligned(base, err) || (smem_addr(base) & 1023)) return;  // every thread alike
+
+    const int tid = (int)threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    int64_t b = blockIdx.x;
+    const int64_t zt = b % a.ztiles;
+    b /= a.ztiles;
+    const int64_t head = b % a.heads;
+    b /= a.heads;
+    const int64_t seg = b % a.nsegments, row = b / a.nsegments;
+    const int64_t t0 = seg * a.segment, t1 = t0 + a.segment < a.length ? t0 + a.segment : a.length;
+    const int z0 = (int)zt * DZ, dz = (int)a.dz - z0 < DZ ? (int)a.dz - z0 : DZ, dx = (int)a.dx;
+    const bool reverse = a.reverse, summary = a.summary;
+
+    if (warp == 8) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_addr(&sm.tmem))
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    }
+    if (tid == 0) {
+        for (int i = 0; i < TC_BARS; ++i) {
+            const bool commit = i == TC_SCORES || i == TC_INTER || i == TC_OUT || i == TC_UPDATE;
+            mbar_init(&bars[i], commit ? 1 : (i == TC_DECAYS ? 32 : (i == TC_FREE ? 256 : 128)));
+        }
+        fence_mbar_init();
+        sm.bad_any[0] = sm.bad_any[1] = 0;
+    }
+    tc_before();
+    __syncthreads();
+    tc_after();
+    const uint32_t tmem = sm.tmem;
+    const uint32_t kOut = tmem + 128, kAdd = tmem + 256, kWz = tmem + 384;
+    const uint32_t lanes = (uint32_t)(warp & 3) << 21;  // this warp's rows: 32 (warp mod 4) in bits 16 up
+
+    auto wait = [&](int bar, uint32_t phase) { return mbar_wait_bounded(&bars[bar], phase & 1, kTcWaitNs); };
+    // Calls f(part, n) for every part of the segment in the direction of the pass, n its first
+    // chunk's number; a summary takes the part that reaches the next segment.
+    auto each_part = [&](auto f) {
+        int64_t at = summary == reverse ? t0 : t1 - 1;
+        if (!summary) at = reverse ? t1 - 1 : t0;
+        uint32_t n = 0;
+        while (true) {
+            const TcPart p = tc_part(a, row, t0, t1, at);
+            const int chunks = (int)((p.end - p.begin + C - 1) / C);
+            if (!f(p, chunks, n)) return false;
+            n += chunks;
+            at = reverse ? p.begin - 1 : p.end;
+            if (summary || (reverse ? at < t0 : at >= t1)) return true;
+        }
+    };
+    auto chunk_at = [&](const TcPart& p, int chunks, int i) {
+        return p.begin + (int64_t)(reverse ? chunks - 1 - i : i) * C;
+    };
+    auto count_at = [&](const TcPart& p, int64_t t) { return (int)(p.end - t < C ? p.end - t : C); };
+    auto begins_at = [&](const TcPart& p) { return reverse ? p.last : p.first; };
+    // whether the part's first chunk meets a state that is not zero
+    auto starts_with_state = [&](const TcPart& p) { return begins_at(p) ? a.initial != nullptr : !summary && a.nsegments > 1; };
+
+    bool fine = true;
+    if (warp < 4) {
+        // ---- A: a token each thread ----
+        const bf16* px = static_cast<const bf16*>(a.x.data) + row * a.x.seq + (head / a.x.share) * a.x.head;
+        const bf16* pp = BWD && a.partner.data
+                             ? static_cast<const bf16*>(a.partner.data) + row * a.partner.seq +
+                                   (head / a.partner.share) * a.partner.head + z0
+                             : nullptr;
+        const int r = tid;
+        auto fetch = [&](int64_t t, int count) {
+            tc_load<DX>(tile_x, px + t * a.x.tok, a.x.tok, count, dx, tid);
+            copy_commit();
+        };
+        fine = each_part([&](const TcPart& p, int chunks, uint32_t n0) {
+            if (!summary) fetch(chunk_at(p, chunks, 0), count_at(p, chunk_at(p, chunks, 0)));
+            for (int i = 0; i < chunks; ++i) {
+                const uint32_t n = n0 + i, half = n & 1;
+                const int64_t t = chunk_at(p, chunks, i);
+                const int count = count_at(p, t);
+                const bool some = i > 0 || starts_with_state(p);
+                if (summary) {
+                    if (!wait(TC_DECAYS, n)) return false;
+                    mbar_arrive(&bars[TC_FREE]);
+                    continue;
+                }
+                copy_wait<0>();
+                fence_proxy_async_smem();
+                mbar_arrive(&bars[TC_X]);
+                if (!wait(TC_DECAYS, n) || !wait(TC_SCORES, n)) return false;
+                tc_after();
+                const float2 G = sm.G[r];
+                const float inter = ex2(reverse ? (sm.all_hi - G.x) + (sm.all_lo - G.y) : G.x) * a.scale_inter;
+                float diagonal = 0.f;
+                // scores of columns c0 .. c0 + 31 weighted, to pieces
+                auto weigh = [&](int c0, const uint32_t (&s)[32]) {
+                    uint32_t out[PO][16];
+                    const bool none = reverse ? c0 + 31 < warp * 32 : c0 > warp * 32 + 31;
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) {
+                        float v[2] = {0.f, 0.f};
+                        if (!none) {
+                            const float4 g = *reinterpret_cast<const float4*>(&sm.G[c0 + 2 * j]);
+                            const float d[2] = {(G.x - g.x) + (G.y - g.y), (G.x - g.z) + (G.y - g.w)};
+#pragma unroll
+                            for (int e = 0; e < 2; ++e) {
+                                const int c = c0 + 2 * j + e;
+                                const float w = __uint_as_float(s[2 * j + e]) * (ex2(reverse ? -d[e] : d[e]) * a.scale_pair);
+                                v[e] = (reverse ? c >= r : c <= r) ? w : 0.f;
+                                if (BWD && c == r) diagonal = v[e], v[e] = 0.f;
+                            }
+                        }
+                        uint32_t q[PO];
+                        tc_split<PO>(v[0], v[1], q);
+#pragma unroll
+                        for (int u = 0; u < PO; ++u) out[u][j] = q[u];
+                    }
+#pragma unroll
+                    for (int u = 0; u < PO; ++u) tc_st16(tmem + lanes + u * 64 + c0 / 2, out[u]);
+                };
+                if constexpr (BWD) {
+                    // the second pieces go where the last columns of scores are: those are read first
+                    uint32_t s2[32], s3[32], s[32];
+                    tc_ld32(tmem + lanes + 64, s2);
+                    tc_ld32(tmem + lanes + 96, s3);
+                    tc_ld32(tmem + lanes, s);
+                    tc_wait_ld(s2);
+                    tc_wait_ld(s3);
+                    tc_wait_ld(s);
+                    weigh(0, s);
+                    tc_ld32(tmem + lanes + 32, s);
+                    tc_wait_ld(s);
+                    weigh(32, s);
+                    weigh(64, s2);
+                    weigh(96, s3);
+                } else {
+#pragma unroll 1
+                    for (int c0 = 0; c0 < C; c0 += 32) {
+                        uint32_t s[32];
+                        tc_ld32(tmem + lanes + c0, s);
+                        tc_wait_ld(s);
+                        weigh(c0, s);
+                    }
+                }
+                mbar_arrive(&bars[TC_FREE]);
+                const bf16* partner = pp && r < count ? pp + (t + r) * a.partner.tok : nullptr;
+                // partner values of 32 columns, zeros beyond dz
+                auto dot = [&](int c0, const uint32_t (&v)[32], float sum) {
+                    if (!partner) return sum;
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        if (c0 + 8 * j < dz) {
+                            const uint4 q = *reinterpret_cast<const uint4*>(partner + c0 + 8 * j);
+                            const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) {
+                                sum = fmaf(__uint_as_float(w[e] << 16), __uint_as_float(v[8 * j + 2 * e]), sum);
+                                sum = fmaf(__uint_as_float(w[e] & 0xffff0000u), __uint_as_float(v[8 * j + 2 * e + 1]), sum);
+                            }
+                        }
+                    }
+                    return sum;
+                };
+                float between = 0.f;
+                if (some) {
+                    if (!wait(TC_INTER, n)) return false;
+                    tc_after();
+#pragma unroll 1
+                    for (int c0 = 0; c0 < DZ; c0 += 32) {
+                        uint32_t v[32];
+                        tc_ld32(kOut + lanes + c0, v);
+                        tc_wait_ld(v);
+#pragma unroll
+                        for (int j = 0; j < 32; ++j) v[j] = __float_as_uint(__uint_as_float(v[j]) * inter);
+                        tc_st32(kOut + lanes + c0, v);
+                        if (BWD) between = dot(c0, v, between);
+                    }
+                }
+                tc_wait_st();
+                tc_before();
+                mbar_arrive(&bars[TC_WEIGHTED]);
+                // the products with x are over: scores, and (waited for above) those with the state
+                if (i + 1 < chunks) fetch(chunk_at(p, chunks, i + 1), count_at(p, chunk_at(p, chunks, i + 1)));
+                // B has looked at z by the time that the outputs are there
+                if (!wait(TC_OUT, n)) return false;
+                tc_after();
+                const int64_t at = row * a.out_seq + (t + r) * a.out_tok + head * a.out_head + z0;
+                const char* sz = tile_z + (Shape::kStageZ == 2 ? half * Shape::kTileZ : 0);
+                const bool bad = sm.bad_any[half];
+                float all = 0.f;
+#pragma unroll 1
+                for (int c0 = 0; c0 < DZ; c0 += 32) {
+                    uint32_t v[32];
+                    tc_ld32(kOut + lanes + c0, v);
+                    tc_wait_ld(v);
+                    if (BWD) {
+                        all = dot(c0, v, all);
+                        // a token's pair with itself, in float32: it has no part in the decay's gradient
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            const int c = c0 / 8 + j;
+                            const uint4 q = *reinterpret_cast<const uint4*>(sz + (c >> 3) * PANEL + tc_chunk(r, c & 7));
+                            const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) {
+                                float& lo = reinterpret_cast<float&>(v[8 * j + 2 * e]);
+                                float& hi = reinterpret_cast<float&>(v[8 * j + 2 * e + 1]);
+                                lo = fmaf(diagonal, __uint_as_float(w[e] << 16), lo);
+                                hi = fmaf(diagonal, __uint_as_float(w[e] & 0xffff0000u), hi);
+                            }
+                        }
+                    }
+                    if (bad) {  // a value of z that is no number or infinite, by this token
+#pragma unroll
+                        for (int j = 0; j < 32; ++j) {
+                            const int k = sm.bad_at[half][c0 + j];
+                            if (reverse ? r < k : r + 1 >= k) v[j] = 0x7fffffffu;
+                        }
+                    }
+                    if (r < count) {
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            if (c0 + 8 * j >= dz) continue;
+                            if (a.out_f32) {
+                                float* o = static_cast<float*>(a.out) + at + c0 + 8 * j;
+                                *reinterpret_cast<uint4*>(o) = make_uint4(v[8 * j], v[8 * j + 1], v[8 * j + 2], v[8 * j + 3]);
+                                *reinterpret_cast<uint4*>(o + 4) =
+                                    make_uint4(v[8 * j + 4], v[8 * j + 5], v[8 * j + 6], v[8 * j + 7]);
+                            } else {
+                                uint32_t q[4];
+#pragma unroll
+                                for (int e = 0; e < 4; ++e)
+                                    q[e] = tc_pack(__uint_as_float(v[8 * j + 2 * e]), __uint_as_float(v[8 * j + 2 * e + 1]));
+                                *reinterpret_cast<uint4*>(static_cast<bf16*>(a.out) + at + c0 + 8 * j) =
+                                    make_uint4(q[0], q[1], q[2], q[3]);
+                            }
+                        }
+                    }
+                }
+                if (partner) {
+                    const int64_t k = (zt * a.heads + head) * (a.rows * a.length) + row * a.length + t + r;
+                    a.dots_inter[k] = between;
+                    a.dots_all[k] = all;
+                }
+                tc_before();
+                mbar_arrive(&bars[TC_TAKEN]);
+            }
+            return true;
+        });
+    } else if (warp < 8) {
+        // ---- B: a column of z each thread ----
+        const bf16* py = static_cast<const bf16*>(a.y.data) + row * a.y.seq + (head / a.y.share) * a.y.head;
+        const bf16* pz = static_cast<const bf16*>(a.z.data) + row * a.z.seq + (head / a.z.share) * a.z.head + z0;
+        const int m = tid - 128;
+        auto fetch_y = [&](int k, int64_t t, int count) {
+            tc_load<DX>(tile_y + k * Shape::kTileX, py + t * a.y.tok, a.y.tok, count, dx, m);
+        };
+        auto fetch_z = [&](int k, int64_t t, int count) {
+            tc_load<DZ>(tile_z + (Shape::kStageZ == 2 ? k * Shape::kTileZ : 0), pz + t * a.z.tok, a.z.tok, count, dz, m);
+        };
+        float S[DX];  // row m of S^T
+        const int64_t carry_at = (((row * a.nsegments + seg) * a.heads + head) * a.ztiles + zt) * (DX * 128) + m * 4;
+        // S as an operand: row m, columns in panels of 64
+        auto put_state = [&] {
+            if (m < DZ && !summary) {
+#pragma unroll
+                for (int c = 0; c < DX / 8; ++c) {
+                    uint32_t q[4][PO];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) tc_split<PO>(S[8 * c + 2 * e], S[8 * c + 2 * e + 1], q[e]);
+#pragma unroll
+                    for (int u = 0; u < PO; ++u)
+                        *reinterpret_cast<uint4*>(tile_s + u * (DZ * DX * 2) + (c >> 3) * (DZ * 128) + tc_chunk(m, c & 7)) =
+                            make_uint4(q[0][u], q[1][u], q[2][u], q[3][u]);
+                }
+            }
+            fence_proxy_async_smem();
+            tc_before();
+            mbar_arrive(&bars[TC_STATE]);
+        };
+        double gone = 0.0;
+        bool from_start = false;
+        fine = each_part([&](const TcPart& p, int chunks, uint32_t n0) {
+            const int64_t state_at = (p.seq * a.heads + head) * a.dx * a.dz;
+            const int64_t mine = (z0 + m) * a.state_z;
+            from_start = begins_at(p);
+#pragma unroll
+            for (int j = 0; j < DX; ++j) S[j] = 0.f;
+            if (from_start) {
+                if (a.initial && m < dz) {
+                    const float* q = a.initial + state_at + mine;
+#pragma unroll
+                    for (int j = 0; j < DX; ++j)
+                        if (j < dx) S[j] = q[j * a.state_x];
+                }
+            } else if (!summary && a.nsegments > 1) {
+                const float4* q = reinterpret_cast<const float4*>(a.carry + carry_at);
+#pragma unroll
+                for (int j = 0; j < DX / 4; ++j) {
+                    const float4 v = q[j * 128];
+                    S[4 * j] = v.x, S[4 * j + 1] = v.y, S[4 * j + 2] = v.z, S[4 * j + 3] = v.w;
+                }
+            }
+            // the last chunk's products are over (its outputs' too, which read z)
+            if (n0 > 0 && !summary && !wait(TC_OUT, n0 - 1)) return false;
+            fetch_y(n0 & 1, chunk_at(p, chunks, 0), count_at(p, chunk_at(p, chunks, 0)));
+            fetch_z(n0 & 1, chunk_at(p, chunks, 0), count_at(p, chunk_at(p, chunks, 0)));
+            copy_commit();
+            put_state();
+            for (int i = 0; i < chunks; ++i) {
+                const uint32_t n = n0 + i, half = n & 1;
+                copy_wait<0>();
+                fence_proxy_async_smem();
+                mbar_arrive(&bars[TC_YZ0 + half]);
+                asm volatile("bar.sync 1, 128;" ::: "memory");  // all of z is there
+                const bool next = i + 1 < chunks;
+                const int64_t tn = next ? chunk_at(p, chunks, i + 1) : 0;
+                // the stage of the chunk before is free when its outputs are there (its part of the
+                // state was waited for) and, in the gradients, A has read its rows of z
+                if (i > 0 && !summary && (!wait(TC_OUT, n - 1) || (BWD && !wait(TC_TAKEN, n - 1)))) return false;
+                if (next) {
+                    fetch_y(half ^ 1, tn, count_at(p, tn));
+                    if (Shape::kStageZ == 2) fetch_z(half ^ 1, tn, count_at(p, tn));
+                    copy_commit();
+                }
+                if (!wait(TC_DECAYS, n)) return false;
+                const float total = sm.total;
+                if (summary) gone += sm.total_log2;
+                // column m of z, weighted, in three pieces
+                char* sz = tile_z + (Shape::kStageZ == 2 ? half * Shape::kTileZ : 0) + (m >> 6) * PANEL + (m & 7) * 2;
+                float odd = 0.f;
+#pragma unroll 1
+                for (int k = 0; k < C / 16; ++k) {
+                    uint32_t q[3][8];
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                        float v[2] = {0.f, 0.f};
+                        if (m < DZ) {
+#pragma unroll
+                            for (int e = 0; e < 2; ++e) {
+                                const int tk = 16 * k + 2 * j + e;
+                                const uint32_t u = *reinterpret_cast<const unsigned short*>(sz + tc_chunk(tk, (m >> 3) & 7));
+                                v[e] = __uint_as_float(u << 16);
+                                odd = fmaf(v[e], 0.f, odd);
+                            }
+                        }
+                        const float2 w = *reinterpret_cast<const float2*>(&sm.update[16 * k + 2 * j]);
+                        uint32_t s[3];
+                        tc_split<3>(v[0] * w.x, v[1] * w.y, s);
+#pragma unroll
+                        for (int u = 0; u < 3; ++u) q[u][j] = s[u];
+                    }
+                    tc_st8(kWz + lanes + 8 * k, q[0]);
+                    tc_st8(kWz + lanes + 64 + 8 * k, q[1]);
+#pragma unroll
+                    for (int c = 0; c < 2; ++c)
+                        *reinterpret_cast<uint4*>(tile_w + (k >> 2) * PANEL + tc_chunk(m, (k & 3) * 2 + c)) =
+                            make_uint4(q[2][4 * c], q[2][4 * c + 1], q[2][4 * c + 2], q[2][4 * c + 3]);
+                }
+                mbar_arrive(&bars[TC_FREE]);
+                if (!summary) {
+                    // 0 times what is not finite is not 0: such values leave the tile, and the outputs
+                    // that they are in are set by hand
+                    const bool any = __any_sync(0xffffffffu, !(odd == 0.f));
+                    int k = reverse ? 0 : 255;
+                    if (!(odd == 0.f)) {
+                        for (int tk = 0; tk < C; ++tk) {
+                            unsigned short* u = reinterpret_cast<unsigned short*>(sz + tc_chunk(tk, (m >> 3) & 7));
+                            if ((*u & 0x7f80) == 0x7f80) {
+                                *u = 0;
+                                if (reverse || k == 255) k = tk + 1;
+                            }
+                        }
+                    }
+                    sm.bad_at[half][m] = (unsigned char)k;
+                    if (lane == 0 && any) atomicOr(&sm.bad_any[half], 1 << (warp & 3));
+                    if (lane == 0 && !any) atomicAnd(&sm.bad_any[half], ~(1 << (warp & 3)));
+                }
+                tc_wait_st();
+                fence_proxy_async_smem();
+                tc_before();
+                mbar_arrive(&bars[TC_WZ]);
+
+                if (!wait(TC_UPDATE, n)) return false;
+                tc_after();
+#pragma unroll
+                for (int c0 = 0; c0 < DX; c0 += 32) {
+                    uint32_t v[32];
+                    tc_ld32(kAdd + lanes + c0, v);
+                    tc_wait_ld(v);
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) S[c0 + j] = fmaf(total, S[c0 + j], __uint_as_float(v[j]));
+                }
+                if (next) {
+                    put_state();
+                    if (Shape::kStageZ == 1) {
+                        if (!summary && (!wait(TC_OUT, n) || (BWD && !wait(TC_TAKEN, n)))) return false;
+                        fetch_z(0, tn, count_at(p, tn));
+                        copy_commit();
+                    }
+                }
+            }
+            if (!summary && (reverse ? p.first : p.last)) {
+                if (a.final_state && m < dz) {
+                    float* q = a.final_state + state_at + mine;
+#pragma unroll
+                    for (int j = 0; j < DX; ++j)
+                        if (j < dx) q[j * a.state_x] = S[j];
+                }
+                if (BWD && a.final_dot) {
+                    const float* q = a.final_dot + state_at + mine;
+                    float sum = 0.f;
+#pragma unroll
+                    for (int j = 0; j < DX; ++j)
+                        if (j < dx && m < dz) sum = fmaf(S[j], q[j * a.state_x], sum);
+#pragma unroll
+                    for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+                    if (lane == 0) sm.warp_sums[warp - 4] = sum;
+                    asm volatile("bar.sync 1, 128;" ::: "memory");
+                    if (m == 0)
+                        a.final_dots[(zt * a.nseq + p.seq) * a.heads + head] =
+                            (sm.warp_sums[0] + sm.warp_sums[1]) + (sm.warp_sums[2] + sm.warp_sums[3]);
+                    asm volatile("bar.sync 1, 128;" ::: "memory");
+                }
+            }
+            // A reads z for the last outputs until it has taken them
+            if (BWD && !summary && !wait(TC_TAKEN, n0 + chunks - 1)) return false;
+            return true;
+        });
+        copy_wait<0>();
+        if (summary && fine) {
+            float4* q = reinterpret_cast<float4*>(a.carry + carry_at);
+#pragma unroll
+            for (int j = 0; j < DX / 4; ++j) q[j * 128] = make_float4(S[4 * j], S[4 * j + 1], S[4 * j + 2], S[4 * j + 3]);
+            if (zt == 0 && m == 0) {
+                const int64_t i = (row * a.nsegments + seg) * a.heads + head;
+                a.carry_decay[i] = (float)gone;
+                a.carry_reset[i] = from_start;
+            }
+        }
+    } else if (warp == 8) {
+        // ---- the products, issued by one thread ----
+        const uint32_t x = smem_addr(tile_x), y = smem_addr(tile_y), z = smem_addr(tile_z), s = smem_addr(tile_s),
+                       w = smem_addr(tile_w);
+        fine = each_part([&](const TcPart& p, int chunks, uint32_t n0) {
+            bool good = true;
+            const bool start = starts_with_state(p);
+            if (lane == 0) {
+                for (int i = 0; i < chunks && good; ++i) {
+                    const uint32_t n = n0 + i, half = n & 1;
+                    const uint32_t yn = y + half * Shape::kTileX, zn = z + (Shape::kStageZ == 2 ? half * Shape::kTileZ : 0);
+                    const bool some = i > 0 || start;
+                    good = (summary || wait(TC_X, n)) && wait(TC_YZ0 + half, n >> 1);
+                    // scores go over the weighted ones of the chunk before
+                    good = good && (summary || n == 0 || wait(TC_OUT, n - 1));
+                    if (!good) break;
+                    tc_after();
+                    if (!summary) {
+#pragma unroll
+                        for (int k = 0; k < DX / 16; ++k)
+                            tc_mma(tmem, tc_desc(x + (k >> 2) * PANEL + (k & 3) * 32, 16),
+                                   tc_desc(yn + (k >> 2) * PANEL + (k & 3) * 32, 16), tc_idesc(C, false), k > 0);
+                        tc_commit(&bars[TC_SCORES]);
+                    }
+                    good = wait(TC_STATE, n) && (summary || n == 0 || wait(TC_TAKEN, n - 1));
+                    if (!good) break;
+                    tc_after();
+                    if (!summary) {
+                        if (some) {
+#pragma unroll
+                            for (int u = PO - 1; u >= 0; --u)
+#pragma unroll
+                                for (int k = 0; k < DX / 16; ++k)
+                                    tc_mma(kOut, tc_desc(x + (k >> 2) * PANEL + (k & 3) * 32, 16),
+                                           tc_desc(s + u * (DZ * DX * 2) + (k >> 2) * (DZ * 128) + (k & 3) * 32, 16),
+                                           tc_idesc(DZ, false), u < PO - 1 || k > 0);
+                        }
+                        tc_commit(&bars[TC_INTER]);  // once per chunk, whether there was a state or not
+                    }
+                    good = wait(TC_WZ, n);
+                    if (!good) break;
+                    tc_after();
+#pragma unroll
+                    for (int k = 0; k < C / 16; ++k)
+                        tc_mma(kAdd, tc_desc(w + (k >> 2) * PANEL + (k & 3) * 32, 16),
+                               tc_desc(yn + k * 2048, PANEL), tc_idesc(DX, true), k > 0);
+#pragma unroll
+                    for (int u = 1; u >= 0; --u)
+#pragma unroll
+                        for (int k = 0; k < C / 16; ++k)
+                            tc_mma_ts(kAdd, kWz + u * 64 + k * 8, tc_desc(yn + k * 2048, PANEL), tc_idesc(DX, true), true);
+                    tc_commit(&bars[TC_UPDATE]);
+                    if (summary) continue;
+                    good = wait(TC_WEIGHTED, n);
+                    if (!good) break;
+                    tc_after();
+#pragma unroll
+                    for (int u = PO - 1; u >= 0; --u)
+#pragma unroll
+                        for (int k = 0; k < C / 16; ++k)
+                            tc_mma_ts(kOut, tmem + u * 64 + k * 8, tc_desc(zn + k * 2048, PANEL), tc_idesc(DZ, true),
+                                      some || u < PO - 1 || k > 0);
+                    tc_commit(&bars[TC_OUT]);
+                }
+            }
+            return __all_sync(0xffffffffu, good) != 0;
+        });
+    } else {
+        // ---- decays: four tokens per lane ----
+        const bf16* pg = static_cast<const bf16*>(a.decay.data) + row * a.decay.seq_stride + head;
+        fine = each_part([&](const TcPart& p, int chunks, uint32_t n0) {
+            float g[4];
+            auto fetch = [&](int i) {
+                const int64_t t = chunk_at(p, chunks, i);
+                const int count = count_at(p, t);
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    g[k] = 4 * lane + k < count ? to_f(pg[(t + 4 * lane + k) * a.decay.tok_stride]) : 0.f;
+            };
+            fetch(0);
+            for (int i = 0; i < chunks; ++i) {
+                const uint32_t n = n0 + i;
+                TcTwo d[4], sum;
+                d[0] = tc_log2_decay(g[0]);
+#pragma unroll
+                for (int k = 1; k < 4; ++k) d[k] = tc_add(d[k - 1], tc_log2_decay(g[k]));
+                sum = d[3];
+                if (i + 1 < chunks) fetch(i + 1);
+#pragma unroll
+                for (int o = 1; o < 32; o *= 2) {
+                    const TcTwo v = {__shfl_up_sync(0xffffffffu, sum.hi, o), __shfl_up_sync(0xffffffffu, sum.lo, o)};
+                    if (lane >= o) sum = tc_add(v, sum);
+                }
+                const TcTwo all = {__shfl_sync(0xffffffffu, sum.hi, 31), __shfl_sync(0xffffffffu, sum.lo, 31)};
+                TcTwo before = {__shfl_up_sync(0xffffffffu, sum.hi, 1), __shfl_up_sync(0xffffffffu, sum.lo, 1)};
+                if (lane == 0) before = {0.f, 0.f};
+                if (n > 0 && !wait(TC_FREE, n - 1)) return false;
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const TcTwo G = tc_add(before, d[k]);
+                    sm.G[4 * lane + k] = make_float2(G.hi, G.lo);
+                    sm.update[4 * lane + k] = ex2(reverse ? G.hi : (all.hi - G.hi) + (all.lo - G.lo)) * a.scale_update;
+                }
+                if (lane == 0) sm.total = ex2(all.hi), sm.total_log2 = sm.all_hi = all.hi, sm.all_lo = all.lo;
+                mbar_arrive(&bars[TC_DECAYS]);
+            }
+            return true;
+        });
+    }
+    copy_wait<0>();
+    if (!fine && lane == 0) atomicCAS(err, 0, KERR_WAIT_TIMEOUT);
+    tc_before();
+    __syncthreads();
+    if (warp == 8) {
+        tc_after();
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
+    }
+}
+
+}  // namespace
+
+template <int DX, int DZ, bool BWD>
+cudaError_t launch_attn_tc(const AttnArgs& args, int* err, cudaStream_t s) {
+    using Shape = TcShape<DX, DZ, BWD>;
+    static LaunchCache cache;
+    LaunchGeom g;
+    cudaError_t e = cache.get(
+        [](int dev, LaunchGeom* out) {
+            return setup_persistent(k_linattn_tc<DX, DZ, BWD>, kTcThreads, kTcBytes<Shape>, dev, out);
+        },
+        &g);
+    if (e != cudaSuccess) return e;
+    AttnArgs a = args;
+    const int64_t blocks = a.rows * a.nsegments * a.heads * a.ztiles;
+    if (blocks > INT32_MAX) return cudaErrorInvalidValue;
+    if (a.nsegments > 1) {
+        a.summary = 1;
+        k_linattn_tc<DX, DZ, BWD><<<(unsigned)blocks, kTcThreads, kTcBytes<Shape>, s>>>(a, err);
+        e = cudaGetLastError();
+        if (e == cudaSuccess) e = attn_carry_pass(a, a.ztiles * (DX * 128 / 4), s);
+        if (e != cudaSuccess) return e;
+        a.summary = 0;
+    }
+    k_linattn_tc<DX, DZ, BWD><<<(unsigned)blocks, kTcThreads, kTcBytes<Shape>, s>>>(a, err);
+    return cudaGetLastError();
+}
+
+}  // namespace gbfft

@@ -110,6 +110,7 @@ def declare(L):
     L.fft_linattn_workspace.argtypes = [desc, ctypes.c_int, ctypes.POINTER(sz)]
     L.fft_linattn_forward.argtypes = [desc, desc, vp, vp, sz, vp]
     L.fft_linattn_backward.argtypes = [desc, desc, vp, sz, vp]
+    L.fft_linattn_check.argtypes = [vp]
     L.fft_linattn_step.argtypes = [desc, desc, vp, i64, vp, vp, vp]
     L.fft_norm_forward.argtypes = [desc, vp, i64, vp, i64, vp, i64, vp, vp, i64, vp]
     L.fft_norm_workspace.argtypes = [desc, ctypes.POINTER(sz)]
@@ -123,7 +124,7 @@ def declare(L):
 SYMBOLS = ("fft_conv_forward", "fft_conv_workspace", "fft_conv_backward", "fft_conv_step",
            "fft_scan_workspace", "fft_scan_forward", "fft_scan_backward", "fft_scan_step",
            "fft_linattn_workspace", "fft_linattn_forward", "fft_linattn_backward",
-           "fft_linattn_step", "fft_norm_forward", "fft_norm_workspace", "fft_norm_backward",
+           "fft_linattn_step", "fft_linattn_check", "fft_norm_forward", "fft_norm_workspace", "fft_norm_backward",
            "fft_gnorm_workspace", "fft_gnorm_forward", "fft_gnorm_backward")
 
 

@@ -571,6 +571,12 @@ typedef struct fft_linattn_grads {
 int fft_linattn_backward(const fft_linattn_desc* d, const fft_linattn_grads* g, void* workspace,
                          size_t workspace_bytes, void* stream);
 
+/* fft_linattn_check - device-side waits of the calls for whole sequences are bounded (2 s); one that
+ * gives up makes its kernel stop early (outputs are then undefined) and sets an error word of the
+ * library on that device.  Synchronises `stream`, reads and clears the word: FFT_OK, FFT_ERR_TIMEOUT
+ * or FFT_ERR_CUDA. */
+int fft_linattn_check(void* stream);
+
 /* fft_linattn_step - one token for each of nseq sequences (length 1, offsets NULL, initial_state
  * not used; rows at seq_stride): state pool [pool][heads][dk][dv] float32, slots as for
  * fft_conv_step.  out may not overlap what is read. */
