@@ -148,7 +148,8 @@ __global__ void k_linattn_shared(const float* parts, fft_heads out, int64_t leng
 struct DecayGradArgs {
     fft_seq decay, ddecay;
     const int64_t* offsets;
-    int64_t nseq, length, rows, heads, segment, nsegments, ztiles;
+    int64_t nseq, length, rows, heads, segment, nsegments;
+    int64_t ztiles, final_tiles;  // that the sums of rows, of states, come in
     int initial;  // sequences have initial states
     // [ztile][head][row * length + t]: of the rows of dq and dk, between chunks and altogether
     const float* q_inter;
@@ -228,7 +229,7 @@ __global__ void __launch_bounds__(kDgWarps * 32) k_decay_grads(const DecayGradAr
             }
         }
         if (a.final_dots)
-            for (int64_t z = 0; z < a.ztiles; ++z) X += a.final_dots[(z * a.nseq + s.q) * a.heads + head];
+            for (int64_t z = 0; z < a.final_tiles; ++z) X += a.final_dots[(z * a.nseq + s.q) * a.heads + head];
         const int64_t chunks = (end - begin + C - 1) / C;
         for (int64_t c1 = chunks; c1 > 0; c1 -= kDgBatch) {
             const int64_t c0 = c1 > kDgBatch ? c1 - kDgBatch : 0;
@@ -504,7 +505,8 @@ int64_t backward_layout(const fft_linattn_desc& d, const fft_linattn_grads* gr, 
         attn_cut(a, segment);
         take_carry(a, d.dtype, &t);
     }
-    const int64_t tokens = p->q.rows * d.length, dots = zk * d.heads * tokens;
+    // the tcgen05 kernel leaves the sums of rows in halves
+    const int64_t tokens = p->q.rows * d.length, dots = (tc_sizes(d, true) ? 2 : 1) * zk * d.heads * tokens;
     p->q.dots_inter = t.take<float>(dots);
     p->q.dots_all = t.take<float>(dots);
     p->k.dots_inter = t.take<float>(dots);
@@ -528,7 +530,7 @@ int64_t backward_layout(const fft_linattn_desc& d, const fft_linattn_grads* gr, 
     g.heads = d.heads;
     g.segment = segment;
     g.nsegments = p->q.nsegments;
-    g.ztiles = zk;
+    g.ztiles = g.final_tiles = zk;
     g.initial = d.initial_state != nullptr;
     g.q_inter = p->q.dots_inter;
     g.q_all = p->q.dots_all;
@@ -720,6 +722,7 @@ extern "C" int fft_linattn_backward(const fft_linattn_desc* d, const fft_linattn
         // all three on the same kernel: the decay's gradient takes their sums by chunks
         const bool tc = tc_sizes(*d, true) && tc_rows(a) && tc_rows(b) && tc_rows(c);
         for (const AttnArgs* r : {&a, &b, &c}) TRY(status(tc ? run_tc(*r, true, s) : run_backward(*r, d->dtype, s)));
+        if (tc) p.g.ztiles *= 2;
         TRY(status(d->dtype == FFT_F32 ? finish_backward<float>(p, *d, *g, tc, s)
                                        : (d->dtype == FFT_BF16 ? finish_backward<__nv_bfloat16>(p, *d, *g, tc, s)
                                                                : finish_backward<__half>(p, *d, *g, tc, s))));

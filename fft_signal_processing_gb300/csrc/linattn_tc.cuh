@@ -12,10 +12,12 @@
 //                     memory
 // The state itself is float32 in the registers of the warps that own the rows of S^T: what a chunk
 // adds is summed by itself and then added, since the units cut their sums off where float32
-// additions round.  One block per SM, ten warps:
-//   A (four warps, a token each thread): rows of x, weights of the scores, outputs
-//   B (four warps, a column of z each thread): rows of y and z, weighted z^T, the state
-//   one warp issues the products, one sums the decays.
+// additions round.  One block per SM, twenty warps, two for every 32 rows of tensor memory:
+//   A (eight warps, half a token's columns each thread): rows of x, weights of the scores, outputs
+//   B (eight warps, half a row of S^T each thread): rows of y and z, weighted z^T, the state
+//   one warp issues the products, one sums the decays (and two fill up the last group of four).
+// A weight exp(G[r] - G[c]) of another block of 32 columns than the row's own is a product of one
+// factor for each row and one for each column, both from the end of the columns' block (at most 1).
 // They meet at mbarriers, each of which completes once per chunk (twice-buffered ones every other
 // chunk); every wait is bounded in time.
 #pragma once
@@ -28,7 +30,7 @@ namespace {
 
 using bf16 = __nv_bfloat16;
 constexpr int kTcChunk = 128;
-constexpr int kTcThreads = 320;
+constexpr int kTcThreads = 640, kTcGroup = 256;  // A and B: kTcGroup each
 constexpr uint64_t kTcWaitNs = 2000000000ull;
 
 // ---- tcgen05 --------------------------------------------------------------------------------
@@ -109,6 +111,40 @@ __device__ __forceinline__ void tc_st8(uint32_t addr, const uint32_t (&r)[8]) {
                  "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
                  : "memory");
 }
+__device__ __forceinline__ void tc_ld16(uint32_t addr, uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
+        "%15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(addr));
+}
+__device__ __forceinline__ void tc_wait_ld16(uint32_t (&r)[16]) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+                   "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])
+                 :
+                 : "memory");
+}
+// 16 rows by 8 columns in the layout of a matrix load: thread l has rows l / 4 (r[0], r[2]) and
+// l / 4 + 8, columns l % 4 (r[0], r[1]) and l % 4 + 4.
+__device__ __forceinline__ void tc_st_block(uint32_t addr, const uint32_t (&r)[4]) {
+    asm volatile("tcgen05.st.sync.aligned.16x128b.x2.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(r[0]), "r"(r[1]),
+                 "r"(r[2]), "r"(r[3])
+                 : "memory");
+}
+// Four 8 x 8 blocks of shared memory, row addresses from lanes 0..7, 8..15, ...; transposed.
+__device__ __forceinline__ void tc_ldmatrix_t(uint32_t addr, uint32_t (&f)[4]) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(f[0]), "=r"(f[1]), "=r"(f[2]), "=r"(f[3])
+                 : "r"(addr)
+                 : "memory");
+}
+__device__ __forceinline__ void tc_stmatrix(uint32_t addr, const uint32_t (&f)[4]) {
+    asm volatile("stmatrix.sync.aligned.m8n8.x4.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(f[0]), "r"(f[1]),
+                 "r"(f[2]), "r"(f[3])
+                 : "memory");
+}
 __device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
     asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_addr(bar)) : "memory");
 }
@@ -120,20 +156,16 @@ __device__ __forceinline__ uint32_t tc_pack(float x, float y) {
     asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(y), "f"(x));
     return r;
 }
-// What a piece leaves over; nothing where the piece is not finite.
-__device__ __forceinline__ float tc_rest(float v, uint32_t bits) {
-    const float h = __uint_as_float(bits);
-    return fabsf(h) < INFINITY ? v - h : 0.f;
+__device__ __forceinline__ float2 tc_values(uint32_t p) {
+    return make_float2(__uint_as_float(p << 16), __uint_as_float(p & 0xffff0000u));
 }
+// Pieces of 8 bits (of an infinity: itself and no numbers).
 template <int N>
-__device__ __forceinline__ void tc_split(float x, float y, uint32_t (&p)[N]) {
+__device__ __forceinline__ void tc_split(float2 v, uint32_t (&p)[N]) {
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-        p[i] = tc_pack(x, y);
-        if (i + 1 < N) {
-            x = tc_rest(x, p[i] << 16);
-            y = tc_rest(y, p[i] & 0xffff0000u);
-        }
+        p[i] = tc_pack(v.x, v.y);
+        if (i + 1 < N) v = fma2(tc_values(p[i]), splat(-1.f), v);
     }
 }
 
@@ -154,21 +186,28 @@ struct TcShape {
 enum { TC_X, TC_YZ0, TC_YZ1, TC_SCORES, TC_INTER, TC_OUT, TC_UPDATE, TC_WEIGHTED, TC_STATE, TC_WZ, TC_TAKEN, TC_DECAYS,
        TC_FREE, TC_BARS };
 
-// Behind the tiles.
+// Behind the tiles.  BUFFERS: stages of z.
+template <bool BWD, int BUFFERS>
 struct TcSmall {
     float2 G[kTcChunk];  // the sums of the decays (log2) in two floats
     float update[kTcChunk];
+    float column[kTcChunk];  // factors of the columns of scores, from the end of their block of 32
     float total, total_log2, all_hi, all_lo;
     uint64_t bars[TC_BARS];
-    // of every column of z the place of a value that is not finite, plus 1: the first one, 255 for none;
-    // reversed the last one, 0 for none
-    unsigned char bad_at[2][kTcChunk];
-    int bad_any[2];
-    float warp_sums[4];
+    // of every column of z, by halves of the tokens, the place of a value that is not finite, plus 1:
+    // the first one, 255 for none; reversed the last one, 0 for none.  Set where bad_any is.
+    unsigned char bad_at[BUFFERS][2][kTcChunk];
+    int bad_any[BUFFERS];
+    float diagonal[BWD ? kTcChunk : 1];  // weighted scores of tokens with themselves
+    float warp_sums[8];
     uint32_t tmem;
 };
-template <class Shape> constexpr int kTcBytes = Shape::kTiles + (int)sizeof(TcSmall);
-static_assert(224 * 1024 + sizeof(TcSmall) <= 227 * 1024, "shared memory");
+template <int DX, int DZ, bool BWD> constexpr int tc_bytes() {
+    using Shape = TcShape<DX, DZ, BWD>;
+    constexpr int bytes = Shape::kTiles + (int)sizeof(TcSmall<BWD, Shape::kStageZ>);
+    static_assert(bytes <= 227 * 1024, "shared memory");
+    return bytes;
+}
 
 // A number in two floats, 48 bits.
 struct TcTwo {
@@ -203,16 +242,25 @@ __device__ __forceinline__ TcPart tc_part(const AttnArgs& a, int64_t row, int64_
     return p;
 }
 
-// Copies rows of up to D values into a swizzled tile, zeros beyond count and dim: 128 threads.
+// Copies rows of up to D values into a swizzled tile, zeros beyond count and dim.  A thread's rows
+// are a multiple of 8 apart, so the swizzle is the same for all of them.
 template <int D>
 __device__ __forceinline__ void tc_load(char* tile, const bf16* g, int64_t tok, int count, int dim, int tid) {
-    constexpr int N = D / 8;
-#pragma unroll 4
-    for (int i = tid; i < kTcChunk * N; i += 128) {
-        const int r = i / N, c = i % N;
-        const bool in = r < count && c * 8 < dim;
-        copy16(tile + (c >> 3) * (kTcChunk * 128) + tc_chunk(r, c & 7), in ? g + r * tok + c * 8 : g, in);
+    constexpr int N = D / 8, STEP = kTcGroup / N;
+    static_assert(STEP % 8 == 0, "rows of a thread");
+    const int c = tid % N, r = tid / N;
+    const bf16* src = g + r * tok + c * 8;
+    char* dst = tile + (c >> 3) * (kTcChunk * 128) + tc_chunk(r, c & 7);
+    const int live = c * 8 < dim ? count : 0;
+#pragma unroll
+    for (int k = 0; k < kTcChunk; k += STEP) {
+        const bool in = r + k < live;
+        copy16(dst + k * 128, in ? src : g, in);
+        src += STEP * tok;
     }
+}
+__device__ __forceinline__ void tc_meet(int bar, int threads) {
+    asm volatile("bar.sync %0, %1;" ::"r"(bar), "r"(threads) : "memory");
 }
 
 template <int DX, int DZ, bool BWD>
@@ -225,7 +273,8 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_linattn_tc(const AttnArgs a, 
     char* tile_z = tile_y + Shape::kStageY * Shape::kTileX;
     char* tile_s = tile_z + Shape::kStageZ * Shape::kTileZ;
     char* tile_w = tile_s + Shape::kTileS;
-    TcSmall& sm = *reinterpret_cast<TcSmall*>(base + Shape::kTiles);
+    using Small = TcSmall<BWD, Shape::kStageZ>;
+    Small& sm = *reinterpret_cast<Small*>(base + Shape::kTiles);
     uint64_t* bars = sm.bars;
     if (!tma_stage_aligned(base, err) || (smem_addr(base) & 1023)) return;  // every thread alike
 
@@ -240,7 +289,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_linattn_tc(const AttnArgs a, 
     const int z0 = (int)zt * DZ, dz = (int)a.dz - z0 < DZ ? (int)a.dz - z0 : DZ, dx = (int)a.dx;
     const bool reverse = a.reverse, summary = a.summary;
 
-    if (warp == 8) {
+    if (warp == 16) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_addr(&sm.tmem))
                      : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
@@ -248,10 +297,9 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_linattn_tc(const AttnArgs a, 
     if (tid == 0) {
         for (int i = 0; i < TC_BARS; ++i) {
             const bool commit = i == TC_SCORES || i == TC_INTER || i == TC_OUT || i == TC_UPDATE;
-            mbar_init(&bars[i], commit ? 1 : (i == TC_DECAYS ? 32 : (i == TC_FREE ? 256 : 128)));
+            mbar_init(&bars[i], commit ? 1 : (i == TC_DECAYS ? 32 : (i == TC_FREE ? 2 * kTcGroup : kTcGroup)));
         }
         fence_mbar_init();
-        sm.bad_any[0] = sm.bad_any[1] = 0;
     }
     tc_before();
     __syncthreads();
@@ -285,14 +333,16 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_linattn_tc(const AttnArgs a, 
     auto starts_with_state = [&](const TcPart& p) { return begins_at(p) ? a.initial != nullptr : !summary && a.nsegments > 1; };
 
     bool fine = true;
-    if (warp < 4) {
-        // ---- A: a token each thread ----
+    const int quad = warp & 3;  // rows 32 quad .. of tensor memory
+    if (warp < 8) {
+        // ---- A: half a token's columns each thread ----
         const bf16* px = static_cast<const bf16*>(a.x.data) + row * a.x.seq + (head / a.x.share) * a.x.head;
         const bf16* pp = BWD && a.partner.data
                              ? static_cast<const bf16*>(a.partner.data) + row * a.partner.seq +
                                    (head / a.partner.share) * a.partner.head + z0
                              : nullptr;
-        const int r = tid;
+        const int r = tid & 127, side = warp >> 2;
+        constexpr int HALF = DZ / 2;
         auto fetch = [&](int64_t t, int count) {
             tc_load<DX>(tile_x, px + t * a.x.tok, a.x.tok, count, dx, tid);
             copy_commit();
@@ -316,71 +366,77 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_linattn_tc(const AttnArgs a, 
                 tc_after();
                 const float2 G = sm.G[r];
                 const float inter = ex2(reverse ? (sm.all_hi - G.x) + (sm.all_lo - G.y) : G.x) * a.scale_inter;
-                float diagonal = 0.f;
-                // scores of columns c0 .. c0 + 31 weighted, to pieces
-                auto weigh = [&](int c0, const uint32_t (&s)[32]) {
-                    uint32_t out[PO][16];
-                    const bool none = reverse ? c0 + 31 < warp * 32 : c0 > warp * 32 + 31;
+                uint32_t s[2][32];
+                tc_ld32(tmem + lanes + side * 64, s[0]);
+                tc_ld32(tmem + lanes + side * 64 + 32, s[1]);
+                tc_wait_ld(s[0]);
+                tc_wait_ld(s[1]);
+                tc_meet(2 + quad, 64);  // the other half of these rows has been read too
 #pragma unroll
-                    for (int j = 0; j < 16; ++j) {
-                        float v[2] = {0.f, 0.f};
-                        if (!none) {
+                for (int k = 0; k < 4; ++k) {  // 16 columns at a time
+                    const int cb = side * 2 + k / 2, c0 = cb * 32 + (k & 1) * 16;
+                    const uint32_t* sk = s[k / 2] + (k & 1) * 16;
+                    uint32_t out[PO][8];
+                    if (cb == quad) {  // the rows' own block
+                        const float sign = reverse ? -1.f : 1.f;
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) {
                             const float4 g = *reinterpret_cast<const float4*>(&sm.G[c0 + 2 * j]);
                             const float d[2] = {(G.x - g.x) + (G.y - g.y), (G.x - g.z) + (G.y - g.w)};
+                            float v[2];
 #pragma unroll
                             for (int e = 0; e < 2; ++e) {
-                                const int c = c0 + 2 * j + e;
-                                const float w = __uint_as_float(s[2 * j + e]) * (ex2(reverse ? -d[e] : d[e]) * a.scale_pair);
-                                v[e] = (reverse ? c >= r : c <= r) ? w : 0.f;
-                                if (BWD && c == r) diagonal = v[e], v[e] = 0.f;
+                                const int c = (k & 1) * 16 + 2 * j + e;
+                                const float w = __uint_as_float(sk[2 * j + e]) * (ex2(sign * d[e]) * a.scale_pair);
+                                v[e] = (reverse ? c >= lane : c <= lane) ? w : 0.f;
+                                if (BWD && c == lane) sm.diagonal[r] = v[e], v[e] = 0.f;
+                            }
+                            uint32_t q[PO];
+                            tc_split<PO>(make_float2(v[0], v[1]), q);
+#pragma unroll
+                            for (int u = 0; u < PO; ++u) out[u][j] = q[u];
+                        }
+                    } else if (reverse ? cb > quad : cb < quad) {
+                        const float2 e = sm.G[reverse ? cb * 32 - 1 : cb * 32 + 31];
+                        const float d = (G.x - e.x) + (G.y - e.y);
+                        const float2 w = splat(ex2(reverse ? -d : d) * a.scale_pair);
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            const float4 f = *reinterpret_cast<const float4*>(&sm.column[c0 + 4 * j]);
+#pragma unroll
+                            for (int e2 = 0; e2 < 2; ++e2) {
+                                const float2 v = make_float2(__uint_as_float(sk[4 * j + 2 * e2]),
+                                                             __uint_as_float(sk[4 * j + 2 * e2 + 1]));
+                                uint32_t q[PO];
+                                tc_split<PO>(mul2(mul2(v, e2 ? make_float2(f.z, f.w) : make_float2(f.x, f.y)), w), q);
+#pragma unroll
+                                for (int u = 0; u < PO; ++u) out[u][2 * j + e2] = q[u];
                             }
                         }
-                        uint32_t q[PO];
-                        tc_split<PO>(v[0], v[1], q);
+                    } else {
 #pragma unroll
-                        for (int u = 0; u < PO; ++u) out[u][j] = q[u];
+                        for (int u = 0; u < PO; ++u)
+#pragma unroll
+                            for (int j = 0; j < 8; ++j) out[u][j] = 0;
                     }
 #pragma unroll
-                    for (int u = 0; u < PO; ++u) tc_st16(tmem + lanes + u * 64 + c0 / 2, out[u]);
-                };
-                if constexpr (BWD) {
-                    // the second pieces go where the last columns of scores are: those are read first
-                    uint32_t s2[32], s3[32], s[32];
-                    tc_ld32(tmem + lanes + 64, s2);
-                    tc_ld32(tmem + lanes + 96, s3);
-                    tc_ld32(tmem + lanes, s);
-                    tc_wait_ld(s2);
-                    tc_wait_ld(s3);
-                    tc_wait_ld(s);
-                    weigh(0, s);
-                    tc_ld32(tmem + lanes + 32, s);
-                    tc_wait_ld(s);
-                    weigh(32, s);
-                    weigh(64, s2);
-                    weigh(96, s3);
-                } else {
-#pragma unroll 1
-                    for (int c0 = 0; c0 < C; c0 += 32) {
-                        uint32_t s[32];
-                        tc_ld32(tmem + lanes + c0, s);
-                        tc_wait_ld(s);
-                        weigh(c0, s);
-                    }
+                    for (int u = 0; u < PO; ++u) tc_st8(tmem + lanes + u * 64 + c0 / 2, out[u]);
                 }
                 mbar_arrive(&bars[TC_FREE]);
                 const bf16* partner = pp && r < count ? pp + (t + r) * a.partner.tok : nullptr;
-                // partner values of 32 columns, zeros beyond dz
-                auto dot = [&](int c0, const uint32_t (&v)[32], float sum) {
+                // products with the partner's values of 16 columns, zeros beyond dz
+                auto dot = [&](int c0, const uint32_t (&v)[16], float sum) {
                     if (!partner) return sum;
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) {
+                    for (int j = 0; j < 2; ++j) {
                         if (c0 + 8 * j < dz) {
                             const uint4 q = *reinterpret_cast<const uint4*>(partner + c0 + 8 * j);
                             const uint32_t w[4] = {q.x, q.y, q.z, q.w};
 #pragma unroll
                             for (int e = 0; e < 4; ++e) {
-                                sum = fmaf(__uint_as_float(w[e] << 16), __uint_as_float(v[8 * j + 2 * e]), sum);
-                                sum = fmaf(__uint_as_float(w[e] & 0xffff0000u), __uint_as_float(v[8 * j + 2 * e + 1]), sum);
+                                const float2 f = tc_values(w[e]);
+                                sum = fmaf(f.x, __uint_as_float(v[8 * j + 2 * e]), sum);
+                                sum = fmaf(f.y, __uint_as_float(v[8 * j + 2 * e + 1]), sum);
                             }
                         }
                     }
@@ -390,14 +446,14 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_linattn_tc(const AttnArgs a, 
                 if (some) {
                     if (!wait(TC_INTER, n)) return false;
                     tc_after();
-#pragma unroll 1
-                    for (int c0 = 0; c0 < DZ; c0 += 32) {
-                        uint32_t v[32];
-                        tc_ld32(kOut + lanes + c0, v);
-                        tc_wait_ld(v);
+#pragma unroll 2
+                    for (int c0 = side * HALF; c0 < side * HALF + HALF; c0 += 16) {
+                        uint32_t v[16];
+                        tc_ld16(kOut + lanes + c0, v);
+                        tc_wait_ld16(v);
 #pragma unroll
-                        for (int j = 0; j < 32; ++j) v[j] = __float_as_uint(__uint_as_float(v[j]) * inter);
-                        tc_st32(kOut + lanes + c0, v);
+                        for (int j = 0; j < 16; ++j) v[j] = __float_as_uint(__uint_as_float(v[j]) * inter);
+                        tc_st16(kOut + lanes + c0, v);
                         if (BWD) between = dot(c0, v, between);
                     }
                 }
@@ -411,40 +467,42 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_linattn_tc(const AttnArgs a, 
                 tc_after();
                 const int64_t at = row * a.out_seq + (t + r) * a.out_tok + head * a.out_head + z0;
                 const char* sz = tile_z + (Shape::kStageZ == 2 ? half * Shape::kTileZ : 0);
-                const bool bad = sm.bad_any[half];
+                const int bz = Shape::kStageZ == 2 ? half : 0;
+                const bool bad = sm.bad_any[bz];
+                const float diagonal = BWD ? sm.diagonal[r] : 0.f;
                 float all = 0.f;
-#pragma unroll 1
-                for (int c0 = 0; c0 < DZ; c0 += 32) {
-                    uint32_t v[32];
-                    tc_ld32(kOut + lanes + c0, v);
-                    tc_wait_ld(v);
+#pragma unroll 2
+                for (int c0 = side * HALF; c0 < side * HALF + HALF; c0 += 16) {
+                    uint32_t v[16];
+                    tc_ld16(kOut + lanes + c0, v);
+                    tc_wait_ld16(v);
                     if (BWD) {
                         all = dot(c0, v, all);
                         // a token's pair with itself, in float32: it has no part in the decay's gradient
 #pragma unroll
-                        for (int j = 0; j < 4; ++j) {
+                        for (int j = 0; j < 2; ++j) {
                             const int c = c0 / 8 + j;
                             const uint4 q = *reinterpret_cast<const uint4*>(sz + (c >> 3) * PANEL + tc_chunk(r, c & 7));
                             const uint32_t w[4] = {q.x, q.y, q.z, q.w};
 #pragma unroll
                             for (int e = 0; e < 4; ++e) {
-                                float& lo = reinterpret_cast<float&>(v[8 * j + 2 * e]);
-                                float& hi = reinterpret_cast<float&>(v[8 * j + 2 * e + 1]);
-                                lo = fmaf(diagonal, __uint_as_float(w[e] << 16), lo);
-                                hi = fmaf(diagonal, __uint_as_float(w[e] & 0xffff0000u), hi);
+                                const float2 f = tc_values(w[e]);
+                                uint32_t &lo = v[8 * j + 2 * e], &hi = v[8 * j + 2 * e + 1];
+                                lo = __float_as_uint(fmaf(diagonal, f.x, __uint_as_float(lo)));
+                                hi = __float_as_uint(fmaf(diagonal, f.y, __uint_as_float(hi)));
                             }
                         }
                     }
                     if (bad) {  // a value of z that is no number or infinite, by this token
 #pragma unroll
-                        for (int j = 0; j < 32; ++j) {
-                            const int k = sm.bad_at[half][c0 + j];
-                            if (reverse ? r < k : r + 1 >= k) v[j] = 0x7fffffffu;
+                        for (int j = 0; j < 16; ++j) {
+                            const int k0 = sm.bad_at[bz][0][c0 + j], k1 = sm.bad_at[bz][1][c0 + j];
+                            if (reverse ? r < k0 || r < k1 : r + 1 >= k0 || r + 1 >= k1) v[j] = 0x7fffffffu;
                         }
                     }
                     if (r < count) {
 #pragma unroll
-                        for (int j = 0; j < 4; ++j) {
+                        for (int j = 0; j < 2; ++j) {
                             if (c0 + 8 * j >= dz) continue;
                             if (a.out_f32) {
                                 float* o = static_cast<float*>(a.out) + at + c0 + 8 * j;
@@ -463,7 +521,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_linattn_tc(const AttnArgs a, 
                     }
                 }
                 if (partner) {
-                    const int64_t k = (zt * a.heads + head) * (a.rows * a.length) + row * a.length + t + r;
+                    const int64_t k = ((zt * 2 + side) * a.heads + head) * (a.rows * a.length) + row * a.length + t + r;
                     a.dots_inter[k] = between;
                     a.dots_all[k] = all;
                 }
@@ -472,27 +530,31 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_linattn_tc(const AttnArgs a, 
             }
             return true;
         });
-    } else if (warp < 8) {
-        // ---- B: a column of z each thread ----
+    } else if (warp < 16) {
+        // ---- B: half a row of S^T each thread; half the tokens of z^T ----
         const bf16* py = static_cast<const bf16*>(a.y.data) + row * a.y.seq + (head / a.y.share) * a.y.head;
         const bf16* pz = static_cast<const bf16*>(a.z.data) + row * a.z.seq + (head / a.z.share) * a.z.head + z0;
-        const int m = tid - 128;
+        const int id = tid - kTcGroup, m = id & 127, side = id >> 7;
+        constexpr int HALF = DX / 2;
+        const int x0 = side * HALF;
         auto fetch_y = [&](int k, int64_t t, int count) {
-            tc_load<DX>(tile_y + k * Shape::kTileX, py + t * a.y.tok, a.y.tok, count, dx, m);
+            tc_load<DX>(tile_y + k * Shape::kTileX, py + t * a.y.tok, a.y.tok, count, dx, id);
         };
         auto fetch_z = [&](int k, int64_t t, int count) {
-            tc_load<DZ>(tile_z + (Shape::kStageZ == 2 ? k * Shape::kTileZ : 0), pz + t * a.z.tok, a.z.tok, count, dz, m);
+            tc_load<DZ>(tile_z + (Shape::kStageZ == 2 ? k * Shape::kTileZ : 0), pz + t * a.z.tok, a.z.tok, count, dz, id);
         };
-        float S[DX];  // row m of S^T
-        const int64_t carry_at = (((row * a.nsegments + seg) * a.heads + head) * a.ztiles + zt) * (DX * 128) + m * 4;
+        float2 S[HALF / 2];  // row m of S^T, columns x0 ..
+        const int64_t carry_at = (((row * a.nsegments + seg) * a.heads + head) * a.ztiles + zt) * (DX * 128) +
+                                 (side * (HALF / 4) * 128 + m) * 4;
         // S as an operand: row m, columns in panels of 64
         auto put_state = [&] {
             if (m < DZ && !summary) {
 #pragma unroll
-                for (int c = 0; c < DX / 8; ++c) {
+                for (int k = 0; k < HALF / 8; ++k) {
+                    const int c = x0 / 8 + k;
                     uint32_t q[4][PO];
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) tc_split<PO>(S[8 * c + 2 * e], S[8 * c + 2 * e + 1], q[e]);
+                    for (int e = 0; e < 4; ++e) tc_split<PO>(S[4 * k + e], q[e]);
 #pragma unroll
                     for (int u = 0; u < PO; ++u)
                         *reinterpret_cast<uint4*>(tile_s + u * (DZ * DX * 2) + (c >> 3) * (DZ * 128) + tc_chunk(m, c & 7)) =
@@ -503,118 +565,132 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_linattn_tc(const AttnArgs a, 
             tc_before();
             mbar_arrive(&bars[TC_STATE]);
         };
+        // f(value, x) of the values that this thread holds
+        auto each_state = [&](auto f) {
+            if (m < dz) {
+#pragma unroll
+                for (int j = 0; j < HALF / 2; ++j) {
+                    if (x0 + 2 * j < dx) f(S[j].x, x0 + 2 * j);
+                    if (x0 + 2 * j + 1 < dx) f(S[j].y, x0 + 2 * j + 1);
+                }
+            }
+        };
         double gone = 0.0;
         bool from_start = false;
         fine = each_part([&](const TcPart& p, int chunks, uint32_t n0) {
-            const int64_t state_at = (p.seq * a.heads + head) * a.dx * a.dz;
-            const int64_t mine = (z0 + m) * a.state_z;
+            const int64_t mine = (p.seq * a.heads + head) * a.dx * a.dz + (z0 + m) * a.state_z;
             from_start = begins_at(p);
-#pragma unroll
-            for (int j = 0; j < DX; ++j) S[j] = 0.f;
-            if (from_start) {
-                if (a.initial && m < dz) {
-                    const float* q = a.initial + state_at + mine;
-#pragma unroll
-                    for (int j = 0; j < DX; ++j)
-                        if (j < dx) S[j] = q[j * a.state_x];
-                }
-            } else if (!summary && a.nsegments > 1) {
-                const float4* q = reinterpret_cast<const float4*>(a.carry + carry_at);
-#pragma unroll
-                for (int j = 0; j < DX / 4; ++j) {
-                    const float4 v = q[j * 128];
-                    S[4 * j] = v.x, S[4 * j + 1] = v.y, S[4 * j + 2] = v.z, S[4 * j + 3] = v.w;
-                }
-            }
             // the last chunk's products are over (its outputs' too, which read z)
             if (n0 > 0 && !summary && !wait(TC_OUT, n0 - 1)) return false;
             fetch_y(n0 & 1, chunk_at(p, chunks, 0), count_at(p, chunk_at(p, chunks, 0)));
             fetch_z(n0 & 1, chunk_at(p, chunks, 0), count_at(p, chunk_at(p, chunks, 0)));
             copy_commit();
+#pragma unroll
+            for (int j = 0; j < HALF / 2; ++j) S[j] = splat(0.f);
+            if (from_start) {
+                if (a.initial) {
+                    const float* q = a.initial + mine;
+                    each_state([&](float& v, int x) { v = q[x * a.state_x]; });
+                }
+            } else if (!summary && a.nsegments > 1) {
+                const float4* q = reinterpret_cast<const float4*>(a.carry + carry_at);
+#pragma unroll
+                for (int j = 0; j < HALF / 4; ++j) {
+                    const float4 v = q[j * 128];
+                    S[2 * j] = make_float2(v.x, v.y), S[2 * j + 1] = make_float2(v.z, v.w);
+                }
+            }
             put_state();
             for (int i = 0; i < chunks; ++i) {
                 const uint32_t n = n0 + i, half = n & 1;
                 copy_wait<0>();
                 fence_proxy_async_smem();
                 mbar_arrive(&bars[TC_YZ0 + half]);
-                asm volatile("bar.sync 1, 128;" ::: "memory");  // all of z is there
+                const int bz = Shape::kStageZ == 2 ? half : 0;
+                if (id == 0) sm.bad_any[bz] = 0;
+                tc_meet(1, kTcGroup);  // all of z is there
                 const bool next = i + 1 < chunks;
                 const int64_t tn = next ? chunk_at(p, chunks, i + 1) : 0;
-                // the stage of the chunk before is free when its outputs are there (its part of the
-                // state was waited for) and, in the gradients, A has read its rows of z
-                if (i > 0 && !summary && (!wait(TC_OUT, n - 1) || (BWD && !wait(TC_TAKEN, n - 1)))) return false;
-                if (next) {
-                    fetch_y(half ^ 1, tn, count_at(p, tn));
-                    if (Shape::kStageZ == 2) fetch_z(half ^ 1, tn, count_at(p, tn));
-                    copy_commit();
-                }
                 if (!wait(TC_DECAYS, n)) return false;
-                const float total = sm.total;
+                const float2 total = splat(sm.total);
                 if (summary) gone += sm.total_log2;
-                // column m of z, weighted, in three pieces
-                char* sz = tile_z + (Shape::kStageZ == 2 ? half * Shape::kTileZ : 0) + (m >> 6) * PANEL + (m & 7) * 2;
-                float odd = 0.f;
-#pragma unroll 1
-                for (int k = 0; k < C / 16; ++k) {
-                    uint32_t q[3][8];
+                // this warp's 32 columns of z and half of the tokens, weighted, in three pieces
+                char* sz = tile_z + (Shape::kStageZ == 2 ? half * Shape::kTileZ : 0);
+                const uint32_t z_at = smem_addr(sz), w_at = smem_addr(tile_w);
+                float2 odd = splat(0.f);
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) {
-                        float v[2] = {0.f, 0.f};
-                        if (m < DZ) {
+                for (int k = 0; k < 4; ++k) {
+                    const int k0 = side * 64 + k * 16;
+                    const float2 w0 = *reinterpret_cast<const float2*>(&sm.update[k0 + 2 * (lane & 3)]);
+                    const float2 w1 = *reinterpret_cast<const float2*>(&sm.update[k0 + 8 + 2 * (lane & 3)]);
 #pragma unroll
-                            for (int e = 0; e < 2; ++e) {
-                                const int tk = 16 * k + 2 * j + e;
-                                const uint32_t u = *reinterpret_cast<const unsigned short*>(sz + tc_chunk(tk, (m >> 3) & 7));
-                                v[e] = __uint_as_float(u << 16);
-                                odd = fmaf(v[e], 0.f, odd);
-                            }
+                    for (int rb = 0; rb < 2; ++rb) {
+                        const int m0 = quad * 32 + rb * 16;
+                        uint32_t f[4] = {}, q[3][4];
+                        if (m0 < DZ) {
+                            const int tk = k0 + (lane & 7) + (lane >> 4) * 8, c = m0 / 8 + ((lane >> 3) & 1);
+                            tc_ldmatrix_t(z_at + (c >> 3) * PANEL + tc_chunk(tk, c & 7), f);
                         }
-                        const float2 w = *reinterpret_cast<const float2*>(&sm.update[16 * k + 2 * j]);
-                        uint32_t s[3];
-                        tc_split<3>(v[0] * w.x, v[1] * w.y, s);
 #pragma unroll
-                        for (int u = 0; u < 3; ++u) q[u][j] = s[u];
+                        for (int h = 0; h < 4; ++h) {
+                            const float2 v = tc_values(f[h]);
+                            odd = fma2(v, splat(0.f), odd);
+                            uint32_t g[3];
+                            tc_split<3>(mul2(v, h < 2 ? w0 : w1), g);
+#pragma unroll
+                            for (int u = 0; u < 3; ++u) q[u][h] = g[u];
+                        }
+                        const uint32_t to = kWz + lanes + ((uint32_t)(rb * 16) << 16) + k0 / 2;
+                        tc_st_block(to, q[0]);
+                        tc_st_block(to + 64, q[1]);
+                        // rows m0 .. m0 + 15 of the third piece's tile, 16 tokens
+                        const int rw = m0 + (lane & 7) + ((lane >> 3) & 1) * 8, c = (k0 & 63) / 8 + (lane >> 4);
+                        tc_stmatrix(w_at + side * PANEL + tc_chunk(rw, c), q[2]);
                     }
-                    tc_st8(kWz + lanes + 8 * k, q[0]);
-                    tc_st8(kWz + lanes + 64 + 8 * k, q[1]);
-#pragma unroll
-                    for (int c = 0; c < 2; ++c)
-                        *reinterpret_cast<uint4*>(tile_w + (k >> 2) * PANEL + tc_chunk(m, (k & 3) * 2 + c)) =
-                            make_uint4(q[2][4 * c], q[2][4 * c + 1], q[2][4 * c + 2], q[2][4 * c + 3]);
                 }
                 mbar_arrive(&bars[TC_FREE]);
                 if (!summary) {
                     // 0 times what is not finite is not 0: such values leave the tile, and the outputs
                     // that they are in are set by hand
-                    const bool any = __any_sync(0xffffffffu, !(odd == 0.f));
+                    const bool any = __any_sync(0xffffffffu, !(odd.x == 0.f && odd.y == 0.f));
                     int k = reverse ? 0 : 255;
-                    if (!(odd == 0.f)) {
-                        for (int tk = 0; tk < C; ++tk) {
-                            unsigned short* u = reinterpret_cast<unsigned short*>(sz + tc_chunk(tk, (m >> 3) & 7));
+                    if (any && m < DZ) {
+                        for (int tk = side * 64; tk < side * 64 + 64; ++tk) {
+                            unsigned short* u = reinterpret_cast<unsigned short*>(sz + (m >> 6) * PANEL +
+                                                                                 tc_chunk(tk, (m >> 3) & 7) + (m & 7) * 2);
                             if ((*u & 0x7f80) == 0x7f80) {
                                 *u = 0;
                                 if (reverse || k == 255) k = tk + 1;
                             }
                         }
                     }
-                    sm.bad_at[half][m] = (unsigned char)k;
-                    if (lane == 0 && any) atomicOr(&sm.bad_any[half], 1 << (warp & 3));
-                    if (lane == 0 && !any) atomicAnd(&sm.bad_any[half], ~(1 << (warp & 3)));
+                    sm.bad_at[bz][side][m] = (unsigned char)k;
+                    if (lane == 0 && any) atomicOr(&sm.bad_any[bz], 1);
                 }
                 tc_wait_st();
                 fence_proxy_async_smem();
                 tc_before();
                 mbar_arrive(&bars[TC_WZ]);
 
+                // the stage of the chunk before is free when its outputs are there (its part of the
+                // state was waited for) and, in the gradients, A has read its rows of z
+                if (next) {
+                    if (i > 0 && !summary && (!wait(TC_OUT, n - 1) || (BWD && !wait(TC_TAKEN, n - 1)))) return false;
+                    fetch_y(half ^ 1, tn, count_at(p, tn));
+                    if (Shape::kStageZ == 2) fetch_z(half ^ 1, tn, count_at(p, tn));
+                    copy_commit();
+                }
                 if (!wait(TC_UPDATE, n)) return false;
                 tc_after();
 #pragma unroll
-                for (int c0 = 0; c0 < DX; c0 += 32) {
-                    uint32_t v[32];
-                    tc_ld32(kAdd + lanes + c0, v);
-                    tc_wait_ld(v);
+                for (int c0 = 0; c0 < HALF; c0 += 16) {
+                    uint32_t v[16];
+                    tc_ld16(kAdd + lanes + x0 + c0, v);
+                    tc_wait_ld16(v);
 #pragma unroll
-                    for (int j = 0; j < 32; ++j) S[c0 + j] = fmaf(total, S[c0 + j], __uint_as_float(v[j]));
+                    for (int j = 0; j < 8; ++j)
+                        S[c0 / 2 + j] = fma2(total, S[c0 / 2 + j],
+                                             make_float2(__uint_as_float(v[2 * j]), __uint_as_float(v[2 * j + 1])));
                 }
                 if (next) {
                     put_state();
@@ -626,26 +702,24 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_linattn_tc(const AttnArgs a, 
                 }
             }
             if (!summary && (reverse ? p.first : p.last)) {
-                if (a.final_state && m < dz) {
-                    float* q = a.final_state + state_at + mine;
-#pragma unroll
-                    for (int j = 0; j < DX; ++j)
-                        if (j < dx) q[j * a.state_x] = S[j];
+                if (a.final_state) {
+                    float* q = a.final_state + mine;
+                    each_state([&](float& v, int x) { q[x * a.state_x] = v; });
                 }
                 if (BWD && a.final_dot) {
-                    const float* q = a.final_dot + state_at + mine;
+                    const float* q = a.final_dot + mine;
                     float sum = 0.f;
-#pragma unroll
-                    for (int j = 0; j < DX; ++j)
-                        if (j < dx && m < dz) sum = fmaf(S[j], q[j * a.state_x], sum);
+                    each_state([&](float& v, int x) { sum = fmaf(v, q[x * a.state_x], sum); });
 #pragma unroll
                     for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-                    if (lane == 0) sm.warp_sums[warp - 4] = sum;
-                    asm volatile("bar.sync 1, 128;" ::: "memory");
-                    if (m == 0)
-                        a.final_dots[(zt * a.nseq + p.seq) * a.heads + head] =
-                            (sm.warp_sums[0] + sm.warp_sums[1]) + (sm.warp_sums[2] + sm.warp_sums[3]);
-                    asm volatile("bar.sync 1, 128;" ::: "memory");
+                    if (lane == 0) sm.warp_sums[warp - 8] = sum;
+                    tc_meet(1, kTcGroup);
+                    if (id == 0) {
+                        sum = 0.f;
+                        for (int w = 0; w < 8; ++w) sum += sm.warp_sums[w];
+                        a.final_dots[(zt * a.nseq + p.seq) * a.heads + head] = sum;
+                    }
+                    tc_meet(1, kTcGroup);
                 }
             }
             // A reads z for the last outputs until it has taken them
@@ -656,14 +730,14 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_linattn_tc(const AttnArgs a, 
         if (summary && fine) {
             float4* q = reinterpret_cast<float4*>(a.carry + carry_at);
 #pragma unroll
-            for (int j = 0; j < DX / 4; ++j) q[j * 128] = make_float4(S[4 * j], S[4 * j + 1], S[4 * j + 2], S[4 * j + 3]);
-            if (zt == 0 && m == 0) {
+            for (int j = 0; j < HALF / 4; ++j) q[j * 128] = make_float4(S[2 * j].x, S[2 * j].y, S[2 * j + 1].x, S[2 * j + 1].y);
+            if (zt == 0 && id == 0) {
                 const int64_t i = (row * a.nsegments + seg) * a.heads + head;
                 a.carry_decay[i] = (float)gone;
                 a.carry_reset[i] = from_start;
             }
         }
-    } else if (warp == 8) {
+    } else if (warp == 16) {
         // ---- the products, issued by one thread ----
         const uint32_t x = smem_addr(tile_x), y = smem_addr(tile_y), z = smem_addr(tile_z), s = smem_addr(tile_s),
                        w = smem_addr(tile_w);
@@ -730,7 +804,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_linattn_tc(const AttnArgs a, 
             }
             return __all_sync(0xffffffffu, good) != 0;
         });
-    } else {
+    } else if (warp == 17) {
         // ---- decays: four tokens per lane ----
         const bf16* pg = static_cast<const bf16*>(a.decay.data) + row * a.decay.seq_stride + head;
         fine = each_part([&](const TcPart& p, int chunks, uint32_t n0) {
@@ -756,6 +830,9 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_linattn_tc(const AttnArgs a, 
                     const TcTwo v = {__shfl_up_sync(0xffffffffu, sum.hi, o), __shfl_up_sync(0xffffffffu, sum.lo, o)};
                     if (lane >= o) sum = tc_add(v, sum);
                 }
+                // factors of columns: to the end of their block of 32 tokens, or (reversed) from its start
+                const int edge = reverse ? (lane & ~7) - 1 : lane | 7;
+                const TcTwo end = {__shfl_sync(0xffffffffu, sum.hi, edge & 31), __shfl_sync(0xffffffffu, sum.lo, edge & 31)};
                 const TcTwo all = {__shfl_sync(0xffffffffu, sum.hi, 31), __shfl_sync(0xffffffffu, sum.lo, 31)};
                 TcTwo before = {__shfl_up_sync(0xffffffffu, sum.hi, 1), __shfl_up_sync(0xffffffffu, sum.lo, 1)};
                 if (lane == 0) before = {0.f, 0.f};
@@ -764,6 +841,8 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_linattn_tc(const AttnArgs a, 
                 for (int k = 0; k < 4; ++k) {
                     const TcTwo G = tc_add(before, d[k]);
                     sm.G[4 * lane + k] = make_float2(G.hi, G.lo);
+                    const float to_end = (end.hi - G.hi) + (end.lo - G.lo);
+                    sm.column[4 * lane + k] = edge < 0 ? 0.f : ex2(reverse ? -to_end : to_end);
                     sm.update[4 * lane + k] = ex2(reverse ? G.hi : (all.hi - G.hi) + (all.lo - G.lo)) * a.scale_update;
                 }
                 if (lane == 0) sm.total = ex2(all.hi), sm.total_log2 = sm.all_hi = all.hi, sm.all_lo = all.lo;
@@ -776,7 +855,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_linattn_tc(const AttnArgs a, 
     if (!fine && lane == 0) atomicCAS(err, 0, KERR_WAIT_TIMEOUT);
     tc_before();
     __syncthreads();
-    if (warp == 8) {
+    if (warp == 16) {
         tc_after();
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
     }
@@ -791,7 +870,7 @@ cudaError_t launch_attn_tc(const AttnArgs& args, int* err, cudaStream_t s) {
     LaunchGeom g;
     cudaError_t e = cache.get(
         [](int dev, LaunchGeom* out) {
-            return setup_persistent(k_linattn_tc<DX, DZ, BWD>, kTcThreads, kTcBytes<Shape>, dev, out);
+            return setup_persistent(k_linattn_tc<DX, DZ, BWD>, kTcThreads, tc_bytes<DX, DZ, BWD>(), dev, out);
         },
         &g);
     if (e != cudaSuccess) return e;
@@ -800,13 +879,13 @@ cudaError_t launch_attn_tc(const AttnArgs& args, int* err, cudaStream_t s) {
     if (blocks > INT32_MAX) return cudaErrorInvalidValue;
     if (a.nsegments > 1) {
         a.summary = 1;
-        k_linattn_tc<DX, DZ, BWD><<<(unsigned)blocks, kTcThreads, kTcBytes<Shape>, s>>>(a, err);
+        k_linattn_tc<DX, DZ, BWD><<<(unsigned)blocks, kTcThreads, tc_bytes<DX, DZ, BWD>(), s>>>(a, err);
         e = cudaGetLastError();
         if (e == cudaSuccess) e = attn_carry_pass(a, a.ztiles * (DX * 128 / 4), s);
         if (e != cudaSuccess) return e;
         a.summary = 0;
     }
-    k_linattn_tc<DX, DZ, BWD><<<(unsigned)blocks, kTcThreads, kTcBytes<Shape>, s>>>(a, err);
+    k_linattn_tc<DX, DZ, BWD><<<(unsigned)blocks, kTcThreads, tc_bytes<DX, DZ, BWD>(), s>>>(a, err);
     return cudaGetLastError();
 }
 
