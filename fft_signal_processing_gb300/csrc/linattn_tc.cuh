@@ -13,9 +13,11 @@
 // The state itself is float32 in the registers of the warps that own the rows of S^T: what a chunk
 // adds is summed by itself and then added, since the units cut their sums off where float32
 // additions round.  One block per SM, twenty warps, two for every 32 rows of tensor memory:
-//   A (eight warps, half a token's columns each thread): rows of x, weights of the scores, outputs
-//   B (eight warps, half a row of S^T each thread): rows of y and z, weighted z^T, the state
-//   one warp issues the products, one sums the decays (and two fill up the last group of four).
+//   A (eight warps, half a token's columns each thread): weights of the scores, outputs
+//   B (eight warps, half a row of S^T each thread): weighted z^T, the state
+//   one warp each issues the products, sums the decays, copies rows of y and z, copies rows of x:
+//   a fence before the units read shared memory waits for the thread's copies under way, so those
+//   that copy do nothing else.
 // A weight exp(G[r] - G[c]) of another block of 32 columns than the row's own is a product of one
 // factor for each row and one for each column, both from the end of the columns' block (at most 1).
 // They meet at mbarriers, each of which completes once per chunk (twice-buffered ones every other
@@ -183,7 +185,7 @@ struct TcShape {
     static constexpr int kTiles = kTileX + kStageY * kTileX + kStageZ * kTileZ + kTileS + kTileW;
 };
 
-enum { TC_X, TC_YZ0, TC_YZ1, TC_SCORES, TC_INTER, TC_OUT, TC_UPDATE, TC_WEIGHTED, TC_STATE, TC_WZ, TC_TAKEN, TC_DECAYS,
+enum { TC_X, TC_YZ0, TC_YZ1, TC_SCORES, TC_INTER, TC_OUT, TC_UPDATE, TC_WEIGHTED, TC_STATE, TC_WZ, TC_TAKEN0, TC_TAKEN1, TC_DECAYS,
        TC_FREE, TC_BARS };
 
 // Behind the tiles.  BUFFERS: stages of z.
@@ -196,8 +198,8 @@ struct TcSmall {
     uint64_t bars[TC_BARS];
     // of every column of z, by halves of the tokens, the place of a value that is not finite, plus 1:
     // the first one, 255 for none; reversed the last one, 0 for none.  Set where bad_any is.
-    unsigned char bad_at[BUFFERS][2][kTcChunk];
-    int bad_any[BUFFERS];
+    alignas(8) unsigned char bad_at[BUFFERS][2][kTcChunk];
+    unsigned char bad_any[BUFFERS][8];  // by warps
     float diagonal[BWD ? kTcChunk : 1];  // weighted scores of tokens with themselves
     float warp_sums[8];
     uint32_t tmem;
@@ -242,22 +244,38 @@ __device__ __forceinline__ TcPart tc_part(const AttnArgs& a, int64_t row, int64_
     return p;
 }
 
-// Copies rows of up to D values into a swizzled tile, zeros beyond count and dim.  A thread's rows
-// are a multiple of 8 apart, so the swizzle is the same for all of them.
+// Copies rows of up to D values into a swizzled tile, zeros beyond count and dim: one warp.
 template <int D>
-__device__ __forceinline__ void tc_load(char* tile, const bf16* g, int64_t tok, int count, int dim, int tid) {
-    constexpr int N = D / 8, STEP = kTcGroup / N;
-    static_assert(STEP % 8 == 0, "rows of a thread");
-    const int c = tid % N, r = tid / N;
+__device__ __forceinline__ void tc_load(char* tile, const bf16* g, int64_t tok, int count, int dim, int lane) {
+    constexpr int N = D / 8, STEP = 32 / N;  // 16-byte pieces of a row; rows that the warp takes at once
+    static_assert(8 % STEP == 0, "rows of a lane");
+    const int c = lane % N, r = lane / N;
     const bf16* src = g + r * tok + c * 8;
-    char* dst = tile + (c >> 3) * (kTcChunk * 128) + tc_chunk(r, c & 7);
-    const int live = c * 8 < dim ? count : 0;
-#pragma unroll
+    char* dst = tile + (c >> 3) * (kTcChunk * 128) + r * 128;
+    const int live = c * 8 < dim ? count : 0, swizzled = (c & 7) ^ r;
+#pragma unroll 8
     for (int k = 0; k < kTcChunk; k += STEP) {
         const bool in = r + k < live;
-        copy16(dst + k * 128, in ? src : g, in);
+        copy16(dst + k * 128 + ((swizzled ^ (k & 7)) << 4), in ? src : g, in);
         src += STEP * tok;
     }
+}
+// Pieces of 16 bytes change places within four lanes: piece j of lane i becomes piece i of lane j.
+__device__ __forceinline__ void tc_transpose(uint4 (&p)[4], int lane) {
+    auto swap = [&](uint4& lo, uint4& hi, int bit) {
+        const bool up = lane & bit;
+        uint4 v = up ? lo : hi;
+        v.x = __shfl_xor_sync(0xffffffffu, v.x, bit);
+        v.y = __shfl_xor_sync(0xffffffffu, v.y, bit);
+        v.z = __shfl_xor_sync(0xffffffffu, v.z, bit);
+        v.w = __shfl_xor_sync(0xffffffffu, v.w, bit);
+        if (up) lo = v;
+        else hi = v;
+    };
+    swap(p[0], p[2], 2);
+    swap(p[1], p[3], 2);
+    swap(p[0], p[1], 1);
+    swap(p[2], p[3], 1);
 }
 __device__ __forceinline__ void tc_meet(int bar, int threads) {
     asm volatile("bar.sync %0, %1;" ::"r"(bar), "r"(threads) : "memory");
@@ -297,7 +315,8 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_linattn_tc(const AttnArgs a, 
     if (tid == 0) {
         for (int i = 0; i < TC_BARS; ++i) {
             const bool commit = i == TC_SCORES || i == TC_INTER || i == TC_OUT || i == TC_UPDATE;
-            mbar_init(&bars[i], commit ? 1 : (i == TC_DECAYS ? 32 : (i == TC_FREE ? 2 * kTcGroup : kTcGroup)));
+            const bool warps = i == TC_DECAYS || i == TC_X || i == TC_YZ0 || i == TC_YZ1;
+            mbar_init(&bars[i], commit ? 1 : (warps ? 32 : (i == TC_FREE ? 2 * kTcGroup : kTcGroup)));
         }
         fence_mbar_init();
     }
@@ -336,19 +355,13 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_linattn_tc(const AttnArgs a, 
     const int quad = warp & 3;  // rows 32 quad .. of tensor memory
     if (warp < 8) {
         // ---- A: half a token's columns each thread ----
-        const bf16* px = static_cast<const bf16*>(a.x.data) + row * a.x.seq + (head / a.x.share) * a.x.head;
         const bf16* pp = BWD && a.partner.data
                              ? static_cast<const bf16*>(a.partner.data) + row * a.partner.seq +
                                    (head / a.partner.share) * a.partner.head + z0
                              : nullptr;
         const int r = tid & 127, side = warp >> 2;
         constexpr int HALF = DZ / 2;
-        auto fetch = [&](int64_t t, int count) {
-            tc_load<DX>(tile_x, px + t * a.x.tok, a.x.tok, count, dx, tid);
-            copy_commit();
-        };
         fine = each_part([&](const TcPart& p, int chunks, uint32_t n0) {
-            if (!summary) fetch(chunk_at(p, chunks, 0), count_at(p, chunk_at(p, chunks, 0)));
             for (int i = 0; i < chunks; ++i) {
                 const uint32_t n = n0 + i, half = n & 1;
                 const int64_t t = chunk_at(p, chunks, i);
@@ -359,9 +372,6 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_linattn_tc(const AttnArgs a, 
                     mbar_arrive(&bars[TC_FREE]);
                     continue;
                 }
-                copy_wait<0>();
-                fence_proxy_async_smem();
-                mbar_arrive(&bars[TC_X]);
                 if (!wait(TC_DECAYS, n) || !wait(TC_SCORES, n)) return false;
                 tc_after();
                 const float2 G = sm.G[r];
@@ -423,21 +433,28 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_linattn_tc(const AttnArgs a, 
                     for (int u = 0; u < PO; ++u) tc_st8(tmem + lanes + u * 64 + c0 / 2, out[u]);
                 }
                 mbar_arrive(&bars[TC_FREE]);
-                const bf16* partner = pp && r < count ? pp + (t + r) * a.partner.tok : nullptr;
-                // products with the partner's values of 16 columns, zeros beyond dz
-                auto dot = [&](int c0, const uint32_t (&v)[16], float sum) {
-                    if (!partner) return sum;
+                // Rows go to and from memory in 64 bytes by four lanes; a lane's own row is among theirs.
+                const int r4 = r & ~3;
+                // products with the partner's values of 32 columns, zeros beyond dz
+                auto dot = [&](int c0, const uint32_t (&v)[32], float sum) {
+                    if (!pp) return sum;
+                    uint4 q[4];
 #pragma unroll
-                    for (int j = 0; j < 2; ++j) {
-                        if (c0 + 8 * j < dz) {
-                            const uint4 q = *reinterpret_cast<const uint4*>(partner + c0 + 8 * j);
-                            const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+                    for (int k = 0; k < 4; ++k) {
+                        const int c = c0 + 8 * (lane & 3);
+                        q[k] = make_uint4(0, 0, 0, 0);
+                        if (r4 + k < count && c < dz)
+                            q[k] = *reinterpret_cast<const uint4*>(pp + (t + r4 + k) * a.partner.tok + c);
+                    }
+                    tc_transpose(q, lane);
 #pragma unroll
-                            for (int e = 0; e < 4; ++e) {
-                                const float2 f = tc_values(w[e]);
-                                sum = fmaf(f.x, __uint_as_float(v[8 * j + 2 * e]), sum);
-                                sum = fmaf(f.y, __uint_as_float(v[8 * j + 2 * e + 1]), sum);
-                            }
+                    for (int k = 0; k < 4; ++k) {
+                        const uint32_t w[4] = {q[k].x, q[k].y, q[k].z, q[k].w};
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const float2 f = tc_values(w[e]);
+                            sum = fmaf(f.x, __uint_as_float(v[8 * k + 2 * e]), sum);
+                            sum = fmaf(f.y, __uint_as_float(v[8 * k + 2 * e + 1]), sum);
                         }
                     }
                     return sum;
@@ -446,41 +463,38 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_linattn_tc(const AttnArgs a, 
                 if (some) {
                     if (!wait(TC_INTER, n)) return false;
                     tc_after();
-#pragma unroll 2
-                    for (int c0 = side * HALF; c0 < side * HALF + HALF; c0 += 16) {
-                        uint32_t v[16];
-                        tc_ld16(kOut + lanes + c0, v);
-                        tc_wait_ld16(v);
+#pragma unroll 1
+                    for (int c0 = side * HALF; c0 < side * HALF + HALF; c0 += 32) {
+                        uint32_t v[32];
+                        tc_ld32(kOut + lanes + c0, v);
+                        tc_wait_ld(v);
 #pragma unroll
-                        for (int j = 0; j < 16; ++j) v[j] = __float_as_uint(__uint_as_float(v[j]) * inter);
-                        tc_st16(kOut + lanes + c0, v);
+                        for (int j = 0; j < 32; ++j) v[j] = __float_as_uint(__uint_as_float(v[j]) * inter);
+                        tc_st32(kOut + lanes + c0, v);
                         if (BWD) between = dot(c0, v, between);
                     }
                 }
                 tc_wait_st();
                 tc_before();
                 mbar_arrive(&bars[TC_WEIGHTED]);
-                // the products with x are over: scores, and (waited for above) those with the state
-                if (i + 1 < chunks) fetch(chunk_at(p, chunks, i + 1), count_at(p, chunk_at(p, chunks, i + 1)));
                 // B has looked at z by the time that the outputs are there
                 if (!wait(TC_OUT, n)) return false;
                 tc_after();
-                const int64_t at = row * a.out_seq + (t + r) * a.out_tok + head * a.out_head + z0;
                 const char* sz = tile_z + (Shape::kStageZ == 2 ? half * Shape::kTileZ : 0);
                 const int bz = Shape::kStageZ == 2 ? half : 0;
-                const bool bad = sm.bad_any[bz];
+                const bool bad = *reinterpret_cast<const uint64_t*>(sm.bad_any[bz]) != 0;
                 const float diagonal = BWD ? sm.diagonal[r] : 0.f;
                 float all = 0.f;
-#pragma unroll 2
-                for (int c0 = side * HALF; c0 < side * HALF + HALF; c0 += 16) {
-                    uint32_t v[16];
-                    tc_ld16(kOut + lanes + c0, v);
-                    tc_wait_ld16(v);
+#pragma unroll 1
+                for (int c0 = side * HALF; c0 < side * HALF + HALF; c0 += 32) {
+                    uint32_t v[32];
+                    tc_ld32(kOut + lanes + c0, v);
+                    tc_wait_ld(v);
                     if (BWD) {
                         all = dot(c0, v, all);
                         // a token's pair with itself, in float32: it has no part in the decay's gradient
 #pragma unroll
-                        for (int j = 0; j < 2; ++j) {
+                        for (int j = 0; j < 4; ++j) {
                             const int c = c0 / 8 + j;
                             const uint4 q = *reinterpret_cast<const uint4*>(sz + (c >> 3) * PANEL + tc_chunk(r, c & 7));
                             const uint32_t w[4] = {q.x, q.y, q.z, q.w};
@@ -495,54 +509,59 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_linattn_tc(const AttnArgs a, 
                     }
                     if (bad) {  // a value of z that is no number or infinite, by this token
 #pragma unroll
-                        for (int j = 0; j < 16; ++j) {
+                        for (int j = 0; j < 32; ++j) {
                             const int k0 = sm.bad_at[bz][0][c0 + j], k1 = sm.bad_at[bz][1][c0 + j];
                             if (reverse ? r < k0 || r < k1 : r + 1 >= k0 || r + 1 >= k1) v[j] = 0x7fffffffu;
                         }
                     }
-                    if (r < count) {
+                    const int64_t at = row * a.out_seq + (t + r4) * a.out_tok + head * a.out_head + z0;
+                    if (a.out_f32) {
 #pragma unroll
-                        for (int j = 0; j < 2; ++j) {
-                            if (c0 + 8 * j >= dz) continue;
-                            if (a.out_f32) {
-                                float* o = static_cast<float*>(a.out) + at + c0 + 8 * j;
-                                *reinterpret_cast<uint4*>(o) = make_uint4(v[8 * j], v[8 * j + 1], v[8 * j + 2], v[8 * j + 3]);
-                                *reinterpret_cast<uint4*>(o + 4) =
-                                    make_uint4(v[8 * j + 4], v[8 * j + 5], v[8 * j + 6], v[8 * j + 7]);
-                            } else {
-                                uint32_t q[4];
+                        for (int h = 0; h < 2; ++h) {
+                            uint4 q[4];
 #pragma unroll
-                                for (int e = 0; e < 4; ++e)
-                                    q[e] = tc_pack(__uint_as_float(v[8 * j + 2 * e]), __uint_as_float(v[8 * j + 2 * e + 1]));
-                                *reinterpret_cast<uint4*>(static_cast<bf16*>(a.out) + at + c0 + 8 * j) =
-                                    make_uint4(q[0], q[1], q[2], q[3]);
-                            }
+                            for (int k = 0; k < 4; ++k)
+                                q[k] = make_uint4(v[16 * h + 4 * k], v[16 * h + 4 * k + 1], v[16 * h + 4 * k + 2], v[16 * h + 4 * k + 3]);
+                            tc_transpose(q, lane);
+                            const int c = c0 + 16 * h + 4 * (lane & 3);
+#pragma unroll
+                            for (int k = 0; k < 4; ++k)
+                                if (r4 + k < count && c < dz)
+                                    *reinterpret_cast<uint4*>(static_cast<float*>(a.out) + at + k * a.out_tok + c) = q[k];
                         }
+                    } else {
+                        uint4 q[4];
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            uint32_t w[4];
+#pragma unroll
+                            for (int e = 0; e < 4; ++e)
+                                w[e] = tc_pack(__uint_as_float(v[8 * k + 2 * e]), __uint_as_float(v[8 * k + 2 * e + 1]));
+                            q[k] = make_uint4(w[0], w[1], w[2], w[3]);
+                        }
+                        tc_transpose(q, lane);
+                        const int c = c0 + 8 * (lane & 3);
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+                            if (r4 + k < count && c < dz)
+                                *reinterpret_cast<uint4*>(static_cast<bf16*>(a.out) + at + k * a.out_tok + c) = q[k];
                     }
                 }
-                if (partner) {
+                if (pp && r < count) {
                     const int64_t k = ((zt * 2 + side) * a.heads + head) * (a.rows * a.length) + row * a.length + t + r;
                     a.dots_inter[k] = between;
                     a.dots_all[k] = all;
                 }
                 tc_before();
-                mbar_arrive(&bars[TC_TAKEN]);
+                mbar_arrive(&bars[TC_TAKEN0 + half]);
             }
             return true;
         });
     } else if (warp < 16) {
         // ---- B: half a row of S^T each thread; half the tokens of z^T ----
-        const bf16* py = static_cast<const bf16*>(a.y.data) + row * a.y.seq + (head / a.y.share) * a.y.head;
-        const bf16* pz = static_cast<const bf16*>(a.z.data) + row * a.z.seq + (head / a.z.share) * a.z.head + z0;
         const int id = tid - kTcGroup, m = id & 127, side = id >> 7;
         constexpr int HALF = DX / 2;
         const int x0 = side * HALF;
-        auto fetch_y = [&](int k, int64_t t, int count) {
-            tc_load<DX>(tile_y + k * Shape::kTileX, py + t * a.y.tok, a.y.tok, count, dx, id);
-        };
-        auto fetch_z = [&](int k, int64_t t, int count) {
-            tc_load<DZ>(tile_z + (Shape::kStageZ == 2 ? k * Shape::kTileZ : 0), pz + t * a.z.tok, a.z.tok, count, dz, id);
-        };
         float2 S[HALF / 2];  // row m of S^T, columns x0 ..
         const int64_t carry_at = (((row * a.nsegments + seg) * a.heads + head) * a.ztiles + zt) * (DX * 128) +
                                  (side * (HALF / 4) * 128 + m) * 4;
@@ -580,11 +599,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_linattn_tc(const AttnArgs a, 
         fine = each_part([&](const TcPart& p, int chunks, uint32_t n0) {
             const int64_t mine = (p.seq * a.heads + head) * a.dx * a.dz + (z0 + m) * a.state_z;
             from_start = begins_at(p);
-            // the last chunk's products are over (its outputs' too, which read z)
-            if (n0 > 0 && !summary && !wait(TC_OUT, n0 - 1)) return false;
-            fetch_y(n0 & 1, chunk_at(p, chunks, 0), count_at(p, chunk_at(p, chunks, 0)));
-            fetch_z(n0 & 1, chunk_at(p, chunks, 0), count_at(p, chunk_at(p, chunks, 0)));
-            copy_commit();
+            // the last chunk's products are over, those with the state among them
 #pragma unroll
             for (int j = 0; j < HALF / 2; ++j) S[j] = splat(0.f);
             if (from_start) {
@@ -603,15 +618,8 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_linattn_tc(const AttnArgs a, 
             put_state();
             for (int i = 0; i < chunks; ++i) {
                 const uint32_t n = n0 + i, half = n & 1;
-                copy_wait<0>();
-                fence_proxy_async_smem();
-                mbar_arrive(&bars[TC_YZ0 + half]);
-                const int bz = Shape::kStageZ == 2 ? half : 0;
-                if (id == 0) sm.bad_any[bz] = 0;
-                tc_meet(1, kTcGroup);  // all of z is there
                 const bool next = i + 1 < chunks;
-                const int64_t tn = next ? chunk_at(p, chunks, i + 1) : 0;
-                if (!wait(TC_DECAYS, n)) return false;
+                if (!wait(TC_YZ0 + half, n >> 1) || !wait(TC_DECAYS, n)) return false;
                 const float2 total = splat(sm.total);
                 if (summary) gone += sm.total_log2;
                 // this warp's 32 columns of z and half of the tokens, weighted, in three pieces
@@ -664,22 +672,15 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_linattn_tc(const AttnArgs a, 
                             }
                         }
                     }
+                    const int bz = Shape::kStageZ == 2 ? half : 0;
                     sm.bad_at[bz][side][m] = (unsigned char)k;
-                    if (lane == 0 && any) atomicOr(&sm.bad_any[bz], 1);
+                    if (lane == 0) sm.bad_any[bz][warp - 8] = any;
                 }
                 tc_wait_st();
                 fence_proxy_async_smem();
                 tc_before();
                 mbar_arrive(&bars[TC_WZ]);
 
-                // the stage of the chunk before is free when its outputs are there (its part of the
-                // state was waited for) and, in the gradients, A has read its rows of z
-                if (next) {
-                    if (i > 0 && !summary && (!wait(TC_OUT, n - 1) || (BWD && !wait(TC_TAKEN, n - 1)))) return false;
-                    fetch_y(half ^ 1, tn, count_at(p, tn));
-                    if (Shape::kStageZ == 2) fetch_z(half ^ 1, tn, count_at(p, tn));
-                    copy_commit();
-                }
                 if (!wait(TC_UPDATE, n)) return false;
                 tc_after();
 #pragma unroll
@@ -692,14 +693,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_linattn_tc(const AttnArgs a, 
                         S[c0 / 2 + j] = fma2(total, S[c0 / 2 + j],
                                              make_float2(__uint_as_float(v[2 * j]), __uint_as_float(v[2 * j + 1])));
                 }
-                if (next) {
-                    put_state();
-                    if (Shape::kStageZ == 1) {
-                        if (!summary && (!wait(TC_OUT, n) || (BWD && !wait(TC_TAKEN, n)))) return false;
-                        fetch_z(0, tn, count_at(p, tn));
-                        copy_commit();
-                    }
-                }
+                if (next) put_state();
             }
             if (!summary && (reverse ? p.first : p.last)) {
                 if (a.final_state) {
@@ -722,11 +716,8 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_linattn_tc(const AttnArgs a, 
                     tc_meet(1, kTcGroup);
                 }
             }
-            // A reads z for the last outputs until it has taken them
-            if (BWD && !summary && !wait(TC_TAKEN, n0 + chunks - 1)) return false;
             return true;
         });
-        copy_wait<0>();
         if (summary && fine) {
             float4* q = reinterpret_cast<float4*>(a.carry + carry_at);
 #pragma unroll
@@ -761,7 +752,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_linattn_tc(const AttnArgs a, 
                                    tc_desc(yn + (k >> 2) * PANEL + (k & 3) * 32, 16), tc_idesc(C, false), k > 0);
                         tc_commit(&bars[TC_SCORES]);
                     }
-                    good = wait(TC_STATE, n) && (summary || n == 0 || wait(TC_TAKEN, n - 1));
+                    good = wait(TC_STATE, n) && (summary || n == 0 || wait(TC_TAKEN0 + (half ^ 1), (n - 1) >> 1));
                     if (!good) break;
                     tc_after();
                     if (!summary) {
@@ -776,9 +767,19 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_linattn_tc(const AttnArgs a, 
                         }
                         tc_commit(&bars[TC_INTER]);  // once per chunk, whether there was a state or not
                     }
-                    good = wait(TC_WZ, n);
+                    // outputs before the state: A works on them meanwhile
+                    good = wait(TC_WZ, n) && (summary || wait(TC_WEIGHTED, n));
                     if (!good) break;
                     tc_after();
+                    if (!summary) {
+#pragma unroll
+                        for (int u = PO - 1; u >= 0; --u)
+#pragma unroll
+                            for (int k = 0; k < C / 16; ++k)
+                                tc_mma_ts(kOut, tmem + u * 64 + k * 8, tc_desc(zn + k * 2048, PANEL), tc_idesc(DZ, true),
+                                          some || u < PO - 1 || k > 0);
+                        tc_commit(&bars[TC_OUT]);
+                    }
 #pragma unroll
                     for (int k = 0; k < C / 16; ++k)
                         tc_mma(kAdd, tc_desc(w + (k >> 2) * PANEL + (k & 3) * 32, 16),
@@ -789,17 +790,6 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_linattn_tc(const AttnArgs a, 
                         for (int k = 0; k < C / 16; ++k)
                             tc_mma_ts(kAdd, kWz + u * 64 + k * 8, tc_desc(yn + k * 2048, PANEL), tc_idesc(DX, true), true);
                     tc_commit(&bars[TC_UPDATE]);
-                    if (summary) continue;
-                    good = wait(TC_WEIGHTED, n);
-                    if (!good) break;
-                    tc_after();
-#pragma unroll
-                    for (int u = PO - 1; u >= 0; --u)
-#pragma unroll
-                        for (int k = 0; k < C / 16; ++k)
-                            tc_mma_ts(kOut, tmem + u * 64 + k * 8, tc_desc(zn + k * 2048, PANEL), tc_idesc(DZ, true),
-                                      some || u < PO - 1 || k > 0);
-                    tc_commit(&bars[TC_OUT]);
                 }
             }
             return __all_sync(0xffffffffu, good) != 0;
@@ -850,6 +840,55 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_linattn_tc(const AttnArgs a, 
             }
             return true;
         });
+    }
+    else if (warp == 18) {
+        // ---- rows of y and z ----
+        const bf16* py = static_cast<const bf16*>(a.y.data) + row * a.y.seq + (head / a.y.share) * a.y.head;
+        const bf16* pz = static_cast<const bf16*>(a.z.data) + row * a.z.seq + (head / a.z.share) * a.z.head + z0;
+        fine = each_part([&](const TcPart& p, int chunks, uint32_t n0) {
+            for (int i = 0; i < chunks; ++i) {
+                const uint32_t n = n0 + i, half = n & 1;
+                const int64_t t = chunk_at(p, chunks, i);
+                const int count = count_at(p, t);
+                // y's stage is free: the chunk before the last had been waited for below
+                tc_load<DX>(tile_y + half * Shape::kTileX, py + t * a.y.tok, a.y.tok, count, dx, lane);
+                // z's, once A has taken the outputs of the chunk that was there (in the gradients it
+                // reads z for them; else their product is over, which is waited for below as well)
+                if (Shape::kStageZ == 1) {
+                    if (n > 0 && !summary && !wait(TC_TAKEN0 + (half ^ 1), (n - 1) >> 1)) return false;
+                } else if (BWD) {
+                    if (n > 1 && !summary && !wait(TC_TAKEN0 + half, (n - 2) >> 1)) return false;
+                }
+                if (Shape::kStageZ == 1 && summary && n > 0 && !wait(TC_UPDATE, n - 1)) return false;
+                tc_load<DZ>(tile_z + (Shape::kStageZ == 2 ? half * Shape::kTileZ : 0), pz + t * a.z.tok, a.z.tok, count, dz,
+                            lane);
+                copy_commit();
+                copy_wait<0>();
+                fence_proxy_async_smem();
+                // The products of the chunk before are over, so the next one's rows may follow; told of
+                // only then, the barrier cannot be a phase ahead of this wait.
+                if (n > 0 && !wait(TC_UPDATE, n - 1)) return false;
+                mbar_arrive(&bars[TC_YZ0 + half]);
+            }
+            return true;
+        });
+    } else {
+        // ---- rows of x ----
+        const bf16* px = static_cast<const bf16*>(a.x.data) + row * a.x.seq + (head / a.x.share) * a.x.head;
+        if (!summary)
+            fine = each_part([&](const TcPart& p, int chunks, uint32_t n0) {
+                for (int i = 0; i < chunks; ++i) {
+                    const uint32_t n = n0 + i;
+                    const int64_t t = chunk_at(p, chunks, i);
+                    if (n > 0 && !wait(TC_INTER, n - 1)) return false;  // scores and those with the state
+                    tc_load<DX>(tile_x, px + t * a.x.tok, a.x.tok, count_at(p, t), dx, lane);
+                    copy_commit();
+                    copy_wait<0>();
+                    fence_proxy_async_smem();
+                    mbar_arrive(&bars[TC_X]);
+                }
+                return true;
+            });
     }
     copy_wait<0>();
     if (!fine && lane == 0) atomicCAS(err, 0, KERR_WAIT_TIMEOUT);
