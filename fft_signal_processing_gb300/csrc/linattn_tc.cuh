@@ -12,8 +12,10 @@
 //                     memory
 // The state itself is float32 in the registers of the warps that own the rows of S^T: what a chunk
 // adds is summed by itself and then added, since the units cut their sums off where float32
-// additions round.  One block per SM, twenty warps, two for every 32 rows of tensor memory:
-//   A (eight warps, half a token's columns each thread): weights of the scores, outputs
+// additions round.  One block per SM (what is spilled has no room in its level-1 cache
+// beside the tiles, so warps are counted by their registers):
+//   A (four warps, a token each thread; eight in the gradients, half its columns): weights of the
+//   scores, outputs
 //   B (eight warps, half a row of S^T each thread): weighted z^T, the state
 //   one warp each issues the products, sums the decays, copies rows of y and z, copies rows of x:
 //   a fence before the units read shared memory waits for the thread's copies under way, so those
@@ -32,7 +34,7 @@ namespace {
 
 using bf16 = __nv_bfloat16;
 constexpr int kTcChunk = 128;
-constexpr int kTcThreads = 640, kTcGroup = 256;  // A and B: kTcGroup each
+constexpr int kTcB = 256;  // threads of B
 constexpr uint64_t kTcWaitNs = 2000000000ull;
 
 // ---- tcgen05 --------------------------------------------------------------------------------
@@ -61,6 +63,12 @@ __device__ __forceinline__ void tc_mma_ts(uint32_t d, uint32_t a, uint64_t b, ui
         "r"((uint32_t)add)
         : "memory");
 }
+// Sixteen summed values a step: operands summed over their columns go 32 bytes on within a panel of
+// 64 columns, operands summed over their rows 16 rows.  Loops that stay loops: descriptors that are
+// kept for a whole part would need more registers than there are.
+__device__ __forceinline__ uint64_t tc_columns(uint32_t tile, int panel, int k) {
+    return tc_desc(tile + (k >> 2) * panel + (k & 3) * 32, 16);
+}
 __device__ __forceinline__ void tc_commit(uint64_t* bar) {
     asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_addr(bar))
                  : "memory");
@@ -73,13 +81,12 @@ __device__ __forceinline__ void tc_wait_ld(uint32_t (&r)[32]) {
                  : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
                    "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]),
                    "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]), "+r"(r[23]),
-                   "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]), "+r"(r[30]), "+r"(r[31])
-                 :
-                 : "memory");
+                   "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]), "+r"(r[30]), "+r"(r[31]));
 }
 __device__ __forceinline__ void tc_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
-// 32 columns of this warp's 32 rows, one row per thread.
+// Accesses to tensor memory and matrix loads keep their order (volatile) but do not hold up others:
+// barriers and fences do. 32 columns of this warp's 32 rows, one row per thread.
 __device__ __forceinline__ void tc_ld32(uint32_t addr, uint32_t (&r)[32]) {
     asm volatile(
         "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
@@ -97,21 +104,18 @@ __device__ __forceinline__ void tc_st32(uint32_t addr, const uint32_t (&r)[32]) 
         "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
         "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]),
         "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
-        "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
-        : "memory");
+        "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31]));
 }
 __device__ __forceinline__ void tc_st16(uint32_t addr, const uint32_t (&r)[16]) {
     asm volatile(
         "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
         "%15, %16};" ::"r"(addr),
         "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
-        "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
-        : "memory");
+        "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]));
 }
 __device__ __forceinline__ void tc_st8(uint32_t addr, const uint32_t (&r)[8]) {
     asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(addr), "r"(r[0]),
-                 "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
-                 : "memory");
+                 "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]));
 }
 __device__ __forceinline__ void tc_ld16(uint32_t addr, uint32_t (&r)[16]) {
     asm volatile(
@@ -124,28 +128,23 @@ __device__ __forceinline__ void tc_ld16(uint32_t addr, uint32_t (&r)[16]) {
 __device__ __forceinline__ void tc_wait_ld16(uint32_t (&r)[16]) {
     asm volatile("tcgen05.wait::ld.sync.aligned;"
                  : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
-                   "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])
-                 :
-                 : "memory");
+                   "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]));
 }
 // 16 rows by 8 columns in the layout of a matrix load: thread l has rows l / 4 (r[0], r[2]) and
 // l / 4 + 8, columns l % 4 (r[0], r[1]) and l % 4 + 4.
 __device__ __forceinline__ void tc_st_block(uint32_t addr, const uint32_t (&r)[4]) {
     asm volatile("tcgen05.st.sync.aligned.16x128b.x2.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(r[0]), "r"(r[1]),
-                 "r"(r[2]), "r"(r[3])
-                 : "memory");
+                 "r"(r[2]), "r"(r[3]));
 }
 // Four 8 x 8 blocks of shared memory, row addresses from lanes 0..7, 8..15, ...; transposed.
 __device__ __forceinline__ void tc_ldmatrix_t(uint32_t addr, uint32_t (&f)[4]) {
     asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
                  : "=r"(f[0]), "=r"(f[1]), "=r"(f[2]), "=r"(f[3])
-                 : "r"(addr)
-                 : "memory");
+                 : "r"(addr));
 }
 __device__ __forceinline__ void tc_stmatrix(uint32_t addr, const uint32_t (&f)[4]) {
     asm volatile("stmatrix.sync.aligned.m8n8.x4.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(f[0]), "r"(f[1]),
-                 "r"(f[2]), "r"(f[3])
-                 : "memory");
+                 "r"(f[2]), "r"(f[3]));
 }
 __device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
     asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_addr(bar)) : "memory");
@@ -175,6 +174,8 @@ __device__ __forceinline__ void tc_split(float2 v, uint32_t (&p)[N]) {
 
 template <int DX, int DZ, bool BWD>
 struct TcShape {
+    static constexpr int kSides = BWD ? 2 : 1, kA = 128 * kSides;  // threads of A
+    static constexpr int kThreads = kA + kTcB + 128;
     static constexpr int kPO = BWD ? 2 : 1;  // pieces of weighted scores and of the state as an operand
     static constexpr int kTileX = kTcChunk * DX * 2, kTileZ = kTcChunk * DZ * 2, kTileS = kPO * DZ * DX * 2,
                          kTileW = kTcChunk * kTcChunk * 2;
@@ -185,7 +186,7 @@ struct TcShape {
     static constexpr int kTiles = kTileX + kStageY * kTileX + kStageZ * kTileZ + kTileS + kTileW;
 };
 
-enum { TC_X, TC_YZ0, TC_YZ1, TC_SCORES, TC_INTER, TC_OUT, TC_UPDATE, TC_WEIGHTED, TC_STATE, TC_WZ, TC_TAKEN0, TC_TAKEN1, TC_DECAYS,
+enum { TC_X, TC_Y0, TC_Y1, TC_Z0, TC_Z1, TC_SCORES, TC_INTER, TC_OUT, TC_UPDATE0, TC_UPDATE1, TC_WEIGHTED, TC_STATE, TC_WZ, TC_TAKEN0, TC_TAKEN1, TC_DECAYS,
        TC_FREE, TC_BARS };
 
 // Behind the tiles.  BUFFERS: stages of z.
@@ -194,7 +195,7 @@ struct TcSmall {
     float2 G[kTcChunk];  // the sums of the decays (log2) in two floats
     float update[kTcChunk];
     float column[kTcChunk];  // factors of the columns of scores, from the end of their block of 32
-    float total, total_log2, all_hi, all_lo;
+    float total, all_hi, all_lo;
     uint64_t bars[TC_BARS];
     // of every column of z, by halves of the tokens, the place of a value that is not finite, plus 1:
     // the first one, 255 for none; reversed the last one, 0 for none.  Set where bad_any is.
@@ -230,15 +231,15 @@ __device__ __forceinline__ TcTwo tc_log2_decay(float g) {
 // The part of a segment that belongs to one sequence (offsets of any kind: it holds token `at` and
 // stays in the segment).
 struct TcPart {
-    int64_t begin, end, seq;
+    int begin, end, seq;
     bool first, last;
 };
-__device__ __forceinline__ TcPart tc_part(const AttnArgs& a, int64_t row, int64_t t0, int64_t t1, int64_t at) {
+__device__ __forceinline__ TcPart tc_part(const AttnArgs& a, int row, int t0, int t1, int at) {
     const SeqAt s = seq_at(a.offsets, a.nseq, a.length, row, at);
     TcPart p;
-    p.seq = s.q;
-    p.begin = s.begin > at ? at : (s.begin < t0 ? t0 : s.begin);
-    p.end = s.end <= at ? at + 1 : (s.end > t1 ? t1 : s.end);
+    p.seq = (int)s.q;
+    p.begin = s.begin > at ? at : (s.begin < t0 ? t0 : (int)s.begin);
+    p.end = s.end <= at ? at + 1 : (s.end > t1 ? t1 : (int)s.end);
     p.first = p.begin == 0 || (s.begin >= t0 && s.begin <= at);
     p.last = p.end == a.length || (s.end <= t1 && s.end > at);
     return p;
@@ -253,7 +254,7 @@ __device__ __forceinline__ void tc_load(char* tile, const bf16* g, int64_t tok, 
     const bf16* src = g + r * tok + c * 8;
     char* dst = tile + (c >> 3) * (kTcChunk * 128) + r * 128;
     const int live = c * 8 < dim ? count : 0, swizzled = (c & 7) ^ r;
-#pragma unroll 8
+#pragma unroll 4
     for (int k = 0; k < kTcChunk; k += STEP) {
         const bool in = r + k < live;
         copy16(dst + k * 128 + ((swizzled ^ (k & 7)) << 4), in ? src : g, in);
@@ -282,9 +283,10 @@ __device__ __forceinline__ void tc_meet(int bar, int threads) {
 }
 
 template <int DX, int DZ, bool BWD>
-__global__ void __launch_bounds__(kTcThreads, 1) k_linattn_tc(const AttnArgs a, int* err) {
+__global__ void __launch_bounds__(TcShape<DX, DZ, BWD>::kThreads, 1) k_linattn_tc(const AttnArgs a, int* err) {
     using Shape = TcShape<DX, DZ, BWD>;
-    constexpr int C = kTcChunk, PO = Shape::kPO, PANEL = C * 128;
+    constexpr int C = kTcChunk, PO = Shape::kPO, PANEL = C * 128, SIDES = Shape::kSides;
+    constexpr int B0 = Shape::kA / 32, M0 = B0 + kTcB / 32;  // first warps of B and of the others
     extern __shared__ __align__(1024) char base[];
     char* tile_x = base;
     char* tile_y = tile_x + Shape::kTileX;
@@ -297,26 +299,27 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_linattn_tc(const AttnArgs a, 
     if (!tma_stage_aligned(base, err) || (smem_addr(base) & 1023)) return;  // every thread alike
 
     const int tid = (int)threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    int64_t b = blockIdx.x;
-    const int64_t zt = b % a.ztiles;
-    b /= a.ztiles;
-    const int64_t head = b % a.heads;
-    b /= a.heads;
-    const int64_t seg = b % a.nsegments, row = b / a.nsegments;
-    const int64_t t0 = seg * a.segment, t1 = t0 + a.segment < a.length ? t0 + a.segment : a.length;
-    const int z0 = (int)zt * DZ, dz = (int)a.dz - z0 < DZ ? (int)a.dz - z0 : DZ, dx = (int)a.dx;
+    // lengths and counts of blocks are below 2^31
+    unsigned b = blockIdx.x;
+    const int zt = (int)(b % (unsigned)a.ztiles);
+    b /= (unsigned)a.ztiles;
+    const int head = (int)(b % (unsigned)a.heads);
+    b /= (unsigned)a.heads;
+    const int seg = (int)(b % (unsigned)a.nsegments), row = (int)(b / (unsigned)a.nsegments);
+    const int t0 = (int)(seg * a.segment), t1 = (int)(t0 + a.segment < a.length ? t0 + a.segment : a.length);
+    const int z0 = zt * DZ, dz = (int)a.dz - z0 < DZ ? (int)a.dz - z0 : DZ, dx = (int)a.dx;
     const bool reverse = a.reverse, summary = a.summary;
 
-    if (warp == 16) {
+    if (warp == M0) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_addr(&sm.tmem))
                      : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
     }
     if (tid == 0) {
         for (int i = 0; i < TC_BARS; ++i) {
-            const bool commit = i == TC_SCORES || i == TC_INTER || i == TC_OUT || i == TC_UPDATE;
-            const bool warps = i == TC_DECAYS || i == TC_X || i == TC_YZ0 || i == TC_YZ1;
-            mbar_init(&bars[i], commit ? 1 : (warps ? 32 : (i == TC_FREE ? 2 * kTcGroup : kTcGroup)));
+            const bool commit = i == TC_SCORES || i == TC_INTER || i == TC_OUT || i == TC_UPDATE0 || i == TC_UPDATE1;
+            const bool warps = i == TC_DECAYS || (i >= TC_X && i <= TC_Z1);
+            mbar_init(&bars[i], commit ? 1 : (warps ? 32 : (i == TC_FREE ? Shape::kA + kTcB : (i == TC_STATE || i == TC_WZ ? kTcB : Shape::kA))));
         }
         fence_mbar_init();
     }
@@ -331,12 +334,12 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_linattn_tc(const AttnArgs a, 
     // Calls f(part, n) for every part of the segment in the direction of the pass, n its first
     // chunk's number; a summary takes the part that reaches the next segment.
     auto each_part = [&](auto f) {
-        int64_t at = summary == reverse ? t0 : t1 - 1;
+        int at = summary == reverse ? t0 : t1 - 1;
         if (!summary) at = reverse ? t1 - 1 : t0;
         uint32_t n = 0;
         while (true) {
             const TcPart p = tc_part(a, row, t0, t1, at);
-            const int chunks = (int)((p.end - p.begin + C - 1) / C);
+            const int chunks = (p.end - p.begin + C - 1) / C;
             if (!f(p, chunks, n)) return false;
             n += chunks;
             at = reverse ? p.begin - 1 : p.end;
@@ -344,27 +347,27 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_linattn_tc(const AttnArgs a, 
         }
     };
     auto chunk_at = [&](const TcPart& p, int chunks, int i) {
-        return p.begin + (int64_t)(reverse ? chunks - 1 - i : i) * C;
+        return p.begin + (reverse ? chunks - 1 - i : i) * C;
     };
-    auto count_at = [&](const TcPart& p, int64_t t) { return (int)(p.end - t < C ? p.end - t : C); };
+    auto count_at = [&](const TcPart& p, int t) { return p.end - t < C ? p.end - t : C; };
     auto begins_at = [&](const TcPart& p) { return reverse ? p.last : p.first; };
     // whether the part's first chunk meets a state that is not zero
     auto starts_with_state = [&](const TcPart& p) { return begins_at(p) ? a.initial != nullptr : !summary && a.nsegments > 1; };
 
     bool fine = true;
     const int quad = warp & 3;  // rows 32 quad .. of tensor memory
-    if (warp < 8) {
-        // ---- A: half a token's columns each thread ----
+    if (warp < B0) {
+        // ---- A: a token, or half of one's columns, each thread ----
         const bf16* pp = BWD && a.partner.data
                              ? static_cast<const bf16*>(a.partner.data) + row * a.partner.seq +
                                    (head / a.partner.share) * a.partner.head + z0
                              : nullptr;
         const int r = tid & 127, side = warp >> 2;
-        constexpr int HALF = DZ / 2;
+        constexpr int COLUMNS = DZ / SIDES;
         fine = each_part([&](const TcPart& p, int chunks, uint32_t n0) {
             for (int i = 0; i < chunks; ++i) {
                 const uint32_t n = n0 + i, half = n & 1;
-                const int64_t t = chunk_at(p, chunks, i);
+                const int t = chunk_at(p, chunks, i);
                 const int count = count_at(p, t);
                 const bool some = i > 0 || starts_with_state(p);
                 if (summary) {
@@ -376,16 +379,11 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_linattn_tc(const AttnArgs a, 
                 tc_after();
                 const float2 G = sm.G[r];
                 const float inter = ex2(reverse ? (sm.all_hi - G.x) + (sm.all_lo - G.y) : G.x) * a.scale_inter;
-                uint32_t s[2][32];
-                tc_ld32(tmem + lanes + side * 64, s[0]);
-                tc_ld32(tmem + lanes + side * 64 + 32, s[1]);
-                tc_wait_ld(s[0]);
-                tc_wait_ld(s[1]);
-                tc_meet(2 + quad, 64);  // the other half of these rows has been read too
+                auto weigh = [&](int cb, const uint32_t (&s)[32]) {
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {  // 16 columns at a time
-                    const int cb = side * 2 + k / 2, c0 = cb * 32 + (k & 1) * 16;
-                    const uint32_t* sk = s[k / 2] + (k & 1) * 16;
+                for (int k = 0; k < 2; ++k) {  // 16 columns at a time
+                    const int c0 = cb * 32 + k * 16;
+                    const uint32_t* sk = s + k * 16;
                     uint32_t out[PO][8];
                     if (cb == quad) {  // the rows' own block
                         const float sign = reverse ? -1.f : 1.f;
@@ -396,7 +394,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_linattn_tc(const AttnArgs a, 
                             float v[2];
 #pragma unroll
                             for (int e = 0; e < 2; ++e) {
-                                const int c = (k & 1) * 16 + 2 * j + e;
+                                const int c = k * 16 + 2 * j + e;
                                 const float w = __uint_as_float(sk[2 * j + e]) * (ex2(sign * d[e]) * a.scale_pair);
                                 v[e] = (reverse ? c >= lane : c <= lane) ? w : 0.f;
                                 if (BWD && c == lane) sm.diagonal[r] = v[e], v[e] = 0.f;
@@ -432,6 +430,20 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_linattn_tc(const AttnArgs a, 
 #pragma unroll
                     for (int u = 0; u < PO; ++u) tc_st8(tmem + lanes + u * 64 + c0 / 2, out[u]);
                 }
+                };
+                // The weighted scores go where scores are that have been read (by the other half's
+                // threads too): the first piece in columns 0 to 63, the second in the others.
+#pragma unroll 1
+                for (int cb = side * 2; cb < side * 2 + 4 / SIDES; cb += 2) {
+                    uint32_t s[2][32];
+                    tc_ld32(tmem + lanes + cb * 32, s[0]);
+                    tc_ld32(tmem + lanes + cb * 32 + 32, s[1]);
+                    tc_wait_ld(s[0]);
+                    tc_wait_ld(s[1]);
+                    if (SIDES == 2) tc_meet(2 + quad, 64);
+                    weigh(cb, s[0]);
+                    weigh(cb + 1, s[1]);
+                }
                 mbar_arrive(&bars[TC_FREE]);
                 // Rows go to and from memory in 64 bytes by four lanes; a lane's own row is among theirs.
                 const int r4 = r & ~3;
@@ -444,7 +456,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_linattn_tc(const AttnArgs a, 
                         const int c = c0 + 8 * (lane & 3);
                         q[k] = make_uint4(0, 0, 0, 0);
                         if (r4 + k < count && c < dz)
-                            q[k] = *reinterpret_cast<const uint4*>(pp + (t + r4 + k) * a.partner.tok + c);
+                            q[k] = *reinterpret_cast<const uint4*>(pp + (int64_t)(t + r4 + k) * a.partner.tok + c);
                     }
                     tc_transpose(q, lane);
 #pragma unroll
@@ -464,7 +476,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_linattn_tc(const AttnArgs a, 
                     if (!wait(TC_INTER, n)) return false;
                     tc_after();
 #pragma unroll 1
-                    for (int c0 = side * HALF; c0 < side * HALF + HALF; c0 += 32) {
+                    for (int c0 = side * COLUMNS; c0 < side * COLUMNS + COLUMNS; c0 += 32) {
                         uint32_t v[32];
                         tc_ld32(kOut + lanes + c0, v);
                         tc_wait_ld(v);
@@ -486,7 +498,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_linattn_tc(const AttnArgs a, 
                 const float diagonal = BWD ? sm.diagonal[r] : 0.f;
                 float all = 0.f;
 #pragma unroll 1
-                for (int c0 = side * HALF; c0 < side * HALF + HALF; c0 += 32) {
+                for (int c0 = side * COLUMNS; c0 < side * COLUMNS + COLUMNS; c0 += 32) {
                     uint32_t v[32];
                     tc_ld32(kOut + lanes + c0, v);
                     tc_wait_ld(v);
@@ -548,7 +560,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_linattn_tc(const AttnArgs a, 
                     }
                 }
                 if (pp && r < count) {
-                    const int64_t k = ((zt * 2 + side) * a.heads + head) * (a.rows * a.length) + row * a.length + t + r;
+                    const int64_t k = ((zt * SIDES + side) * a.heads + head) * (a.rows * a.length) + row * a.length + t + r;
                     a.dots_inter[k] = between;
                     a.dots_all[k] = all;
                 }
@@ -557,26 +569,27 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_linattn_tc(const AttnArgs a, 
             }
             return true;
         });
-    } else if (warp < 16) {
+    } else if (warp < M0) {
         // ---- B: half a row of S^T each thread; half the tokens of z^T ----
-        const int id = tid - kTcGroup, m = id & 127, side = id >> 7;
+        const int id = tid - Shape::kA, m = id & 127, side = id >> 7;
         constexpr int HALF = DX / 2;
         const int x0 = side * HALF;
         float2 S[HALF / 2];  // row m of S^T, columns x0 ..
-        const int64_t carry_at = (((row * a.nsegments + seg) * a.heads + head) * a.ztiles + zt) * (DX * 128) +
+        const int64_t carry_at = ((((int64_t)row * a.nsegments + seg) * a.heads + head) * a.ztiles + zt) * (DX * 128) +
                                  (side * (HALF / 4) * 128 + m) * 4;
         // S as an operand: row m, columns in panels of 64
+        char* state_row = tile_s + (x0 >> 6) * (DZ * 128) + m * 128;
+        const int swizzle = ((m & 7) ^ (x0 / 8 & 7)) << 4;
         auto put_state = [&] {
             if (m < DZ && !summary) {
 #pragma unroll
                 for (int k = 0; k < HALF / 8; ++k) {
-                    const int c = x0 / 8 + k;
                     uint32_t q[4][PO];
 #pragma unroll
                     for (int e = 0; e < 4; ++e) tc_split<PO>(S[4 * k + e], q[e]);
 #pragma unroll
                     for (int u = 0; u < PO; ++u)
-                        *reinterpret_cast<uint4*>(tile_s + u * (DZ * DX * 2) + (c >> 3) * (DZ * 128) + tc_chunk(m, c & 7)) =
+                        *reinterpret_cast<uint4*>(state_row + u * (DZ * DX * 2) + (swizzle ^ (k << 4))) =
                             make_uint4(q[0][u], q[1][u], q[2][u], q[3][u]);
                 }
             }
@@ -584,29 +597,26 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_linattn_tc(const AttnArgs a, 
             tc_before();
             mbar_arrive(&bars[TC_STATE]);
         };
-        // f(value, x) of the values that this thread holds
-        auto each_state = [&](auto f) {
-            if (m < dz) {
+        // f(value, address) of the values that this thread holds, in states at p (the next address from
+        // the last one: all of them at once would be kept in registers)
+        auto each_state = [&](auto* p, auto f) {
+            if (m >= dz) return;
+            p += x0 * a.state_x;
 #pragma unroll
-                for (int j = 0; j < HALF / 2; ++j) {
-                    if (x0 + 2 * j < dx) f(S[j].x, x0 + 2 * j);
-                    if (x0 + 2 * j + 1 < dx) f(S[j].y, x0 + 2 * j + 1);
-                }
+            for (int j = 0; j < HALF; ++j) {
+                if (x0 + j < dx) f(j & 1 ? S[j / 2].y : S[j / 2].x, p);
+                p += a.state_x;
+                asm volatile("" : "+l"(p));
             }
         };
-        double gone = 0.0;
-        bool from_start = false;
         fine = each_part([&](const TcPart& p, int chunks, uint32_t n0) {
             const int64_t mine = (p.seq * a.heads + head) * a.dx * a.dz + (z0 + m) * a.state_z;
-            from_start = begins_at(p);
+            const bool from_start = begins_at(p);
             // the last chunk's products are over, those with the state among them
 #pragma unroll
             for (int j = 0; j < HALF / 2; ++j) S[j] = splat(0.f);
             if (from_start) {
-                if (a.initial) {
-                    const float* q = a.initial + mine;
-                    each_state([&](float& v, int x) { v = q[x * a.state_x]; });
-                }
+                if (a.initial) each_state(a.initial + mine, [](float& v, const float* q) { v = *q; });
             } else if (!summary && a.nsegments > 1) {
                 const float4* q = reinterpret_cast<const float4*>(a.carry + carry_at);
 #pragma unroll
@@ -619,42 +629,39 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_linattn_tc(const AttnArgs a, 
             for (int i = 0; i < chunks; ++i) {
                 const uint32_t n = n0 + i, half = n & 1;
                 const bool next = i + 1 < chunks;
-                if (!wait(TC_YZ0 + half, n >> 1) || !wait(TC_DECAYS, n)) return false;
-                const float2 total = splat(sm.total);
-                if (summary) gone += sm.total_log2;
+                if (!wait(TC_Z0 + half, n >> 1) || !wait(TC_DECAYS, n)) return false;
+                const float total = sm.total;
                 // this warp's 32 columns of z and half of the tokens, weighted, in three pieces
                 char* sz = tile_z + (Shape::kStageZ == 2 ? half * Shape::kTileZ : 0);
                 const uint32_t z_at = smem_addr(sz), w_at = smem_addr(tile_w);
                 float2 odd = splat(0.f);
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    const int k0 = side * 64 + k * 16;
-                    const float2 w0 = *reinterpret_cast<const float2*>(&sm.update[k0 + 2 * (lane & 3)]);
-                    const float2 w1 = *reinterpret_cast<const float2*>(&sm.update[k0 + 8 + 2 * (lane & 3)]);
-#pragma unroll
-                    for (int rb = 0; rb < 2; ++rb) {
-                        const int m0 = quad * 32 + rb * 16;
-                        uint32_t f[4] = {}, q[3][4];
-                        if (m0 < DZ) {
-                            const int tk = k0 + (lane & 7) + (lane >> 4) * 8, c = m0 / 8 + ((lane >> 3) & 1);
-                            tc_ldmatrix_t(z_at + (c >> 3) * PANEL + tc_chunk(tk, c & 7), f);
-                        }
-#pragma unroll
-                        for (int h = 0; h < 4; ++h) {
-                            const float2 v = tc_values(f[h]);
-                            odd = fma2(v, splat(0.f), odd);
-                            uint32_t g[3];
-                            tc_split<3>(mul2(v, h < 2 ? w0 : w1), g);
-#pragma unroll
-                            for (int u = 0; u < 3; ++u) q[u][h] = g[u];
-                        }
-                        const uint32_t to = kWz + lanes + ((uint32_t)(rb * 16) << 16) + k0 / 2;
-                        tc_st_block(to, q[0]);
-                        tc_st_block(to + 64, q[1]);
-                        // rows m0 .. m0 + 15 of the third piece's tile, 16 tokens
-                        const int rw = m0 + (lane & 7) + ((lane >> 3) & 1) * 8, c = (k0 & 63) / 8 + (lane >> 4);
-                        tc_stmatrix(w_at + side * PANEL + tc_chunk(rw, c), q[2]);
+                // two blocks of 16 columns by four of 16 tokens; a loop, since addresses of all eight would be
+                // kept for the whole part
+#pragma unroll(BWD ? 1 : 2)
+                for (int it = 0; it < 8; ++it) {
+                    const int m0 = quad * 32 + (it & 1) * 16, tk = side * 64 + (it >> 1) * 16;
+                    const float2 w0 = *reinterpret_cast<const float2*>(&sm.update[tk + 2 * (lane & 3)]);
+                    const float2 w1 = *reinterpret_cast<const float2*>(&sm.update[tk + 8 + 2 * (lane & 3)]);
+                    uint32_t f[4] = {}, q[3][4];
+                    if (m0 < DZ) {
+                        const int at = tk + (lane & 7) + (lane >> 4) * 8, c = m0 / 8 + ((lane >> 3) & 1);
+                        tc_ldmatrix_t(z_at + (c >> 3) * PANEL + tc_chunk(at, c & 7), f);
                     }
+#pragma unroll
+                    for (int h = 0; h < 4; ++h) {
+                        const float2 v = tc_values(f[h]);
+                        odd = fma2(v, splat(0.f), odd);
+                        uint32_t g[3];
+                        tc_split<3>(mul2(v, h < 2 ? w0 : w1), g);
+#pragma unroll
+                        for (int u = 0; u < 3; ++u) q[u][h] = g[u];
+                    }
+                    const uint32_t to = kWz + lanes + ((uint32_t)(it & 1) << 20) + tk / 2;
+                    tc_st_block(to, q[0]);
+                    tc_st_block(to + 64, q[1]);
+                    // rows m0 .. m0 + 15 of the third piece's tile, 16 tokens
+                    const int rw = m0 + (lane & 7) + ((lane >> 3) & 1) * 8, c = (tk & 63) / 8 + (lane >> 4);
+                    tc_stmatrix(w_at + side * PANEL + tc_chunk(rw, c), q[2]);
                 }
                 mbar_arrive(&bars[TC_FREE]);
                 if (!summary) {
@@ -674,14 +681,14 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_linattn_tc(const AttnArgs a, 
                     }
                     const int bz = Shape::kStageZ == 2 ? half : 0;
                     sm.bad_at[bz][side][m] = (unsigned char)k;
-                    if (lane == 0) sm.bad_any[bz][warp - 8] = any;
+                    if (lane == 0) sm.bad_any[bz][warp - B0] = any;
                 }
                 tc_wait_st();
                 fence_proxy_async_smem();
                 tc_before();
                 mbar_arrive(&bars[TC_WZ]);
 
-                if (!wait(TC_UPDATE, n)) return false;
+                if (!wait(TC_UPDATE0 + half, n >> 1)) return false;
                 tc_after();
 #pragma unroll
                 for (int c0 = 0; c0 < HALF; c0 += 16) {
@@ -690,30 +697,26 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_linattn_tc(const AttnArgs a, 
                     tc_wait_ld16(v);
 #pragma unroll
                     for (int j = 0; j < 8; ++j)
-                        S[c0 / 2 + j] = fma2(total, S[c0 / 2 + j],
+                        S[c0 / 2 + j] = fma2(splat(total), S[c0 / 2 + j],
                                              make_float2(__uint_as_float(v[2 * j]), __uint_as_float(v[2 * j + 1])));
                 }
                 if (next) put_state();
             }
             if (!summary && (reverse ? p.first : p.last)) {
-                if (a.final_state) {
-                    float* q = a.final_state + mine;
-                    each_state([&](float& v, int x) { q[x * a.state_x] = v; });
-                }
+                if (a.final_state) each_state(a.final_state + mine, [](float& v, float* q) { *q = v; });
                 if (BWD && a.final_dot) {
-                    const float* q = a.final_dot + mine;
                     float sum = 0.f;
-                    each_state([&](float& v, int x) { sum = fmaf(v, q[x * a.state_x], sum); });
+                    each_state(a.final_dot + mine, [&](float& v, const float* q) { sum = fmaf(v, *q, sum); });
 #pragma unroll
                     for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-                    if (lane == 0) sm.warp_sums[warp - 8] = sum;
-                    tc_meet(1, kTcGroup);
+                    if (lane == 0) sm.warp_sums[warp - B0] = sum;
+                    tc_meet(1, kTcB);
                     if (id == 0) {
                         sum = 0.f;
                         for (int w = 0; w < 8; ++w) sum += sm.warp_sums[w];
                         a.final_dots[(zt * a.nseq + p.seq) * a.heads + head] = sum;
                     }
-                    tc_meet(1, kTcGroup);
+                    tc_meet(1, kTcB);
                 }
             }
             return true;
@@ -722,35 +725,32 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_linattn_tc(const AttnArgs a, 
             float4* q = reinterpret_cast<float4*>(a.carry + carry_at);
 #pragma unroll
             for (int j = 0; j < HALF / 4; ++j) q[j * 128] = make_float4(S[2 * j].x, S[2 * j].y, S[2 * j + 1].x, S[2 * j + 1].y);
-            if (zt == 0 && id == 0) {
-                const int64_t i = (row * a.nsegments + seg) * a.heads + head;
-                a.carry_decay[i] = (float)gone;
-                a.carry_reset[i] = from_start;
-            }
         }
-    } else if (warp == 16) {
+    } else if (warp == M0) {
         // ---- the products, issued by one thread ----
         const uint32_t x = smem_addr(tile_x), y = smem_addr(tile_y), z = smem_addr(tile_z), s = smem_addr(tile_s),
                        w = smem_addr(tile_w);
         fine = each_part([&](const TcPart& p, int chunks, uint32_t n0) {
             bool good = true;
             const bool start = starts_with_state(p);
+            auto scores = [&](uint32_t n) {
+                const uint32_t yn = y + (n & 1) * Shape::kTileX;
+#pragma unroll
+                for (int k = 0; k < DX / 16; ++k)
+                    tc_mma(tmem, tc_columns(x, PANEL, k), tc_columns(yn, PANEL, k), tc_idesc(C, false), k > 0);
+                tc_commit(&bars[TC_SCORES]);
+            };
             if (lane == 0) {
                 for (int i = 0; i < chunks && good; ++i) {
                     const uint32_t n = n0 + i, half = n & 1;
                     const uint32_t yn = y + half * Shape::kTileX, zn = z + (Shape::kStageZ == 2 ? half * Shape::kTileZ : 0);
                     const bool some = i > 0 || start;
-                    good = (summary || wait(TC_X, n)) && wait(TC_YZ0 + half, n >> 1);
-                    // scores go over the weighted ones of the chunk before
-                    good = good && (summary || n == 0 || wait(TC_OUT, n - 1));
-                    if (!good) break;
-                    tc_after();
-                    if (!summary) {
-#pragma unroll
-                        for (int k = 0; k < DX / 16; ++k)
-                            tc_mma(tmem, tc_desc(x + (k >> 2) * PANEL + (k & 3) * 32, 16),
-                                   tc_desc(yn + (k >> 2) * PANEL + (k & 3) * 32, 16), tc_idesc(C, false), k > 0);
-                        tc_commit(&bars[TC_SCORES]);
+                    if (i == 0 || summary) {
+                        good = wait(TC_Y0 + half, n >> 1) &&
+                               (summary || (wait(TC_X, n) && (n == 0 || wait(TC_OUT, n - 1))));
+                        if (!good) break;
+                        tc_after();
+                        if (!summary) scores(n);
                     }
                     good = wait(TC_STATE, n) && (summary || n == 0 || wait(TC_TAKEN0 + (half ^ 1), (n - 1) >> 1));
                     if (!good) break;
@@ -761,8 +761,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_linattn_tc(const AttnArgs a, 
                             for (int u = PO - 1; u >= 0; --u)
 #pragma unroll
                                 for (int k = 0; k < DX / 16; ++k)
-                                    tc_mma(kOut, tc_desc(x + (k >> 2) * PANEL + (k & 3) * 32, 16),
-                                           tc_desc(s + u * (DZ * DX * 2) + (k >> 2) * (DZ * 128) + (k & 3) * 32, 16),
+                                    tc_mma(kOut, tc_columns(x, PANEL, k), tc_columns(s + u * (DZ * DX * 2), DZ * 128, k),
                                            tc_idesc(DZ, false), u < PO - 1 || k > 0);
                         }
                         tc_commit(&bars[TC_INTER]);  // once per chunk, whether there was a state or not
@@ -782,25 +781,33 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_linattn_tc(const AttnArgs a, 
                     }
 #pragma unroll
                     for (int k = 0; k < C / 16; ++k)
-                        tc_mma(kAdd, tc_desc(w + (k >> 2) * PANEL + (k & 3) * 32, 16),
-                               tc_desc(yn + k * 2048, PANEL), tc_idesc(DX, true), k > 0);
+                        tc_mma(kAdd, tc_columns(w, PANEL, k), tc_desc(yn + k * 2048, PANEL), tc_idesc(DX, true), k > 0);
+                    // The next chunk's scores between the pieces of the state, so that A has them in time;
+                    // they go over this one's weighted scores, whose product is over by then.
+                    if (i + 1 < chunks && !summary) {
+                        good = wait(TC_Y0 + (half ^ 1), (n + 1) >> 1) && wait(TC_X, n + 1) && wait(TC_OUT, n);
+                        if (!good) break;
+                        tc_after();
+                        scores(n + 1);
+                    }
 #pragma unroll
                     for (int u = 1; u >= 0; --u)
 #pragma unroll
                         for (int k = 0; k < C / 16; ++k)
                             tc_mma_ts(kAdd, kWz + u * 64 + k * 8, tc_desc(yn + k * 2048, PANEL), tc_idesc(DX, true), true);
-                    tc_commit(&bars[TC_UPDATE]);
+                    tc_commit(&bars[TC_UPDATE0 + half]);
                 }
             }
             return __all_sync(0xffffffffu, good) != 0;
         });
-    } else if (warp == 17) {
+    } else if (warp == M0 + 1) {
         // ---- decays: four tokens per lane ----
         const bf16* pg = static_cast<const bf16*>(a.decay.data) + row * a.decay.seq_stride + head;
+        TcTwo gone = {0.f, 0.f};
         fine = each_part([&](const TcPart& p, int chunks, uint32_t n0) {
             float g[4];
             auto fetch = [&](int i) {
-                const int64_t t = chunk_at(p, chunks, i);
+                const int t = chunk_at(p, chunks, i);
                 const int count = count_at(p, t);
 #pragma unroll
                 for (int k = 0; k < 4; ++k)
@@ -835,40 +842,49 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_linattn_tc(const AttnArgs a, 
                     sm.column[4 * lane + k] = edge < 0 ? 0.f : ex2(reverse ? -to_end : to_end);
                     sm.update[4 * lane + k] = ex2(reverse ? G.hi : (all.hi - G.hi) + (all.lo - G.lo)) * a.scale_update;
                 }
-                if (lane == 0) sm.total = ex2(all.hi), sm.total_log2 = sm.all_hi = all.hi, sm.all_lo = all.lo;
+                if (lane == 0) sm.total = ex2(all.hi), sm.all_hi = all.hi, sm.all_lo = all.lo;
+                gone = tc_add(gone, all);
                 mbar_arrive(&bars[TC_DECAYS]);
+            }
+            if (summary && zt == 0 && lane == 0) {
+                const int64_t at = ((int64_t)row * a.nsegments + seg) * a.heads + head;
+                a.carry_decay[at] = gone.hi;
+                a.carry_reset[at] = begins_at(p);
             }
             return true;
         });
     }
-    else if (warp == 18) {
+    else if (warp == M0 + 2) {
         // ---- rows of y and z ----
         const bf16* py = static_cast<const bf16*>(a.y.data) + row * a.y.seq + (head / a.y.share) * a.y.head;
         const bf16* pz = static_cast<const bf16*>(a.z.data) + row * a.z.seq + (head / a.z.share) * a.z.head + z0;
         fine = each_part([&](const TcPart& p, int chunks, uint32_t n0) {
             for (int i = 0; i < chunks; ++i) {
                 const uint32_t n = n0 + i, half = n & 1;
-                const int64_t t = chunk_at(p, chunks, i);
+                const int t = chunk_at(p, chunks, i);
                 const int count = count_at(p, t);
-                // y's stage is free: the chunk before the last had been waited for below
+                // A stage is free when the products of the chunk that was there are over and, in the
+                // gradients, A has read its rows of z for the outputs.  (None of these barriers can be a
+                // phase ahead of its wait: the next one needs the rows that are copied here.)
+                if (n > 1 && !wait(TC_UPDATE0 + half, (n - 2) >> 1)) return false;
                 tc_load<DX>(tile_y + half * Shape::kTileX, py + t * a.y.tok, a.y.tok, count, dx, lane);
-                // z's, once A has taken the outputs of the chunk that was there (in the gradients it
-                // reads z for them; else their product is over, which is waited for below as well)
+                copy_commit();
                 if (Shape::kStageZ == 1) {
-                    if (n > 0 && !summary && !wait(TC_TAKEN0 + (half ^ 1), (n - 1) >> 1)) return false;
+                    copy_wait<0>();
+                    fence_proxy_async_smem();
+                    mbar_arrive(&bars[TC_Y0 + half]);
+                    const int last = summary ? TC_UPDATE0 : TC_TAKEN0;
+                    if (n > 0 && !wait(last + (half ^ 1), (n - 1) >> 1)) return false;
                 } else if (BWD) {
                     if (n > 1 && !summary && !wait(TC_TAKEN0 + half, (n - 2) >> 1)) return false;
                 }
-                if (Shape::kStageZ == 1 && summary && n > 0 && !wait(TC_UPDATE, n - 1)) return false;
                 tc_load<DZ>(tile_z + (Shape::kStageZ == 2 ? half * Shape::kTileZ : 0), pz + t * a.z.tok, a.z.tok, count, dz,
                             lane);
                 copy_commit();
                 copy_wait<0>();
                 fence_proxy_async_smem();
-                // The products of the chunk before are over, so the next one's rows may follow; told of
-                // only then, the barrier cannot be a phase ahead of this wait.
-                if (n > 0 && !wait(TC_UPDATE, n - 1)) return false;
-                mbar_arrive(&bars[TC_YZ0 + half]);
+                if (Shape::kStageZ == 2) mbar_arrive(&bars[TC_Y0 + half]);
+                mbar_arrive(&bars[TC_Z0 + half]);
             }
             return true;
         });
@@ -879,7 +895,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_linattn_tc(const AttnArgs a, 
             fine = each_part([&](const TcPart& p, int chunks, uint32_t n0) {
                 for (int i = 0; i < chunks; ++i) {
                     const uint32_t n = n0 + i;
-                    const int64_t t = chunk_at(p, chunks, i);
+                    const int t = chunk_at(p, chunks, i);
                     if (n > 0 && !wait(TC_INTER, n - 1)) return false;  // scores and those with the state
                     tc_load<DX>(tile_x, px + t * a.x.tok, a.x.tok, count_at(p, t), dx, lane);
                     copy_commit();
@@ -894,7 +910,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_linattn_tc(const AttnArgs a, 
     if (!fine && lane == 0) atomicCAS(err, 0, KERR_WAIT_TIMEOUT);
     tc_before();
     __syncthreads();
-    if (warp == 16) {
+    if (warp == M0) {
         tc_after();
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
     }
@@ -909,7 +925,7 @@ cudaError_t launch_attn_tc(const AttnArgs& args, int* err, cudaStream_t s) {
     LaunchGeom g;
     cudaError_t e = cache.get(
         [](int dev, LaunchGeom* out) {
-            return setup_persistent(k_linattn_tc<DX, DZ, BWD>, kTcThreads, tc_bytes<DX, DZ, BWD>(), dev, out);
+            return setup_persistent(k_linattn_tc<DX, DZ, BWD>, Shape::kThreads, tc_bytes<DX, DZ, BWD>(), dev, out);
         },
         &g);
     if (e != cudaSuccess) return e;
@@ -918,13 +934,13 @@ cudaError_t launch_attn_tc(const AttnArgs& args, int* err, cudaStream_t s) {
     if (blocks > INT32_MAX) return cudaErrorInvalidValue;
     if (a.nsegments > 1) {
         a.summary = 1;
-        k_linattn_tc<DX, DZ, BWD><<<(unsigned)blocks, kTcThreads, tc_bytes<DX, DZ, BWD>(), s>>>(a, err);
+        k_linattn_tc<DX, DZ, BWD><<<(unsigned)blocks, Shape::kThreads, tc_bytes<DX, DZ, BWD>(), s>>>(a, err);
         e = cudaGetLastError();
         if (e == cudaSuccess) e = attn_carry_pass(a, a.ztiles * (DX * 128 / 4), s);
         if (e != cudaSuccess) return e;
         a.summary = 0;
     }
-    k_linattn_tc<DX, DZ, BWD><<<(unsigned)blocks, kTcThreads, tc_bytes<DX, DZ, BWD>(), s>>>(a, err);
+    k_linattn_tc<DX, DZ, BWD><<<(unsigned)blocks, Shape::kThreads, tc_bytes<DX, DZ, BWD>(), s>>>(a, err);
     return cudaGetLastError();
 }
 
