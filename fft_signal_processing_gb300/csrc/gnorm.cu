@@ -28,7 +28,7 @@ struct GnArgs {
     fft_seq dout, dz;
     float* mean;           // [sequence][group]
     float* rstd;
-    float* records;        // tiles' means and squares, or sums of w and w n: [record][group][3]
+    float* records;        // tiles' origin, sum and squares, or sums of w and w n: [record][group][3]
     float* sums;           // [sequence][group][2]: mean(w) and mean(w n)
     float* parts;          // [part][2][channels]: dweight, dbias
     int64_t rows, tile, tiles;
@@ -37,11 +37,6 @@ struct GnArgs {
 };
 
 __device__ __forceinline__ float silu(float y) { return y * sigmoid(y); }
-// d silu(y) / dy
-__device__ __forceinline__ float dsilu(float y) {
-    const float s = sigmoid(y);
-    return s * fmaf(y, 1.f - s, 1.f);
-}
 
 // A thread's channels: weight and bias in registers.
 template <class T, int VEC>
@@ -63,17 +58,63 @@ __device__ __forceinline__ Pack<T, VEC> load(const fft_seq& s, int64_t at, bool 
     return p;
 }
 
-// out of one value; backward: what reaches y, and dz.
-__device__ __forceinline__ float outcome(const fft_gnorm_desc& d, float y, float z) {
-    const float p = d.silu ? silu(y) : y;
-    return d.z.data ? p * silu(z) : p;
-}
-__device__ __forceinline__ float reaches(const fft_gnorm_desc& d, float y, float z, float g, float* dz) {
-    if (d.z.data) {
-        *dz = g * (d.silu ? silu(y) : y) * dsilu(z);
-        g *= silu(z);
+// What an output is of y and the gate, and (gradients) what of g reaches y and the gate: a pack's values,
+// asked once what there is.
+template <class T, int VEC>
+__device__ __forceinline__ void outcome(const fft_gnorm_desc& d, float (&y)[VEC], const Pack<T, VEC>& z) {
+    if (d.silu) {
+#pragma unroll
+        for (int k = 0; k < VEC; ++k) y[k] = silu(y[k]);
     }
-    return d.silu ? g * dsilu(y) : g;
+    if (d.z.data) {
+#pragma unroll
+        for (int k = 0; k < VEC; ++k) y[k] *= silu(to_f(z.v[k]));
+    }
+}
+// y becomes what reaches it.
+template <class T, int VEC>
+__device__ __forceinline__ void reaches(const fft_gnorm_desc& d, float (&y)[VEC], const Pack<T, VEC>& z, const Pack<T, VEC>& g,
+                                        float (&dz)[VEC]) {
+    float f[VEC];
+#pragma unroll
+    for (int k = 0; k < VEC; ++k) f[k] = to_f(g.v[k]);
+    if (d.z.data) {
+#pragma unroll
+        for (int k = 0; k < VEC; ++k) {
+            const float zk = to_f(z.v[k]), s = sigmoid(zk);
+            dz[k] = f[k] * (s * fmaf(zk, 1.f - s, 1.f));
+            f[k] *= zk * s;
+        }
+    }
+    if (d.silu) {
+#pragma unroll
+        for (int k = 0; k < VEC; ++k) {
+            const float s = sigmoid(y[k]);
+            dz[k] *= y[k] * s;
+            y[k] = f[k] * (s * fmaf(y[k], 1.f - s, 1.f));
+        }
+    } else {
+#pragma unroll
+        for (int k = 0; k < VEC; ++k) {
+            dz[k] *= y[k];
+            y[k] = f[k];
+        }
+    }
+}
+template <class T, int VEC>
+__device__ __forceinline__ Pack<T, VEC> rounded(const float (&v)[VEC]) {
+    Pack<T, VEC> o;
+    if constexpr (VEC == 1) {
+        o.v[0] = from_f<T>(v[0]);
+    } else {
+#pragma unroll
+        for (int k = 0; k < VEC; k += 2) {
+            const Pack<T, 2> p = from_f2<T>(make_float2(v[k], v[k + 1]));
+            o.v[k] = p.v[0];
+            o.v[k + 1] = p.v[1];
+        }
+    }
+    return o;
 }
 
 // ---- sequences of one token -----------------------------------------------------------------
@@ -150,43 +191,42 @@ __global__ void __launch_bounds__(kThreads) k_gn_token(const GnArgs a, int lanes
             }
 #pragma unroll
             for (int j = 0; j < NV; ++j) {
-                Pack<T, VEC> o;
 #pragma unroll
-                for (int k = 0; k < VEC; ++k)
-                    o.v[k] = from_f<T>(outcome(d, fmaf(x[j][k] * rstd, ch[j].w[k], ch[j].b[k]),
-                                               d.z.data ? to_f(pz[j].v[k]) : 0.f));
-                if (in[j]) st_pack<VEC>(static_cast<T*>(a.out.data) + row * a.out.seq_stride + at[j], o);
+                for (int k = 0; k < VEC; ++k) x[j][k] = fmaf(x[j][k] * rstd, ch[j].w[k], ch[j].b[k]);
+                outcome<T, VEC>(d, x[j], pz[j]);
+                if (in[j])
+                    st_pack<VEC>(static_cast<T*>(a.out.data) + row * a.out.seq_stride + at[j], rounded<T, VEC>(x[j]));
             }
         } else {
             float w[NV][VEC], s1 = 0.f, s2 = 0.f;
 #pragma unroll
             for (int j = 0; j < NV; ++j) {
-                Pack<T, VEC> o;
+                float dz[VEC] = {};
 #pragma unroll
                 for (int k = 0; k < VEC; ++k) {
-                    const float n = (to_f(px[j].v[k]) - mean) * rstd;
-                    float dz = 0.f;
-                    const float dy = reaches(d, fmaf(n, ch[j].w[k], ch[j].b[k]), d.z.data ? to_f(pz[j].v[k]) : 0.f,
-                                             to_f(pg[j].v[k]), &dz);
-                    x[j][k] = n;
-                    w[j][k] = in[j] ? dy * ch[j].w[k] : 0.f;
-                    dw[j][k] = fmaf(dy, n, dw[j][k]);
-                    db[j][k] += dy;
-                    s1 += w[j][k];
-                    s2 = fmaf(w[j][k], n, s2);
-                    o.v[k] = from_f<T>(dz);
+                    x[j][k] = (to_f(px[j].v[k]) - mean) * rstd;
+                    w[j][k] = fmaf(x[j][k], ch[j].w[k], ch[j].b[k]);
                 }
-                if (in[j] && d.z.data) st_pack<VEC>(static_cast<T*>(a.dz.data) + row * a.dz.seq_stride + at[j], o);
+                reaches<T, VEC>(d, w[j], pz[j], pg[j], dz);
+#pragma unroll
+                for (int k = 0; k < VEC; ++k) {
+                    dw[j][k] = fmaf(w[j][k], x[j][k], dw[j][k]);
+                    db[j][k] += w[j][k];
+                    w[j][k] = in[j] ? w[j][k] * ch[j].w[k] : 0.f;
+                    s1 += w[j][k];
+                    s2 = fmaf(w[j][k], x[j][k], s2);
+                }
+                if (in[j] && d.z.data)
+                    st_pack<VEC>(static_cast<T*>(a.dz.data) + row * a.dz.seq_stride + at[j], rounded<T, VEC>(dz));
             }
             s1 = lanes_sum(s1, lanes, mask) * inv;
             s2 = lanes_sum(s2, lanes, mask) * inv;
 #pragma unroll
             for (int j = 0; j < NV; ++j) {
-                Pack<T, VEC> o;
 #pragma unroll
-                for (int k = 0; k < VEC; ++k)
-                    o.v[k] = from_f<T>((w[j][k] - fmaf(x[j][k], s2, s1)) * rstd);
-                if (in[j]) st_pack<VEC>(static_cast<T*>(a.out.data) + row * a.out.seq_stride + at[j], o);
+                for (int k = 0; k < VEC; ++k) w[j][k] = (w[j][k] - fmaf(x[j][k], s2, s1)) * rstd;
+                if (in[j])
+                    st_pack<VEC>(static_cast<T*>(a.out.data) + row * a.out.seq_stride + at[j], rounded<T, VEC>(w[j]));
             }
         }
     }
@@ -202,17 +242,6 @@ __global__ void __launch_bounds__(kThreads) k_gn_token(const GnArgs a, int lanes
 }
 
 // ---- longer sequences -----------------------------------------------------------------------
-
-// Count, mean and sum of squares about it.
-struct Moments {
-    float n, mean, m2;
-};
-__device__ __forceinline__ Moments join(const Moments& a, const Moments& b) {
-    const float n = a.n + b.n;
-    if (n == 0.f) return a;
-    const float t = b.n / n, delta = b.mean - a.mean;
-    return {n, fmaf(delta, t, a.mean), a.m2 + b.m2 + delta * delta * a.n * t};
-}
 
 // The block's part of the grid: a tile of tokens, a set of whole groups.  Thread (tx, ty) takes the
 // packs tx, tx + blockDim.x, ... of the set's channels and every blockDim.y-th token.
@@ -244,10 +273,10 @@ __device__ __forceinline__ int64_t record_of(const GnArgs& a, int64_t row, int64
     return a.d.offsets ? tile + q : row * a.tiles + tile;
 }
 
-// Two sums over the threads of each group of the set: f(tx, ty) values lie in red, a warp takes a
-// group.
-template <int N, class Join>
-__device__ __forceinline__ void by_group(const float (*red)[kThreads], int groups, int packs, int single, Join done) {
+// done(group, lane, first tx, count) for every group of the set: a warp takes one, whose values the
+// threads first .. first + count - 1 of every ty have left.
+template <class Join>
+__device__ __forceinline__ void by_group(int groups, int packs, int single, Join done) {
     const int tid = (int)(threadIdx.y * blockDim.x + threadIdx.x), lane = tid & 31, warps = (int)(blockDim.x * blockDim.y) / 32;
     for (int g = tid / 32; g < groups; g += warps) {
         // the threads tx of group g: all of them where a set is one group
@@ -258,56 +287,47 @@ __device__ __forceinline__ void by_group(const float (*red)[kThreads], int group
 
 template <class T, int VEC>
 __global__ void __launch_bounds__(kThreads) k_gn_moments(const GnArgs a) {
-    __shared__ float red[3][kThreads];
+    __shared__ float red[2][kThreads];
     const fft_gnorm_desc& d = a.d;
     const TileAt t = tile_at(a, false);
     const int tx = (int)threadIdx.x, ty = (int)threadIdx.y, bx = (int)blockDim.x, by = (int)blockDim.y;
     const int packs = a.cg / VEC, all = packs * t.groups;
+    const T* base = static_cast<const T*>(d.x.data) + t.row * d.x.seq_stride + (int64_t)t.group0 * a.cg;
     for (int64_t at = t.t0; at < t.t1;) {
         const SeqAt s = part_at(a, t.row, at, t.t1);
-        Moments m = {0.f, 0.f, 0.f};
-        const T* base = static_cast<const T*>(d.x.data) + t.row * d.x.seq_stride + (int64_t)t.group0 * a.cg;
+        float s1 = 0.f, s2 = 0.f;
         for (int p = tx; p < all; p += bx) {
             const T* x = base + p * VEC;
             const float shift = to_f(base[s.begin * d.x.tok_stride + p / packs * a.cg]);
-            float s1[VEC] = {}, s2[VEC] = {};
-            int n = 0;
-#pragma unroll 4
-            for (int64_t i = s.begin + ty; i < s.end; i += by, ++n) {
+            float v1[VEC] = {}, v2[VEC] = {};
+#pragma unroll 8
+            for (int64_t i = s.begin + ty; i < s.end; i += by) {
                 const Pack<T, VEC> v = ld_pack<VEC>(x + i * d.x.tok_stride);
 #pragma unroll
                 for (int k = 0; k < VEC; ++k) {
                     const float e = to_f(v.v[k]) - shift;
-                    s1[k] += e;
-                    s2[k] = fmaf(e, e, s2[k]);
+                    v1[k] += e;
+                    v2[k] = fmaf(e, e, v2[k]);
                 }
             }
-            if (n == 0) continue;
-            const float inv = 1.f / (float)n;
 #pragma unroll
-            for (int k = 0; k < VEC; ++k)  // a square that is no number stays one
-                m = join(m, {(float)n, s1[k] * inv, fmaxf(fmaf(-s1[k] * inv, s1[k], s2[k]), 0.f) + 0.f * s2[k]});
+            for (int k = 0; k < VEC; ++k) s1 += v1[k], s2 += v2[k];
         }
-        const int tid = ty * bx + tx;
-        red[0][tid] = m.n, red[1][tid] = m.mean, red[2][tid] = m.m2;
+        red[0][ty * bx + tx] = s1, red[1][ty * bx + tx] = s2;
         __syncthreads();
-        by_group<3>(red, t.groups, packs, a.each == 1, [&](int g, int lane, int first, int count) {
-            Moments v = {0.f, 0.f, 0.f};
+        by_group(t.groups, packs, a.each == 1, [&](int g, int lane, int first, int count) {
+            float v1 = 0.f, v2 = 0.f;
             for (int i = lane; i < count * by; i += 32) {
                 const int at2 = i / count * bx + first + i % count;
-                v = join(v, {red[0][at2], red[1][at2], red[2][at2]});
+                v1 += red[0][at2], v2 += red[1][at2];
             }
 #pragma unroll
-            for (int o = 1; o < 32; o *= 2) {
-                const Moments w = {__shfl_xor_sync(0xffffffffu, v.n, o), __shfl_xor_sync(0xffffffffu, v.mean, o),
-                                   __shfl_xor_sync(0xffffffffu, v.m2, o)};
-                v = lane & o ? join(w, v) : join(v, w);  // the same order in both lanes
-            }
+            for (int o = 16; o; o >>= 1) v1 += __shfl_xor_sync(0xffffffffu, v1, o), v2 += __shfl_xor_sync(0xffffffffu, v2, o);
             if (lane == 0) {
                 float* r = a.records + (record_of(a, t.row, t.tile, s.q) * d.groups + t.group0 + g) * 3;
-                r[0] = to_f(base[s.begin * d.x.tok_stride + g * a.cg]);  // what the mean is counted from
-                r[1] = v.mean;
-                r[2] = v.m2;
+                r[0] = to_f(base[s.begin * d.x.tok_stride + g * a.cg]);  // what the sums are counted from
+                r[1] = v1;
+                r[2] = v2;
             }
         });
         __syncthreads();
@@ -340,9 +360,10 @@ __global__ void __launch_bounds__(kThreads) k_gn_join(const GnArgs a) {
             } else {
                 const int64_t lo = k * a.tile > begin ? k * a.tile : begin,
                               hi = (k + 1) * a.tile < end ? (k + 1) * a.tile : end;
-                const double c = (double)(hi - lo) * a.cg, all = n + c, delta = (double)r[0] + (double)r[1] - mean;
+                const double c = (double)(hi - lo) * a.cg, all = n + c, own = (double)r[1] / c,
+                             delta = (double)r[0] + own - mean;
                 mean += delta * (c / all);
-                m2 += r[2] + delta * delta * (n * c / all);
+                m2 += ((double)r[2] - own * (double)r[1]) + delta * delta * (n * c / all);
                 n = all;
             }
         }
@@ -370,7 +391,7 @@ __global__ void __launch_bounds__(kThreads) k_gn_join(const GnArgs a) {
         a.sums[i * 2 + 1] = (float)(m2 / count);
     } else {
         a.mean[i] = (float)mean;
-        a.rstd[i] = (float)(1.0 / sqrt(m2 / count + (double)d.eps));
+        a.rstd[i] = (float)(1.0 / sqrt((m2 < 0.0 ? 0.0 : m2) / count + (double)d.eps));
     }
 }
 
@@ -395,26 +416,39 @@ __global__ void __launch_bounds__(kThreads) k_gn_apply(const GnArgs a) {
             const T* go = BWD ? static_cast<const T*>(a.dout.data) + t.row * a.dout.seq_stride + c : nullptr;
             T* out = static_cast<T*>(a.out.data) + t.row * a.out.seq_stride + c;
             T* dz = BWD ? static_cast<T*>(a.dz.data) + t.row * a.dz.seq_stride + c : nullptr;
-#pragma unroll 2
-            for (int64_t i = s.begin + ty; i < s.end; i += by) {
-                const Pack<T, VEC> px = ld_pack<VEC>(x + i * d.x.tok_stride);
-                Pack<T, VEC> pz = {}, pg = {}, o, oz;
-                if (d.z.data) pz = ld_pack<VEC>(z + i * d.z.tok_stride);
-                if (BWD) pg = ld_pack<VEC>(go + i * a.dout.tok_stride);
+            // the rows of four tokens before the first of them is stored (out may be x or z)
+            constexpr int DEEP = 4;
+            for (int64_t i0 = s.begin + ty; i0 < s.end; i0 += DEEP * by) {
+                Pack<T, VEC> px[DEEP], pz[DEEP], pg[DEEP];
 #pragma unroll
-                for (int k = 0; k < VEC; ++k) {
-                    const float n = (to_f(px.v[k]) - mean) * rstd, y = fmaf(n, ch.w[k], ch.b[k]);
-                    if constexpr (BWD) {
-                        float v = 0.f;
-                        const float w = reaches(d, y, to_f(pz.v[k]), to_f(pg.v[k]), &v) * ch.w[k];
-                        o.v[k] = from_f<T>((w - fmaf(n, s2, s1)) * rstd);
-                        oz.v[k] = from_f<T>(v);
-                    } else {
-                        o.v[k] = from_f<T>(outcome(d, y, to_f(pz.v[k])));
-                    }
+                for (int u = 0; u < DEEP; ++u) {
+                    const int64_t i = i0 + u * by;
+                    const bool in = i < s.end;
+                    px[u] = pz[u] = pg[u] = Pack<T, VEC>{};
+                    if (in) px[u] = ld_pack<VEC>(x + i * d.x.tok_stride);
+                    if (in && d.z.data) pz[u] = ld_pack<VEC>(z + i * d.z.tok_stride);
+                    if (BWD && in) pg[u] = ld_pack<VEC>(go + i * a.dout.tok_stride);
                 }
-                st_pack<VEC>(out + i * a.out.tok_stride, o);
-                if (BWD && d.z.data) st_pack<VEC>(dz + i * a.dz.tok_stride, oz);
+#pragma unroll
+                for (int u = 0; u < DEEP; ++u) {
+                    const int64_t i = i0 + u * by;
+                    if (i >= s.end) break;
+                    float n[VEC], y[VEC], dzv[VEC] = {};
+#pragma unroll
+                    for (int k = 0; k < VEC; ++k) {
+                        n[k] = (to_f(px[u].v[k]) - mean) * rstd;
+                        y[k] = fmaf(n[k], ch.w[k], ch.b[k]);
+                    }
+                    if constexpr (BWD) {
+                        reaches<T, VEC>(d, y, pz[u], pg[u], dzv);
+#pragma unroll
+                        for (int k = 0; k < VEC; ++k) y[k] = (y[k] * ch.w[k] - fmaf(n[k], s2, s1)) * rstd;
+                    } else {
+                        outcome<T, VEC>(d, y, pz[u]);
+                    }
+                    st_pack<VEC>(out + i * a.out.tok_stride, rounded<T, VEC>(y));
+                    if (BWD && d.z.data) st_pack<VEC>(dz + i * a.dz.tok_stride, rounded<T, VEC>(dzv));
+                }
             }
         }
         at = s.end;
@@ -448,28 +482,32 @@ __global__ void __launch_bounds__(kThreads) k_gn_sums(const GnArgs a) {
                 const T* x = static_cast<const T*>(d.x.data) + t.row * d.x.seq_stride + c;
                 const T* z = static_cast<const T*>(d.z.data) + t.row * d.z.seq_stride + c;
                 const T* go = static_cast<const T*>(a.dout.data) + t.row * a.dout.seq_stride + c;
-#pragma unroll 2
+#pragma unroll 4
                 for (int64_t i = s.begin + ty; i < s.end; i += by) {
                     const Pack<T, VEC> px = ld_pack<VEC>(x + i * d.x.tok_stride);
                     Pack<T, VEC> pz = {};
                     if (d.z.data) pz = ld_pack<VEC>(z + i * d.z.tok_stride);
                     const Pack<T, VEC> pg = ld_pack<VEC>(go + i * a.dout.tok_stride);
+                    float n[VEC], y[VEC], dzv[VEC] = {};
 #pragma unroll
                     for (int k = 0; k < VEC; ++k) {
-                        const float n = (to_f(px.v[k]) - mean) * rstd;
-                        float v;
-                        const float dy = reaches(d, fmaf(n, ch.w[k], ch.b[k]), to_f(pz.v[k]), to_f(pg.v[k]), &v);
-                        const float dn = dy * n;
+                        n[k] = (to_f(px.v[k]) - mean) * rstd;
+                        y[k] = fmaf(n[k], ch.w[k], ch.b[k]);
+                    }
+                    reaches<T, VEC>(d, y, pz, pg, dzv);
+#pragma unroll
+                    for (int k = 0; k < VEC; ++k) {
+                        const float dn = y[k] * n[k];
                         dw[k] += dn;
-                        db[k] += dy;
-                        s1 = fmaf(dy, ch.w[k], s1);
+                        db[k] += y[k];
+                        s1 = fmaf(y[k], ch.w[k], s1);
                         s2 = fmaf(dn, ch.w[k], s2);
                     }
                 }
             }
             red[0][tid] = s1, red[1][tid] = s2;
             __syncthreads();
-            by_group<2>(red, t.groups, packs, a.each == 1, [&](int g, int lane, int first, int count) {
+            by_group(t.groups, packs, a.each == 1, [&](int g, int lane, int first, int count) {
                 float v1 = 0.f, v2 = 0.f;
                 for (int i = lane; i < count * by; i += 32) {
                     const int at2 = i / count * bx + first + i % count;
@@ -562,11 +600,11 @@ int64_t token_step(const fft_gnorm_desc& d, int lanes, bool backward) {
     const int64_t step = subs / d.groups;
     return step < 1 ? 1 : (step > d.nseq ? d.nseq : step);
 }
-// Tokens of a tile: as many as leave every SM eight blocks, 16 to 128.
+// Tokens of a tile: as many as leave every SM four blocks, 16 to 128.
 int64_t tile_of(const fft_gnorm_desc& d) {
     const int64_t rows = d.offsets ? 1 : d.nseq;
     int64_t tile = 128;
-    while (tile > 16 && rows * ((d.length + tile - 1) / tile) * ((d.channels + 2047) / 2048) < (int64_t)num_sms() * 8) tile /= 2;
+    while (tile > 16 && rows * ((d.length + tile - 1) / tile) * ((d.channels + 2047) / 2048) < (int64_t)num_sms() * 4) tile /= 2;
     return tile;
 }
 int64_t gnorm_layout(const fft_gnorm_desc& d, bool backward, GnArgs* a, char* w) {

@@ -23,16 +23,18 @@ struct AttnStepArgs {
 };
 
 // A block takes 32 columns of one head's state: VEC columns per thread, so 32 / VEC lanes hold a row
-// and the rows are dealt to groups of lanes, four loads of each under way at once.
+// and the rows are dealt to groups of lanes, eight loads of each under way at once.  Bound by the
+// states' bytes for many sequences and by latency for one; queries and keys go through shared memory,
+// which leaves registers for eight blocks to an SM.
 template <class T, int VEC>
-__global__ void __launch_bounds__(kStepThreads) k_linattn_step(const AttnStepArgs a) {
-    constexpr int LANES = kStepCols / VEC, GROUPS = kStepThreads / LANES, DEEP = VEC == 4 ? 8 : 4;
-    __shared__ float red[GROUPS][kStepCols + 1];
+__global__ void __launch_bounds__(kStepThreads, 8) k_linattn_step(const AttnStepArgs a) {
+    constexpr int LANES = kStepCols / VEC, GROUPS = kStepThreads / LANES, DEEP = 8;
+    __shared__ float red[GROUPS][kStepCols + 1], qk[2][kAttnMaxDim];
     const int lane = (int)threadIdx.x % LANES, group = (int)threadIdx.x / LANES;
-    int64_t b = blockIdx.x;
-    const int ct = (int)(b % a.ctiles);
-    b /= a.ctiles;
-    const int64_t h = b % a.d.heads, q = b / a.d.heads, g = h / (a.d.heads / a.d.groups);
+    unsigned b = blockIdx.x;
+    const int ct = (int)(b % (unsigned)a.ctiles);
+    b /= (unsigned)a.ctiles;
+    const int64_t h = b % (unsigned)a.d.heads, q = b / (unsigned)a.d.heads, g = h / (a.d.heads / a.d.groups);
     const int dk = (int)a.d.dk, dv = (int)a.d.dv, c = ct * kStepCols + lane * VEC;
     const bool in = c < dv;
     const int64_t from = a.slots ? a.slots[q] : q, to = a.slots_out ? a.slots_out[q] : from;
@@ -41,36 +43,34 @@ __global__ void __launch_bounds__(kStepThreads) k_linattn_step(const AttnStepArg
     const T* kp = static_cast<const T*>(a.d.k.data) + q * a.d.k.seq_stride + g * a.d.k.head_stride;
     const T* vp = static_cast<const T*>(a.d.v.data) + q * a.d.v.seq_stride + h * a.d.v.head_stride + c;
     const float gl = to_f(static_cast<const T*>(a.d.decay.data)[q * a.d.decay.seq_stride + h]);
-    float y[VEC] = {};
-    if (live) {
-        const float e = ex2((gl > 0.f ? 0.f : (gl < -200.f ? -200.f : gl)) * kLog2e);
-        const int64_t per = (int64_t)dk * dv;
-        const float* src = a.state + (from * a.d.heads + h) * per + c;
-        float* dst = a.state + (to * a.d.heads + h) * per + c;
-        float v[VEC];
+    const int64_t per = (int64_t)dk * dv;
+    const float* src = a.state + (live ? (from * a.d.heads + h) * per + c : 0);
+    float* dst = a.state + (live ? (to * a.d.heads + h) * per + c : 0);
+    Pack<float, VEC> s[DEEP];
+    auto fetch = [&](int r0) {
 #pragma unroll
-        for (int k = 0; k < VEC; ++k) v[k] = in ? to_f(vp[k]) : 0.f;
-        for (int r0 = group; r0 < dk; r0 += GROUPS * DEEP) {
-            Pack<float, VEC> s[DEEP];
-            float qv[DEEP], kv[DEEP];
+        for (int i = 0; i < DEEP; ++i)
+            if (live && in && r0 + i * GROUPS < dk) s[i] = ld_pack<VEC>(src + (r0 + i * GROUPS) * dv);
+    };
+    fetch(group);
+    for (int i = (int)threadIdx.x; i < dk; i += kStepThreads) qk[0][i] = to_f(qp[i]), qk[1][i] = to_f(kp[i]);
+    float v[VEC], y[VEC] = {};
 #pragma unroll
-            for (int i = 0; i < DEEP; ++i) {
-                const int r = r0 + i * GROUPS;
-                if (r < dk && in) s[i] = ld_pack<VEC>(src + (int64_t)r * dv);
-                qv[i] = r < dk ? to_f(qp[r]) : 0.f;
-                kv[i] = r < dk ? to_f(kp[r]) : 0.f;
-            }
+    for (int k = 0; k < VEC; ++k) v[k] = in ? to_f(vp[k]) : 0.f;
+    const float e = ex2((gl > 0.f ? 0.f : (gl < -200.f ? -200.f : gl)) * kLog2e);
+    __syncthreads();
+    for (int r0 = group; r0 < dk; r0 += GROUPS * DEEP) {
+        if (r0 != group) fetch(r0);
 #pragma unroll
-            for (int i = 0; i < DEEP; ++i) {
-                const int r = r0 + i * GROUPS;
-                if (r < dk && in) {
+        for (int i = 0; i < DEEP; ++i) {
+            const int r = r0 + i * GROUPS;
+            if (live && in && r < dk) {
 #pragma unroll
-                    for (int k = 0; k < VEC; ++k) {
-                        s[i].v[k] = fmaf(e, s[i].v[k], kv[i] * v[k]);
-                        y[k] = fmaf(qv[i], s[i].v[k], y[k]);
-                    }
-                    st_pack<VEC>(dst + (int64_t)r * dv, s[i]);
+                for (int k = 0; k < VEC; ++k) {
+                    s[i].v[k] = fmaf(e, s[i].v[k], qk[1][r] * v[k]);
+                    y[k] = fmaf(qk[0][r], s[i].v[k], y[k]);
                 }
+                st_pack<VEC>(dst + r * dv, s[i]);
             }
         }
     }
