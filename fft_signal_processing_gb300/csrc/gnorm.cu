@@ -36,86 +36,112 @@ struct GnArgs {
     int backward;
 };
 
-__device__ __forceinline__ float silu(float y) { return y * sigmoid(y); }
-
-// A thread's channels: weight and bias in registers.
-template <class T, int VEC>
-struct Channel {
-    float w[VEC], b[VEC];
-    __device__ __forceinline__ void load(const fft_gnorm_desc& d, int64_t c, bool in) {
-        const int f32 = d.param_dtype == FFT_F32;
-#pragma unroll
-        for (int k = 0; k < VEC; ++k) {
-            w[k] = in ? (d.weight ? ld_param<T>(d.weight, c + k, f32) : 1.f) : 0.f;
-            b[k] = in && d.bias ? ld_param<T>(d.bias, c + k, f32) : 0.f;
-        }
-    }
+// VEC values as pairs, two float32 operations to an instruction (of one value: the first of a pair
+// whose second is 0 throughout).
+template <int VEC>
+struct Values {
+    static constexpr int N = (VEC + 1) / 2;
+    float2 v[N];
 };
 template <class T, int VEC>
-__device__ __forceinline__ Pack<T, VEC> load(const fft_seq& s, int64_t at, bool in) {
-    Pack<T, VEC> p = {};
-    if (in) p = ld_pack<VEC>(static_cast<const T*>(s.data) + at);
-    return p;
-}
-
-// What an output is of y and the gate, and (gradients) what of g reaches y and the gate: a pack's values,
-// asked once what there is.
-template <class T, int VEC>
-__device__ __forceinline__ void outcome(const fft_gnorm_desc& d, float (&y)[VEC], const Pack<T, VEC>& z) {
-    if (d.silu) {
+__device__ __forceinline__ Values<VEC> unpack(const Pack<T, VEC>& p) {
+    Values<VEC> x;
 #pragma unroll
-        for (int k = 0; k < VEC; ++k) y[k] = silu(y[k]);
-    }
-    if (d.z.data) {
-#pragma unroll
-        for (int k = 0; k < VEC; ++k) y[k] *= silu(to_f(z.v[k]));
-    }
-}
-// y becomes what reaches it.
-template <class T, int VEC>
-__device__ __forceinline__ void reaches(const fft_gnorm_desc& d, float (&y)[VEC], const Pack<T, VEC>& z, const Pack<T, VEC>& g,
-                                        float (&dz)[VEC]) {
-    float f[VEC];
-#pragma unroll
-    for (int k = 0; k < VEC; ++k) f[k] = to_f(g.v[k]);
-    if (d.z.data) {
-#pragma unroll
-        for (int k = 0; k < VEC; ++k) {
-            const float zk = to_f(z.v[k]), s = sigmoid(zk);
-            dz[k] = f[k] * (s * fmaf(zk, 1.f - s, 1.f));
-            f[k] *= zk * s;
-        }
-    }
-    if (d.silu) {
-#pragma unroll
-        for (int k = 0; k < VEC; ++k) {
-            const float s = sigmoid(y[k]);
-            dz[k] *= y[k] * s;
-            y[k] = f[k] * (s * fmaf(y[k], 1.f - s, 1.f));
-        }
-    } else {
-#pragma unroll
-        for (int k = 0; k < VEC; ++k) {
-            dz[k] *= y[k];
-            y[k] = f[k];
-        }
-    }
+    for (int k = 0; k < VEC; k += 2) x.v[k / 2] = make_float2(to_f(p.v[k]), VEC > 1 ? to_f(p.v[k + (VEC > 1)]) : 0.f);
+    return x;
 }
 template <class T, int VEC>
-__device__ __forceinline__ Pack<T, VEC> rounded(const float (&v)[VEC]) {
+__device__ __forceinline__ Pack<T, VEC> rounded(const Values<VEC>& x) {
     Pack<T, VEC> o;
     if constexpr (VEC == 1) {
-        o.v[0] = from_f<T>(v[0]);
+        o.v[0] = from_f<T>(x.v[0].x);
     } else {
 #pragma unroll
         for (int k = 0; k < VEC; k += 2) {
-            const Pack<T, 2> p = from_f2<T>(make_float2(v[k], v[k + 1]));
+            const Pack<T, 2> p = from_f2<T>(x.v[k / 2]);
             o.v[k] = p.v[0];
             o.v[k + 1] = p.v[1];
         }
     }
     return o;
 }
+
+// A thread's channels: weight and bias in registers.
+template <class T, int VEC>
+struct Channel {
+    Values<VEC> w, b;
+    __device__ __forceinline__ void load(const fft_gnorm_desc& d, int64_t c, bool in) {
+        const int f32 = d.param_dtype == FFT_F32;
+#pragma unroll
+        for (int k = 0; k < Values<VEC>::N; ++k) w.v[k] = b.v[k] = splat(0.f);
+#pragma unroll
+        for (int k = 0; k < VEC; ++k) {
+            (k & 1 ? w.v[k / 2].y : w.v[k / 2].x) = in ? (d.weight ? ld_param<T>(d.weight, c + k, f32) : 1.f) : 0.f;
+            (k & 1 ? b.v[k / 2].y : b.v[k / 2].x) = in && d.bias ? ld_param<T>(d.bias, c + k, f32) : 0.f;
+        }
+    }
+};
+template <class T, int VEC>
+__device__ __forceinline__ Pack<T, VEC> load(const T* p, bool in) {
+    Pack<T, VEC> v = {};
+    if (in) v = ld_pack<VEC>(p);
+    return v;
+}
+
+// Sigmoids of a pair; of a single value only the first.
+template <int VEC>
+__device__ __forceinline__ float2 sigmoids(float2 v) {
+    if constexpr (VEC == 1) return make_float2(sigmoid(v.x), 0.f);
+    return sigmoid2(v);
+}
+// What an output is of y and the gate, and (gradients) what of g reaches y and the gate: a pack's values,
+// asked once what there is.
+template <int VEC>
+__device__ __forceinline__ void outcome(const fft_gnorm_desc& d, Values<VEC>& y, const Values<VEC>& z) {
+    if (d.silu) {
+#pragma unroll
+        for (int k = 0; k < y.N; ++k) y.v[k] = mul2(y.v[k], sigmoids<VEC>(y.v[k]));
+    }
+    if (d.z.data) {
+#pragma unroll
+        for (int k = 0; k < y.N; ++k) y.v[k] = mul2(y.v[k], mul2(z.v[k], sigmoids<VEC>(z.v[k])));
+    }
+}
+// The slope of SiLU at y, s being its sigmoid.
+__device__ __forceinline__ float2 slope(float2 y, float2 s) {
+    return mul2(s, fma2(y, fma2(s, splat(-1.f), splat(1.f)), splat(1.f)));
+}
+// y becomes what reaches it; g is used up.
+template <int VEC>
+__device__ __forceinline__ void reaches(const fft_gnorm_desc& d, Values<VEC>& y, const Values<VEC>& z, Values<VEC>& g,
+                                        Values<VEC>& dz) {
+    if (d.z.data) {
+#pragma unroll
+        for (int k = 0; k < y.N; ++k) {
+            const float2 s = sigmoids<VEC>(z.v[k]);
+            dz.v[k] = mul2(g.v[k], slope(z.v[k], s));
+            g.v[k] = mul2(g.v[k], mul2(z.v[k], s));
+        }
+    } else {
+#pragma unroll
+        for (int k = 0; k < y.N; ++k) dz.v[k] = splat(0.f);
+    }
+    if (d.silu) {
+#pragma unroll
+        for (int k = 0; k < y.N; ++k) {
+            const float2 s = sigmoids<VEC>(y.v[k]);
+            dz.v[k] = mul2(dz.v[k], mul2(y.v[k], s));
+            y.v[k] = mul2(g.v[k], slope(y.v[k], s));
+        }
+    } else {
+#pragma unroll
+        for (int k = 0; k < y.N; ++k) {
+            dz.v[k] = mul2(dz.v[k], y.v[k]);
+            y.v[k] = g.v[k];
+        }
+    }
+}
+__device__ __forceinline__ float2 minus(float v) { return splat(-v); }
 
 // ---- sequences of one token -----------------------------------------------------------------
 
@@ -125,9 +151,14 @@ __device__ __forceinline__ float lanes_sum(float v, int lanes, unsigned mask) {
 }
 
 // `lanes` threads hold a group: NV packs of VEC values each.  They take the rows row0, row0 + step,
-// ... , the next row's values under way.
+// ... ; of 16-byte packs the rows ahead wait in shared memory, where a thread reads only what it has
+// copied itself, so that the ring needs neither a barrier nor registers (of single values the next
+// row's are loaded ahead).  Blocks of an SM by the registers of so many values.
+template <int VEC, int NV, bool BWD> constexpr int kGnBlocks = NV * VEC <= 8 && VEC > 1 ? (BWD ? 2 : 4) : (VEC > 1 && !BWD ? 2 : 1);
+constexpr int kGnAhead = 4;  // rows of the ring
 template <class T, int VEC, int NV, bool BWD>
-__global__ void __launch_bounds__(kThreads) k_gn_token(const GnArgs a, int lanes, int64_t step) {
+__global__ void __launch_bounds__(kThreads, kGnBlocks<VEC, NV, BWD>) k_gn_token(const GnArgs a, int lanes, int64_t step) {
+    constexpr int P = Values<VEC>::N;
     const fft_gnorm_desc& d = a.d;
     const int tid = (int)threadIdx.x, lane = tid & (lanes - 1);
     const unsigned mask = lanes == 32 ? 0xffffffffu : ((1u << lanes) - 1u) << ((tid & 31) & ~(lanes - 1));
@@ -135,109 +166,157 @@ __global__ void __launch_bounds__(kThreads) k_gn_token(const GnArgs a, int lanes
     const int64_t group = sub % d.groups, row0 = sub / d.groups;
     if (row0 >= step) return;
     Channel<T, VEC> ch[NV];
-    int64_t at[NV];
+    const int64_t c0 = group * a.cg + lane * VEC;
+    const int hop = lanes * VEC;  // from one pack of the thread to the next
     bool in[NV];
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-        const int c = (lane + j * lanes) * VEC;
-        in[j] = c < a.cg;
-        at[j] = group * a.cg + c;
-        ch[j].load(d, at[j], in[j]);
+        in[j] = lane * VEC + j * hop < a.cg;
+        ch[j].load(d, c0 + j * hop, in[j]);
     }
-    float dw[BWD ? NV : 1][VEC] = {}, db[BWD ? NV : 1][VEC] = {};
-    Pack<T, VEC> nx[NV], nz[NV], ng[BWD ? NV : 1];
-    float nmean = 0.f, nrstd = 0.f;
-    auto fetch = [&](int64_t row) {
-        const bool live = row < a.rows;
+    Values<VEC> dw[BWD ? NV : 1], db[BWD ? NV : 1];
+    if (BWD) {
+#pragma unroll
+        for (int j = 0; j < NV; ++j)
+#pragma unroll
+            for (int k = 0; k < P; ++k) dw[j].v[k] = db[j].v[k] = splat(0.f);
+    }
+    const bool gate = d.z.data;
+    const T* x = static_cast<const T*>(d.x.data) + row0 * d.x.seq_stride + c0;
+    const T* z = static_cast<const T*>(d.z.data) + row0 * d.z.seq_stride + c0;
+    const T* g = static_cast<const T*>(a.dout.data) + row0 * a.dout.seq_stride + c0;
+    T* out = static_cast<T*>(a.out.data) + row0 * a.out.seq_stride + c0;
+    T* oz = static_cast<T*>(a.dz.data) + row0 * a.dz.seq_stride + c0;
+    float* mp = a.mean + row0 * d.groups + group;
+    float* rp = a.rstd + row0 * d.groups + group;
+    const int64_t hx = step * d.x.seq_stride, hz = step * d.z.seq_stride, hg = step * a.dout.seq_stride,
+                  ho = step * a.out.seq_stride, hd = step * a.dz.seq_stride, hm = step * d.groups;
+    constexpr bool RING = VEC > 1;
+    constexpr int PIECES = NV * (BWD ? 3 : 2);
+    extern __shared__ uint4 ring[];
+    Pack<T, VEC> now[RING ? 1 : 3][RING ? 1 : NV];
+    auto piece = [&](int stage, int k) { return ring + (stage * PIECES + k) * kThreads + tid; };
+    // the next row of those that come, whether there is one or not
+    auto fetch = [&](int stage, bool live) {
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
-            nx[j] = load<T, VEC>(d.x, row * d.x.seq_stride + at[j], live && in[j]);
-            if (d.z.data) nz[j] = load<T, VEC>(d.z, row * d.z.seq_stride + at[j], live && in[j]);
-            if (BWD) ng[j] = load<T, VEC>(a.dout, row * a.dout.seq_stride + at[j], live && in[j]);
+            const bool there = live && in[j];
+            if constexpr (RING) {
+                copy16(piece(stage, j), there ? x + j * hop : static_cast<const T*>(d.x.data), there);
+                if (gate) copy16(piece(stage, NV + j), there ? z + j * hop : static_cast<const T*>(d.z.data), there);
+                if (BWD) copy16(piece(stage, 2 * NV + j), there ? g + j * hop : static_cast<const T*>(a.dout.data), there);
+            } else {
+                now[0][j] = load<T, VEC>(x + j * hop, there);
+                if (gate) now[1][j] = load<T, VEC>(z + j * hop, there);
+                if (BWD) now[2][j] = load<T, VEC>(g + j * hop, there);
+            }
         }
-        if (BWD && live) nmean = a.mean[row * d.groups + group], nrstd = a.rstd[row * d.groups + group];
+        if (RING) copy_commit();
+        x += hx;
+        if (gate) z += hz;
+        if (BWD) g += hg;
     };
-    fetch(row0);
+    if constexpr (RING) {
+        for (int k = 0; k < kGnAhead - 1; ++k) fetch(k, row0 + k * step < a.rows);
+    } else {
+        fetch(0, true);
+    }
+    float nmean = 0.f, nrstd = 0.f;
+    if (BWD) nmean = *mp, nrstd = *rp;
     const float inv = 1.f / (float)a.cg;
+    int stage = 0;
     for (int64_t row = row0; row < a.rows; row += step) {
-        Pack<T, VEC> px[NV], pz[NV], pg[BWD ? NV : 1];
+        Values<VEC> v[NV], zv[NV], gv[BWD ? NV : 1];
+        if constexpr (RING) {
+            fetch((stage + kGnAhead - 1) % kGnAhead, row + (kGnAhead - 1) * step < a.rows);
+            copy_wait<kGnAhead - 1>();
+        }
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
-            px[j] = nx[j];
-            if (d.z.data) pz[j] = nz[j];
-            if (BWD) pg[j] = ng[j];
+            auto take = [&](int k) {
+                if constexpr (RING) return *reinterpret_cast<const Pack<T, VEC>*>(piece(stage, k * NV + j));
+                else return now[k][j];
+            };
+            v[j] = unpack<T, VEC>(take(0));
+            zv[j] = unpack<T, VEC>(gate ? take(1) : Pack<T, VEC>{});
+            if (BWD) gv[j] = unpack<T, VEC>(take(2));
         }
+        stage = (stage + 1) % kGnAhead;
         float mean = nmean, rstd = nrstd;
-        fetch(row + step);
-        float x[NV][VEC];
+        if (!RING) fetch(0, row + step < a.rows);
+        if (BWD && row + step < a.rows) mp += hm, rp += hm, nmean = *mp, nrstd = *rp;
         if constexpr (!BWD) {
-            float sum = 0.f, sq = 0.f;
+            float2 sum = splat(0.f), sq = splat(0.f);
 #pragma unroll
             for (int j = 0; j < NV; ++j)
 #pragma unroll
-                for (int k = 0; k < VEC; ++k) x[j][k] = to_f(px[j].v[k]), sum += x[j][k];
-            mean = lanes_sum(sum, lanes, mask) * inv;
+                for (int k = 0; k < P; ++k) sum = add2(sum, v[j].v[k]);
+            mean = lanes_sum(sum.x + sum.y, lanes, mask) * inv;
 #pragma unroll
             for (int j = 0; j < NV; ++j)
 #pragma unroll
-                for (int k = 0; k < VEC; ++k) {
-                    x[j][k] = in[j] ? x[j][k] - mean : 0.f;
-                    sq = fmaf(x[j][k], x[j][k], sq);
+                for (int k = 0; k < P; ++k) {
+                    v[j].v[k] = in[j] ? add2(v[j].v[k], minus(mean)) : splat(0.f);
+                    if (VEC == 1) v[j].v[k].y = 0.f;
+                    sq = fma2(v[j].v[k], v[j].v[k], sq);
                 }
-            rstd = rsqrtf(fmaf(lanes_sum(sq, lanes, mask), inv, d.eps));
-            if (lane == 0) {
-                a.mean[row * d.groups + group] = mean;
-                a.rstd[row * d.groups + group] = rstd;
-            }
+            rstd = rsqrtf(fmaf(lanes_sum(sq.x + sq.y, lanes, mask), inv, d.eps));
+            if (lane == 0) *mp = mean, *rp = rstd;
 #pragma unroll
             for (int j = 0; j < NV; ++j) {
 #pragma unroll
-                for (int k = 0; k < VEC; ++k) x[j][k] = fmaf(x[j][k] * rstd, ch[j].w[k], ch[j].b[k]);
-                outcome<T, VEC>(d, x[j], pz[j]);
-                if (in[j])
-                    st_pack<VEC>(static_cast<T*>(a.out.data) + row * a.out.seq_stride + at[j], rounded<T, VEC>(x[j]));
+                for (int k = 0; k < P; ++k) v[j].v[k] = fma2(mul2(v[j].v[k], splat(rstd)), ch[j].w.v[k], ch[j].b.v[k]);
+                outcome<VEC>(d, v[j], zv[j]);
+                if (in[j]) st_pack<VEC>(out + j * hop, rounded<T, VEC>(v[j]));
             }
+            mp += hm, rp += hm;
         } else {
-            float w[NV][VEC], s1 = 0.f, s2 = 0.f;
+            float2 s1 = splat(0.f), s2 = splat(0.f);
+            Values<VEC> w[NV];
 #pragma unroll
             for (int j = 0; j < NV; ++j) {
-                float dz[VEC] = {};
+                Values<VEC> dz;
 #pragma unroll
-                for (int k = 0; k < VEC; ++k) {
-                    x[j][k] = (to_f(px[j].v[k]) - mean) * rstd;
-                    w[j][k] = fmaf(x[j][k], ch[j].w[k], ch[j].b[k]);
+                for (int k = 0; k < P; ++k) {
+                    v[j].v[k] = mul2(add2(v[j].v[k], minus(mean)), splat(rstd));
+                    if (VEC == 1) v[j].v[k].y = 0.f;
+                    w[j].v[k] = fma2(v[j].v[k], ch[j].w.v[k], ch[j].b.v[k]);
                 }
-                reaches<T, VEC>(d, w[j], pz[j], pg[j], dz);
+                reaches<VEC>(d, w[j], zv[j], gv[j], dz);
+                if (in[j] && gate) st_pack<VEC>(oz + j * hop, rounded<T, VEC>(dz));
 #pragma unroll
-                for (int k = 0; k < VEC; ++k) {
-                    dw[j][k] = fmaf(w[j][k], x[j][k], dw[j][k]);
-                    db[j][k] += w[j][k];
-                    w[j][k] = in[j] ? w[j][k] * ch[j].w[k] : 0.f;
-                    s1 += w[j][k];
-                    s2 = fmaf(w[j][k], x[j][k], s2);
+                for (int k = 0; k < P; ++k) {
+                    dw[j].v[k] = fma2(w[j].v[k], v[j].v[k], dw[j].v[k]);
+                    db[j].v[k] = add2(w[j].v[k], db[j].v[k]);
+                    w[j].v[k] = in[j] ? mul2(w[j].v[k], ch[j].w.v[k]) : splat(0.f);
+                    s1 = add2(s1, w[j].v[k]);
+                    s2 = fma2(w[j].v[k], v[j].v[k], s2);
                 }
-                if (in[j] && d.z.data)
-                    st_pack<VEC>(static_cast<T*>(a.dz.data) + row * a.dz.seq_stride + at[j], rounded<T, VEC>(dz));
             }
-            s1 = lanes_sum(s1, lanes, mask) * inv;
-            s2 = lanes_sum(s2, lanes, mask) * inv;
+            const float m1 = lanes_sum(s1.x + s1.y, lanes, mask) * inv, m2 = lanes_sum(s2.x + s2.y, lanes, mask) * inv;
 #pragma unroll
             for (int j = 0; j < NV; ++j) {
 #pragma unroll
-                for (int k = 0; k < VEC; ++k) w[j][k] = (w[j][k] - fmaf(x[j][k], s2, s1)) * rstd;
-                if (in[j])
-                    st_pack<VEC>(static_cast<T*>(a.out.data) + row * a.out.seq_stride + at[j], rounded<T, VEC>(w[j]));
+                for (int k = 0; k < P; ++k)
+                    w[j].v[k] = mul2(add2(w[j].v[k], fma2(v[j].v[k], minus(m2), minus(m1))), splat(rstd));
+                if (in[j]) st_pack<VEC>(out + j * hop, rounded<T, VEC>(w[j]));
             }
+            if (gate) oz += hd;
         }
+        out += ho;
     }
+    copy_wait<0>();  // no copy under way at the end
     if constexpr (BWD) {
         if (!a.parts) return;
-        float* p = a.parts + row0 * 2 * d.channels;
+        float* p = a.parts + row0 * 2 * d.channels + c0;
 #pragma unroll
         for (int j = 0; j < NV; ++j)
 #pragma unroll
             for (int k = 0; k < VEC; ++k)
-                if (in[j]) p[at[j] + k] = dw[j][k], p[d.channels + at[j] + k] = db[j][k];
+                if (in[j]) {
+                    p[j * hop + k] = k & 1 ? dw[j].v[k / 2].y : dw[j].v[k / 2].x;
+                    p[d.channels + j * hop + k] = k & 1 ? db[j].v[k / 2].y : db[j].v[k / 2].x;
+                }
     }
 }
 
@@ -299,19 +378,19 @@ __global__ void __launch_bounds__(kThreads) k_gn_moments(const GnArgs a) {
         for (int p = tx; p < all; p += bx) {
             const T* x = base + p * VEC;
             const float shift = to_f(base[s.begin * d.x.tok_stride + p / packs * a.cg]);
-            float v1[VEC] = {}, v2[VEC] = {};
+            float2 v1 = splat(0.f), v2 = splat(0.f);
 #pragma unroll 8
             for (int64_t i = s.begin + ty; i < s.end; i += by) {
-                const Pack<T, VEC> v = ld_pack<VEC>(x + i * d.x.tok_stride);
+                const Values<VEC> v = unpack<T, VEC>(ld_pack<VEC>(x + i * d.x.tok_stride));
 #pragma unroll
-                for (int k = 0; k < VEC; ++k) {
-                    const float e = to_f(v.v[k]) - shift;
-                    v1[k] += e;
-                    v2[k] = fmaf(e, e, v2[k]);
+                for (int k = 0; k < v.N; ++k) {
+                    float2 e = add2(v.v[k], minus(shift));
+                    if (VEC == 1) e.y = 0.f;
+                    v1 = add2(v1, e);
+                    v2 = fma2(e, e, v2);
                 }
             }
-#pragma unroll
-            for (int k = 0; k < VEC; ++k) s1 += v1[k], s2 += v2[k];
+            s1 += v1.x + v1.y, s2 += v2.x + v2.y;
         }
         red[0][ty * bx + tx] = s1, red[1][ty * bx + tx] = s2;
         __syncthreads();
@@ -349,59 +428,65 @@ __global__ void __launch_bounds__(kThreads) k_gn_join(const GnArgs a) {
         begin = begin < 0 ? 0 : (begin > d.length ? d.length : begin);
         end = end > d.length ? d.length : end;
     }
-    double n = 0.0, mean = 0.0, m2 = 0.0;
+    // sums about the origin of the sequence's first tile: few operations, since those in 64 bits are slow
+    double t1 = 0.0, t2 = 0.0;
+    float origin = 0.f;
     if (end > begin) {
         const int64_t first = begin / a.tile, last = (end - 1) / a.tile;
+        if (!BWD) origin = a.records[(record_of(a, q, first, q) * d.groups + g) * 3];
         for (int64_t k = first + lane; k <= last; k += 32) {
             const float* r = a.records + (record_of(a, q, k, q) * d.groups + g) * 3;
             if constexpr (BWD) {
-                mean += r[0];
-                m2 += r[1];
+                t1 += r[0];
+                t2 += r[1];
             } else {
                 const int64_t lo = k * a.tile > begin ? k * a.tile : begin,
                               hi = (k + 1) * a.tile < end ? (k + 1) * a.tile : end;
-                const double c = (double)(hi - lo) * a.cg, all = n + c, own = (double)r[1] / c,
-                             delta = (double)r[0] + own - mean;
-                mean += delta * (c / all);
-                m2 += ((double)r[2] - own * (double)r[1]) + delta * delta * (n * c / all);
-                n = all;
+                const double c = (double)((int)(hi - lo) * (int64_t)a.cg), o = (double)r[0] - (double)origin;
+                t1 += fma(c, o, (double)r[1]);
+                t2 += fma(fma(c, o, 2.0 * (double)r[1]), o, (double)r[2]);
             }
         }
     }
 #pragma unroll
     for (int o = 1; o < 32; o *= 2) {
-        const double bn = __shfl_xor_sync(0xffffffffu, n, o), bm = __shfl_xor_sync(0xffffffffu, mean, o),
-                     b2 = __shfl_xor_sync(0xffffffffu, m2, o);
-        if constexpr (BWD) {
-            mean += bm;
-            m2 += b2;
-        } else {
-            const double all = n + bn, delta = bm - mean;
-            if (all > 0.0) {
-                m2 += b2 + delta * delta * (n * bn / all);
-                mean += delta * (bn / all);
-            }
-            n = all;
-        }
+        t1 += __shfl_xor_sync(0xffffffffu, t1, o);
+        t2 += __shfl_xor_sync(0xffffffffu, t2, o);
     }
     if (lane) return;
     const double count = end > begin ? (double)(end - begin) * a.cg : 1.0;
     if constexpr (BWD) {
-        a.sums[i * 2] = (float)(mean / count);
-        a.sums[i * 2 + 1] = (float)(m2 / count);
+        a.sums[i * 2] = (float)(t1 / count);
+        a.sums[i * 2 + 1] = (float)(t2 / count);
     } else {
-        a.mean[i] = (float)mean;
-        a.rstd[i] = (float)(1.0 / sqrt((m2 < 0.0 ? 0.0 : m2) / count + (double)d.eps));
+        const double mean = t1 / count, var = t2 / count - mean * mean;
+        a.mean[i] = (float)((double)origin + mean);
+        a.rstd[i] = (float)(1.0 / sqrt((var < 0.0 ? 0.0 : var) + (double)d.eps));
     }
 }
 
+// Rows ahead of a thread of the second pass: pieces of 16 bytes, or of 4 (single float32 values).
+template <class T, int VEC, bool BWD>
+struct GnRing {
+    static constexpr int kPiece = (int)sizeof(T) * VEC, kAhead = 6, kPieces = BWD ? 3 : 2;
+    static constexpr size_t kBytes = kPiece >= 4 ? (size_t)kAhead * kPieces * kPiece * kThreads : 0;
+};
+
 // Second pass: outputs, or (backward) gradients of x and z.
 template <class T, int VEC, bool BWD>
-__global__ void __launch_bounds__(kThreads) k_gn_apply(const GnArgs a) {
+__global__ void __launch_bounds__(kThreads, 2) k_gn_apply(const GnArgs a) {
     const fft_gnorm_desc& d = a.d;
     const TileAt t = tile_at(a, true);
     const int tx = (int)threadIdx.x, ty = (int)threadIdx.y, bx = (int)blockDim.x, by = (int)blockDim.y;
     const int packs = a.cg / VEC, all = packs * t.groups;
+    using Ring = GnRing<T, VEC, BWD>;
+    constexpr bool RING = Ring::kBytes > 0;
+    constexpr int BYTES = Ring::kPiece, AHEAD = Ring::kAhead;
+    extern __shared__ uint4 ring[];
+    auto piece = [&](int stage, int k) {
+        return reinterpret_cast<char*>(ring) + ((stage * Ring::kPieces + k) * kThreads + ty * bx + tx) * BYTES;
+    };
+    const bool gate = d.z.data;
     for (int64_t at = t.t0; at < t.t1;) {
         const SeqAt s = part_at(a, t.row, at, t.t1);
         for (int p = tx; p < all; p += bx) {
@@ -416,38 +501,59 @@ __global__ void __launch_bounds__(kThreads) k_gn_apply(const GnArgs a) {
             const T* go = BWD ? static_cast<const T*>(a.dout.data) + t.row * a.dout.seq_stride + c : nullptr;
             T* out = static_cast<T*>(a.out.data) + t.row * a.out.seq_stride + c;
             T* dz = BWD ? static_cast<T*>(a.dz.data) + t.row * a.dz.seq_stride + c : nullptr;
-            // the rows of four tokens before the first of them is stored (out may be x or z)
-            constexpr int DEEP = 4;
-            for (int64_t i0 = s.begin + ty; i0 < s.end; i0 += DEEP * by) {
-                Pack<T, VEC> px[DEEP], pz[DEEP], pg[DEEP];
+            auto finish = [&](const Pack<T, VEC>& px, const Pack<T, VEC>& pz, const Pack<T, VEC>& pg, int64_t i) {
+                Values<VEC> n = unpack<T, VEC>(px), y, dzv, zv = unpack<T, VEC>(pz), gv = unpack<T, VEC>(pg);
 #pragma unroll
-                for (int u = 0; u < DEEP; ++u) {
-                    const int64_t i = i0 + u * by;
-                    const bool in = i < s.end;
-                    px[u] = pz[u] = pg[u] = Pack<T, VEC>{};
-                    if (in) px[u] = ld_pack<VEC>(x + i * d.x.tok_stride);
-                    if (in && d.z.data) pz[u] = ld_pack<VEC>(z + i * d.z.tok_stride);
-                    if (BWD && in) pg[u] = ld_pack<VEC>(go + i * a.dout.tok_stride);
+                for (int k = 0; k < n.N; ++k) {
+                    n.v[k] = mul2(add2(n.v[k], minus(mean)), splat(rstd));
+                    y.v[k] = fma2(n.v[k], ch.w.v[k], ch.b.v[k]);
                 }
+                if constexpr (BWD) {
+                    reaches<VEC>(d, y, zv, gv, dzv);
 #pragma unroll
-                for (int u = 0; u < DEEP; ++u) {
-                    const int64_t i = i0 + u * by;
-                    if (i >= s.end) break;
-                    float n[VEC], y[VEC], dzv[VEC] = {};
-#pragma unroll
-                    for (int k = 0; k < VEC; ++k) {
-                        n[k] = (to_f(px[u].v[k]) - mean) * rstd;
-                        y[k] = fmaf(n[k], ch.w[k], ch.b[k]);
-                    }
-                    if constexpr (BWD) {
-                        reaches<T, VEC>(d, y, pz[u], pg[u], dzv);
-#pragma unroll
-                        for (int k = 0; k < VEC; ++k) y[k] = (y[k] * ch.w[k] - fmaf(n[k], s2, s1)) * rstd;
-                    } else {
-                        outcome<T, VEC>(d, y, pz[u]);
-                    }
-                    st_pack<VEC>(out + i * a.out.tok_stride, rounded<T, VEC>(y));
-                    if (BWD && d.z.data) st_pack<VEC>(dz + i * a.dz.tok_stride, rounded<T, VEC>(dzv));
+                    for (int k = 0; k < n.N; ++k)
+                        y.v[k] = mul2(fma2(y.v[k], ch.w.v[k], fma2(n.v[k], minus(s2), minus(s1))), splat(rstd));
+                    if (gate) st_pack<VEC>(dz + i * a.dz.tok_stride, rounded<T, VEC>(dzv));
+                } else {
+                    outcome<VEC>(d, y, zv);
+                }
+                st_pack<VEC>(out + i * a.out.tok_stride, rounded<T, VEC>(y));
+            };
+            if constexpr (RING) {
+                // rows ahead wait in shared memory, where a thread reads only what it has copied itself
+                int64_t from = s.begin + ty;
+                auto fetch = [&](int stage) {
+                    const bool in = from < s.end;
+                    auto one = [&](int k, const T* p) {
+                        if constexpr (BYTES == 16) copy16(piece(stage, k), p, in);
+                        else copy4(piece(stage, k), p, in);
+                    };
+                    one(0, in ? x + from * d.x.tok_stride : x);
+                    if (gate) one(1, in ? z + from * d.z.tok_stride : z);
+                    if (BWD) one(2, in ? go + from * a.dout.tok_stride : go);
+                    copy_commit();
+                    from += by;
+                };
+                for (int k = 0; k < AHEAD - 1; ++k) fetch(k);
+                int stage = 0;
+                for (int64_t i = s.begin + ty; i < s.end; i += by) {
+                    fetch((stage + AHEAD - 1) % AHEAD);
+                    copy_wait<AHEAD - 1>();
+                    Pack<T, VEC> pz = {}, pg = {};
+                    const Pack<T, VEC> px = *reinterpret_cast<const Pack<T, VEC>*>(piece(stage, 0));
+                    if (gate) pz = *reinterpret_cast<const Pack<T, VEC>*>(piece(stage, 1));
+                    if (BWD) pg = *reinterpret_cast<const Pack<T, VEC>*>(piece(stage, 2));
+                    finish(px, pz, pg, i);
+                    stage = (stage + 1) % AHEAD;
+                }
+                copy_wait<0>();
+            } else {
+                for (int64_t i = s.begin + ty; i < s.end; i += by) {
+                    const Pack<T, VEC> px = ld_pack<VEC>(x + i * d.x.tok_stride);
+                    Pack<T, VEC> pz = {}, pg = {};
+                    if (gate) pz = ld_pack<VEC>(z + i * d.z.tok_stride);
+                    if (BWD) pg = ld_pack<VEC>(go + i * a.dout.tok_stride);
+                    finish(px, pz, pg, i);
                 }
             }
         }
@@ -472,7 +578,9 @@ __global__ void __launch_bounds__(kThreads) k_gn_sums(const GnArgs a) {
         const int64_t c = (int64_t)t.group0 * a.cg + p * VEC;
         Channel<T, VEC> ch;
         ch.load(d, c, in);
-        float dw[VEC] = {}, db[VEC] = {};
+        Values<VEC> dw, db;
+#pragma unroll
+        for (int k = 0; k < dw.N; ++k) dw.v[k] = db.v[k] = splat(0.f);
         for (int64_t at = t.t0; at < t.t1;) {
             const SeqAt s = part_at(a, t.row, at, t.t1);
             float s1 = 0.f, s2 = 0.f;
@@ -482,28 +590,29 @@ __global__ void __launch_bounds__(kThreads) k_gn_sums(const GnArgs a) {
                 const T* x = static_cast<const T*>(d.x.data) + t.row * d.x.seq_stride + c;
                 const T* z = static_cast<const T*>(d.z.data) + t.row * d.z.seq_stride + c;
                 const T* go = static_cast<const T*>(a.dout.data) + t.row * a.dout.seq_stride + c;
-#pragma unroll 4
+                float2 p1 = splat(0.f), p2 = splat(0.f);
+#pragma unroll(VEC == 1 ? 8 : 4)
                 for (int64_t i = s.begin + ty; i < s.end; i += by) {
-                    const Pack<T, VEC> px = ld_pack<VEC>(x + i * d.x.tok_stride);
-                    Pack<T, VEC> pz = {};
-                    if (d.z.data) pz = ld_pack<VEC>(z + i * d.z.tok_stride);
-                    const Pack<T, VEC> pg = ld_pack<VEC>(go + i * a.dout.tok_stride);
-                    float n[VEC], y[VEC], dzv[VEC] = {};
+                    Values<VEC> n = unpack<T, VEC>(ld_pack<VEC>(x + i * d.x.tok_stride)), y, dzv,
+                                zv = unpack<T, VEC>(load<T, VEC>(z + i * d.z.tok_stride, d.z.data != nullptr)),
+                                gv = unpack<T, VEC>(ld_pack<VEC>(go + i * a.dout.tok_stride));
 #pragma unroll
-                    for (int k = 0; k < VEC; ++k) {
-                        n[k] = (to_f(px.v[k]) - mean) * rstd;
-                        y[k] = fmaf(n[k], ch.w[k], ch.b[k]);
+                    for (int k = 0; k < n.N; ++k) {
+                        n.v[k] = mul2(add2(n.v[k], minus(mean)), splat(rstd));
+                        if (VEC == 1) n.v[k].y = 0.f;
+                        y.v[k] = fma2(n.v[k], ch.w.v[k], ch.b.v[k]);
                     }
-                    reaches<T, VEC>(d, y, pz, pg, dzv);
+                    reaches<VEC>(d, y, zv, gv, dzv);
 #pragma unroll
-                    for (int k = 0; k < VEC; ++k) {
-                        const float dn = y[k] * n[k];
-                        dw[k] += dn;
-                        db[k] += y[k];
-                        s1 = fmaf(y[k], ch.w[k], s1);
-                        s2 = fmaf(dn, ch.w[k], s2);
+                    for (int k = 0; k < n.N; ++k) {
+                        const float2 dn = mul2(y.v[k], n.v[k]);
+                        dw.v[k] = add2(dw.v[k], dn);
+                        db.v[k] = add2(db.v[k], y.v[k]);
+                        p1 = fma2(y.v[k], ch.w.v[k], p1);
+                        p2 = fma2(dn, ch.w.v[k], p2);
                     }
                 }
+                s1 = p1.x + p1.y, s2 = p2.x + p2.y;
             }
             red[0][tid] = s1, red[1][tid] = s2;
             __syncthreads();
@@ -527,8 +636,8 @@ __global__ void __launch_bounds__(kThreads) k_gn_sums(const GnArgs a) {
         if (!a.parts) continue;
 #pragma unroll
         for (int k = 0; k < VEC; ++k) {
-            chans[tid * VEC + k] = dw[k];
-            chans[(bx * by + tid) * VEC + k] = db[k];
+            chans[tid * VEC + k] = k & 1 ? dw.v[k / 2].y : dw.v[k / 2].x;
+            chans[(bx * by + tid) * VEC + k] = k & 1 ? db.v[k / 2].y : db.v[k / 2].x;
         }
         __syncthreads();
         float* out = a.parts + (t.row * a.tiles + t.tile) * 2 * d.channels + (int64_t)t.group0 * a.cg + (int64_t)p0 * VEC;
@@ -587,10 +696,11 @@ int64_t up16(int64_t bytes) { return (bytes + 15) / 16 * 16; }
 bool by_token(const fft_gnorm_desc& d) {  // sequences of one token whose groups fit their lanes
     return !d.offsets && d.length == 1 && d.channels / d.groups <= 32 * kTokenValues;
 }
-// Lanes that share a group of the token kernel: a pack each, up to a warp.
-int token_lanes(int64_t packs) {
+// Lanes that share a group of the token kernel: a pack of one value each, two longer ones (fewer
+// steps of their sums), up to a warp.
+int token_lanes(int64_t packs, bool wide) {
     int lanes = 1;
-    while (lanes < 32 && lanes < packs) lanes *= 2;
+    while (lanes < 32 && lanes * (wide ? 2 : 1) < packs) lanes *= 2;
     return lanes;
 }
 // Rows that the token kernel's threads start at: as many as the SMs hold, at three blocks each where
@@ -600,11 +710,12 @@ int64_t token_step(const fft_gnorm_desc& d, int lanes, bool backward) {
     const int64_t step = subs / d.groups;
     return step < 1 ? 1 : (step > d.nseq ? d.nseq : step);
 }
-// Tokens of a tile: as many as leave every SM four blocks, 16 to 128.
+// Tokens of a tile: as many as leave every SM eight blocks of 512 channels, 16 to 128.  Measured: 8 x 4096
+// tokens of 1024 channels with tiles of 16 and 32 94 and 72 us, 20011 of 330 channels 82 and 110 us.
 int64_t tile_of(const fft_gnorm_desc& d) {
-    const int64_t rows = d.offsets ? 1 : d.nseq;
+    const int64_t rows = d.offsets ? 1 : d.nseq, wide = (d.channels + 511) / 512;
     int64_t tile = 128;
-    while (tile > 16 && rows * ((d.length + tile - 1) / tile) * ((d.channels + 2047) / 2048) < (int64_t)num_sms() * 4) tile /= 2;
+    while (tile > 16 && rows * ((d.length + tile - 1) / tile) * wide < (int64_t)num_sms() * 8) tile /= 2;
     return tile;
 }
 int64_t gnorm_layout(const fft_gnorm_desc& d, bool backward, GnArgs* a, char* w) {
@@ -619,7 +730,7 @@ int64_t gnorm_layout(const fft_gnorm_desc& d, bool backward, GnArgs* a, char* w)
     if (by_token(d)) {
         // packs of one value, where rows are off 16-byte boundaries, have no fewer lanes
         const int64_t vec = 16 / (int64_t)dtype_size(d.dtype);
-        if (backward) a->parts = take(token_step(d, token_lanes((a->cg + vec - 1) / vec), true) * 2 * d.channels);
+        if (backward) a->parts = take(token_step(d, token_lanes((a->cg + vec - 1) / vec, true), true) * 2 * d.channels);
         return at;
     }
     a->tile = tile_of(d);
@@ -637,9 +748,25 @@ bool vec_rows(const fft_seq& s, const fft_gnorm_desc& d, int64_t vec) {
                        (d.offsets || d.nseq < 2 || s.seq_stride % vec == 0));
 }
 
+template <class T, int VEC, int NV, bool BWD>
+cudaError_t launch_token(const GnArgs& a, unsigned blocks, int lanes, int64_t step, cudaStream_t s) {
+    constexpr size_t bytes = VEC > 1 ? (size_t)kGnAhead * NV * (BWD ? 3 : 2) * 16 * kThreads : 0;
+    if constexpr (bytes > 0) {
+        static LaunchCache cache;
+        LaunchGeom g;
+        const cudaError_t e = cache.get(
+            [](int dev, LaunchGeom* out) {
+                return setup_persistent(k_gn_token<T, VEC, NV, BWD>, kThreads, bytes, dev, out);
+            },
+            &g);
+        if (e != cudaSuccess) return e;
+    }
+    k_gn_token<T, VEC, NV, BWD><<<blocks, kThreads, bytes, s>>>(a, lanes, step);
+    return cudaGetLastError();
+}
 template <class T, int VEC, bool BWD>
 cudaError_t run_token(const GnArgs& a, int64_t* parts, cudaStream_t s) {
-    const int packs = a.cg / VEC, lanes = token_lanes(packs);
+    const int packs = a.cg / VEC, lanes = token_lanes(packs, VEC > 1);
     const int nv = (packs + lanes - 1) / lanes;
     const int64_t step = token_step(a.d, lanes, BWD);
     const int64_t blocks = (step * a.d.groups * lanes + kThreads - 1) / kThreads;
@@ -647,13 +774,13 @@ cudaError_t run_token(const GnArgs& a, int64_t* parts, cudaStream_t s) {
     *parts = step;
     const unsigned n = (unsigned)blocks;
     constexpr int MOST = kTokenValues / VEC;
-    if (nv <= 1) k_gn_token<T, VEC, 1, BWD><<<n, kThreads, 0, s>>>(a, lanes, step);
-    else if (nv <= 2 || MOST == 2) k_gn_token<T, VEC, 2, BWD><<<n, kThreads, 0, s>>>(a, lanes, step);
-    else if constexpr (MOST >= 4) {
-        if (nv <= 4 || MOST == 4) k_gn_token<T, VEC, 4, BWD><<<n, kThreads, 0, s>>>(a, lanes, step);
-        else if constexpr (MOST >= 16) {
-            if (nv <= 8) k_gn_token<T, VEC, 8, BWD><<<n, kThreads, 0, s>>>(a, lanes, step);
-            else k_gn_token<T, VEC, 16, BWD><<<n, kThreads, 0, s>>>(a, lanes, step);
+    if (nv <= 1) return launch_token<T, VEC, 1, BWD>(a, n, lanes, step, s);
+    if (nv <= 2 || MOST == 2) return launch_token<T, VEC, 2, BWD>(a, n, lanes, step, s);
+    if constexpr (MOST >= 4) {
+        if (nv <= 4 || MOST == 4) return launch_token<T, VEC, 4, BWD>(a, n, lanes, step, s);
+        if constexpr (MOST >= 16) {
+            if (nv <= 8) return launch_token<T, VEC, 8, BWD>(a, n, lanes, step, s);
+            return launch_token<T, VEC, 16, BWD>(a, n, lanes, step, s);
         }
     }
     return cudaGetLastError();
@@ -681,7 +808,18 @@ cudaError_t run_tiles(GnArgs a, int64_t* parts, cudaStream_t s) {
     else
         k_gn_moments<T, VEC><<<n, threads, 0, s>>>(a);
     k_gn_join<BWD><<<(unsigned)joins, kThreads, 0, s>>>(a);
-    k_gn_apply<T, VEC, BWD><<<n, threads, 0, s>>>(a);
+    constexpr size_t bytes = GnRing<T, VEC, BWD>::kBytes;
+    if constexpr (bytes > 0) {
+        static LaunchCache cache;
+        LaunchGeom g;
+        const cudaError_t e = cache.get(
+            [](int dev, LaunchGeom* out) {
+                return setup_persistent(k_gn_apply<T, VEC, BWD>, kThreads, bytes, dev, out);
+            },
+            &g);
+        if (e != cudaSuccess) return e;
+    }
+    k_gn_apply<T, VEC, BWD><<<n, threads, bytes, s>>>(a);
     return cudaGetLastError();
 }
 
@@ -778,6 +916,10 @@ extern "C" int fft_gnorm_backward(const fft_gnorm_desc* d, const fft_gnorm_grads
                                                         : run_gnorm<__half, true>(a, &parts, s));
     }
     const int64_t c = d->channels;
+    if (g->dweight && g->dbias == g->dweight + c) {  // one behind the other, as in the partial rows
+        if (e == cudaSuccess) e = run_sum_parts(a.parts, parts, 2 * c, 2 * c, g->dweight, 2 * c, 1, s);
+        return status(e);
+    }
     if (e == cudaSuccess && g->dweight) e = run_sum_parts(a.parts, parts, 2 * c, c, g->dweight, c, 1, s);
     if (e == cudaSuccess && g->dbias) e = run_sum_parts(a.parts ? a.parts + c : nullptr, parts, 2 * c, c, g->dbias, c, 1, s);
     return status(e);

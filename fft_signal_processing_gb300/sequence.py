@@ -780,9 +780,10 @@ def group_norm_backward(dout, x, mean, rstd, weight=None, bias=None, z=None, sil
     with on:
         dx = x.new_empty(x.shape)
         dz = x.new_empty(x.shape) if z is not None else None
-        make = x.new_empty if nseq else x.new_zeros
-        dw = make(weight.shape, dtype=f32) if weight is not None else None
-        db = make(bias.shape, dtype=f32) if bias is not None else None
+        # one behind the other, which takes one kernel less
+        params = (x.new_empty if nseq else x.new_zeros)((2, x.shape[-1]), dtype=f32)
+        dw = params[0] if weight is not None else None
+        db = params[1] if bias is not None else None
         if nseq == 0:
             return GroupNormGrads(dx, dz, dw, db)
         grads = _GNORM_GRADS.pack(mp, rp, *rows(dout, packed), *rows(dx, packed),
