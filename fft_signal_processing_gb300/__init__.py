@@ -13,11 +13,13 @@ calls raise instead of computing anything another way.
     Plan(1024, 1, dims=2, ny=512, direction=INVERSE, normalize=True).c2c(img)  # 512 x 1024
     shift(y)                                                # standalone fftshift
 
-The sequence operators (short causal convolution, selective state-space scan, residual norm) are
-in the module `sequence` and under the package's own name:
+The sequence operators (short causal convolution, selective state-space scan, linear attention with
+decays, residual norm, group norm) are in the module `sequence` and under the package's own name:
 
     out = causal_conv(x, weight, bias, silu=True)           # x [sequences, tokens, channels]
     y = selective_scan(u, delta, A, B, C, D=D, z=z, softplus=True)
+    o = linear_attention(q, k, v, decay)                    # v [sequences, tokens, heads, dv]
+    g = group_norm(x, groups, weight, bias, z=z).out        # each row's groups, or a sequence's
     r = residual_norm(x, weight, residual=res)
 """
 import ctypes
@@ -26,9 +28,9 @@ import os
 from . import sequence
 from .sequence import (causal_conv, causal_conv_backward, causal_conv_step, group_norm,
                        group_norm_backward, linear_attention,
-                       linear_attention_backward, linear_attention_step, residual_norm,
-                       residual_norm_backward, selective_scan, selective_scan_backward,
-                       selective_scan_step)
+                       linear_attention_backward, linear_attention_check,
+                       linear_attention_step, residual_norm, residual_norm_backward,
+                       selective_scan, selective_scan_backward, selective_scan_step)
 
 FORWARD = -1
 INVERSE = +1

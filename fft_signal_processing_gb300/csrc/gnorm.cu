@@ -465,26 +465,27 @@ __global__ void __launch_bounds__(kThreads) k_gn_join(const GnArgs a) {
     }
 }
 
-// Rows ahead of a thread of the second pass: pieces of 16 bytes, or of 4 (single float32 values).
+// Rows ahead of a thread of the second pass, in pieces of 16 bytes.  (Single values
+// are loaded four tokens at a time instead, by as many blocks as 64 registers leave room for.)
 template <class T, int VEC, bool BWD>
 struct GnRing {
-    static constexpr int kPiece = (int)sizeof(T) * VEC, kAhead = 6, kPieces = BWD ? 3 : 2;
-    static constexpr size_t kBytes = kPiece >= 4 ? (size_t)kAhead * kPieces * kPiece * kThreads : 0;
+    static constexpr int kAhead = 6, kPieces = BWD ? 3 : 2;
+    static constexpr size_t kBytes = VEC > 1 ? (size_t)kAhead * kPieces * 16 * kThreads : 0;
 };
 
 // Second pass: outputs, or (backward) gradients of x and z.
 template <class T, int VEC, bool BWD>
-__global__ void __launch_bounds__(kThreads, 2) k_gn_apply(const GnArgs a) {
+__global__ void __launch_bounds__(kThreads, VEC > 1 ? 2 : 4) k_gn_apply(const GnArgs a) {
     const fft_gnorm_desc& d = a.d;
     const TileAt t = tile_at(a, true);
     const int tx = (int)threadIdx.x, ty = (int)threadIdx.y, bx = (int)blockDim.x, by = (int)blockDim.y;
     const int packs = a.cg / VEC, all = packs * t.groups;
     using Ring = GnRing<T, VEC, BWD>;
     constexpr bool RING = Ring::kBytes > 0;
-    constexpr int BYTES = Ring::kPiece, AHEAD = Ring::kAhead;
+    constexpr int AHEAD = Ring::kAhead;
     extern __shared__ uint4 ring[];
     auto piece = [&](int stage, int k) {
-        return reinterpret_cast<char*>(ring) + ((stage * Ring::kPieces + k) * kThreads + ty * bx + tx) * BYTES;
+        return reinterpret_cast<char*>(ring) + ((stage * Ring::kPieces + k) * kThreads + ty * bx + tx) * 16;
     };
     const bool gate = d.z.data;
     for (int64_t at = t.t0; at < t.t1;) {
@@ -524,13 +525,9 @@ __global__ void __launch_bounds__(kThreads, 2) k_gn_apply(const GnArgs a) {
                 int64_t from = s.begin + ty;
                 auto fetch = [&](int stage) {
                     const bool in = from < s.end;
-                    auto one = [&](int k, const T* p) {
-                        if constexpr (BYTES == 16) copy16(piece(stage, k), p, in);
-                        else copy4(piece(stage, k), p, in);
-                    };
-                    one(0, in ? x + from * d.x.tok_stride : x);
-                    if (gate) one(1, in ? z + from * d.z.tok_stride : z);
-                    if (BWD) one(2, in ? go + from * a.dout.tok_stride : go);
+                    copy16(piece(stage, 0), in ? x + from * d.x.tok_stride : x, in);
+                    if (gate) copy16(piece(stage, 1), in ? z + from * d.z.tok_stride : z, in);
+                    if (BWD) copy16(piece(stage, 2), in ? go + from * a.dout.tok_stride : go, in);
                     copy_commit();
                     from += by;
                 };
@@ -548,12 +545,27 @@ __global__ void __launch_bounds__(kThreads, 2) k_gn_apply(const GnArgs a) {
                 }
                 copy_wait<0>();
             } else {
-                for (int64_t i = s.begin + ty; i < s.end; i += by) {
-                    const Pack<T, VEC> px = ld_pack<VEC>(x + i * d.x.tok_stride);
-                    Pack<T, VEC> pz = {}, pg = {};
-                    if (gate) pz = ld_pack<VEC>(z + i * d.z.tok_stride);
-                    if (BWD) pg = ld_pack<VEC>(go + i * a.dout.tok_stride);
-                    finish(px, pz, pg, i);
+                constexpr int DEEP = 4;
+                const int64_t first = s.begin + ty, hx = by * d.x.tok_stride, hz = by * d.z.tok_stride,
+                              hg = by * a.dout.tok_stride;
+                const T *xp = x + first * d.x.tok_stride, *zp = z + first * d.z.tok_stride,
+                        *gp = go + first * a.dout.tok_stride;
+                const int count = s.end > first ? (int)((s.end - first + by - 1) / by) : 0;
+                for (int i0 = 0; i0 < count; i0 += DEEP) {
+                    Pack<T, VEC> px[DEEP], pz[DEEP], pg[DEEP];
+#pragma unroll
+                    for (int u = 0; u < DEEP; ++u) {
+                        const bool in = i0 + u < count;
+                        px[u] = load<T, VEC>(xp, in);
+                        pz[u] = load<T, VEC>(zp, in && gate);
+                        pg[u] = load<T, VEC>(gp, in && BWD);
+                        xp += hx;
+                        if (gate) zp += hz;
+                        if (BWD) gp += hg;
+                    }
+#pragma unroll
+                    for (int u = 0; u < DEEP; ++u)
+                        if (i0 + u < count) finish(px[u], pz[u], pg[u], first + (i0 + u) * by);
                 }
             }
         }
@@ -563,13 +575,14 @@ __global__ void __launch_bounds__(kThreads, 2) k_gn_apply(const GnArgs a) {
 
 // First pass of the gradients: sums of w and w n of every part, of dy n and dy of every channel.
 template <class T, int VEC>
-__global__ void __launch_bounds__(kThreads) k_gn_sums(const GnArgs a) {
+__global__ void __launch_bounds__(kThreads, VEC > 1 ? 2 : 4) k_gn_sums(const GnArgs a) {
     __shared__ float red[2][kThreads];
     extern __shared__ float chans[];  // [2][ty][tx * VEC]
     const fft_gnorm_desc& d = a.d;
     const TileAt t = tile_at(a, false);
     const int tx = (int)threadIdx.x, ty = (int)threadIdx.y, bx = (int)blockDim.x, by = (int)blockDim.y;
     const int packs = a.cg / VEC, all = packs * t.groups, tid = ty * bx + tx;
+    const bool gate = d.z.data;
     // packs outermost, since a channel's sums run over all parts; with several rounds of packs (a
     // set of one group of many channels) the parts' sums go on from what is there
     for (int p0 = 0; p0 < all; p0 += bx) {
@@ -591,25 +604,42 @@ __global__ void __launch_bounds__(kThreads) k_gn_sums(const GnArgs a) {
                 const T* z = static_cast<const T*>(d.z.data) + t.row * d.z.seq_stride + c;
                 const T* go = static_cast<const T*>(a.dout.data) + t.row * a.dout.seq_stride + c;
                 float2 p1 = splat(0.f), p2 = splat(0.f);
-#pragma unroll(VEC == 1 ? 8 : 4)
-                for (int64_t i = s.begin + ty; i < s.end; i += by) {
-                    Values<VEC> n = unpack<T, VEC>(ld_pack<VEC>(x + i * d.x.tok_stride)), y, dzv,
-                                zv = unpack<T, VEC>(load<T, VEC>(z + i * d.z.tok_stride, d.z.data != nullptr)),
-                                gv = unpack<T, VEC>(ld_pack<VEC>(go + i * a.dout.tok_stride));
+                constexpr int DEEP = VEC == 1 ? 4 : 2;  // tokens loaded before the first of them is used
+                const int64_t first = s.begin + ty, hx = by * d.x.tok_stride, hz = by * d.z.tok_stride,
+                              hg = by * a.dout.tok_stride;
+                x += first * d.x.tok_stride, go += first * a.dout.tok_stride;
+                if (gate) z += first * d.z.tok_stride;
+                const int count = s.end > first ? (int)((s.end - first + by - 1) / by) : 0;
+                for (int i0 = 0; i0 < count; i0 += DEEP) {
+                    Pack<T, VEC> px[DEEP], pz[DEEP], pg[DEEP];
 #pragma unroll
-                    for (int k = 0; k < n.N; ++k) {
-                        n.v[k] = mul2(add2(n.v[k], minus(mean)), splat(rstd));
-                        if (VEC == 1) n.v[k].y = 0.f;
-                        y.v[k] = fma2(n.v[k], ch.w.v[k], ch.b.v[k]);
+                    for (int u = 0; u < DEEP; ++u) {
+                        const bool in = i0 + u < count;
+                        px[u] = load<T, VEC>(x, in);
+                        pg[u] = load<T, VEC>(go, in);
+                        pz[u] = load<T, VEC>(z, in && gate);
+                        x += hx, go += hg;
+                        if (gate) z += hz;
                     }
-                    reaches<VEC>(d, y, zv, gv, dzv);
 #pragma unroll
-                    for (int k = 0; k < n.N; ++k) {
-                        const float2 dn = mul2(y.v[k], n.v[k]);
-                        dw.v[k] = add2(dw.v[k], dn);
-                        db.v[k] = add2(db.v[k], y.v[k]);
-                        p1 = fma2(y.v[k], ch.w.v[k], p1);
-                        p2 = fma2(dn, ch.w.v[k], p2);
+                    for (int u = 0; u < DEEP; ++u) {
+                        Values<VEC> n = unpack<T, VEC>(px[u]), y, dzv, zv = unpack<T, VEC>(pz[u]), gv = unpack<T, VEC>(pg[u]);
+#pragma unroll
+                        for (int k = 0; k < n.N; ++k) {
+                            n.v[k] = mul2(add2(n.v[k], minus(mean)), splat(rstd));
+                            if (VEC == 1) n.v[k].y = 0.f;
+                            y.v[k] = fma2(n.v[k], ch.w.v[k], ch.b.v[k]);
+                        }
+                        reaches<VEC>(d, y, zv, gv, dzv);
+#pragma unroll
+                        for (int k = 0; k < n.N; ++k) {
+                            if (i0 + u >= count) break;  // (a statistic that is no number times 0 is none)
+                            const float2 dn = mul2(y.v[k], n.v[k]);
+                            dw.v[k] = add2(dw.v[k], dn);
+                            db.v[k] = add2(db.v[k], y.v[k]);
+                            p1 = fma2(y.v[k], ch.w.v[k], p1);
+                            p2 = fma2(dn, ch.w.v[k], p2);
+                        }
                     }
                 }
                 s1 = p1.x + p1.y, s2 = p2.x + p2.y;
@@ -711,7 +741,7 @@ int64_t token_step(const fft_gnorm_desc& d, int lanes, bool backward) {
     return step < 1 ? 1 : (step > d.nseq ? d.nseq : step);
 }
 // Tokens of a tile: as many as leave every SM eight blocks of 512 channels, 16 to 128.  Measured: 8 x 4096
-// tokens of 1024 channels with tiles of 16 and 32 94 and 72 us, 20011 of 330 channels 82 and 110 us.
+// tokens of 1024 channels 94 us with tiles of 16 and 72 us with tiles of 32.
 int64_t tile_of(const fft_gnorm_desc& d) {
     const int64_t rows = d.offsets ? 1 : d.nseq, wide = (d.channels + 511) / 512;
     int64_t tile = 128;

@@ -573,6 +573,14 @@ def linear_attention_backward(dout, q, k, v, decay, scale=None, initial_state=No
     return AttentionGrads(dq, dkey, dval, dg, di)
 
 
+def linear_attention_check(stream=None):
+    """Synchronises the stream and raises GbfftError where a device-side wait of an earlier call of
+    linear_attention or its gradients on the current device has run out (fft_linattn_check)."""
+    if _L is None:
+        _setup()
+    _check(_L.fft_linattn_check(_stream(stream, _device())[1]), "fft_linattn_check")
+
+
 def linear_attention_step(state, q, k, v, decay, scale=None, slots=None, slots_out=None, out=None,
                           stream=None):
     """One token for each sequence (fft_linattn_step): q, k [sequences, groups, dk], v [sequences, heads,
