@@ -25,7 +25,9 @@ struct AttnStepArgs {
 // A block takes 32 columns of one head's state: VEC columns per thread, so 32 / VEC lanes hold a row
 // and the rows are dealt to groups of lanes, eight loads of each under way at once.  Bound by the
 // states' bytes for many sequences and by latency for one; queries and keys go through shared memory,
-// which leaves registers for eight blocks to an SM.
+// which leaves registers for eight blocks to an SM.  Measured: 128 sequences of 16 heads of 128 x 128 48 us,
+// 5.7 TB/s (84% of the copy rate; 81 us with queries and keys in registers, four blocks); one sequence of 32
+// heads of 64 x 64 16 us with the host side of the call.
 template <class T, int VEC>
 __global__ void __launch_bounds__(kStepThreads, 8) k_linattn_step(const AttnStepArgs a) {
     constexpr int LANES = kStepCols / VEC, GROUPS = kStepThreads / LANES, DEEP = 8;
