@@ -304,6 +304,7 @@ __global__ void __launch_bounds__(WARPS * 32, AttnShape<T, DX, WARPS, BWD>::kBlo
     const int64_t t0 = seg * a.segment, t1 = t0 + a.segment < a.length ? t0 + a.segment : a.length;
     const int z0 = (int)zt * Z, dz = (int)a.dz - z0 < Z ? (int)a.dz - z0 : Z, dx = (int)a.dx;
     const bool reverse = a.reverse, summary = a.summary;
+    const bool busy = warp * 16 < dz;  // this warp has columns
 
     const T* px = summary ? nullptr : rows_at<T>(a.x, row, head);
     const T* py = rows_at<T>(a.y, row, head);
@@ -413,6 +414,7 @@ __global__ void __launch_bounds__(WARPS * 32, AttnShape<T, DX, WARPS, BWD>::kBlo
                 float acc[COLS / 8][4] = {};
 #pragma unroll 2
                 for (int k = 0; k < DX / 16; ++k) {
+                    if (k * 16 >= dx) break;
                     Pair<T> fa[4];
                     uint32_t pa[NP][4];
                     load_rows<T>(sx, XS, m * 16, k * 16, fa);
@@ -464,9 +466,10 @@ __global__ void __launch_bounds__(WARPS * 32, AttnShape<T, DX, WARPS, BWD>::kBlo
                     for (int n = 0; n < 2; ++n)
 #pragma unroll
                         for (int k = 0; k < 4; ++k) o[m][n][k] = 0.f;
-                if (some) {
+                if (some && busy) {
 #pragma unroll
                     for (int k = 0; k < DX / 16; ++k) {
+                        if (k * 16 >= dx) break;
                         uint32_t ps[PO][4];
 #pragma unroll
                         for (int h = 0; h < 4; ++h) {
@@ -541,7 +544,8 @@ __global__ void __launch_bounds__(WARPS * 32, AttnShape<T, DX, WARPS, BWD>::kBlo
                 }
             }
             if (!summary) {
-                if (!__any_sync(0xffffffffu, !(odd == 0.f))) {
+                if (!busy) {
+                } else if (!__any_sync(0xffffffffu, !(odd == 0.f))) {
 #pragma unroll
                     for (int k = 0; k < 4; ++k) {
                         uint32_t pv[NP][4];
@@ -641,6 +645,7 @@ __global__ void __launch_bounds__(WARPS * 32, AttnShape<T, DX, WARPS, BWD>::kBlo
             constexpr int WIDE = NP == 1 ? 2 : 1;
 #pragma unroll
             for (int j = 0; j < NX / 2; j += WIDE) {
+                if (!busy || j * 16 >= dx) break;
                 float add[WIDE][2][4] = {};
 #pragma unroll
                 for (int k = 0; k < 4; ++k)

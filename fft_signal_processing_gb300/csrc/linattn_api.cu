@@ -113,16 +113,29 @@ __global__ void k_linattn_carry(const AttnArgs a, int64_t quads) {
     const float* gone = a.carry_decay + row * a.nsegments * a.heads + head;
     const int* reset = a.carry_reset + row * a.nsegments * a.heads + head;
     float4 c = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int64_t k = 0; k < a.nsegments; ++k) {
-        const int64_t s = a.reverse ? a.nsegments - 1 - k : k;
-        const float4 own = p[s * step];
-        p[s * step] = c;
-        const bool r = reset[s * a.heads];
-        const float f = ex2(gone[s * a.heads]);
-        c.x = r ? own.x : fmaf(f, c.x, own.x);
-        c.y = r ? own.y : fmaf(f, c.y, own.y);
-        c.z = r ? own.z : fmaf(f, c.z, own.z);
-        c.w = r ? own.w : fmaf(f, c.w, own.w);
+    constexpr int DEEP = 8;  // segments loaded before the first of them is stored
+    for (int64_t k0 = 0; k0 < a.nsegments; k0 += DEEP) {
+        float4 own[DEEP];
+        float f[DEEP];
+        bool r[DEEP];
+#pragma unroll
+        for (int u = 0; u < DEEP; ++u) {
+            if (k0 + u >= a.nsegments) break;
+            const int64_t s = a.reverse ? a.nsegments - 1 - k0 - u : k0 + u;
+            own[u] = p[s * step];
+            r[u] = reset[s * a.heads];
+            f[u] = ex2(gone[s * a.heads]);
+        }
+#pragma unroll
+        for (int u = 0; u < DEEP; ++u) {
+            if (k0 + u >= a.nsegments) break;
+            const int64_t s = a.reverse ? a.nsegments - 1 - k0 - u : k0 + u;
+            p[s * step] = c;
+            c.x = r[u] ? own[u].x : fmaf(f[u], c.x, own[u].x);
+            c.y = r[u] ? own[u].y : fmaf(f[u], c.y, own[u].y);
+            c.z = r[u] ? own[u].z : fmaf(f[u], c.z, own[u].z);
+            c.w = r[u] ? own[u].w : fmaf(f[u], c.w, own[u].w);
+        }
     }
 }
 
