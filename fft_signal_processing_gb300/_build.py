@@ -4,7 +4,8 @@ Each translation unit under csrc/ is compiled in parallel to an object file, the
 fft_signal_processing_gb300/libgbfft.so.  Objects are rebuilt only when a source or header is
 newer than them.  build(checked=True) makes the checked variant libgbfft_checked.so from the
 same sources with -DGBFFT_CHECKED (device-side index checks that report FFT_ERR_BOUNDS), in an
-object directory of its own; tests load it through GBFFT_CHECKED=1.
+object directory of its own; tests load it through GBFFT_CHECKED=1.  The sequence operators carry no
+such checks: both libraries link the same objects of theirs.
 """
 import concurrent.futures as cf
 import glob
@@ -20,6 +21,9 @@ OBJ = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libgbfft.so")
 OBJ_CHECKED = os.path.join(PKG, "_build_checked")
 LIB_CHECKED = os.path.join(PKG, "libgbfft_checked.so")
+
+# Sources without index checks (the sequence operators), by the beginnings of their names.
+UNCHECKED = ("conv_", "gnorm", "linattn_", "norm", "scan_", "seq_")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-O2",
@@ -57,15 +61,21 @@ def _compile(src: str, extra, verbose: bool, objdir: str = OBJ) -> str:
 
 def build(force: bool = False, verbose: bool = False, extra=(), checked: bool = False) -> str:
     objdir, lib = (OBJ_CHECKED, LIB_CHECKED) if checked else (OBJ, LIB)
-    extra = list(extra) + (["-DGBFFT_CHECKED"] if checked else [])
     os.makedirs(objdir, exist_ok=True)
+    os.makedirs(OBJ, exist_ok=True)
     if force:
         for o in glob.glob(os.path.join(objdir, "*.o")):
             os.remove(o)
     srcs = sorted(glob.glob(os.path.join(CSRC, "*.cu")))
+
+    def compiled(src):
+        own = checked and not os.path.basename(src).startswith(UNCHECKED)
+        return _compile(src, list(extra) + (["-DGBFFT_CHECKED"] if own else []), verbose,
+                        objdir if own else OBJ)
+
     workers = max(1, min(len(srcs), os.cpu_count() or 1))
     with cf.ThreadPoolExecutor(workers) as ex:
-        objs = list(ex.map(lambda s: _compile(s, extra, verbose, objdir), srcs))
+        objs = list(ex.map(compiled, srcs))
     if (not force and os.path.exists(lib)
             and os.path.getmtime(lib) >= max(os.path.getmtime(o) for o in objs)):
         return lib

@@ -440,8 +440,8 @@ AttnRows rows_of(const fft_heads& t, int64_t dim, int64_t heads, const fft_linat
 int64_t up16(int64_t bytes) { return (bytes + 15) / 16 * 16; }
 
 // One pass of the kernel: shapes, and time cut into as many segments as give the least time, counted
-// in rounds of resident blocks times the chunks of a segment.  A cut call reads keys and values
-// twice.
+// in rounds of resident blocks times the chunks of a segment, a chunk as 4, `start` more for every block and
+// half as much again for the summaries of a cut call, which reads keys and values twice.
 void attn_plan(const fft_linattn_desc& d, int64_t dx, int64_t dz, AttnArgs* a) {
     a->offsets = d.offsets;
     a->nseq = d.nseq;
@@ -457,14 +457,14 @@ void attn_plan(const fft_linattn_desc& d, int64_t dx, int64_t dz, AttnArgs* a) {
 bool tc_sizes(const fft_linattn_desc& d, bool backward) {
     return d.dtype == FFT_BF16 && d.dk <= 128 && (!backward || d.dv <= 128);
 }
-int64_t attn_segment(const fft_linattn_desc& d, int64_t ztiles, int64_t resident, int64_t chunk) {
+int64_t attn_segment(const fft_linattn_desc& d, int64_t ztiles, int64_t resident, int64_t chunk, int64_t start) {
     const int64_t rows = d.offsets ? 1 : d.nseq, blocks = rows * d.heads * ztiles;
     int64_t segment = (d.length + chunk - 1) / chunk * chunk, best = INT64_MAX;
     for (int64_t k = 1; k <= 256; ++k) {
         int64_t size = (d.length + k - 1) / k;
         size = (size + chunk - 1) / chunk * chunk;
         const int64_t n = (d.length + size - 1) / size;
-        const int64_t cost = (blocks * n + resident - 1) / resident * (size / chunk * (n > 1 ? 3 : 2) + 4) + (n > 1 ? 8 : 0);
+        const int64_t cost = (blocks * n + resident - 1) / resident * (size / chunk * (n > 1 ? 6 : 4) + start) + (n > 1 ? 2 * start : 0);
         if (cost < best) best = cost, segment = size;
         if (size <= chunk) break;
     }
@@ -497,7 +497,7 @@ int64_t forward_layout(const fft_linattn_desc& d, AttnArgs* a, char* w) {
     attn_plan(d, d.dk, d.dv, a);
     const bool tc = tc_sizes(d, false);
     const int64_t resident = (int64_t)num_sms() * (!tc && attn_warps(d.dtype, d.dk, d.dv) == 4 ? 2 : 1);
-    attn_cut(a, attn_segment(d, a->ztiles, resident, tc ? kTcChunk : kAttnChunk));
+    attn_cut(a, attn_segment(d, a->ztiles, resident, tc ? kTcChunk : kAttnChunk, 8));
     Taker t = {w};
     take_carry(a, d.dtype, &t);
     return t.at;
@@ -514,7 +514,11 @@ int64_t backward_layout(const fft_linattn_desc& d, const fft_linattn_grads* gr, 
     attn_plan(d, d.dv, d.dk, &p->k);
     attn_plan(d, d.dk, d.dv, &p->v);
     const int64_t zk = p->q.ztiles, zv = p->v.ztiles;
-    const int64_t segment = attn_segment(d, zk > zv ? zk : zv, (int64_t)num_sms(), tc_sizes(d, true) ? kTcChunk : kAttnChunk);
+    // start: the tcgen05 kernel's chunks take longer than a block's start here (4 x 2048 tokens of 16 heads of
+    // 128 x 128, 480 us with 8, uncut, and 454 us with 3, cut in two); 13 packed rows of 4001 tokens of 8 heads in
+    // float16 391 us with 8 and 421 us with 3
+    const bool tc = tc_sizes(d, true);
+    const int64_t segment = attn_segment(d, zk > zv ? zk : zv, (int64_t)num_sms(), tc ? kTcChunk : kAttnChunk, tc ? 3 : 8);
     Taker t = {w};
     for (AttnArgs* a : {&p->q, &p->k, &p->v}) {
         attn_cut(a, segment);
