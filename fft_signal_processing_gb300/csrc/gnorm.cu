@@ -4,7 +4,7 @@
 // and its gradients, with dy what reaches y and w = weight dy:
 //   dx = rstd (w - mean(w) - n mean(w n)),  dweight = sum dy n,  dbias = sum dy.
 // A few operations per element: bound by HBM where rows are whole 16-byte pieces.  Measured with inputs
-// that change from call to call: 16384 rows of 2048 bfloat16 channels in 16 groups, gated, 44 us, 4.7 TB/s
+// that change from call to call: 16384 rows of 2048 bfloat16 channels in 16 groups, gated, 43 us, 4.7 TB/s
 // (69% of the copy rate; 81 with rows ahead in registers and one value to an instruction); its gradients
 // for 8192 rows 60 us; 8 x 4096 tokens of 1024 channels, SiLU, 72 us (first pass 26, joining 11, second 29),
 // x read twice; gradients of packed 20011 tokens of 330 float32 channels in groups of 55, value by value, 85 us.

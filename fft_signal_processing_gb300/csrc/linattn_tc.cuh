@@ -25,9 +25,9 @@
 // They meet at mbarriers, each of which completes once per chunk (twice-buffered ones every other
 // chunk); every wait is bounded in time.
 //
-// Measured: one sequence of 16384 tokens, 16 heads of 128 x 128, time cut in 9: 152 us, 1.8 TB/s of q, k,
+// Measured: one sequence of 16384 tokens, 16 heads of 128 x 128, time cut in 9: 148 us, 1.8 TB/s of q, k,
 // v and outputs; 8 x 2048 tokens of 32 heads of 128 x 64 169 us; gradients of 4 x 2048 tokens of 16 heads
-// 486 us.  A chunk takes about 9300 cycles, the units' products about 4500 of them (scores 1000, with
+// 455 us.  A chunk takes about 9300 cycles, the units' products about 4500 of them (scores 1000, with
 // the state 1000, outputs 600, state 1800): bound by the chain from weighted z over the state's product to
 // the next chunk's, and within it by the latency of the weighting at three warps a scheduler.
 #pragma once
