@@ -14,8 +14,9 @@
 // at a stride.  Longer sequences are read twice, by blocks of a tile of tokens and whole groups: the
 // first pass leaves mean and sum of squares of every tile, joined by counts (Chan, Golub and
 // LeVeque's update), the second one runs through the tiles from the last one on, which the first
-// has left in L2.  Its sums are taken about one of the group's own values, so that groups far from
-// zero lose nothing.
+// has left in L2.  Sums are taken about the mean of the few values that a thread holds at once and
+// runs of them are joined about their means, so that neither a level that all values share nor one
+// value far from the rest costs the others their digits.
 #include "launch_cache.cuh"
 #include "seq_common.cuh"
 #include "seq_overlap.h"
@@ -32,7 +33,7 @@ struct GnArgs {
     fft_seq dout, dz;
     float* mean;           // [sequence][group]
     float* rstd;
-    float* records;        // tiles' origin, sum and squares, or sums of w and w n: [record][group][3]
+    float* records;        // tiles' origin, sum and squares about it, or sums of w and w n: [record][group][3]
     float* sums;           // [sequence][group][2]: mean(w) and mean(w n)
     float* parts;          // [part][2][channels]: dweight, dbias
     int64_t rows, tile, tiles;
@@ -368,49 +369,83 @@ __device__ __forceinline__ void by_group(int groups, int packs, int single, Join
     }
 }
 
+// What a run of values leaves: how many (exact: a tile has fewer than 2^24), their mean in two floats, the
+// sum of squares about it.
+struct Moments {
+    float n, hi, lo, m2;
+};
+__device__ __forceinline__ Moments join(const Moments& a, const Moments& b) {
+    if (b.n == 0.f) return a;
+    if (a.n == 0.f) return b;
+    const float n = a.n + b.n, part = b.n * rcp(n), delta = (b.hi - a.hi) + (b.lo - a.lo), move = delta * part;
+    const float hi = a.hi + move, t = hi - a.hi;
+    const float lost = (a.hi - (hi - t)) + (move - t);  // by the rounding of hi
+    return {n, hi, a.lo + lost, a.m2 + b.m2 + delta * (a.n * part) * delta};
+}
+
 template <class T, int VEC>
 __global__ void __launch_bounds__(kThreads) k_gn_moments(const GnArgs a) {
-    __shared__ float red[2][kThreads];
+    __shared__ Moments red[kThreads];
     const fft_gnorm_desc& d = a.d;
     const TileAt t = tile_at(a, false);
     const int tx = (int)threadIdx.x, ty = (int)threadIdx.y, bx = (int)blockDim.x, by = (int)blockDim.y;
     const int packs = a.cg / VEC, all = packs * t.groups;
     const T* base = static_cast<const T*>(d.x.data) + t.row * d.x.seq_stride + (int64_t)t.group0 * a.cg;
+    constexpr int DEEP = VEC > 1 ? 8 : 16;  // tokens of a run
     for (int64_t at = t.t0; at < t.t1;) {
         const SeqAt s = part_at(a, t.row, at, t.t1);
-        float s1 = 0.f, s2 = 0.f;
+        const int64_t first = s.begin + ty, hop = by * d.x.tok_stride;
+        const int count = s.end > first ? (int)((s.end - first + by - 1) / by) : 0;
+        Moments all_of = {};
         for (int p = tx; p < all; p += bx) {
-            const T* x = base + p * VEC;
-            const float shift = to_f(base[s.begin * d.x.tok_stride + p / packs * a.cg]);
-            float2 v1 = splat(0.f), v2 = splat(0.f);
-#pragma unroll 8
-            for (int64_t i = s.begin + ty; i < s.end; i += by) {
-                const Values<VEC> v = unpack<T, VEC>(ld_pack<VEC>(x + i * d.x.tok_stride));
+            const T* x = base + p * VEC + first * d.x.tok_stride;
+            for (int i0 = 0; i0 < count; i0 += DEEP) {
+                Pack<T, VEC> px[DEEP];
 #pragma unroll
-                for (int k = 0; k < v.N; ++k) {
-                    float2 e = add2(v.v[k], minus(shift));
-                    if (VEC == 1) e.y = 0.f;
-                    v1 = add2(v1, e);
-                    v2 = fma2(e, e, v2);
+                for (int u = 0; u < DEEP; ++u) px[u] = load<T, VEC>(x, i0 + u < count), x += hop;
+                const int live = count - i0 < DEEP ? count - i0 : DEEP;
+                const float n = (float)(live * VEC), inv = rcp(n);
+                // near the mean (zeros behind the last token add nothing)
+                float2 v = splat(0.f);
+#pragma unroll
+                for (int u = 0; u < DEEP; ++u) {
+                    const Values<VEC> e = unpack<T, VEC>(px[u]);
+#pragma unroll
+                    for (int k = 0; k < e.N; ++k) v = fma2(e.v[k], splat(inv), v);
                 }
-            }
-            s1 += v1.x + v1.y, s2 += v2.x + v2.y;
-        }
-        red[0][ty * bx + tx] = s1, red[1][ty * bx + tx] = s2;
-        __syncthreads();
-        by_group(t.groups, packs, a.each == 1, [&](int g, int lane, int first, int count) {
-            float v1 = 0.f, v2 = 0.f;
-            for (int i = lane; i < count * by; i += 32) {
-                const int at2 = i / count * bx + first + i % count;
-                v1 += red[0][at2], v2 += red[1][at2];
-            }
+                const float mid = v.x + v.y;
+                float2 v1 = splat(0.f), v2 = splat(0.f);
 #pragma unroll
-            for (int o = 16; o; o >>= 1) v1 += __shfl_xor_sync(0xffffffffu, v1, o), v2 += __shfl_xor_sync(0xffffffffu, v2, o);
+                for (int u = 0; u < DEEP; ++u) {
+                    if (u >= live) break;
+                    const Values<VEC> e = unpack<T, VEC>(px[u]);
+#pragma unroll
+                    for (int k = 0; k < e.N; ++k) {
+                        float2 w = add2(e.v[k], minus(mid));
+                        if (VEC == 1) w.y = 0.f;
+                        v1 = add2(v1, w);
+                        v2 = fma2(w, w, v2);
+                    }
+                }
+                const float rest = (v1.x + v1.y) * inv, squares = v2.x + v2.y;
+                // (squares beyond float32 stay infinite)
+                all_of = join(all_of, {n, mid, rest, squares < INFINITY ? fmaf(-rest * n, rest, squares) : squares});
+            }
+        }
+        red[ty * bx + tx] = all_of;
+        __syncthreads();
+        by_group(t.groups, packs, a.each == 1, [&](int g, int lane, int first_tx, int threads) {
+            Moments m = {};
+            for (int i = lane; i < threads * by; i += 32) m = join(m, red[i / threads * bx + first_tx + i % threads]);
+#pragma unroll
+            for (int o = 16; o; o >>= 1)
+                m = join(m, {__shfl_xor_sync(0xffffffffu, m.n, o), __shfl_xor_sync(0xffffffffu, m.hi, o),
+                             __shfl_xor_sync(0xffffffffu, m.lo, o), __shfl_xor_sync(0xffffffffu, m.m2, o)});
             if (lane == 0) {
                 float* r = a.records + (record_of(a, t.row, t.tile, s.q) * d.groups + t.group0 + g) * 3;
-                r[0] = to_f(base[s.begin * d.x.tok_stride + g * a.cg]);  // what the sums are counted from
-                r[1] = v1;
-                r[2] = v2;
+                r[0] = m.hi;  // what the sums are counted from
+                r[1] = m.n * m.lo;
+                r[2] = fmaf(m.n * m.lo, m.lo, m.m2);
             }
         });
         __syncthreads();
