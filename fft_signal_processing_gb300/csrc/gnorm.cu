@@ -37,8 +37,8 @@ struct GnArgs {
     float* sums;           // [sequence][group][2]: mean(w) and mean(w n)
     float* parts;          // [part][2][channels]: dweight, dbias
     int64_t rows, tile, tiles;
+    int64_t walks;         // that all rows' tiles are dealt to for the sums of the gradients
     int cg, each, sets;    // channels of a group; groups of a block, blocks for all groups
-    int backward;
 };
 
 // VEC values as pairs, two float32 operations to an instruction (of one value: the first of a pair
@@ -333,17 +333,19 @@ struct TileAt {
     int64_t row, tile, t0, t1;
     int group0, groups;
 };
-__device__ __forceinline__ TileAt tile_at(const GnArgs& a, bool last_first) {
-    int64_t b = last_first ? (int64_t)gridDim.x - 1 - blockIdx.x : blockIdx.x;
+__device__ __forceinline__ TileAt tile_of_set(const GnArgs& a, int set, int64_t n) {
     TileAt t;
-    t.group0 = (int)(b % a.sets) * a.each;
-    b /= a.sets;
-    t.tile = b % a.tiles;
-    t.row = b / a.tiles;
+    t.group0 = set * a.each;
+    t.tile = n % a.tiles;
+    t.row = n / a.tiles;
     t.t0 = t.tile * a.tile;
     t.t1 = t.t0 + a.tile < a.d.length ? t.t0 + a.tile : a.d.length;
     t.groups = (int)a.d.groups - t.group0 < a.each ? (int)a.d.groups - t.group0 : a.each;
     return t;
+}
+__device__ __forceinline__ TileAt tile_at(const GnArgs& a, bool last_first) {
+    const int64_t b = last_first ? (int64_t)gridDim.x - 1 - blockIdx.x : blockIdx.x;
+    return tile_of_set(a, (int)(b % a.sets), b / a.sets);
 }
 // Tokens of one sequence in a tile, from token `at` on; offsets of any kind stay in the tile.
 __device__ __forceinline__ SeqAt part_at(const GnArgs& a, int64_t row, int64_t at, int64_t t1) {
@@ -612,95 +614,101 @@ __global__ void __launch_bounds__(kThreads, VEC > 1 ? 2 : 4) k_gn_apply(const Gn
     }
 }
 
-// First pass of the gradients: sums of w and w n of every part, of dy n and dy of every channel.
+// First pass of the gradients: sums of w and w n of every part, of dy n and dy of every channel.  A block
+// takes a set's tiles at a stride and leaves one row of channel sums for all of them.
 template <class T, int VEC>
 __global__ void __launch_bounds__(kThreads, VEC > 1 ? 2 : 4) k_gn_sums(const GnArgs a) {
     __shared__ float red[2][kThreads];
     extern __shared__ float chans[];  // [2][ty][tx * VEC]
     const fft_gnorm_desc& d = a.d;
-    const TileAt t = tile_at(a, false);
+    const int set = (int)(blockIdx.x % (unsigned)a.sets);
+    const int64_t walk = blockIdx.x / (unsigned)a.sets, all_tiles = a.rows * a.tiles;
+    const int64_t c0 = (int64_t)set * a.each * a.cg;
     const int tx = (int)threadIdx.x, ty = (int)threadIdx.y, bx = (int)blockDim.x, by = (int)blockDim.y;
-    const int packs = a.cg / VEC, all = packs * t.groups, tid = ty * bx + tx;
+    const int packs = a.cg / VEC, all = packs * tile_of_set(a, set, 0).groups, tid = ty * bx + tx;
     const bool gate = d.z.data;
     // packs outermost, since a channel's sums run over all parts; with several rounds of packs (a
     // set of one group of many channels) the parts' sums go on from what is there
     for (int p0 = 0; p0 < all; p0 += bx) {
         const int p = p0 + tx;
         const bool in = p < all;
-        const int64_t c = (int64_t)t.group0 * a.cg + p * VEC;
+        const int64_t c = c0 + p * VEC;
         Channel<T, VEC> ch;
         ch.load(d, c, in);
         Values<VEC> dw, db;
 #pragma unroll
         for (int k = 0; k < dw.N; ++k) dw.v[k] = db.v[k] = splat(0.f);
-        for (int64_t at = t.t0; at < t.t1;) {
-            const SeqAt s = part_at(a, t.row, at, t.t1);
-            float s1 = 0.f, s2 = 0.f;
-            if (in) {
-                const int64_t g = t.group0 + p / packs;
-                const float mean = a.mean[s.q * d.groups + g], rstd = a.rstd[s.q * d.groups + g];
-                const T* x = static_cast<const T*>(d.x.data) + t.row * d.x.seq_stride + c;
-                const T* z = static_cast<const T*>(d.z.data) + t.row * d.z.seq_stride + c;
-                const T* go = static_cast<const T*>(a.dout.data) + t.row * a.dout.seq_stride + c;
-                float2 p1 = splat(0.f), p2 = splat(0.f);
-                constexpr int DEEP = VEC == 1 ? 4 : 2;  // tokens loaded before the first of them is used
-                const int64_t first = s.begin + ty, hx = by * d.x.tok_stride, hz = by * d.z.tok_stride,
-                              hg = by * a.dout.tok_stride;
-                x += first * d.x.tok_stride, go += first * a.dout.tok_stride;
-                if (gate) z += first * d.z.tok_stride;
-                const int count = s.end > first ? (int)((s.end - first + by - 1) / by) : 0;
-                for (int i0 = 0; i0 < count; i0 += DEEP) {
-                    Pack<T, VEC> px[DEEP], pz[DEEP], pg[DEEP];
+        for (int64_t n = walk; n < all_tiles; n += a.walks) {
+            const TileAt t = tile_of_set(a, set, n);
+            for (int64_t at = t.t0; at < t.t1;) {
+                const SeqAt s = part_at(a, t.row, at, t.t1);
+                float s1 = 0.f, s2 = 0.f;
+                if (in) {
+                    const int64_t g = t.group0 + p / packs;
+                    const float mean = a.mean[s.q * d.groups + g], rstd = a.rstd[s.q * d.groups + g];
+                    const T* x = static_cast<const T*>(d.x.data) + t.row * d.x.seq_stride + c;
+                    const T* z = static_cast<const T*>(d.z.data) + t.row * d.z.seq_stride + c;
+                    const T* go = static_cast<const T*>(a.dout.data) + t.row * a.dout.seq_stride + c;
+                    float2 p1 = splat(0.f), p2 = splat(0.f);
+                    constexpr int DEEP = VEC == 1 ? 4 : 2;  // tokens loaded before the first of them is used
+                    const int64_t first = s.begin + ty, hx = by * d.x.tok_stride, hz = by * d.z.tok_stride,
+                                  hg = by * a.dout.tok_stride;
+                    x += first * d.x.tok_stride, go += first * a.dout.tok_stride;
+                    if (gate) z += first * d.z.tok_stride;
+                    const int count = s.end > first ? (int)((s.end - first + by - 1) / by) : 0;
+                    for (int i0 = 0; i0 < count; i0 += DEEP) {
+                        Pack<T, VEC> px[DEEP], pz[DEEP], pg[DEEP];
 #pragma unroll
-                    for (int u = 0; u < DEEP; ++u) {
-                        const bool in = i0 + u < count;
-                        px[u] = load<T, VEC>(x, in);
-                        pg[u] = load<T, VEC>(go, in);
-                        pz[u] = load<T, VEC>(z, in && gate);
-                        x += hx, go += hg;
-                        if (gate) z += hz;
-                    }
-#pragma unroll
-                    for (int u = 0; u < DEEP; ++u) {
-                        Values<VEC> n = unpack<T, VEC>(px[u]), y, dzv, zv = unpack<T, VEC>(pz[u]), gv = unpack<T, VEC>(pg[u]);
-#pragma unroll
-                        for (int k = 0; k < n.N; ++k) {
-                            n.v[k] = mul2(add2(n.v[k], minus(mean)), splat(rstd));
-                            if (VEC == 1) n.v[k].y = 0.f;
-                            y.v[k] = fma2(n.v[k], ch.w.v[k], ch.b.v[k]);
+                        for (int u = 0; u < DEEP; ++u) {
+                            const bool in = i0 + u < count;
+                            px[u] = load<T, VEC>(x, in);
+                            pg[u] = load<T, VEC>(go, in);
+                            pz[u] = load<T, VEC>(z, in && gate);
+                            x += hx, go += hg;
+                            if (gate) z += hz;
                         }
-                        reaches<VEC>(d, y, zv, gv, dzv);
 #pragma unroll
-                        for (int k = 0; k < n.N; ++k) {
-                            if (i0 + u >= count) break;  // (a statistic that is no number times 0 is none)
-                            const float2 dn = mul2(y.v[k], n.v[k]);
-                            dw.v[k] = add2(dw.v[k], dn);
-                            db.v[k] = add2(db.v[k], y.v[k]);
-                            p1 = fma2(y.v[k], ch.w.v[k], p1);
-                            p2 = fma2(dn, ch.w.v[k], p2);
+                        for (int u = 0; u < DEEP; ++u) {
+                            Values<VEC> n = unpack<T, VEC>(px[u]), y, dzv, zv = unpack<T, VEC>(pz[u]), gv = unpack<T, VEC>(pg[u]);
+#pragma unroll
+                            for (int k = 0; k < n.N; ++k) {
+                                n.v[k] = mul2(add2(n.v[k], minus(mean)), splat(rstd));
+                                if (VEC == 1) n.v[k].y = 0.f;
+                                y.v[k] = fma2(n.v[k], ch.w.v[k], ch.b.v[k]);
+                            }
+                            reaches<VEC>(d, y, zv, gv, dzv);
+#pragma unroll
+                            for (int k = 0; k < n.N; ++k) {
+                                if (i0 + u >= count) break;  // (a statistic that is no number times 0 is none)
+                                const float2 dn = mul2(y.v[k], n.v[k]);
+                                dw.v[k] = add2(dw.v[k], dn);
+                                db.v[k] = add2(db.v[k], y.v[k]);
+                                p1 = fma2(y.v[k], ch.w.v[k], p1);
+                                p2 = fma2(dn, ch.w.v[k], p2);
+                            }
                         }
                     }
+                    s1 = p1.x + p1.y, s2 = p2.x + p2.y;
                 }
-                s1 = p1.x + p1.y, s2 = p2.x + p2.y;
+                red[0][tid] = s1, red[1][tid] = s2;
+                __syncthreads();
+                by_group(t.groups, packs, a.each == 1, [&](int g, int lane, int first, int count) {
+                    float v1 = 0.f, v2 = 0.f;
+                    for (int i = lane; i < count * by; i += 32) {
+                        const int at2 = i / count * bx + first + i % count;
+                        v1 += red[0][at2], v2 += red[1][at2];
+                    }
+#pragma unroll
+                    for (int o = 16; o; o >>= 1) v1 += __shfl_xor_sync(0xffffffffu, v1, o), v2 += __shfl_xor_sync(0xffffffffu, v2, o);
+                    if (lane == 0) {
+                        float* r = a.records + (record_of(a, t.row, t.tile, s.q) * d.groups + t.group0 + g) * 3;
+                        r[0] = p0 ? r[0] + v1 : v1;
+                        r[1] = p0 ? r[1] + v2 : v2;
+                    }
+                });
+                __syncthreads();
+                at = s.end;
             }
-            red[0][tid] = s1, red[1][tid] = s2;
-            __syncthreads();
-            by_group(t.groups, packs, a.each == 1, [&](int g, int lane, int first, int count) {
-                float v1 = 0.f, v2 = 0.f;
-                for (int i = lane; i < count * by; i += 32) {
-                    const int at2 = i / count * bx + first + i % count;
-                    v1 += red[0][at2], v2 += red[1][at2];
-                }
-#pragma unroll
-                for (int o = 16; o; o >>= 1) v1 += __shfl_xor_sync(0xffffffffu, v1, o), v2 += __shfl_xor_sync(0xffffffffu, v2, o);
-                if (lane == 0) {
-                    float* r = a.records + (record_of(a, t.row, t.tile, s.q) * d.groups + t.group0 + g) * 3;
-                    r[0] = p0 ? r[0] + v1 : v1;
-                    r[1] = p0 ? r[1] + v2 : v2;
-                }
-            });
-            __syncthreads();
-            at = s.end;
         }
         if (!a.parts) continue;
 #pragma unroll
@@ -709,7 +717,7 @@ __global__ void __launch_bounds__(kThreads, VEC > 1 ? 2 : 4) k_gn_sums(const GnA
             chans[(bx * by + tid) * VEC + k] = k & 1 ? db.v[k / 2].y : db.v[k / 2].x;
         }
         __syncthreads();
-        float* out = a.parts + (t.row * a.tiles + t.tile) * 2 * d.channels + (int64_t)t.group0 * a.cg + (int64_t)p0 * VEC;
+        float* out = a.parts + walk * 2 * d.channels + c0 + (int64_t)p0 * VEC;
         const int width = (all - p0 < bx ? all - p0 : bx) * VEC;
         for (int i = tid; i < 2 * width; i += bx * by) {
             const int which = i / width, k = i % width;
@@ -787,6 +795,24 @@ int64_t tile_of(const fft_gnorm_desc& d) {
     while (tile > 16 && rows * ((d.length + tile - 1) / tile) * wide < (int64_t)num_sms() * 8) tile /= 2;
     return tile;
 }
+// Groups of a block and blocks for all of them, of like size, with packs of `vec` values.
+void gnorm_sets(const fft_gnorm_desc& d, int64_t vec, GnArgs* a) {
+    const int64_t packs = d.channels / d.groups / vec;
+    int64_t each = packs >= kThreads ? 1 : kThreads / packs;
+    if (each > d.groups) each = d.groups;
+    a->sets = (int)((d.groups + each - 1) / each);
+    a->each = (int)((d.groups + a->sets - 1) / a->sets);
+    // Walks of the gradients' sums, each of which leaves two rows of channels: eight blocks for every SM (fewer
+    // where a block takes its channels in several rounds, one at least), and no more than 65536 tokens for a
+    // walk, whose threads' sums are float32.  One for every tile instead left rows of four times the bytes of
+    // x where sequences are short (16384 rows of 4096 channels in 4 groups: 538 MB of workspace, 21 MB now).
+    const int64_t rounds = (packs + kThreads - 1) / kThreads, tokens = a->rows * d.length;
+    const int64_t most = a->rows * a->tiles, sms = num_sms();
+    int64_t walks = sms * 8 / (a->sets * rounds);
+    if (walks < sms / a->sets) walks = sms / a->sets;
+    if (walks < tokens / 65536) walks = tokens / 65536;
+    a->walks = walks < 1 ? 1 : (walks < most ? walks : most);
+}
 int64_t gnorm_layout(const fft_gnorm_desc& d, bool backward, GnArgs* a, char* w) {
     int64_t at = 0;
     auto take = [&](int64_t floats) {
@@ -807,7 +833,10 @@ int64_t gnorm_layout(const fft_gnorm_desc& d, bool backward, GnArgs* a, char* w)
     a->records = take((a->rows * a->tiles + (d.offsets ? d.nseq : 0)) * d.groups * 3);
     if (backward) {
         a->sums = take(d.nseq * d.groups * 2);
-        a->parts = take(a->rows * a->tiles * 2 * d.channels);
+        // rows off 16-byte boundaries go value by value, which makes no fewer sets and so no more walks
+        const int64_t vec = 16 / (int64_t)dtype_size(d.dtype);
+        gnorm_sets(d, a->cg % vec ? 1 : vec, a);
+        a->parts = take(a->walks * 2 * d.channels);
     }
     return at;
 }
@@ -858,10 +887,7 @@ cudaError_t run_token(const GnArgs& a, int64_t* parts, cudaStream_t s) {
 template <class T, int VEC, bool BWD>
 cudaError_t run_tiles(GnArgs a, int64_t* parts, cudaStream_t s) {
     const int packs = a.cg / VEC;
-    a.each = packs >= kThreads ? 1 : kThreads / packs;
-    if (a.each > a.d.groups) a.each = (int)a.d.groups;
-    a.sets = (int)((a.d.groups + a.each - 1) / a.each);
-    a.each = (int)((a.d.groups + a.sets - 1) / a.sets);  // of like size
+    gnorm_sets(a.d, VEC, &a);
     const int all = packs * a.each;
     int bx = 1;  // whole warps: a power of two, or a multiple of 32
     while (bx < 32 && bx < all) bx *= 2;
@@ -869,11 +895,11 @@ cudaError_t run_tiles(GnArgs a, int64_t* parts, cudaStream_t s) {
     const int by = kThreads / bx;
     const int64_t blocks = a.rows * a.tiles * a.sets, joins = (a.d.nseq * a.d.groups + 7) / 8;
     if (blocks > INT32_MAX || joins > INT32_MAX) return cudaErrorInvalidValue;
-    *parts = a.rows * a.tiles;
+    *parts = a.walks;
     const dim3 threads((unsigned)bx, (unsigned)by);
     const unsigned n = (unsigned)blocks;
     if constexpr (BWD)
-        k_gn_sums<T, VEC><<<n, threads, 2 * bx * by * VEC * sizeof(float), s>>>(a);
+        k_gn_sums<T, VEC><<<(unsigned)(a.walks * a.sets), threads, 2 * bx * by * VEC * sizeof(float), s>>>(a);
     else
         k_gn_moments<T, VEC><<<n, threads, 0, s>>>(a);
     k_gn_join<BWD><<<(unsigned)joins, kThreads, 0, s>>>(a);
@@ -978,7 +1004,6 @@ extern "C" int fft_gnorm_backward(const fft_gnorm_desc* d, const fft_gnorm_grads
         a.dz = g->dz;
         a.mean = const_cast<float*>(g->mean);
         a.rstd = const_cast<float*>(g->rstd);
-        a.backward = 1;
         if (!g->dweight && !g->dbias) a.parts = nullptr;
         e = d->dtype == FFT_F32 ? run_gnorm<float, true>(a, &parts, s)
                                 : (d->dtype == FFT_BF16 ? run_gnorm<__nv_bfloat16, true>(a, &parts, s)
