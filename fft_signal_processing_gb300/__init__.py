@@ -29,7 +29,7 @@ from . import sequence
 from .sequence import (causal_conv, causal_conv_backward, causal_conv_step, group_norm,
                        group_norm_backward, linear_attention,
                        linear_attention_backward, linear_attention_check,
-                       linear_attention_step, residual_norm, residual_norm_backward,
+                       linear_attention_set_wait_timeout, linear_attention_step, residual_norm, residual_norm_backward,
                        selective_scan, selective_scan_backward, selective_scan_step)
 
 FORWARD = -1

@@ -50,6 +50,7 @@ struct AttnArgs {
     int* carry_reset;    // [row][segment][head]
     float* dots_inter;   // [ztile][head][row * length + t]
     float* dots_all;
+    uint32_t wait_ns;  // limit of a device-side wait; 0: none is begun
 };
 
 // Padded sizes of the kernel's variants.

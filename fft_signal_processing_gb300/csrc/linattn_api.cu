@@ -1,6 +1,8 @@
 // C entry points of linear attention: checks on the host, cuts of time, workspace layout, and the
 // kernels around k_linattn (gradients of the decay and of shared heads, states of sequences without
 // tokens, single tokens).  Declared in include/gbfft.h.
+#include <atomic>
+
 #include "linattn.h"
 #include "seq_overlap.h"
 #include "tma.cuh"
@@ -591,10 +593,12 @@ bool tc_rows(const AttnArgs& a) {
     return a.x.vec == 16 && a.y.vec == 16 && a.z.vec == 16 && (!a.partner.data || a.partner.vec == 16) &&
            aligned_to(a.out, 16) && even(a.out_seq) && even(a.out_tok) && even(a.out_head);
 }
-cudaError_t run_tc(const AttnArgs& a, bool backward, cudaStream_t s) {
+std::atomic<uint32_t> g_wait_ns{2000000000u};  // limit of a device-side wait
+cudaError_t run_tc(AttnArgs a, bool backward, cudaStream_t s) {
     int* err = nullptr;
     const cudaError_t e = error_word(&err);
     if (e != cudaSuccess) return e;
+    a.wait_ns = g_wait_ns.load();
     return backward ? attn_tc_bwd(a, err, s) : attn_tc_fwd(a, err, s);
 }
 cudaError_t run_forward(const AttnArgs& a, int dtype, cudaStream_t s) {
@@ -757,6 +761,11 @@ extern "C" int fft_linattn_check(void* stream) {
     if (h == 0) return FFT_OK;
     if (cudaMemset(word, 0, sizeof(int)) != cudaSuccess) return FFT_ERR_CUDA;
     return kerr_status(h);
+}
+
+extern "C" int fft_linattn_set_wait_timeout(uint64_t ns) {
+    g_wait_ns.store(ns < 4000000000u ? (uint32_t)ns : 4000000000u);
+    return FFT_OK;
 }
 
 extern "C" int fft_linattn_step(const fft_linattn_desc* d, const fft_heads* out, float* state, int64_t pool,

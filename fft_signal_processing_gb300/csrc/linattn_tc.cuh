@@ -22,12 +22,15 @@
 //   that copy do nothing else.
 // A weight exp(G[r] - G[c]) of another block of 32 columns than the row's own is a product of one
 // factor for each row and one for each column, both from the end of the columns' block (at most 1).
-// They meet at mbarriers, each of which completes once per chunk (twice-buffered ones every other
-// chunk); every wait is bounded in time.
+// They meet at mbarriers only, each of which completes once per chunk (twice-buffered ones every other
+// chunk).  Every wait is bounded in time, and a warp's lanes give up together, so that none of them goes
+// on into an instruction of the whole warp alone.  A warp that gives up goes to the block's end; those that
+// wait for it give up in turn, the warp that issues products waits for them there, and so no product
+// outlives its block.
 //
-// Measured: one sequence of 16384 tokens, 16 heads of 128 x 128, time cut in 9: 148 us, 1.8 TB/s of q, k,
-// v and outputs; 8 x 2048 tokens of 32 heads of 128 x 64 169 us; gradients of 4 x 2048 tokens of 16 heads
-// 455 us.  A chunk takes about 9300 cycles, the units' products about 4500 of them (scores 1000, with
+// Measured: one sequence of 16384 tokens, 16 heads of 128 x 128, time cut in 9: 158 us, 1.7 TB/s of q, k,
+// v and outputs; 8 x 2048 tokens of 32 heads of 128 x 64 175 us; gradients of 4 x 2048 tokens of 16 heads
+// 459 us.  A chunk takes about 9300 cycles, the units' products about 4500 of them (scores 1000, with
 // the state 1000, outputs 600, state 1800): bound by the chain from weighted z over the state's product to
 // the next chunk's, and within it by the latency of the weighting at three warps a scheduler.
 #pragma once
@@ -41,7 +44,6 @@ namespace {
 using bf16 = __nv_bfloat16;
 constexpr int kTcChunk = 128;
 constexpr int kTcB = 256;  // threads of B
-constexpr uint64_t kTcWaitNs = 2000000000ull;
 
 // ---- tcgen05 --------------------------------------------------------------------------------
 
@@ -193,7 +195,7 @@ struct TcShape {
 };
 
 enum { TC_X, TC_Y0, TC_Y1, TC_Z0, TC_Z1, TC_SCORES, TC_INTER, TC_OUT, TC_UPDATE0, TC_UPDATE1, TC_WEIGHTED, TC_STATE, TC_WZ, TC_TAKEN0, TC_TAKEN1, TC_DECAYS,
-       TC_FREE, TC_BARS };
+       TC_FREE, TC_PAIR0, TC_PAIR1, TC_PAIR2, TC_PAIR3, TC_MEET, TC_DRAIN, TC_BARS };
 
 // Behind the tiles.  BUFFERS: stages of z.
 template <bool BWD, int BUFFERS>
@@ -284,8 +286,19 @@ __device__ __forceinline__ void tc_transpose(uint4 (&p)[4], int lane) {
     swap(p[0], p[1], 1);
     swap(p[2], p[3], 1);
 }
-__device__ __forceinline__ void tc_meet(int bar, int threads) {
-    asm volatile("bar.sync %0, %1;" ::"r"(bar), "r"(threads) : "memory");
+
+// Waits for at most `limit` nanoseconds, by the low half of the timer, which passes 0 every 4.3 s.
+__device__ __forceinline__ uint32_t tc_ns() {
+    uint32_t t;
+    asm volatile("mov.u32 %0, %%globaltimer_lo;" : "=r"(t));
+    return t;
+}
+__device__ __forceinline__ bool tc_lane_wait(uint64_t* bar, uint32_t parity, uint32_t limit) {
+    if (mbar_try_wait(bar, parity)) return true;
+    const uint32_t begun = tc_ns();
+    while (!mbar_try_wait(bar, parity))
+        if (tc_ns() - begun > limit) return false;
+    return true;
 }
 
 template <int DX, int DZ, bool BWD>
@@ -303,6 +316,10 @@ __global__ void __launch_bounds__(TcShape<DX, DZ, BWD>::kThreads, 1) k_linattn_t
     Small& sm = *reinterpret_cast<Small*>(base + Shape::kTiles);
     uint64_t* bars = sm.bars;
     if (!tma_stage_aligned(base, err) || (smem_addr(base) & 1023)) return;  // every thread alike
+    if (a.wait_ns == 0) {  // a limit of 0: no wait is begun
+        if (threadIdx.x == 0) atomicCAS(err, 0, KERR_WAIT_TIMEOUT);
+        return;
+    }
 
     const int tid = (int)threadIdx.x, warp = tid >> 5, lane = tid & 31;
     // lengths and counts of blocks are below 2^31
@@ -323,9 +340,10 @@ __global__ void __launch_bounds__(TcShape<DX, DZ, BWD>::kThreads, 1) k_linattn_t
     }
     if (tid == 0) {
         for (int i = 0; i < TC_BARS; ++i) {
-            const bool commit = i == TC_SCORES || i == TC_INTER || i == TC_OUT || i == TC_UPDATE0 || i == TC_UPDATE1;
+            const bool commit = i == TC_SCORES || i == TC_INTER || i == TC_OUT || i == TC_UPDATE0 || i == TC_UPDATE1 || i == TC_DRAIN;
             const bool warps = i == TC_DECAYS || (i >= TC_X && i <= TC_Z1);
-            mbar_init(&bars[i], commit ? 1 : (warps ? 32 : (i == TC_FREE ? Shape::kA + kTcB : (i == TC_STATE || i == TC_WZ ? kTcB : Shape::kA))));
+            const bool all_b = i == TC_STATE || i == TC_WZ || i == TC_MEET, pair = i >= TC_PAIR0 && i <= TC_PAIR3;
+            mbar_init(&bars[i], commit ? 1 : (warps ? 32 : (pair ? 64 : (i == TC_FREE ? Shape::kA + kTcB : (all_b ? kTcB : Shape::kA)))));
         }
         fence_mbar_init();
     }
@@ -336,7 +354,10 @@ __global__ void __launch_bounds__(TcShape<DX, DZ, BWD>::kThreads, 1) k_linattn_t
     const uint32_t kOut = tmem + 128, kAdd = tmem + 256, kWz = tmem + 384;
     const uint32_t lanes = (uint32_t)(warp & 3) << 21;  // this warp's rows: 32 (warp mod 4) in bits 16 up
 
-    auto wait = [&](int bar, uint32_t phase) { return mbar_wait_bounded(&bars[bar], phase & 1, kTcWaitNs); };
+    // The votes and a limit that is an argument cost 1 to 6% (148, 169 and 455 us without them): a lane that went
+    // on alone, or a warp that waited for one that has left, would not end.
+    auto lane_wait = [&](int bar, uint32_t phase) { return tc_lane_wait(&bars[bar], phase & 1, a.wait_ns); };
+    auto wait = [&](int bar, uint32_t phase) { return __all_sync(0xffffffffu, lane_wait(bar, phase)) != 0; };
     // Calls f(part, n) for every part of the segment in the direction of the pass, n its first
     // chunk's number; a summary takes the part that reaches the next segment.
     auto each_part = [&](auto f) {
@@ -446,7 +467,10 @@ __global__ void __launch_bounds__(TcShape<DX, DZ, BWD>::kThreads, 1) k_linattn_t
                     tc_ld32(tmem + lanes + cb * 32 + 32, s[1]);
                     tc_wait_ld(s[0]);
                     tc_wait_ld(s[1]);
-                    if (SIDES == 2) tc_meet(2 + quad, 64);
+                    if (SIDES == 2) {  // once per chunk, as this loop runs once
+                        mbar_arrive(&bars[TC_PAIR0 + quad]);
+                        if (!wait(TC_PAIR0 + quad, n)) return false;
+                    }
                     weigh(cb, s[0]);
                     weigh(cb + 1, s[1]);
                 }
@@ -581,6 +605,7 @@ __global__ void __launch_bounds__(TcShape<DX, DZ, BWD>::kThreads, 1) k_linattn_t
         constexpr int HALF = DX / 2;
         const int x0 = side * HALF;
         float2 S[HALF / 2];  // row m of S^T, columns x0 ..
+        uint32_t met = 0;    // times that all of B has met
         const int64_t carry_at = ((((int64_t)row * a.nsegments + seg) * a.heads + head) * a.ztiles + zt) * (DX * 128) +
                                  (side * (HALF / 4) * 128 + m) * 4;
         // S as an operand: row m, columns in panels of 64
@@ -643,7 +668,7 @@ __global__ void __launch_bounds__(TcShape<DX, DZ, BWD>::kThreads, 1) k_linattn_t
                 float2 odd = splat(0.f);
                 // two blocks of 16 columns by four of 16 tokens; a loop, since addresses of all eight would be
                 // kept for the whole part
-#pragma unroll(BWD ? 1 : 2)
+#pragma unroll 1
                 for (int it = 0; it < 8; ++it) {
                     const int m0 = quad * 32 + (it & 1) * 16, tk = side * 64 + (it >> 1) * 16;
                     const float2 w0 = *reinterpret_cast<const float2*>(&sm.update[tk + 2 * (lane & 3)]);
@@ -716,13 +741,15 @@ __global__ void __launch_bounds__(TcShape<DX, DZ, BWD>::kThreads, 1) k_linattn_t
 #pragma unroll
                     for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
                     if (lane == 0) sm.warp_sums[warp - B0] = sum;
-                    tc_meet(1, kTcB);
+                    mbar_arrive(&bars[TC_MEET]);
+                    if (!wait(TC_MEET, met++)) return false;
                     if (id == 0) {
                         sum = 0.f;
                         for (int w = 0; w < 8; ++w) sum += sm.warp_sums[w];
                         a.final_dots[(zt * a.nseq + p.seq) * a.heads + head] = sum;
                     }
-                    tc_meet(1, kTcB);
+                    mbar_arrive(&bars[TC_MEET]);
+                    if (!wait(TC_MEET, met++)) return false;
                 }
             }
             return true;
@@ -736,11 +763,13 @@ __global__ void __launch_bounds__(TcShape<DX, DZ, BWD>::kThreads, 1) k_linattn_t
         // ---- the products, issued by one thread ----
         const uint32_t x = smem_addr(tile_x), y = smem_addr(tile_y), z = smem_addr(tile_z), s = smem_addr(tile_s),
                        w = smem_addr(tile_w);
+        bool issued = false;
         fine = each_part([&](const TcPart& p, int chunks, uint32_t n0) {
             bool good = true;
             const bool start = starts_with_state(p);
             auto scores = [&](uint32_t n) {
                 const uint32_t yn = y + (n & 1) * Shape::kTileX;
+                issued = true;
 #pragma unroll
                 for (int k = 0; k < DX / 16; ++k)
                     tc_mma(tmem, tc_columns(x, PANEL, k), tc_columns(yn, PANEL, k), tc_idesc(C, false), k > 0);
@@ -752,13 +781,13 @@ __global__ void __launch_bounds__(TcShape<DX, DZ, BWD>::kThreads, 1) k_linattn_t
                     const uint32_t yn = y + half * Shape::kTileX, zn = z + (Shape::kStageZ == 2 ? half * Shape::kTileZ : 0);
                     const bool some = i > 0 || start;
                     if (i == 0 || summary) {
-                        good = wait(TC_Y0 + half, n >> 1) &&
-                               (summary || (wait(TC_X, n) && (n == 0 || wait(TC_OUT, n - 1))));
+                        good = lane_wait(TC_Y0 + half, n >> 1) &&
+                               (summary || (lane_wait(TC_X, n) && (n == 0 || lane_wait(TC_OUT, n - 1))));
                         if (!good) break;
                         tc_after();
                         if (!summary) scores(n);
                     }
-                    good = wait(TC_STATE, n) && (summary || n == 0 || wait(TC_TAKEN0 + (half ^ 1), (n - 1) >> 1));
+                    good = lane_wait(TC_STATE, n) && (summary || n == 0 || lane_wait(TC_TAKEN0 + (half ^ 1), (n - 1) >> 1));
                     if (!good) break;
                     tc_after();
                     if (!summary) {
@@ -773,7 +802,7 @@ __global__ void __launch_bounds__(TcShape<DX, DZ, BWD>::kThreads, 1) k_linattn_t
                         tc_commit(&bars[TC_INTER]);  // once per chunk, whether there was a state or not
                     }
                     // outputs before the state: A works on them meanwhile
-                    good = wait(TC_WZ, n) && (summary || wait(TC_WEIGHTED, n));
+                    good = lane_wait(TC_WZ, n) && (summary || lane_wait(TC_WEIGHTED, n));
                     if (!good) break;
                     tc_after();
                     if (!summary) {
@@ -785,13 +814,14 @@ __global__ void __launch_bounds__(TcShape<DX, DZ, BWD>::kThreads, 1) k_linattn_t
                                           some || u < PO - 1 || k > 0);
                         tc_commit(&bars[TC_OUT]);
                     }
+                    issued = true;
 #pragma unroll
                     for (int k = 0; k < C / 16; ++k)
                         tc_mma(kAdd, tc_columns(w, PANEL, k), tc_desc(yn + k * 2048, PANEL), tc_idesc(DX, true), k > 0);
                     // The next chunk's scores between the pieces of the state, so that A has them in time;
                     // they go over this one's weighted scores, whose product is over by then.
                     if (i + 1 < chunks && !summary) {
-                        good = wait(TC_Y0 + (half ^ 1), (n + 1) >> 1) && wait(TC_X, n + 1) && wait(TC_OUT, n);
+                        good = lane_wait(TC_Y0 + (half ^ 1), (n + 1) >> 1) && lane_wait(TC_X, n + 1) && lane_wait(TC_OUT, n);
                         if (!good) break;
                         tc_after();
                         scores(n + 1);
@@ -806,6 +836,13 @@ __global__ void __launch_bounds__(TcShape<DX, DZ, BWD>::kThreads, 1) k_linattn_t
             }
             return __all_sync(0xffffffffu, good) != 0;
         });
+        // no product outlives the block, whoever has given up
+        bool over = true;
+        if (issued) {  // (by lane 0)
+            tc_commit(&bars[TC_DRAIN]);
+            over = mbar_wait_bounded(&bars[TC_DRAIN], 0, kDrainLimitNs);
+        }
+        fine = __all_sync(0xffffffffu, over) && fine;
     } else if (warp == M0 + 1) {
         // ---- decays: four tokens per lane ----
         const bf16* pg = static_cast<const bf16*>(a.decay.data) + row * a.decay.seq_stride + head;
@@ -913,7 +950,9 @@ __global__ void __launch_bounds__(TcShape<DX, DZ, BWD>::kThreads, 1) k_linattn_t
             });
     }
     copy_wait<0>();
-    if (!fine && lane == 0) atomicCAS(err, 0, KERR_WAIT_TIMEOUT);
+    if (!fine && lane == 0) atomicCAS(err, 0, KERR_WAIT_TIMEOUT);  // `fine` is the whole warp's
+    __syncwarp();
+    tc_wait_st();
     tc_before();
     __syncthreads();
     if (warp == M0) {

@@ -111,6 +111,7 @@ def declare(L):
     L.fft_linattn_forward.argtypes = [desc, desc, vp, vp, sz, vp]
     L.fft_linattn_backward.argtypes = [desc, desc, vp, sz, vp]
     L.fft_linattn_check.argtypes = [vp]
+    L.fft_linattn_set_wait_timeout.argtypes = [ctypes.c_uint64]
     L.fft_linattn_step.argtypes = [desc, desc, vp, i64, vp, vp, vp]
     L.fft_norm_forward.argtypes = [desc, vp, i64, vp, i64, vp, i64, vp, vp, i64, vp]
     L.fft_norm_workspace.argtypes = [desc, ctypes.POINTER(sz)]
@@ -124,7 +125,8 @@ def declare(L):
 SYMBOLS = ("fft_conv_forward", "fft_conv_workspace", "fft_conv_backward", "fft_conv_step",
            "fft_scan_workspace", "fft_scan_forward", "fft_scan_backward", "fft_scan_step",
            "fft_linattn_workspace", "fft_linattn_forward", "fft_linattn_backward",
-           "fft_linattn_step", "fft_linattn_check", "fft_norm_forward", "fft_norm_workspace", "fft_norm_backward",
+           "fft_linattn_step", "fft_linattn_check", "fft_linattn_set_wait_timeout", "fft_norm_forward",
+           "fft_norm_workspace", "fft_norm_backward",
            "fft_gnorm_workspace", "fft_gnorm_forward", "fft_gnorm_backward")
 
 
@@ -579,6 +581,14 @@ def linear_attention_check(stream=None):
     if _L is None:
         _setup()
     _check(_L.fft_linattn_check(_stream(stream, _device())[1]), "fft_linattn_check")
+
+
+def linear_attention_set_wait_timeout(ns=2 * 10 ** 9):
+    """Time limit of the device-side waits of the calls that follow (fft_linattn_set_wait_timeout); 0: each
+    gives up at once (a diagnostic hook)."""
+    if _L is None:
+        _setup()
+    _check(_L.fft_linattn_set_wait_timeout(int(ns)), "fft_linattn_set_wait_timeout")
 
 
 def linear_attention_step(state, q, k, v, decay, scale=None, slots=None, slots_out=None, out=None,

@@ -577,6 +577,11 @@ int fft_linattn_backward(const fft_linattn_desc* d, const fft_linattn_grads* g, 
  * or FFT_ERR_CUDA. */
 int fft_linattn_check(void* stream);
 
+/* fft_linattn_set_wait_timeout - time limit, in nanoseconds, of every device-side wait of the calls that
+ * follow, in all threads of the process (default 2 s, at most 4 s); 0 makes each wait give up at once (a
+ * diagnostic hook).  Returns FFT_OK. */
+int fft_linattn_set_wait_timeout(uint64_t ns);
+
 /* fft_linattn_step - one token for each of nseq sequences (length 1, offsets NULL, initial_state
  * not used; rows at seq_stride): state pool [pool][heads][dk][dv] float32, slots as for
  * fft_conv_step.  out may not overlap what is read. */
