@@ -2,6 +2,7 @@
 // kernels around k_linattn (gradients of the decay and of shared heads, states of sequences without
 // tokens, single tokens).  Declared in include/gbfft.h.
 #include <atomic>
+#include <mutex>
 
 #include "linattn.h"
 #include "seq_overlap.h"
@@ -582,8 +583,9 @@ template <class F32, class B16, class F16>
 cudaError_t by_type(int dtype, F32 f32, B16 b16, F16 f16, const AttnArgs& a, cudaStream_t s) {
     return dtype == FFT_F32 ? f32(a, s) : (dtype == FFT_BF16 ? b16(a, s) : f16(a, s));
 }
-// The device's error word: set by a wait that has run out.
-__device__ int g_attn_error;
+// The device's error word: set by a wait that has run out; and what a check has taken out of it.
+__device__ int g_attn_error, g_attn_taken;
+__global__ void k_take_error() { g_attn_taken = atomicExch(&g_attn_error, 0); }
 cudaError_t error_word(int** word) {
     return cudaGetSymbolAddress(reinterpret_cast<void**>(word), g_attn_error);
 }
@@ -754,12 +756,18 @@ extern "C" int fft_linattn_backward(const fft_linattn_desc* d, const fft_linattn
 }
 
 extern "C" int fft_linattn_check(void* stream) {
-    if (cudaStreamSynchronize((cudaStream_t)stream) != cudaSuccess) return FFT_ERR_CUDA;
-    int *word = nullptr, h = 0;
-    if (error_word(&word) != cudaSuccess || cudaMemcpy(&h, word, sizeof(int), cudaMemcpyDeviceToHost) != cudaSuccess)
+    // read and cleared in one operation, by one thread at a time: no error between the two is lost
+    static std::mutex one;
+    std::lock_guard<std::mutex> lock(one);
+    cudaStream_t s = (cudaStream_t)stream;
+    void* taken = nullptr;
+    int h = 0;
+    if (cudaGetSymbolAddress(&taken, g_attn_taken) != cudaSuccess) return FFT_ERR_CUDA;
+    k_take_error<<<1, 1, 0, s>>>();
+    if (cudaGetLastError() != cudaSuccess ||
+        cudaMemcpyAsync(&h, taken, sizeof(int), cudaMemcpyDeviceToHost, s) != cudaSuccess ||
+        cudaStreamSynchronize(s) != cudaSuccess)
         return FFT_ERR_CUDA;
-    if (h == 0) return FFT_OK;
-    if (cudaMemset(word, 0, sizeof(int)) != cudaSuccess) return FFT_ERR_CUDA;
     return kerr_status(h);
 }
 

@@ -573,8 +573,9 @@ int fft_linattn_backward(const fft_linattn_desc* d, const fft_linattn_grads* g, 
 
 /* fft_linattn_check - device-side waits of the calls for whole sequences are bounded (2 s); one that
  * gives up makes its kernel stop early (outputs are then undefined) and sets an error word of the
- * library on that device.  Synchronises `stream`, reads and clears the word: FFT_OK, FFT_ERR_TIMEOUT
- * or FFT_ERR_CUDA. */
+ * library on that device.  Behind the work in `stream`, reads and clears the word in one operation and
+ * synchronises the stream: FFT_OK, FFT_ERR_TIMEOUT or FFT_ERR_CUDA.  The word is the device's: whoever
+ * asks first learns of a wait on any stream.  Not for a capturing stream. */
 int fft_linattn_check(void* stream);
 
 /* fft_linattn_set_wait_timeout - time limit, in nanoseconds, of every device-side wait of the calls that
