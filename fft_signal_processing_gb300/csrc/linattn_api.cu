@@ -429,16 +429,15 @@ struct Place {
     fft_heads t;
     int64_t dim, heads;
 };
+int64_t place_bytes(const Place& p, const fft_linattn_desc& d) {
+    if (!p.t.data || d.length < 1) return 0;
+    return ((d.offsets ? 0 : (d.nseq - 1) * p.t.seq_stride) + (d.length - 1) * p.t.tok_stride +
+            (p.heads - 1) * p.t.head_stride + p.dim) * (int64_t)dtype_size(d.dtype);
+}
 bool places_meet(const Place& a, const Place& b, const fft_linattn_desc& d) {
     const size_t e = dtype_size(d.dtype);
     auto together = [](const Place& p) { return p.heads == 1 || p.t.head_stride == p.dim; };
-    const int64_t nseq = d.offsets ? 1 : d.nseq;
-    auto bytes = [&](const Place& p) -> int64_t {
-        if (!p.t.data || d.length < 1) return 0;
-        return ((nseq - 1) * p.t.seq_stride + (d.length - 1) * p.t.tok_stride + (p.heads - 1) * p.t.head_stride +
-                p.dim) * (int64_t)e;
-    };
-    if (!bytes_meet(a.t.data, bytes(a), b.t.data, bytes(b))) return false;
+    if (!bytes_meet(a.t.data, place_bytes(a, d), b.t.data, place_bytes(b, d))) return false;
     if (!together(a) || !together(b)) return true;
     const fft_seq x = {a.t.data, a.t.seq_stride, a.t.tok_stride}, y = {b.t.data, b.t.seq_stride, b.t.tok_stride};
     return seqs_meet(x, y, a.dim * a.heads, b.dim * b.heads, d.nseq, d.length, d.offsets, e);
@@ -447,6 +446,21 @@ Place decay_place(const fft_seq& t, int64_t heads) { return {{t.data, t.seq_stri
 bool meets_inputs(const Place& out, const fft_linattn_desc& d) {
     return places_meet(out, {d.q, d.dk, d.groups}, d) || places_meet(out, {d.k, d.dk, d.groups}, d) ||
            places_meet(out, {d.v, d.dv, d.heads}, d) || places_meet(out, decay_place(d.decay, d.heads), d);
+}
+// Bytes of `count` states (heads, dk and dv are at most 2^32 together), and whether rows reach into them, or
+// states into what is read.
+int64_t state_bytes(int64_t count, const fft_linattn_desc& d) {
+    const int64_t one = d.heads * d.dk * d.dv;
+    return (count > kMaxElements / one ? kMaxElements : count * one) * 4;
+}
+bool meets_states(const Place& p, const float* states, int64_t count, const fft_linattn_desc& d) {
+    return bytes_meet(p.t.data, place_bytes(p, d), states, state_bytes(count, d));
+}
+bool states_meet_inputs(const float* states, const fft_linattn_desc& d) {
+    for (const Place& p : {Place{d.q, d.dk, d.groups}, Place{d.k, d.dk, d.groups}, Place{d.v, d.dv, d.heads},
+                           decay_place(d.decay, d.heads)})
+        if (meets_states(p, states, d.nseq, d)) return true;
+    return false;
 }
 
 AttnRows rows_of(const fft_heads& t, int64_t dim, int64_t heads, const fft_linattn_desc& d, int share) {
@@ -688,8 +702,11 @@ extern "C" int fft_linattn_forward(const fft_linattn_desc* d, const fft_heads* o
     if (!out) return FFT_ERR_INVALID_ARG;
     TRY(check_heads(*out, d->dv, d->heads, *d, true));
     if (!aligned_to(final_state, 4) || !aligned_to(workspace, 16)) return FFT_ERR_MISALIGNED;
-    const int64_t states = d->nseq * d->heads * d->dk * d->dv * 4;
-    if (meets_inputs({*out, d->dv, d->heads}, *d) || bytes_meet(final_state, states, d->initial_state, states))
+    const int64_t states = state_bytes(d->nseq, *d);
+    const Place place = {*out, d->dv, d->heads};
+    if (meets_inputs(place, *d) || meets_states(place, d->initial_state, d->nseq, *d) ||
+        meets_states(place, final_state, d->nseq, *d) || states_meet_inputs(final_state, *d) ||
+        bytes_meet(final_state, states, d->initial_state, states))
         return FFT_ERR_INVALID_ARG;
     cudaStream_t s = (cudaStream_t)stream;
     if (d->length > 0) {
@@ -724,12 +741,15 @@ extern "C" int fft_linattn_backward(const fft_linattn_desc* d, const fft_linattn
     TRY(check_decay(g->ddecay, *d, true));
     if (!aligned_to(g->dfinal_state, 4) || !aligned_to(g->dinitial_state, 4) || !aligned_to(workspace, 16))
         return FFT_ERR_MISALIGNED;
-    const int64_t states = d->nseq * d->heads * d->dk * d->dv * 4;
+    const int64_t states = state_bytes(d->nseq, *d);
     const Place dout = {g->dout, d->dv, d->heads};
     for (const Place& o : {Place{g->dq, d->dk, d->groups}, Place{g->dk, d->dk, d->groups},
                            Place{g->dv, d->dv, d->heads}, decay_place(g->ddecay, d->heads)})
-        if (meets_inputs(o, *d) || places_meet(o, dout, *d)) return FFT_ERR_INVALID_ARG;
-    if (bytes_meet(g->dinitial_state, states, d->initial_state, states) ||
+        if (meets_inputs(o, *d) || places_meet(o, dout, *d) || meets_states(o, d->initial_state, d->nseq, *d) ||
+            meets_states(o, g->dfinal_state, d->nseq, *d) || meets_states(o, g->dinitial_state, d->nseq, *d))
+            return FFT_ERR_INVALID_ARG;
+    if (states_meet_inputs(g->dinitial_state, *d) || meets_states(dout, g->dinitial_state, d->nseq, *d) ||
+        bytes_meet(g->dinitial_state, states, d->initial_state, states) ||
         bytes_meet(g->dinitial_state, states, g->dfinal_state, states))
         return FFT_ERR_INVALID_ARG;
     cudaStream_t s = (cudaStream_t)stream;
@@ -803,7 +823,8 @@ extern "C" int fft_linattn_step(const fft_linattn_desc* d, const fft_heads* out,
     if ((pool > 0 && !state) || (!slots && pool < d->nseq)) return FFT_ERR_INVALID_ARG;
     if (!aligned_to(slots, 8) || !aligned_to(slots_out, 8) || !aligned_to(state, 4)) return FFT_ERR_MISALIGNED;
     TRY(check_heads(*out, d->dv, d->heads, *d, true));
-    if (meets_inputs({*out, d->dv, d->heads}, *d)) return FFT_ERR_INVALID_ARG;
+    const Place place = {*out, d->dv, d->heads};
+    if (meets_inputs(place, *d) || meets_states(place, state, pool, *d)) return FFT_ERR_INVALID_ARG;
     const AttnStepArgs a = {*d, *out, state, slots, slots_out, pool, 0};
     cudaStream_t s = (cudaStream_t)stream;
     return status(d->dtype == FFT_F32 ? attn_step<float>(a, s)

@@ -549,7 +549,7 @@ typedef struct fft_linattn_desc {
 int fft_linattn_workspace(const fft_linattn_desc* d, int backward, size_t* bytes);
 
 /* fft_linattn_forward - out and, unless NULL, final_state.  Other blocks read what a block has
- * read: out may not overlap q, k, v or decay, nor final_state initial_state
+ * read: neither out nor final_state may overlap q, k, v, decay, initial_state or one another
  * (FFT_ERR_INVALID_ARG).  Columns of the same rows are told apart where heads lie back to back;
  * otherwise tensors whose ranges of addresses meet count as overlapping.
  * Returns FFT_OK, FFT_ERR_INVALID_ARG, FFT_ERR_UNSUPPORTED_SIZE, FFT_ERR_MISALIGNED or
@@ -567,7 +567,8 @@ typedef struct fft_linattn_grads {
     float* dinitial_state; /* or NULL */
 } fft_linattn_grads;
 
-/* The gradients may not overlap what is read (FFT_ERR_INVALID_ARG). */
+/* The gradients may not overlap what is read, the states among it, nor dinitial_state the others
+ * (FFT_ERR_INVALID_ARG). */
 int fft_linattn_backward(const fft_linattn_desc* d, const fft_linattn_grads* g, void* workspace,
                          size_t workspace_bytes, void* stream);
 
@@ -585,7 +586,7 @@ int fft_linattn_set_wait_timeout(uint64_t ns);
 
 /* fft_linattn_step - one token for each of nseq sequences (length 1, offsets NULL, initial_state
  * not used; rows at seq_stride): state pool [pool][heads][dk][dv] float32, slots as for
- * fft_conv_step.  out may not overlap what is read. */
+ * fft_conv_step.  out may not overlap what is read, the pool among it (FFT_ERR_INVALID_ARG). */
 int fft_linattn_step(const fft_linattn_desc* d, const fft_heads* out, float* state, int64_t pool,
                      const int64_t* slots, const int64_t* slots_out, void* stream);
 
