@@ -212,7 +212,8 @@ __device__ __forceinline__ float tiles_sum(const float* p, int64_t tiles, int64_
 // over the chunk's tokens, where qi and ki are those rows' pairs with tokens of other chunks and qa,
 // ka those within the chunk; X in turn is that of the next chunk and what the rows between change.
 // Only between chunks do such sums run on, over terms that were formed from states in two or three
-// pieces, so that what cancels within a chunk is not carried along.
+// pieces, so that what cancels within a chunk is not carried along.  (Terms that are not finite cancel
+// nothing: they may reach any token of their sequence and head, and none of another one.)
 // One block per segment and head; a warp takes every eighth chunk.
 constexpr int kDgWarps = 8, kDgBatch = 64;
 constexpr int kTcChunk = 128;  // tokens of a chunk of the tcgen05 kernel

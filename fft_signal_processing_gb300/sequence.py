@@ -558,7 +558,7 @@ def linear_attention_backward(dout, q, k, v, decay, scale=None, initial_state=No
                               dfinal_state=None, stream=None):
     """Gradients of linear_attention from dout (and dfinal_state): AttentionGrads.  Those of queries and
     keys are sums over the heads that share them; ddecay has decay's shape, also where decay is a view
-    whose strides are 0."""
+    whose strides are 0.  A value that is not finite may reach all of its sequence's and heads' gradients."""
     desc, dev, nseq, heads, dk, dv = _attn_desc(q, k, v, decay, scale, initial_state, offsets)
     _need(dout, dev, v.dtype, v.shape, "dout")
     packed, shape = offsets is not None, (nseq, heads, dk, dv)

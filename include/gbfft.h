@@ -522,7 +522,9 @@ int fft_norm_backward(const fft_norm_desc* d, const void* dout, int64_t dout_str
  * an fft_seq with rows of `heads` values, whose strides may be 0 (decays that do not change).
  * Sequences, decay and their gradients are of dtype; states [nseq][heads][dk][dv] are float32.
  * 1 <= dk, dv <= FFT_LINATTN_MAX_DIM; groups divides heads, at most FFT_LINATTN_MAX_HEADS.
- * A value that is not finite reaches the outputs of its own token and later ones only.
+ * A value that is not finite reaches the outputs of its own token and later ones only; in the
+ * gradients it may reach all tokens of its sequence and of the heads that read it (ddecay is a
+ * difference of sums that run along the sequence), but no other sequence or head.
  */
 #define FFT_LINATTN_MAX_DIM 256
 #define FFT_LINATTN_MAX_HEADS 65535
