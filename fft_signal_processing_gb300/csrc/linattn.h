@@ -13,6 +13,7 @@
 namespace gbfft {
 
 constexpr int kAttnChunk = 64;     // tokens that one step of the kernel takes
+constexpr int kTcChunk = 128;      // and of the tcgen05 kernel; the decay's gradient takes sums by them
 constexpr int kAttnMaxDim = 256;   // dk and dv
 
 // Rows of one head at data + (q * seq + t * tok + (h / share) * head) elements.

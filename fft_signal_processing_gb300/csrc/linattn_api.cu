@@ -216,7 +216,6 @@ __device__ __forceinline__ float tiles_sum(const float* p, int64_t tiles, int64_
 // nothing: they may reach any token of their sequence and head, and none of another one.)
 // One block per segment and head; a warp takes every eighth chunk.
 constexpr int kDgWarps = 8, kDgBatch = 64;
-constexpr int kTcChunk = 128;  // tokens of a chunk of the tcgen05 kernel
 
 // What the tokens of a segment's first sequence change (X at the segment's start less that at its
 // end), and whether that sequence ends there.

@@ -42,7 +42,6 @@ namespace gbfft {
 namespace {
 
 using bf16 = __nv_bfloat16;
-constexpr int kTcChunk = 128;
 constexpr int kTcB = 256;  // threads of B
 
 // ---- tcgen05 --------------------------------------------------------------------------------
