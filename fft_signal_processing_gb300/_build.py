@@ -5,7 +5,7 @@ fft_signal_processing_gb300/libgbfft.so.  Objects are rebuilt only when a source
 newer than them.  build(checked=True) makes the checked variant libgbfft_checked.so from the
 same sources with -DGBFFT_CHECKED (device-side index checks that report FFT_ERR_BOUNDS), in an
 object directory of its own; tests load it through GBFFT_CHECKED=1.  The sequence operators carry no
-such checks: both libraries link the same objects of theirs.
+such checks: both libraries link the same objects of theirs, unless flags are given.
 """
 import concurrent.futures as cf
 import glob
@@ -63,15 +63,21 @@ def build(force: bool = False, verbose: bool = False, extra=(), checked: bool = 
     objdir, lib = (OBJ_CHECKED, LIB_CHECKED) if checked else (OBJ, LIB)
     os.makedirs(objdir, exist_ok=True)
     os.makedirs(OBJ, exist_ok=True)
-    if force:
-        for o in glob.glob(os.path.join(objdir, "*.o")):
-            os.remove(o)
     srcs = sorted(glob.glob(os.path.join(CSRC, "*.cu")))
+
+    def where(src):
+        shared = checked and not extra and os.path.basename(src).startswith(UNCHECKED)
+        return OBJ if shared else objdir
+
+    if force:
+        for src in srcs:
+            o = os.path.join(where(src), os.path.basename(src) + ".o")
+            if os.path.exists(o):
+                os.remove(o)
 
     def compiled(src):
         own = checked and not os.path.basename(src).startswith(UNCHECKED)
-        return _compile(src, list(extra) + (["-DGBFFT_CHECKED"] if own else []), verbose,
-                        objdir if own else OBJ)
+        return _compile(src, list(extra) + (["-DGBFFT_CHECKED"] if own else []), verbose, where(src))
 
     workers = max(1, min(len(srcs), os.cpu_count() or 1))
     with cf.ThreadPoolExecutor(workers) as ex:
