@@ -512,6 +512,11 @@ def _heads(t, packed):
     return (t.data_ptr(), 0, st[0], st[1]) if packed else (t.data_ptr(), st[0], st[1], st[2])
 
 
+def _scale(scale, dk):
+    """dk ** -0.5 unless given; rows without values are the library's to refuse."""
+    return (dk or 1) ** -0.5 if scale is None else scale
+
+
 def _attn_desc(q, k, v, decay, scale, initial_state, offsets):
     """(packed fft_linattn_desc, device, sequences, heads, dk, dv)."""
     code, dev = _first(q, "q")
@@ -529,7 +534,7 @@ def _attn_desc(q, k, v, decay, scale, initial_state, offsets):
     nseq, length = (offsets.numel() - 1, lead[0]) if packed else lead
     count, length, at = _batch(offsets, dev, nseq, length, packed)
     st = decay.stride()
-    desc = _ATTN.pack(code, dk ** -0.5 if scale is None else scale, count, length, heads, groups, dk, dv,
+    desc = _ATTN.pack(code, _scale(scale, dk), count, length, heads, groups, dk, dv,
                       at, _flat(initial_state, dev, torch.float32, (nseq, heads, dk, dv), "initial_state"),
                       *_heads(q, packed), *_heads(k, packed), *_heads(v, packed),
                       *((decay.data_ptr(), 0, st[0]) if packed else (decay.data_ptr(), st[0], st[1])))
@@ -606,7 +611,7 @@ def linear_attention_step(state, q, k, v, decay, scale=None, slots=None, slots_o
     _need(k, dev, dtype, qs, "k")
     _need(v, dev, dtype, (nseq, heads, dv), "v")
     qt, kt, vt = q.stride(), k.stride(), v.stride()
-    desc = _ATTN.pack(code, dk ** -0.5 if scale is None else scale, nseq, 1, heads, groups, dk, dv, 0, 0,
+    desc = _ATTN.pack(code, _scale(scale, dk), nseq, 1, heads, groups, dk, dv, 0, 0,
                       q.data_ptr(), qt[0], 0, qt[1], k.data_ptr(), kt[0], 0, kt[1],
                       v.data_ptr(), vt[0], 0, vt[1], *_token(decay, dev, dtype, (nseq, heads), "decay"))
     size = state.shape[0]
