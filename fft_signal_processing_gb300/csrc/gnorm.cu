@@ -407,15 +407,21 @@ __global__ void __launch_bounds__(kThreads) k_gn_moments(const GnArgs a) {
                 for (int u = 0; u < DEEP; ++u) px[u] = load<T, VEC>(x, i0 + u < count), x += hop;
                 const int live = count - i0 < DEEP ? count - i0 : DEEP;
                 const float n = (float)(live * VEC), inv = rcp(n);
-                // near the mean (zeros behind the last token add nothing)
+                // near the mean, and the value itself where all are alike
+                const float one = to_f(px[0].v[0]);
                 float2 v = splat(0.f);
 #pragma unroll
                 for (int u = 0; u < DEEP; ++u) {
+                    if (u >= live) break;
                     const Values<VEC> e = unpack<T, VEC>(px[u]);
 #pragma unroll
-                    for (int k = 0; k < e.N; ++k) v = fma2(e.v[k], splat(inv), v);
+                    for (int k = 0; k < e.N; ++k) {
+                        float2 w = add2(e.v[k], minus(one));
+                        if (VEC == 1) w.y = 0.f;
+                        v = fma2(w, splat(inv), v);
+                    }
                 }
-                const float mid = v.x + v.y;
+                const float mid = one + (v.x + v.y);
                 float2 v1 = splat(0.f), v2 = splat(0.f);
 #pragma unroll
                 for (int u = 0; u < DEEP; ++u) {
