@@ -251,12 +251,15 @@ __global__ void __launch_bounds__(kThreads, kGnBlocks<VEC, NV, BWD>) k_gn_token(
         if (!RING) fetch(0, row + step < a.rows);
         if (BWD && row + step < a.rows) mp += hm, rp += hm, nmean = *mp, nrstd = *rp;
         if constexpr (!BWD) {
+            // 2^-9 of the values (a group here has at most 2^9), so that sums of a type's lowest values stay finite
+            constexpr float DOWN = 1.f / 512.f;
+            static_assert(32 * kTokenValues * DOWN <= 1.f, "sums");
             float2 sum = splat(0.f), sq = splat(0.f);
 #pragma unroll
             for (int j = 0; j < NV; ++j)
 #pragma unroll
-                for (int k = 0; k < P; ++k) sum = add2(sum, v[j].v[k]);
-            mean = lanes_sum(sum.x + sum.y, lanes, mask) * inv;
+                for (int k = 0; k < P; ++k) sum = fma2(v[j].v[k], splat(DOWN), sum);
+            mean = lanes_sum(sum.x + sum.y, lanes, mask) * (inv * (1.f / DOWN));
 #pragma unroll
             for (int j = 0; j < NV; ++j)
 #pragma unroll
