@@ -220,22 +220,6 @@ __device__ __forceinline__ const T* rows_at(const AttnRows& r, int64_t row, int6
     return static_cast<const T*>(r.data) + row * r.seq + (head / r.share) * r.head;
 }
 
-// A number in two floats, 48 bits.
-struct Two {
-    float hi, lo;
-};
-__device__ __forceinline__ Two add(Two a, Two b) {
-    const float s = a.hi + b.hi, t = s - a.hi;
-    const float e = (a.hi - (s - t)) + (b.hi - t) + (a.lo + b.lo);
-    const float hi = s + e;
-    return {hi, e - (hi - s)};
-}
-// A log decay in units of log2: at most 0 (a NaN stays), and at least -288, where every float32
-// number has become 0.
-__device__ __forceinline__ Two log2_decay(float g) {
-    const float c = g > 0.f ? 0.f : (g < -200.f ? -200.f : g), hi = c * kLog2e;
-    return {hi, fmaf(c, 1.9259630e-8f, fmaf(c, kLog2e, -hi))};  // log2(e) beyond 24 bits
-}
 // The chunk's sums and factors from the log decays of tokens 2 lane and 2 lane + 1: one warp.
 __device__ __forceinline__ void make_decays(Decays& dc, float g0, float g1, bool reverse, float inter, float update) {
     const int lane = (int)threadIdx.x & 31;

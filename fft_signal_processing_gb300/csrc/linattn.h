@@ -54,6 +54,23 @@ struct AttnArgs {
     uint32_t wait_ns;  // limit of a device-side wait; 0: none is begun
 };
 
+// A number in two floats, 48 bits.
+struct Two {
+    float hi, lo;
+};
+__device__ __forceinline__ Two add(Two a, Two b) {
+    const float s = a.hi + b.hi, t = s - a.hi;
+    const float e = (a.hi - (s - t)) + (b.hi - t) + (a.lo + b.lo);
+    const float hi = s + e;
+    return {hi, e - (hi - s)};
+}
+// A log decay in units of log2: at most 0 (a NaN stays), and at least -288, where every float32
+// number has become 0.
+__device__ __forceinline__ Two log2_decay(float g) {
+    const float c = g > 0.f ? 0.f : (g < -200.f ? -200.f : g), hi = c * kLog2e;
+    return {hi, fmaf(c, 1.9259630e-8f, fmaf(c, kLog2e, -hi))};  // log2(e) beyond 24 bits
+}
+
 // Padded sizes of the kernel's variants.
 inline int attn_pad(int64_t d) { return d <= 64 ? 64 : (d <= 128 ? 128 : 256); }
 inline int attn_warps(int dtype, int64_t dx, int64_t dz) {

@@ -31,9 +31,8 @@ struct AttnStepArgs {
 // the Taylor series of exp(f ln 2), whose 1 is added last, and 2^n comes in two factors, since n may be below
 // -126.
 __device__ __forceinline__ float step_decay(float g) {
-    const float c = g > 0.f ? 0.f : (g < -104.f ? -104.f : g), hi = c * kLog2e;
-    const float lo = fmaf(c, 1.9259630e-8f, fmaf(c, kLog2e, -hi));  // log2(e) beyond 24 bits
-    const float n = rintf(hi), t = ((hi - n) + lo) * kLn2;
+    const Two d = log2_decay(g < -104.f ? -104.f : g);  // exp(-104) is below half of the smallest number
+    const float n = rintf(d.hi), t = ((d.hi - n) + d.lo) * kLn2;
     float p = 1.f / 5040.f;
     p = fmaf(p, t, 1.f / 720.f);
     p = fmaf(p, t, 1.f / 120.f);

@@ -219,22 +219,6 @@ template <int DX, int DZ, bool BWD> constexpr int tc_bytes() {
     return bytes;
 }
 
-// A number in two floats, 48 bits.
-struct TcTwo {
-    float hi, lo;
-};
-__device__ __forceinline__ TcTwo tc_add(TcTwo a, TcTwo b) {
-    const float s = a.hi + b.hi, t = s - a.hi;
-    const float e = (a.hi - (s - t)) + (b.hi - t) + (a.lo + b.lo);
-    const float hi = s + e;
-    return {hi, e - (hi - s)};
-}
-// A log decay in units of log2: at most 0 (a NaN stays), at least -288.
-__device__ __forceinline__ TcTwo tc_log2_decay(float g) {
-    const float c = g > 0.f ? 0.f : (g < -200.f ? -200.f : g), hi = c * kLog2e;
-    return {hi, fmaf(c, 1.9259630e-8f, fmaf(c, kLog2e, -hi))};  // log2(e) beyond 24 bits
-}
-
 // The part of a segment that belongs to one sequence (offsets of any kind: it holds token `at` and
 // stays in the segment).
 struct TcPart {
@@ -845,7 +829,7 @@ __global__ void __launch_bounds__(TcShape<DX, DZ, BWD>::kThreads, 1) k_linattn_t
     } else if (warp == M0 + 1) {
         // ---- decays: four tokens per lane ----
         const bf16* pg = static_cast<const bf16*>(a.decay.data) + row * a.decay.seq_stride + head;
-        TcTwo gone = {0.f, 0.f};
+        Two gone = {0.f, 0.f};
         fine = each_part([&](const TcPart& p, int chunks, uint32_t n0) {
             float g[4];
             auto fetch = [&](int i) {
@@ -858,34 +842,34 @@ __global__ void __launch_bounds__(TcShape<DX, DZ, BWD>::kThreads, 1) k_linattn_t
             fetch(0);
             for (int i = 0; i < chunks; ++i) {
                 const uint32_t n = n0 + i;
-                TcTwo d[4], sum;
-                d[0] = tc_log2_decay(g[0]);
+                Two d[4], sum;
+                d[0] = log2_decay(g[0]);
 #pragma unroll
-                for (int k = 1; k < 4; ++k) d[k] = tc_add(d[k - 1], tc_log2_decay(g[k]));
+                for (int k = 1; k < 4; ++k) d[k] = add(d[k - 1], log2_decay(g[k]));
                 sum = d[3];
                 if (i + 1 < chunks) fetch(i + 1);
 #pragma unroll
                 for (int o = 1; o < 32; o *= 2) {
-                    const TcTwo v = {__shfl_up_sync(0xffffffffu, sum.hi, o), __shfl_up_sync(0xffffffffu, sum.lo, o)};
-                    if (lane >= o) sum = tc_add(v, sum);
+                    const Two v = {__shfl_up_sync(0xffffffffu, sum.hi, o), __shfl_up_sync(0xffffffffu, sum.lo, o)};
+                    if (lane >= o) sum = add(v, sum);
                 }
                 // factors of columns: to the end of their block of 32 tokens, or (reversed) from its start
                 const int edge = reverse ? (lane & ~7) - 1 : lane | 7;
-                const TcTwo end = {__shfl_sync(0xffffffffu, sum.hi, edge & 31), __shfl_sync(0xffffffffu, sum.lo, edge & 31)};
-                const TcTwo all = {__shfl_sync(0xffffffffu, sum.hi, 31), __shfl_sync(0xffffffffu, sum.lo, 31)};
-                TcTwo before = {__shfl_up_sync(0xffffffffu, sum.hi, 1), __shfl_up_sync(0xffffffffu, sum.lo, 1)};
+                const Two end = {__shfl_sync(0xffffffffu, sum.hi, edge & 31), __shfl_sync(0xffffffffu, sum.lo, edge & 31)};
+                const Two all = {__shfl_sync(0xffffffffu, sum.hi, 31), __shfl_sync(0xffffffffu, sum.lo, 31)};
+                Two before = {__shfl_up_sync(0xffffffffu, sum.hi, 1), __shfl_up_sync(0xffffffffu, sum.lo, 1)};
                 if (lane == 0) before = {0.f, 0.f};
                 if (n > 0 && !wait(TC_FREE, n - 1)) return false;
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
-                    const TcTwo G = tc_add(before, d[k]);
+                    const Two G = add(before, d[k]);
                     sm.G[4 * lane + k] = make_float2(G.hi, G.lo);
                     const float to_end = (end.hi - G.hi) + (end.lo - G.lo);
                     sm.column[4 * lane + k] = edge < 0 ? 0.f : ex2(reverse ? -to_end : to_end);
                     sm.update[4 * lane + k] = ex2(reverse ? G.hi : (all.hi - G.hi) + (all.lo - G.lo)) * a.scale_update;
                 }
                 if (lane == 0) sm.total = ex2(all.hi), sm.all_hi = all.hi, sm.all_lo = all.lo;
-                gone = tc_add(gone, all);
+                gone = add(gone, all);
                 mbar_arrive(&bars[TC_DECAYS]);
             }
             if (summary && zt == 0 && lane == 0) {
