@@ -6,8 +6,10 @@
 // A few operations per element: bound by HBM where rows are whole 16-byte pieces.  Measured with inputs
 // that change from call to call: 16384 rows of 2048 bfloat16 channels in 16 groups, gated, 43 us, 4.7 TB/s
 // (69% of the copy rate; 81 with rows ahead in registers and one value to an instruction); its gradients
-// for 8192 rows 60 us; 8 x 4096 tokens of 1024 channels, SiLU, 72 us (first pass 26, joining 11, second 29),
-// x read twice; gradients of packed 20011 tokens of 330 float32 channels in groups of 55, value by value, 85 us.
+// for 8192 rows 60 us; 8 x 4096 tokens of 1024 channels, SiLU, 76 us (first pass 30, joining 13, second 30),
+// x read twice; gradients of packed 20011 tokens of 330 float32 channels in groups of 55, value by value, 86 us.
+// Sigmoids are approximate exponentials and reciprocals (2^-22): float32 gradients are 2.1e-7 from 64 bits
+// where exact ones in float32 are 0.9e-7.
 //
 // Sequences of one token (what follows the heads of an attention) are read once: the lanes that
 // share a group hold its values in registers, keep their channels' weights there too and take rows
@@ -797,7 +799,7 @@ int64_t token_step(const fft_gnorm_desc& d, int lanes, bool backward) {
     return step < 1 ? 1 : (step > d.nseq ? d.nseq : step);
 }
 // Tokens of a tile: as many as leave every SM eight blocks of 512 channels, 16 to 128.  Measured: 8 x 4096
-// tokens of 1024 channels 94 us with tiles of 16 and 72 us with tiles of 32.
+// tokens of 1024 channels 94 us with tiles of 16 and 72 us with tiles of 32 (and a first pass of 26 us).
 int64_t tile_of(const fft_gnorm_desc& d) {
     const int64_t rows = d.offsets ? 1 : d.nseq, wide = (d.channels + 511) / 512;
     int64_t tile = 128;

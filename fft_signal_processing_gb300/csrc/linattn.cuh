@@ -22,8 +22,8 @@
 // shared memory, the next chunk's under way where two fit.
 //
 // This kernel takes what the tcgen05 one does not: float32, float16, rows off 16-byte boundaries, dk
-// above 128.  Measured: packed 10007 tokens of 6 heads of 40 x 72 float32 200 us; gradients of packed 4001
-// tokens of 8 heads of 64 x 96 float16 400 us (250 and 480 with columns and warps beyond the sizes at work); 1 x 16384 tokens of 16 heads of 128 x 128 bfloat16 364 us,
+// above 128.  Measured: packed 10007 tokens of 6 heads of 40 x 72 float32 191 to 203 us; gradients of packed 4001
+// tokens of 8 heads of 64 x 96 float16 403 to 420 us (250 and 480 with columns and warps beyond the sizes at work); 1 x 16384 tokens of 16 heads of 128 x 128 bfloat16 364 us,
 // where the tensor pipe was busy 15% at 1.3 instructions a cycle: bound by latency at 8 warps of 255
 // registers to an SM.
 #pragma once

@@ -30,7 +30,7 @@
 //
 // Measured: one sequence of 16384 tokens, 16 heads of 128 x 128, time cut in 9: 158 us, 1.7 TB/s of q, k,
 // v and outputs; 8 x 2048 tokens of 32 heads of 128 x 64 175 us; gradients of 4 x 2048 tokens of 16 heads
-// 459 us.  A chunk takes about 9300 cycles, the units' products about 4500 of them (scores 1000, with
+// 459 us.  A chunk took about 9300 cycles at 148 us, the units' products about 4500 of them (scores 1000, with
 // the state 1000, outputs 600, state 1800): bound by the chain from weighted z over the state's product to
 // the next chunk's, and within it by the latency of the weighting at three warps a scheduler.
 #pragma once
